@@ -1232,6 +1232,20 @@ thread_local std::string g_init_error;
 
 }  // namespace
 
+namespace k2 {
+void set_error(const char* fmt, ...) {
+  char buf[512];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(buf, sizeof buf, fmt, ap);
+  va_end(ap);
+  try {
+    g_init_error = buf;
+  } catch (...) {  // no memory for the message: the status still says what happened
+  }
+}
+}  // namespace k2
+
 // ---------------------------------------------------------------------------
 // C ABI
 // ---------------------------------------------------------------------------

@@ -516,4 +516,7 @@ cudaError_t launch_argmax_rows(const float* logits, int rows, int V, int* next, 
                                int part_stride, unsigned* guard, cudaStream_t s, bool pdl = false);
 cudaError_t misc_init_attrs();
 
+// The message of k2_last_error(NULL): why this thread's last call without a context was refused.
+void set_error(const char* fmt, ...);
+
 }  // namespace k2

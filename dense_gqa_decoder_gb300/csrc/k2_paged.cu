@@ -1,0 +1,446 @@
+// The host-side bookkeeping of a block-paged cache, on the GPU: the tables of
+// the next step (k2_paged_plan) and the quantizing append (k2_paged_append).
+// What they compute is stated in include/k2.h.
+#include <algorithm>
+
+#include "k2_paged.cuh"
+
+namespace k2 {
+
+namespace {
+
+// ---- tables, slots and positions from request lengths -----------------------------------------
+//
+// A step's plan is three prefix sums over the requests (new tokens, blocks
+// taken, blocks given back), after which every token, new block and returned
+// block finds its request by binary search and its block by arithmetic on the
+// state before the step: the x-th entry of the free stack with the returned
+// blocks on top is d_free[x] below the old count F, else the (x - F)-th
+// returned block.  What the kernel writes (table entries of new blocks, stack
+// entries at or above F) is nothing that it reads, and the words that it may
+// write over its own inputs (count, lengths) are written after a barrier of
+// all CTAs, so one launch suffices.
+//
+// Bound by latency, not by bytes: one CTA does a decode step; the tokens of a
+// large step are spread over a cluster of up to 8 CTAs, whose hardware barrier
+// is what lets them share the free count without another launch.
+constexpr int kPlanThreads = 1024, kPlanPer = K2_PAGED_MAX_REQUESTS / kPlanThreads;
+constexpr int kPlanCap = 1 << 30;  // sums saturate here: min(a + b, cap) is associative for a, b >= 0
+static_assert(kPlanPer * kPlanThreads == K2_PAGED_MAX_REQUESTS, "whole requests per thread");
+
+struct PlanArgs {
+  const int* cached;
+  const int* fresh;
+  int requests, block_log2;
+  int* table;
+  int table_stride;
+  int* free_ids;
+  int free_capacity;
+  const int* free_count;
+  int* free_count_out;
+  int* kv_len;
+  int* cu_new;
+  int* slots;
+  int* positions;
+  int max_tokens;
+  int* status;
+};
+
+__device__ __forceinline__ int sat_add(int a, int b) { return min(a + b, kPlanCap); }
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// the r in [0, n) with sum[r] <= x < sum[r + 1]
+__device__ __forceinline__ int find_request(const int* sum, int n, int x) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (sum[mid] <= x) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a, int ctas) {
+  __shared__ int tok[K2_PAGED_MAX_REQUESTS + 1], take[K2_PAGED_MAX_REQUESTS + 1], give[K2_PAGED_MAX_REQUESTS + 1];
+  __shared__ int cached[K2_PAGED_MAX_REQUESTS];
+  __shared__ int part[3][32];
+  __shared__ int reasons;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, R = a.requests;
+  const int mask = (1 << a.block_log2) - 1;
+  auto blocks = [&](int n) { return (n >> a.block_log2) + ((n & mask) != 0); };
+  const int F = *a.free_count;
+  const long long room = static_cast<long long>(a.table_stride) << a.block_log2;
+  int bad = F < 0 || F > a.free_capacity ? K2_PLAN_NO_BLOCKS : 0;
+  if (tid == 0) reasons = 0;
+  __syncthreads();
+
+  // this thread's kPlanPer requests, then the sums over the block
+  int own[3] = {0, 0, 0}, v[kPlanPer][3];
+#pragma unroll
+  for (int i = 0; i < kPlanPer; ++i) {
+    const int r = tid * kPlanPer + i;
+    v[i][0] = v[i][1] = v[i][2] = 0;
+    if (r < R) {
+      const int c = a.cached[r], f = a.fresh[r];
+      cached[r] = c;
+      if (c < 0 || f < -1) {
+        bad |= K2_PLAN_BAD_LENGTH;
+      } else if (static_cast<long long>(c) + max(f, 0) > min(room, 0x7fffffffll)) {
+        bad |= K2_PLAN_TABLE_FULL;
+      } else if (f >= 0) {
+        v[i][0] = min(f, kPlanCap);
+        v[i][1] = blocks(c + f) - blocks(c);
+      } else {
+        v[i][2] = blocks(c);
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < 3; ++q) own[q] = sat_add(own[q], v[i][q]);
+  }
+  int inc[3];
+#pragma unroll
+  for (int q = 0; q < 3; ++q) {
+    inc[q] = own[q];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, inc[q], o);
+      if (lane >= o) inc[q] = sat_add(inc[q], u);
+    }
+    if (lane == 31) part[q][warp] = inc[q];
+  }
+  __syncthreads();
+  if (warp < 3) {
+    int t = part[warp][lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, t, o);
+      if (lane >= o) t = sat_add(t, u);
+    }
+    part[warp][lane] = t;
+  }
+  if (bad) atomicOr(&reasons, bad);
+  __syncthreads();
+  bad = reasons;
+  {
+    int* sums[3] = {tok, take, give};
+#pragma unroll
+    for (int q = 0; q < 3; ++q) {
+      const int before = __shfl_up_sync(0xffffffffu, inc[q], 1);
+      int run = sat_add(warp ? part[q][warp - 1] : 0, lane ? before : 0);
+#pragma unroll
+      for (int i = 0; i < kPlanPer; ++i) {
+        const int r = tid * kPlanPer + i;
+        if (r < R) sums[q][r] = run;
+        run = sat_add(run, v[i][q]);
+      }
+    }
+  }
+  const int T = part[0][31], taken = part[1][31], given = part[2][31];
+  if (tid == 0) {
+    tok[R] = T;
+    take[R] = taken;
+    give[R] = given;
+  }
+  const long long top = static_cast<long long>(F) + given;  // the stack with the returned blocks on it
+  if (taken > top || top - taken > a.free_capacity) bad |= K2_PLAN_NO_BLOCKS;
+  if (T > a.max_tokens) bad |= K2_PLAN_TOKENS_FULL;
+  __syncthreads();
+
+  const int step = ctas * kPlanThreads, first = blockIdx.x * kPlanThreads + tid;
+  if (!bad) {
+    auto returned = [&](int k) -> int {
+      const int r = find_request(give, R, k);
+      return a.table[static_cast<size_t>(r) * a.table_stride + (k - give[r])];
+    };
+    auto popped = [&](int k) -> int {
+      const long long x = top - 1 - k;
+      return x < F ? a.free_ids[x] : returned(static_cast<int>(x - F));
+    };
+    for (int t = first; t < a.max_tokens; t += step) {
+      int pos = 0, slot = -1;
+      if (t < T) {
+        const int r = find_request(tok, R, t);
+        pos = cached[r] + (t - tok[r]);
+        const int b = pos >> a.block_log2, old = blocks(cached[r]);
+        const int id = b < old ? a.table[static_cast<size_t>(r) * a.table_stride + b] : popped(take[r] + b - old);
+        // an id that is no block (a caller's stray entry) gives no slot
+        if (id >= 0 && id <= (0x7fffffff >> a.block_log2)) slot = (id << a.block_log2) | (pos & mask);
+      }
+      a.slots[t] = slot;
+      a.positions[t] = pos;
+    }
+    for (int k = first; k < taken; k += step) {
+      const int r = find_request(take, R, k);
+      a.table[static_cast<size_t>(r) * a.table_stride + blocks(cached[r]) + (k - take[r])] = popped(k);
+    }
+    for (int k = first; k < given - taken; k += step) a.free_ids[F + k] = returned(k);
+  } else {
+    for (int t = first; t < a.max_tokens; t += step) {
+      a.slots[t] = -1;
+      a.positions[t] = 0;
+    }
+  }
+  // kv_len may be cached and free_count_out free_count: written once every CTA has read them
+  int keep[kPlanPer];
+#pragma unroll
+  for (int i = 0; i < kPlanPer; ++i) {
+    const int r = tid * kPlanPer + i;
+    keep[i] = r < R && !bad ? (a.fresh[r] < 0 ? 0 : cached[r] + a.fresh[r]) : r < R ? max(cached[r], 0) : 0;
+  }
+  if (ctas > 1) cluster_sync();
+  else __syncthreads();
+  if (blockIdx.x != 0) return;
+#pragma unroll
+  for (int i = 0; i < kPlanPer; ++i) {
+    const int r = tid * kPlanPer + i;
+    if (r < R) {
+      a.kv_len[r] = keep[i];
+      a.cu_new[r] = bad ? 0 : tok[r];
+    }
+  }
+  if (tid == 0) {
+    a.cu_new[R] = bad ? 0 : T;
+    *a.free_count_out = bad ? F : static_cast<int>(top - taken);
+    a.status[0] = bad ? 0 : T;
+    a.status[1] = taken;
+    a.status[2] = given;
+    a.status[3] = bad;
+  }
+}
+
+// ---- quantizing append -------------------------------------------------------------------------
+//
+// A run is the maximal stretch of consecutive tokens with consecutive slots of
+// one block.  Each token has a CTA; the first token of a run takes the run,
+// one warp per (head, K or V): a lane holds head_dim / 32 neighbouring
+// elements of a row.  The others leave at once.  So the scale of a block and
+// head has one writer, and no atomics decide anything.
+template <typename T>
+struct Row4;  // N neighbouring elements of a row as fp32
+template <>
+struct Row4<float> {
+  template <int N>
+  __device__ __forceinline__ static void load(const float* p, float* f) {
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+      const float2 v = __ldg(reinterpret_cast<const float2*>(p + i));
+      f[i] = v.x;
+      f[i + 1] = v.y;
+    }
+  }
+};
+template <>
+struct Row4<__nv_bfloat16> {
+  template <int N>
+  __device__ __forceinline__ static void load(const __nv_bfloat16* p, float* f) {
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+      const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(p + i));
+      f[i] = bf16lo(w);
+      f[i + 1] = bf16hi(w);
+    }
+  }
+};
+template <>
+struct Row4<__half> {
+  template <int N>
+  __device__ __forceinline__ static void load(const __half* p, float* f) {
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+      const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(p + i));
+      const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&w));
+      f[i] = v.x;
+      f[i + 1] = v.y;
+    }
+  }
+};
+
+template <int N>
+struct Codes;  // N neighbouring codes
+template <>
+struct Codes<4> { using type = uint32_t; };
+template <>
+struct Codes<2> { using type = uint16_t; };
+
+constexpr int kAppendHeads = 8;  // KV heads of one CTA (two warps each)
+
+struct AppendArgs {
+  const void* k;
+  const void* v;
+  long long k_stride, v_stride;
+  const int* slots;
+  int tokens;
+};
+
+template <typename T, typename C, int D>
+__global__ void append_kernel(const PagedPool p, const AppendArgs a) {
+  constexpr int E = D / 32;
+  using Word = typename Codes<E>::type;
+  const int t = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = blockIdx.y * kAppendHeads + (warp >> 1);
+  const bool is_v = warp & 1;
+  const int B = 1 << p.block_log2, bmask = B - 1;
+  const int slot = a.slots[t];
+  if (slot < 0) return;
+  if (slot >= (static_cast<long long>(p.n_blocks) << p.block_log2)) {
+    if (threadIdx.x == 0 && blockIdx.y == 0) raise_flag(p.flags, K2_PAGED_BAD_SLOT);
+    return;
+  }
+  if (g >= p.n_kv) return;
+  const int o = slot & bmask;
+  if (o > 0 && t > 0 && a.slots[t - 1] == slot - 1) return;  // inside a run
+  int n = 1;
+  for (bool more = true; more;) {
+    const int i = n + lane;
+    const bool same = o + i < B && t + i < a.tokens && a.slots[t + i] == slot + i;
+    const unsigned m = __ballot_sync(0xffffffffu, same);
+    const int run = m == 0xffffffffu ? 32 : __ffs(~m) - 1;
+    n += run;
+    more = run == 32;
+  }
+  const size_t at = static_cast<size_t>(slot >> p.block_log2) * p.n_kv + g;
+  const T* src = static_cast<const T*>(is_v ? a.v : a.k) + t * (is_v ? a.v_stride : a.k_stride) + g * D + lane * E;
+  const long long stride = is_v ? a.v_stride : a.k_stride;
+  uint8_t* codes = (is_v ? p.v : p.k) + (at << p.block_log2) * D + lane * E;
+  float* scale = (is_v ? p.vs : p.ks) + at;
+  float top = 0.f;
+  for (int i = 0; i < n; ++i) {
+    float f[E];
+    Row4<T>::template load<E>(src + i * stride, f);
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const float m = fabsf(f[e]);
+      if (m <= 3.402823466e38f) top = fmaxf(top, m);  // finite
+    }
+  }
+  top = warp_max(top);
+  const float was = o > 0 ? *scale : 0.f;
+  const float now = fmaxf(was, __fdiv_rn(top, C::kMax));
+  if (o > 0 && now > was) {
+    const float ratio = __fdiv_rn(was, now);
+    for (int i = 0; i < o; ++i) {
+      Word* w = reinterpret_cast<Word*>(codes + static_cast<size_t>(i) * D);
+      const uint32_t c = *w;
+      uint32_t u = 0;
+#pragma unroll
+      for (int e = 0; e < E; ++e) u |= quantize<C>(__fmul_rn(C::value((c >> (8 * e)) & 0xFFu), ratio), 1.f) << (8 * e);
+      *w = static_cast<Word>(u);
+    }
+  }
+  __syncwarp();
+  if (lane == 0) *scale = now;
+  for (int i = 0; i < n; ++i) {
+    float f[E];
+    Row4<T>::template load<E>(src + i * stride, f);
+    uint32_t u = 0;
+#pragma unroll
+    for (int e = 0; e < E; ++e) u |= quantize<C>(f[e], now) << (8 * e);
+    *reinterpret_cast<Word*>(codes + static_cast<size_t>(o + i) * D) = static_cast<Word>(u);
+  }
+}
+
+template <typename T, typename C>
+cudaError_t launch_append(const PagedPool& p, int head_dim, const AppendArgs& a, cudaStream_t s) {
+  const dim3 grid(a.tokens, (p.n_kv + kAppendHeads - 1) / kAppendHeads);
+  const int threads = 64 * std::min(p.n_kv, kAppendHeads);
+  if (head_dim == 128) append_kernel<T, C, 128><<<grid, threads, 0, s>>>(p, a);
+  else append_kernel<T, C, 64><<<grid, threads, 0, s>>>(p, a);
+  return cudaGetLastError();
+}
+template <typename T>
+cudaError_t launch_append(const PagedPool& p, const k2_paged_kv& kv, const AppendArgs& a, cudaStream_t s) {
+  return kv.dtype == K2_I8 ? launch_append<T, CodeI8>(p, kv.head_dim, a, s)
+                           : launch_append<T, CodeF8>(p, kv.head_dim, a, s);
+}
+
+}  // namespace
+
+}  // namespace k2
+
+using namespace k2;
+
+extern "C" {
+
+k2_status k2_paged_plan(const int32_t* d_cached, const int32_t* d_fresh, int32_t requests, int32_t block_tokens,
+                        int32_t* d_table, int32_t table_stride, int32_t* d_free, int32_t free_capacity,
+                        const int32_t* d_free_count, int32_t* d_free_count_out, int32_t* d_kv_len,
+                        int32_t* d_cu_new, int32_t* d_slots, int32_t* d_positions, int32_t max_tokens,
+                        int32_t* d_status, void* stream) {
+  if (!d_cached || !d_fresh || !d_table || !d_free || !d_free_count || !d_free_count_out || !d_kv_len || !d_cu_new ||
+      !d_slots || !d_positions || !d_status) {
+    set_error("every pointer of a plan must be non-null");
+    return K2_ERR_ARG;
+  }
+  if (block_tokens != 16 && block_tokens != 32 && block_tokens != 64 && block_tokens != 128) {
+    set_error("block_tokens must be 16, 32, 64 or 128 (got %d)", block_tokens);
+    return K2_ERR_UNSUPPORTED;
+  }
+  if (requests < 1 || requests > K2_PAGED_MAX_REQUESTS) {
+    set_error("requests %d outside [1, %d]", requests, K2_PAGED_MAX_REQUESTS);
+    return K2_ERR_SHAPE;
+  }
+  if (table_stride < 1 || free_capacity < 1 || max_tokens < 1 || max_tokens > kPlanCap - 1) {
+    set_error("table_stride, free_capacity and max_tokens must be positive, max_tokens below 2^30 (got %d, %d, %d)",
+              table_stride, free_capacity, max_tokens);
+    return K2_ERR_SHAPE;
+  }
+  PlanArgs a = {d_cached, d_fresh, requests, 31 - __builtin_clz(block_tokens), d_table, table_stride, d_free,
+                free_capacity, d_free_count, d_free_count_out, d_kv_len, d_cu_new, d_slots, d_positions, max_tokens,
+                d_status};
+  int ctas = 1;
+  while (ctas < 8 && ctas * 4 * kPlanThreads < max_tokens) ctas *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(kPlanThreads);
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = ctas;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = ctas > 1 ? 1 : 0;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, plan_kernel, a, ctas);
+  if (e == cudaSuccess) return K2_OK;
+  set_error("plan launch: %s", cudaGetErrorString(e));
+  return K2_ERR_CUDA;
+}
+
+k2_status k2_paged_append(const k2_paged_kv* kv, const void* d_k, const void* d_v, int32_t dtype, int64_t k_stride,
+                          int64_t v_stride, const int32_t* d_slots, int32_t tokens, void* stream) {
+  const k2_status st = check_paged_kv(kv);
+  if (st != K2_OK) return st;
+  if (dtype != K2_BF16 && dtype != K2_F16 && dtype != K2_F32) {
+    set_error("K and V rows must be K2_BF16, K2_F16 or K2_F32 (got dtype %d)", dtype);
+    return K2_ERR_UNSUPPORTED;
+  }
+  if (tokens < 0) {
+    set_error("tokens must be >= 0 (got %d)", tokens);
+    return K2_ERR_ARG;
+  }
+  if (tokens == 0) return K2_OK;
+  if (!d_k || !d_v || !d_slots) {
+    set_error("d_k, d_v and d_slots must be non-null");
+    return K2_ERR_ARG;
+  }
+  const int64_t row = static_cast<int64_t>(kv->n_kv_heads) * kv->head_dim;
+  const int bytes = dtype == K2_F32 ? 4 : 2;
+  if ((tokens > 1 && (k_stride < row || v_stride < row)) || k_stride * bytes % 16 || v_stride * bytes % 16 ||
+      !aligned16(d_k) || !aligned16(d_v)) {
+    set_error("K and V rows must be 16-byte aligned and at least n_kv_heads * head_dim elements apart");
+    return K2_ERR_ARG;
+  }
+  const PagedPool p(*kv);
+  const AppendArgs a = {d_k, d_v, k_stride, v_stride, d_slots, tokens};
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = dtype == K2_F32    ? launch_append<float>(p, *kv, a, s)
+                        : dtype == K2_BF16 ? launch_append<__nv_bfloat16>(p, *kv, a, s)
+                                           : launch_append<__half>(p, *kv, a, s);
+  if (e == cudaSuccess) return K2_OK;
+  set_error("append launch: %s", cudaGetErrorString(e));
+  return K2_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -22,6 +22,9 @@ K2_F32, K2_BF16, K2_F16, K2_I8, K2_F8, K2_Q4 = range(6)
  K2_OPT_WAIT_LIMIT_US, K2_OPT_STALL_PHASE, K2_OPT_L2_AHEAD, K2_OPT_L2_AHEAD_PHASES, K2_OPT_TRACE,
  K2_OPT_PREFILL_ATTN, K2_OPT_PREFILL_SPLIT, K2_OPT_PREFILL_GEMM) = range(14)
 KERNEL_CLASSES = ("embed", "qkv", "attn", "o_proj", "gate_up", "down", "lm_head", "step", "sample")
+K2_PAGED_BAD_SLOT, K2_PAGED_BAD_BLOCK, K2_PAGED_BAD_LENGTH = 1, 2, 4
+K2_PLAN_BAD_LENGTH, K2_PLAN_TABLE_FULL, K2_PLAN_NO_BLOCKS, K2_PLAN_TOKENS_FULL = 1, 2, 4, 8
+K2_PAGED_MAX_REQUESTS = 2048
 DTYPES = {"f32": K2_F32, "bf16": K2_BF16, "f16": K2_F16, "i8": K2_I8, "f8": K2_F8, "q4": K2_Q4}
 
 
@@ -63,6 +66,19 @@ def sampling(temperature=0.0, top_k=0, top_p=1.0, min_p=0.0, repetition_penalty=
                     repetition_penalty=repetition_penalty, seed=seed)
 
 
+class PagedKv(C.Structure):
+    _fields_ = [("k", C.c_void_p), ("v", C.c_void_p), ("k_scale", C.c_void_p), ("v_scale", C.c_void_p),
+                ("n_blocks", C.c_int32), ("block_tokens", C.c_int32), ("n_kv_heads", C.c_int32),
+                ("head_dim", C.c_int32), ("dtype", C.c_int32), ("flags", C.c_void_p)]
+
+
+class LogitRules(C.Structure):
+    _fields_ = [("repetition", C.c_void_p), ("presence", C.c_void_p), ("frequency", C.c_void_p),
+                ("ids", C.c_void_p), ("ids_stride", C.c_int64), ("ids_len", C.c_void_p), ("prompt_len", C.c_void_p),
+                ("bias_offset", C.c_void_p), ("bias_ids", C.c_void_p), ("bias", C.c_void_p), ("n_bias", C.c_int32),
+                ("mask", C.c_void_p), ("mask_stride", C.c_int64), ("n_masks", C.c_int32), ("mask_row", C.c_void_p)]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"libk2.so is not built ({LIB_PATH}); run dense_gqa_decoder_gb300.build")
@@ -99,6 +115,12 @@ def _load():
         "k2_quantize_q4": (C.c_int, [vp, i32, i32, vp, vp, vp]),
         "k2_decode_speculative": (C.c_int, [vp, i32, vp, i32, i32, vp, C.POINTER(i32), vp]),
         "k2_spec_logits_view": (C.c_int, [vp, C.POINTER(vp), C.POINTER(i32)]),
+        "k2_paged_plan": (C.c_int, [vp, vp, i32, i32, vp, i32, vp, i32, vp, vp, vp, vp, vp, vp, i32, vp, vp]),
+        "k2_paged_append": (C.c_int, [vp, vp, vp, i32, i64, i64, vp, i32, vp]),
+        "k2_paged_workspace_bytes": (C.c_size_t, []),
+        "k2_paged_attention": (C.c_int, [vp, vp, i32, i64, vp, vp, vp, i32, i32, i32, i32, i32, C.c_float, vp, i64, vp,
+                                         C.c_size_t, vp]),
+        "k2_adjust_logits": (C.c_int, [C.POINTER(LogitRules), vp, i64, vp, i64, i32, i32, vp]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -113,7 +135,8 @@ EXPORTED = ("k2_workspace_bytes", "k2_init_weights", "k2_free", "k2_last_error",
             "k2_sync_status", "k2_clear_status", "k2_set_option", "k2_profile_decode", "k2_greedy_head_noalloc",
             "k2_kv_state_bytes", "k2_kv_save", "k2_kv_peek", "k2_kv_load", "k2_set_sampling", "k2_sample_logits",
             "k2_philox", "k2_spec_draft", "k2_decode_speculative", "k2_quantize_fp8",
-            "k2_quantize_q4", "k2_spec_logits_view")
+            "k2_quantize_q4", "k2_spec_logits_view", "k2_paged_plan", "k2_paged_append",
+            "k2_paged_workspace_bytes", "k2_paged_attention", "k2_adjust_logits")
 
 
 def _ptr(t):
@@ -362,6 +385,205 @@ def quantize_q4(src, stream=None):
     if st != K2_OK:
         raise K2Error(st, "k2_quantize_q4 failed")
     return codes, scales
+
+
+# ---- a block-paged 8-bit cache for many requests -----------------------------------------------
+
+_ROW_DTYPES = {torch.float32: K2_F32, torch.bfloat16: K2_BF16, torch.float16: K2_F16}
+
+
+def _call(st):
+    if st != K2_OK:
+        raise K2Error(st, (LIB.k2_last_error(None) or b"").decode())
+
+
+def _need(what, t, dtype, shape, device):
+    """The C calls read raw pointers: a contiguous tensor of this type and shape
+    (None: any extent) on the device of the call."""
+    if t.dtype is not dtype or t.device != device or not t.is_contiguous() or len(t.shape) != len(shape) or any(
+            n is not None and n != m for n, m in zip(shape, t.shape)):
+        raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, got "
+                         f"{t.dtype} {tuple(t.shape)} on {t.device}")
+
+
+def _device(t):
+    """The call's device: that of `t`, which has to be the current one (the C
+    calls launch there)."""
+    d = t.device
+    if d.type != "cuda" or d.index != torch.cuda.current_device():
+        raise ValueError(f"the tensors must be on the current CUDA device, got {d}")
+    return d
+
+
+class PagedCache:
+    """A pool of 8-bit blocks (k2_paged_kv) and the tensors that hold it: k and v
+    [n_blocks, n_kv_heads, block_tokens, head_dim] (int8 or float8_e4m3fn codes),
+    k_scale and v_scale [n_blocks, n_kv_heads] float32, and `flags`, an int32
+    tensor of one word that device-side faults are OR-ed into (K2_PAGED_*)."""
+
+    def __init__(self, n_blocks, block_tokens, n_kv_heads, head_dim, dtype="i8"):
+        if dtype not in ("i8", "f8"):
+            raise ValueError(f"a paged cache holds 'i8' or 'f8' codes, got {dtype!r}")
+        shape = (n_blocks, n_kv_heads, block_tokens, head_dim)
+        code = torch.int8 if dtype == "i8" else torch.float8_e4m3fn
+        self._bind(torch.zeros(shape, dtype=torch.int8, device="cuda").view(code),
+                   torch.zeros(shape, dtype=torch.int8, device="cuda").view(code),
+                   torch.zeros(shape[:2], device="cuda"), torch.zeros(shape[:2], device="cuda"))
+
+    @classmethod
+    def of(cls, k, v, k_scale, v_scale):
+        """A cache over tensors that the caller made (not copied)."""
+        self = cls.__new__(cls)
+        self._bind(k, v, k_scale, v_scale)
+        return self
+
+    def _bind(self, k, v, k_scale, v_scale):
+        dev = _device(k)
+        if k.dtype not in (torch.int8, torch.float8_e4m3fn) or k.dim() != 4:
+            raise ValueError(f"k must be a 4-dimensional int8 or float8_e4m3fn tensor, got {k.dtype} {tuple(k.shape)}")
+        _need("k", k, k.dtype, k.shape, dev)
+        _need("v", v, k.dtype, k.shape, dev)
+        _need("k_scale", k_scale, torch.float32, k.shape[:2], dev)
+        _need("v_scale", v_scale, torch.float32, k.shape[:2], dev)
+        self.k, self.v, self.k_scale, self.v_scale, self.device = k, v, k_scale, v_scale, dev
+        self.flags = torch.zeros(1, dtype=torch.int32, device=dev)
+        n, g, b, d = k.shape
+        self.n_blocks, self.n_kv_heads, self.block_tokens, self.head_dim = n, g, b, d
+        self.desc = PagedKv(k=k.data_ptr(), v=v.data_ptr(), k_scale=k_scale.data_ptr(), v_scale=v_scale.data_ptr(),
+                            n_blocks=n, block_tokens=b, n_kv_heads=g, head_dim=d,
+                            dtype=K2_I8 if k.dtype is torch.int8 else K2_F8, flags=self.flags.data_ptr())
+        self._ref = C.addressof(self.desc)
+
+
+def paged_plan(cached, fresh, table, free, free_count, block_tokens, *, kv_len, cu_new, slots, positions, status,
+               free_count_out=None, stream=None):
+    """k2_paged_plan on int32 device tensors: cached, fresh, kv_len [requests],
+    table [requests, columns], free [blocks], free_count [1] (and free_count_out,
+    default the same), cu_new [requests + 1], slots and positions [max_tokens],
+    status [4].  kv_len may be cached."""
+    dev = _device(cached)
+    if free_count_out is None:
+        free_count_out = free_count
+    r = cached.numel()
+    i32 = torch.int32
+    for what, t, shape in (("cached", cached, (r,)), ("fresh", fresh, (r,)), ("table", table, (r, None)),
+                           ("free", free, (None,)), ("free_count", free_count, (1,)),
+                           ("free_count_out", free_count_out, (1,)), ("kv_len", kv_len, (r,)),
+                           ("cu_new", cu_new, (r + 1,)), ("slots", slots, (None,)),
+                           ("positions", positions, slots.shape), ("status", status, (4,))):
+        _need(what, t, i32, shape, dev)
+    _call(LIB.k2_paged_plan(cached.data_ptr(), fresh.data_ptr(), r, block_tokens, table.data_ptr(), table.shape[1],
+                            free.data_ptr(), free.numel(), free_count.data_ptr(), free_count_out.data_ptr(),
+                            kv_len.data_ptr(), cu_new.data_ptr(), slots.data_ptr(), positions.data_ptr(),
+                            slots.numel(), status.data_ptr(), _stream(stream)))
+
+
+def _rows(what, t, dtype, heads, head_dim, device):
+    """[tokens, heads, head_dim] rows whose tokens may be apart (a slice of packed rows)."""
+    if t.dtype is not dtype or t.device != device or t.dim() != 3 or t.shape[1] != heads or t.shape[2] != head_dim \
+            or t.stride(2) != 1 or (heads > 1 and t.stride(1) != head_dim):
+        raise ValueError(f"{what} must be [tokens, {heads}, {head_dim}] {dtype} rows on {device}, each row contiguous, "
+                         f"got {t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
+
+
+def paged_append(cache, k, v, slots, stream=None):
+    """k2_paged_append: K and V rows [tokens, n_kv_heads, head_dim] (bf16, fp16 or
+    fp32; tokens may be strided) to the int32 slots [tokens]."""
+    dev = _device(k)
+    if dev != cache.device:
+        raise ValueError(f"the rows are on {dev}, the cache on {cache.device}")
+    if k.dtype not in _ROW_DTYPES:
+        raise ValueError(f"k and v must be float32, bfloat16 or float16, got {k.dtype}")
+    _rows("k", k, k.dtype, cache.n_kv_heads, cache.head_dim, dev)
+    _rows("v", v, k.dtype, cache.n_kv_heads, cache.head_dim, dev)
+    n = k.shape[0]
+    if v.shape[0] != n:
+        raise ValueError(f"k has {n} rows, v {v.shape[0]}")
+    _need("slots", slots, torch.int32, (n,), dev)
+    _call(LIB.k2_paged_append(cache._ref, k.data_ptr(), v.data_ptr(), _ROW_DTYPES[k.dtype], k.stride(0), v.stride(0),
+                              slots.data_ptr(), n, _stream(stream)))
+
+
+def paged_workspace():
+    """A zeroed workspace for paged_attention calls that do not overlap."""
+    return torch.zeros(int(LIB.k2_paged_workspace_bytes()), dtype=torch.uint8, device="cuda")
+
+
+def paged_attention(cache, q, out, cu_q, kv_len, table, max_q, workspace, scale=None, stream=None):
+    """k2_paged_attention: q and out [tokens, n_heads, head_dim] (bf16 or fp16;
+    tokens may be strided), cu_q [requests + 1], kv_len [requests], table
+    [requests, columns] int32; max_q: the most queries of one request; scale:
+    default head_dim ** -0.5."""
+    dev = _device(q)
+    if dev != cache.device:
+        raise ValueError(f"the queries are on {dev}, the cache on {cache.device}")
+    if q.dtype not in (torch.bfloat16, torch.float16):
+        raise ValueError(f"q must be bfloat16 or float16, got {q.dtype}")
+    heads, d = (q.shape[1] if q.dim() == 3 else 0), cache.head_dim
+    _rows("q", q, q.dtype, heads, d, dev)
+    _rows("out", out, q.dtype, heads, d, dev)
+    if out.shape[0] != q.shape[0]:
+        raise ValueError(f"q has {q.shape[0]} rows, out {out.shape[0]}")
+    r = kv_len.numel()
+    _need("cu_q", cu_q, torch.int32, (r + 1,), dev)
+    _need("kv_len", kv_len, torch.int32, (r,), dev)
+    _need("table", table, torch.int32, (r, None), dev)
+    _need("workspace", workspace, torch.uint8, (None,), dev)
+    _call(LIB.k2_paged_attention(cache._ref, q.data_ptr(), _ROW_DTYPES[q.dtype], q.stride(0), cu_q.data_ptr(),
+                                 kv_len.data_ptr(), table.data_ptr(), table.shape[1], r, q.shape[0], heads, max_q,
+                                 d ** -0.5 if scale is None else scale, out.data_ptr(), out.stride(0),
+                                 workspace.data_ptr(), workspace.numel(), _stream(stream)))
+
+
+def adjust_logits(logits, out=None, *, repetition=None, presence=None, frequency=None, ids=None, ids_len=None,
+                  prompt_len=None, bias=None, mask=None, mask_row=None, stream=None):
+    """k2_adjust_logits on logits [rows, vocab] fp32 (rows may be strided) into
+    `out` (default: in place): repetition, presence, frequency [rows] fp32; ids
+    [rows, n], ids_len, prompt_len [rows] int32; bias = (offsets [rows + 1], ids,
+    values fp32); mask [masks, >= ceil(vocab / 32)] int32 words, mask_row [rows]."""
+    dev = _device(logits)
+    if out is None:
+        out = logits
+    for what, t in (("logits", logits), ("out", out)):
+        if t.dtype is not torch.float32 or t.device != dev or t.dim() != 2 or t.shape != logits.shape or t.stride(1) != 1:
+            raise ValueError(f"{what} must be [rows, vocab] float32 rows on {dev}, got {t.dtype} {tuple(t.shape)} on "
+                             f"{t.device}")
+    rows, vocab = logits.shape
+    u = LogitRules()
+    for what, t in (("repetition", repetition), ("presence", presence), ("frequency", frequency)):
+        if t is not None:
+            _need(what, t, torch.float32, (rows,), dev)
+            setattr(u, what, t.data_ptr())
+    if ids is not None:
+        _need("ids", ids, torch.int32, (rows, None), dev)
+        if ids_len is None:
+            raise ValueError("ids need ids_len")
+        _need("ids_len", ids_len, torch.int32, (rows,), dev)
+        u.ids, u.ids_stride, u.ids_len = ids.data_ptr(), ids.shape[1], ids_len.data_ptr()
+        if prompt_len is not None:
+            _need("prompt_len", prompt_len, torch.int32, (rows,), dev)
+            u.prompt_len = prompt_len.data_ptr()
+        if not ids.numel():  # no row holds a token: nothing to penalise
+            u = LogitRules()
+    if bias is not None:
+        offset, bias_ids, values = bias
+        _need("bias offsets", offset, torch.int32, (rows + 1,), dev)
+        _need("bias ids", bias_ids, torch.int32, (None,), dev)
+        _need("bias values", values, torch.float32, bias_ids.shape, dev)
+        if bias_ids.numel():
+            u.bias_offset, u.bias_ids, u.bias = offset.data_ptr(), bias_ids.data_ptr(), values.data_ptr()
+            u.n_bias = bias_ids.numel()
+    if mask is not None:
+        _need("mask", mask, torch.int32, (None, None), dev)
+        if mask.shape[1] < (vocab + 31) // 32 or (mask_row is None and mask.shape[0] < rows):
+            raise ValueError(f"mask must have {(vocab + 31) // 32} words for each of its rows (and a row for each of the "
+                             f"logits without mask_row), got {tuple(mask.shape)}")
+        u.mask, u.mask_stride, u.n_masks = mask.data_ptr(), mask.shape[1], mask.shape[0]
+        if mask_row is not None:
+            _need("mask_row", mask_row, torch.int32, (rows,), dev)
+            u.mask_row = mask_row.data_ptr()
+    _call(LIB.k2_adjust_logits(C.byref(u), logits.data_ptr(), logits.stride(0), out.data_ptr(), out.stride(0), rows, vocab,
+                               _stream(stream)))
 
 
 def spec_draft(tokens, max_draft=8) -> list:

@@ -474,6 +474,158 @@ k2_status k2_quantize_fp8(const void* d_src, int32_t rows, int32_t cols, uint8_t
 k2_status k2_quantize_q4(const void* d_src, int32_t rows, int32_t cols, int8_t* d_codes, float* d_scales,
                          void* stream);
 
+/* ---- serving many requests: a block-paged 8-bit cache ---------------------------
+ *
+ * A pool of blocks shared by any number of requests, for callers that serve
+ * requests of unknown length (the context's own cache reserves max_context rows
+ * per sequence).  A block holds block_tokens consecutive positions of one
+ * request: their K and V rows of every KV head as 8-bit codes, with one fp32
+ * scale per block and KV head for K and one for V; a row's values are
+ * code * scale.  A request's block table names its blocks in order: position p
+ * lies in block table[p / block_tokens] at row p % block_tokens, and its "slot"
+ * is block * block_tokens + row.  One pool per layer; all layers share the
+ * tables.  A step of many requests is
+ *   k2_paged_plan       tables, slots, positions and lengths of the step
+ *   k2_paged_append     the step's K/V rows into the pool    (per layer)
+ *   k2_paged_attention  the step's queries over it           (per layer)
+ *   k2_adjust_logits    per-request rules, then k2_sample_logits
+ * No context is needed; the calls allocate nothing and enqueue their work on
+ * `stream`.  They may be captured into a CUDA graph: every length is read on the
+ * device.  Why a call was refused: k2_last_error(NULL).
+ *
+ * Faults that only the device can see (a slot or block outside the pool,
+ * lengths that contradict each other) are skipped, never read or written, and
+ * leave a bit in *flags. */
+typedef struct {
+  void* k;         /* codes [n_blocks][n_kv_heads][block_tokens][head_dim], 16-byte aligned */
+  void* v;
+  float* k_scale;  /* [n_blocks][n_kv_heads] */
+  float* v_scale;
+  int32_t n_blocks;
+  int32_t block_tokens; /* 16, 32, 64 or 128 */
+  int32_t n_kv_heads;
+  int32_t head_dim;     /* 64 or 128 */
+  int32_t dtype;        /* K2_I8: codes -127 .. 127; K2_F8: E4M3 codes */
+  uint32_t* flags;      /* device word that faults are OR-ed into (the caller clears it); nullable */
+} k2_paged_kv;
+
+enum {
+  K2_PAGED_BAD_SLOT = 1,   /* a slot >= n_blocks * block_tokens: that row was not stored */
+  K2_PAGED_BAD_BLOCK = 2,  /* a table entry outside [0, n_blocks) within a request's length: its keys
+                              were left out */
+  K2_PAGED_BAD_LENGTH = 4  /* cu_q not ascending or beyond the query rows, more queries than max_q or
+                              than keys, or a length beyond the table: the request's rows are zeros
+                              where they lie inside the query rows */
+};
+#define K2_PAGED_MAX_REQUESTS 2048
+
+/* Block tables, slot map, positions and lengths of the next step, from the
+ * requests' lengths.  Request r has d_cached[r] tokens in the pool (its first
+ * ceil(cached / block_tokens) table entries) and gets d_fresh[r] new ones;
+ * d_fresh[r] = -1 says that it is finished: its blocks go back to the free
+ * list and its length becomes 0.
+ *
+ * The free list is a stack: d_free[0 .. *d_free_count) holds free block ids.
+ * First the finished requests' blocks are pushed (in request order, each in
+ * table order), then the new blocks are popped from the top, in request
+ * order.  Entries of d_free at or above the new count keep their contents, as
+ * do table entries that name no new block.
+ *   d_table [requests][table_stride]  in/out
+ *   d_free [free_capacity], d_free_count [1] -> d_free_count_out [1] (may be the same)
+ *   d_kv_len [requests]      cached + fresh (may be d_cached)
+ *   d_cu_new [requests + 1]  first new token of each request: prefix sums of the new tokens
+ *   d_slots, d_positions [max_tokens]  per new token, requests one after another; entries beyond
+ *                            the last token are -1 and 0 (rows that a padded step carries along)
+ *   d_status [4]             tokens, blocks taken, blocks given back, 0 -- or, when the step is
+ *                            refused, 0, blocks wanted, blocks given back, a sum of the reasons below
+ * A refused step changes no table, free list or count: every slot is -1, cu_new
+ * all 0, and kv_len repeats cached (0 where that is negative). */
+enum {
+  K2_PLAN_BAD_LENGTH = 1,  /* cached < 0 or fresh < -1 */
+  K2_PLAN_TABLE_FULL = 2,  /* a length beyond table_stride * block_tokens */
+  K2_PLAN_NO_BLOCKS = 4,   /* fewer free blocks than the step needs, or more free ids than free_capacity */
+  K2_PLAN_TOKENS_FULL = 8  /* more new tokens than max_tokens */
+};
+k2_status k2_paged_plan(const int32_t* d_cached, const int32_t* d_fresh, int32_t requests, int32_t block_tokens,
+                        int32_t* d_table, int32_t table_stride, int32_t* d_free, int32_t free_capacity,
+                        const int32_t* d_free_count, int32_t* d_free_count_out, int32_t* d_kv_len,
+                        int32_t* d_cu_new, int32_t* d_slots, int32_t* d_positions, int32_t max_tokens,
+                        int32_t* d_status, void* stream);
+
+/* Stores K and V rows [tokens][n_kv_heads][head_dim] (dtype K2_BF16, K2_F16 or
+ * K2_F32; heads contiguous, tokens k_stride / v_stride elements apart, so that
+ * slices of packed q|k|v rows can be given; 16-byte aligned rows) at slots
+ * d_slots[tokens]; a negative slot stores nothing.  The rows that one call adds
+ * to a block must be consecutive tokens with consecutive slots (what
+ * k2_paged_plan gives); a slot named twice leaves its block's rows undefined.
+ *
+ * Per block and KV head: with a = the largest finite magnitude among the new
+ * rows and o the first new row's place in the block, the scale becomes
+ * s' = max(o > 0 ? s : 0, a / q), q = 127 (K2_I8) or 448 (K2_F8).  If it grew,
+ * the o rows before are rounded to it, code <- round(code * (s / s')).  New rows
+ * get code = round(x / s'), clamped to +-q (infinities too), 0 for NaN or
+ * s' = 0.  All in fp32, rounded to nearest with ties to even.  So a block
+ * entered at its first row starts afresh, and a row's error is at most half a
+ * step of the block's final scale, plus half a step of each scale that it was
+ * rounded to before. */
+k2_status k2_paged_append(const k2_paged_kv* kv, const void* d_k, const void* d_v, int32_t dtype, int64_t k_stride,
+                          int64_t v_stride, const int32_t* d_slots, int32_t tokens, void* stream);
+
+/* Bytes of the workspace of k2_paged_attention on the current device (any
+ * number of requests).  Zero it once before its first use; every call leaves
+ * its counters at zero again.  Calls that may overlap on the GPU need one each. */
+size_t k2_paged_workspace_bytes(void);
+
+/* Causal attention of each request's newest tokens over its blocks.  Request
+ * r's query rows are d_q[d_cu_q[r] .. d_cu_q[r + 1]) ([tokens][n_heads][head_dim],
+ * dtype K2_BF16 or K2_F16, rows q_stride elements apart, 16-byte aligned); they
+ * are the last of its d_kv_len[r] positions, so query i of n sees keys
+ * 0 .. kv_len - n + i (already appended).  Query heads n_heads / n_kv_heads
+ * (1 .. 16) share a KV head.  d_out is written like d_q (out_stride); rows of no
+ * request are left as they were, a query that sees no key gets zeros.  max_q:
+ * the most queries of one request.  Scores scale * q.k and the softmax are held
+ * in fp32; codes and queries enter the products exactly, probabilities as
+ * fp16. */
+k2_status k2_paged_attention(const k2_paged_kv* kv, const void* d_q, int32_t dtype, int64_t q_stride,
+                             const int32_t* d_cu_q, const int32_t* d_kv_len, const int32_t* d_table,
+                             int32_t table_stride, int32_t requests, int32_t tokens, int32_t n_heads, int32_t max_q,
+                             float scale, void* d_out, int64_t out_stride, void* d_workspace, size_t ws_bytes,
+                             void* stream);
+
+/* Rules on logits that differ per row (k2_set_sampling's repetition penalty is
+ * one number for all rows and edits nothing it is given).  For row r of
+ * d_logits (fp32, ld elements apart) in this order, into d_out (may be d_logits):
+ *   1. an id among the row's tokens, ids[r * ids_stride .. + ids_len[r]):
+ *      l -> l / repetition[r] if l > 0, l * repetition[r] otherwise;
+ *   2. an id that occurs c > 0 times among the tokens from prompt_len[r] on
+ *      (the answer): l -> (l - frequency[r] * c) - presence[r];
+ *   3. bias: l -> l + bias[j] for every entry j in [bias_offset[r],
+ *      bias_offset[r + 1]) whose bias_ids[j] is the id, in the order of j;
+ *   4. grammar: -inf where bit id % 32 of word id / 32 of mask mask_row[r] is
+ *      0 (whatever the value was); no mask if mask_row[r] is outside [0, n_masks).
+ * Ids outside [0, vocab) are ignored.  NULL arrays switch a rule off (prompt_len
+ * NULL: everything is the answer; mask_row NULL: row r uses mask r).  A row whose
+ * mask leaves nothing is all -inf: k2_sample_logits then raises its guard. */
+typedef struct {
+  const float* repetition; /* [rows] > 0; nullable */
+  const float* presence;   /* [rows]; nullable */
+  const float* frequency;  /* [rows]; nullable */
+  const int32_t* ids;      /* [rows][ids_stride]; nullable with the three above */
+  int64_t ids_stride;
+  const int32_t* ids_len;    /* [rows] */
+  const int32_t* prompt_len; /* [rows]; nullable */
+  const int32_t* bias_offset; /* [rows + 1]; nullable: no biases */
+  const int32_t* bias_ids;
+  const float* bias;
+  int32_t n_bias;          /* entries of bias_ids and bias: offsets are cut to [0, n_bias] */
+  const uint32_t* mask;    /* [n_masks][mask_stride] words; nullable: no masks */
+  int64_t mask_stride;     /* >= ceil(vocab / 32) */
+  int32_t n_masks;
+  const int32_t* mask_row; /* [rows]; nullable */
+} k2_logit_rules;
+k2_status k2_adjust_logits(const k2_logit_rules* rules, const float* d_logits, int64_t ld, float* d_out,
+                           int64_t ld_out, int32_t rows, int32_t vocab, void* stream);
+
 /* ---- without a workspace ---------------------------------------------------- */
 
 /* The pages have no counterpart to this call: it exists for callers that
