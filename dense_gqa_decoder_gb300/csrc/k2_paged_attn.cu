@@ -3,6 +3,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "k2_paged.cuh"
 
@@ -22,8 +23,6 @@ struct PagedAttnArgs {
   long long out_stride;
 };
 
-constexpr int kThreads = 128, kWarps = kThreads / 32, kMaxRep = 16;
-
 template <typename T>
 __device__ __forceinline__ T from_f32(float v);
 template <>
@@ -31,26 +30,582 @@ __device__ __forceinline__ __half from_f32<__half>(float v) { return __float2hal
 template <>
 __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
+
+constexpr int kMaxRep = 16;  // query heads per KV head
+constexpr int kMaxKeys = 1 << 30;
+
+// ---- what both kernels need to know about a request -----------------------------------------
+struct Req {
+  int q0, nq, len;  // first query row, queries, keys
+  bool ok;          // consistent lengths
+};
+__device__ __forceinline__ Req request(const PagedAttnArgs& a, int block_log2, int r) {
+  Req x;
+  x.q0 = a.cu_q[r];
+  const int q1 = a.cu_q[r + 1];
+  x.len = a.kv_len[r];
+  x.ok = x.q0 >= 0 && q1 >= x.q0 && q1 <= a.tokens;
+  x.nq = x.ok ? q1 - x.q0 : 0;
+  if (x.nq > 0)
+    x.ok = x.nq <= a.max_q && x.nq <= x.len && x.len <= kMaxKeys &&
+           x.len <= (static_cast<long long>(a.table_stride) << block_log2);
+  return x;
+}
+
+__device__ __forceinline__ float exp2_approx(float x) {  // 2^x (2^-inf = 0), relative error about 2^-22
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+constexpr float kLog2e = 1.4426950408889634f;
+
+// Codes to fp16, exactly.  int8: with its sign bit flipped a code is u = c + 128,
+// and the fp16 number with the bits 0x6400 | u is 1024 + u, so one subtraction of
+// 1152 gives c.  E4M3 values are fp16 values.
+template <typename C>
+struct Widen;
+template <>
+struct Widen<CodeI8> {
+  // the word's codes as the bytes that pair() takes
+  __device__ __forceinline__ static uint32_t prep(uint32_t w) { return w ^ 0x80808080u; }
+  // bytes 0 and 1 (HI: 2 and 3) of a prepared word
+  template <bool HI>
+  __device__ __forceinline__ static uint32_t pair(uint32_t w) {
+    const uint32_t m = __byte_perm(w, 0x64646464u, HI ? 0x4342 : 0x4140);
+    const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&m), __half2half2(__ushort_as_half(0x6480)));
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+};
+template <>
+struct Widen<CodeF8> {
+  __device__ __forceinline__ static uint32_t prep(uint32_t w) { return w; }
+  template <bool HI>
+  __device__ __forceinline__ static uint32_t pair(uint32_t w) {
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(HI ? w >> 16 : w & 0xFFFFu), __NV_E4M3);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+};
+
+__device__ __forceinline__ uint32_t movmatrix(uint32_t a) {  // transpose of an 8 x 8 fp16 matrix held by the warp
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
+__device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void* src, bool take) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(take ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+  return v;
+}
+
+// Eight neighbouring query elements as fp32
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, float* f) {
+  const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
+  Unpack<T>::run(v, f);
+}
+// four outputs
+template <typename T>
+__device__ __forceinline__ void store4(T* p, float a, float b, float c, float d) {
+  T v[4] = {from_f32<T>(a), from_f32<T>(b), from_f32<T>(c), from_f32<T>(d)};
+  *reinterpret_cast<uint2*>(p) = *reinterpret_cast<const uint2*>(v);
+}
+
+// ---- few query rows per request: decode and speculative steps -------------------------------
+//
+// Memory bound: every code is read once, for rep * queries rows (2 flop per code
+// and row).  The tensor cores take the rows of a KV head together: with the rows
+// as the narrow side of mma.m16n8k16, S^T = K Q^T and O^T = V^T P^T need one MMA
+// each per 16 keys, 16 dims and 8 rows, and the codes, widened to fp16 in
+// registers, are the wide operand.  Dims may be permuted inside a dot product, so
+// a lane's codes of a K row are 32 (head_dim 64: 16) neighbouring bytes; a lane's
+// dims of V are neighbours too, and pairs of keys are interleaved by byte
+// permutes.  S^T's accumulators become P^T's operand by one 8 x 8 transpose each.
+//
+// Work is cut into tiles of 16 keys of one (request, KV head); the CTAs take
+// equal shares of all tiles of the step, whatever the lengths, which they find
+// from the lengths themselves (a prefix sum of the requests' tiles).  In a CTA
+// the warps take the tiles of a share in turn, each through a ring of its own
+// that cp.async fills ahead (no barrier inside a share).  A share that holds only
+// a part of a (request, head) leaves (maximum, sum, output) in the workspace, and
+// the CTA that arrives last joins the parts, in order.
+//
+// Query rows are scaled by a power of two to fp16's upper range (exact for bf16
+// and fp16 inputs); probabilities p enter P.V as fp16(p * (vs / vref) * 2^14), vs
+// the block's V scale and vref the largest so far, so that no block's scale costs
+// precision while the ratio stays above 2^-28.
+constexpr int kDecWarps = 4, kDecThreads = 32 * kDecWarps, kDecKeys = 16;
+constexpr int kDecMaxRows = 32;
+
+template <int D, int NT>
+struct Dec {
+  static constexpr int kRows = 8 * NT;
+  static constexpr int kStage = 2 * kDecKeys * D;                // K and V codes of a tile
+  static constexpr int kStages = D == 128 ? 3 : 6;
+  static constexpr int kRing = kStage * kStages;                 // per warp
+  static constexpr int kLd = D + 4;                              // floats of a row of the joined output
+  static constexpr int kMerge = kDecWarps * kRows * (kLd + 2) * 4;
+  static constexpr int kSmem = kRing * kDecWarps > kMerge ? kRing * kDecWarps : kMerge;
+  static constexpr int kCtas = NT == 1 ? 4 : NT == 2 ? 3 : 2;    // per SM
+};
+constexpr int kDecSlotFloats = kDecMaxRows * (128 + 2);  // one part: rows x (output, maximum, sum)
+constexpr int kDecMaxCtas = 1024;
+
+// byte offset of 16-byte chunk c of row r in a tile of D-byte rows, swizzled so
+// that the fragment reads below are free of bank conflicts
+template <int D>
+__device__ __forceinline__ int tile_at(int r, int c) {
+  if constexpr (D == 128) return r * 128 + ((c ^ (r & 7)) << 4);
+  else return (r >> 1) * 128 + (((((r & 1) << 2) | c) ^ ((r & 6))) << 4);
+}
+
+struct DecShare {  // the flat tile range of CTA c of n over `total` tiles
+  __device__ __forceinline__ static long long first(long long total, int n, int c) { return total * c / n; }
+  __device__ __forceinline__ static int cta_of(long long total, int n, long long x) {
+    int c = static_cast<int>(x * n / total);
+    while (c + 1 < n && first(total, n, c + 1) <= x) ++c;
+    while (c > 0 && first(total, n, c) > x) --c;
+    return c;
+  }
+};
+
+template <typename T, typename C, int D, int NT>
+__global__ void __launch_bounds__(kDecThreads, Dec<D, NT>::kCtas)
+    paged_decode_kernel(const PagedPool p, const PagedAttnArgs a, int small_rows, unsigned* counters, float* parts) {
+  using S = Dec<D, NT>;
+  using W = Widen<C>;
+  constexpr int KS = D / 16;        // k-steps of S^T
+  constexpr int MT = D / 16;        // m-tiles of O^T
+  constexpr int QW = D / 4;         // dims of a lane's query row
+  constexpr int VB = D / 8;         // dims of a lane's V rows
+  constexpr int NS = S::kStages;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ long long s_sum[kDecWarps];
+  __shared__ long long s_base;
+  __shared__ int s_req, s_last;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gq = lane >> 2, t = lane & 3;
+  const int rep = a.n_heads / p.n_kv;
+
+  // the tiles of every request, and this CTA's share of them
+  auto tiles_of = [&](const Req& x) -> int {
+    return x.ok && x.nq > 0 && x.nq * rep <= small_rows ? (x.len + kDecKeys - 1) / kDecKeys : 0;
+  };
+  const int per = (a.requests + kDecThreads - 1) / kDecThreads;
+  long long own = 0;
+  bool faulty = false;
+  for (int i = 0; i < per; ++i) {
+    const int r = tid * per + i;
+    if (r < a.requests) {
+      const Req x = request(a, p.block_log2, r);
+      faulty |= !x.ok;
+      own += static_cast<long long>(tiles_of(x)) * p.n_kv;
+    }
+  }
+  long long inc = own;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long u = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += u;
+  }
+  if (lane == 31) s_sum[warp] = inc;
+  faulty = __syncthreads_or(faulty) != 0;
+  long long total = 0, before = inc - own;
+#pragma unroll
+  for (int w = 0; w < kDecWarps; ++w) {
+    if (w < warp) before += s_sum[w];
+    total += s_sum[w];
+  }
+  if (faulty) {  // requests whose lengths contradict each other: zeros in their rows
+    for (int r = blockIdx.x; r < a.requests; r += gridDim.x) {
+      if (request(a, p.block_log2, r).ok) continue;
+      if (tid == 0) raise_flag(p.flags, K2_PAGED_BAD_LENGTH);
+      const int lo = max(a.cu_q[r], 0), hi = min(a.cu_q[r + 1], a.tokens), w = a.n_heads * D / 4;
+      for (long long i = tid; i < static_cast<long long>(hi - lo) * w; i += kDecThreads)
+        store4(static_cast<T*>(a.out) + (lo + i / w) * a.out_stride + 4 * (i % w), 0.f, 0.f, 0.f, 0.f);
+    }
+  }
+  if (total == 0) return;
+  // at least two tiles per warp of a CTA: fewer CTAs, fewer parts to join
+  const int ctas = static_cast<int>(min(static_cast<long long>(gridDim.x), (total + 2 * kDecWarps - 1) / (2 * kDecWarps)));
+  if (blockIdx.x >= ctas) return;
+  const long long x0 = DecShare::first(total, ctas, blockIdx.x), x1 = DecShare::first(total, ctas, blockIdx.x + 1);
+  if (before <= x0 && x0 < before + own) {  // one thread: its requests hold the share's first tile
+    long long at = before;
+    for (int i = 0; i < per; ++i) {
+      const int r = tid * per + i;
+      if (r >= a.requests) break;
+      const long long n = static_cast<long long>(tiles_of(request(a, p.block_log2, r))) * p.n_kv;
+      if (x0 < at + n) {
+        s_req = r;
+        s_base = at;
+        break;
+      }
+      at += n;
+    }
+  }
+  __syncthreads();
+  int r = s_req;
+  long long base = s_base;  // flat index of request r's first tile
+
+  uint8_t* ring = smem + warp * S::kRing;
+  const uint32_t ring_u = smem_u32(ring);
+  float* mo = reinterpret_cast<float*>(smem);                 // joined: [warp][row][kLd] outputs
+  float* mml = mo + kDecWarps * S::kRows * S::kLd;            // [warp][row] (maximum, sum)
+
+  for (long long x = x0; x < x1;) {
+    Req q = request(a, p.block_log2, r);
+    int nt = tiles_of(q);
+    while (x >= base + static_cast<long long>(nt) * p.n_kv) {
+      base += static_cast<long long>(nt) * p.n_kv;
+      q = request(a, p.block_log2, ++r);
+      nt = tiles_of(q);
+    }
+    const int g = static_cast<int>((x - base) / nt);
+    const long long item = base + static_cast<long long>(g) * nt;       // flat index of (r, g)'s first tile
+    const int ta = static_cast<int>(x - item), tb = static_cast<int>(min(static_cast<long long>(nt), x1 - item));
+    x = item + tb;
+    const int rows = q.nq * rep;
+    const int* table = a.table + static_cast<size_t>(r) * a.table_stride;
+
+    // query rows as the narrow operand: n-tile j holds rows 8j + gq, this lane their dims QW t ..
+    uint32_t qf[NT][KS][2];
+    float f0[NT], f1[NT];  // what turns an accumulator of rows 8j + 2t, + 1 into base-2 scores (times the K scale)
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      const int row = 8 * j + gq;
+      float v[QW], top = 0.f;
+      if (row < rows) {
+        const int i = row / rep, h = row - i * rep;
+        const T* src = static_cast<const T*>(a.q) + (q.q0 + i) * a.q_stride + (g * rep + h) * D + QW * t;
+#pragma unroll
+        for (int e = 0; e < QW; e += 8) load8(src + e, v + e);
+      } else {
+#pragma unroll
+        for (int e = 0; e < QW; ++e) v[e] = 0.f;
+      }
+#pragma unroll
+      for (int e = 0; e < QW; ++e) top = fmaxf(top, fabsf(v[e]));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      // 2^up brings the largest magnitude into [2^14, 2^15)
+      const int ex = static_cast<int>(__float_as_uint(top) >> 23);
+      const int up = top > 0.f && ex < 255 ? 14 + 127 - ex : 0;
+      const int ua = up / 2, ub = up - ua;  // in two steps: 2^up itself may not be a normal number
+      const float sa = __uint_as_float((127 + ua) << 23), sb = __uint_as_float((127 + ub) << 23);
+#pragma unroll
+      for (int kk = 0; kk < KS; ++kk) {
+        qf[j][kk][0] = pack_half2(v[4 * kk] * sa * sb, v[4 * kk + 1] * sa * sb);
+        qf[j][kk][1] = pack_half2(v[4 * kk + 2] * sa * sb, v[4 * kk + 3] * sa * sb);
+      }
+      const float ia = __uint_as_float((127 - ua) << 23), ib = __uint_as_float((127 - ub) << 23);
+      const float back = a.scale * kLog2e * ia * ib;
+      f0[j] = __shfl_sync(0xffffffffu, back, 8 * t);
+      f1[j] = __shfl_sync(0xffffffffu, back, 8 * t + 4);
+    }
+
+    // this warp's tiles: ta + warp + kDecWarps i, i < n; lane l holds the block and scales of tile 32 c + l
+    const int n = tb - ta > warp ? (tb - ta - warp + kDecWarps - 1) / kDecWarps : 0;
+    int id = -1, id_next = -1;
+    float ks = 0.f, vs = 0.f, ks_next = 0.f, vs_next = 0.f;
+    auto fetch_ids = [&](int c, int& d, float& k_s, float& v_s) {
+      const int i = 32 * c + lane;
+      d = -1;
+      k_s = v_s = 0.f;
+      if (i < n) {
+        d = __ldg(table + (((ta + warp + kDecWarps * i) * kDecKeys) >> p.block_log2));
+        if (d < 0 || d >= p.n_blocks) {
+          raise_flag(p.flags, K2_PAGED_BAD_BLOCK);
+          d = -1;
+        } else {
+          const size_t at = static_cast<size_t>(d) * p.n_kv + g;
+          k_s = __ldg(p.ks + at);
+          v_s = __ldg(p.vs + at);
+        }
+      }
+    };
+    fetch_ids(0, id, ks, vs);
+    if (n > 32) fetch_ids(1, id_next, ks_next, vs_next);
+    auto issue = [&](int i, int cur) {  // requests tile i; cur: the batch that id holds
+      if (i < n) {
+        const int d = __shfl_sync(0xffffffffu, (i >> 5) == cur ? id : id_next, i & 31);
+        if (d >= 0) {
+          const int key0 = (ta + warp + kDecWarps * i) * kDecKeys;
+          const size_t at = (((static_cast<size_t>(d) * p.n_kv + g) << p.block_log2) + (key0 & ((1 << p.block_log2) - 1))) * D;
+          const uint32_t dst = ring_u + (i % NS) * S::kStage;
+          constexpr int CH = D / 16;  // chunks per row
+#pragma unroll
+          for (int c0 = 0; c0 < kDecKeys * CH; c0 += 32) {
+            const int row = (c0 + lane) / CH, c = (c0 + lane) % CH;
+            const bool take = key0 + row < q.len;
+            cp_async16_zfill(dst + tile_at<D>(row, c), p.k + at + row * D + c * 16, take);
+            cp_async16_zfill(dst + kDecKeys * D + tile_at<D>(row, c), p.v + at + row * D + c * 16, take);
+          }
+        }
+      }
+      cp_async_commit();
+    };
+
+    float o[NT][MT][4], m0[NT], m1[NT], l0[NT], l1[NT], vref = 0.f;
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      m0[j] = m1[j] = -INFINITY;
+      l0[j] = l1[j] = 0.f;
+#pragma unroll
+      for (int e = 0; e < MT; ++e) o[j][e][0] = o[j][e][1] = o[j][e][2] = o[j][e][3] = 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < NS - 1; ++i) issue(i, 0);
+
+    for (int i = 0; i < n; ++i) {
+      const int cur = i >> 5;
+      if (i > 0 && (i & 31) == 0) {
+        id = id_next;
+        ks = ks_next;
+        vs = vs_next;
+        if (32 * (cur + 1) < n) fetch_ids(cur + 1, id_next, ks_next, vs_next);
+      }
+      cp_async_wait<NS - 2>();
+      __syncwarp();  // everyone's copies of tile i have landed, and everyone is done with tile i - 1
+      issue(i + NS - 1, cur);
+      const int d = __shfl_sync(0xffffffffu, id, i & 31);
+      const float k_s = __shfl_sync(0xffffffffu, ks, i & 31), v_s = __shfl_sync(0xffffffffu, vs, i & 31);
+      if (d < 0) continue;
+      const uint32_t kt = ring_u + (i % NS) * S::kStage, vt = kt + kDecKeys * D;
+      // S^T: keys gq and gq + 8 of the tile, this lane's QW dims of each
+      float sc[NT][4], sd[NT][4];
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sc[j][e] = sd[j][e] = 0.f;
+#pragma unroll
+      for (int c = 0; c < QW / 16; ++c) {
+        const uint4 ka = lds128(kt + tile_at<D>(gq, (QW / 16) * t + c));
+        const uint4 kb = lds128(kt + tile_at<D>(gq + 8, (QW / 16) * t + c));
+        const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const uint32_t xa = W::prep(wa[w]), xb = W::prep(wb[w]);
+          const uint32_t af[4] = {W::template pair<false>(xa), W::template pair<false>(xb), W::template pair<true>(xa),
+                                  W::template pair<true>(xb)};
+          const int kk = 4 * c + w;
+#pragma unroll
+          for (int j = 0; j < NT; ++j) mma16816(kk & 1 ? sd[j] : sc[j], af, qf[j][kk][0], qf[j][kk][1]);
+        }
+      }
+      // V: the reference scale, and what the block's probabilities are multiplied with
+      const float av = fabsf(v_s);
+      float shrink = 1.f;
+      if (av > vref) {
+        shrink = vref / av;
+        vref = av;
+      }
+      const float pv = vref > 0.f ? v_s * __frcp_rn(vref) * 16384.f : 0.f;
+      const int key = (ta + warp + kDecWarps * i) * kDecKeys;
+      const bool edge = key + kDecKeys > q.len - q.nq + 1;  // some row does not see all of the tile
+      uint32_t pf[NT][2];
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        const float fa = f0[j] * k_s, fb = f1[j] * k_s;
+        float s[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[e] = (sc[j][e] + sd[j][e]) * (e & 1 ? fb : fa);
+        if (edge) {
+          const int ra = 8 * j + 2 * t, first = q.len - q.nq;  // row's last key: first + row / rep
+          const int la = first + ra / rep - key, lb = first + (ra + 1) / rep - key;
+          if (gq > la) s[0] = -INFINITY;
+          if (gq > lb) s[1] = -INFINITY;
+          if (gq + 8 > la) s[2] = -INFINITY;
+          if (gq + 8 > lb) s[3] = -INFINITY;
+        }
+        float ma = fmaxf(s[0], s[2]), mb = fmaxf(s[1], s[3]);
+#pragma unroll
+        for (int sh = 4; sh < 32; sh <<= 1) {
+          ma = fmaxf(ma, __shfl_xor_sync(0xffffffffu, ma, sh));
+          mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, sh));
+        }
+        const float na = fmaxf(m0[j], ma), nb = fmaxf(m1[j], mb);
+        if (__any_sync(0xffffffffu, na > m0[j] || nb > m1[j]) || shrink != 1.f) {
+          const float ca = na == -INFINITY ? 1.f : exp2_approx(m0[j] - na), cb = nb == -INFINITY ? 1.f : exp2_approx(m1[j] - nb);
+          l0[j] *= ca;
+          l1[j] *= cb;
+#pragma unroll
+          for (int e = 0; e < MT; ++e) {
+            o[j][e][0] *= ca * shrink;
+            o[j][e][1] *= cb * shrink;
+            o[j][e][2] *= ca * shrink;
+            o[j][e][3] *= cb * shrink;
+          }
+          m0[j] = na;
+          m1[j] = nb;
+        }
+        const float za = na == -INFINITY ? 0.f : na, zb = nb == -INFINITY ? 0.f : nb;  // no key seen yet: every p is 0
+        const float p0 = exp2_approx(s[0] - za), p1 = exp2_approx(s[1] - zb), p2 = exp2_approx(s[2] - za),
+                    p3 = exp2_approx(s[3] - zb);
+        l0[j] += p0 + p2;
+        l1[j] += p1 + p3;
+        pf[j][0] = movmatrix(pack_half2(p0 * pv, p1 * pv));
+        pf[j][1] = movmatrix(pack_half2(p2 * pv, p3 * pv));
+      }
+      // O^T += V^T P^T: keys 2t, 2t + 1, 2t + 8, 2t + 9, this lane's VB dims of each
+      uint32_t vw[4][VB / 4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int row = 2 * t + (e & 1) + (e & 2) * 4;
+        if constexpr (D == 128) {
+          const uint4 v = lds128(vt + tile_at<D>(row, gq));
+          vw[e][0] = W::prep(v.x);
+          vw[e][1] = W::prep(v.y);
+          vw[e][2] = W::prep(v.z);
+          vw[e][3] = W::prep(v.w);
+        } else {
+          const uint2 v = lds64(vt + tile_at<D>(row, gq >> 1) + (gq & 1) * 8);
+          vw[e][0] = W::prep(v.x);
+          vw[e][1] = W::prep(v.y);
+        }
+      }
+#pragma unroll
+      for (int w = 0; w < VB / 4; ++w) {
+        const uint32_t xa = __byte_perm(vw[0][w], vw[1][w], 0x5140), xb = __byte_perm(vw[0][w], vw[1][w], 0x7362);
+        const uint32_t ya = __byte_perm(vw[2][w], vw[3][w], 0x5140), yb = __byte_perm(vw[2][w], vw[3][w], 0x7362);
+        const uint32_t a0[4] = {W::template pair<false>(xa), W::template pair<true>(xa), W::template pair<false>(ya),
+                                W::template pair<true>(ya)};
+        const uint32_t a1[4] = {W::template pair<false>(xb), W::template pair<true>(xb), W::template pair<false>(yb),
+                                W::template pair<true>(yb)};
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          mma16816(o[j][2 * w], a0, pf[j][0], pf[j][1]);
+          mma16816(o[j][2 * w + 1], a1, pf[j][0], pf[j][1]);
+        }
+      }
+    }
+
+    // join the warps' parts in shared memory (the rings are drained)
+    cp_async_wait<0>();
+    __syncthreads();
+    const float unit = vref * (1.f / 16384.f);
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+#pragma unroll
+      for (int sh = 4; sh < 32; sh <<= 1) {
+        l0[j] += __shfl_xor_sync(0xffffffffu, l0[j], sh);
+        l1[j] += __shfl_xor_sync(0xffffffffu, l1[j], sh);
+      }
+      const int ra = 8 * j + 2 * t;
+      float* oa = mo + (warp * S::kRows + ra) * S::kLd + VB * gq;
+      float* ob = oa + S::kLd;
+#pragma unroll
+      for (int e = 0; e < MT; ++e) {
+        *reinterpret_cast<float2*>(oa + 2 * e) = make_float2(o[j][e][0] * unit, o[j][e][2] * unit);
+        *reinterpret_cast<float2*>(ob + 2 * e) = make_float2(o[j][e][1] * unit, o[j][e][3] * unit);
+      }
+      if (gq == 0) {
+        *reinterpret_cast<float2*>(mml + 2 * (warp * S::kRows + ra)) = make_float2(m0[j], l0[j]);
+        *reinterpret_cast<float2*>(mml + 2 * (warp * S::kRows + ra + 1)) = make_float2(m1[j], l1[j]);
+      }
+    }
+    __syncthreads();
+    const bool whole = ta == 0 && tb == nt;
+    constexpr int SLOT = kDecMaxRows * (D + 2);
+    // a part's place: this CTA's slot 0 if the item began before the share, else slot 1
+    float* slot = parts + (2 * static_cast<size_t>(blockIdx.x) + (ta == 0 ? 1 : 0)) * kDecSlotFloats;
+    auto put = [&](int row, int c, float4 v, float l) {
+      const float inv = l > 0.f ? 1.f / l : 0.f;
+      const int i = row / rep, h = row - i * rep;
+      store4(static_cast<T*>(a.out) + (q.q0 + i) * a.out_stride + (g * rep + h) * D + c, v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+    };
+    for (int e = tid; e < rows * (D / 4); e += kDecThreads) {
+      const int row = e / (D / 4), c = 4 * (e % (D / 4));
+      float m = -INFINITY, l = 0.f;
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < kDecWarps; ++w) m = fmaxf(m, mml[2 * (w * S::kRows + row)]);
+#pragma unroll
+      for (int w = 0; w < kDecWarps; ++w) {
+        const float2 ml = *reinterpret_cast<const float2*>(mml + 2 * (w * S::kRows + row));
+        const float f = m > -INFINITY ? exp2_approx(ml.x - m) : 0.f;
+        const float4 u = *reinterpret_cast<const float4*>(mo + (w * S::kRows + row) * S::kLd + c);
+        l += ml.y * f;
+        v.x += u.x * f;
+        v.y += u.y * f;
+        v.z += u.z * f;
+        v.w += u.w * f;
+      }
+      if (whole) {
+        put(row, c, v, l);
+      } else {
+        *reinterpret_cast<float4*>(slot + row * D + c) = v;
+        if (c == 0) *reinterpret_cast<float2*>(slot + kDecMaxRows * D + 2 * row) = make_float2(m, l);
+      }
+    }
+    static_assert(SLOT <= kDecSlotFloats, "a part fits its slot");
+    if (!whole) {
+      // the item's parts lie with CTAs c0 .. c1; the last to arrive joins them in that order
+      const int c0 = DecShare::cta_of(total, ctas, item), c1 = DecShare::cta_of(total, ctas, item + nt - 1);
+      __threadfence();
+      __syncthreads();
+      if (tid == 0) {
+        s_last = atomicAdd(counters + c0, 1u) == static_cast<unsigned>(c1 - c0);
+        if (s_last) counters[c0] = 0u;  // as the next call wants it
+      }
+      __syncthreads();
+      if (s_last) {
+        __threadfence();
+        for (int e = tid; e < rows * (D / 4); e += kDecThreads) {
+          const int row = e / (D / 4), c = 4 * (e % (D / 4));
+          float m = -INFINITY, l = 0.f;
+          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+          for (int k = c0; k <= c1; ++k) {
+            const float* part = parts + (2 * static_cast<size_t>(k) + (k == c0 ? 1 : 0)) * kDecSlotFloats;
+            const float2 ml = __ldcg(reinterpret_cast<const float2*>(part + kDecMaxRows * D + 2 * row));
+            const float4 u = __ldcg(reinterpret_cast<const float4*>(part + row * D + c));
+            const float mn = fmaxf(m, ml.x);
+            const float fa = mn > -INFINITY ? exp2_approx(m - mn) : 0.f, fb = mn > -INFINITY ? exp2_approx(ml.x - mn) : 0.f;
+            m = mn;
+            l = l * fa + ml.y * fb;
+            v.x = v.x * fa + u.x * fb;
+            v.y = v.y * fa + u.y * fb;
+            v.z = v.z * fa + u.z * fb;
+            v.w = v.w * fa + u.w * fb;
+          }
+          put(row, c, v, l);
+        }
+      }
+    }
+    __syncthreads();  // the rings take the next item's tiles
+  }
+}
+constexpr int kThreads = 128, kWarps = kThreads / 32;
+
 // One CTA per query token and KV head: its warps take every fourth key, a lane
 // head_dim / 32 neighbouring dims; each warp keeps a running maximum, sum and
 // output per query head, merged at the end.
 template <typename T, typename C, int D>
-__global__ void __launch_bounds__(kThreads) paged_attn_simple_kernel(const PagedPool p, const PagedAttnArgs a) {
+__global__ void __launch_bounds__(kThreads) paged_attn_simple_kernel(const PagedPool p, const PagedAttnArgs a, int small_rows) {
   constexpr int E = D / 32;
   __shared__ float qs[kMaxRep][D];
   __shared__ float sm[kWarps][kMaxRep], sl[kWarps][kMaxRep], so[kWarps][kMaxRep][D];
   const int t = blockIdx.x, g = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rep = a.n_heads / p.n_kv;
-  if (t == 0 && g == 0)
-    for (int i = tid; i < a.requests; i += kThreads)
-      if (a.cu_q[i] < 0 || a.cu_q[i + 1] < a.cu_q[i] || a.cu_q[i + 1] > a.tokens) raise_flag(p.flags, K2_PAGED_BAD_LENGTH);
   int r = 0;
   while (r < a.requests && !(a.cu_q[r] <= t && t < a.cu_q[r + 1])) ++r;
   if (r == a.requests) return;
-  const int q0 = a.cu_q[r], nq = a.cu_q[r + 1] - q0, len = a.kv_len[r];
-  const bool ok = q0 >= 0 && a.cu_q[r + 1] <= a.tokens && nq <= a.max_q && nq <= len &&
-                  len <= (static_cast<long long>(a.table_stride) << p.block_log2);
-  if (!ok && tid == 0) raise_flag(p.flags, K2_PAGED_BAD_LENGTH);
+  const Req x = request(a, p.block_log2, r);
+  const int q0 = x.q0, nq = x.nq, len = x.len;
+  const bool ok = x.ok;
+  if (!ok || nq * rep <= small_rows) return;
   const int keys = ok ? len - nq + (t - q0) + 1 : 0;
   const T* q = static_cast<const T*>(a.q) + t * a.q_stride + static_cast<size_t>(g) * rep * D;
   for (int i = tid; i < rep * D; i += kThreads) qs[i / D][i % D] = to_f32(q[i]) * a.scale;
@@ -104,13 +659,61 @@ __global__ void __launch_bounds__(kThreads) paged_attn_simple_kernel(const Paged
   }
 }
 
-template <typename T, typename C>
-cudaError_t launch(const PagedPool& p, int head_dim, const PagedAttnArgs& a, cudaStream_t s) {
-  const dim3 grid(a.tokens, p.n_kv);
-  if (head_dim == 128) paged_attn_simple_kernel<T, C, 128><<<grid, kThreads, 0, s>>>(p, a);
-  else paged_attn_simple_kernel<T, C, 64><<<grid, kThreads, 0, s>>>(p, a);
+
+// ---- launches ------------------------------------------------------------------------------------
+struct Workspace {
+  unsigned* counters;
+  float* parts;
+};
+
+// opts a kernel in to its shared memory, once per device (bit `dev` of `ready`)
+cudaError_t allow_smem(const void* kernel, int bytes, int dev, std::atomic<uint64_t>& ready) {
+  const uint64_t bit = 1ull << dev;
+  if (ready.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) ready.fetch_or(bit, std::memory_order_release);
+  return e;
+}
+
+template <typename T, typename C, int D, int NT>
+cudaError_t launch_decode(const PagedPool& p, const PagedAttnArgs& a, int small_rows, const Workspace& w, int sms, int dev, cudaStream_t s) {
+  using S = Dec<D, NT>;
+  auto kernel = paged_decode_kernel<T, C, D, NT>;
+  static std::atomic<uint64_t> ready{0};
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), S::kSmem, dev, ready);
+  if (e != cudaSuccess) return e;
+  kernel<<<std::min(sms * S::kCtas, kDecMaxCtas), kDecThreads, S::kSmem, s>>>(p, a, small_rows, w.counters, w.parts);
   return cudaGetLastError();
 }
+
+template <typename T, typename C, int D>
+cudaError_t launch(const PagedPool& p, const PagedAttnArgs& a, const Workspace& w, int sms, int dev, cudaStream_t s) {
+  const int rep = a.n_heads / p.n_kv;
+  const long long most = static_cast<long long>(a.max_q) * rep;
+  // all requests with few rows: the narrowest kernel that holds them; else only the single tokens (and what
+  // fits beside them) are taken apart from the prompt chunks
+  const int small_rows = most <= 8 ? 8 : most <= 16 ? 16 : most <= kDecMaxRows ? kDecMaxRows : rep <= 8 ? 8 : 16;
+  cudaError_t e = small_rows == 8    ? launch_decode<T, C, D, 1>(p, a, small_rows, w, sms, dev, s)
+                  : small_rows == 16 ? launch_decode<T, C, D, 2>(p, a, small_rows, w, sms, dev, s)
+                                     : launch_decode<T, C, D, 4>(p, a, small_rows, w, sms, dev, s);
+  if (e != cudaSuccess || most <= small_rows) return e;
+  paged_attn_simple_kernel<T, C, D><<<dim3(a.tokens, p.n_kv), kThreads, 0, s>>>(p, a, small_rows);
+  return cudaGetLastError();
+}
+template <typename T, typename C>
+cudaError_t launch(const PagedPool& p, int head_dim, const PagedAttnArgs& a, const Workspace& w, int sms, int dev, cudaStream_t s) {
+  return head_dim == 128 ? launch<T, C, 128>(p, a, w, sms, dev, s) : launch<T, C, 64>(p, a, w, sms, dev, s);
+}
+
+// the current device and its SMs (0: none)
+int sm_count(int* dev) {
+  int n = 0;
+  *dev = 0;
+  if (cudaGetDevice(dev) != cudaSuccess || *dev < 0 || *dev >= 64) return 0;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, *dev) != cudaSuccess) return 0;
+  return n;
+}
+constexpr size_t kCounterBytes = sizeof(unsigned) * kDecMaxCtas;
 
 }  // namespace
 
@@ -120,7 +723,11 @@ using namespace k2;
 
 extern "C" {
 
-size_t k2_paged_workspace_bytes(void) { return 256; }
+size_t k2_paged_workspace_bytes(void) {
+  // two parts of a CTA's share each
+  int dev = 0;
+  return kCounterBytes + sizeof(float) * 2 * kDecSlotFloats * static_cast<size_t>(std::min(4 * sm_count(&dev), kDecMaxCtas));
+}
 
 k2_status k2_paged_attention(const k2_paged_kv* kv, const void* d_q, int32_t dtype, int64_t q_stride,
                              const int32_t* d_cu_q, const int32_t* d_kv_len, const int32_t* d_table,
@@ -162,16 +769,23 @@ k2_status k2_paged_attention(const k2_paged_kv* kv, const void* d_q, int32_t dty
               k2_paged_workspace_bytes(), ws_bytes);
     return K2_ERR_WORKSPACE;
   }
+  int dev = 0;
+  const int sms = sm_count(&dev);
+  if (sms == 0) {
+    set_error("no CUDA device");
+    return K2_ERR_CUDA;
+  }
+  const Workspace w = {static_cast<unsigned*>(d_workspace),
+                       reinterpret_cast<float*>(static_cast<uint8_t*>(d_workspace) + kCounterBytes)};
   const PagedPool p(*kv);
   const PagedAttnArgs a = {d_q, q_stride, d_cu_q, d_kv_len, d_table, table_stride, requests,
                            tokens, n_heads, std::min(max_q, tokens), scale, d_out, out_stride};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  cudaError_t e;
-  if (dtype == K2_F16)
-    e = kv->dtype == K2_I8 ? launch<__half, CodeI8>(p, kv->head_dim, a, s) : launch<__half, CodeF8>(p, kv->head_dim, a, s);
-  else
-    e = kv->dtype == K2_I8 ? launch<__nv_bfloat16, CodeI8>(p, kv->head_dim, a, s)
-                           : launch<__nv_bfloat16, CodeF8>(p, kv->head_dim, a, s);
+  const int d = kv->head_dim;
+  const cudaError_t e = dtype == K2_F16
+                            ? (kv->dtype == K2_I8 ? launch<__half, CodeI8>(p, d, a, w, sms, dev, s) : launch<__half, CodeF8>(p, d, a, w, sms, dev, s))
+                            : (kv->dtype == K2_I8 ? launch<__nv_bfloat16, CodeI8>(p, d, a, w, sms, dev, s)
+                                                  : launch<__nv_bfloat16, CodeF8>(p, d, a, w, sms, dev, s));
   if (e == cudaSuccess) return K2_OK;
   set_error("attention launch: %s", cudaGetErrorString(e));
   return K2_ERR_CUDA;

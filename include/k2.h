@@ -514,7 +514,7 @@ enum {
   K2_PAGED_BAD_BLOCK = 2,  /* a table entry outside [0, n_blocks) within a request's length: its keys
                               were left out */
   K2_PAGED_BAD_LENGTH = 4  /* cu_q not ascending or beyond the query rows, more queries than max_q or
-                              than keys, or a length beyond the table: the request's rows are zeros
+                              than keys, or a length beyond the table or 2^30: the request's rows are zeros
                               where they lie inside the query rows */
 };
 #define K2_PAGED_MAX_REQUESTS 2048
