@@ -39,9 +39,10 @@ inline k2_status check_paged_kv(const k2_paged_kv* kv) {
     set_error("n_kv_heads must be in [1, 128] and n_blocks >= 1 (got %d, %d)", kv->n_kv_heads, kv->n_blocks);
     return K2_ERR_SHAPE;
   }
-  // slots are 32-bit numbers
-  if (static_cast<int64_t>(kv->n_blocks) * kv->block_tokens > INT32_MAX) {
-    set_error("n_blocks * block_tokens must stay below 2^31");
+  // slots are 32-bit numbers, and so are the kernels' places in units of 16 rows of all heads
+  if (static_cast<int64_t>(kv->n_blocks) * kv->block_tokens > INT32_MAX ||
+      static_cast<int64_t>(kv->n_blocks) * kv->block_tokens / 16 * kv->n_kv_heads >= UINT32_MAX) {
+    set_error("n_blocks * block_tokens must stay below 2^31, and times n_kv_heads below 2^36");
     return K2_ERR_SHAPE;
   }
   return K2_OK;

@@ -94,6 +94,9 @@ __device__ __forceinline__ uint32_t movmatrix(uint32_t a) {  // transpose of an 
 __device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void* src, bool take) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(take ? 16 : 0) : "memory");
 }
+__device__ __forceinline__ void cp_async16_to(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_async_wait() {
@@ -134,9 +137,10 @@ __device__ __forceinline__ void store4(T* p, float a, float b, float c, float d)
 // dims of V are neighbours too, and pairs of keys are interleaved by byte
 // permutes.  S^T's accumulators become P^T's operand by one 8 x 8 transpose each.
 //
-// Work is cut into tiles of 16 keys of one (request, KV head); the CTAs take
+// Work is cut into tiles of 32 keys of one (request, KV head); the CTAs take
 // equal shares of all tiles of the step, whatever the lengths, which they find
-// from the lengths themselves (a prefix sum of the requests' tiles).  In a CTA
+// from the lengths themselves (a prefix sum of the requests' tiles, each item
+// counted with kDecStart more for what its start and end cost).  In a CTA
 // the warps take the tiles of a share in turn, each through a ring of its own
 // that cp.async fills ahead (no barrier inside a share).  A share that holds only
 // a part of a (request, head) leaves (maximum, sum, output) in the workspace, and
@@ -146,19 +150,23 @@ __device__ __forceinline__ void store4(T* p, float a, float b, float c, float d)
 // and fp16 inputs); probabilities p enter P.V as fp16(p * (vs / vref) * 2^14), vs
 // the block's V scale and vref the largest so far, so that no block's scale costs
 // precision while the ratio stays above 2^-28.
-constexpr int kDecWarps = 4, kDecThreads = 32 * kDecWarps, kDecKeys = 16;
+constexpr int kDecWarps = 4, kDecThreads = 32 * kDecWarps;
+constexpr int kDecKeys = 32;   // of a tile: two halves of 16, which may lie in two blocks
+constexpr int kDecStart = 4;   // an item's start and end in tiles
+constexpr int kDecShare = 8;   // smallest share: fewer CTAs for small steps, and fewer parts to join
 constexpr int kDecMaxRows = 32;
 
 template <int D, int NT>
 struct Dec {
   static constexpr int kRows = 8 * NT;
-  static constexpr int kStage = 2 * kDecKeys * D;                // K and V codes of a tile
-  static constexpr int kStages = D == 128 ? 3 : 6;
+  static constexpr int kHalf = 16 * D;                           // K (or V) codes of half a tile
+  static constexpr int kStage = 4 * kHalf;                       // K half 0, K half 1, V half 0, V half 1
+  static constexpr int kStages = D == 128 ? 2 : 4;
   static constexpr int kRing = kStage * kStages;                 // per warp
   static constexpr int kLd = D + 4;                              // floats of a row of the joined output
   static constexpr int kMerge = kDecWarps * kRows * (kLd + 2) * 4;
   static constexpr int kSmem = kRing * kDecWarps > kMerge ? kRing * kDecWarps : kMerge;
-  static constexpr int kCtas = NT == 1 ? 4 : NT == 2 ? 3 : 2;    // per SM
+  static constexpr int kCtas = NT <= 2 ? 3 : 2;                  // per SM
 };
 constexpr int kDecSlotFloats = kDecMaxRows * (128 + 2);  // one part: rows x (output, maximum, sum)
 constexpr int kDecMaxCtas = 1024;
@@ -202,6 +210,7 @@ __global__ void __launch_bounds__(kDecThreads, Dec<D, NT>::kCtas)
   auto tiles_of = [&](const Req& x) -> int {
     return x.ok && x.nq > 0 && x.nq * rep <= small_rows ? (x.len + kDecKeys - 1) / kDecKeys : 0;
   };
+  auto units_of = [&](int tiles) -> long long { return tiles ? static_cast<long long>(tiles + kDecStart) * p.n_kv : 0; };
   const int per = (a.requests + kDecThreads - 1) / kDecThreads;
   long long own = 0;
   bool faulty = false;
@@ -210,7 +219,7 @@ __global__ void __launch_bounds__(kDecThreads, Dec<D, NT>::kCtas)
     if (r < a.requests) {
       const Req x = request(a, p.block_log2, r);
       faulty |= !x.ok;
-      own += static_cast<long long>(tiles_of(x)) * p.n_kv;
+      own += units_of(tiles_of(x));
     }
   }
   long long inc = own;
@@ -237,16 +246,15 @@ __global__ void __launch_bounds__(kDecThreads, Dec<D, NT>::kCtas)
     }
   }
   if (total == 0) return;
-  // at least two tiles per warp of a CTA: fewer CTAs, fewer parts to join
-  const int ctas = static_cast<int>(min(static_cast<long long>(gridDim.x), (total + 2 * kDecWarps - 1) / (2 * kDecWarps)));
+  const int ctas = static_cast<int>(min(static_cast<long long>(gridDim.x), (total + kDecShare - 1) / kDecShare));
   if (blockIdx.x >= ctas) return;
   const long long x0 = DecShare::first(total, ctas, blockIdx.x), x1 = DecShare::first(total, ctas, blockIdx.x + 1);
-  if (before <= x0 && x0 < before + own) {  // one thread: its requests hold the share's first tile
+  if (before <= x0 && x0 < before + own) {  // one thread: its requests hold the share's first unit
     long long at = before;
     for (int i = 0; i < per; ++i) {
       const int r = tid * per + i;
       if (r >= a.requests) break;
-      const long long n = static_cast<long long>(tiles_of(request(a, p.block_log2, r))) * p.n_kv;
+      const long long n = units_of(tiles_of(request(a, p.block_log2, r)));
       if (x0 < at + n) {
         s_req = r;
         s_base = at;
@@ -257,27 +265,96 @@ __global__ void __launch_bounds__(kDecThreads, Dec<D, NT>::kCtas)
   }
   __syncthreads();
   int r = s_req;
-  long long base = s_base;  // flat index of request r's first tile
+  long long base = s_base;  // flat index of request r's first unit
 
-  uint8_t* ring = smem + warp * S::kRing;
-  const uint32_t ring_u = smem_u32(ring);
+  const uint32_t ring_u = smem_u32(smem + warp * S::kRing);
   float* mo = reinterpret_cast<float*>(smem);                 // joined: [warp][row][kLd] outputs
   float* mml = mo + kDecWarps * S::kRows * S::kLd;            // [warp][row] (maximum, sum)
+
+  // where this lane's 16-byte chunks of half a tile go: chunk c0 + lane of 16 D / 16 (the rows lie one after another)
+  constexpr int CP = D / 32;  // chunks per lane
+  uint32_t put_at[CP];
+  int row_of[CP];
+#pragma unroll
+  for (int c = 0; c < CP; ++c) {
+    row_of[c] = (32 * c + lane) / (D / 16);
+    put_at[c] = ring_u + tile_at<D>(row_of[c], (32 * c + lane) % (D / 16));
+  }
+  const uint8_t* src_k = p.k + 16 * lane;
+  const uint8_t* src_v = p.v + 16 * lane;
 
   for (long long x = x0; x < x1;) {
     Req q = request(a, p.block_log2, r);
     int nt = tiles_of(q);
-    while (x >= base + static_cast<long long>(nt) * p.n_kv) {
-      base += static_cast<long long>(nt) * p.n_kv;
+    while (x >= base + units_of(nt)) {
+      base += units_of(nt);
       q = request(a, p.block_log2, ++r);
       nt = tiles_of(q);
     }
-    const int g = static_cast<int>((x - base) / nt);
-    const long long item = base + static_cast<long long>(g) * nt;       // flat index of (r, g)'s first tile
-    const int ta = static_cast<int>(x - item), tb = static_cast<int>(min(static_cast<long long>(nt), x1 - item));
-    x = item + tb;
+    const int g = static_cast<int>((x - base) / (nt + kDecStart));
+    const long long item = base + static_cast<long long>(g) * (nt + kDecStart) + kDecStart;  // unit of (r, g)'s first tile
+    const int ta = static_cast<int>(max(x0 - item, 0ll)), tb = static_cast<int>(min(static_cast<long long>(nt), x1 - item));
+    x = item + nt;
+    if (ta >= tb) continue;
     const int rows = q.nq * rep;
     const int* table = a.table + static_cast<size_t>(r) * a.table_stride;
+
+    // this warp's tiles: ta + warp + kDecWarps i, i < n; lane l holds half l of 16 tiles: its place in the pool in
+    // units of 16 rows (~0: no such block) and its scales
+    const int n = tb - ta > warp ? (tb - ta - warp + kDecWarps - 1) / kDecWarps : 0;
+    const int first = ta + warp;
+    unsigned at = ~0u, at_next = ~0u;
+    float ks = 0.f, vs = 0.f, ks_next = 0.f, vs_next = 0.f;
+    auto fetch = [&](int c, unsigned& d, float& k_s, float& v_s) {
+      const int i = 16 * c + (lane >> 1), key0 = (first + kDecWarps * i) * kDecKeys + 16 * (lane & 1);
+      d = ~0u;
+      k_s = v_s = 0.f;
+      if (i < n && key0 < q.len) {
+        const int id = __ldg(table + (key0 >> p.block_log2));
+        if (id < 0 || id >= p.n_blocks) {
+          raise_flag(p.flags, K2_PAGED_BAD_BLOCK);
+        } else {
+          const unsigned b = static_cast<unsigned>(id) * p.n_kv + g;
+          d = (b << (p.block_log2 - 4)) + ((key0 & ((1 << p.block_log2) - 1)) >> 4);
+          k_s = __ldg(p.ks + b);
+          v_s = __ldg(p.vs + b);
+        }
+      }
+    };
+    fetch(0, at, ks, vs);
+    if (n > 16) fetch(1, at_next, ks_next, vs_next);
+    auto issue = [&](int i, int stage, int cur) {  // requests tile i into a stage; cur: the batch that `at` holds
+      if (i < n) {
+        const bool next = (i >> 4) != cur;
+        const int key0 = (first + kDecWarps * i) * kDecKeys;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const unsigned d = __shfl_sync(0xffffffffu, next ? at_next : at, (2 * i + h) & 31);
+          const int left = d == ~0u ? 0 : q.len - key0 - 16 * h;  // rows of this half (the others become zeros)
+          const size_t off = d == ~0u ? 0 : static_cast<size_t>(d) * S::kHalf;
+          const uint8_t* kp = src_k + off;
+          const uint8_t* vp = src_v + off;
+          const uint32_t st = stage * S::kStage + h * S::kHalf;
+          if (left >= 16) {
+#pragma unroll
+            for (int c = 0; c < CP; ++c) {
+              cp_async16_to(put_at[c] + st, kp + 512 * c);
+              cp_async16_to(put_at[c] + st + 2 * S::kHalf, vp + 512 * c);
+            }
+          } else {
+#pragma unroll
+            for (int c = 0; c < CP; ++c) {
+              const bool take = row_of[c] < left;
+              cp_async16_zfill(put_at[c] + st, take ? kp + 512 * c : p.k, take);
+              cp_async16_zfill(put_at[c] + st + 2 * S::kHalf, take ? vp + 512 * c : p.v, take);
+            }
+          }
+        }
+      }
+      cp_async_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < NS - 1; ++i) issue(i, i, 0);
 
     // query rows as the narrow operand: n-tile j holds rows 8j + gq, this lane their dims QW t ..
     uint32_t qf[NT][KS][2];
@@ -315,49 +392,7 @@ __global__ void __launch_bounds__(kDecThreads, Dec<D, NT>::kCtas)
       f1[j] = __shfl_sync(0xffffffffu, back, 8 * t + 4);
     }
 
-    // this warp's tiles: ta + warp + kDecWarps i, i < n; lane l holds the block and scales of tile 32 c + l
-    const int n = tb - ta > warp ? (tb - ta - warp + kDecWarps - 1) / kDecWarps : 0;
-    int id = -1, id_next = -1;
-    float ks = 0.f, vs = 0.f, ks_next = 0.f, vs_next = 0.f;
-    auto fetch_ids = [&](int c, int& d, float& k_s, float& v_s) {
-      const int i = 32 * c + lane;
-      d = -1;
-      k_s = v_s = 0.f;
-      if (i < n) {
-        d = __ldg(table + (((ta + warp + kDecWarps * i) * kDecKeys) >> p.block_log2));
-        if (d < 0 || d >= p.n_blocks) {
-          raise_flag(p.flags, K2_PAGED_BAD_BLOCK);
-          d = -1;
-        } else {
-          const size_t at = static_cast<size_t>(d) * p.n_kv + g;
-          k_s = __ldg(p.ks + at);
-          v_s = __ldg(p.vs + at);
-        }
-      }
-    };
-    fetch_ids(0, id, ks, vs);
-    if (n > 32) fetch_ids(1, id_next, ks_next, vs_next);
-    auto issue = [&](int i, int cur) {  // requests tile i; cur: the batch that id holds
-      if (i < n) {
-        const int d = __shfl_sync(0xffffffffu, (i >> 5) == cur ? id : id_next, i & 31);
-        if (d >= 0) {
-          const int key0 = (ta + warp + kDecWarps * i) * kDecKeys;
-          const size_t at = (((static_cast<size_t>(d) * p.n_kv + g) << p.block_log2) + (key0 & ((1 << p.block_log2) - 1))) * D;
-          const uint32_t dst = ring_u + (i % NS) * S::kStage;
-          constexpr int CH = D / 16;  // chunks per row
-#pragma unroll
-          for (int c0 = 0; c0 < kDecKeys * CH; c0 += 32) {
-            const int row = (c0 + lane) / CH, c = (c0 + lane) % CH;
-            const bool take = key0 + row < q.len;
-            cp_async16_zfill(dst + tile_at<D>(row, c), p.k + at + row * D + c * 16, take);
-            cp_async16_zfill(dst + kDecKeys * D + tile_at<D>(row, c), p.v + at + row * D + c * 16, take);
-          }
-        }
-      }
-      cp_async_commit();
-    };
-
-    float o[NT][MT][4], m0[NT], m1[NT], l0[NT], l1[NT], vref = 0.f;
+    float o[NT][MT][4], m0[NT], m1[NT], l0[NT], l1[NT], vref = 0.f, vinv = 0.f;
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
       m0[j] = m1[j] = -INFINITY;
@@ -365,78 +400,92 @@ __global__ void __launch_bounds__(kDecThreads, Dec<D, NT>::kCtas)
 #pragma unroll
       for (int e = 0; e < MT; ++e) o[j][e][0] = o[j][e][1] = o[j][e][2] = o[j][e][3] = 0.f;
     }
-#pragma unroll
-    for (int i = 0; i < NS - 1; ++i) issue(i, 0);
 
+    int stage = 0, ahead = NS - 1;  // of tile i, of tile i + NS - 1
     for (int i = 0; i < n; ++i) {
-      const int cur = i >> 5;
-      if (i > 0 && (i & 31) == 0) {
-        id = id_next;
+      const int cur = i >> 4;
+      if (i > 0 && (i & 15) == 0) {
+        at = at_next;
         ks = ks_next;
         vs = vs_next;
-        if (32 * (cur + 1) < n) fetch_ids(cur + 1, id_next, ks_next, vs_next);
+        if (16 * (cur + 1) < n) fetch(cur + 1, at_next, ks_next, vs_next);
       }
       cp_async_wait<NS - 2>();
       __syncwarp();  // everyone's copies of tile i have landed, and everyone is done with tile i - 1
-      issue(i + NS - 1, cur);
-      const int d = __shfl_sync(0xffffffffu, id, i & 31);
-      const float k_s = __shfl_sync(0xffffffffu, ks, i & 31), v_s = __shfl_sync(0xffffffffu, vs, i & 31);
-      if (d < 0) continue;
-      const uint32_t kt = ring_u + (i % NS) * S::kStage, vt = kt + kDecKeys * D;
-      // S^T: keys gq and gq + 8 of the tile, this lane's QW dims of each
-      float sc[NT][4], sd[NT][4];
+      issue(i + NS - 1, ahead, cur);
+      const uint32_t kt = ring_u + stage * S::kStage, vt = kt + 2 * S::kHalf;
+      ahead = ahead + 1 == NS ? 0 : ahead + 1;
+      stage = stage + 1 == NS ? 0 : stage + 1;
+      float k_s[2], v_s[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        k_s[h] = __shfl_sync(0xffffffffu, ks, (2 * i + h) & 31);
+        v_s[h] = __shfl_sync(0xffffffffu, vs, (2 * i + h) & 31);
+      }
+      // S^T: keys gq and gq + 8 of each half, this lane's QW dims of each
+      float sc[NT][8];
 #pragma unroll
       for (int j = 0; j < NT; ++j)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) sc[j][e] = sd[j][e] = 0.f;
+        for (int e = 0; e < 8; ++e) sc[j][e] = 0.f;
 #pragma unroll
       for (int c = 0; c < QW / 16; ++c) {
-        const uint4 ka = lds128(kt + tile_at<D>(gq, (QW / 16) * t + c));
-        const uint4 kb = lds128(kt + tile_at<D>(gq + 8, (QW / 16) * t + c));
-        const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          const uint32_t xa = W::prep(wa[w]), xb = W::prep(wb[w]);
-          const uint32_t af[4] = {W::template pair<false>(xa), W::template pair<false>(xb), W::template pair<true>(xa),
-                                  W::template pair<true>(xb)};
-          const int kk = 4 * c + w;
+        for (int h = 0; h < 2; ++h) {
+          const uint4 ka = lds128(kt + h * S::kHalf + tile_at<D>(gq, (QW / 16) * t + c));
+          const uint4 kb = lds128(kt + h * S::kHalf + tile_at<D>(gq + 8, (QW / 16) * t + c));
+          const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
 #pragma unroll
-          for (int j = 0; j < NT; ++j) mma16816(kk & 1 ? sd[j] : sc[j], af, qf[j][kk][0], qf[j][kk][1]);
+          for (int w = 0; w < 4; ++w) {
+            const uint32_t xa = W::prep(wa[w]), xb = W::prep(wb[w]);
+            const uint32_t af[4] = {W::template pair<false>(xa), W::template pair<false>(xb), W::template pair<true>(xa),
+                                    W::template pair<true>(xb)};
+#pragma unroll
+            for (int j = 0; j < NT; ++j) mma16816(sc[j] + 4 * h, af, qf[j][4 * c + w][0], qf[j][4 * c + w][1]);
+          }
         }
       }
-      // V: the reference scale, and what the block's probabilities are multiplied with
-      const float av = fabsf(v_s);
+      // V: the reference scale, and what each half's probabilities are multiplied with
+      const float av = fmaxf(fabsf(v_s[0]), fabsf(v_s[1]));
       float shrink = 1.f;
       if (av > vref) {
-        shrink = vref / av;
+        shrink = vref * __frcp_rn(av);
         vref = av;
+        vinv = __frcp_rn(av) * 16384.f;
       }
-      const float pv = vref > 0.f ? v_s * __frcp_rn(vref) * 16384.f : 0.f;
-      const int key = (ta + warp + kDecWarps * i) * kDecKeys;
-      const bool edge = key + kDecKeys > q.len - q.nq + 1;  // some row does not see all of the tile
-      uint32_t pf[NT][2];
+      const int key = (first + kDecWarps * i) * kDecKeys;
+      // some row does not see all of the tile, or a half is missing
+      const bool edge = key + kDecKeys > q.len - q.nq + 1 || __shfl_sync(0xffffffffu, at, (2 * i) & 31) == ~0u ||
+                        __shfl_sync(0xffffffffu, at, (2 * i + 1) & 31) == ~0u;
+      uint32_t pf[NT][4];
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
-        const float fa = f0[j] * k_s, fb = f1[j] * k_s;
-        float s[4];
+        float s[8];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[e] = (sc[j][e] + sd[j][e]) * (e & 1 ? fb : fa);
-        if (edge) {
-          const int ra = 8 * j + 2 * t, first = q.len - q.nq;  // row's last key: first + row / rep
-          const int la = first + ra / rep - key, lb = first + (ra + 1) / rep - key;
-          if (gq > la) s[0] = -INFINITY;
-          if (gq > lb) s[1] = -INFINITY;
-          if (gq + 8 > la) s[2] = -INFINITY;
-          if (gq + 8 > lb) s[3] = -INFINITY;
+        for (int h = 0; h < 2; ++h) {
+          const float fa = f0[j] * k_s[h], fb = f1[j] * k_s[h];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[4 * h + e] = sc[j][4 * h + e] * (e & 1 ? fb : fa);
         }
-        float ma = fmaxf(s[0], s[2]), mb = fmaxf(s[1], s[3]);
+        if (edge) {
+          const int ra = 8 * j + 2 * t, seen = q.len - q.nq;  // a row's last key: seen + row / rep
+          const int la = seen + ra / rep - key, lb = seen + (ra + 1) / rep - key;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const bool off = __shfl_sync(0xffffffffu, at, (2 * i + h) & 31) == ~0u;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (off || 16 * h + gq + (e & 2) * 4 > (e & 1 ? lb : la)) s[4 * h + e] = -INFINITY;
+          }
+        }
+        float ma = fmaxf(fmaxf(s[0], s[2]), fmaxf(s[4], s[6])), mb = fmaxf(fmaxf(s[1], s[3]), fmaxf(s[5], s[7]));
 #pragma unroll
         for (int sh = 4; sh < 32; sh <<= 1) {
           ma = fmaxf(ma, __shfl_xor_sync(0xffffffffu, ma, sh));
           mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, sh));
         }
-        const float na = fmaxf(m0[j], ma), nb = fmaxf(m1[j], mb);
-        if (__any_sync(0xffffffffu, na > m0[j] || nb > m1[j]) || shrink != 1.f) {
+        if (__any_sync(0xffffffffu, ma > m0[j] || mb > m1[j]) || shrink != 1.f) {
+          const float na = fmaxf(m0[j], ma), nb = fmaxf(m1[j], mb);
           const float ca = na == -INFINITY ? 1.f : exp2_approx(m0[j] - na), cb = nb == -INFINITY ? 1.f : exp2_approx(m1[j] - nb);
           l0[j] *= ca;
           l1[j] *= cb;
@@ -450,43 +499,50 @@ __global__ void __launch_bounds__(kDecThreads, Dec<D, NT>::kCtas)
           m0[j] = na;
           m1[j] = nb;
         }
-        const float za = na == -INFINITY ? 0.f : na, zb = nb == -INFINITY ? 0.f : nb;  // no key seen yet: every p is 0
-        const float p0 = exp2_approx(s[0] - za), p1 = exp2_approx(s[1] - zb), p2 = exp2_approx(s[2] - za),
-                    p3 = exp2_approx(s[3] - zb);
-        l0[j] += p0 + p2;
-        l1[j] += p1 + p3;
-        pf[j][0] = movmatrix(pack_half2(p0 * pv, p1 * pv));
-        pf[j][1] = movmatrix(pack_half2(p2 * pv, p3 * pv));
-      }
-      // O^T += V^T P^T: keys 2t, 2t + 1, 2t + 8, 2t + 9, this lane's VB dims of each
-      uint32_t vw[4][VB / 4];
+        const float za = m0[j] == -INFINITY ? 0.f : m0[j], zb = m1[j] == -INFINITY ? 0.f : m1[j];  // no key seen yet: every p is 0
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int row = 2 * t + (e & 1) + (e & 2) * 4;
-        if constexpr (D == 128) {
-          const uint4 v = lds128(vt + tile_at<D>(row, gq));
-          vw[e][0] = W::prep(v.x);
-          vw[e][1] = W::prep(v.y);
-          vw[e][2] = W::prep(v.z);
-          vw[e][3] = W::prep(v.w);
-        } else {
-          const uint2 v = lds64(vt + tile_at<D>(row, gq >> 1) + (gq & 1) * 8);
-          vw[e][0] = W::prep(v.x);
-          vw[e][1] = W::prep(v.y);
+        for (int e = 0; e < 8; ++e) s[e] = exp2_approx(s[e] - (e & 1 ? zb : za));
+        l0[j] += (s[0] + s[2]) + (s[4] + s[6]);
+        l1[j] += (s[1] + s[3]) + (s[5] + s[7]);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float pv = v_s[h] * vinv;
+          pf[j][2 * h] = movmatrix(pack_half2(s[4 * h] * pv, s[4 * h + 1] * pv));
+          pf[j][2 * h + 1] = movmatrix(pack_half2(s[4 * h + 2] * pv, s[4 * h + 3] * pv));
         }
       }
+      // O^T += V^T P^T: keys 2t, 2t + 1, 2t + 8, 2t + 9 of each half, this lane's VB dims of each
 #pragma unroll
-      for (int w = 0; w < VB / 4; ++w) {
-        const uint32_t xa = __byte_perm(vw[0][w], vw[1][w], 0x5140), xb = __byte_perm(vw[0][w], vw[1][w], 0x7362);
-        const uint32_t ya = __byte_perm(vw[2][w], vw[3][w], 0x5140), yb = __byte_perm(vw[2][w], vw[3][w], 0x7362);
-        const uint32_t a0[4] = {W::template pair<false>(xa), W::template pair<true>(xa), W::template pair<false>(ya),
-                                W::template pair<true>(ya)};
-        const uint32_t a1[4] = {W::template pair<false>(xb), W::template pair<true>(xb), W::template pair<false>(yb),
-                                W::template pair<true>(yb)};
+      for (int h = 0; h < 2; ++h) {
+        uint32_t vw[4][VB / 4];
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          mma16816(o[j][2 * w], a0, pf[j][0], pf[j][1]);
-          mma16816(o[j][2 * w + 1], a1, pf[j][0], pf[j][1]);
+        for (int e = 0; e < 4; ++e) {
+          const int row = 2 * t + (e & 1) + (e & 2) * 4;
+          if constexpr (D == 128) {
+            const uint4 v = lds128(vt + h * S::kHalf + tile_at<D>(row, gq));
+            vw[e][0] = W::prep(v.x);
+            vw[e][1] = W::prep(v.y);
+            vw[e][2] = W::prep(v.z);
+            vw[e][3] = W::prep(v.w);
+          } else {
+            const uint2 v = lds64(vt + h * S::kHalf + tile_at<D>(row, gq >> 1) + (gq & 1) * 8);
+            vw[e][0] = W::prep(v.x);
+            vw[e][1] = W::prep(v.y);
+          }
+        }
+#pragma unroll
+        for (int w = 0; w < VB / 4; ++w) {
+          const uint32_t xa = __byte_perm(vw[0][w], vw[1][w], 0x5140), xb = __byte_perm(vw[0][w], vw[1][w], 0x7362);
+          const uint32_t ya = __byte_perm(vw[2][w], vw[3][w], 0x5140), yb = __byte_perm(vw[2][w], vw[3][w], 0x7362);
+          const uint32_t a0[4] = {W::template pair<false>(xa), W::template pair<true>(xa), W::template pair<false>(ya),
+                                  W::template pair<true>(ya)};
+          const uint32_t a1[4] = {W::template pair<false>(xb), W::template pair<true>(xb), W::template pair<false>(yb),
+                                  W::template pair<true>(yb)};
+#pragma unroll
+          for (int j = 0; j < NT; ++j) {
+            mma16816(o[j][2 * w], a0, pf[j][2 * h], pf[j][2 * h + 1]);
+            mma16816(o[j][2 * w + 1], a1, pf[j][2 * h], pf[j][2 * h + 1]);
+          }
         }
       }
     }
@@ -517,7 +573,6 @@ __global__ void __launch_bounds__(kDecThreads, Dec<D, NT>::kCtas)
     }
     __syncthreads();
     const bool whole = ta == 0 && tb == nt;
-    constexpr int SLOT = kDecMaxRows * (D + 2);
     // a part's place: this CTA's slot 0 if the item began before the share, else slot 1
     float* slot = parts + (2 * static_cast<size_t>(blockIdx.x) + (ta == 0 ? 1 : 0)) * kDecSlotFloats;
     auto put = [&](int row, int c, float4 v, float l) {
@@ -549,7 +604,6 @@ __global__ void __launch_bounds__(kDecThreads, Dec<D, NT>::kCtas)
         if (c == 0) *reinterpret_cast<float2*>(slot + kDecMaxRows * D + 2 * row) = make_float2(m, l);
       }
     }
-    static_assert(SLOT <= kDecSlotFloats, "a part fits its slot");
     if (!whole) {
       // the item's parts lie with CTAs c0 .. c1; the last to arrive joins them in that order
       const int c0 = DecShare::cta_of(total, ctas, item), c1 = DecShare::cta_of(total, ctas, item + nt - 1);
@@ -562,25 +616,37 @@ __global__ void __launch_bounds__(kDecThreads, Dec<D, NT>::kCtas)
       __syncthreads();
       if (s_last) {
         __threadfence();
+        const int np = c1 - c0 + 1;
+        auto part = [&](int k) { return parts + (2 * static_cast<size_t>(c0 + k) + (k == 0 ? 1 : 0)) * kDecSlotFloats; };
+        float* wt = reinterpret_cast<float*>(smem);  // [row][np] what each part's output is multiplied with
+        __shared__ float s_inv[kDecMaxRows];
+        for (int row = warp; row < rows; row += kDecWarps) {
+          float m = -INFINITY, l = 0.f;
+          for (int k = lane; k < np; k += 32) m = fmaxf(m, __ldcg(part(k) + kDecMaxRows * D + 2 * row));
+          m = warp_max(m);
+          for (int k = lane; k < np; k += 32) {
+            const float2 ml = __ldcg(reinterpret_cast<const float2*>(part(k) + kDecMaxRows * D + 2 * row));
+            const float f = m > -INFINITY ? exp2_approx(ml.x - m) : 0.f;
+            wt[row * np + k] = f;
+            l += ml.y * f;
+          }
+          l = warp_sum(l);
+          if (lane == 0) s_inv[row] = l;
+        }
+        __syncthreads();
         for (int e = tid; e < rows * (D / 4); e += kDecThreads) {
           const int row = e / (D / 4), c = 4 * (e % (D / 4));
-          float m = -INFINITY, l = 0.f;
           float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-          for (int k = c0; k <= c1; ++k) {
-            const float* part = parts + (2 * static_cast<size_t>(k) + (k == c0 ? 1 : 0)) * kDecSlotFloats;
-            const float2 ml = __ldcg(reinterpret_cast<const float2*>(part + kDecMaxRows * D + 2 * row));
-            const float4 u = __ldcg(reinterpret_cast<const float4*>(part + row * D + c));
-            const float mn = fmaxf(m, ml.x);
-            const float fa = mn > -INFINITY ? exp2_approx(m - mn) : 0.f, fb = mn > -INFINITY ? exp2_approx(ml.x - mn) : 0.f;
-            m = mn;
-            l = l * fa + ml.y * fb;
-            v.x = v.x * fa + u.x * fb;
-            v.y = v.y * fa + u.y * fb;
-            v.z = v.z * fa + u.z * fb;
-            v.w = v.w * fa + u.w * fb;
+#pragma unroll 8
+          for (int k = 0; k < np; ++k) {
+            const float4 u = __ldcg(reinterpret_cast<const float4*>(part(k) + row * D + c));
+            const float f = wt[row * np + k];
+            v.x += u.x * f;
+            v.y += u.y * f;
+            v.z += u.z * f;
+            v.w += u.w * f;
           }
-          put(row, c, v, l);
+          put(row, c, v, s_inv[row]);
         }
       }
     }
