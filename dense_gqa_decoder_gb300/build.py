@@ -16,7 +16,8 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libk2.so")
 SOURCES = ["k2_capi.cu", "k2_sample.cu", "k2_gemv.cu", "k2_gemv_packed.cu", "k2_attn.cu", "k2_misc.cu", "k2_noalloc.cu", "k2_mega.cu",
-           "k2_tcgemm.cu", "k2_prefill.cu", "k2_paged.cu", "k2_paged_attn.cu", "k2_rules.cu"]
+           "k2_tcgemm.cu", "k2_prefill.cu", "k2_paged.cu", "k2_paged_attn.cu", "k2_paged_chunk.cu",
+           "k2_rules.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-cudart", "shared",
          "--expt-relaxed-constexpr"]

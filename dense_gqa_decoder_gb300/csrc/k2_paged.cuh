@@ -3,7 +3,10 @@
 #pragma once
 
 #include <cuda_runtime.h>
+#include <math.h>
 #include <stdint.h>
+
+#include <atomic>
 
 #include "../../include/k2.h"
 #include "k2_common.cuh"
@@ -95,5 +98,143 @@ __device__ __forceinline__ uint32_t quantize(float x, float s) {
   const float y = __fdiv_rn(x, s);
   return s > 0.f && y == y ? C::round(y) : 0u;
 }
+
+// ---- attention: what its two kernels share ---------------------------------------------------
+
+struct PagedAttnArgs {
+  const void* q;
+  long long q_stride;
+  const int* cu_q;
+  const int* kv_len;
+  const int* table;
+  int table_stride, requests, tokens, n_heads, max_q;
+  float scale;
+  void* out;
+  long long out_stride;
+};
+
+template <typename T>
+__device__ __forceinline__ T from_f32(float v);
+template <>
+__device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+
+
+constexpr int kMaxRep = 16;  // query heads per KV head
+constexpr int kMaxKeys = 1 << 30;
+
+// ---- what both kernels need to know about a request -----------------------------------------
+struct Req {
+  int q0, nq, len;  // first query row, queries, keys
+  bool ok;          // consistent lengths
+};
+__device__ __forceinline__ Req request(const PagedAttnArgs& a, int block_log2, int r) {
+  Req x;
+  x.q0 = a.cu_q[r];
+  const int q1 = a.cu_q[r + 1];
+  x.len = a.kv_len[r];
+  x.ok = x.q0 >= 0 && q1 >= x.q0 && q1 <= a.tokens;
+  x.nq = x.ok ? q1 - x.q0 : 0;
+  if (x.nq > 0)
+    x.ok = x.nq <= a.max_q && x.nq <= x.len && x.len <= kMaxKeys &&
+           x.len <= (static_cast<long long>(a.table_stride) << block_log2);
+  return x;
+}
+
+__device__ __forceinline__ float exp2_approx(float x) {  // 2^x (2^-inf = 0), relative error about 2^-22
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+constexpr float kLog2e = 1.4426950408889634f;
+
+// Codes to fp16, exactly.  int8: with its sign bit flipped a code is u = c + 128,
+// and the fp16 number with the bits 0x6400 | u is 1024 + u, so one subtraction of
+// 1152 gives c.  E4M3 values are fp16 values.
+template <typename C>
+struct Widen;
+template <>
+struct Widen<CodeI8> {
+  // the word's codes as the bytes that pair() takes
+  __device__ __forceinline__ static uint32_t prep(uint32_t w) { return w ^ 0x80808080u; }
+  // bytes 0 and 1 (HI: 2 and 3) of a prepared word
+  template <bool HI>
+  __device__ __forceinline__ static uint32_t pair(uint32_t w) {
+    const uint32_t m = __byte_perm(w, 0x64646464u, HI ? 0x4342 : 0x4140);
+    const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&m), __half2half2(__ushort_as_half(0x6480)));
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+};
+template <>
+struct Widen<CodeF8> {
+  __device__ __forceinline__ static uint32_t prep(uint32_t w) { return w; }
+  template <bool HI>
+  __device__ __forceinline__ static uint32_t pair(uint32_t w) {
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(HI ? w >> 16 : w & 0xFFFFu), __NV_E4M3);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+};
+
+__device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void* src, bool take) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(take ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async16_to(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void cp_async4(void* dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+
+// Eight neighbouring query elements as fp32
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, float* f) {
+  const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
+  Unpack<T>::run(v, f);
+}
+// four outputs
+template <typename T>
+__device__ __forceinline__ void store4(T* p, float a, float b, float c, float d) {
+  T v[4] = {from_f32<T>(a), from_f32<T>(b), from_f32<T>(c), from_f32<T>(d)};
+  *reinterpret_cast<uint2*>(p) = *reinterpret_cast<const uint2*>(v);
+}
+
+struct Share {  // equal shares of `total` units of work: the first unit of CTA c of n, and the CTA of unit x
+  __device__ __forceinline__ static long long first(long long total, int n, int c) { return total * c / n; }
+  __device__ __forceinline__ static int cta_of(long long total, int n, long long x) {
+    int c = static_cast<int>(x * n / total);
+    while (c + 1 < n && first(total, n, c + 1) <= x) ++c;
+    while (c > 0 && first(total, n, c) > x) --c;
+    return c;
+  }
+};
+
+
+// the workspace of k2_paged_attention: one counter per CTA, then two parts of its share for each
+constexpr int kAttnMaxCtas = 1024;
+constexpr size_t kCounterBytes = sizeof(unsigned) * kAttnMaxCtas;
+struct AttnWorkspace {
+  unsigned* counters;
+  float* parts;
+};
+
+// opts a kernel in to its shared memory, once per device (bit `dev` of `ready`)
+inline cudaError_t allow_smem(const void* kernel, int bytes, int dev, std::atomic<uint64_t>& ready) {
+  const uint64_t bit = 1ull << dev;
+  if (ready.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) ready.fetch_or(bit, std::memory_order_release);
+  return e;
+}
+
+// prompt chunks (k2_paged_chunk.cu): the requests with more than small_rows query rows
+size_t paged_chunk_part_bytes();  // of one CTA's two parts
+cudaError_t launch_paged_chunk(const PagedPool& p, const PagedAttnArgs& a, int head_dim, int kv_dtype, int q_dtype,
+                               int small_rows, const AttnWorkspace& w, int sms, int dev, cudaStream_t s);
 
 }  // namespace k2

@@ -3,7 +3,6 @@
 #include <math.h>
 
 #include <algorithm>
-#include <atomic>
 
 #include "k2_paged.cuh"
 
@@ -11,96 +10,10 @@ namespace k2 {
 
 namespace {
 
-struct PagedAttnArgs {
-  const void* q;
-  long long q_stride;
-  const int* cu_q;
-  const int* kv_len;
-  const int* table;
-  int table_stride, requests, tokens, n_heads, max_q;
-  float scale;
-  void* out;
-  long long out_stride;
-};
-
-template <typename T>
-__device__ __forceinline__ T from_f32(float v);
-template <>
-__device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
-template <>
-__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
-
-
-constexpr int kMaxRep = 16;  // query heads per KV head
-constexpr int kMaxKeys = 1 << 30;
-
-// ---- what both kernels need to know about a request -----------------------------------------
-struct Req {
-  int q0, nq, len;  // first query row, queries, keys
-  bool ok;          // consistent lengths
-};
-__device__ __forceinline__ Req request(const PagedAttnArgs& a, int block_log2, int r) {
-  Req x;
-  x.q0 = a.cu_q[r];
-  const int q1 = a.cu_q[r + 1];
-  x.len = a.kv_len[r];
-  x.ok = x.q0 >= 0 && q1 >= x.q0 && q1 <= a.tokens;
-  x.nq = x.ok ? q1 - x.q0 : 0;
-  if (x.nq > 0)
-    x.ok = x.nq <= a.max_q && x.nq <= x.len && x.len <= kMaxKeys &&
-           x.len <= (static_cast<long long>(a.table_stride) << block_log2);
-  return x;
-}
-
-__device__ __forceinline__ float exp2_approx(float x) {  // 2^x (2^-inf = 0), relative error about 2^-22
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-constexpr float kLog2e = 1.4426950408889634f;
-
-// Codes to fp16, exactly.  int8: with its sign bit flipped a code is u = c + 128,
-// and the fp16 number with the bits 0x6400 | u is 1024 + u, so one subtraction of
-// 1152 gives c.  E4M3 values are fp16 values.
-template <typename C>
-struct Widen;
-template <>
-struct Widen<CodeI8> {
-  // the word's codes as the bytes that pair() takes
-  __device__ __forceinline__ static uint32_t prep(uint32_t w) { return w ^ 0x80808080u; }
-  // bytes 0 and 1 (HI: 2 and 3) of a prepared word
-  template <bool HI>
-  __device__ __forceinline__ static uint32_t pair(uint32_t w) {
-    const uint32_t m = __byte_perm(w, 0x64646464u, HI ? 0x4342 : 0x4140);
-    const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&m), __half2half2(__ushort_as_half(0x6480)));
-    return *reinterpret_cast<const uint32_t*>(&h);
-  }
-};
-template <>
-struct Widen<CodeF8> {
-  __device__ __forceinline__ static uint32_t prep(uint32_t w) { return w; }
-  template <bool HI>
-  __device__ __forceinline__ static uint32_t pair(uint32_t w) {
-    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(HI ? w >> 16 : w & 0xFFFFu), __NV_E4M3);
-    return *reinterpret_cast<const uint32_t*>(&h);
-  }
-};
-
 __device__ __forceinline__ uint32_t movmatrix(uint32_t a) {  // transpose of an 8 x 8 fp16 matrix held by the warp
   uint32_t d;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
   return d;
-}
-__device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void* src, bool take) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(take ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void cp_async16_to(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
   uint4 v;
@@ -111,19 +24,6 @@ __device__ __forceinline__ uint2 lds64(uint32_t a) {
   uint2 v;
   asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
   return v;
-}
-
-// Eight neighbouring query elements as fp32
-template <typename T>
-__device__ __forceinline__ void load8(const T* p, float* f) {
-  const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
-  Unpack<T>::run(v, f);
-}
-// four outputs
-template <typename T>
-__device__ __forceinline__ void store4(T* p, float a, float b, float c, float d) {
-  T v[4] = {from_f32<T>(a), from_f32<T>(b), from_f32<T>(c), from_f32<T>(d)};
-  *reinterpret_cast<uint2*>(p) = *reinterpret_cast<const uint2*>(v);
 }
 
 // ---- few query rows per request: decode and speculative steps -------------------------------
@@ -169,7 +69,6 @@ struct Dec {
   static constexpr int kCtas = NT <= 2 ? 3 : 2;                  // per SM
 };
 constexpr int kDecSlotFloats = kDecMaxRows * (128 + 2);  // one part: rows x (output, maximum, sum)
-constexpr int kDecMaxCtas = 1024;
 
 // byte offset of 16-byte chunk c of row r in a tile of D-byte rows, swizzled so
 // that the fragment reads below are free of bank conflicts
@@ -178,16 +77,6 @@ __device__ __forceinline__ int tile_at(int r, int c) {
   if constexpr (D == 128) return r * 128 + ((c ^ (r & 7)) << 4);
   else return (r >> 1) * 128 + (((((r & 1) << 2) | c) ^ ((r & 6))) << 4);
 }
-
-struct DecShare {  // the flat tile range of CTA c of n over `total` tiles
-  __device__ __forceinline__ static long long first(long long total, int n, int c) { return total * c / n; }
-  __device__ __forceinline__ static int cta_of(long long total, int n, long long x) {
-    int c = static_cast<int>(x * n / total);
-    while (c + 1 < n && first(total, n, c + 1) <= x) ++c;
-    while (c > 0 && first(total, n, c) > x) --c;
-    return c;
-  }
-};
 
 template <typename T, typename C, int D, int NT>
 __global__ void __launch_bounds__(kDecThreads, Dec<D, NT>::kCtas)
@@ -248,7 +137,7 @@ __global__ void __launch_bounds__(kDecThreads, Dec<D, NT>::kCtas)
   if (total == 0) return;
   const int ctas = static_cast<int>(min(static_cast<long long>(gridDim.x), (total + kDecShare - 1) / kDecShare));
   if (blockIdx.x >= ctas) return;
-  const long long x0 = DecShare::first(total, ctas, blockIdx.x), x1 = DecShare::first(total, ctas, blockIdx.x + 1);
+  const long long x0 = Share::first(total, ctas, blockIdx.x), x1 = Share::first(total, ctas, blockIdx.x + 1);
   if (before <= x0 && x0 < before + own) {  // one thread: its requests hold the share's first unit
     long long at = before;
     for (int i = 0; i < per; ++i) {
@@ -606,7 +495,7 @@ __global__ void __launch_bounds__(kDecThreads, Dec<D, NT>::kCtas)
     }
     if (!whole) {
       // the item's parts lie with CTAs c0 .. c1; the last to arrive joins them in that order
-      const int c0 = DecShare::cta_of(total, ctas, item), c1 = DecShare::cta_of(total, ctas, item + nt - 1);
+      const int c0 = Share::cta_of(total, ctas, item), c1 = Share::cta_of(total, ctas, item + nt - 1);
       __threadfence();
       __syncthreads();
       if (tid == 0) {
@@ -653,122 +542,34 @@ __global__ void __launch_bounds__(kDecThreads, Dec<D, NT>::kCtas)
     __syncthreads();  // the rings take the next item's tiles
   }
 }
-constexpr int kThreads = 128, kWarps = kThreads / 32;
-
-// One CTA per query token and KV head: its warps take every fourth key, a lane
-// head_dim / 32 neighbouring dims; each warp keeps a running maximum, sum and
-// output per query head, merged at the end.
-template <typename T, typename C, int D>
-__global__ void __launch_bounds__(kThreads) paged_attn_simple_kernel(const PagedPool p, const PagedAttnArgs a, int small_rows) {
-  constexpr int E = D / 32;
-  __shared__ float qs[kMaxRep][D];
-  __shared__ float sm[kWarps][kMaxRep], sl[kWarps][kMaxRep], so[kWarps][kMaxRep][D];
-  const int t = blockIdx.x, g = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int rep = a.n_heads / p.n_kv;
-  int r = 0;
-  while (r < a.requests && !(a.cu_q[r] <= t && t < a.cu_q[r + 1])) ++r;
-  if (r == a.requests) return;
-  const Req x = request(a, p.block_log2, r);
-  const int q0 = x.q0, nq = x.nq, len = x.len;
-  const bool ok = x.ok;
-  if (!ok || nq * rep <= small_rows) return;
-  const int keys = ok ? len - nq + (t - q0) + 1 : 0;
-  const T* q = static_cast<const T*>(a.q) + t * a.q_stride + static_cast<size_t>(g) * rep * D;
-  for (int i = tid; i < rep * D; i += kThreads) qs[i / D][i % D] = to_f32(q[i]) * a.scale;
-  __syncthreads();
-  float m[kMaxRep], l[kMaxRep], o[kMaxRep][E];
-  for (int h = 0; h < kMaxRep; ++h) {
-    m[h] = -INFINITY;
-    l[h] = 0.f;
-    for (int e = 0; e < E; ++e) o[h][e] = 0.f;
-  }
-  for (int j = warp; j < keys; j += kWarps) {
-    const int b = a.table[static_cast<size_t>(r) * a.table_stride + (j >> p.block_log2)];
-    if (b < 0 || b >= p.n_blocks) {
-      if (lane == 0) raise_flag(p.flags, K2_PAGED_BAD_BLOCK);
-      continue;
-    }
-    const size_t at = static_cast<size_t>(b) * p.n_kv + g;
-    const size_t row = ((at << p.block_log2) + (j & ((1 << p.block_log2) - 1))) * D + lane * E;
-    float kf[E], vf[E];
-    for (int e = 0; e < E; ++e) {
-      kf[e] = C::value(p.k[row + e]) * p.ks[at];
-      vf[e] = C::value(p.v[row + e]) * p.vs[at];
-    }
-    for (int h = 0; h < rep; ++h) {
-      float s = 0.f;
-      for (int e = 0; e < E; ++e) s += qs[h][lane * E + e] * kf[e];
-      s = warp_sum(s);
-      const float mn = fmaxf(m[h], s), al = expf(m[h] - mn), w = expf(s - mn);
-      l[h] = l[h] * al + w;
-      for (int e = 0; e < E; ++e) o[h][e] = o[h][e] * al + w * vf[e];
-      m[h] = mn;
-    }
-  }
-  for (int h = 0; h < rep; ++h) {
-    sm[warp][h] = m[h];
-    sl[warp][h] = l[h];
-    for (int e = 0; e < E; ++e) so[warp][h][lane * E + e] = o[h][e];
-  }
-  __syncthreads();
-  T* out = static_cast<T*>(a.out) + t * a.out_stride + static_cast<size_t>(g) * rep * D;
-  for (int i = tid; i < rep * D; i += kThreads) {
-    const int h = i / D, d = i % D;
-    float mm = -INFINITY, ll = 0.f, oo = 0.f;
-    for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, sm[w][h]);
-    for (int w = 0; w < kWarps; ++w) {
-      const float f = mm > -INFINITY ? expf(sm[w][h] - mm) : 0.f;
-      ll += sl[w][h] * f;
-      oo += so[w][h][d] * f;
-    }
-    out[i] = from_f32<T>(ll > 0.f ? oo / ll : 0.f);
-  }
-}
-
 
 // ---- launches ------------------------------------------------------------------------------------
-struct Workspace {
-  unsigned* counters;
-  float* parts;
-};
-
-// opts a kernel in to its shared memory, once per device (bit `dev` of `ready`)
-cudaError_t allow_smem(const void* kernel, int bytes, int dev, std::atomic<uint64_t>& ready) {
-  const uint64_t bit = 1ull << dev;
-  if (ready.load(std::memory_order_acquire) & bit) return cudaSuccess;
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e == cudaSuccess) ready.fetch_or(bit, std::memory_order_release);
-  return e;
-}
-
 template <typename T, typename C, int D, int NT>
-cudaError_t launch_decode(const PagedPool& p, const PagedAttnArgs& a, int small_rows, const Workspace& w, int sms, int dev, cudaStream_t s) {
+cudaError_t launch_decode(const PagedPool& p, const PagedAttnArgs& a, int small_rows, const AttnWorkspace& w, int sms, int dev, cudaStream_t s) {
   using S = Dec<D, NT>;
   auto kernel = paged_decode_kernel<T, C, D, NT>;
   static std::atomic<uint64_t> ready{0};
   const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), S::kSmem, dev, ready);
   if (e != cudaSuccess) return e;
-  kernel<<<std::min(sms * S::kCtas, kDecMaxCtas), kDecThreads, S::kSmem, s>>>(p, a, small_rows, w.counters, w.parts);
+  kernel<<<std::min(sms * S::kCtas, kAttnMaxCtas), kDecThreads, S::kSmem, s>>>(p, a, small_rows, w.counters, w.parts);
   return cudaGetLastError();
 }
 
-template <typename T, typename C, int D>
-cudaError_t launch(const PagedPool& p, const PagedAttnArgs& a, const Workspace& w, int sms, int dev, cudaStream_t s) {
-  const int rep = a.n_heads / p.n_kv;
+// all requests with few rows: the narrowest kernel that holds them; else only the single tokens (and what fits
+// beside them) are taken apart from the prompt chunks
+int small_rows_of(const PagedAttnArgs& a, int rep) {
   const long long most = static_cast<long long>(a.max_q) * rep;
-  // all requests with few rows: the narrowest kernel that holds them; else only the single tokens (and what
-  // fits beside them) are taken apart from the prompt chunks
-  const int small_rows = most <= 8 ? 8 : most <= 16 ? 16 : most <= kDecMaxRows ? kDecMaxRows : rep <= 8 ? 8 : 16;
-  cudaError_t e = small_rows == 8    ? launch_decode<T, C, D, 1>(p, a, small_rows, w, sms, dev, s)
-                  : small_rows == 16 ? launch_decode<T, C, D, 2>(p, a, small_rows, w, sms, dev, s)
-                                     : launch_decode<T, C, D, 4>(p, a, small_rows, w, sms, dev, s);
-  if (e != cudaSuccess || most <= small_rows) return e;
-  paged_attn_simple_kernel<T, C, D><<<dim3(a.tokens, p.n_kv), kThreads, 0, s>>>(p, a, small_rows);
-  return cudaGetLastError();
+  return most <= 8 ? 8 : most <= 16 ? 16 : most <= kDecMaxRows ? kDecMaxRows : rep <= 8 ? 8 : 16;
+}
+template <typename T, typename C, int D>
+cudaError_t launch(const PagedPool& p, const PagedAttnArgs& a, int small_rows, const AttnWorkspace& w, int sms, int dev, cudaStream_t s) {
+  return small_rows == 8    ? launch_decode<T, C, D, 1>(p, a, small_rows, w, sms, dev, s)
+         : small_rows == 16 ? launch_decode<T, C, D, 2>(p, a, small_rows, w, sms, dev, s)
+                            : launch_decode<T, C, D, 4>(p, a, small_rows, w, sms, dev, s);
 }
 template <typename T, typename C>
-cudaError_t launch(const PagedPool& p, int head_dim, const PagedAttnArgs& a, const Workspace& w, int sms, int dev, cudaStream_t s) {
-  return head_dim == 128 ? launch<T, C, 128>(p, a, w, sms, dev, s) : launch<T, C, 64>(p, a, w, sms, dev, s);
+cudaError_t launch(const PagedPool& p, int head_dim, const PagedAttnArgs& a, int small_rows, const AttnWorkspace& w, int sms, int dev, cudaStream_t s) {
+  return head_dim == 128 ? launch<T, C, 128>(p, a, small_rows, w, sms, dev, s) : launch<T, C, 64>(p, a, small_rows, w, sms, dev, s);
 }
 
 // the current device and its SMs (0: none)
@@ -779,7 +580,6 @@ int sm_count(int* dev) {
   if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, *dev) != cudaSuccess) return 0;
   return n;
 }
-constexpr size_t kCounterBytes = sizeof(unsigned) * kDecMaxCtas;
 
 }  // namespace
 
@@ -790,9 +590,10 @@ using namespace k2;
 extern "C" {
 
 size_t k2_paged_workspace_bytes(void) {
-  // two parts of a CTA's share each
   int dev = 0;
-  return kCounterBytes + sizeof(float) * 2 * kDecSlotFloats * static_cast<size_t>(std::min(4 * sm_count(&dev), kDecMaxCtas));
+  const size_t sms = static_cast<size_t>(sm_count(&dev));
+  const size_t few = sizeof(float) * 2 * kDecSlotFloats * std::min<size_t>(3 * sms, kAttnMaxCtas);
+  return kCounterBytes + std::max(few, paged_chunk_part_bytes() * std::min<size_t>(sms, kAttnMaxCtas));
 }
 
 k2_status k2_paged_attention(const k2_paged_kv* kv, const void* d_q, int32_t dtype, int64_t q_stride,
@@ -841,17 +642,23 @@ k2_status k2_paged_attention(const k2_paged_kv* kv, const void* d_q, int32_t dty
     set_error("no CUDA device");
     return K2_ERR_CUDA;
   }
-  const Workspace w = {static_cast<unsigned*>(d_workspace),
+  const AttnWorkspace w = {static_cast<unsigned*>(d_workspace),
                        reinterpret_cast<float*>(static_cast<uint8_t*>(d_workspace) + kCounterBytes)};
   const PagedPool p(*kv);
   const PagedAttnArgs a = {d_q, q_stride, d_cu_q, d_kv_len, d_table, table_stride, requests,
                            tokens, n_heads, std::min(max_q, tokens), scale, d_out, out_stride};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int d = kv->head_dim;
-  const cudaError_t e = dtype == K2_F16
-                            ? (kv->dtype == K2_I8 ? launch<__half, CodeI8>(p, d, a, w, sms, dev, s) : launch<__half, CodeF8>(p, d, a, w, sms, dev, s))
-                            : (kv->dtype == K2_I8 ? launch<__nv_bfloat16, CodeI8>(p, d, a, w, sms, dev, s)
-                                                  : launch<__nv_bfloat16, CodeF8>(p, d, a, w, sms, dev, s));
+  const int rep = n_heads / kv->n_kv_heads, small = small_rows_of(a, rep);
+  cudaError_t e;
+  if (dtype == K2_F16)
+    e = kv->dtype == K2_I8 ? launch<__half, CodeI8>(p, d, a, small, w, sms, dev, s)
+                           : launch<__half, CodeF8>(p, d, a, small, w, sms, dev, s);
+  else
+    e = kv->dtype == K2_I8 ? launch<__nv_bfloat16, CodeI8>(p, d, a, small, w, sms, dev, s)
+                           : launch<__nv_bfloat16, CodeF8>(p, d, a, small, w, sms, dev, s);
+  if (e == cudaSuccess && static_cast<int64_t>(a.max_q) * rep > small)
+    e = launch_paged_chunk(p, a, d, kv->dtype, dtype, small, w, sms, dev, s);
   if (e == cudaSuccess) return K2_OK;
   set_error("attention launch: %s", cudaGetErrorString(e));
   return K2_ERR_CUDA;

@@ -1,0 +1,638 @@
+// Attention of prompt chunks over a block-paged 8-bit cache (k2_paged_attention
+// for requests with many query rows), on the 5th-generation tensor cores.
+//
+// Compute bound: 4 flop per (query row, key, dim) and an exponential per score.
+// A CTA takes up to 256 query rows of one KV head -- two tiles of 128 = 128 / rep
+// tokens x rep heads -- over the keys in tiles of 64:
+//   four warps widen the tile's codes to fp16 (exact) into shared memory, K and V
+//     alike as swizzled rows (V enters P.V through an MN-major descriptor);
+//   one thread issues S = Q K^T (S in tensor memory) and O += P V (P and O in
+//     tensor memory);
+//   four warps per query tile take a row per thread: no exchange between threads
+//     anywhere in the softmax.
+// The two query tiles alternate: while one's softmax runs, the other's MMAs do,
+// and S of the next key tile is issued as soon as the scores are in registers.
+//
+// Scales: the queries carry a power of two that brings a row into fp16's upper
+// range (exact); a block's K scale multiplies its 16 scores' common factor, and its V
+// scale enters the exponent, p' = 2^(s - m + log2(vs / vref) + 11), so neither costs
+// an operation per score.  vref is the largest V scale of the CTA's keys; the row's
+// sum takes each block's p' times 2^-(log2(vs / vref) + 11).  m moves only when a
+// tile's maximum exceeds it by kLazy (then O is rescaled in tensor memory), so
+// p' <= 2^15; p' is rounded to fp16, in full precision down to 2^-14.
+//
+// As for single tokens, every CTA takes an equal share of the step's keys (an item =
+// request, KV head, block of query tokens; counted in keys, each with kChStart more
+// for its start and end); parts of an item are joined by the last CTA to arrive.
+#include <math.h>
+
+#include <algorithm>
+
+#include "k2_paged.cuh"
+#include "k2_tc.cuh"
+
+namespace k2 {
+
+namespace {
+
+constexpr int kSoftWarps = 8, kConvWarps = 4;
+constexpr int kChThreads = 32 * (kSoftWarps + kConvWarps + 1);
+constexpr int kChRows = 128, kChKeys = 64, kChStages = 3;
+constexpr int kCodeTiles = 4;  // key tiles of codes on their way (each thread's own copies)
+constexpr int kChStart = 256;  // an item's start and end, in keys
+constexpr int kChShare = 1024; // smallest share of a CTA, in keys
+constexpr float kLazy = 4.0f, kUp = 11.0f;
+constexpr int kPartFloats = 2 * kChRows * (128 + 2);  // one part: rows x (output, maximum, sum)
+
+template <int D>
+struct Ch {
+  static constexpr int NA = D / 64;                  // 64-dim swizzle atoms of a row
+  static constexpr int QA = kChRows * 128;           // one atom of a query tile
+  static constexpr int QB = NA * QA;                 // a query tile
+  static constexpr int KA = kChKeys * 128;           // one atom of K (or V) of a key tile
+  static constexpr int KB = NA * KA;
+  static constexpr int OFF_ST = 2 * QB;
+  static constexpr int OFF_CODES = OFF_ST + kChStages * 2 * KB;
+  static constexpr int CODES = 2 * kChKeys * D;      // K and V codes of a key tile
+  // and at least the weights of the parts of an item, which take the same memory when they are joined
+  static constexpr int BYTES = OFF_CODES + kCodeTiles * CODES > 160 * 1024 ? OFF_CODES + kCodeTiles * CODES : 160 * 1024;
+  static constexpr int PARTS = BYTES / (4 * 2 * kChRows) - 1;  // parts that can be joined: the most CTAs
+  static constexpr int DYN = BYTES + 1024;           // + alignment to 1024 B
+  // tensor memory: O of both query tiles, S, then P (two fp16 per column)
+  static constexpr int TM_S = 2 * D, TM_P = 2 * D + 2 * kChKeys, TM_COLS = 512;
+  // instruction descriptors (kind::f16): fp16 A and B, fp32 D, M = 128; for O, B (V) is MN-major (bit 16)
+  static constexpr uint32_t IDESC_S = (1u << 4) | (static_cast<uint32_t>(kChKeys >> 3) << 17) | (8u << 24);
+  static constexpr uint32_t IDESC_O = (1u << 4) | (1u << 16) | (static_cast<uint32_t>(D >> 3) << 17) | (8u << 24);
+};
+
+// D += A B with A in tensor memory
+__device__ __forceinline__ void mma_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// 64 columns of this warp's lanes
+__device__ __forceinline__ void tmem_ld64(uint32_t taddr, uint32_t* v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,"
+      "%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];\n\ttcgen05.wait::ld.sync.aligned;"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+        "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]),
+        "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]),
+        "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31]), "=r"(v[32]),
+        "=r"(v[33]), "=r"(v[34]), "=r"(v[35]), "=r"(v[36]), "=r"(v[37]), "=r"(v[38]), "=r"(v[39]), "=r"(v[40]),
+        "=r"(v[41]), "=r"(v[42]), "=r"(v[43]), "=r"(v[44]), "=r"(v[45]), "=r"(v[46]), "=r"(v[47]), "=r"(v[48]),
+        "=r"(v[49]), "=r"(v[50]), "=r"(v[51]), "=r"(v[52]), "=r"(v[53]), "=r"(v[54]), "=r"(v[55]), "=r"(v[56]),
+        "=r"(v[57]), "=r"(v[58]), "=r"(v[59]), "=r"(v[60]), "=r"(v[61]), "=r"(v[62]), "=r"(v[63])
+      : "r"(taddr)
+      : "memory");
+}
+
+// A wait for completion `n` (0, 1, ...) of a barrier; false once it, or another wait of the CTA, gave up
+__device__ __forceinline__ bool await(uint64_t* bar, int n, volatile int* stop) {
+  const uint32_t parity = static_cast<uint32_t>(n) & 1u;
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = globaltimer();
+  while (!mbar_try_wait(bar, parity)) {
+    if (*stop) return false;
+    if (globaltimer() - t0 > kWaitLimitNs) {
+      *stop = 1;
+      return false;
+    }
+  }
+  return true;
+}
+
+template <typename T, typename C, int D>
+__global__ void __launch_bounds__(kChThreads, 1)
+    paged_chunk_kernel(const PagedPool p, const PagedAttnArgs a, int small_rows, const AttnWorkspace w) {
+  using S = Ch<D>;
+  using W = Widen<C>;
+  constexpr int ST = kChStages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  __shared__ __align__(8) uint64_t kv_full[ST], kv_empty[ST], s_full[2], s_free[2], p_ready[2], o_done[2], drained;
+  __shared__ __align__(16) float sc_k[ST][4], sc_up[ST][4], sc_down[ST][4];  // of a tile's 16-key quarters
+  __shared__ __align__(16) float sc_raw[kCodeTiles][4][2];  // K and V scale of a quarter whose codes are on their way
+  __shared__ uint32_t tmem_slot;
+  __shared__ int stop, s_last, s_req;
+  __shared__ unsigned s_vref;
+  __shared__ long long s_sum[kChThreads / 32], s_base;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rep = a.n_heads / p.n_kv;
+  const int QT = kChRows / rep, TT = 2 * QT;  // tokens of a query tile, of an item
+
+  // ---- the share of this CTA ----------------------------------------------------------------
+  struct Cost {
+    long long head;  // one KV head's items
+    int nb, basek;   // items, keys before the first query
+  };
+  auto cost_of = [&](const Req& x) -> Cost {
+    Cost c = {0, 0, 0};
+    if (x.ok && static_cast<long long>(x.nq) * rep > small_rows) {
+      c.nb = (x.nq + TT - 1) / TT;
+      c.basek = x.len - x.nq;
+      c.head = c.nb * (static_cast<long long>(kChStart) + c.basek) + static_cast<long long>(TT) * c.nb * (c.nb - 1) / 2 + x.nq;
+    }
+    return c;
+  };
+  const int per = (a.requests + kChThreads - 1) / kChThreads;
+  long long own = 0;
+  for (int i = 0; i < per; ++i) {
+    const int r = tid * per + i;
+    if (r < a.requests) own += cost_of(request(a, p.block_log2, r)).head * p.n_kv;
+  }
+  long long inc = own;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long u = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += u;
+  }
+  if (lane == 31) s_sum[warp] = inc;
+  if (tid == 0) {
+    stop = 0;
+    s_vref = 0u;
+    for (int i = 0; i < ST; ++i) {
+      mbar_init(&kv_full[i], kConvWarps);
+      mbar_init(&kv_empty[i], 1);
+    }
+    for (int q = 0; q < 2; ++q) {
+      mbar_init(&s_full[q], 1);
+      mbar_init(&s_free[q], 4);
+      mbar_init(&p_ready[q], 4);
+      mbar_init(&o_done[q], 1);
+    }
+    mbar_init(&drained, 1);
+    fence_mbar_init();
+  }
+  __syncthreads();
+  long long total = 0, before = inc - own;
+  for (int i = 0; i < kChThreads / 32; ++i) {
+    if (i < warp) before += s_sum[i];
+    total += s_sum[i];
+  }
+  if (total == 0) return;
+  const int ctas = static_cast<int>(min(static_cast<long long>(gridDim.x), (total + kChShare - 1) / kChShare));
+  if (blockIdx.x >= ctas) return;
+  const long long x0 = Share::first(total, ctas, blockIdx.x), x1 = Share::first(total, ctas, blockIdx.x + 1);
+  if (before <= x0 && x0 < before + own) {
+    long long at = before;
+    for (int i = 0; i < per; ++i) {
+      const int r = tid * per + i;
+      if (r >= a.requests) break;
+      const long long n = cost_of(request(a, p.block_log2, r)).head * p.n_kv;
+      if (x0 < at + n) {
+        s_req = r;
+        s_base = at;
+        break;
+      }
+      at += n;
+    }
+  }
+  if (warp == 0) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_slot)), "r"(S::TM_COLS)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_before();
+  __syncthreads();
+  tc_after();
+  const uint32_t tmem = tmem_slot;
+  int r = s_req;
+  long long base = s_base;
+  int n_kv = 0, n_q[2] = {0, 0};  // key tiles so far: of the ring, of each query tile
+  bool dead = false;
+
+  for (long long x = x0; x < x1;) {
+    // ---- the item at x -----------------------------------------------------------------------
+    Req q = request(a, p.block_log2, r);
+    Cost cost = cost_of(q);
+    while (x >= base + cost.head * p.n_kv) {
+      base += cost.head * p.n_kv;
+      q = request(a, p.block_log2, ++r);
+      cost = cost_of(q);
+    }
+    const int g = static_cast<int>((x - base) / cost.head);
+    const long long rem = x - base - g * cost.head;
+    auto before_b = [&](int b) { return b * (static_cast<long long>(kChStart) + cost.basek) + static_cast<long long>(TT) * b * (b + 1) / 2; };
+    int b = 0;
+    for (int hi = cost.nb; hi - b > 1;) {
+      const int mid = (b + hi) >> 1;
+      if (before_b(mid) <= rem) b = mid;
+      else hi = mid;
+    }
+    const long long item = base + g * cost.head + before_b(b) + kChStart;  // place of the item's first key
+    const int t0 = b * TT, kend = cost.basek + min(q.nq, t0 + TT), nkt = (kend + kChKeys - 1) / kChKeys;
+    const int ta = x0 <= item ? 0 : static_cast<int>(min((x0 - item + kChKeys - 1) / kChKeys, static_cast<long long>(nkt)));
+    const int tb = x1 <= item ? 0 : static_cast<int>(min((x1 - item + kChKeys - 1) / kChKeys, static_cast<long long>(nkt)));
+    x = item + kend;
+    if (ta >= tb) continue;
+    const bool whole = ta == 0 && tb == nkt;
+    const int nqt = t0 + QT < q.nq ? 2 : 1, tiles = tb - ta;
+    const int* table = a.table + static_cast<size_t>(r) * a.table_stride;
+    // softmax threads: row `row` of query tile qi
+    const int qi = warp >> 2, row = (warp & 3) * 32 + lane;
+    const int tok = t0 + qi * QT + row / rep, head = g * rep + row % rep;
+    const bool soft = warp < kSoftWarps && qi < nqt;
+    const bool row_ok = soft && row < QT * rep && tok < q.nq;
+    float f_row = 0.f;
+    if (!dead) {
+      if (soft) {  // the row into shared memory as fp16, scaled by a power of two
+        const T* src = static_cast<const T*>(a.q) + (q.q0 + tok) * a.q_stride + static_cast<size_t>(head) * D;
+        auto dims8 = [&](int c, float* f) {
+          const uint4 v = row_ok ? __ldg(reinterpret_cast<const uint4*>(src) + c) : make_uint4(0, 0, 0, 0);
+          Unpack<T>::run(v, f);
+        };
+        float top = 0.f;
+#pragma unroll 4
+        for (int c = 0; c < D / 8; ++c) {
+          float f[8];
+          dims8(c, f);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(f[e]));
+        }
+        const int ex = static_cast<int>(__float_as_uint(top) >> 23);
+        const int up = top > 0.f && ex < 255 ? 14 + 127 - ex : 0;
+        const int ua = up / 2, ub = up - ua;  // in two steps: 2^up itself may not be a normal number
+        const float sign = a.scale < 0.f ? -1.f : 1.f;
+        const float sa = __uint_as_float((127 + ua) << 23) * sign, sb = __uint_as_float((127 + ub) << 23);
+        f_row = fabsf(a.scale) * kLog2e * __uint_as_float((127 - ua) << 23) * __uint_as_float((127 - ub) << 23);
+        uint8_t* dst = smem + qi * S::QB;
+#pragma unroll 4
+        for (int c = 0; c < D / 8; ++c) {
+          float f[8];
+          dims8(c, f);
+          uint32_t h[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) h[e] = pack_half2(f[2 * e] * sa * sb, f[2 * e + 1] * sa * sb);
+          *reinterpret_cast<uint4*>(dst + (c >> 3) * S::QA + sw128(row, 8 * (c & 7))) = make_uint4(h[0], h[1], h[2], h[3]);
+        }
+      }
+      // the largest V scale of the CTA's keys
+      const int j0 = (ta * kChKeys) >> p.block_log2, j1 = (min(tb * kChKeys, kend) - 1) >> p.block_log2;
+      float top = 0.f;
+      for (int j = j0 + tid; j <= j1; j += kChThreads) {
+        const int id = __ldg(table + j);
+        if (id >= 0 && id < p.n_blocks) top = fmaxf(top, __ldg(p.vs + static_cast<size_t>(id) * p.n_kv + g));
+      }
+      top = warp_max(top);
+      if (lane == 0) atomicMax(&s_vref, __float_as_uint(top));
+      fence_proxy_async();  // Q (generic stores) before the MMAs read it
+      __syncthreads();
+    }
+    const float vref = __uint_as_float(s_vref);
+    float m_ref = -INFINITY, l = 0.f;
+
+    if (dead) {
+    } else if (warp >= kSoftWarps && warp < kSoftWarps + kConvWarps) {
+      // ---- codes to fp16 ---------------------------------------------------------------------
+      const int ct = tid - 32 * kSoftWarps;
+      constexpr int CH = D / 16, N = kChKeys * CH / (32 * kConvWarps);  // 16-code chunks per row, per thread
+      constexpr int RS = 32 * kConvWarps / CH;                          // rows between a thread's chunks
+      const int row0 = ct / CH, ch = ct % CH;
+      const int bmask = (1 << p.block_log2) - 1;
+      // the block of each chunk's quarter, and (threads 0 .. 3) of quarter ct; -1: none
+      int id[N], mine = -1;
+      auto ids_of = [&](int kt) {
+        auto block_at = [&](int key0) {
+          int d = key0 < kend ? __ldg(table + (key0 >> p.block_log2)) : -1;
+          if (key0 < kend && (d < 0 || d >= p.n_blocks)) {
+            raise_flag(p.flags, K2_PAGED_BAD_BLOCK);
+            d = -1;
+          }
+          return d;
+        };
+#pragma unroll
+        for (int c = 0; c < N; ++c) id[c] = block_at(kt * kChKeys + ((row0 + c * RS) & ~15));
+        if (ct < 4) mine = block_at(kt * kChKeys + 16 * ct);
+      };
+      // requests this thread's codes of tile i (ids of it in `id`), rows behind the last key as zeros
+      auto request_codes = [&](int i) {
+        const int slot = (n_kv + i) % kCodeTiles, kt = ta + i;
+        const uint32_t dst = smem_u32(smem + S::OFF_CODES + slot * S::CODES) + 16 * ct;
+#pragma unroll
+        for (int c = 0; c < N; ++c) {
+          const int key = kt * kChKeys + row0 + c * RS;
+          const bool take = id[c] >= 0 && key < q.len;
+          const size_t off = take ? (((static_cast<size_t>(id[c]) * p.n_kv + g) << p.block_log2) + (key & bmask)) * D + ch * 16 : 0;
+          cp_async16_zfill(dst + 16 * 32 * kConvWarps * c, p.k + off, take);
+          cp_async16_zfill(dst + 16 * 32 * kConvWarps * c + S::CODES / 2, p.v + off, take);
+        }
+        if (ct < 4) {
+          if (mine >= 0) {
+            const size_t at = static_cast<size_t>(mine) * p.n_kv + g;
+            cp_async4(&sc_raw[slot][ct][0], p.ks + at);
+            cp_async4(&sc_raw[slot][ct][1], p.vs + at);
+          } else {
+            sc_raw[slot][ct][0] = -1.f;
+            sc_raw[slot][ct][1] = 0.f;
+          }
+        }
+      };
+      ids_of(ta);
+#pragma unroll 1
+      for (int i = 0; i < kCodeTiles - 1; ++i) {
+        if (i < tiles) {
+          request_codes(i);
+          ids_of(ta + i + 1);
+        }
+        cp_async_commit();
+      }
+#pragma unroll 1
+      for (int i = 0; i < tiles; ++i) {
+        const int n = n_kv + i, st = n % ST, slot = n % kCodeTiles;
+        if (i + kCodeTiles - 1 < tiles) {
+          request_codes(i + kCodeTiles - 1);
+          ids_of(ta + i + kCodeTiles);
+        }
+        cp_async_commit();
+        cp_async_wait<kCodeTiles - 1>();
+        if (n >= ST && !__all_sync(0xffffffffu, await(&kv_empty[st], n / ST - 1, &stop))) break;
+        uint8_t* kst = smem + S::OFF_ST + st * 2 * S::KB;
+        const uint8_t* cst = smem + S::OFF_CODES + slot * S::CODES + 16 * ct;
+#pragma unroll
+        for (int c = 0; c < N; ++c) {
+          const int rr = row0 + c * RS;
+          const int atom = ch >> 2, e0 = (ch & 3) * 16;
+          uint8_t* ka = kst + atom * S::KA;
+          const uint32_t lo = sw128(rr, e0), hi = sw128(rr, e0 + 8);
+          const bool swap = atom != 0;  // lanes of the two atoms write opposite halves: no bank conflicts
+#pragma unroll
+          for (int m = 0; m < 2; ++m) {
+            const uint4 u = *reinterpret_cast<const uint4*>(cst + 16 * 32 * kConvWarps * c + m * (S::CODES / 2));
+            const uint32_t w0 = W::prep(swap ? u.z : u.x), w1 = W::prep(swap ? u.w : u.y), w2 = W::prep(swap ? u.x : u.z),
+                           w3 = W::prep(swap ? u.y : u.w);
+            uint8_t* dst = ka + m * S::KB;
+            *reinterpret_cast<uint4*>(dst + (swap ? hi : lo)) = make_uint4(
+                W::template pair<false>(w0), W::template pair<true>(w0), W::template pair<false>(w1), W::template pair<true>(w1));
+            *reinterpret_cast<uint4*>(dst + (swap ? lo : hi)) = make_uint4(
+                W::template pair<false>(w2), W::template pair<true>(w2), W::template pair<false>(w3), W::template pair<true>(w3));
+          }
+        }
+        if (ct < 4) {
+          const float k_s = sc_raw[slot][ct][0], v_s = sc_raw[slot][ct][1];
+          const float ratio = vref > 0.f ? fmaxf(v_s / vref, 8.6736174e-19f) : 8.6736174e-19f;  // 2^-60: as good as zero
+          const float up = log2f(ratio) + kUp;
+          sc_k[st][ct] = k_s;
+          sc_up[st][ct] = k_s < 0.f ? 0.f : up;
+          sc_down[st][ct] = k_s < 0.f ? 0.f : exp2f(-up);
+        }
+        fence_proxy_async();  // generic stores before the MMAs read them
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&kv_full[st]);
+      }
+      cp_async_wait<0>();
+    } else if (warp == kSoftWarps + kConvWarps) {
+      // ---- the MMAs ------------------------------------------------------------------------------
+      if (lane == 0) {
+        auto issue_s = [&](int j, int n) {  // S of query tile j over ring tile n
+          const uint8_t* kst = smem + S::OFF_ST + (n % ST) * 2 * S::KB;
+          const uint8_t* qst = smem + j * S::QB;
+#pragma unroll
+          for (int e = 0; e < D / 16; ++e)
+            mma(tmem + S::TM_S + kChKeys * j, smem_desc(qst + (e >> 2) * S::QA + (e & 3) * 32),
+                smem_desc(kst + (e >> 2) * S::KA + (e & 3) * 32), S::IDESC_S, e > 0 ? 1u : 0u);
+          mma_commit(&s_full[j]);
+        };
+        auto issue_o = [&](int j, int n, bool first) {
+          const uint8_t* vst = smem + S::OFF_ST + (n % ST) * 2 * S::KB + S::KB;
+#pragma unroll
+          for (int e = 0; e < kChKeys / 16; ++e)
+            mma_ta(tmem + j * D, tmem + S::TM_P + 32 * j + 8 * e, smem_desc_mn(vst + e * 16 * 128, S::KA, 8 * 128), S::IDESC_O,
+                   first && e == 0 ? 0u : 1u);
+          mma_commit(&o_done[j]);
+        };
+        bool ok = await(&kv_full[n_kv % ST], n_kv / ST, &stop);
+        if (ok) {
+          tc_after();
+          for (int j = 0; j < nqt; ++j) issue_s(j, n_kv);
+        }
+        for (int i = 0; i < tiles && ok; ++i) {
+          const int n = n_kv + i;
+          if (i + 1 < tiles && !(ok = await(&kv_full[(n + 1) % ST], (n + 1) / ST, &stop))) break;
+          for (int j = 0; j < nqt && ok; ++j) {
+            const int m = n_q[j] + i;
+            if (i + 1 < tiles) {  // the scores of tile i are in registers: S of the next tile
+              if (!(ok = await(&s_free[j], m, &stop))) break;
+              tc_after();
+              issue_s(j, n + 1);
+            }
+            if (!(ok = await(&p_ready[j], m, &stop))) break;
+            tc_after();
+            issue_o(j, n, i == 0);
+          }
+          if (ok) mma_commit(&kv_empty[n % ST]);
+        }
+        if (!ok) {  // whatever is in flight ends before the memory goes away
+          mma_commit(&drained);
+          (void)mbar_wait(&drained, 0);
+        }
+      }
+    } else if (soft) {
+      // ---- softmax: one row per thread -------------------------------------------------------------
+      const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+      const int qpos = cost.basek + tok;  // the row sees keys 0 .. qpos
+      bool ok = true;
+      for (int i = 0; i < tiles; ++i) {
+        const int n = n_kv + i, m = n_q[qi] + i, st = n % ST;
+        ok = await(&kv_full[st], n / ST, &stop) && await(&s_full[qi], m, &stop);  // the tile's scales; its scores
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        const float4 kq = *reinterpret_cast<const float4*>(sc_k[st]), uq = *reinterpret_cast<const float4*>(sc_up[st]),
+                     dq = *reinterpret_cast<const float4*>(sc_down[st]);
+        const float kk[4] = {kq.x, kq.y, kq.z, kq.w}, uu[4] = {uq.x, uq.y, uq.z, uq.w}, dd[4] = {dq.x, dq.y, dq.z, dq.w};
+        tc_after();
+        uint32_t raw[kChKeys];
+        tmem_ld64(tmem + lanes + S::TM_S + kChKeys * qi, raw);
+        tc_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s_free[qi]);
+        float s[kChKeys], c1[4];
+#pragma unroll
+        for (int e = 0; e < kChKeys; ++e) s[e] = __uint_as_float(raw[e]);
+#pragma unroll
+        for (int h = 0; h < 4; ++h) c1[h] = f_row * kk[h];
+        const int last = row_ok ? qpos - (ta + i) * kChKeys : -1;  // last visible column
+        const bool gap = fminf(fminf(kk[0], kk[1]), fminf(kk[2], kk[3])) < 0.f;
+        if (__any_sync(0xffffffffu, last < kChKeys - 1) || gap) {
+#pragma unroll
+          for (int e = 0; e < kChKeys; ++e) s[e] = e <= last && kk[e >> 4] >= 0.f ? s[e] * c1[e >> 4] : -INFINITY;
+#pragma unroll
+          for (int h = 0; h < 4; ++h) c1[h] = 1.f;
+        }
+        float mt = -INFINITY;
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+          float v = s[16 * h];
+#pragma unroll
+          for (int e = 1; e < 16; ++e) v = fmaxf(v, s[16 * h + e]);
+          mt = fmaxf(mt, v * c1[h]);  // factors are >= 0
+        }
+        const bool move = mt > -INFINITY && (m_ref == -INFINITY || mt > m_ref + kLazy);
+        const float alpha = move ? (m_ref == -INFINITY ? 0.f : exp2_approx(m_ref - mt)) : 1.f;
+        if (move) {
+          l *= alpha;
+          m_ref = mt;
+        }
+        const float zm = m_ref == -INFINITY ? 0.f : m_ref;  // no visible key yet: every p is 0
+        uint32_t pk[kChKeys / 2];
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+          const float c2 = uu[h] - zm;
+          float sum = 0.f;
+#pragma unroll
+          for (int e = 0; e < 16; e += 2) {
+            const float p0 = exp2_approx(fmaf(s[16 * h + e], c1[h], c2)), p1 = exp2_approx(fmaf(s[16 * h + e + 1], c1[h], c2));
+            sum += p0 + p1;
+            pk[8 * h + e / 2] = pack_half2(p0, p1);
+          }
+          l = fmaf(sum, dd[h], l);
+        }
+        if (i > 0) {  // the previous P.V has read P and written O
+          ok = __all_sync(0xffffffffu, await(&o_done[qi], m - 1, &stop));
+          if (!ok) break;
+          tc_after();
+          if (__any_sync(0xffffffffu, move)) {
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+              uint32_t ov[32];
+              tmem_ld32(tmem + lanes + qi * D + c, ov);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
+              tmem_st32(tmem + lanes + qi * D + c, ov);
+            }
+          }
+        }
+        tmem_st32(tmem + lanes + S::TM_P + 32 * qi, pk);
+        tc_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_ready[qi]);
+      }
+      if (ok) (void)await(&o_done[qi], n_q[qi] + tiles - 1, &stop);
+    }
+    __syncthreads();
+    tc_after();
+    if (stop && !dead) {
+      dead = true;
+      if (tid == 0) raise_flag(p.flags, K2_PAGED_TIMEOUT);
+    }
+    n_kv += tiles;
+    n_q[0] += tiles;
+    if (nqt == 2) n_q[1] += tiles;
+    if (tid == 0) s_vref = 0u;  // read above by everyone
+
+    // ---- the item's rows, or this CTA's part of them -----------------------------------------------
+    float* part = w.parts + (2 * static_cast<size_t>(blockIdx.x) + (ta == 0 ? 1 : 0)) * kPartFloats;
+    if (soft) {
+      const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+      const float nan = __uint_as_float(0x7fffffffu);
+      const float unit = dead ? nan : vref * (1.f / 2048.f);  // 2^-kUp
+      const float inv = whole ? (l > 0.f ? unit / l : dead ? nan : 0.f) : unit;
+      T* out = static_cast<T*>(a.out) + (q.q0 + tok) * a.out_stride + static_cast<size_t>(head) * D;
+      const int lrow = qi * kChRows + row;
+#pragma unroll 1
+      for (int c = 0; c < D; c += 32) {
+        uint32_t ov[32];
+        tmem_ld32(tmem + lanes + qi * D + c, ov);
+        if (whole) {
+          if (row_ok) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 4)
+              store4(out + c + e, __uint_as_float(ov[e]) * inv, __uint_as_float(ov[e + 1]) * inv, __uint_as_float(ov[e + 2]) * inv,
+                     __uint_as_float(ov[e + 3]) * inv);
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; e += 4)
+            *reinterpret_cast<float4*>(part + (static_cast<size_t>((c + e) / 4) * (2 * kChRows) + lrow) * 4) =
+                make_float4(__uint_as_float(ov[e]) * inv, __uint_as_float(ov[e + 1]) * inv, __uint_as_float(ov[e + 2]) * inv,
+                            __uint_as_float(ov[e + 3]) * inv);
+        }
+      }
+      if (!whole) *reinterpret_cast<float2*>(part + 2 * kChRows * D + 2 * lrow) = make_float2(dead ? 0.f : m_ref, dead ? 1.f : l);
+    }
+    if (!whole) {
+      const int c0 = Share::cta_of(total, ctas, item), c1 = Share::cta_of(total, ctas, item + static_cast<long long>(kChKeys) * (nkt - 1));
+      __threadfence();
+      __syncthreads();
+      if (tid == 0) {
+        s_last = atomicAdd(w.counters + c0, 1u) == static_cast<unsigned>(c1 - c0);
+        if (s_last) w.counters[c0] = 0u;  // as the next call wants it
+      }
+      __syncthreads();
+      if (s_last) {
+        __threadfence();
+        const int np = c1 - c0 + 1;
+        auto part_of = [&](int k) { return w.parts + (2 * static_cast<size_t>(c0 + k) + (k == 0 ? 1 : 0)) * kPartFloats; };
+        float* wt = reinterpret_cast<float*>(smem);       // the parts' weights, [k][row]
+        float* inv = wt + S::PARTS * 2 * kChRows;         // and the sums' reciprocals
+        const int nr = nqt * kChRows;
+        for (int e = tid; e < nr; e += kChThreads) {
+          float m = -INFINITY, sum = 0.f;
+          for (int k = 0; k < np; ++k) m = fmaxf(m, __ldcg(part_of(k) + 2 * kChRows * D + 2 * e));
+          for (int k = 0; k < np; ++k) {
+            const float2 ml = __ldcg(reinterpret_cast<const float2*>(part_of(k) + 2 * kChRows * D + 2 * e));
+            const float f = m > -INFINITY ? exp2_approx(ml.x - m) : 0.f;
+            wt[k * 2 * kChRows + e] = f;
+            sum += ml.y * f;
+          }
+          inv[e] = sum > 0.f ? 1.f / sum : 0.f;
+        }
+        __syncthreads();
+        for (int e = tid; e < nr * (D / 4); e += kChThreads) {
+          const int rr = e % nr, c4 = e / nr, j = rr / kChRows, ro = rr % kChRows;
+          const int i = t0 + j * QT + ro / rep;
+          if (ro >= QT * rep || i >= q.nq) continue;
+          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+          for (int k = 0; k < np; ++k) {
+            const float4 u = __ldcg(reinterpret_cast<const float4*>(part_of(k) + (static_cast<size_t>(c4) * (2 * kChRows) + rr) * 4));
+            const float f = wt[k * 2 * kChRows + rr];
+            v.x += u.x * f;
+            v.y += u.y * f;
+            v.z += u.z * f;
+            v.w += u.w * f;
+          }
+          const float f = inv[rr];
+          store4(static_cast<T*>(a.out) + (q.q0 + i) * a.out_stride + (g * rep + ro % rep) * D + 4 * c4, v.x * f, v.y * f, v.z * f, v.w * f);
+        }
+      }
+    }
+    tc_before();
+    __syncthreads();  // Q, the stages and tensor memory take the next item
+    tc_after();
+  }
+  if (warp == 0)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(S::TM_COLS) : "memory");
+}
+
+template <typename T, typename C, int D>
+cudaError_t launch(const PagedPool& p, const PagedAttnArgs& a, int small_rows, const AttnWorkspace& w, int sms, int dev, cudaStream_t s) {
+  auto kernel = paged_chunk_kernel<T, C, D>;
+  static std::atomic<uint64_t> ready{0};
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), Ch<D>::DYN, dev, ready);
+  if (e != cudaSuccess) return e;
+  kernel<<<std::min({sms, kAttnMaxCtas, Ch<D>::PARTS}), kChThreads, Ch<D>::DYN, s>>>(p, a, small_rows, w);
+  return cudaGetLastError();
+}
+template <typename T, typename C>
+cudaError_t launch(const PagedPool& p, const PagedAttnArgs& a, int d, int small_rows, const AttnWorkspace& w, int sms, int dev, cudaStream_t s) {
+  return d == 128 ? launch<T, C, 128>(p, a, small_rows, w, sms, dev, s) : launch<T, C, 64>(p, a, small_rows, w, sms, dev, s);
+}
+
+}  // namespace
+
+size_t paged_chunk_part_bytes() { return 2 * sizeof(float) * kPartFloats; }
+
+cudaError_t launch_paged_chunk(const PagedPool& p, const PagedAttnArgs& a, int head_dim, int kv_dtype, int q_dtype,
+                               int small_rows, const AttnWorkspace& w, int sms, int dev, cudaStream_t s) {
+  if (q_dtype == K2_F16)
+    return kv_dtype == K2_I8 ? launch<__half, CodeI8>(p, a, head_dim, small_rows, w, sms, dev, s)
+                             : launch<__half, CodeF8>(p, a, head_dim, small_rows, w, sms, dev, s);
+  return kv_dtype == K2_I8 ? launch<__nv_bfloat16, CodeI8>(p, a, head_dim, small_rows, w, sms, dev, s)
+                           : launch<__nv_bfloat16, CodeF8>(p, a, head_dim, small_rows, w, sms, dev, s);
+}
+
+}  // namespace k2

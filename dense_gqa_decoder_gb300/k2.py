@@ -22,7 +22,7 @@ K2_F32, K2_BF16, K2_F16, K2_I8, K2_F8, K2_Q4 = range(6)
  K2_OPT_WAIT_LIMIT_US, K2_OPT_STALL_PHASE, K2_OPT_L2_AHEAD, K2_OPT_L2_AHEAD_PHASES, K2_OPT_TRACE,
  K2_OPT_PREFILL_ATTN, K2_OPT_PREFILL_SPLIT, K2_OPT_PREFILL_GEMM) = range(14)
 KERNEL_CLASSES = ("embed", "qkv", "attn", "o_proj", "gate_up", "down", "lm_head", "step", "sample")
-K2_PAGED_BAD_SLOT, K2_PAGED_BAD_BLOCK, K2_PAGED_BAD_LENGTH = 1, 2, 4
+K2_PAGED_BAD_SLOT, K2_PAGED_BAD_BLOCK, K2_PAGED_BAD_LENGTH, K2_PAGED_TIMEOUT = 1, 2, 4, 8
 K2_PLAN_BAD_LENGTH, K2_PLAN_TABLE_FULL, K2_PLAN_NO_BLOCKS, K2_PLAN_TOKENS_FULL = 1, 2, 4, 8
 K2_PAGED_MAX_REQUESTS = 2048
 DTYPES = {"f32": K2_F32, "bf16": K2_BF16, "f16": K2_F16, "i8": K2_I8, "f8": K2_F8, "q4": K2_Q4}

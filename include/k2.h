@@ -499,7 +499,7 @@ k2_status k2_quantize_q4(const void* d_src, int32_t rows, int32_t cols, int8_t* 
 typedef struct {
   void* k;         /* codes [n_blocks][n_kv_heads][block_tokens][head_dim], 16-byte aligned */
   void* v;
-  float* k_scale;  /* [n_blocks][n_kv_heads] */
+  float* k_scale;  /* [n_blocks][n_kv_heads], finite and >= 0 */
   float* v_scale;
   int32_t n_blocks;
   int32_t block_tokens; /* 16, 32, 64 or 128 */
@@ -513,9 +513,10 @@ enum {
   K2_PAGED_BAD_SLOT = 1,   /* a slot >= n_blocks * block_tokens: that row was not stored */
   K2_PAGED_BAD_BLOCK = 2,  /* a table entry outside [0, n_blocks) within a request's length: its keys
                               were left out */
-  K2_PAGED_BAD_LENGTH = 4  /* cu_q not ascending or beyond the query rows, more queries than max_q or
+  K2_PAGED_BAD_LENGTH = 4, /* cu_q not ascending or beyond the query rows, more queries than max_q or
                               than keys, or a length beyond the table or 2^30: the request's rows are zeros
                               where they lie inside the query rows */
+  K2_PAGED_TIMEOUT = 8     /* a bounded wait inside the attention ran out: the rows concerned are NaN */
 };
 #define K2_PAGED_MAX_REQUESTS 2048
 
