@@ -4,9 +4,10 @@
 // Compute bound: 4 flop per (query row, key, dim) and an exponential per score.
 // A CTA takes up to 256 query rows of one KV head -- two tiles of 128 = 128 / rep
 // tokens x rep heads -- over the keys in tiles of 64:
-//   four warps widen the tile's codes to fp16 (exact) into shared memory, K and V
+//   one warp fetches the tile's codes (bulk copies of 16 rows, kCodeTiles tiles ahead) and its scales;
+//   four warps widen the codes to fp16 (exact) into shared memory, K and V
 //     alike as swizzled rows (V enters P.V through an MN-major descriptor);
-//   one thread issues S = Q K^T (S in tensor memory) and O += P V (P and O in
+//   one warp issues S = Q K^T (S in tensor memory) and O += P V (P and O in
 //     tensor memory);
 //   four warps per query tile take a row per thread: no exchange between threads
 //     anywhere in the softmax.
@@ -36,9 +37,13 @@ namespace k2 {
 namespace {
 
 constexpr int kSoftWarps = 8, kConvWarps = 4;
-constexpr int kChThreads = 32 * (kSoftWarps + kConvWarps + 1);
+constexpr int kMmaWarp = kSoftWarps + kConvWarps, kFetchWarp = kMmaWarp + 1;
+constexpr int kChThreads = 32 * (kFetchWarp + 1);
 constexpr int kChRows = 128, kChKeys = 64, kChStages = 3;
-constexpr int kCodeTiles = 4;  // key tiles of codes on their way (each thread's own copies)
+constexpr int kCodeTiles = 4;  // key tiles of codes on their way
+// tiles whose scales are kept: one is read by a softmax warp up to kCodeTiles + kChStages - 1 tiles after it was fetched
+constexpr int kScaleTiles = 8;
+static_assert(kScaleTiles >= kCodeTiles + kChStages, "scales outlive their tile");
 constexpr int kChStart = 256;  // an item's start and end, in keys
 constexpr int kChShare = 1024; // smallest share of a CTA, in keys
 constexpr float kLazy = 4.0f, kUp = 11.0f;
@@ -65,8 +70,24 @@ struct Ch {
   static constexpr uint32_t IDESC_O = (1u << 4) | (1u << 16) | (static_cast<uint32_t>(D >> 3) << 17) | (8u << 24);
 };
 
-// D += A B with A in tensor memory
-__device__ __forceinline__ void mma_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+// One lane of a warp, chosen so that the compiler knows it is one: the operands of what it then issues go through
+// uniform registers without a detour (8 MMAs take 45 cycles each to issue, against 78 from a branch on the lane's
+// number, and the smaller ones execute in 48).
+__device__ __forceinline__ bool elect() {
+  uint32_t ok;
+  asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\tselp.u32 %0, 1, 0, e;\n\t}" : "=r"(ok));
+  return ok != 0;
+}
+// D (+)= A B, A and B in shared memory / A in tensor memory
+template <bool ACC>
+__device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a), "l"(b), "r"(idesc), "n"(ACC ? 1 : 0)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
       "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
@@ -114,9 +135,10 @@ __global__ void __launch_bounds__(kChThreads, 1)
   constexpr int ST = kChStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  __shared__ __align__(8) uint64_t kv_full[ST], kv_empty[ST], s_full[2], s_free[2], p_ready[2], o_done[2], drained;
-  __shared__ __align__(16) float sc_k[ST][4], sc_up[ST][4], sc_down[ST][4];  // of a tile's 16-key quarters
-  __shared__ __align__(16) float sc_raw[kCodeTiles][4][2];  // K and V scale of a quarter whose codes are on their way
+  __shared__ __align__(8) uint64_t kv_full[ST], kv_empty[ST], code_full[kCodeTiles], code_empty[kCodeTiles], s_full[2], s_free[2], p_ready[2], o_done[2], drained;
+  // of a tile's 16-key quarters: the K scale (-1: no keys), log2(vs / vref) + kUp and 2^- of that
+  __shared__ __align__(16) float sc_k[kScaleTiles][4], sc_up[kScaleTiles][4], sc_down[kScaleTiles][4];
+  __shared__ float s_row[2 * kChRows];  // each row's factor from accumulators to base-2 scores
   __shared__ uint32_t tmem_slot;
   __shared__ int stop, s_last, s_req;
   __shared__ unsigned s_vref;
@@ -158,6 +180,10 @@ __global__ void __launch_bounds__(kChThreads, 1)
     for (int i = 0; i < ST; ++i) {
       mbar_init(&kv_full[i], kConvWarps);
       mbar_init(&kv_empty[i], 1);
+    }
+    for (int i = 0; i < kCodeTiles; ++i) {
+      mbar_init(&code_full[i], 1);
+      mbar_init(&code_empty[i], kConvWarps);
     }
     for (int q = 0; q < 2; ++q) {
       mbar_init(&s_full[q], 1);
@@ -238,45 +264,47 @@ __global__ void __launch_bounds__(kChThreads, 1)
     const int tok = t0 + qi * QT + row / rep, head = g * rep + row % rep;
     const bool soft = warp < kSoftWarps && qi < nqt;
     const bool row_ok = soft && row < QT * rep && tok < q.nq;
-    float f_row = 0.f;
     if (!dead) {
-      if (soft) {  // the row into shared memory as fp16, scaled by a power of two
-        const T* src = static_cast<const T*>(a.q) + (q.q0 + tok) * a.q_stride + static_cast<size_t>(head) * D;
-        auto dims8 = [&](int c, float* f) {
-          const uint4 v = row_ok ? __ldg(reinterpret_cast<const uint4*>(src) + c) : make_uint4(0, 0, 0, 0);
-          Unpack<T>::run(v, f);
-        };
-        float top = 0.f;
-#pragma unroll 4
-        for (int c = 0; c < D / 8; ++c) {
-          float f[8];
-          dims8(c, f);
+      const int j0 = (ta * kChKeys) >> p.block_log2, j1 = (min(tb * kChKeys, kend) - 1) >> p.block_log2;
+      int vid[4];  // blocks of the CTA's keys, for their V scales: on their way while the queries are read
 #pragma unroll
-          for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(f[e]));
-        }
+      for (int e = 0; e < 4; ++e) vid[e] = j0 + tid + e * kChThreads <= j1 ? __ldg(table + j0 + tid + e * kChThreads) : -1;
+      // the query rows into shared memory as fp16, each scaled by a power of two; D / 8 lanes take a row
+      constexpr int LR = D / 8, RW = 32 / LR;  // lanes per row, rows per warp and step
+      const float sign = a.scale < 0.f ? -1.f : 1.f;
+#pragma unroll 10
+      for (int e = warp * RW + lane / LR; e < nqt * kChRows; e += RW * (kChThreads / 32)) {
+        const int j = e / kChRows, ro = e % kChRows, i = t0 + j * QT + ro / rep, c = lane % LR;
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (ro < QT * rep && i < q.nq)
+          v = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + (q.q0 + i) * a.q_stride + static_cast<size_t>(g * rep + ro % rep) * D) + c);
+        float f[8], top = 0.f;
+        Unpack<T>::run(v, f);
+#pragma unroll
+        for (int d = 0; d < 8; ++d) top = fmaxf(top, fabsf(f[d]));
+#pragma unroll
+        for (int o = 1; o < LR; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
         const int ex = static_cast<int>(__float_as_uint(top) >> 23);
         const int up = top > 0.f && ex < 255 ? 14 + 127 - ex : 0;
         const int ua = up / 2, ub = up - ua;  // in two steps: 2^up itself may not be a normal number
-        const float sign = a.scale < 0.f ? -1.f : 1.f;
         const float sa = __uint_as_float((127 + ua) << 23) * sign, sb = __uint_as_float((127 + ub) << 23);
-        f_row = fabsf(a.scale) * kLog2e * __uint_as_float((127 - ua) << 23) * __uint_as_float((127 - ub) << 23);
-        uint8_t* dst = smem + qi * S::QB;
-#pragma unroll 4
-        for (int c = 0; c < D / 8; ++c) {
-          float f[8];
-          dims8(c, f);
-          uint32_t h[4];
+        uint32_t h[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) h[e] = pack_half2(f[2 * e] * sa * sb, f[2 * e + 1] * sa * sb);
-          *reinterpret_cast<uint4*>(dst + (c >> 3) * S::QA + sw128(row, 8 * (c & 7))) = make_uint4(h[0], h[1], h[2], h[3]);
-        }
+        for (int d = 0; d < 4; ++d) h[d] = pack_half2(f[2 * d] * sa * sb, f[2 * d + 1] * sa * sb);
+        *reinterpret_cast<uint4*>(smem + j * S::QB + (c >> 3) * S::QA + sw128(ro, 8 * (c & 7))) = make_uint4(h[0], h[1], h[2], h[3]);
+        if (c == 0) s_row[e] = fabsf(a.scale) * kLog2e * __uint_as_float((127 - ua) << 23) * __uint_as_float((127 - ub) << 23);
       }
       // the largest V scale of the CTA's keys
-      const int j0 = (ta * kChKeys) >> p.block_log2, j1 = (min(tb * kChKeys, kend) - 1) >> p.block_log2;
       float top = 0.f;
-      for (int j = j0 + tid; j <= j1; j += kChThreads) {
-        const int id = __ldg(table + j);
-        if (id >= 0 && id < p.n_blocks) top = fmaxf(top, __ldg(p.vs + static_cast<size_t>(id) * p.n_kv + g));
+#pragma unroll 1
+      for (int j = j0 + tid; j <= j1; j += 4 * kChThreads) {
+        if (j != j0 + tid)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) vid[e] = j + e * kChThreads <= j1 ? __ldg(table + j + e * kChThreads) : -1;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (static_cast<unsigned>(vid[e]) < static_cast<unsigned>(p.n_blocks))
+            top = fmaxf(top, __ldg(p.vs + static_cast<size_t>(vid[e]) * p.n_kv + g));
       }
       top = warp_max(top);
       if (lane == 0) atomicMax(&s_vref, __float_as_uint(top));
@@ -293,155 +321,169 @@ __global__ void __launch_bounds__(kChThreads, 1)
       constexpr int CH = D / 16, N = kChKeys * CH / (32 * kConvWarps);  // 16-code chunks per row, per thread
       constexpr int RS = 32 * kConvWarps / CH;                          // rows between a thread's chunks
       const int row0 = ct / CH, ch = ct % CH;
-      const int bmask = (1 << p.block_log2) - 1;
-      // the block of each chunk's quarter, and (threads 0 .. 3) of quarter ct; -1: none
-      int id[N], mine = -1;
-      auto ids_of = [&](int kt) {
-        auto block_at = [&](int key0) {
-          int d = key0 < kend ? __ldg(table + (key0 >> p.block_log2)) : -1;
-          if (key0 < kend && (d < 0 || d >= p.n_blocks)) {
-            raise_flag(p.flags, K2_PAGED_BAD_BLOCK);
-            d = -1;
-          }
-          return d;
-        };
-#pragma unroll
-        for (int c = 0; c < N; ++c) id[c] = block_at(kt * kChKeys + ((row0 + c * RS) & ~15));
-        if (ct < 4) mine = block_at(kt * kChKeys + 16 * ct);
-      };
-      // requests this thread's codes of tile i (ids of it in `id`), rows behind the last key as zeros
-      auto request_codes = [&](int i) {
-        const int slot = (n_kv + i) % kCodeTiles, kt = ta + i;
-        const uint32_t dst = smem_u32(smem + S::OFF_CODES + slot * S::CODES) + 16 * ct;
-#pragma unroll
-        for (int c = 0; c < N; ++c) {
-          const int key = kt * kChKeys + row0 + c * RS;
-          const bool take = id[c] >= 0 && key < q.len;
-          const size_t off = take ? (((static_cast<size_t>(id[c]) * p.n_kv + g) << p.block_log2) + (key & bmask)) * D + ch * 16 : 0;
-          cp_async16_zfill(dst + 16 * 32 * kConvWarps * c, p.k + off, take);
-          cp_async16_zfill(dst + 16 * 32 * kConvWarps * c + S::CODES / 2, p.v + off, take);
-        }
-        if (ct < 4) {
-          if (mine >= 0) {
-            const size_t at = static_cast<size_t>(mine) * p.n_kv + g;
-            cp_async4(&sc_raw[slot][ct][0], p.ks + at);
-            cp_async4(&sc_raw[slot][ct][1], p.vs + at);
-          } else {
-            sc_raw[slot][ct][0] = -1.f;
-            sc_raw[slot][ct][1] = 0.f;
-          }
-        }
-      };
-      ids_of(ta);
-#pragma unroll 1
-      for (int i = 0; i < kCodeTiles - 1; ++i) {
-        if (i < tiles) {
-          request_codes(i);
-          ids_of(ta + i + 1);
-        }
-        cp_async_commit();
-      }
+      const int atom = ch >> 2, e0 = (ch & 3) * 16;
+      const bool swap = atom != 0;  // lanes of the two atoms write opposite halves: no bank conflicts
 #pragma unroll 1
       for (int i = 0; i < tiles; ++i) {
         const int n = n_kv + i, st = n % ST, slot = n % kCodeTiles;
-        if (i + kCodeTiles - 1 < tiles) {
-          request_codes(i + kCodeTiles - 1);
-          ids_of(ta + i + kCodeTiles);
-        }
-        cp_async_commit();
-        cp_async_wait<kCodeTiles - 1>();
-        if (n >= ST && !__all_sync(0xffffffffu, await(&kv_empty[st], n / ST - 1, &stop))) break;
-        uint8_t* kst = smem + S::OFF_ST + st * 2 * S::KB;
+        if (!__all_sync(0xffffffffu, await(&code_full[slot], n / kCodeTiles, &stop))) break;
         const uint8_t* cst = smem + S::OFF_CODES + slot * S::CODES + 16 * ct;
+        uint4 kc[N], vc[N];
 #pragma unroll
         for (int c = 0; c < N; ++c) {
-          const int rr = row0 + c * RS;
-          const int atom = ch >> 2, e0 = (ch & 3) * 16;
-          uint8_t* ka = kst + atom * S::KA;
-          const uint32_t lo = sw128(rr, e0), hi = sw128(rr, e0 + 8);
-          const bool swap = atom != 0;  // lanes of the two atoms write opposite halves: no bank conflicts
+          kc[c] = *reinterpret_cast<const uint4*>(cst + 16 * 32 * kConvWarps * c);
+          vc[c] = *reinterpret_cast<const uint4*>(cst + 16 * 32 * kConvWarps * c + S::CODES / 2);
+        }
+        // rows behind the request's last key, and quarters without a block, are zeros
+        const float4 kq = *reinterpret_cast<const float4*>(sc_k[n % kScaleTiles]);
+        if ((ta + i + 1) * kChKeys > q.len || fminf(fminf(kq.x, kq.y), fminf(kq.z, kq.w)) < 0.f) {
+#pragma unroll
+          for (int c = 0; c < N; ++c) {
+            const int rr = row0 + c * RS;
+            if ((ta + i) * kChKeys + rr >= q.len || sc_k[n % kScaleTiles][rr >> 4] < 0.f) kc[c] = vc[c] = make_uint4(0, 0, 0, 0);
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&code_empty[slot]);
+        if (n >= ST && !__all_sync(0xffffffffu, await(&kv_empty[st], n / ST - 1, &stop))) break;
+        uint8_t* kst = smem + S::OFF_ST + st * 2 * S::KB + atom * S::KA;
+#pragma unroll
+        for (int c = 0; c < N; ++c) {
+          const uint32_t lo = sw128(row0 + c * RS, e0), hi = sw128(row0 + c * RS, e0 + 8);
 #pragma unroll
           for (int m = 0; m < 2; ++m) {
-            const uint4 u = *reinterpret_cast<const uint4*>(cst + 16 * 32 * kConvWarps * c + m * (S::CODES / 2));
+            const uint4 u = m ? vc[c] : kc[c];
             const uint32_t w0 = W::prep(swap ? u.z : u.x), w1 = W::prep(swap ? u.w : u.y), w2 = W::prep(swap ? u.x : u.z),
                            w3 = W::prep(swap ? u.y : u.w);
-            uint8_t* dst = ka + m * S::KB;
+            uint8_t* dst = kst + m * S::KB;
             *reinterpret_cast<uint4*>(dst + (swap ? hi : lo)) = make_uint4(
                 W::template pair<false>(w0), W::template pair<true>(w0), W::template pair<false>(w1), W::template pair<true>(w1));
             *reinterpret_cast<uint4*>(dst + (swap ? lo : hi)) = make_uint4(
                 W::template pair<false>(w2), W::template pair<true>(w2), W::template pair<false>(w3), W::template pair<true>(w3));
           }
         }
-        if (ct < 4) {
-          const float k_s = sc_raw[slot][ct][0], v_s = sc_raw[slot][ct][1];
-          const float ratio = vref > 0.f ? fmaxf(v_s / vref, 8.6736174e-19f) : 8.6736174e-19f;  // 2^-60: as good as zero
-          const float up = log2f(ratio) + kUp;
-          sc_k[st][ct] = k_s;
-          sc_up[st][ct] = k_s < 0.f ? 0.f : up;
-          sc_down[st][ct] = k_s < 0.f ? 0.f : exp2f(-up);
-        }
         fence_proxy_async();  // generic stores before the MMAs read them
         __syncwarp();
         if (lane == 0) mbar_arrive(&kv_full[st]);
       }
-      cp_async_wait<0>();
-    } else if (warp == kSoftWarps + kConvWarps) {
+    } else if (warp == kFetchWarp) {
+      // ---- codes and scales from memory -------------------------------------------------------------
+      // lanes 0 .. 7: K (even) and V codes of quarter lane / 2; lanes 8 .. 11: the scales of quarter lane - 8
+      const int quarter = lane < 8 ? lane >> 1 : lane & 3;
+      const bool copies = lane < 8, scales = lane >= 8 && lane < 12;
+      auto id_of = [&](int i) {
+        const int key0 = (ta + i) * kChKeys + 16 * quarter;
+        return i < tiles && key0 < kend ? __ldg(table + (key0 >> p.block_log2)) : -2;  // -2: behind the last key
+      };
+      auto scales_of = [&](int id, float& k_s, float& v_s) {
+        k_s = -1.f;
+        v_s = 0.f;
+        if (scales && static_cast<unsigned>(id) < static_cast<unsigned>(p.n_blocks)) {
+          const size_t at = static_cast<size_t>(id) * p.n_kv + g;
+          k_s = __ldg(p.ks + at);
+          v_s = __ldg(p.vs + at);
+        }
+      };
+      int id = id_of(0), id_next = id_of(1);
+      float k_s, v_s, k_next, v_next;
+      scales_of(id, k_s, v_s);
+      int i = 0;
+#pragma unroll 1
+      for (; i < tiles; ++i) {
+        const int n = n_kv + i, slot = n % kCodeTiles;
+        const int id_after = id_of(i + 2);
+        scales_of(id_next, k_next, v_next);
+        if (n >= kCodeTiles && !__all_sync(0xffffffffu, await(&code_empty[slot], n / kCodeTiles - 1, &stop))) break;
+        const bool valid = static_cast<unsigned>(id) < static_cast<unsigned>(p.n_blocks);
+        if (!valid && id != -2 && lane < 8) raise_flag(p.flags, K2_PAGED_BAD_BLOCK);
+        if (scales) {
+          // a scale of (as good as) zero counts as 2^-60
+          const float up = __log2f(vref > 0.f ? fmaxf(__fdividef(v_s, vref), 8.6736174e-19f) : 8.6736174e-19f) + kUp;
+          sc_k[n % kScaleTiles][quarter] = k_s;
+          sc_up[n % kScaleTiles][quarter] = k_s < 0.f ? 0.f : up;
+          sc_down[n % kScaleTiles][quarter] = k_s < 0.f ? 0.f : exp2_approx(-up);
+        }
+        const unsigned some = __ballot_sync(0xffffffffu, copies && valid);
+        __syncwarp();
+        if (lane == 0) mbar_arrive_expect_tx(&code_full[slot], __popc(some) * 16 * D);  // after the warp's scale stores
+        __syncwarp();
+        if (copies && valid) {
+          const int key0 = (ta + i) * kChKeys + 16 * quarter;
+          const size_t off = (((static_cast<size_t>(id) * p.n_kv + g) << p.block_log2) + (key0 & ((1 << p.block_log2) - 1))) * D;
+          bulk_g2s(smem + S::OFF_CODES + slot * S::CODES + (lane & 1) * (S::CODES / 2) + quarter * 16 * D,
+                   (lane & 1 ? p.v : p.k) + off, 16 * D, &code_full[slot]);
+        }
+        id = id_next;
+        id_next = id_after;
+        k_s = k_next;
+        v_s = v_next;
+      }
+      if (i < tiles)  // given up: copies in flight land before the memory goes away
+        for (int n = n_kv + max(0, i - kCodeTiles); n < n_kv + i; ++n) (void)mbar_wait(&code_full[n % kCodeTiles], (n / kCodeTiles) & 1);
+    } else if (warp == kMmaWarp) {
       // ---- the MMAs ------------------------------------------------------------------------------
-      if (lane == 0) {
-        auto issue_s = [&](int j, int n) {  // S of query tile j over ring tile n
-          const uint8_t* kst = smem + S::OFF_ST + (n % ST) * 2 * S::KB;
-          const uint8_t* qst = smem + j * S::QB;
+      const uint32_t tm = tmem;
+      if (elect()) {
+      const uint64_t qd = smem_desc(smem), kd = smem_desc(smem + S::OFF_ST),
+                     vd = smem_desc_mn(smem + S::OFF_ST + S::KB, S::KA, 8 * 128);
+      auto issue_s = [&](int j, int st) {  // S of query tile j over stage st (offsets in units of 16 bytes)
+        const uint64_t qj = qd + static_cast<uint64_t>(j * (S::QB >> 4)), ks = kd + static_cast<uint64_t>(st * (2 * S::KB >> 4));
+        const uint32_t d = tm + S::TM_S + kChKeys * j;
+        mma_ss<false>(d, qj, ks, S::IDESC_S);
 #pragma unroll
-          for (int e = 0; e < D / 16; ++e)
-            mma(tmem + S::TM_S + kChKeys * j, smem_desc(qst + (e >> 2) * S::QA + (e & 3) * 32),
-                smem_desc(kst + (e >> 2) * S::KA + (e & 3) * 32), S::IDESC_S, e > 0 ? 1u : 0u);
-          mma_commit(&s_full[j]);
-        };
-        auto issue_o = [&](int j, int n, bool first) {
-          const uint8_t* vst = smem + S::OFF_ST + (n % ST) * 2 * S::KB + S::KB;
+        for (int e = 1; e < D / 16; ++e)
+          mma_ss<true>(d, qj + ((e >> 2) * S::QA + (e & 3) * 32 >> 4), ks + ((e >> 2) * S::KA + (e & 3) * 32 >> 4), S::IDESC_S);
+        mma_commit(&s_full[j]);
+      };
+      auto issue_o = [&](int j, int st, bool first) {
+        const uint64_t vs = vd + static_cast<uint64_t>(st * (2 * S::KB >> 4));
 #pragma unroll
-          for (int e = 0; e < kChKeys / 16; ++e)
-            mma_ta(tmem + j * D, tmem + S::TM_P + 32 * j + 8 * e, smem_desc_mn(vst + e * 16 * 128, S::KA, 8 * 128), S::IDESC_O,
-                   first && e == 0 ? 0u : 1u);
-          mma_commit(&o_done[j]);
-        };
-        bool ok = await(&kv_full[n_kv % ST], n_kv / ST, &stop);
-        if (ok) {
-          tc_after();
-          for (int j = 0; j < nqt; ++j) issue_s(j, n_kv);
-        }
-        for (int i = 0; i < tiles && ok; ++i) {
-          const int n = n_kv + i;
-          if (i + 1 < tiles && !(ok = await(&kv_full[(n + 1) % ST], (n + 1) / ST, &stop))) break;
-          for (int j = 0; j < nqt && ok; ++j) {
-            const int m = n_q[j] + i;
-            if (i + 1 < tiles) {  // the scores of tile i are in registers: S of the next tile
-              if (!(ok = await(&s_free[j], m, &stop))) break;
-              tc_after();
-              issue_s(j, n + 1);
-            }
-            if (!(ok = await(&p_ready[j], m, &stop))) break;
+        for (int e = 0; e < kChKeys / 16; ++e)
+          mma_ts(tm + j * D, tm + S::TM_P + 32 * j + 8 * e, vs + (e * 16 * 128 >> 4), S::IDESC_O, first && e == 0 ? 0u : 1u);
+        mma_commit(&o_done[j]);
+      };
+      auto waited = [&](uint64_t* bar, int n) { return await(bar, n, &stop); };
+      int st = n_kv % ST;
+      bool ok = waited(&kv_full[st], n_kv / ST);
+      if (ok) {
+        tc_after();
+        for (int j = 0; j < nqt; ++j) issue_s(j, st);
+      }
+      for (int i = 0; i < tiles && ok; ++i) {
+        const int n = n_kv + i, next = st + 1 == ST ? 0 : st + 1;
+        if (i + 1 < tiles && !(ok = waited(&kv_full[next], (n + 1) / ST))) break;
+        for (int j = 0; j < nqt && ok; ++j) {
+          const int m = n_q[j] + i;
+          if (i + 1 < tiles) {  // the scores of tile i are in registers: S of the next tile
+            if (!(ok = waited(&s_free[j], m))) break;
             tc_after();
-            issue_o(j, n, i == 0);
+            issue_s(j, next);
           }
-          if (ok) mma_commit(&kv_empty[n % ST]);
+          if (!(ok = waited(&p_ready[j], m))) break;
+          tc_after();
+          issue_o(j, st, i == 0);
         }
-        if (!ok) {  // whatever is in flight ends before the memory goes away
-          mma_commit(&drained);
-          (void)mbar_wait(&drained, 0);
-        }
+        if (ok) mma_commit(&kv_empty[st]);
+        st = next;
+      }
+      if (!ok) {  // whatever is in flight ends before the memory goes away
+        mma_commit(&drained);
+        (void)mbar_wait(&drained, 0);
+      }
       }
     } else if (soft) {
       // ---- softmax: one row per thread -------------------------------------------------------------
       const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
       const int qpos = cost.basek + tok;  // the row sees keys 0 .. qpos
+      const float f_row = s_row[qi * kChRows + row];
       bool ok = true;
       for (int i = 0; i < tiles; ++i) {
         const int n = n_kv + i, m = n_q[qi] + i, st = n % ST;
         ok = await(&kv_full[st], n / ST, &stop) && await(&s_full[qi], m, &stop);  // the tile's scales; its scores
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
-        const float4 kq = *reinterpret_cast<const float4*>(sc_k[st]), uq = *reinterpret_cast<const float4*>(sc_up[st]),
-                     dq = *reinterpret_cast<const float4*>(sc_down[st]);
+        const int sl = n % kScaleTiles;
+        const float4 kq = *reinterpret_cast<const float4*>(sc_k[sl]), uq = *reinterpret_cast<const float4*>(sc_up[sl]),
+                     dq = *reinterpret_cast<const float4*>(sc_down[sl]);
         const float kk[4] = {kq.x, kq.y, kq.z, kq.w}, uu[4] = {uq.x, uq.y, uq.z, uq.w}, dd[4] = {dq.x, dq.y, dq.z, dq.w};
         tc_after();
         uint32_t raw[kChKeys];
