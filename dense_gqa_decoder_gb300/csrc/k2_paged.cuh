@@ -211,13 +211,7 @@ struct Share {  // equal shares of `total` units of work: the first unit of CTA 
 };
 
 
-// the workspace of k2_paged_attention: one counter per CTA, then two parts of its share for each
 constexpr int kAttnMaxCtas = 1024;
-constexpr size_t kCounterBytes = sizeof(unsigned) * kAttnMaxCtas;
-struct AttnWorkspace {
-  unsigned* counters;
-  float* parts;
-};
 
 // opts a kernel in to its shared memory, once per device (bit `dev` of `ready`)
 inline cudaError_t allow_smem(const void* kernel, int bytes, int dev, std::atomic<uint64_t>& ready) {
@@ -231,6 +225,6 @@ inline cudaError_t allow_smem(const void* kernel, int bytes, int dev, std::atomi
 // prompt chunks (k2_paged_chunk.cu): the requests with more than small_rows query rows
 size_t paged_chunk_part_bytes();  // of one CTA's two parts
 cudaError_t launch_paged_chunk(const PagedPool& p, const PagedAttnArgs& a, int head_dim, int kv_dtype, int q_dtype,
-                               int small_rows, const AttnWorkspace& w, int sms, int dev, cudaStream_t s);
+                               int small_rows, float* parts, int sms, int dev, cudaStream_t s);
 
 }  // namespace k2

@@ -94,6 +94,7 @@ __global__ void __launch_bounds__(kDecThreads, Dec<D, NT>::kCtas)
   __shared__ int s_req, s_last;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gq = lane >> 2, t = lane & 3;
   const int rep = a.n_heads / p.n_kv;
+  pdl_trigger();  // the kernel for prompt chunks may start beside this one
 
   // the tiles of every request, and this CTA's share of them
   auto tiles_of = [&](const Req& x) -> int {
@@ -544,6 +545,11 @@ __global__ void __launch_bounds__(kDecThreads, Dec<D, NT>::kCtas)
 }
 
 // ---- launches ------------------------------------------------------------------------------------
+struct AttnWorkspace {
+  unsigned* counters;
+  float* parts;
+};
+
 template <typename T, typename C, int D, int NT>
 cudaError_t launch_decode(const PagedPool& p, const PagedAttnArgs& a, int small_rows, const AttnWorkspace& w, int sms, int dev, cudaStream_t s) {
   using S = Dec<D, NT>;
@@ -581,6 +587,12 @@ int sm_count(int* dev) {
   return n;
 }
 
+// the workspace: the decode kernel's counters (one per CTA) and two parts of each CTA's share, then the chunk kernel's parts
+constexpr size_t kCounterBytes = sizeof(unsigned) * kAttnMaxCtas;
+size_t few_bytes(size_t sms) {
+  return kCounterBytes + sizeof(float) * 2 * kDecSlotFloats * std::min<size_t>(3 * sms, kAttnMaxCtas);
+}
+
 }  // namespace
 
 }  // namespace k2
@@ -592,8 +604,7 @@ extern "C" {
 size_t k2_paged_workspace_bytes(void) {
   int dev = 0;
   const size_t sms = static_cast<size_t>(sm_count(&dev));
-  const size_t few = sizeof(float) * 2 * kDecSlotFloats * std::min<size_t>(3 * sms, kAttnMaxCtas);
-  return kCounterBytes + std::max(few, paged_chunk_part_bytes() * std::min<size_t>(sms, kAttnMaxCtas));
+  return few_bytes(sms) + paged_chunk_part_bytes() * std::min<size_t>(sms, kAttnMaxCtas);
 }
 
 k2_status k2_paged_attention(const k2_paged_kv* kv, const void* d_q, int32_t dtype, int64_t q_stride,
@@ -642,8 +653,8 @@ k2_status k2_paged_attention(const k2_paged_kv* kv, const void* d_q, int32_t dty
     set_error("no CUDA device");
     return K2_ERR_CUDA;
   }
-  const AttnWorkspace w = {static_cast<unsigned*>(d_workspace),
-                       reinterpret_cast<float*>(static_cast<uint8_t*>(d_workspace) + kCounterBytes)};
+  uint8_t* ws = static_cast<uint8_t*>(d_workspace);
+  const AttnWorkspace w = {reinterpret_cast<unsigned*>(ws), reinterpret_cast<float*>(ws + kCounterBytes)};
   const PagedPool p(*kv);
   const PagedAttnArgs a = {d_q, q_stride, d_cu_q, d_kv_len, d_table, table_stride, requests,
                            tokens, n_heads, std::min(max_q, tokens), scale, d_out, out_stride};
@@ -658,7 +669,7 @@ k2_status k2_paged_attention(const k2_paged_kv* kv, const void* d_q, int32_t dty
     e = kv->dtype == K2_I8 ? launch<__nv_bfloat16, CodeI8>(p, d, a, small, w, sms, dev, s)
                            : launch<__nv_bfloat16, CodeF8>(p, d, a, small, w, sms, dev, s);
   if (e == cudaSuccess && static_cast<int64_t>(a.max_q) * rep > small)
-    e = launch_paged_chunk(p, a, d, kv->dtype, dtype, small, w, sms, dev, s);
+    e = launch_paged_chunk(p, a, d, kv->dtype, dtype, small, reinterpret_cast<float*>(ws + few_bytes(static_cast<size_t>(sms))), sms, dev, s);
   if (e == cudaSuccess) return K2_OK;
   set_error("attention launch: %s", cudaGetErrorString(e));
   return K2_ERR_CUDA;

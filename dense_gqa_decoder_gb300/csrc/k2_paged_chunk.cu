@@ -59,9 +59,7 @@ struct Ch {
   static constexpr int OFF_ST = 2 * QB;
   static constexpr int OFF_CODES = OFF_ST + kChStages * 2 * KB;
   static constexpr int CODES = 2 * kChKeys * D;      // K and V codes of a key tile
-  // and at least the weights of the parts of an item, which take the same memory when they are joined
-  static constexpr int BYTES = OFF_CODES + kCodeTiles * CODES > 160 * 1024 ? OFF_CODES + kCodeTiles * CODES : 160 * 1024;
-  static constexpr int PARTS = BYTES / (4 * 2 * kChRows) - 1;  // parts that can be joined: the most CTAs
+  static constexpr int BYTES = OFF_CODES + kCodeTiles * CODES;
   static constexpr int DYN = BYTES + 1024;           // + alignment to 1024 B
   // tensor memory: O of both query tiles, S, then P (two fp16 per column)
   static constexpr int TM_S = 2 * D, TM_P = 2 * D + 2 * kChKeys, TM_COLS = 512;
@@ -93,6 +91,16 @@ __device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
       "r"(a_tmem), "l"(b), "r"(idesc), "r"(accumulate)
       : "memory");
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
 }
 // 64 columns of this warp's lanes
 __device__ __forceinline__ void tmem_ld64(uint32_t taddr, uint32_t* v) {
@@ -127,9 +135,124 @@ __device__ __forceinline__ bool await(uint64_t* bar, int n, volatile int* stop) 
   return true;
 }
 
+// The step's work as one line of keys: requests one after another, in each the KV heads, in each the blocks of query
+// tokens (items), an item's keys after kChStart units for its start and end.  The CTAs take equal shares of it.
+struct ChunkWork {
+  int rep, qt, tt, n_kv, small_rows;  // query heads per KV head; tokens of a query tile, of an item
+  const PagedAttnArgs& a;
+  int block_log2;
+
+  struct Cost {
+    long long head;  // one KV head's items
+    int nb, basek;   // items, keys before the first query
+  };
+  __device__ __forceinline__ ChunkWork(const PagedPool& p, const PagedAttnArgs& args, int small)
+      : rep(args.n_heads / p.n_kv), qt(kChRows / rep), tt(2 * qt), n_kv(p.n_kv), small_rows(small), a(args),
+        block_log2(p.block_log2) {}
+  __device__ __forceinline__ Req req(int r) const { return request(a, block_log2, r); }
+  __device__ __forceinline__ Cost cost(const Req& x) const {
+    Cost c = {0, 0, 0};
+    if (x.ok && static_cast<long long>(x.nq) * rep > small_rows) {
+      c.nb = (x.nq + tt - 1) / tt;
+      c.basek = x.len - x.nq;
+      c.head = c.nb * (static_cast<long long>(kChStart) + c.basek) + static_cast<long long>(tt) * c.nb * (c.nb - 1) / 2 + x.nq;
+    }
+    return c;
+  }
+  // place of item b in its head
+  __device__ __forceinline__ long long start(const Cost& c, int b) const {
+    return b * (static_cast<long long>(kChStart) + c.basek) + static_cast<long long>(tt) * b * (b + 1) / 2;
+  }
+  __device__ __forceinline__ static int ctas(long long total, int most) {
+    return static_cast<int>(min(static_cast<long long>(most), (total + kChShare - 1) / kChShare));
+  }
+
+  struct Item {
+    Req q;
+    int r, g, t0;       // request, KV head, first query token
+    int kend, nkt, basek;
+    long long at;       // place of its first key
+    long long end;      // and behind its last
+  };
+  // the item at place x, of request r or a later one; base: place of request r
+  __device__ __forceinline__ Item item(long long x, int& r, long long& base) const {
+    Item i;
+    i.q = req(r);
+    Cost c = cost(i.q);
+    while (x >= base + c.head * n_kv) {
+      base += c.head * n_kv;
+      i.q = req(++r);
+      c = cost(i.q);
+    }
+    i.r = r;
+    i.g = static_cast<int>((x - base) / c.head);
+    const long long rem = x - base - i.g * c.head;
+    int b = 0;
+    for (int hi = c.nb; hi - b > 1;) {
+      const int mid = (b + hi) >> 1;
+      if (start(c, mid) <= rem) b = mid;
+      else hi = mid;
+    }
+    i.t0 = b * tt;
+    i.basek = c.basek;
+    i.kend = c.basek + min(i.q.nq, i.t0 + tt);
+    i.nkt = (i.kend + kChKeys - 1) / kChKeys;
+    i.at = base + i.g * c.head + start(c, b) + kChStart;
+    i.end = i.at + i.kend;
+    return i;
+  }
+};
+
+// The prefix sums over the requests, by a block of THREADS threads: the total, and (find) the request at a place
+template <int THREADS>
+struct ChunkScan {
+  long long total, own, before;
+  int per;
+  __device__ __forceinline__ ChunkScan(const ChunkWork& w, long long* sums) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    per = (w.a.requests + THREADS - 1) / THREADS;
+    own = 0;
+    for (int i = 0; i < per; ++i) {
+      const int r = tid * per + i;
+      if (r < w.a.requests) own += w.cost(w.req(r)).head * w.n_kv;
+    }
+    long long inc = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long u = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += u;
+    }
+    if (lane == 31) sums[warp] = inc;
+    __syncthreads();
+    total = 0;
+    before = inc - own;
+#pragma unroll
+    for (int i = 0; i < THREADS / 32; ++i) {
+      if (i < warp) before += sums[i];
+      total += sums[i];
+    }
+  }
+  // one thread writes the request that holds place x, and that request's place
+  __device__ __forceinline__ void find(const ChunkWork& w, long long x, int* req, long long* base) const {
+    if (x < before || x >= before + own) return;
+    long long at = before;
+    for (int i = 0; i < per; ++i) {
+      const int r = threadIdx.x * per + i;
+      if (r >= w.a.requests) break;
+      const long long n = w.cost(w.req(r)).head * w.n_kv;
+      if (x < at + n) {
+        *req = r;
+        *base = at;
+        return;
+      }
+      at += n;
+    }
+  }
+};
+
 template <typename T, typename C, int D>
 __global__ void __launch_bounds__(kChThreads, 1)
-    paged_chunk_kernel(const PagedPool p, const PagedAttnArgs a, int small_rows, const AttnWorkspace w) {
+    paged_chunk_kernel(const PagedPool p, const PagedAttnArgs a, int small_rows, float* parts) {
   using S = Ch<D>;
   using W = Widen<C>;
   constexpr int ST = kChStages;
@@ -140,40 +263,15 @@ __global__ void __launch_bounds__(kChThreads, 1)
   __shared__ __align__(16) float sc_k[kScaleTiles][4], sc_up[kScaleTiles][4], sc_down[kScaleTiles][4];
   __shared__ float s_row[2 * kChRows];  // each row's factor from accumulators to base-2 scores
   __shared__ uint32_t tmem_slot;
-  __shared__ int stop, s_last, s_req;
+  __shared__ int stop, s_req;
   __shared__ unsigned s_vref;
   __shared__ long long s_sum[kChThreads / 32], s_base;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int rep = a.n_heads / p.n_kv;
-  const int QT = kChRows / rep, TT = 2 * QT;  // tokens of a query tile, of an item
-
-  // ---- the share of this CTA ----------------------------------------------------------------
-  struct Cost {
-    long long head;  // one KV head's items
-    int nb, basek;   // items, keys before the first query
-  };
-  auto cost_of = [&](const Req& x) -> Cost {
-    Cost c = {0, 0, 0};
-    if (x.ok && static_cast<long long>(x.nq) * rep > small_rows) {
-      c.nb = (x.nq + TT - 1) / TT;
-      c.basek = x.len - x.nq;
-      c.head = c.nb * (static_cast<long long>(kChStart) + c.basek) + static_cast<long long>(TT) * c.nb * (c.nb - 1) / 2 + x.nq;
-    }
-    return c;
-  };
-  const int per = (a.requests + kChThreads - 1) / kChThreads;
-  long long own = 0;
-  for (int i = 0; i < per; ++i) {
-    const int r = tid * per + i;
-    if (r < a.requests) own += cost_of(request(a, p.block_log2, r)).head * p.n_kv;
-  }
-  long long inc = own;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long u = __shfl_up_sync(0xffffffffu, inc, o);
-    if (lane >= o) inc += u;
-  }
-  if (lane == 31) s_sum[warp] = inc;
+  const ChunkWork work(p, a, small_rows);
+  const int rep = work.rep, QT = work.qt;
+  const unsigned rep_inv = (65536u + rep - 1) / rep;  // x / rep = x * rep_inv >> 16 for x < 128 (rep <= 16)
+  auto by_rep = [&](int ro) { return static_cast<int>(static_cast<unsigned>(ro) * rep_inv >> 16); };
+  pdl_trigger();  // the kernel that joins the parts waits for this one's end
   if (tid == 0) {
     stop = 0;
     s_vref = 0u;
@@ -194,30 +292,15 @@ __global__ void __launch_bounds__(kChThreads, 1)
     mbar_init(&drained, 1);
     fence_mbar_init();
   }
-  __syncthreads();
-  long long total = 0, before = inc - own;
-  for (int i = 0; i < kChThreads / 32; ++i) {
-    if (i < warp) before += s_sum[i];
-    total += s_sum[i];
+  const ChunkScan<kChThreads> scan(work, s_sum);
+  const long long total = scan.total;
+  const int ctas = ChunkWork::ctas(total, gridDim.x);
+  if (blockIdx.x >= ctas) {
+    pdl_wait();  // this kernel started beside the one for few rows: it ends after it
+    return;
   }
-  if (total == 0) return;
-  const int ctas = static_cast<int>(min(static_cast<long long>(gridDim.x), (total + kChShare - 1) / kChShare));
-  if (blockIdx.x >= ctas) return;
   const long long x0 = Share::first(total, ctas, blockIdx.x), x1 = Share::first(total, ctas, blockIdx.x + 1);
-  if (before <= x0 && x0 < before + own) {
-    long long at = before;
-    for (int i = 0; i < per; ++i) {
-      const int r = tid * per + i;
-      if (r >= a.requests) break;
-      const long long n = cost_of(request(a, p.block_log2, r)).head * p.n_kv;
-      if (x0 < at + n) {
-        s_req = r;
-        s_base = at;
-        break;
-      }
-      at += n;
-    }
-  }
+  scan.find(work, x0, &s_req, &s_base);
   if (warp == 0) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_slot)), "r"(S::TM_COLS)
                  : "memory");
@@ -234,34 +317,20 @@ __global__ void __launch_bounds__(kChThreads, 1)
 
   for (long long x = x0; x < x1;) {
     // ---- the item at x -----------------------------------------------------------------------
-    Req q = request(a, p.block_log2, r);
-    Cost cost = cost_of(q);
-    while (x >= base + cost.head * p.n_kv) {
-      base += cost.head * p.n_kv;
-      q = request(a, p.block_log2, ++r);
-      cost = cost_of(q);
-    }
-    const int g = static_cast<int>((x - base) / cost.head);
-    const long long rem = x - base - g * cost.head;
-    auto before_b = [&](int b) { return b * (static_cast<long long>(kChStart) + cost.basek) + static_cast<long long>(TT) * b * (b + 1) / 2; };
-    int b = 0;
-    for (int hi = cost.nb; hi - b > 1;) {
-      const int mid = (b + hi) >> 1;
-      if (before_b(mid) <= rem) b = mid;
-      else hi = mid;
-    }
-    const long long item = base + g * cost.head + before_b(b) + kChStart;  // place of the item's first key
-    const int t0 = b * TT, kend = cost.basek + min(q.nq, t0 + TT), nkt = (kend + kChKeys - 1) / kChKeys;
+    const ChunkWork::Item it = work.item(x, r, base);
+    const Req q = it.q;
+    const int g = it.g, t0 = it.t0, kend = it.kend, nkt = it.nkt;
+    const long long item = it.at;
     const int ta = x0 <= item ? 0 : static_cast<int>(min((x0 - item + kChKeys - 1) / kChKeys, static_cast<long long>(nkt)));
     const int tb = x1 <= item ? 0 : static_cast<int>(min((x1 - item + kChKeys - 1) / kChKeys, static_cast<long long>(nkt)));
-    x = item + kend;
+    x = it.end;
     if (ta >= tb) continue;
     const bool whole = ta == 0 && tb == nkt;
     const int nqt = t0 + QT < q.nq ? 2 : 1, tiles = tb - ta;
     const int* table = a.table + static_cast<size_t>(r) * a.table_stride;
     // softmax threads: row `row` of query tile qi
     const int qi = warp >> 2, row = (warp & 3) * 32 + lane;
-    const int tok = t0 + qi * QT + row / rep, head = g * rep + row % rep;
+    const int dt = by_rep(row), tok = t0 + qi * QT + dt, head = g * rep + row - dt * rep;
     const bool soft = warp < kSoftWarps && qi < nqt;
     const bool row_ok = soft && row < QT * rep && tok < q.nq;
     if (!dead) {
@@ -274,10 +343,10 @@ __global__ void __launch_bounds__(kChThreads, 1)
       const float sign = a.scale < 0.f ? -1.f : 1.f;
 #pragma unroll 10
       for (int e = warp * RW + lane / LR; e < nqt * kChRows; e += RW * (kChThreads / 32)) {
-        const int j = e / kChRows, ro = e % kChRows, i = t0 + j * QT + ro / rep, c = lane % LR;
+        const int j = e / kChRows, ro = e % kChRows, dt = by_rep(ro), i = t0 + j * QT + dt, c = lane % LR;
         uint4 v = make_uint4(0, 0, 0, 0);
         if (ro < QT * rep && i < q.nq)
-          v = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + (q.q0 + i) * a.q_stride + static_cast<size_t>(g * rep + ro % rep) * D) + c);
+          v = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + (q.q0 + i) * a.q_stride + static_cast<size_t>(g * rep + ro - dt * rep) * D) + c);
         float f[8], top = 0.f;
         Unpack<T>::run(v, f);
 #pragma unroll
@@ -474,7 +543,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
     } else if (soft) {
       // ---- softmax: one row per thread -------------------------------------------------------------
       const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-      const int qpos = cost.basek + tok;  // the row sees keys 0 .. qpos
+      const int qpos = it.basek + tok;  // the row sees keys 0 .. qpos
       const float f_row = s_row[qi * kChRows + row];
       bool ok = true;
       for (int i = 0; i < tiles; ++i) {
@@ -507,10 +576,10 @@ __global__ void __launch_bounds__(kChThreads, 1)
         float mt = -INFINITY;
 #pragma unroll
         for (int h = 0; h < 4; ++h) {
-          float v = s[16 * h];
+          float v = max3(s[16 * h], s[16 * h + 1], s[16 * h + 2]);
 #pragma unroll
-          for (int e = 1; e < 16; ++e) v = fmaxf(v, s[16 * h + e]);
-          mt = fmaxf(mt, v * c1[h]);  // factors are >= 0
+          for (int e = 3; e < 15; e += 2) v = max3(v, s[16 * h + e], s[16 * h + e + 1]);
+          mt = fmaxf(mt, fmaxf(v, s[16 * h + 15]) * c1[h]);  // factors are >= 0
         }
         const bool move = mt > -INFINITY && (m_ref == -INFINITY || mt > m_ref + kLazy);
         const float alpha = move ? (m_ref == -INFINITY ? 0.f : exp2_approx(m_ref - mt)) : 1.f;
@@ -523,13 +592,19 @@ __global__ void __launch_bounds__(kChThreads, 1)
 #pragma unroll
         for (int h = 0; h < 4; ++h) {
           const float c2 = uu[h] - zm;
-          float sum = 0.f;
+          const f32x2 c11 = pk2(c1[h], c1[h]), c22 = pk2(c2, c2);
+          f32x2 sums = pk2(0.f, 0.f);
 #pragma unroll
           for (int e = 0; e < 16; e += 2) {
-            const float p0 = exp2_approx(fmaf(s[16 * h + e], c1[h], c2)), p1 = exp2_approx(fmaf(s[16 * h + e + 1], c1[h], c2));
-            sum += p0 + p1;
+            const f32x2 x2 = fma2(pk2(s[16 * h + e], s[16 * h + e + 1]), c11, c22);
+            float p0, p1;
+            asm("mov.b64 {%0, %1}, %2;" : "=f"(p0), "=f"(p1) : "l"(x2));
+            p0 = exp2_approx(p0);
+            p1 = exp2_approx(p1);
+            sums = add2(sums, pk2(p0, p1));
             pk[8 * h + e / 2] = pack_half2(p0, p1);
           }
+          const float sum = sum2(sums);
           l = fmaf(sum, dd[h], l);
         }
         if (i > 0) {  // the previous P.V has read P and written O
@@ -566,7 +641,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
     if (tid == 0) s_vref = 0u;  // read above by everyone
 
     // ---- the item's rows, or this CTA's part of them -----------------------------------------------
-    float* part = w.parts + (2 * static_cast<size_t>(blockIdx.x) + (ta == 0 ? 1 : 0)) * kPartFloats;
+    float* part = parts + (2 * static_cast<size_t>(blockIdx.x) + (ta == 0 ? 1 : 0)) * kPartFloats;
     if (soft) {
       const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
       const float nan = __uint_as_float(0x7fffffffu);
@@ -595,72 +670,98 @@ __global__ void __launch_bounds__(kChThreads, 1)
       }
       if (!whole) *reinterpret_cast<float2*>(part + 2 * kChRows * D + 2 * lrow) = make_float2(dead ? 0.f : m_ref, dead ? 1.f : l);
     }
-    if (!whole) {
-      const int c0 = Share::cta_of(total, ctas, item), c1 = Share::cta_of(total, ctas, item + static_cast<long long>(kChKeys) * (nkt - 1));
-      __threadfence();
-      __syncthreads();
-      if (tid == 0) {
-        s_last = atomicAdd(w.counters + c0, 1u) == static_cast<unsigned>(c1 - c0);
-        if (s_last) w.counters[c0] = 0u;  // as the next call wants it
-      }
-      __syncthreads();
-      if (s_last) {
-        __threadfence();
-        const int np = c1 - c0 + 1;
-        auto part_of = [&](int k) { return w.parts + (2 * static_cast<size_t>(c0 + k) + (k == 0 ? 1 : 0)) * kPartFloats; };
-        float* wt = reinterpret_cast<float*>(smem);       // the parts' weights, [k][row]
-        float* inv = wt + S::PARTS * 2 * kChRows;         // and the sums' reciprocals
-        const int nr = nqt * kChRows;
-        for (int e = tid; e < nr; e += kChThreads) {
-          float m = -INFINITY, sum = 0.f;
-          for (int k = 0; k < np; ++k) m = fmaxf(m, __ldcg(part_of(k) + 2 * kChRows * D + 2 * e));
-          for (int k = 0; k < np; ++k) {
-            const float2 ml = __ldcg(reinterpret_cast<const float2*>(part_of(k) + 2 * kChRows * D + 2 * e));
-            const float f = m > -INFINITY ? exp2_approx(ml.x - m) : 0.f;
-            wt[k * 2 * kChRows + e] = f;
-            sum += ml.y * f;
-          }
-          inv[e] = sum > 0.f ? 1.f / sum : 0.f;
-        }
-        __syncthreads();
-        for (int e = tid; e < nr * (D / 4); e += kChThreads) {
-          const int rr = e % nr, c4 = e / nr, j = rr / kChRows, ro = rr % kChRows;
-          const int i = t0 + j * QT + ro / rep;
-          if (ro >= QT * rep || i >= q.nq) continue;
-          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-          for (int k = 0; k < np; ++k) {
-            const float4 u = __ldcg(reinterpret_cast<const float4*>(part_of(k) + (static_cast<size_t>(c4) * (2 * kChRows) + rr) * 4));
-            const float f = wt[k * 2 * kChRows + rr];
-            v.x += u.x * f;
-            v.y += u.y * f;
-            v.z += u.z * f;
-            v.w += u.w * f;
-          }
-          const float f = inv[rr];
-          store4(static_cast<T*>(a.out) + (q.q0 + i) * a.out_stride + (g * rep + ro % rep) * D + 4 * c4, v.x * f, v.y * f, v.z * f, v.w * f);
-        }
-      }
-    }
     tc_before();
     __syncthreads();  // Q, the stages and tensor memory take the next item
     tc_after();
   }
+  pdl_wait();  // as above
   if (warp == 0)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(S::TM_COLS) : "memory");
 }
 
+// Items that several CTAs had a part of: block (c, slice) joins the one that began in CTA c's share, a slice of its
+// columns.  Joined by the last CTA to arrive, as the few rows of a decode step are, the parts (133 KB each) would
+// pass through one SM: 23 us for nine of them.
+constexpr int kJoinThreads = 2 * kChRows, kJoinSlices = 8;
+template <typename T, int D>
+__global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedPool p, const PagedAttnArgs a, int small_rows, const float* parts) {
+  __shared__ long long s_sum[kJoinThreads / 32], s_base;
+  __shared__ int s_req;
+  const ChunkWork work(p, a, small_rows);
+  const ChunkScan<kJoinThreads> scan(work, s_sum);
+  const int ctas = ChunkWork::ctas(scan.total, gridDim.x), c0 = blockIdx.x;
+  bool job = c0 + 1 < ctas;  // the last share ends with its last item
+  ChunkWork::Item it;
+  int c1 = 0;
+  if (job) {
+    const long long last = Share::first(scan.total, ctas, c0 + 1) - 1;  // of the share
+    scan.find(work, last, &s_req, &s_base);
+    __syncthreads();
+    int r = s_req;
+    long long base = s_base;
+    it = work.item(last, r, base);
+    c1 = Share::cta_of(scan.total, ctas, it.at + static_cast<long long>(kChKeys) * (it.nkt - 1));
+    job = Share::cta_of(scan.total, ctas, it.at) == c0 && c1 > c0;
+  }
+  pdl_wait();  // the parts
+  if (!job) return;
+  const int lr = threadIdx.x, ro = lr % kChRows, i = it.t0 + (lr / kChRows) * work.qt + ro / work.rep;
+  if (ro >= work.qt * work.rep || i >= it.q.nq) return;
+  auto part = [&](int k) { return parts + (2 * static_cast<size_t>(k) + (k == c0 ? 1 : 0)) * kPartFloats; };
+  float m = -INFINITY, l = 0.f;
+#pragma unroll 4
+  for (int k = c0; k <= c1; ++k) m = fmaxf(m, __ldcg(part(k) + 2 * kChRows * D + 2 * lr));
+  constexpr int N = D / 4 / kJoinSlices;
+  float4 v[N];
+#pragma unroll
+  for (int c = 0; c < N; ++c) v[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int k = c0; k <= c1; ++k) {
+    const float* from = part(k);
+    const float2 ml = __ldcg(reinterpret_cast<const float2*>(from + 2 * kChRows * D + 2 * lr));
+    const float f = m > -INFINITY ? exp2_approx(ml.x - m) : 0.f;
+    l += ml.y * f;
+#pragma unroll
+    for (int c = 0; c < N; ++c) {
+      const float4 u = __ldcg(reinterpret_cast<const float4*>(from + (static_cast<size_t>(blockIdx.y * N + c) * (2 * kChRows) + lr) * 4));
+      v[c].x += u.x * f;
+      v[c].y += u.y * f;
+      v[c].z += u.z * f;
+      v[c].w += u.w * f;
+    }
+  }
+  const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;  // a NaN stays one
+  T* out = static_cast<T*>(a.out) + (it.q.q0 + i) * a.out_stride + static_cast<size_t>(it.g * work.rep + ro % work.rep) * D + 4 * blockIdx.y * N;
+#pragma unroll
+  for (int c = 0; c < N; ++c) store4(out + 4 * c, v[c].x * inv, v[c].y * inv, v[c].z * inv, v[c].w * inv);
+}
+
 template <typename T, typename C, int D>
-cudaError_t launch(const PagedPool& p, const PagedAttnArgs& a, int small_rows, const AttnWorkspace& w, int sms, int dev, cudaStream_t s) {
+cudaError_t launch(const PagedPool& p, const PagedAttnArgs& a, int small_rows, float* w, int sms, int dev, cudaStream_t s) {
   auto kernel = paged_chunk_kernel<T, C, D>;
   static std::atomic<uint64_t> ready{0};
-  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), Ch<D>::DYN, dev, ready);
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), Ch<D>::DYN, dev, ready);
   if (e != cudaSuccess) return e;
-  kernel<<<std::min({sms, kAttnMaxCtas, Ch<D>::PARTS}), kChThreads, Ch<D>::DYN, s>>>(p, a, small_rows, w);
-  return cudaGetLastError();
+  // beside the kernel for few rows (it lets this one start at once): they share no output, nor workspace
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(std::min(sms, kAttnMaxCtas));
+  cfg.blockDim = dim3(kChThreads);
+  cfg.dynamicSmemBytes = Ch<D>::DYN;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, kernel, p, a, small_rows, w);
+  if (e != cudaSuccess) return e;
+  cfg.gridDim.y = kJoinSlices;
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, paged_join_kernel<T, D>, p, a, small_rows, static_cast<const float*>(w));
 }
 template <typename T, typename C>
-cudaError_t launch(const PagedPool& p, const PagedAttnArgs& a, int d, int small_rows, const AttnWorkspace& w, int sms, int dev, cudaStream_t s) {
+cudaError_t launch(const PagedPool& p, const PagedAttnArgs& a, int d, int small_rows, float* w, int sms, int dev, cudaStream_t s) {
   return d == 128 ? launch<T, C, 128>(p, a, small_rows, w, sms, dev, s) : launch<T, C, 64>(p, a, small_rows, w, sms, dev, s);
 }
 
@@ -669,7 +770,7 @@ cudaError_t launch(const PagedPool& p, const PagedAttnArgs& a, int d, int small_
 size_t paged_chunk_part_bytes() { return 2 * sizeof(float) * kPartFloats; }
 
 cudaError_t launch_paged_chunk(const PagedPool& p, const PagedAttnArgs& a, int head_dim, int kv_dtype, int q_dtype,
-                               int small_rows, const AttnWorkspace& w, int sms, int dev, cudaStream_t s) {
+                               int small_rows, float* w, int sms, int dev, cudaStream_t s) {
   if (q_dtype == K2_F16)
     return kv_dtype == K2_I8 ? launch<__half, CodeI8>(p, a, head_dim, small_rows, w, sms, dev, s)
                              : launch<__half, CodeF8>(p, a, head_dim, small_rows, w, sms, dev, s);
