@@ -7,12 +7,15 @@
 //   one warp fetches the tile's codes (bulk copies of 16 rows, kCodeTiles tiles ahead) and its scales;
 //   four warps widen the codes to fp16 (exact) into shared memory, K and V
 //     alike as swizzled rows (V enters P.V through an MN-major descriptor);
-//   one warp issues S = Q K^T (S in tensor memory) and O += P V (P and O in
+//   one warp per query tile issues S = Q K^T (S in tensor memory) and O += P V (P and O in
 //     tensor memory);
 //   four warps per query tile take a row per thread: no exchange between threads
 //     anywhere in the softmax.
 // The two query tiles alternate: while one's softmax runs, the other's MMAs do,
 // and S of the next key tile is issued as soon as the scores are in registers.
+//
+// int8 codes of K enter as 1152 + c (the widening without its subtraction): 1152 times the sum of the query row is
+// taken off the scores, whose fp32 accumulator it makes about nine times a full-scale score's, far below the rounding of p.
 //
 // Scales: the queries carry a power of two that brings a row into fp16's upper
 // range (exact); a block's K scale multiplies its 16 scores' common factor, and its V
@@ -37,8 +40,8 @@ namespace k2 {
 namespace {
 
 constexpr int kSoftWarps = 8, kConvWarps = 4;
-constexpr int kMmaWarp = kSoftWarps + kConvWarps, kFetchWarp = kMmaWarp + 1;
-constexpr int kChThreads = 32 * (kFetchWarp + 1);
+constexpr int kFetchWarp = kSoftWarps + kConvWarps, kMmaWarp = kFetchWarp + 1;  // and one more: one per query tile
+constexpr int kChThreads = 32 * (kMmaWarp + 2);
 constexpr int kChRows = 128, kChKeys = 64, kChStages = 3;
 constexpr int kCodeTiles = 4;  // key tiles of codes on their way
 // tiles whose scales are kept: one is read by a softmax warp up to kCodeTiles + kChStages - 1 tiles after it was fetched
@@ -250,6 +253,12 @@ struct ChunkScan {
   }
 };
 
+// two waits whose first tries overlap (a try takes over a hundred cycles)
+__device__ __forceinline__ bool await2(uint64_t* a, int na, uint64_t* b, int nb, volatile int* stop) {
+  const bool x = mbar_try_wait(a, static_cast<uint32_t>(na) & 1u), y = mbar_try_wait(b, static_cast<uint32_t>(nb) & 1u);
+  return (x || await(a, na, stop)) && (y || await(b, nb, stop));
+}
+
 template <typename T, typename C, int D>
 __global__ void __launch_bounds__(kChThreads, 1)
     paged_chunk_kernel(const PagedPool p, const PagedAttnArgs a, int small_rows, float* parts) {
@@ -258,10 +267,12 @@ __global__ void __launch_bounds__(kChThreads, 1)
   constexpr int ST = kChStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  __shared__ __align__(8) uint64_t kv_full[ST], kv_empty[ST], code_full[kCodeTiles], code_empty[kCodeTiles], s_full[2], s_free[2], p_ready[2], o_done[2], drained;
+  __shared__ __align__(8) uint64_t kv_full[ST], kv_empty[ST], code_full[kCodeTiles], code_empty[kCodeTiles], s_full[2], s_free[2], p_ready[2], o_done[2], drained[2];
   // of a tile's 16-key quarters: the K scale (-1: no keys), log2(vs / vref) + kUp and 2^- of that
   __shared__ __align__(16) float sc_k[kScaleTiles][4], sc_up[kScaleTiles][4], sc_down[kScaleTiles][4];
-  __shared__ float s_row[2 * kChRows];  // each row's factor from accumulators to base-2 scores
+  // each query row's power of two (+ 113), and what its scores' accumulators are too large by (W::kOffset times the row's sum)
+  __shared__ uint8_t s_up[2 * kChRows];
+  __shared__ float s_off[W::kOffset != 0.f ? 2 * kChRows : 1];
   __shared__ uint32_t tmem_slot;
   __shared__ int stop, s_req;
   __shared__ unsigned s_vref;
@@ -277,7 +288,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
     s_vref = 0u;
     for (int i = 0; i < ST; ++i) {
       mbar_init(&kv_full[i], kConvWarps);
-      mbar_init(&kv_empty[i], 1);
+      mbar_init(&kv_empty[i], 2);
     }
     for (int i = 0; i < kCodeTiles; ++i) {
       mbar_init(&code_full[i], 1);
@@ -288,8 +299,8 @@ __global__ void __launch_bounds__(kChThreads, 1)
       mbar_init(&s_free[q], 4);
       mbar_init(&p_ready[q], 4);
       mbar_init(&o_done[q], 1);
+      mbar_init(&drained[q], 1);
     }
-    mbar_init(&drained, 1);
     fence_mbar_init();
   }
   const ChunkScan<kChThreads> scan(work, s_sum);
@@ -360,8 +371,16 @@ __global__ void __launch_bounds__(kChThreads, 1)
         uint32_t h[4];
 #pragma unroll
         for (int d = 0; d < 4; ++d) h[d] = pack_half2(f[2 * d] * sa * sb, f[2 * d + 1] * sa * sb);
+        if constexpr (W::kOffset != 0.f) {
+          float sum = 0.f;
+#pragma unroll
+          for (int d = 0; d < 8; ++d) sum += f[d] * sa * sb;  // (exact products)
+#pragma unroll
+          for (int o = 1; o < LR; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+          if (c == 0) s_off[e] = W::kOffset * sum;
+        }
         *reinterpret_cast<uint4*>(smem + j * S::QB + (c >> 3) * S::QA + sw128(ro, 8 * (c & 7))) = make_uint4(h[0], h[1], h[2], h[3]);
-        if (c == 0) s_row[e] = fabsf(a.scale) * kLog2e * __uint_as_float((127 - ua) << 23) * __uint_as_float((127 - ub) << 23);
+        if (c == 0) s_up[e] = static_cast<uint8_t>(up + 113);  // -113 .. 141
       }
       // the largest V scale of the CTA's keys
       float top = 0.f;
@@ -387,21 +406,22 @@ __global__ void __launch_bounds__(kChThreads, 1)
     } else if (warp >= kSoftWarps && warp < kSoftWarps + kConvWarps) {
       // ---- codes to fp16 ---------------------------------------------------------------------
       const int ct = tid - 32 * kSoftWarps;
-      constexpr int CH = D / 16, N = kChKeys * CH / (32 * kConvWarps);  // 16-code chunks per row, per thread
+      constexpr int CH = D / 8, N = kChKeys * CH / (32 * kConvWarps);  // 8-code chunks per row, per thread
       constexpr int RS = 32 * kConvWarps / CH;                          // rows between a thread's chunks
       const int row0 = ct / CH, ch = ct % CH;
-      const int atom = ch >> 2, e0 = (ch & 3) * 16;
-      const bool swap = atom != 0;  // lanes of the two atoms write opposite halves: no bank conflicts
+      uint32_t put[N];  // where this thread's codes go, within K (or V) of a stage
+#pragma unroll
+      for (int c = 0; c < N; ++c) put[c] = (ch >> 3) * S::KA + sw128(row0 + c * RS, 8 * (ch & 7));
 #pragma unroll 1
       for (int i = 0; i < tiles; ++i) {
         const int n = n_kv + i, st = n % ST, slot = n % kCodeTiles;
         if (!__all_sync(0xffffffffu, await(&code_full[slot], n / kCodeTiles, &stop))) break;
-        const uint8_t* cst = smem + S::OFF_CODES + slot * S::CODES + 16 * ct;
-        uint4 kc[N], vc[N];
+        const uint8_t* cst = smem + S::OFF_CODES + slot * S::CODES + 8 * ct;
+        uint2 kc[N], vc[N];
 #pragma unroll
         for (int c = 0; c < N; ++c) {
-          kc[c] = *reinterpret_cast<const uint4*>(cst + 16 * 32 * kConvWarps * c);
-          vc[c] = *reinterpret_cast<const uint4*>(cst + 16 * 32 * kConvWarps * c + S::CODES / 2);
+          kc[c] = *reinterpret_cast<const uint2*>(cst + 8 * 32 * kConvWarps * c);
+          vc[c] = *reinterpret_cast<const uint2*>(cst + 8 * 32 * kConvWarps * c + S::CODES / 2);
         }
         // rows behind the request's last key, and quarters without a block, are zeros
         const float4 kq = *reinterpret_cast<const float4*>(sc_k[n % kScaleTiles]);
@@ -409,27 +429,20 @@ __global__ void __launch_bounds__(kChThreads, 1)
 #pragma unroll
           for (int c = 0; c < N; ++c) {
             const int rr = row0 + c * RS;
-            if ((ta + i) * kChKeys + rr >= q.len || sc_k[n % kScaleTiles][rr >> 4] < 0.f) kc[c] = vc[c] = make_uint4(0, 0, 0, 0);
+            if ((ta + i) * kChKeys + rr >= q.len || sc_k[n % kScaleTiles][rr >> 4] < 0.f) kc[c] = vc[c] = make_uint2(0, 0);
           }
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&code_empty[slot]);
         if (n >= ST && !__all_sync(0xffffffffu, await(&kv_empty[st], n / ST - 1, &stop))) break;
-        uint8_t* kst = smem + S::OFF_ST + st * 2 * S::KB + atom * S::KA;
+        uint8_t* kst = smem + S::OFF_ST + st * 2 * S::KB;
 #pragma unroll
         for (int c = 0; c < N; ++c) {
-          const uint32_t lo = sw128(row0 + c * RS, e0), hi = sw128(row0 + c * RS, e0 + 8);
-#pragma unroll
-          for (int m = 0; m < 2; ++m) {
-            const uint4 u = m ? vc[c] : kc[c];
-            const uint32_t w0 = W::prep(swap ? u.z : u.x), w1 = W::prep(swap ? u.w : u.y), w2 = W::prep(swap ? u.x : u.z),
-                           w3 = W::prep(swap ? u.y : u.w);
-            uint8_t* dst = kst + m * S::KB;
-            *reinterpret_cast<uint4*>(dst + (swap ? hi : lo)) = make_uint4(
-                W::template pair<false>(w0), W::template pair<true>(w0), W::template pair<false>(w1), W::template pair<true>(w1));
-            *reinterpret_cast<uint4*>(dst + (swap ? lo : hi)) = make_uint4(
-                W::template pair<false>(w2), W::template pair<true>(w2), W::template pair<false>(w3), W::template pair<true>(w3));
-          }
+          const uint32_t k0 = W::prep(kc[c].x), k1 = W::prep(kc[c].y), v0 = W::prep(vc[c].x), v1 = W::prep(vc[c].y);
+          *reinterpret_cast<uint4*>(kst + put[c]) = make_uint4(W::template raw<false>(k0), W::template raw<true>(k0),
+                                                               W::template raw<false>(k1), W::template raw<true>(k1));
+          *reinterpret_cast<uint4*>(kst + S::KB + put[c]) = make_uint4(W::template pair<false>(v0), W::template pair<true>(v0),
+                                                                       W::template pair<false>(v1), W::template pair<true>(v1));
         }
         fence_proxy_async();  // generic stores before the MMAs read them
         __syncwarp();
@@ -489,66 +502,66 @@ __global__ void __launch_bounds__(kChThreads, 1)
       }
       if (i < tiles)  // given up: copies in flight land before the memory goes away
         for (int n = n_kv + max(0, i - kCodeTiles); n < n_kv + i; ++n) (void)mbar_wait(&code_full[n % kCodeTiles], (n / kCodeTiles) & 1);
-    } else if (warp == kMmaWarp) {
-      // ---- the MMAs ------------------------------------------------------------------------------
-      const uint32_t tm = tmem;
+    } else if (warp >= kMmaWarp) {
+      // ---- the MMAs of query tile j ----------------------------------------------------------------
+      const int j = warp - kMmaWarp;
       if (elect()) {
-      const uint64_t qd = smem_desc(smem), kd = smem_desc(smem + S::OFF_ST),
-                     vd = smem_desc_mn(smem + S::OFF_ST + S::KB, S::KA, 8 * 128);
-      auto issue_s = [&](int j, int st) {  // S of query tile j over stage st (offsets in units of 16 bytes)
-        const uint64_t qj = qd + static_cast<uint64_t>(j * (S::QB >> 4)), ks = kd + static_cast<uint64_t>(st * (2 * S::KB >> 4));
-        const uint32_t d = tm + S::TM_S + kChKeys * j;
-        mma_ss<false>(d, qj, ks, S::IDESC_S);
+        const uint64_t qd = smem_desc(smem) + static_cast<uint64_t>(j * (S::QB >> 4)), kd = smem_desc(smem + S::OFF_ST),
+                       vd = smem_desc_mn(smem + S::OFF_ST + S::KB, S::KA, 8 * 128);
+        const uint32_t ts = tmem + S::TM_S + kChKeys * j, tp = tmem + S::TM_P + 32 * j, to = tmem + j * D;
+        auto issue_s = [&](int st) {  // S over stage st (offsets in units of 16 bytes)
+          const uint64_t ks = kd + static_cast<uint64_t>(st * (2 * S::KB >> 4));
+          mma_ss<false>(ts, qd, ks, S::IDESC_S);
 #pragma unroll
-        for (int e = 1; e < D / 16; ++e)
-          mma_ss<true>(d, qj + ((e >> 2) * S::QA + (e & 3) * 32 >> 4), ks + ((e >> 2) * S::KA + (e & 3) * 32 >> 4), S::IDESC_S);
-        mma_commit(&s_full[j]);
-      };
-      auto issue_o = [&](int j, int st, bool first) {
-        const uint64_t vs = vd + static_cast<uint64_t>(st * (2 * S::KB >> 4));
-#pragma unroll
-        for (int e = 0; e < kChKeys / 16; ++e)
-          mma_ts(tm + j * D, tm + S::TM_P + 32 * j + 8 * e, vs + (e * 16 * 128 >> 4), S::IDESC_O, first && e == 0 ? 0u : 1u);
-        mma_commit(&o_done[j]);
-      };
-      auto waited = [&](uint64_t* bar, int n) { return await(bar, n, &stop); };
-      int st = n_kv % ST;
-      bool ok = waited(&kv_full[st], n_kv / ST);
-      if (ok) {
-        tc_after();
-        for (int j = 0; j < nqt; ++j) issue_s(j, st);
-      }
-      for (int i = 0; i < tiles && ok; ++i) {
-        const int n = n_kv + i, next = st + 1 == ST ? 0 : st + 1;
-        if (i + 1 < tiles && !(ok = waited(&kv_full[next], (n + 1) / ST))) break;
-        for (int j = 0; j < nqt && ok; ++j) {
-          const int m = n_q[j] + i;
-          if (i + 1 < tiles) {  // the scores of tile i are in registers: S of the next tile
-            if (!(ok = waited(&s_free[j], m))) break;
+          for (int e = 1; e < D / 16; ++e)
+            mma_ss<true>(ts, qd + ((e >> 2) * S::QA + (e & 3) * 32 >> 4), ks + ((e >> 2) * S::KA + (e & 3) * 32 >> 4), S::IDESC_S);
+          mma_commit(&s_full[j]);
+        };
+        bool ok = true;
+        int st = n_kv % ST;
+        if (j < nqt) {
+          if ((ok = await(&kv_full[st], n_kv / ST, &stop))) {
             tc_after();
-            issue_s(j, next);
+            issue_s(st);
           }
-          if (!(ok = waited(&p_ready[j], m))) break;
-          tc_after();
-          issue_o(j, st, i == 0);
+          for (int i = 0; i < tiles && ok; ++i) {
+            const int n = n_kv + i, m = n_q[j] + i, next = st + 1 == ST ? 0 : st + 1;
+            if (i + 1 < tiles) {  // the scores of tile i are in registers: S of the next tile
+              if (!(ok = await2(&kv_full[next], (n + 1) / ST, &s_free[j], m, &stop))) break;
+              tc_after();
+              issue_s(next);
+            }
+            if (!(ok = await(&p_ready[j], m, &stop))) break;
+            tc_after();
+            const uint64_t vs = vd + static_cast<uint64_t>(st * (2 * S::KB >> 4));
+#pragma unroll
+            for (int e = 0; e < kChKeys / 16; ++e)
+              mma_ts(to, tp + 8 * e, vs + (e * 16 * 128 >> 4), S::IDESC_O, i == 0 && e == 0 ? 0u : 1u);
+            mma_commit(&o_done[j]);
+            mma_commit(&kv_empty[st]);
+            st = next;
+          }
+        } else {  // no such query tile: the stages are only given back
+          for (int i = 0; i < tiles && ok; ++i, st = st + 1 == ST ? 0 : st + 1)
+            if ((ok = await(&kv_full[st], (n_kv + i) / ST, &stop))) mbar_arrive(&kv_empty[st]);
         }
-        if (ok) mma_commit(&kv_empty[st]);
-        st = next;
-      }
-      if (!ok) {  // whatever is in flight ends before the memory goes away
-        mma_commit(&drained);
-        (void)mbar_wait(&drained, 0);
-      }
+        if (!ok) {  // whatever is in flight ends before the memory goes away
+          mma_commit(&drained[j]);
+          (void)mbar_wait(&drained[j], 0);
+        }
       }
     } else if (soft) {
       // ---- softmax: one row per thread -------------------------------------------------------------
       const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
       const int qpos = it.basek + tok;  // the row sees keys 0 .. qpos
-      const float f_row = s_row[qi * kChRows + row];
+      const int up = s_up[qi * kChRows + row] - 113, ua = up / 2;
+      // from accumulators to base-2 scores
+      const float f_row = fabsf(a.scale) * kLog2e * __uint_as_float((127 - ua) << 23) * __uint_as_float((127 - up + ua) << 23);
+      const float q_off = W::kOffset != 0.f ? s_off[qi * kChRows + row] : 0.f;
       bool ok = true;
       for (int i = 0; i < tiles; ++i) {
         const int n = n_kv + i, m = n_q[qi] + i, st = n % ST;
-        ok = await(&kv_full[st], n / ST, &stop) && await(&s_full[qi], m, &stop);  // the tile's scales; its scores
+        ok = await2(&kv_full[st], n / ST, &s_full[qi], m, &stop);  // the tile's scales; its scores
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
         const int sl = n % kScaleTiles;
         const float4 kq = *reinterpret_cast<const float4*>(sc_k[sl]), uq = *reinterpret_cast<const float4*>(sc_up[sl]),
@@ -567,9 +580,10 @@ __global__ void __launch_bounds__(kChThreads, 1)
         for (int h = 0; h < 4; ++h) c1[h] = f_row * kk[h];
         const int last = row_ok ? qpos - (ta + i) * kChKeys : -1;  // last visible column
         const bool gap = fminf(fminf(kk[0], kk[1]), fminf(kk[2], kk[3])) < 0.f;
-        if (__any_sync(0xffffffffu, last < kChKeys - 1) || gap) {
+        const bool masked = __any_sync(0xffffffffu, last < kChKeys - 1) || gap;
+        if (masked) {
 #pragma unroll
-          for (int e = 0; e < kChKeys; ++e) s[e] = e <= last && kk[e >> 4] >= 0.f ? s[e] * c1[e >> 4] : -INFINITY;
+          for (int e = 0; e < kChKeys; ++e) s[e] = e <= last && kk[e >> 4] >= 0.f ? (s[e] - q_off) * c1[e >> 4] : -INFINITY;
 #pragma unroll
           for (int h = 0; h < 4; ++h) c1[h] = 1.f;
         }
@@ -579,7 +593,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
           float v = max3(s[16 * h], s[16 * h + 1], s[16 * h + 2]);
 #pragma unroll
           for (int e = 3; e < 15; e += 2) v = max3(v, s[16 * h + e], s[16 * h + e + 1]);
-          mt = fmaxf(mt, fmaxf(v, s[16 * h + 15]) * c1[h]);  // factors are >= 0
+          mt = fmaxf(mt, (fmaxf(v, s[16 * h + 15]) - (masked ? 0.f : q_off)) * c1[h]);  // factors are >= 0
         }
         const bool move = mt > -INFINITY && (m_ref == -INFINITY || mt > m_ref + kLazy);
         const float alpha = move ? (m_ref == -INFINITY ? 0.f : exp2_approx(m_ref - mt)) : 1.f;
@@ -591,7 +605,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
         uint32_t pk[kChKeys / 2];
 #pragma unroll
         for (int h = 0; h < 4; ++h) {
-          const float c2 = uu[h] - zm;
+          const float c2 = uu[h] - zm - (masked ? 0.f : q_off * c1[h]);
           const f32x2 c11 = pk2(c1[h], c1[h]), c22 = pk2(c2, c2);
           f32x2 sums = pk2(0.f, 0.f);
 #pragma unroll
