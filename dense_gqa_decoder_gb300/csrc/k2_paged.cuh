@@ -208,16 +208,26 @@ __device__ __forceinline__ void store4(T* p, float a, float b, float c, float d)
   *reinterpret_cast<uint2*>(p) = *reinterpret_cast<const uint2*>(v);
 }
 
-struct Share {  // equal shares of `total` units of work: the first unit of CTA c of n, and the CTA of unit x
-  __device__ __forceinline__ static long long first(long long total, int n, int c) { return total * c / n; }
-  __device__ __forceinline__ static int cta_of(long long total, int n, long long x) {
-    int c = static_cast<int>(x * n / total);
-    while (c + 1 < n && first(total, n, c + 1) <= x) ++c;
-    while (c > 0 && first(total, n, c) > x) --c;
-    return c;
+// a / b for a >= 0, b > 0: a division of 32 bits where that holds both
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
+}
+// Equal shares of `total` units of work for n CTAs, the first `more` of them one longer: the first unit of CTA c, and
+// the CTA of unit x.
+struct Share {
+  long long each;
+  int more;
+  __device__ __forceinline__ Share(long long total, int n) {
+    each = quotient(total, n);
+    more = static_cast<int>(total - each * n);
+  }
+  __device__ __forceinline__ long long first(int c) const { return each * c + min(c, more); }
+  __device__ __forceinline__ int cta_of(long long x) const {
+    const long long longer = (each + 1) * more;
+    return static_cast<int>(x < longer ? quotient(x, each + 1) : more + quotient(x - longer, each));
   }
 };
-
 
 constexpr int kAttnMaxCtas = 1024;
 

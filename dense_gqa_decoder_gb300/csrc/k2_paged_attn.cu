@@ -138,7 +138,8 @@ __global__ void __launch_bounds__(kDecThreads, Dec<D, NT>::kCtas)
   if (total == 0) return;
   const int ctas = static_cast<int>(min(static_cast<long long>(gridDim.x), (total + kDecShare - 1) / kDecShare));
   if (blockIdx.x >= ctas) return;
-  const long long x0 = Share::first(total, ctas, blockIdx.x), x1 = Share::first(total, ctas, blockIdx.x + 1);
+  const Share share(total, ctas);
+  const long long x0 = share.first(blockIdx.x), x1 = share.first(blockIdx.x + 1);
   if (before <= x0 && x0 < before + own) {  // one thread: its requests hold the share's first unit
     long long at = before;
     for (int i = 0; i < per; ++i) {
@@ -181,7 +182,7 @@ __global__ void __launch_bounds__(kDecThreads, Dec<D, NT>::kCtas)
       q = request(a, p.block_log2, ++r);
       nt = tiles_of(q);
     }
-    const int g = static_cast<int>((x - base) / (nt + kDecStart));
+    const int g = static_cast<int>(quotient(x - base, nt + kDecStart));
     const long long item = base + static_cast<long long>(g) * (nt + kDecStart) + kDecStart;  // unit of (r, g)'s first tile
     const int ta = static_cast<int>(max(x0 - item, 0ll)), tb = static_cast<int>(min(static_cast<long long>(nt), x1 - item));
     x = item + nt;
@@ -496,7 +497,7 @@ __global__ void __launch_bounds__(kDecThreads, Dec<D, NT>::kCtas)
     }
     if (!whole) {
       // the item's parts lie with CTAs c0 .. c1; the last to arrive joins them in that order
-      const int c0 = Share::cta_of(total, ctas, item), c1 = Share::cta_of(total, ctas, item + nt - 1);
+      const int c0 = share.cta_of(item), c1 = share.cta_of(item + nt - 1);
       __threadfence();
       __syncthreads();
       if (tid == 0) {

@@ -188,7 +188,7 @@ struct ChunkWork {
       c = cost(i.q);
     }
     i.r = r;
-    i.g = static_cast<int>((x - base) / c.head);
+    i.g = static_cast<int>(quotient(x - base, c.head));
     const long long rem = x - base - i.g * c.head;
     int b = 0;
     for (int hi = c.nb; hi - b > 1;) {
@@ -310,7 +310,8 @@ __global__ void __launch_bounds__(kChThreads, 1)
     pdl_wait();  // this kernel started beside the one for few rows: it ends after it
     return;
   }
-  const long long x0 = Share::first(total, ctas, blockIdx.x), x1 = Share::first(total, ctas, blockIdx.x + 1);
+  const Share share(total, ctas);
+  const long long x0 = share.first(blockIdx.x), x1 = share.first(blockIdx.x + 1);
   scan.find(work, x0, &s_req, &s_base);
   if (warp == 0) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_slot)), "r"(S::TM_COLS)
@@ -578,7 +579,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
         for (int e = 0; e < kChKeys; ++e) s[e] = __uint_as_float(raw[e]);
 #pragma unroll
         for (int h = 0; h < 4; ++h) c1[h] = f_row * kk[h];
-        const int last = row_ok ? qpos - (ta + i) * kChKeys : -1;  // last visible column
+        const int last = row_ok ? qpos - (ta + i) * kChKeys : kChKeys;  // last visible column (padding rows: of no account)
         const bool gap = fminf(fminf(kk[0], kk[1]), fminf(kk[2], kk[3])) < 0.f;
         const bool masked = __any_sync(0xffffffffu, last < kChKeys - 1) || gap;
         if (masked) {
@@ -708,14 +709,15 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedPoo
   ChunkWork::Item it;
   int c1 = 0;
   if (job) {
-    const long long last = Share::first(scan.total, ctas, c0 + 1) - 1;  // of the share
+    const Share share(scan.total, ctas);
+    const long long last = share.first(c0 + 1) - 1;  // of this CTA's share
     scan.find(work, last, &s_req, &s_base);
     __syncthreads();
     int r = s_req;
     long long base = s_base;
     it = work.item(last, r, base);
-    c1 = Share::cta_of(scan.total, ctas, it.at + static_cast<long long>(kChKeys) * (it.nkt - 1));
-    job = Share::cta_of(scan.total, ctas, it.at) == c0 && c1 > c0;
+    c1 = share.cta_of(it.at + static_cast<long long>(kChKeys) * (it.nkt - 1));
+    job = share.cta_of(it.at) == c0 && c1 > c0;
   }
   pdl_wait();  // the parts
   if (!job) return;
