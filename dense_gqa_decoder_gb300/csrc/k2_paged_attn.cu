@@ -54,7 +54,7 @@ constexpr int kDecWarps = 4, kDecThreads = 32 * kDecWarps;
 constexpr int kDecKeys = 32;   // of a tile: two halves of 16, which may lie in two blocks
 constexpr int kDecStart = 4;   // an item's start and end in tiles
 constexpr int kDecShare = 8;   // smallest share: fewer CTAs for small steps, and fewer parts to join
-constexpr int kDecMaxRows = 32;
+constexpr int kDecMaxRows = 16;
 
 template <int D, int NT>
 struct Dec {
@@ -66,7 +66,7 @@ struct Dec {
   static constexpr int kLd = D + 4;                              // floats of a row of the joined output
   static constexpr int kMerge = kDecWarps * kRows * (kLd + 2) * 4;
   static constexpr int kSmem = kRing * kDecWarps > kMerge ? kRing * kDecWarps : kMerge;
-  static constexpr int kCtas = NT <= 2 ? 3 : 2;                  // per SM
+  static constexpr int kCtas = 3;                                // per SM
 };
 constexpr int kDecSlotFloats = kDecMaxRows * (128 + 2);  // one part: rows x (output, maximum, sum)
 
@@ -562,17 +562,16 @@ cudaError_t launch_decode(const PagedPool& p, const PagedAttnArgs& a, int small_
   return cudaGetLastError();
 }
 
-// all requests with few rows: the narrowest kernel that holds them; else only the single tokens (and what fits
+// all requests with few rows: the narrower kernel that holds them; else only the single tokens (and what fits
 // beside them) are taken apart from the prompt chunks
 int small_rows_of(const PagedAttnArgs& a, int rep) {
   const long long most = static_cast<long long>(a.max_q) * rep;
-  return most <= 8 ? 8 : most <= 16 ? 16 : most <= kDecMaxRows ? kDecMaxRows : rep <= 8 ? 8 : 16;
+  return most <= 8 ? 8 : most <= kDecMaxRows ? kDecMaxRows : rep <= 8 ? 8 : 16;
 }
 template <typename T, typename C, int D>
 cudaError_t launch(const PagedPool& p, const PagedAttnArgs& a, int small_rows, const AttnWorkspace& w, int sms, int dev, cudaStream_t s) {
-  return small_rows == 8    ? launch_decode<T, C, D, 1>(p, a, small_rows, w, sms, dev, s)
-         : small_rows == 16 ? launch_decode<T, C, D, 2>(p, a, small_rows, w, sms, dev, s)
-                            : launch_decode<T, C, D, 4>(p, a, small_rows, w, sms, dev, s);
+  return small_rows == 8 ? launch_decode<T, C, D, 1>(p, a, small_rows, w, sms, dev, s)
+                         : launch_decode<T, C, D, 2>(p, a, small_rows, w, sms, dev, s);
 }
 template <typename T, typename C>
 cudaError_t launch(const PagedPool& p, int head_dim, const PagedAttnArgs& a, int small_rows, const AttnWorkspace& w, int sms, int dev, cudaStream_t s) {
