@@ -2,6 +2,7 @@
 // the next step (k2_paged_plan) and the quantizing append (k2_paged_append).
 // What they compute is stated in include/k2.h.
 #include <algorithm>
+#include <type_traits>
 
 #include "k2_paged.cuh"
 
@@ -214,49 +215,54 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a, in
 // ---- quantizing append -------------------------------------------------------------------------
 //
 // A run is the maximal stretch of consecutive tokens with consecutive slots of
-// one block.  Each token has a CTA; the first token of a run takes the run,
-// one warp per (head, K or V): a lane holds head_dim / 32 neighbouring
-// elements of a row.  The others leave at once.  So the scale of a block and
-// head has one writer, and no atomics decide anything.
-template <typename T>
-struct Row4;  // N neighbouring elements of a row as fp32
+// one block.  A unit of work is a run's K or V rows of one head, so the scale of a
+// block and head has one writer and no atomics decide anything.  A unit is taken
+// by block_tokens / 16 warps, each with up to 16 rows in registers: the rows are
+// read once, their maxima joined, then rounded and stored.  Such a group of warps
+// looks through a window of tokens for runs that begin there; the window is wide
+// where tokens are many (most of a prompt's tokens begin no run), one token where
+// they are few (every token of a decode step begins one).
+//
+// Bound by the rows' bytes (4 in and 2 out per element pair) for prompts and by
+// latency for decode steps.  The quotient x / s decides a code only through its
+// rounding, so it is taken as x * (1 / s), at most 2^-22 |x / s| off, and divided
+// only where that could change the code.
+template <typename T, int E>
+struct RowBits;  // E neighbouring elements of a row, as loaded
 template <>
-struct Row4<float> {
-  template <int N>
-  __device__ __forceinline__ static void load(const float* p, float* f) {
+struct RowBits<float, 4> { using type = float4; };
+template <>
+struct RowBits<float, 2> { using type = float2; };
+template <>
+struct RowBits<__nv_bfloat16, 4> { using type = uint2; };
+template <>
+struct RowBits<__nv_bfloat16, 2> { using type = uint32_t; };
+template <>
+struct RowBits<__half, 4> { using type = uint2; };
+template <>
+struct RowBits<__half, 2> { using type = uint32_t; };
+
+template <typename T, int E>
+__device__ __forceinline__ void to_floats(const typename RowBits<T, E>::type& v, float* f) {
+  if constexpr (sizeof(T) == 4) {
+    const float* p = reinterpret_cast<const float*>(&v);
 #pragma unroll
-    for (int i = 0; i < N; i += 2) {
-      const float2 v = __ldg(reinterpret_cast<const float2*>(p + i));
-      f[i] = v.x;
-      f[i + 1] = v.y;
+    for (int i = 0; i < E; ++i) f[i] = p[i];
+  } else {
+    const uint32_t* p = reinterpret_cast<const uint32_t*>(&v);
+#pragma unroll
+    for (int i = 0; i < E; i += 2) {
+      if constexpr (std::is_same<T, __half>::value) {
+        const float2 t = __half22float2(*reinterpret_cast<const __half2*>(p + i / 2));
+        f[i] = t.x;
+        f[i + 1] = t.y;
+      } else {
+        f[i] = bf16lo(p[i / 2]);
+        f[i + 1] = bf16hi(p[i / 2]);
+      }
     }
   }
-};
-template <>
-struct Row4<__nv_bfloat16> {
-  template <int N>
-  __device__ __forceinline__ static void load(const __nv_bfloat16* p, float* f) {
-#pragma unroll
-    for (int i = 0; i < N; i += 2) {
-      const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(p + i));
-      f[i] = bf16lo(w);
-      f[i + 1] = bf16hi(w);
-    }
-  }
-};
-template <>
-struct Row4<__half> {
-  template <int N>
-  __device__ __forceinline__ static void load(const __half* p, float* f) {
-#pragma unroll
-    for (int i = 0; i < N; i += 2) {
-      const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(p + i));
-      const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&w));
-      f[i] = v.x;
-      f[i + 1] = v.y;
-    }
-  }
-};
+}
 
 template <int N>
 struct Codes;  // N neighbouring codes
@@ -265,7 +271,45 @@ struct Codes<4> { using type = uint32_t; };
 template <>
 struct Codes<2> { using type = uint16_t; };
 
-constexpr int kAppendHeads = 8;  // KV heads of one CTA (two warps each)
+// Codes of E elements under scale s > 0, inv = 1 / s (0: s is too small for that); the whole warp takes part.
+template <int E, typename C>
+__device__ __forceinline__ uint32_t fast_codes(const float* f, float s, float inv) {
+  uint32_t u = 0;
+  bool unsure = inv == 0.f;
+  float y[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) y[e] = __fmul_rn(f[e], inv);
+  if constexpr (std::is_same<C, CodeI8>::value) {
+    // |y| <= 127 (1 + 2^-22): y is within 2^-15 of the quotient, so only one that near a midpoint can round the other way
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const float r = rintf(y[e]);
+      unsure |= fabsf(fabsf(y[e] - r) - 0.5f) < 1e-4f;
+      u |= (y[e] == y[e] ? static_cast<uint32_t>(static_cast<int>(fminf(fmaxf(r, -127.f), 127.f))) & 0xFFu : 0u) << (8 * e);
+    }
+  } else {
+    // the quotient lies between y (1 - 2^-20) and y (1 + 2^-20): the same code for both is its code
+#pragma unroll
+    for (int e = 0; e < E; e += 2) {
+      const float a0 = y[e] * (1.f - 9.5367432e-7f), a1 = y[e + 1] * (1.f - 9.5367432e-7f);
+      const float b0 = y[e] * (1.f + 9.5367432e-7f), b1 = y[e + 1] * (1.f + 9.5367432e-7f);
+      uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a0, a1), __NV_SATFINITE, __NV_E4M3);
+      const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(b0, b1), __NV_SATFINITE, __NV_E4M3);
+      unsure |= lo != hi;
+      if (!(y[e] == y[e])) lo &= 0xFF00u;
+      if (!(y[e + 1] == y[e + 1])) lo &= 0x00FFu;
+      u |= lo << (8 * e);
+    }
+  }
+  if (__any_sync(0xffffffffu, unsure)) {
+    u = 0;
+#pragma unroll
+    for (int e = 0; e < E; ++e) u |= quantize<C>(f[e], s) << (8 * e);
+  }
+  return u;
+}
+
+constexpr int kAppendThreads = 256, kRunRows = 16;  // rows of a run that one warp takes
 
 struct AppendArgs {
   const void* k;
@@ -273,81 +317,121 @@ struct AppendArgs {
   long long k_stride, v_stride;
   const int* slots;
   int tokens;
+  int window;  // tokens that a group looks through (1 .. 32)
 };
 
 template <typename T, typename C, int D>
-__global__ void append_kernel(const PagedPool p, const AppendArgs a) {
+__global__ void __launch_bounds__(kAppendThreads) append_kernel(const PagedPool p, const AppendArgs a) {
   constexpr int E = D / 32;
+  using Bits = typename RowBits<T, E>::type;
   using Word = typename Codes<E>::type;
-  const int t = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int g = blockIdx.y * kAppendHeads + (warp >> 1);
-  const bool is_v = warp & 1;
+  __shared__ float s_top[kAppendThreads / 32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int B = 1 << p.block_log2, bmask = B - 1;
-  const int slot = a.slots[t];
-  if (slot < 0) return;
-  if (slot >= (static_cast<long long>(p.n_blocks) << p.block_log2)) {
-    if (threadIdx.x == 0 && blockIdx.y == 0) raise_flag(p.flags, K2_PAGED_BAD_SLOT);
-    return;
-  }
-  if (g >= p.n_kv) return;
-  const int o = slot & bmask;
-  if (o > 0 && t > 0 && a.slots[t - 1] == slot - 1) return;  // inside a run
-  int n = 1;
-  for (bool more = true; more;) {
-    const int i = n + lane;
-    const bool same = o + i < B && t + i < a.tokens && a.slots[t + i] == slot + i;
-    const unsigned m = __ballot_sync(0xffffffffu, same);
-    const int run = m == 0xffffffffu ? 32 : __ffs(~m) - 1;
-    n += run;
-    more = run == 32;
-  }
-  const size_t at = static_cast<size_t>(slot >> p.block_log2) * p.n_kv + g;
-  const T* src = static_cast<const T*>(is_v ? a.v : a.k) + t * (is_v ? a.v_stride : a.k_stride) + g * D + lane * E;
+  const int W = B / kRunRows, group = warp / W, wi = warp & (W - 1);  // warps of a unit; this one's unit and place in it
+  const int unit = blockIdx.y * (kAppendThreads / 32 / W) + group;
+  if (unit >= 2 * p.n_kv) return;  // (whole groups)
+  auto sync_group = [&] {
+    if (W > 1) asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(32 * W) : "memory");
+    else __syncwarp();
+  };
+  const int g = unit >> 1;
+  const bool is_v = unit & 1;
+  const long long limit = static_cast<long long>(p.n_blocks) << p.block_log2;
+  const int t0 = blockIdx.x * a.window;
+  // the runs that begin in the window
+  const int tl = t0 + lane;
+  const bool inside = lane < a.window && tl < a.tokens;
+  const int mine = inside ? __ldg(a.slots + tl) : -1, prior = inside && tl > 0 ? __ldg(a.slots + tl - 1) : -1;
+  if (mine >= limit && unit == 0) raise_flag(p.flags, K2_PAGED_BAD_SLOT);
+  unsigned starts = __ballot_sync(0xffffffffu, mine >= 0 && mine < limit && !((mine & bmask) != 0 && prior == mine - 1));
   const long long stride = is_v ? a.v_stride : a.k_stride;
-  uint8_t* codes = (is_v ? p.v : p.k) + (at << p.block_log2) * D + lane * E;
-  float* scale = (is_v ? p.vs : p.ks) + at;
-  float top = 0.f;
-  for (int i = 0; i < n; ++i) {
-    float f[E];
-    Row4<T>::template load<E>(src + i * stride, f);
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const float m = fabsf(f[e]);
-      if (m <= 3.402823466e38f) top = fmaxf(top, m);  // finite
+  while (starts) {
+    const int first = __ffs(starts) - 1;
+    starts &= starts - 1;
+    const int t = t0 + first, slot = __shfl_sync(0xffffffffu, mine, first), o = slot & bmask;
+    int n = 1;
+    for (bool more = true; more;) {
+      const int i = n + lane;
+      const bool same = o + i < B && t + i < a.tokens && __ldg(a.slots + t + i) == slot + i;
+      const unsigned m = __ballot_sync(0xffffffffu, same);
+      const int run = m == 0xffffffffu ? 32 : __ffs(~m) - 1;
+      n += run;
+      more = run == 32;
     }
-  }
-  top = warp_max(top);
-  const float was = o > 0 ? *scale : 0.f;
-  const float now = fmaxf(was, __fdiv_rn(top, C::kMax));
-  if (o > 0 && now > was) {
-    const float ratio = __fdiv_rn(was, now);
-    for (int i = 0; i < o; ++i) {
-      Word* w = reinterpret_cast<Word*>(codes + static_cast<size_t>(i) * D);
-      const uint32_t c = *w;
-      uint32_t u = 0;
+    const size_t at = static_cast<size_t>(slot >> p.block_log2) * p.n_kv + g;
+    const int i0 = wi * kRunRows;
+    const T* src = static_cast<const T*>(is_v ? a.v : a.k) + (t + i0) * stride + g * D + lane * E;
+    uint8_t* codes = (is_v ? p.v : p.k) + (at << p.block_log2) * D + lane * E;
+    float* scale = (is_v ? p.vs : p.ks) + at;
+    const float was = o > 0 ? *scale : 0.f;
+    Bits x[kRunRows];
 #pragma unroll
-      for (int e = 0; e < E; ++e) u |= quantize<C>(__fmul_rn(C::value((c >> (8 * e)) & 0xFFu), ratio), 1.f) << (8 * e);
-      *w = static_cast<Word>(u);
+    for (int i = 0; i < kRunRows; ++i)
+      if (i0 + i < n) x[i] = __ldg(reinterpret_cast<const Bits*>(src + i * stride));
+    float top = 0.f;
+#pragma unroll
+    for (int i = 0; i < kRunRows; ++i) {
+      if (i0 + i >= n) break;
+      float f[E];
+      to_floats<T, E>(x[i], f);
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const float m = fabsf(f[e]);
+        if (m <= 3.402823466e38f) top = fmaxf(top, m);  // finite
+      }
     }
-  }
-  __syncwarp();
-  if (lane == 0) *scale = now;
-  for (int i = 0; i < n; ++i) {
-    float f[E];
-    Row4<T>::template load<E>(src + i * stride, f);
-    uint32_t u = 0;
+    top = warp_max_redux(top);
+    if (W > 1) {
+      if (lane == 0) s_top[warp] = top;
+      sync_group();
+      for (int w = 0; w < W; ++w) top = fmaxf(top, s_top[group * W + w]);
+    }
+    const float now = fmaxf(was, __fdiv_rn(top, C::kMax));
+    if (o > 0 && now > was) {  // the rows before, rounded to the larger scale
+      const float ratio = __fdiv_rn(was, now);
+      for (int i = wi; i < o; i += 8 * W) {
+        Word c[8];
 #pragma unroll
-    for (int e = 0; e < E; ++e) u |= quantize<C>(f[e], now) << (8 * e);
-    *reinterpret_cast<Word*>(codes + static_cast<size_t>(o + i) * D) = static_cast<Word>(u);
+        for (int j = 0; j < 8; ++j)
+          if (i + j * W < o) c[j] = *reinterpret_cast<const Word*>(codes + static_cast<size_t>(i + j * W) * D);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          if (i + j * W >= o) break;
+          uint32_t u = 0;
+#pragma unroll
+          for (int e = 0; e < E; ++e) {
+            const float y = __fmul_rn(C::value((c[j] >> (8 * e)) & 0xFFu), ratio);
+            u |= (y == y ? C::round(y) : 0u) << (8 * e);
+          }
+          *reinterpret_cast<Word*>(codes + static_cast<size_t>(i + j * W) * D) = static_cast<Word>(u);
+        }
+      }
+    }
+    const float inv = now > 1e-30f ? __frcp_rn(now) : 0.f;
+#pragma unroll
+    for (int i = 0; i < kRunRows; ++i) {
+      if (i0 + i >= n) break;
+      float f[E];
+      to_floats<T, E>(x[i], f);
+      const uint32_t u = now > 0.f ? fast_codes<E, C>(f, now, inv) : 0u;
+      *reinterpret_cast<Word*>(codes + static_cast<size_t>(o + i0 + i) * D) = static_cast<Word>(u);
+    }
+    sync_group();  // every warp of the unit has read the old scale, and s_top
+    if (wi == 0 && lane == 0) *scale = now;
   }
 }
 
 template <typename T, typename C>
-cudaError_t launch_append(const PagedPool& p, int head_dim, const AppendArgs& a, cudaStream_t s) {
-  const dim3 grid(a.tokens, (p.n_kv + kAppendHeads - 1) / kAppendHeads);
-  const int threads = 64 * std::min(p.n_kv, kAppendHeads);
-  if (head_dim == 128) append_kernel<T, C, 128><<<grid, threads, 0, s>>>(p, a);
-  else append_kernel<T, C, 64><<<grid, threads, 0, s>>>(p, a);
+cudaError_t launch_append(const PagedPool& p, int head_dim, AppendArgs a, cudaStream_t s) {
+  const int warps = (1 << p.block_log2) / kRunRows, units = 2 * p.n_kv, per_cta = kAppendThreads / 32 / warps;
+  // windows so wide that some 32 warps per SM look through them
+  const long long all = static_cast<long long>(a.tokens) * units * warps / (152 * 32);
+  a.window = 1;
+  while (a.window < 32 && a.window * 2 <= all) a.window *= 2;
+  const dim3 grid((a.tokens + a.window - 1) / a.window, (units + per_cta - 1) / per_cta);
+  if (head_dim == 128) append_kernel<T, C, 128><<<grid, kAppendThreads, 0, s>>>(p, a);
+  else append_kernel<T, C, 64><<<grid, kAppendThreads, 0, s>>>(p, a);
   return cudaGetLastError();
 }
 template <typename T>
@@ -433,7 +517,7 @@ k2_status k2_paged_append(const k2_paged_kv* kv, const void* d_k, const void* d_
     return K2_ERR_ARG;
   }
   const PagedPool p(*kv);
-  const AppendArgs a = {d_k, d_v, k_stride, v_stride, d_slots, tokens};
+  const AppendArgs a = {d_k, d_v, k_stride, v_stride, d_slots, tokens, 1};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const cudaError_t e = dtype == K2_F32    ? launch_append<float>(p, *kv, a, s)
                         : dtype == K2_BF16 ? launch_append<__nv_bfloat16>(p, *kv, a, s)

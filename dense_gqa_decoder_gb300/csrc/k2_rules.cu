@@ -2,12 +2,13 @@
 // already holds, biases, grammar masks, in one pass over the logits.  The
 // rules and their order are stated in include/k2.h.
 //
-// A CTA takes a slice of one row's vocabulary.  The row's token history is
-// read once per slice and counted into shared memory (one word per id: bit 31
-// says "seen", the rest counts the answer's occurrences), so the counts are
-// exact whatever the order of the atomics; the biases of the slice are added
-// by one warp in list order, so that an id listed twice gives the same sum
-// every time.  Then one pass reads the logits and writes the result.
+// Bound by the logits' bytes, read and written once: a thread keeps 16 of them in
+// registers while the row's token history is counted into shared memory (one word
+// per id of the CTA's slice: bit 31 says "seen", bit 30 "has a bias", the rest
+// counts the answer's occurrences), so the counts are exact whatever the order of
+// the atomics.  Biases are few: those of the slice are gathered in list order, and
+// the thread that holds such an id adds its entries in that order, so that an id
+// listed twice gives the same sum every time.
 #include <math.h>
 
 #include <algorithm>
@@ -20,64 +21,181 @@ namespace k2 {
 
 namespace {
 
-constexpr int kRuleThreads = 512;
-constexpr int kRuleSlice = 8192;  // ids of one CTA: 64 KB of shared memory
-constexpr unsigned kSeen = 0x80000000u;
+constexpr int kPerThread = 16;     // logits of a thread
+constexpr int kBiasList = 512;     // biases of a slice that are handled at a time
+constexpr unsigned kSeen = 0x80000000u, kBiased = 0x40000000u, kCount = 0x3FFFFFFFu;
 
-__global__ void __launch_bounds__(kRuleThreads) rules_kernel(const k2_logit_rules u, const float* in, long long ld,
-                                                             float* out, long long ld_out, int vocab) {
-  extern __shared__ unsigned smem[];
-  unsigned* cnt = smem;
-  float* val = reinterpret_cast<float*>(smem + kRuleSlice);
-  const int r = blockIdx.y, tid = threadIdx.x;
-  const int v0 = blockIdx.x * kRuleSlice, n = min(kRuleSlice, vocab - v0);
+// VEC: every row of logits and output is 16-byte aligned
+template <int THREADS, bool VEC>
+__global__ void __launch_bounds__(THREADS) rules_kernel(const k2_logit_rules u, const float* in, long long ld, float* out,
+                                                        long long ld_out, int vocab) {
+  constexpr int SLICE = THREADS * kPerThread;
+  __shared__ __align__(16) unsigned cnt[SLICE];
+  __shared__ int b_id[kBiasList];
+  __shared__ float b_val[kBiasList];
+  __shared__ int w_sum[THREADS / 32 + 1];
+  const int r = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int v0 = blockIdx.x * SLICE, n = min(SLICE, vocab - v0);
   const float* x = in + r * ld + v0;
   float* y = out + r * ld_out + v0;
-  for (int i = tid; i < n; i += kRuleThreads) {
-    cnt[i] = 0;
-    val[i] = x[i];
+  // element j of this thread: four neighbours at a time (VEC), else strided
+  auto place = [&](int j) { return VEC ? 4 * (tid + THREADS * (j >> 2)) + (j & 3) : tid + THREADS * j; };
+  float l[kPerThread];
+  if constexpr (VEC) {
+#pragma unroll
+    for (int j = 0; j < kPerThread; j += 4) {
+      const int at = place(j);
+      if (at + 4 <= n) {
+        const float4 f = *reinterpret_cast<const float4*>(x + at);
+        l[j] = f.x;
+        l[j + 1] = f.y;
+        l[j + 2] = f.z;
+        l[j + 3] = f.w;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) l[j + e] = at + e < n ? x[at + e] : 0.f;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < kPerThread; ++j) l[j] = place(j) < n ? x[place(j)] : 0.f;
   }
-  __syncthreads();
-  if (u.ids != nullptr) {
+  const bool counted = u.repetition != nullptr || u.presence != nullptr || u.frequency != nullptr;
+  if (counted || u.bias_offset != nullptr) {
+#pragma unroll
+    for (int j = 0; j < kPerThread; j += 4) *reinterpret_cast<uint4*>(cnt + 4 * (tid + THREADS * (j >> 2))) = make_uint4(0, 0, 0, 0);
+    __syncthreads();
+  }
+  if (counted) {
     const int* ids = u.ids + r * u.ids_stride;
     const int len = static_cast<int>(min(static_cast<long long>(u.ids_len[r]), static_cast<long long>(u.ids_stride)));
     const int prompt = u.prompt_len != nullptr ? u.prompt_len[r] : 0;
-    for (int i = tid; i < len; i += kRuleThreads) {
-      const unsigned d = static_cast<unsigned>(ids[i] - v0);
+    auto count = [&](int id, int i) {
+      const unsigned d = static_cast<unsigned>(id - v0);
       if (d < static_cast<unsigned>(n)) {
-        atomicOr(&cnt[d], kSeen);
         if (i >= prompt) atomicAdd(&cnt[d], 1u);
+        atomicOr(&cnt[d], kSeen);
       }
+    };
+    int i = 0;
+    if ((reinterpret_cast<uintptr_t>(ids) & 15) == 0) {  // four ids at a time, eight such loads on their way
+      const int4* ids4 = reinterpret_cast<const int4*>(ids);
+      const int quads = len > 0 ? len >> 2 : 0;
+      for (int q0 = tid; q0 < quads; q0 += 8 * THREADS) {
+        int4 v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (q0 + j * THREADS < quads) v[j] = __ldg(ids4 + q0 + j * THREADS);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int q = q0 + j * THREADS;
+          if (q >= quads) break;
+          count(v[j].x, 4 * q);
+          count(v[j].y, 4 * q + 1);
+          count(v[j].z, 4 * q + 2);
+          count(v[j].w, 4 * q + 3);
+        }
+      }
+      i = 4 * quads;
     }
+    for (i += tid; i < len; i += THREADS) count(__ldg(ids + i), i);
     __syncthreads();
     const float rep = u.repetition != nullptr ? u.repetition[r] : 1.f;
     const float freq = u.frequency != nullptr ? u.frequency[r] : 0.f, pres = u.presence != nullptr ? u.presence[r] : 0.f;
-    for (int i = tid; i < n; i += kRuleThreads) {
-      const unsigned c = cnt[i];
+#pragma unroll
+    for (int j = 0; j < kPerThread; ++j) {
+      const unsigned c = cnt[place(j)];
       if (c == 0) continue;
-      float l = val[i];
-      if (u.repetition != nullptr) l = l > 0.f ? __fdiv_rn(l, rep) : __fmul_rn(l, rep);
-      if (c != kSeen) l = __fsub_rn(__fsub_rn(l, __fmul_rn(freq, static_cast<float>(c & ~kSeen))), pres);
-      val[i] = l;
+      if (u.repetition != nullptr) l[j] = l[j] > 0.f ? __fdiv_rn(l[j], rep) : __fmul_rn(l[j], rep);
+      if (c & kCount) l[j] = __fsub_rn(__fsub_rn(l[j], __fmul_rn(freq, static_cast<float>(c & kCount))), pres);
     }
-    __syncthreads();
   }
   if (u.bias_offset != nullptr) {
-    if (tid == 0) {
-      for (int j = max(u.bias_offset[r], 0); j < min(u.bias_offset[r + 1], u.n_bias); ++j) {
-        const unsigned d = static_cast<unsigned>(u.bias_ids[j] - v0);
-        if (d < static_cast<unsigned>(n)) val[d] += u.bias[j];
+    const int j1 = min(u.bias_offset[r + 1], u.n_bias);
+    int listed = 0;  // of the slice so far, in b_id / b_val
+    auto apply = [&] {  // adds the listed biases, in order
+      __syncthreads();
+      for (int i = tid; i < listed; i += THREADS) atomicOr(&cnt[b_id[i]], kBiased);
+      __syncthreads();
+#pragma unroll
+      for (int j = 0; j < kPerThread; ++j) {
+        const int at = place(j);
+        if (!(cnt[at] & kBiased)) continue;
+        for (int i = 0; i < listed; ++i)
+          if (b_id[i] == at) l[j] = __fadd_rn(l[j], b_val[i]);
+        cnt[at] &= ~kBiased;
       }
+      __syncthreads();
+    };
+    for (int j0 = max(u.bias_offset[r], 0); j0 < j1; j0 += THREADS) {
+      const int j = j0 + tid;
+      const unsigned d = j < j1 ? static_cast<unsigned>(__ldg(u.bias_ids + j) - v0) : ~0u;
+      const bool take = d < static_cast<unsigned>(n);
+      const unsigned m = __ballot_sync(0xffffffffu, take);
+      if (lane == 0) w_sum[warp] = __popc(m);
+      __syncthreads();
+      int before = 0, all = 0;
+#pragma unroll
+      for (int w = 0; w < THREADS / 32; ++w) {
+        if (w < warp) before += w_sum[w];
+        all += w_sum[w];
+      }
+      if (listed + all > kBiasList) {  // (all <= THREADS <= kBiasList)
+        apply();
+        listed = 0;
+      }
+      if (take) {
+        const int at = listed + before + __popc(m & ((1u << lane) - 1));
+        b_id[at] = static_cast<int>(d);
+        b_val[at] = __ldg(u.bias + j);
+      }
+      listed += all;
+      __syncthreads();  // w_sum
     }
-    __syncthreads();
+    if (listed > 0) apply();
   }
   const int mr = u.mask == nullptr ? -1 : u.mask_row != nullptr ? u.mask_row[r] : r;
   const bool masked = mr >= 0 && mr < u.n_masks;
   const unsigned* words = masked ? u.mask + mr * u.mask_stride : nullptr;
-  for (int i = tid; i < n; i += kRuleThreads) {
-    const int id = v0 + i;
-    y[i] = masked && !((words[id >> 5] >> (id & 31)) & 1u) ? -INFINITY : val[i];
+  if constexpr (VEC) {
+#pragma unroll
+    for (int j = 0; j < kPerThread; j += 4) {
+      const int at = place(j);
+      if (at >= n) break;
+      if (masked) {  // four neighbours lie in one word
+        const unsigned bits = __ldg(words + ((v0 + at) >> 5)) >> ((v0 + at) & 31);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (!((bits >> e) & 1u)) l[j + e] = -INFINITY;
+      }
+      if (at + 4 <= n) {
+        *reinterpret_cast<float4*>(y + at) = make_float4(l[j], l[j + 1], l[j + 2], l[j + 3]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (at + e < n) y[at + e] = l[j + e];
+      }
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < kPerThread; ++j) {
+      const int at = place(j);
+      if (at >= n) break;
+      if (masked && !((__ldg(words + ((v0 + at) >> 5)) >> ((v0 + at) & 31)) & 1u)) l[j] = -INFINITY;
+      y[at] = l[j];
+    }
   }
+}
+
+template <int THREADS>
+cudaError_t launch_rules(const k2_logit_rules& u, const float* in, long long ld, float* out, long long ld_out, int rows, int vocab,
+                         cudaStream_t s) {
+  const bool vec = ((reinterpret_cast<uintptr_t>(in) | reinterpret_cast<uintptr_t>(out)) & 15) == 0 &&
+                   (rows == 1 || ((ld | ld_out) & 3) == 0);
+  const dim3 grid((vocab + THREADS * kPerThread - 1) / (THREADS * kPerThread), rows);
+  if (vec) rules_kernel<THREADS, true><<<grid, THREADS, 0, s>>>(u, in, ld, out, ld_out, vocab);
+  else rules_kernel<THREADS, false><<<grid, THREADS, 0, s>>>(u, in, ld, out, ld_out, vocab);
+  return cudaGetLastError();
 }
 
 }  // namespace
@@ -122,13 +240,11 @@ extern "C" k2_status k2_adjust_logits(const k2_logit_rules* u, const float* d_lo
     set_error("masks need n_masks >= 1 and rows of at least ceil(vocab / 32) words");
     return K2_ERR_ARG;
   }
-  const int smem = 8 * kRuleSlice;
-  cudaError_t e = cudaFuncSetAttribute(rules_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e == cudaSuccess) {
-    const dim3 grid((vocab + kRuleSlice - 1) / kRuleSlice, rows);
-    rules_kernel<<<grid, kRuleThreads, smem, static_cast<cudaStream_t>(stream)>>>(*u, d_logits, ld, d_out, ld_out, vocab);
-    e = cudaGetLastError();
-  }
+  // each slice reads its row's whole history: large slices, unless they leave SMs idle and the history is short
+  const long long large = static_cast<long long>(rows) * ((vocab + 512 * kPerThread - 1) / (512 * kPerThread));
+  const cudaError_t e = large >= 152 || (u->ids && u->ids_stride > 4096)
+                            ? launch_rules<512>(*u, d_logits, ld, d_out, ld_out, rows, vocab, static_cast<cudaStream_t>(stream))
+                            : launch_rules<128>(*u, d_logits, ld, d_out, ld_out, rows, vocab, static_cast<cudaStream_t>(stream));
   if (e == cudaSuccess) return K2_OK;
   set_error("logit rules launch: %s", cudaGetErrorString(e));
   return K2_ERR_CUDA;
