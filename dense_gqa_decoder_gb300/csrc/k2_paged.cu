@@ -271,42 +271,58 @@ struct Codes<4> { using type = uint32_t; };
 template <>
 struct Codes<2> { using type = uint16_t; };
 
-// Codes of E elements under scale s > 0, inv = 1 / s (0: s is too small for that); the whole warp takes part.
-template <int E, typename C>
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ float2 parts(f32x2 v) {
+  float2 f;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+  return f;
+}
+// two fp32 values to E4M3 codes, the first in the low byte
+__device__ __forceinline__ uint32_t e4m3x2(f32x2 v) {
+  const float2 f = parts(v);
+  return __nv_cvt_float2_to_fp8x2(f, __NV_SATFINITE, __NV_E4M3);
+}
+
+template <typename C, int E>
+__device__ __forceinline__ uint32_t exact_codes(const float* f, float s) {
+  uint32_t u = 0;
+#pragma unroll
+  for (int e = 0; e < E; ++e) u |= quantize<C>(f[e], s) << (8 * e);
+  return u;
+}
+// Codes of E finite elements under scale s, inv = 1 / s; the whole warp takes part.
+template <typename C, int E>
 __device__ __forceinline__ uint32_t fast_codes(const float* f, float s, float inv) {
   uint32_t u = 0;
-  bool unsure = inv == 0.f;
-  float y[E];
+  bool unsure = false;
 #pragma unroll
-  for (int e = 0; e < E; ++e) y[e] = __fmul_rn(f[e], inv);
-  if constexpr (std::is_same<C, CodeI8>::value) {
-    // |y| <= 127 (1 + 2^-22): y is within 2^-15 of the quotient, so only one that near a midpoint can round the other way
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const float r = rintf(y[e]);
-      unsure |= fabsf(fabsf(y[e] - r) - 0.5f) < 1e-4f;
-      u |= (y[e] == y[e] ? static_cast<uint32_t>(static_cast<int>(fminf(fmaxf(r, -127.f), 127.f))) & 0xFFu : 0u) << (8 * e);
-    }
-  } else {
-    // the quotient lies between y (1 - 2^-20) and y (1 + 2^-20): the same code for both is its code
-#pragma unroll
-    for (int e = 0; e < E; e += 2) {
-      const float a0 = y[e] * (1.f - 9.5367432e-7f), a1 = y[e + 1] * (1.f - 9.5367432e-7f);
-      const float b0 = y[e] * (1.f + 9.5367432e-7f), b1 = y[e + 1] * (1.f + 9.5367432e-7f);
-      uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a0, a1), __NV_SATFINITE, __NV_E4M3);
-      const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(b0, b1), __NV_SATFINITE, __NV_E4M3);
+  for (int e = 0; e < E; e += 2) {
+    const f32x2 y = mul2(pk2(f[e], f[e + 1]), pk2(inv, inv));
+    if constexpr (std::is_same<C, CodeI8>::value) {
+      // |y| <= 127 (1 + 2^-22).  Added to 1.5 2^23 it is rounded to an integer, whose low byte is the code; y is within
+      // 2^-15 of the quotient, so only one that near a midpoint can round the other way.
+      const f32x2 magic = pk2(12582912.f, 12582912.f), r = add2(y, magic);
+      const float2 d = parts(add2(y, mul2(add2(r, pk2(-12582912.f, -12582912.f)), pk2(-1.f, -1.f)))), t = parts(r);
+      unsure |= fabsf(d.x) > 0.4999f || fabsf(d.y) > 0.4999f;
+      u |= __byte_perm(__float_as_uint(t.x), __float_as_uint(t.y), 0x0040) << (8 * e) & (0xFFFFu << (8 * e));
+    } else {
+      // the quotient lies between y (1 - 2^-20) and y (1 + 2^-20): the same code for both is its code
+      const uint32_t lo = e4m3x2(mul2(y, pk2(1.f - 9.5367432e-7f, 1.f - 9.5367432e-7f)));
+      const uint32_t hi = e4m3x2(mul2(y, pk2(1.f + 9.5367432e-7f, 1.f + 9.5367432e-7f)));
       unsure |= lo != hi;
-      if (!(y[e] == y[e])) lo &= 0xFF00u;
-      if (!(y[e + 1] == y[e + 1])) lo &= 0x00FFu;
       u |= lo << (8 * e);
     }
   }
-  if (__any_sync(0xffffffffu, unsure)) {
-    u = 0;
-#pragma unroll
-    for (int e = 0; e < E; ++e) u |= quantize<C>(f[e], s) << (8 * e);
-  }
-  return u;
+  return __any_sync(0xffffffffu, unsure) ? exact_codes<C, E>(f, s) : u;
 }
 
 constexpr int kAppendThreads = 256, kRunRows = 16;  // rows of a run that one warp takes
@@ -321,7 +337,7 @@ struct AppendArgs {
 };
 
 template <typename T, typename C, int D>
-__global__ void __launch_bounds__(kAppendThreads) append_kernel(const PagedPool p, const AppendArgs a) {
+__global__ void __launch_bounds__(kAppendThreads, sizeof(T) == 4 ? 2 : 3) append_kernel(const PagedPool p, const AppendArgs a) {
   constexpr int E = D / 32;
   using Bits = typename RowBits<T, E>::type;
   using Word = typename Codes<E>::type;
@@ -369,16 +385,44 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const PagedPool 
 #pragma unroll
     for (int i = 0; i < kRunRows; ++i)
       if (i0 + i < n) x[i] = __ldg(reinterpret_cast<const Bits*>(src + i * stride));
+    // the largest magnitude: 16-bit elements two at a time.  An infinity or a NaN shows in it; the finite elements'
+    // largest is then found the slow way, and every code of the unit is divided for.
     float top = 0.f;
+    if constexpr (sizeof(T) == 4) {
 #pragma unroll
-    for (int i = 0; i < kRunRows; ++i) {
-      if (i0 + i >= n) break;
-      float f[E];
-      to_floats<T, E>(x[i], f);
+      for (int i = 0; i < kRunRows; ++i) {
+        if (i0 + i >= n) break;
+        float f[E];
+        to_floats<T, E>(x[i], f);
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const float m = fabsf(f[e]);
-        if (m <= 3.402823466e38f) top = fmaxf(top, m);  // finite
+        for (int e = 0; e < E; ++e) asm("max.NaN.f32 %0, %0, %1;" : "+f"(top) : "f"(fabsf(f[e])));
+      }
+    } else {
+      using T2 = typename std::conditional<std::is_same<T, __half>::value, __half2, __nv_bfloat162>::type;
+      uint32_t z = 0;
+      T2 top2 = *reinterpret_cast<const T2*>(&z);
+#pragma unroll
+      for (int i = 0; i < kRunRows; ++i) {
+        if (i0 + i >= n) break;
+        const T2* h = reinterpret_cast<const T2*>(&x[i]);
+#pragma unroll
+        for (int e = 0; e < E / 2; ++e) top2 = __hmax2_nan(top2, __habs2(h[e]));
+      }
+      const float ta = to_f32(top2.x), tb = to_f32(top2.y);
+      asm("max.NaN.f32 %0, %1, %2;" : "=f"(top) : "f"(ta), "f"(tb));
+    }
+    bool odd = __any_sync(0xffffffffu, !(top <= 3.402823466e38f));
+    if (odd) {
+      top = 0.f;
+#pragma unroll 1
+      for (int i = 0; i < kRunRows && i0 + i < n; ++i) {
+        float f[E];
+        to_floats<T, E>(__ldg(reinterpret_cast<const Bits*>(src + i * stride)), f);
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          const float m = fabsf(f[e]);
+          if (m <= 3.402823466e38f) top = fmaxf(top, m);
+        }
       }
     }
     top = warp_max_redux(top);
@@ -408,13 +452,14 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const PagedPool 
         }
       }
     }
-    const float inv = now > 1e-30f ? __frcp_rn(now) : 0.f;
+    odd |= !(now > 1e-30f);  // (1 / now may not be finite)
+    const float inv = __frcp_rn(now);
 #pragma unroll
     for (int i = 0; i < kRunRows; ++i) {
       if (i0 + i >= n) break;
       float f[E];
       to_floats<T, E>(x[i], f);
-      const uint32_t u = now > 0.f ? fast_codes<E, C>(f, now, inv) : 0u;
+      const uint32_t u = odd ? exact_codes<C, E>(f, now) : fast_codes<C, E>(f, now, inv);
       *reinterpret_cast<Word*>(codes + static_cast<size_t>(o + i0 + i) * D) = static_cast<Word>(u);
     }
     sync_group();  // every warp of the unit has read the old scale, and s_top

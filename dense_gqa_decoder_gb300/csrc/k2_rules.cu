@@ -22,24 +22,27 @@ namespace k2 {
 namespace {
 
 constexpr int kPerThread = 16;     // logits of a thread
-constexpr int kBiasList = 512;     // biases of a slice that are handled at a time
+constexpr int kBiasList = 512;     // biases of a slice that are handled at a time (>= the threads)
 constexpr unsigned kSeen = 0x80000000u, kBiased = 0x40000000u, kCount = 0x3FFFFFFFu;
 
 // VEC: every row of logits and output is 16-byte aligned
 template <int THREADS, bool VEC>
-__global__ void __launch_bounds__(THREADS) rules_kernel(const k2_logit_rules u, const float* in, long long ld, float* out,
-                                                        long long ld_out, int vocab) {
+__global__ void __launch_bounds__(THREADS, 1536 / THREADS) rules_kernel(const k2_logit_rules u, const float* in, long long ld, float* out,
+                                                                        long long ld_out, int vocab) {
   constexpr int SLICE = THREADS * kPerThread;
   __shared__ __align__(16) unsigned cnt[SLICE];
   __shared__ int b_id[kBiasList];
   __shared__ float b_val[kBiasList];
-  __shared__ int w_sum[THREADS / 32 + 1];
+  __shared__ int w_sum[THREADS / 32];
   const int r = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int v0 = blockIdx.x * SLICE, n = min(SLICE, vocab - v0);
   const float* x = in + r * ld + v0;
   float* y = out + r * ld_out + v0;
   // element j of this thread: four neighbours at a time (VEC), else strided
   auto place = [&](int j) { return VEC ? 4 * (tid + THREADS * (j >> 2)) + (j & 3) : tid + THREADS * j; };
+  const bool counted = u.repetition != nullptr || u.presence != nullptr || u.frequency != nullptr;
+  const int j0 = u.bias_offset != nullptr ? max(__ldg(u.bias_offset + r), 0) : 0;
+  const int j1 = u.bias_offset != nullptr ? min(__ldg(u.bias_offset + r + 1), u.n_bias) : 0;
   float l[kPerThread];
   if constexpr (VEC) {
 #pragma unroll
@@ -60,99 +63,132 @@ __global__ void __launch_bounds__(THREADS) rules_kernel(const k2_logit_rules u, 
 #pragma unroll
     for (int j = 0; j < kPerThread; ++j) l[j] = place(j) < n ? x[place(j)] : 0.f;
   }
-  const bool counted = u.repetition != nullptr || u.presence != nullptr || u.frequency != nullptr;
-  if (counted || u.bias_offset != nullptr) {
+  if (counted || j0 < j1) {
 #pragma unroll
     for (int j = 0; j < kPerThread; j += 4) *reinterpret_cast<uint4*>(cnt + 4 * (tid + THREADS * (j >> 2))) = make_uint4(0, 0, 0, 0);
+    // the first THREADS biases of the row: which of them lie in the slice
+    unsigned d = ~0u;
+    float value = 0.f;
+    if (j0 + tid < j1) {
+      d = static_cast<unsigned>(__ldg(u.bias_ids + j0 + tid) - v0);
+      value = __ldg(u.bias + j0 + tid);
+    }
+    unsigned m = __ballot_sync(0xffffffffu, d < static_cast<unsigned>(n));
+    if (lane == 0) w_sum[warp] = __popc(m);
     __syncthreads();
-  }
-  if (counted) {
-    const int* ids = u.ids + r * u.ids_stride;
-    const int len = static_cast<int>(min(static_cast<long long>(u.ids_len[r]), static_cast<long long>(u.ids_stride)));
-    const int prompt = u.prompt_len != nullptr ? u.prompt_len[r] : 0;
-    auto count = [&](int id, int i) {
-      const unsigned d = static_cast<unsigned>(id - v0);
+    int listed = 0;
+    if (j0 < j1) {  // listed in order
+      int before = 0;
+#pragma unroll
+      for (int w = 0; w < THREADS / 32; ++w) {
+        if (w < warp) before += w_sum[w];
+        listed += w_sum[w];
+      }
       if (d < static_cast<unsigned>(n)) {
-        if (i >= prompt) atomicAdd(&cnt[d], 1u);
-        atomicOr(&cnt[d], kSeen);
+        const int at = before + __popc(m & ((1u << lane) - 1));
+        b_id[at] = static_cast<int>(d);
+        b_val[at] = value;
+        atomicOr(&cnt[d], kBiased);
       }
-    };
-    int i = 0;
-    if ((reinterpret_cast<uintptr_t>(ids) & 15) == 0) {  // four ids at a time, eight such loads on their way
-      const int4* ids4 = reinterpret_cast<const int4*>(ids);
-      const int quads = len > 0 ? len >> 2 : 0;
-      for (int q0 = tid; q0 < quads; q0 += 8 * THREADS) {
-        int4 v[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (q0 + j * THREADS < quads) v[j] = __ldg(ids4 + q0 + j * THREADS);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int q = q0 + j * THREADS;
-          if (q >= quads) break;
-          count(v[j].x, 4 * q);
-          count(v[j].y, 4 * q + 1);
-          count(v[j].z, 4 * q + 2);
-          count(v[j].w, 4 * q + 3);
+    }
+    if (counted) {
+      const int* ids = u.ids + r * u.ids_stride;
+      const int len = static_cast<int>(min(static_cast<long long>(u.ids_len[r]), static_cast<long long>(u.ids_stride)));
+      const int prompt = u.prompt_len != nullptr ? u.prompt_len[r] : 0;
+      auto count = [&](int id, int i) {
+        const unsigned e = static_cast<unsigned>(id - v0);
+        if (e < static_cast<unsigned>(n)) {
+          if (i >= prompt) atomicAdd(&cnt[e], 1u);
+          atomicOr(&cnt[e], kSeen);
         }
-      }
-      i = 4 * quads;
-    }
-    for (i += tid; i < len; i += THREADS) count(__ldg(ids + i), i);
-    __syncthreads();
-    const float rep = u.repetition != nullptr ? u.repetition[r] : 1.f;
-    const float freq = u.frequency != nullptr ? u.frequency[r] : 0.f, pres = u.presence != nullptr ? u.presence[r] : 0.f;
+      };
+      int i = 0;
+      if ((reinterpret_cast<uintptr_t>(ids) & 15) == 0) {  // four ids at a time, four such loads on their way
+        const int4* ids4 = reinterpret_cast<const int4*>(ids);
+        const int quads = len > 0 ? len >> 2 : 0;
+#pragma unroll 1
+        for (int q0 = tid; q0 < quads; q0 += 4 * THREADS) {
+          int4 v[4];
 #pragma unroll
-    for (int j = 0; j < kPerThread; ++j) {
-      const unsigned c = cnt[place(j)];
-      if (c == 0) continue;
-      if (u.repetition != nullptr) l[j] = l[j] > 0.f ? __fdiv_rn(l[j], rep) : __fmul_rn(l[j], rep);
-      if (c & kCount) l[j] = __fsub_rn(__fsub_rn(l[j], __fmul_rn(freq, static_cast<float>(c & kCount))), pres);
+          for (int j = 0; j < 4; ++j)
+            if (q0 + j * THREADS < quads) v[j] = __ldg(ids4 + q0 + j * THREADS);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int q = q0 + j * THREADS;
+            if (q >= quads) break;
+            count(v[j].x, 4 * q);
+            count(v[j].y, 4 * q + 1);
+            count(v[j].z, 4 * q + 2);
+            count(v[j].w, 4 * q + 3);
+          }
+        }
+        i = 4 * quads;
+      }
+#pragma unroll 1
+      for (i += tid; i < len; i += THREADS) count(__ldg(ids + i), i);
     }
-  }
-  if (u.bias_offset != nullptr) {
-    const int j1 = min(u.bias_offset[r + 1], u.n_bias);
-    int listed = 0;  // of the slice so far, in b_id / b_val
-    auto apply = [&] {  // adds the listed biases, in order
+    const float rep = u.repetition != nullptr ? u.repetition[r] : 1.f;
+    // a quotient as a product with the reciprocal, one rounding more: it decides nothing but a few logits' last bits
+    const float inv = 1.f / rep;
+    const float freq = u.frequency != nullptr ? u.frequency[r] : 0.f, pres = u.presence != nullptr ? u.presence[r] : 0.f;
+    __syncthreads();
+    auto touched = [&](unsigned c, float v, int at) {
+      if (c & (kSeen | kCount)) {
+        if (u.repetition != nullptr) v *= v > 0.f ? inv : rep;
+        if (c & kCount) v = __fsub_rn(__fsub_rn(v, __fmul_rn(freq, static_cast<float>(c & kCount))), pres);
+      }
+      if (c & kBiased)
+        for (int i = 0; i < listed; ++i)
+          if (b_id[i] == at) v = __fadd_rn(v, b_val[i]);
+      return v;
+    };
+    if constexpr (VEC) {
+#pragma unroll
+      for (int j = 0; j < kPerThread; j += 4) {
+        const uint4 c = *reinterpret_cast<const uint4*>(cnt + place(j));
+        if ((c.x | c.y | c.z | c.w) == 0) continue;
+        if (c.x) l[j] = touched(c.x, l[j], place(j));
+        if (c.y) l[j + 1] = touched(c.y, l[j + 1], place(j + 1));
+        if (c.z) l[j + 2] = touched(c.z, l[j + 2], place(j + 2));
+        if (c.w) l[j + 3] = touched(c.w, l[j + 3], place(j + 3));
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < kPerThread; ++j) {
+        const unsigned c = cnt[place(j)];
+        if (c) l[j] = touched(c, l[j], place(j));
+      }
+    }
+    // further biases, THREADS at a time
+#pragma unroll 1
+    for (int k = j0 + THREADS; k < j1; k += THREADS) {
       __syncthreads();
-      for (int i = tid; i < listed; i += THREADS) atomicOr(&cnt[b_id[i]], kBiased);
+      for (int i = tid; i < listed; i += THREADS) cnt[b_id[i]] &= ~kBiased;  // (an id listed twice: the same store)
+      d = k + tid < j1 ? static_cast<unsigned>(__ldg(u.bias_ids + k + tid) - v0) : ~0u;
+      const bool take = d < static_cast<unsigned>(n);
+      m = __ballot_sync(0xffffffffu, take);
+      if (lane == 0) w_sum[warp] = __popc(m);
+      __syncthreads();
+      int before = 0;
+      listed = 0;
+#pragma unroll 1
+      for (int w = 0; w < THREADS / 32; ++w) {
+        if (w < warp) before += w_sum[w];
+        listed += w_sum[w];
+      }
+      if (take) {
+        const int at = before + __popc(m & ((1u << lane) - 1));
+        b_id[at] = static_cast<int>(d);
+        b_val[at] = __ldg(u.bias + k + tid);
+        atomicOr(&cnt[d], kBiased);
+      }
       __syncthreads();
 #pragma unroll
       for (int j = 0; j < kPerThread; ++j) {
         const int at = place(j);
-        if (!(cnt[at] & kBiased)) continue;
-        for (int i = 0; i < listed; ++i)
-          if (b_id[i] == at) l[j] = __fadd_rn(l[j], b_val[i]);
-        cnt[at] &= ~kBiased;
+        if (cnt[at] & kBiased) l[j] = touched(kBiased, l[j], at);
       }
-      __syncthreads();
-    };
-    for (int j0 = max(u.bias_offset[r], 0); j0 < j1; j0 += THREADS) {
-      const int j = j0 + tid;
-      const unsigned d = j < j1 ? static_cast<unsigned>(__ldg(u.bias_ids + j) - v0) : ~0u;
-      const bool take = d < static_cast<unsigned>(n);
-      const unsigned m = __ballot_sync(0xffffffffu, take);
-      if (lane == 0) w_sum[warp] = __popc(m);
-      __syncthreads();
-      int before = 0, all = 0;
-#pragma unroll
-      for (int w = 0; w < THREADS / 32; ++w) {
-        if (w < warp) before += w_sum[w];
-        all += w_sum[w];
-      }
-      if (listed + all > kBiasList) {  // (all <= THREADS <= kBiasList)
-        apply();
-        listed = 0;
-      }
-      if (take) {
-        const int at = listed + before + __popc(m & ((1u << lane) - 1));
-        b_id[at] = static_cast<int>(d);
-        b_val[at] = __ldg(u.bias + j);
-      }
-      listed += all;
-      __syncthreads();  // w_sum
     }
-    if (listed > 0) apply();
   }
   const int mr = u.mask == nullptr ? -1 : u.mask_row != nullptr ? u.mask_row[r] : r;
   const bool masked = mr >= 0 && mr < u.n_masks;
