@@ -399,20 +399,28 @@ def _call(st):
 
 def _need(what, t, dtype, shape, device):
     """The C calls read raw pointers: a contiguous tensor of this type and shape
-    (None: any extent) on the device of the call."""
-    if t.dtype is not dtype or t.device != device or not t.is_contiguous() or len(t.shape) != len(shape) or any(
+    (None: any extent) on the device (index) of the call."""
+    if t.dtype is not dtype or t.get_device() != device or not t.is_contiguous() or len(t.shape) != len(shape) or any(
             n is not None and n != m for n, m in zip(shape, t.shape)):
-        raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, got "
+        raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)} on cuda:{device}, got "
                          f"{t.dtype} {tuple(t.shape)} on {t.device}")
 
 
+# The checks below run before every call of a serving loop, so they are written out with the cheapest tensor
+# accessors (16 us of checks and marshalling per plan became 8); what fails one goes to _need, which says why.
 def _device(t):
-    """The call's device: that of `t`, which has to be the current one (the C
-    calls launch there)."""
-    d = t.device
-    if d.type != "cuda" or d.index != torch.cuda.current_device():
-        raise ValueError(f"the tensors must be on the current CUDA device, got {d}")
+    """The call's device index: that of `t`, which has to be the current one (the
+    C calls launch there)."""
+    d = t.get_device()
+    if d < 0 or d != torch.cuda.current_device():
+        raise ValueError(f"the tensors must be on the current CUDA device, got {t.device}")
     return d
+
+
+def _raw_stream(stream, dev):
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 class PagedCache:
@@ -464,26 +472,39 @@ def paged_plan(cached, fresh, table, free, free_count, block_tokens, *, kv_len, 
     dev = _device(cached)
     if free_count_out is None:
         free_count_out = free_count
-    r = cached.numel()
+    r, n = cached.numel(), slots.numel()
     i32 = torch.int32
+    for t in (cached, fresh, table, free, free_count, free_count_out, kv_len, cu_new, slots, positions, status):
+        if t.dtype is not i32 or t.get_device() != dev or not t.is_contiguous():
+            break
+    else:
+        if (cached.dim() == 1 and fresh.numel() == r and table.dim() == 2 and table.size(0) == r and
+                free_count.numel() == 1 and free_count_out.numel() == 1 and kv_len.numel() == r and
+                cu_new.numel() == r + 1 and positions.numel() == n and status.numel() == 4):
+            st = LIB.k2_paged_plan(cached.data_ptr(), fresh.data_ptr(), r, block_tokens, table.data_ptr(),
+                                   table.size(1), free.data_ptr(), free.numel(), free_count.data_ptr(),
+                                   free_count_out.data_ptr(), kv_len.data_ptr(), cu_new.data_ptr(), slots.data_ptr(),
+                                   positions.data_ptr(), n, status.data_ptr(), _raw_stream(stream, dev))
+            if st:
+                _call(st)
+            return
     for what, t, shape in (("cached", cached, (r,)), ("fresh", fresh, (r,)), ("table", table, (r, None)),
                            ("free", free, (None,)), ("free_count", free_count, (1,)),
                            ("free_count_out", free_count_out, (1,)), ("kv_len", kv_len, (r,)),
                            ("cu_new", cu_new, (r + 1,)), ("slots", slots, (None,)),
-                           ("positions", positions, slots.shape), ("status", status, (4,))):
+                           ("positions", positions, (n,)), ("status", status, (4,))):
         _need(what, t, i32, shape, dev)
-    _call(LIB.k2_paged_plan(cached.data_ptr(), fresh.data_ptr(), r, block_tokens, table.data_ptr(), table.shape[1],
-                            free.data_ptr(), free.numel(), free_count.data_ptr(), free_count_out.data_ptr(),
-                            kv_len.data_ptr(), cu_new.data_ptr(), slots.data_ptr(), positions.data_ptr(),
-                            slots.numel(), status.data_ptr(), _stream(stream)))
+    raise ValueError("plan: tensors of another shape than the call's")
 
 
 def _rows(what, t, dtype, heads, head_dim, device):
-    """[tokens, heads, head_dim] rows whose tokens may be apart (a slice of packed rows)."""
-    if t.dtype is not dtype or t.device != device or t.dim() != 3 or t.shape[1] != heads or t.shape[2] != head_dim \
-            or t.stride(2) != 1 or (heads > 1 and t.stride(1) != head_dim):
-        raise ValueError(f"{what} must be [tokens, {heads}, {head_dim}] {dtype} rows on {device}, each row contiguous, "
-                         f"got {t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
+    """[tokens, heads, head_dim] rows whose tokens may be apart (a slice of packed rows): their distance"""
+    if t.dtype is dtype and t.get_device() == device and t.dim() == 3 and t.size(1) == heads and t.size(2) == head_dim:
+        token, head, one = t.stride()
+        if one == 1 and (heads == 1 or head == head_dim):
+            return token
+    raise ValueError(f"{what} must be [tokens, {heads}, {head_dim}] {dtype} rows on cuda:{device}, each row contiguous, "
+                     f"got {t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
 
 
 def paged_append(cache, k, v, slots, stream=None):
@@ -491,17 +512,21 @@ def paged_append(cache, k, v, slots, stream=None):
     fp32; tokens may be strided) to the int32 slots [tokens]."""
     dev = _device(k)
     if dev != cache.device:
-        raise ValueError(f"the rows are on {dev}, the cache on {cache.device}")
-    if k.dtype not in _ROW_DTYPES:
+        raise ValueError(f"the rows are on cuda:{dev}, the cache on cuda:{cache.device}")
+    dtype = _ROW_DTYPES.get(k.dtype)
+    if dtype is None:
         raise ValueError(f"k and v must be float32, bfloat16 or float16, got {k.dtype}")
-    _rows("k", k, k.dtype, cache.n_kv_heads, cache.head_dim, dev)
-    _rows("v", v, k.dtype, cache.n_kv_heads, cache.head_dim, dev)
-    n = k.shape[0]
-    if v.shape[0] != n:
-        raise ValueError(f"k has {n} rows, v {v.shape[0]}")
-    _need("slots", slots, torch.int32, (n,), dev)
-    _call(LIB.k2_paged_append(cache._ref, k.data_ptr(), v.data_ptr(), _ROW_DTYPES[k.dtype], k.stride(0), v.stride(0),
-                              slots.data_ptr(), n, _stream(stream)))
+    ks = _rows("k", k, k.dtype, cache.n_kv_heads, cache.head_dim, dev)
+    vs = _rows("v", v, k.dtype, cache.n_kv_heads, cache.head_dim, dev)
+    n = k.size(0)
+    if v.size(0) != n:
+        raise ValueError(f"k has {n} rows, v {v.size(0)}")
+    if slots.dtype is not torch.int32 or slots.get_device() != dev or slots.numel() != n or not slots.is_contiguous():
+        _need("slots", slots, torch.int32, (n,), dev)
+    st = LIB.k2_paged_append(cache._ref, k.data_ptr(), v.data_ptr(), dtype, ks, vs, slots.data_ptr(), n,
+                             _raw_stream(stream, dev))
+    if st:
+        _call(st)
 
 
 def paged_workspace():
@@ -516,23 +541,35 @@ def paged_attention(cache, q, out, cu_q, kv_len, table, max_q, workspace, scale=
     default head_dim ** -0.5."""
     dev = _device(q)
     if dev != cache.device:
-        raise ValueError(f"the queries are on {dev}, the cache on {cache.device}")
-    if q.dtype not in (torch.bfloat16, torch.float16):
-        raise ValueError(f"q must be bfloat16 or float16, got {q.dtype}")
-    heads, d = (q.shape[1] if q.dim() == 3 else 0), cache.head_dim
-    _rows("q", q, q.dtype, heads, d, dev)
-    _rows("out", out, q.dtype, heads, d, dev)
-    if out.shape[0] != q.shape[0]:
-        raise ValueError(f"q has {q.shape[0]} rows, out {out.shape[0]}")
-    r = kv_len.numel()
-    _need("cu_q", cu_q, torch.int32, (r + 1,), dev)
-    _need("kv_len", kv_len, torch.int32, (r,), dev)
-    _need("table", table, torch.int32, (r, None), dev)
+        raise ValueError(f"the queries are on cuda:{dev}, the cache on cuda:{cache.device}")
+    dtype = q.dtype
+    if dtype is not torch.bfloat16 and dtype is not torch.float16:
+        raise ValueError(f"q must be bfloat16 or float16, got {dtype}")
+    heads, d = (q.size(1) if q.dim() == 3 else 0), cache.head_dim
+    qs = _rows("q", q, dtype, heads, d, dev)
+    os_ = _rows("out", out, dtype, heads, d, dev)
+    n = q.size(0)
+    if out.size(0) != n:
+        raise ValueError(f"q has {n} rows, out {out.size(0)}")
+    r, i32 = kv_len.numel(), torch.int32
+    for t in (cu_q, kv_len, table):
+        if t.dtype is not i32 or t.get_device() != dev or not t.is_contiguous():
+            break
+    else:
+        if (cu_q.numel() == r + 1 and table.dim() == 2 and table.size(0) == r and workspace.dtype is torch.uint8 and
+                workspace.get_device() == dev and workspace.is_contiguous()):
+            st = LIB.k2_paged_attention(cache._ref, q.data_ptr(), _ROW_DTYPES[dtype], qs, cu_q.data_ptr(),
+                                        kv_len.data_ptr(), table.data_ptr(), table.size(1), r, n, heads, max_q,
+                                        d ** -0.5 if scale is None else scale, out.data_ptr(), os_,
+                                        workspace.data_ptr(), workspace.numel(), _raw_stream(stream, dev))
+            if st:
+                _call(st)
+            return
+    _need("cu_q", cu_q, i32, (r + 1,), dev)
+    _need("kv_len", kv_len, i32, (r,), dev)
+    _need("table", table, i32, (r, None), dev)
     _need("workspace", workspace, torch.uint8, (None,), dev)
-    _call(LIB.k2_paged_attention(cache._ref, q.data_ptr(), _ROW_DTYPES[q.dtype], q.stride(0), cu_q.data_ptr(),
-                                 kv_len.data_ptr(), table.data_ptr(), table.shape[1], r, q.shape[0], heads, max_q,
-                                 d ** -0.5 if scale is None else scale, out.data_ptr(), out.stride(0),
-                                 workspace.data_ptr(), workspace.numel(), _stream(stream)))
+    raise ValueError("attention: tensors of another shape than the call's")
 
 
 def adjust_logits(logits, out=None, *, repetition=None, presence=None, frequency=None, ids=None, ids_len=None,
@@ -544,46 +581,54 @@ def adjust_logits(logits, out=None, *, repetition=None, presence=None, frequency
     dev = _device(logits)
     if out is None:
         out = logits
+    f32, i32 = torch.float32, torch.int32
+    rows, vocab = logits.shape if logits.dim() == 2 else (0, 0)
     for what, t in (("logits", logits), ("out", out)):
-        if t.dtype is not torch.float32 or t.device != dev or t.dim() != 2 or t.shape != logits.shape or t.stride(1) != 1:
-            raise ValueError(f"{what} must be [rows, vocab] float32 rows on {dev}, got {t.dtype} {tuple(t.shape)} on "
-                             f"{t.device}")
-    rows, vocab = logits.shape
-    u = LogitRules()
-    for what, t in (("repetition", repetition), ("presence", presence), ("frequency", frequency)):
-        if t is not None:
-            _need(what, t, torch.float32, (rows,), dev)
-            setattr(u, what, t.data_ptr())
+        if t.dtype is not f32 or t.get_device() != dev or t.dim() != 2 or t.size(0) != rows or t.size(1) != vocab or \
+                t.stride(1) != 1:
+            raise ValueError(f"{what} must be [rows, vocab] float32 rows on cuda:{dev}, got {t.dtype} {tuple(t.shape)} "
+                             f"on {t.device}")
+
+    def row(what, t, dtype, n=rows):  # the address of a value per row
+        if t is None:
+            return None
+        if t.dtype is not dtype or t.get_device() != dev or t.numel() != n or not t.is_contiguous():
+            _need(what, t, dtype, (n,), dev)
+        return t.data_ptr()
+    rep, pres, freq = row("repetition", repetition, f32), row("presence", presence, f32), row("frequency", frequency, f32)
+    id_ptr = id_stride = id_len = id_prompt = 0
     if ids is not None:
-        _need("ids", ids, torch.int32, (rows, None), dev)
+        if ids.dtype is not i32 or ids.get_device() != dev or ids.dim() != 2 or ids.size(0) != rows or \
+                not ids.is_contiguous():
+            _need("ids", ids, i32, (rows, None), dev)
         if ids_len is None:
             raise ValueError("ids need ids_len")
-        _need("ids_len", ids_len, torch.int32, (rows,), dev)
-        u.ids, u.ids_stride, u.ids_len = ids.data_ptr(), ids.shape[1], ids_len.data_ptr()
-        if prompt_len is not None:
-            _need("prompt_len", prompt_len, torch.int32, (rows,), dev)
-            u.prompt_len = prompt_len.data_ptr()
-        if not ids.numel():  # no row holds a token: nothing to penalise
-            u = LogitRules()
+        id_len, id_prompt = row("ids_len", ids_len, i32), row("prompt_len", prompt_len, i32)
+        if ids.numel():
+            id_ptr, id_stride = ids.data_ptr(), ids.size(1)
+        else:  # no row holds a token: nothing to penalise
+            rep = pres = freq = id_len = id_prompt = None
+    b_off = b_ids = b_val = n_bias = 0
     if bias is not None:
         offset, bias_ids, values = bias
-        _need("bias offsets", offset, torch.int32, (rows + 1,), dev)
-        _need("bias ids", bias_ids, torch.int32, (None,), dev)
-        _need("bias values", values, torch.float32, bias_ids.shape, dev)
-        if bias_ids.numel():
-            u.bias_offset, u.bias_ids, u.bias = offset.data_ptr(), bias_ids.data_ptr(), values.data_ptr()
-            u.n_bias = bias_ids.numel()
+        b_off, n_bias = row("bias offsets", offset, i32, rows + 1), bias_ids.numel()
+        b_ids, b_val = row("bias ids", bias_ids, i32, n_bias), row("bias values", values, f32, n_bias)
+        if not n_bias:
+            b_off = 0
+    m_ptr = m_stride = n_masks = m_row = 0
     if mask is not None:
-        _need("mask", mask, torch.int32, (None, None), dev)
-        if mask.shape[1] < (vocab + 31) // 32 or (mask_row is None and mask.shape[0] < rows):
+        _need("mask", mask, i32, (None, None), dev)
+        m_ptr, (n_masks, m_stride) = mask.data_ptr(), mask.shape
+        if m_stride < (vocab + 31) // 32 or (mask_row is None and n_masks < rows):
             raise ValueError(f"mask must have {(vocab + 31) // 32} words for each of its rows (and a row for each of the "
                              f"logits without mask_row), got {tuple(mask.shape)}")
-        u.mask, u.mask_stride, u.n_masks = mask.data_ptr(), mask.shape[1], mask.shape[0]
-        if mask_row is not None:
-            _need("mask_row", mask_row, torch.int32, (rows,), dev)
-            u.mask_row = mask_row.data_ptr()
-    _call(LIB.k2_adjust_logits(C.byref(u), logits.data_ptr(), logits.stride(0), out.data_ptr(), out.stride(0), rows, vocab,
-                               _stream(stream)))
+        m_row = row("mask_row", mask_row, i32)
+    u = LogitRules(rep or None, pres or None, freq or None, id_ptr or None, id_stride, id_len or None, id_prompt or None,
+                   b_off or None, b_ids or None, b_val or None, n_bias, m_ptr or None, m_stride, n_masks, m_row or None)
+    st = LIB.k2_adjust_logits(C.byref(u), logits.data_ptr(), logits.stride(0), out.data_ptr(), out.stride(0), rows, vocab,
+                              _raw_stream(stream, dev))
+    if st:
+        _call(st)
 
 
 def spec_draft(tokens, max_draft=8) -> list:
