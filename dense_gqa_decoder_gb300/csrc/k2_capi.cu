@@ -49,7 +49,7 @@ struct Layout {
   size_t vlog, vids, varg, vpv, vpi;               // speculative verification: logits, ids, argmax
   // tensor-core prefill of up to `pchunk` tokens at a time (bf16 weights)
   int pchunk;
-  size_t px, pxh, pxl, pah, pal, pqkv, pq, plog;
+  size_t px, pxh, pxl, pah, pal, pqkv, pq, plog, parg;
   size_t wqkv, wo, wgu, wdown, wlm;  // packed weights; per-layer strides below
   size_t wqkv_layer, wo_layer, wgu_layer, wdown_layer;
   // fp8 weights with a tensor-core prefill: the codes as bf16 in the bf16 packed layout
@@ -148,6 +148,7 @@ Layout layout_of(const k2_config& c) {
     l.pqkv = take(P * s.qkv_n * 4);
     l.pq = take(P * s.nq * s.d * 4);
     l.plog = take(P > 0 ? static_cast<size_t>(s.B) * s.V * 4 : 0);  // batched-decode logits
+    l.parg = take(sizeof(int) * s.B);  // paged step: the argmax of every request
     const size_t nv = P > 0 ? kSpecMax + 1 : 0;
     l.vlog = take(nv * s.V * 4);
     l.vids = take(sizeof(int) * (kSpecMax + 1));
@@ -843,13 +844,23 @@ cudaError_t plan_tc_prefill(k2_ctx* c) {
   return cudaSuccess;
 }
 
+// The rows of a paged step: new tokens of many requests, their K/V and attention over a block-paged cache
+struct PagedBlock {
+  const k2_paged_kv* layers;  // host array
+  const int32_t *positions, *slots, *cu, *kv_len, *table;
+  int table_stride, requests, max_new;
+  void* ws;
+  size_t ws_bytes;
+};
+
 // One block of n <= pchunk prompt tokens of sequence seq at positions
 // pos0 .. pos0+n-1 through every layer; the residual of its last token is left
 // in pX[n-1].
 // d_pos0 (nullable): the block's first position read on the device (a graph
 // replayed at any position), else pos0
-cudaError_t prefill_block(k2_ctx* c, int seq, const int* d_tokens, int n, int pos0, cudaStream_t st,
-                          const int* d_pos0 = nullptr) {
+// paged (nullable): a paged step's rows instead (seq, pos0 and d_pos0 are not used)
+cudaError_t prefill_block(k2_ctx* c, int seq, const int32_t* d_tokens, int n, int pos0, cudaStream_t st,
+                          const int* d_pos0 = nullptr, const PagedBlock* paged = nullptr) {
   const Sizes& s = c->s;
   float* X = reinterpret_cast<float*>(c->ws + c->lay.px);
   auto* xh = reinterpret_cast<__nv_bfloat16*>(c->ws + c->lay.pxh);
@@ -874,8 +885,8 @@ cudaError_t prefill_block(k2_ctx* c, int seq, const int* d_tokens, int n, int po
   // the tcgen05 attention, blocks over 16 tokens): each matrix of the layer is
   // converted to fp16 (exact in fp16's normal range) before its GEMM, and the
   // activations enter as single fp16; elsewhere 3 acts as 1
-  const bool f16 =
-      c->pf_split == 3 && c->cfg.weight_dtype == K2_BF16 && !small && c->pf_tc && c->use_pf_tc && c->w16_ok;
+  const bool f16 = c->pf_split == 3 && c->cfg.weight_dtype == K2_BF16 && !small &&
+                   (paged || (c->pf_tc && c->use_pf_tc)) && c->w16_ok;
   const int mode = f16 ? 3 : c->pf_split == 3 ? 1 : c->pf_split;
   // long fp16 blocks: 256-token tiles (each SM receives 1.5x the bytes of a
   // 128-token tile per K step for twice its MMAs)
@@ -964,7 +975,8 @@ cudaError_t prefill_block(k2_ctx* c, int seq, const int* d_tokens, int n, int po
   const void* m_ah = small ? c->tb_ah.data() : wide ? c->tw_ah.data() : c->tm_ah.data();
   const void* m_al = small ? c->tb_al.data() : split ? c->tm_al.data() : nullptr;
   cudaError_t e = launch_embed_rows(d_tokens, n, c->embed, s.gb, X, s.H, s.V, c->guard,
-                                    c->hist + static_cast<size_t>(seq) * c->lay.cap, 0, nullptr, pos0, d_pos0, st);
+                                    paged ? nullptr : c->hist + static_cast<size_t>(seq) * c->lay.cap, 0, nullptr, pos0,
+                                    d_pos0, st);
   if (f16 && !e) {
     // the second stream starts after the work already on st (an earlier
     // prefill may still read the copies) and converts the first two layers
@@ -981,10 +993,30 @@ cudaError_t prefill_block(k2_ctx* c, int seq, const int* d_tokens, int n, int po
     if (!e)
       e = small ? gemm_sk(wmap(l, 0), c->tcs(l, 0), m_xh, m_xl, s.qkv_n, s.H, TC_STORE, qkv, s.qkv_n)
                 : gemm(wmap(l, 0), c->tcs(l, 0), m_xh, m_xl, s.qkv_n, s.H, TC_STORE, qkv, nullptr, nullptr, s.qkv_n);
-    if (!e)
+    if (!e && paged) {
+      // q as fp16 and k | v as fp32 rows share the query buffer; with bf16 halves ahead of the o_proj GEMM, the fp16
+      // output passes through the SwiGLU buffer (free until the gate/up GEMM)
+      __half* q16 = reinterpret_cast<__half*>(Q);
+      float* kv = reinterpret_cast<float*>(q16 + static_cast<size_t>(n) * s.nq * s.d);
+      __half* o16 = reinterpret_cast<__half*>(f16 ? xh : ah);
+      const int64_t qs = static_cast<int64_t>(s.nq) * s.d, ks = static_cast<int64_t>(s.nkv) * s.d;
+      e = launch_rope_rows(qkv, q16, kv, c->rope, paged->positions, n, s.nq, s.nkv, s.d, c->lay.cap, c->guard, st);
+      k2_status ps = e ? K2_ERR_CUDA
+                       : k2_paged_append(paged->layers + l, kv, kv + ks, K2_F32, 2 * ks, 2 * ks, paged->slots, n, st);
+      // rows of no request (padding) are left alone by the attention: zeros, so that nothing undefined is multiplied
+      if (ps == K2_OK) e = cudaMemsetAsync(o16, 0, static_cast<size_t>(n) * qs * sizeof(__half), st);
+      if (ps == K2_OK && !e)
+        ps = k2_paged_attention(paged->layers + l, q16, K2_F16, qs, paged->cu, paged->kv_len, paged->table,
+                                paged->table_stride, paged->requests, n, s.nq, paged->max_new, scale, o16, qs, paged->ws,
+                                paged->ws_bytes, st);
+      if (ps != K2_OK && !e) e = cudaErrorInvalidValue;
+      if (!e && !f16) e = launch_half_hilo(o16, xh, xl, static_cast<size_t>(n) * qs, st);
+    } else if (!e) {
       e = launch_rope_append(qkv, Q, c->rope, kvdt, c->kc(l), c->vc(l), c->ks(l), c->vs(l), n, s.nq, s.nkv, s.d,
                              pos0, d_pos0, head_row0, c->lay.cap, st, c->pdl);
-    if (!e && small) {
+    }
+    if (paged) {
+    } else if (!e && small) {
       // few queries over a long history: the decode attention in block mode
       // splits every query's keys over a cluster of CTAs
       AttnArgs at = c->p_attn;
@@ -2119,6 +2151,66 @@ k2_status k2_decode_speculative(k2_ctx* c, int32_t seq, const int32_t* h_tokens,
   }
   std::copy(out, out + accepted + 1, h_out);
   *n_out = accepted + 1;
+  return K2_OK;
+}
+
+k2_status k2_paged_step(k2_ctx* c, const k2_paged_kv* layers, const int32_t* d_tokens, const int32_t* d_positions,
+                        const int32_t* d_slots, int32_t tokens, const int32_t* d_cu_new, const int32_t* d_kv_len,
+                        const int32_t* d_table, int32_t table_stride, int32_t requests, int32_t max_new,
+                        int32_t* d_next, float* d_logits, void* d_workspace, size_t ws_bytes, void* stream) {
+  if (!c) return K2_ERR_ARG;
+  const Sizes& s = c->s;
+  if (!c->tc_full || s.d * s.nq > s.I || s.rep < 4)
+    return c->fail(K2_ERR_UNSUPPORTED, "a paged step needs bf16 weights on the tensor-core path (head_dim 64 or 128, 4 query heads per KV head)");
+  if (!layers || !d_tokens || !d_positions || !d_slots || !d_cu_new || !d_kv_len || !d_table || !d_next)
+    return c->fail(K2_ERR_ARG, "layers, d_tokens, d_positions, d_slots, d_cu_new, d_kv_len, d_table and d_next must be non-null");
+  if (tokens < 1 || tokens > c->lay.pchunk)
+    return c->fail(K2_ERR_SHAPE, "tokens %d outside [1, %d] (the context's prefill block)", tokens, c->lay.pchunk);
+  if (requests < 1 || requests > s.B) return c->fail(K2_ERR_SHAPE, "requests %d outside [1, max_batch %d]", requests, s.B);
+  if (table_stride < 1 || max_new < 1)
+    return c->fail(K2_ERR_SHAPE, "table_stride and max_new must be >= 1 (got %d, %d)", table_stride, max_new);
+  for (int l = 0; l < s.L; ++l) {
+    if (layers[l].n_kv_heads != s.nkv || layers[l].head_dim != s.d)
+      return c->fail(K2_ERR_SHAPE, "layer %d's pool has %d KV heads of %d, the model %d of %d", l, layers[l].n_kv_heads,
+                     layers[l].head_dim, s.nkv, s.d);
+    const k2_status ps = k2_paged_append(layers + l, nullptr, nullptr, K2_F32, 0, 0, nullptr, 0, nullptr);  // its checks alone
+    if (ps != K2_OK) return c->fail(ps, "layer %d: %s", l, g_init_error.c_str());
+  }
+  if (!d_workspace || reinterpret_cast<uintptr_t>(d_workspace) % 256 || ws_bytes < k2_paged_workspace_bytes())
+    return c->fail(K2_ERR_WORKSPACE, "workspace must be 256-byte aligned and hold k2_paged_workspace_bytes() = %zu bytes (got %zu)",
+                   k2_paged_workspace_bytes(), ws_bytes);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const PagedBlock pb = {layers, d_positions, d_slots, d_cu_new, d_kv_len, d_table, table_stride, requests, max_new,
+                         d_workspace, ws_bytes};
+  cudaError_t e = prefill_block(c, 0, d_tokens, tokens, 0, st, nullptr, &pb);
+  // the greedy head on each request's last new token
+  float* X = reinterpret_cast<float*>(c->ws + c->lay.px);
+  auto* xh = reinterpret_cast<__nv_bfloat16*>(c->ws + c->lay.pxh);
+  auto* xl = reinterpret_cast<__nv_bfloat16*>(c->ws + c->lay.pxl);
+  float* logits = d_logits ? d_logits : reinterpret_cast<float*>(c->ws + c->lay.plog);
+  if (!e) e = launch_last_rows(X, d_cu_new, requests, tokens, c->resid, s.H, st);
+  if (!e) e = launch_norm_rows(c->resid, requests, c->final_norm, s.wb, xh, xl, s.H, s.G, c->cfg.eps, st);
+  if (!e) {
+    const bool small = requests <= 16;
+    TcGemmArgs g = {};
+    g.N = s.V;
+    g.K = s.H;
+    g.T = requests;
+    g.ksteps = 4 * ((s.H + 255) / 256);
+    g.mode = TC_STORE;
+    g.ldo = s.V;
+    g.tile_tokens = small ? 16 : 128;
+    g.splits = 1;
+    g.out = logits;
+    g.guard = c->guard;
+    g.whole = 1;
+    e = launch_tc_gemm_sk(c->tm_lm.data(), nullptr, small ? c->tb_xh.data() : c->tm_xh.data(),
+                          small ? c->tb_xl.data() : c->tm_xl.data(), g, c->sms, st);
+  }
+  int* arg = reinterpret_cast<int*>(c->ws + c->lay.parg);
+  if (!e) e = launch_argmax_rows(logits, requests, s.V, arg, c->am_val, c->am_idx, kArgmaxPartsMax, c->guard, st);
+  if (!e) e = launch_active_next(arg, d_cu_new, requests, d_next, st);
+  if (e) return c->cuda_fail(e, "paged step");
   return K2_OK;
 }
 

@@ -218,6 +218,66 @@ __global__ void rope_append_kernel(const float* __restrict__ qkv, float* __restr
   }
 }
 
+// The same rotation for rows of many requests, each at its own position: q as fp16, k and v as fp32 rows (the paged
+// append rounds them to its block's scale)
+__global__ void rope_rows_kernel(const float* __restrict__ qkv, __half* __restrict__ q, float* __restrict__ kv,
+                                 const float2* __restrict__ rope, const int* __restrict__ positions, int nq, int nkv, int D,
+                                 int cap, unsigned* __restrict__ guard) {
+  const int t = blockIdx.x, half = D / 2;
+  int pos = positions[t];
+  if (pos < 0 || pos >= cap) {
+    if (threadIdx.x == 0) atomicOr(guard, GUARD_POS);
+    pos = 0;
+  }
+  const float* src = qkv + static_cast<size_t>(t) * (nq + 2 * nkv) * D;
+  bool range = false;
+  for (int idx = threadIdx.x; idx < (nq + 2 * nkv) * half; idx += blockDim.x) {
+    const int h = idx / half, i = idx - h * half;
+    const float2 ab = *reinterpret_cast<const float2*>(src + h * D + 2 * i);
+    float a = ab.x, b = ab.y;
+    if (h < nq + nkv) {
+      const float2 cs = rope[static_cast<size_t>(pos) * half + i];
+      a = ab.x * cs.x - ab.y * cs.y;
+      b = ab.y * cs.x + ab.x * cs.y;
+    }
+    if (h < nq) {
+      range |= !(fabsf(a) <= 65504.f) || !(fabsf(b) <= 65504.f);
+      __half* o = q + (static_cast<size_t>(t) * nq + h) * D + i;
+      o[0] = __float2half_rn(a);
+      o[half] = __float2half_rn(b);
+    } else {
+      float* o = kv + (static_cast<size_t>(t) * 2 * nkv + (h - nq)) * D + i;
+      o[0] = a;
+      o[half] = b;
+    }
+  }
+  if (range) atomicOr(guard, GUARD_RANGE);
+}
+
+__global__ void half_hilo_kernel(const __half2* __restrict__ x, __nv_bfloat162* __restrict__ oh, __nv_bfloat162* __restrict__ ol,
+                                 size_t n2) {
+  for (size_t i = static_cast<size_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < n2; i += static_cast<size_t>(gridDim.x) * blockDim.x) {
+    const float2 f = __half22float2(x[i]);
+    __nv_bfloat162 h, l;
+    split_bf16(f.x, h.x, l.x);
+    split_bf16(f.y, h.y, l.y);
+    oh[i] = h;
+    ol[i] = l;
+  }
+}
+
+__global__ void last_rows_kernel(const float* __restrict__ X, const int* __restrict__ cu, int n, float* __restrict__ out, int H) {
+  const int r = blockIdx.x, last = cu[r + 1] - 1;
+  const bool any = last >= cu[r] && last >= 0 && last < n;
+  for (int i = threadIdx.x; i < H; i += blockDim.x)
+    out[static_cast<size_t>(r) * H + i] = any ? X[static_cast<size_t>(last) * H + i] : 0.f;
+}
+
+__global__ void active_next_kernel(const int* __restrict__ arg, const int* __restrict__ cu, int requests, int* __restrict__ next) {
+  const int r = blockIdx.x * blockDim.x + threadIdx.x;
+  if (r < requests && cu[r + 1] > cu[r]) next[r] = arg[r];
+}
+
 // Causal GQA attention of a block of query tokens against the cache (which
 // already holds the block's own rows).  One CTA per (16 query tokens, KV head):
 // the 16 x REP query rows share every 64-key K/V tile; fp32 scores, online
@@ -826,6 +886,27 @@ cudaError_t launch_argmax_rows(const float* logits, int rows, int V, int* next, 
 
 cudaError_t launch_advance_by(int* seq_len, int seq, int n, cudaStream_t s) {
   advance_by_kernel<<<1, 1, 0, s>>>(seq_len, seq, n);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_rope_rows(const float* qkv, __half* q, float* kv, const float2* rope, const int* positions, int n,
+                             int nq, int nkv, int D, int cap, unsigned* guard, cudaStream_t s) {
+  rope_rows_kernel<<<n, 256, 0, s>>>(qkv, q, kv, rope, positions, nq, nkv, D, cap, guard);
+  return cudaGetLastError();
+}
+cudaError_t launch_half_hilo(const __half* x, __nv_bfloat16* oh, __nv_bfloat16* ol, size_t n, cudaStream_t s) {
+  if (n % 2) return cudaErrorInvalidValue;
+  const int grid = static_cast<int>(std::min<size_t>((n / 2 + 255) / 256, 152 * 8));
+  half_hilo_kernel<<<grid, 256, 0, s>>>(reinterpret_cast<const __half2*>(x), reinterpret_cast<__nv_bfloat162*>(oh),
+                                        reinterpret_cast<__nv_bfloat162*>(ol), n / 2);
+  return cudaGetLastError();
+}
+cudaError_t launch_last_rows(const float* X, const int* cu, int requests, int n, float* out, int H, cudaStream_t s) {
+  last_rows_kernel<<<requests, 256, 0, s>>>(X, cu, n, out, H);
+  return cudaGetLastError();
+}
+cudaError_t launch_active_next(const int* arg, const int* cu, int requests, int* next, cudaStream_t s) {
+  active_next_kernel<<<(requests + 127) / 128, 128, 0, s>>>(arg, cu, requests, next);
   return cudaGetLastError();
 }
 

@@ -120,6 +120,7 @@ def _load():
         "k2_paged_workspace_bytes": (C.c_size_t, []),
         "k2_paged_attention": (C.c_int, [vp, vp, i32, i64, vp, vp, vp, i32, i32, i32, i32, i32, C.c_float, vp, i64, vp,
                                          C.c_size_t, vp]),
+        "k2_paged_step": (C.c_int, [vp, vp, vp, vp, vp, i32, vp, vp, vp, i32, i32, i32, vp, vp, vp, C.c_size_t, vp]),
         "k2_adjust_logits": (C.c_int, [C.POINTER(LogitRules), vp, i64, vp, i64, i32, i32, vp]),
     }
     for name, (res, args) in sig.items():
@@ -136,7 +137,7 @@ EXPORTED = ("k2_workspace_bytes", "k2_init_weights", "k2_free", "k2_last_error",
             "k2_kv_state_bytes", "k2_kv_save", "k2_kv_peek", "k2_kv_load", "k2_set_sampling", "k2_sample_logits",
             "k2_philox", "k2_spec_draft", "k2_decode_speculative", "k2_quantize_fp8",
             "k2_quantize_q4", "k2_spec_logits_view", "k2_paged_plan", "k2_paged_append",
-            "k2_paged_workspace_bytes", "k2_paged_attention", "k2_adjust_logits")
+            "k2_paged_workspace_bytes", "k2_paged_attention", "k2_paged_step", "k2_adjust_logits")
 
 
 def _ptr(t):
@@ -286,6 +287,28 @@ class Context:
         self._check(LIB.k2_decode_speculative(self.ctx, seq, ids, n_ids, max_draft, out, C.byref(n),
                                               _stream(stream)))
         return list(out[:n.value])
+
+    def paged_step(self, caches, tokens, positions, slots, cu_new, kv_len, table, max_new, next_tokens, workspace,
+                   logits=None, stream=None):
+        """k2_paged_step: caches, one PagedCache per layer; tokens, positions, slots
+        [tokens], cu_new [requests + 1], kv_len and next_tokens [requests], table
+        [requests, columns] int32; logits [requests, vocab] float32 or None."""
+        dev = _device(tokens)
+        if len(caches) != self.cfg.n_layers or any(c.device != dev for c in caches):
+            raise ValueError(f"a paged step needs {self.cfg.n_layers} caches on cuda:{dev}, one per layer")
+        n, r, i32 = tokens.numel(), kv_len.numel(), torch.int32
+        for what, t, shape in (("tokens", tokens, (n,)), ("positions", positions, (n,)), ("slots", slots, (n,)),
+                               ("cu_new", cu_new, (r + 1,)), ("kv_len", kv_len, (r,)), ("table", table, (r, None)),
+                               ("next_tokens", next_tokens, (r,))):
+            _need(what, t, i32, shape, dev)
+        if logits is not None:
+            _need("logits", logits, torch.float32, (r, self.cfg.vocab), dev)
+        _need("workspace", workspace, torch.uint8, (None,), dev)
+        layers = (PagedKv * len(caches))(*[c.desc for c in caches])
+        self._check(LIB.k2_paged_step(self.ctx, layers, tokens.data_ptr(), positions.data_ptr(), slots.data_ptr(), n,
+                                      cu_new.data_ptr(), kv_len.data_ptr(), table.data_ptr(), table.size(1), r, max_new,
+                                      next_tokens.data_ptr(), _ptr(logits), workspace.data_ptr(), workspace.numel(),
+                                      _raw_stream(stream, dev)))
 
     def kv_state_bytes(self, seq, n_tokens=0):
         n = C.c_size_t()

@@ -489,7 +489,7 @@ k2_status k2_quantize_q4(const void* d_src, int32_t rows, int32_t cols, int8_t* 
  *   k2_paged_append     the step's K/V rows into the pool    (per layer)
  *   k2_paged_attention  the step's queries over it           (per layer)
  *   k2_adjust_logits    per-request rules, then k2_sample_logits
- * No context is needed; the calls allocate nothing and enqueue their work on
+ * (k2_paged_step runs the model's layers so).  But for that call no context is needed; the calls allocate nothing and enqueue their work on
  * `stream`.  They may be captured into a CUDA graph: every length is read on the
  * device.  Why a call was refused: k2_last_error(NULL).
  *
@@ -592,6 +592,27 @@ k2_status k2_paged_attention(const k2_paged_kv* kv, const void* d_q, int32_t dty
                              int32_t table_stride, int32_t requests, int32_t tokens, int32_t n_heads, int32_t max_q,
                              float scale, void* d_out, int64_t out_stride, void* d_workspace, size_t ws_bytes,
                              void* stream);
+
+/* One step of the model over such a cache: the new tokens of many requests (a
+ * decode step, prompt chunks, or both) through every layer, with their K/V
+ * appended to `layers` (host array of n_layers pools of this model's n_kv_heads and
+ * head_dim) and the greedy id after each request's last new token in d_next[r] (a
+ * request without new tokens keeps its d_next[r]).  d_positions, d_slots, d_cu_new,
+ * d_kv_len and d_table are what k2_paged_plan left; d_tokens [tokens] the ids in
+ * the same order.  Rows beyond the last token (slot -1, position 0) are carried
+ * along without effect; their ids must lie in the vocabulary.  d_logits
+ * (nullable) [requests][vocab] fp32: the logits after each request's last new
+ * token (zeros for one without), for k2_adjust_logits and k2_sample_logits.
+ * max_new: the most new tokens of one request.  The context's own sequences and
+ * cache are not touched; its scratch and the hidden views are.
+ * K2_ERR_UNSUPPORTED unless the model runs its prefill on the tensor cores with
+ * bf16 weights; K2_ERR_SHAPE for more than max_batch requests, more tokens than a
+ * prefill block (min(2048, max_context rounded up to 128)), or pools of another
+ * shape.  A position at or beyond max_context's rows raises the device guard. */
+k2_status k2_paged_step(k2_ctx* ctx, const k2_paged_kv* layers, const int32_t* d_tokens, const int32_t* d_positions,
+                        const int32_t* d_slots, int32_t tokens, const int32_t* d_cu_new, const int32_t* d_kv_len,
+                        const int32_t* d_table, int32_t table_stride, int32_t requests, int32_t max_new,
+                        int32_t* d_next, float* d_logits, void* d_workspace, size_t ws_bytes, void* stream);
 
 /* Rules on logits that differ per row (k2_set_sampling's repetition penalty is
  * one number for all rows and edits nothing it is given).  For row r of

@@ -165,3 +165,40 @@ def rules(logits, repetition=None, presence=None, frequency=None, ids=None, ids_
                 i = np.arange(vocab)
                 x[r, (mask[m].view(np.uint32)[i // 32] >> (i % 32).astype(np.uint32)) & 1 == 0] = -np.inf
     return x
+
+
+class PagedModel:
+    """An ``oracle.k2_oracle.OracleModel``'s layers over rows of many requests, with K/V in block pools of the given
+    code format (float32 rows appended, as the library rounds them) and attention over their values in float64."""
+
+    def __init__(self, model, n_blocks, block, cache):
+        s = model.s
+        self.m, self.cache = model, cache
+        shape = (n_blocks, s.n_kv_heads, block, s.head_dim)
+        self.pools = [[np.zeros(shape, np.uint8), np.zeros(shape[:2], F32), np.zeros(shape, np.uint8), np.zeros(shape[:2], F32)]
+                      for _ in range(s.n_layers)]
+
+    def step(self, tokens, positions, slots, cu, kv_len, table):
+        """Logits after each request's last new token ([requests][vocab]; zeros for a request without one)."""
+        from oracle.k2_oracle import rope_split_half, silu
+        m, s = self.m, self.m.s
+        n = int(cu[-1])
+        if n == 0:
+            return np.zeros((len(kv_len), s.vocab))
+        x = m.embed(np.asarray(tokens)[:n])
+        pos = np.asarray(positions)[:n]
+        for l, (k, ks, v, vs) in enumerate(self.pools):
+            xn = m._norm(x, m._w("attn_norm", l))
+            rows = [(xn @ m._w(w, l).T).reshape(n, -1, s.head_dim) for w in ("wq", "wk", "wv")]
+            q, kr = (rope_split_half(r, pos, s.rope_theta) for r in rows[:2])
+            append(k, ks, kr.astype(F32), slots[:n], self.cache)
+            append(v, vs, rows[2].astype(F32), slots[:n], self.cache)
+            o, _, _ = attention(q, cu, kv_len, table, k, ks, v, vs, self.cache, s.head_dim ** -0.5)
+            x = x + o.reshape(n, -1) @ m._w("wo", l).T
+            xn = m._norm(x, m._w("mlp_norm", l))
+            x = x + (silu(xn @ m._w("w_gate", l).T) * (xn @ m._w("w_up", l).T)) @ m._w("w_down", l).T
+        out = np.zeros((len(kv_len), s.vocab))
+        for r in range(len(kv_len)):
+            if cu[r + 1] > cu[r]:
+                out[r] = m.head(x[cu[r + 1] - 1:cu[r + 1]])[0]
+        return out
