@@ -52,8 +52,8 @@ __device__ __forceinline__ uint2 lds64(uint32_t a) {
 // precision while the ratio stays above 2^-28.
 constexpr int kDecWarps = 4, kDecThreads = 32 * kDecWarps;
 constexpr int kDecKeys = 32;   // of a tile: two halves of 16, which may lie in two blocks
-constexpr int kDecStart = 4;   // an item's start and end in tiles
-constexpr int kDecShare = 8;   // smallest share: fewer CTAs for small steps, and fewer parts to join
+constexpr int kDecStart = 10;  // an item's start and end in tiles (48 requests of 1 .. 32768 tokens: 62 us, 82 with 4)
+constexpr int kDecShare = 4;   // smallest share (one request of 1000 tokens: 9.0 us, 10.6 with 8, 12.1 with 16)
 constexpr int kDecMaxRows = 16;
 
 template <int D, int NT>
@@ -250,6 +250,9 @@ __global__ void __launch_bounds__(kDecThreads, Dec<D, NT>::kCtas)
     // query rows as the narrow operand: n-tile j holds rows 8j + gq, this lane their dims QW t ..
     uint32_t qf[NT][KS][2];
     float f0[NT], f1[NT];  // what turns an accumulator of rows 8j + 2t, + 1 into base-2 scores (times the K scale)
+    // int8 codes of K enter as 1152 + c (the widening without its subtraction): the accumulators of the rows start at
+    // -1152 times the row's sum.  That is about nine times a full-scale score, in fp32: far below the rounding of p.
+    float z0[NT], z1[NT];
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
       const int row = 8 * j + gq;
@@ -281,6 +284,16 @@ __global__ void __launch_bounds__(kDecThreads, Dec<D, NT>::kCtas)
       const float back = a.scale * kLog2e * ia * ib;
       f0[j] = __shfl_sync(0xffffffffu, back, 8 * t);
       f1[j] = __shfl_sync(0xffffffffu, back, 8 * t + 4);
+      z0[j] = z1[j] = 0.f;
+      if constexpr (W::kOffset != 0.f) {
+        float sum = 0.f;
+#pragma unroll
+        for (int e = 0; e < QW; ++e) sum += v[e] * sa * sb;  // (exact products)
+        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+        z0[j] = -W::kOffset * __shfl_sync(0xffffffffu, sum, 8 * t);
+        z1[j] = -W::kOffset * __shfl_sync(0xffffffffu, sum, 8 * t + 4);
+      }
     }
 
     float o[NT][MT][4], m0[NT], m1[NT], l0[NT], l1[NT], vref = 0.f, vinv = 0.f;
@@ -318,7 +331,7 @@ __global__ void __launch_bounds__(kDecThreads, Dec<D, NT>::kCtas)
 #pragma unroll
       for (int j = 0; j < NT; ++j)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) sc[j][e] = 0.f;
+        for (int e = 0; e < 8; ++e) sc[j][e] = e & 1 ? z1[j] : z0[j];
 #pragma unroll
       for (int c = 0; c < QW / 16; ++c) {
 #pragma unroll
@@ -329,8 +342,8 @@ __global__ void __launch_bounds__(kDecThreads, Dec<D, NT>::kCtas)
 #pragma unroll
           for (int w = 0; w < 4; ++w) {
             const uint32_t xa = W::prep(wa[w]), xb = W::prep(wb[w]);
-            const uint32_t af[4] = {W::template pair<false>(xa), W::template pair<false>(xb), W::template pair<true>(xa),
-                                    W::template pair<true>(xb)};
+            const uint32_t af[4] = {W::template raw<false>(xa), W::template raw<false>(xb), W::template raw<true>(xa),
+                                    W::template raw<true>(xb)};
 #pragma unroll
             for (int j = 0; j < NT; ++j) mma16816(sc[j] + 4 * h, af, qf[j][4 * c + w][0], qf[j][4 * c + w][1]);
           }
