@@ -493,6 +493,23 @@ def test_rules_match_the_oracle(k2, rows, vocab, history, n_bias, masks):
     assert torch.equal(d, out)
 
 
+@pytest.mark.parametrize("rows,vocab,history,n_bias,masks", [
+    (64, 40004, 300, 700, 5), (333, 8192, 40, 0, 2), (400, 4, 3, 50, 2), (40, 65539, 500, 30000, 3), (306, 8195, 0, 0, 1)])
+def test_rules_of_many_aligned_rows(k2, rows, vocab, history, n_bias, masks):
+    """Steps of many slices, copied ahead: rows that end inside a slice and inside a group of four, long bias lists."""
+    x, case = rules_case(rows, vocab, history, n_bias, masks, rows + vocab)
+    ld = (vocab + 7) // 4 * 4
+    d, out = torch.full((rows, ld), 3.0, device="cuda"), torch.full((rows, ld), 9.0, device="cuda")
+    d[:, :vocab] = dev(x, torch.float32)
+    given = on_device(case)
+    k2.adjust_logits(d[:, :vocab], out[:, :vocab], **given)
+    check_rules(host(out[:, :vocab]), x, case)
+    assert np.array_equal(host(d[:, :vocab]), x)
+    assert (out[:, vocab:] == 9.0).all() and (d[:, vocab:] == 3.0).all()
+    k2.adjust_logits(d[:, :vocab], **given)  # in place
+    assert torch.equal(d[:, :vocab], out[:, :vocab]) and (d[:, vocab:] == 3.0).all()
+
+
 @pytest.mark.parametrize("only", ["repetition", "presence", "frequency", "bias", "mask", "none", "ids alone"])
 def test_each_rule_alone(k2, only):
     x, case = rules_case(6, 3001, 200, 50, 6, 31)
