@@ -22,10 +22,12 @@ namespace {
 // write over its own inputs (count, lengths) are written after a barrier of
 // all CTAs, so one launch suffices.
 //
-// Bound by latency, not by bytes: one CTA does a decode step; the tokens of a
-// large step are spread over a cluster of up to 8 CTAs, whose hardware barrier
-// is what lets them share the free count without another launch.
+// Bound by latency, not by bytes.  One CTA does a decode step in one launch (64 requests: 4.9 us); the tokens of a large
+// step are spread over a CTA per 1024, each of which sums the lengths up for itself, and a second launch, which has
+// done the same meanwhile, writes what may lie over the inputs (1024 requests and 34000 tokens: 7.5 us, 13.0 in one
+// launch of a cluster of eight CTAs, whose instructions took the time).
 constexpr int kPlanThreads = 1024, kPlanPer = K2_PAGED_MAX_REQUESTS / kPlanThreads;
+constexpr int kPlanCtas = 256;  // of a large step, at most
 constexpr int kPlanCap = 1 << 30;  // sums saturate here: min(a + b, cap) is associative for a, b >= 0
 static_assert(kPlanPer * kPlanThreads == K2_PAGED_MAX_REQUESTS, "whole requests per thread");
 
@@ -49,9 +51,8 @@ struct PlanArgs {
 
 __device__ __forceinline__ int sat_add(int a, int b) { return min(a + b, kPlanCap); }
 
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
+// what a launch does: map the tokens and blocks, write the lengths, or both
+enum { kPlanMap = 1, kPlanFinish = 2 };
 
 // the r in [0, n) with sum[r] <= x < sum[r + 1]
 __device__ __forceinline__ int find_request(const int* sum, int n, int x) {
@@ -64,11 +65,13 @@ __device__ __forceinline__ int find_request(const int* sum, int n, int x) {
   return lo;
 }
 
-__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a, int ctas) {
+template <int PART>
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
   __shared__ int tok[K2_PAGED_MAX_REQUESTS + 1], take[K2_PAGED_MAX_REQUESTS + 1], give[K2_PAGED_MAX_REQUESTS + 1];
   __shared__ int cached[K2_PAGED_MAX_REQUESTS];
   __shared__ int part[3][32];
   __shared__ int reasons;
+  if (PART == kPlanMap) pdl_trigger();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, R = a.requests;
   const int mask = (1 << a.block_log2) - 1;
   auto blocks = [&](int n) { return (n >> a.block_log2) + ((n & mask) != 0); };
@@ -150,8 +153,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a, in
   if (T > a.max_tokens) bad |= K2_PLAN_TOKENS_FULL;
   __syncthreads();
 
-  const int step = ctas * kPlanThreads, first = blockIdx.x * kPlanThreads + tid;
-  if (!bad) {
+  const int step = gridDim.x * kPlanThreads, first = blockIdx.x * kPlanThreads + tid;
+  if ((PART & kPlanMap) && !bad) {
     auto returned = [&](int k) -> int {
       const int r = find_request(give, R, k);
       return a.table[static_cast<size_t>(r) * a.table_stride + (k - give[r])];
@@ -178,37 +181,38 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a, in
       a.table[static_cast<size_t>(r) * a.table_stride + blocks(cached[r]) + (k - take[r])] = popped(k);
     }
     for (int k = first; k < given - taken; k += step) a.free_ids[F + k] = returned(k);
-  } else {
+  } else if (PART & kPlanMap) {
     for (int t = first; t < a.max_tokens; t += step) {
       a.slots[t] = -1;
       a.positions[t] = 0;
     }
   }
-  // kv_len may be cached and free_count_out free_count: written once every CTA has read them
-  int keep[kPlanPer];
+  if constexpr ((PART & kPlanFinish) != 0) {
+    // kv_len may be cached and free_count_out free_count: written once everything has read them
+    int keep[kPlanPer];
 #pragma unroll
-  for (int i = 0; i < kPlanPer; ++i) {
-    const int r = tid * kPlanPer + i;
-    keep[i] = r < R && !bad ? (a.fresh[r] < 0 ? 0 : cached[r] + a.fresh[r]) : r < R ? max(cached[r], 0) : 0;
-  }
-  if (ctas > 1) cluster_sync();
-  else __syncthreads();
-  if (blockIdx.x != 0) return;
-#pragma unroll
-  for (int i = 0; i < kPlanPer; ++i) {
-    const int r = tid * kPlanPer + i;
-    if (r < R) {
-      a.kv_len[r] = keep[i];
-      a.cu_new[r] = bad ? 0 : tok[r];
+    for (int i = 0; i < kPlanPer; ++i) {
+      const int r = tid * kPlanPer + i;
+      keep[i] = r < R && !bad ? (a.fresh[r] < 0 ? 0 : cached[r] + a.fresh[r]) : r < R ? max(cached[r], 0) : 0;
     }
-  }
-  if (tid == 0) {
-    a.cu_new[R] = bad ? 0 : T;
-    *a.free_count_out = bad ? F : static_cast<int>(top - taken);
-    a.status[0] = bad ? 0 : T;
-    a.status[1] = taken;
-    a.status[2] = given;
-    a.status[3] = bad;
+    if (PART == kPlanFinish) pdl_wait();
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kPlanPer; ++i) {
+      const int r = tid * kPlanPer + i;
+      if (r < R) {
+        a.kv_len[r] = keep[i];
+        a.cu_new[r] = bad ? 0 : tok[r];
+      }
+    }
+    if (tid == 0) {
+      a.cu_new[R] = bad ? 0 : T;
+      *a.free_count_out = bad ? F : static_cast<int>(top - taken);
+      a.status[0] = bad ? 0 : T;
+      a.status[1] = taken;
+      a.status[2] = given;
+      a.status[3] = bad;
+    }
   }
 }
 
@@ -519,19 +523,25 @@ k2_status k2_paged_plan(const int32_t* d_cached, const int32_t* d_fresh, int32_t
   PlanArgs a = {d_cached, d_fresh, requests, 31 - __builtin_clz(block_tokens), d_table, table_stride, d_free,
                 free_capacity, d_free_count, d_free_count_out, d_kv_len, d_cu_new, d_slots, d_positions, max_tokens,
                 d_status};
-  int ctas = 1;
-  while (ctas < 8 && ctas * 4 * kPlanThreads < max_tokens) ctas *= 2;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas);
-  cfg.blockDim = dim3(kPlanThreads);
-  cfg.stream = static_cast<cudaStream_t>(stream);
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = ctas;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = ctas > 1 ? 1 : 0;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, plan_kernel, a, ctas);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  if (max_tokens <= kPlanThreads) {
+    plan_kernel<kPlanMap | kPlanFinish><<<1, kPlanThreads, 0, st>>>(a);
+    e = cudaGetLastError();
+  } else {
+    plan_kernel<kPlanMap><<<std::min((max_tokens - 1) / kPlanThreads + 1, kPlanCtas), kPlanThreads, 0, st>>>(a);
+    e = cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(1);
+    cfg.blockDim = dim3(kPlanThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, plan_kernel<kPlanFinish>, a);
+  }
   if (e == cudaSuccess) return K2_OK;
   set_error("plan launch: %s", cudaGetErrorString(e));
   return K2_ERR_CUDA;
