@@ -19,8 +19,7 @@ namespace {
 // blocks on top is d_free[x] below the old count F, else the (x - F)-th
 // returned block.  What the kernel writes (table entries of new blocks, stack
 // entries at or above F) is nothing that it reads, and the words that it may
-// write over its own inputs (count, lengths) are written after a barrier of
-// all CTAs, so one launch suffices.
+// write over its own inputs (count, lengths) are written once all have read them.
 //
 // Bound by latency, not by bytes.  One CTA does a decode step in one launch (64 requests: 4.9 us); the tokens of a large
 // step are spread over a CTA per 1024, each of which sums the lengths up for itself, and a second launch, which has
@@ -227,10 +226,11 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
 // where tokens are many (most of a prompt's tokens begin no run), one token where
 // they are few (every token of a decode step begins one).
 //
-// Bound by the rows' bytes (4 in and 2 out per element pair) for prompts and by
-// latency for decode steps.  The quotient x / s decides a code only through its
-// rounding, so it is taken as x * (1 / s), at most 2^-22 |x / s| off, and divided
-// only where that could change the code.
+// Bound by the rows' bytes (4 in and 2 out per element pair) for prompts, of which 8192 fp16 rows of 8 heads of 128 to
+// E4M3 move 3.4 TB/s in 15.0 us (20 with the division in line: its instructions, sixteen times over, no longer fit the
+// instruction cache; 16 with four CTAs per SM, 17 with 8 rows per warp), and by latency for decode steps (64 rows: 3.0 us).  The
+// quotient x / s decides a code only through its rounding, so it is taken as x * (1 / s), at most 2^-22 |x / s| off, and
+// divided, in a second pass, only where that could change the code.
 template <typename T, int E>
 struct RowBits;  // E neighbouring elements of a row, as loaded
 template <>
@@ -303,30 +303,35 @@ __device__ __forceinline__ uint32_t exact_codes(const float* f, float s) {
   for (int e = 0; e < E; ++e) u |= quantize<C>(f[e], s) << (8 * e);
   return u;
 }
-// Codes of E finite elements under scale s, inv = 1 / s; the whole warp takes part.
+// Codes of E finite elements under a scale of reciprocal inv; `unsure` if a quotient by the scale might have another code.
 template <typename C, int E>
-__device__ __forceinline__ uint32_t fast_codes(const float* f, float s, float inv) {
+__device__ __forceinline__ uint32_t fast_codes(const float* f, float inv, bool& unsure) {
   uint32_t u = 0;
-  bool unsure = false;
+  if constexpr (std::is_same<C, CodeI8>::value) {
+    // |y| <= 127 (1 + 2^-22).  Added to 1.5 2^23 it is rounded to an integer, whose low byte is the code; y is within
+    // 2^-15 of the quotient, so only one that near a midpoint can round the other way.
+    float far = 0.f;
 #pragma unroll
-  for (int e = 0; e < E; e += 2) {
-    const f32x2 y = mul2(pk2(f[e], f[e + 1]), pk2(inv, inv));
-    if constexpr (std::is_same<C, CodeI8>::value) {
-      // |y| <= 127 (1 + 2^-22).  Added to 1.5 2^23 it is rounded to an integer, whose low byte is the code; y is within
-      // 2^-15 of the quotient, so only one that near a midpoint can round the other way.
-      const f32x2 magic = pk2(12582912.f, 12582912.f), r = add2(y, magic);
-      const float2 d = parts(add2(y, mul2(add2(r, pk2(-12582912.f, -12582912.f)), pk2(-1.f, -1.f)))), t = parts(r);
-      unsure |= fabsf(d.x) > 0.4999f || fabsf(d.y) > 0.4999f;
-      u |= __byte_perm(__float_as_uint(t.x), __float_as_uint(t.y), 0x0040) << (8 * e) & (0xFFFFu << (8 * e));
-    } else {
-      // the quotient lies between y (1 - 2^-20) and y (1 + 2^-20): the same code for both is its code
-      const uint32_t lo = e4m3x2(mul2(y, pk2(1.f - 9.5367432e-7f, 1.f - 9.5367432e-7f)));
-      const uint32_t hi = e4m3x2(mul2(y, pk2(1.f + 9.5367432e-7f, 1.f + 9.5367432e-7f)));
-      unsure |= lo != hi;
-      u |= lo << (8 * e);
+    for (int e = 0; e < E; e += 2) {
+      const f32x2 y = mul2(pk2(f[e], f[e + 1]), pk2(inv, inv)), r = add2(y, pk2(12582912.f, 12582912.f));
+      const float2 d = parts(fma2(add2(r, pk2(-12582912.f, -12582912.f)), pk2(-1.f, -1.f), y)), t = parts(r);
+      far = fmaxf(far, fmaxf(fabsf(d.x), fabsf(d.y)));
+      u |= (__byte_perm(__float_as_uint(t.x), __float_as_uint(t.y), 0x0040) & 0xFFFFu) << (8 * e);
     }
+    unsure = far > 0.4999f;
+  } else {
+    // the quotient lies between the products with inv (1 - 2^-20) and inv (1 + 2^-20): the same code for both is its code
+    const float a = inv * (1.f - 9.5367432e-7f), b = inv * (1.f + 9.5367432e-7f);
+    uint32_t hi = 0;
+#pragma unroll
+    for (int e = 0; e < E; e += 2) {
+      const f32x2 x = pk2(f[e], f[e + 1]);
+      u |= e4m3x2(mul2(x, pk2(a, a))) << (8 * e);
+      hi |= e4m3x2(mul2(x, pk2(b, b))) << (8 * e);
+    }
+    unsure = u != hi;
   }
-  return __any_sync(0xffffffffu, unsure) ? exact_codes<C, E>(f, s) : u;
+  return u;
 }
 
 constexpr int kAppendThreads = 256, kRunRows = 16;  // rows of a run that one warp takes
@@ -458,13 +463,25 @@ __global__ void __launch_bounds__(kAppendThreads, sizeof(T) == 4 ? 2 : 3) append
     }
     odd |= !(now > 1e-30f);  // (1 / now may not be finite)
     const float inv = __frcp_rn(now);
+    Word* to = reinterpret_cast<Word*>(codes + static_cast<size_t>(o + i0) * D);
+    unsigned unsure = 0;  // this lane's rows, a bit each
 #pragma unroll
     for (int i = 0; i < kRunRows; ++i) {
       if (i0 + i >= n) break;
       float f[E];
       to_floats<T, E>(x[i], f);
-      const uint32_t u = odd ? exact_codes<C, E>(f, now) : fast_codes<C, E>(f, now, inv);
-      *reinterpret_cast<Word*>(codes + static_cast<size_t>(o + i0 + i) * D) = static_cast<Word>(u);
+      bool u;
+      to[i * (D / sizeof(Word))] = static_cast<Word>(fast_codes<C, E>(f, inv, u));
+      unsure |= static_cast<unsigned>(u) << i;
+    }
+    unsure = odd ? (1u << max(0, min(n - i0, kRunRows))) - 1 : unsure;
+#pragma unroll 1
+    while (unsure) {
+      const int i = __ffs(unsure) - 1;
+      unsure &= unsure - 1;
+      float f[E];
+      to_floats<T, E>(__ldg(reinterpret_cast<const Bits*>(src + i * stride)), f);
+      to[i * (D / sizeof(Word))] = static_cast<Word>(exact_codes<C, E>(f, now));
     }
     sync_group();  // every warp of the unit has read the old scale, and s_top
     if (wi == 0 && lane == 0) *scale = now;

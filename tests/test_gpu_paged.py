@@ -102,6 +102,16 @@ def test_a_refused_plan_changes_nothing(k2, cached, fresh, stride, blocks, max_t
     assert (got["slots"] == -1).all() and not got["cu"].any()
 
 
+def test_a_refused_large_plan_changes_nothing(k2):
+    """More tokens than one CTA maps, and a request whose table is full."""
+    cached, fresh = np.arange(40), np.full(40, 100)
+    cached[7] = 200
+    table, free, count = plan_state(cached, 13, 900, 16, 4)
+    got = check_plan(k2, cached, fresh, table, free, count, 16, 5000)
+    assert got["status"][3] == P.TABLE_FULL and np.array_equal(got["table"], table) and np.array_equal(got["free"], free)
+    assert (got["slots"] == -1).all() and not got["cu"].any()
+
+
 def test_plan_refuses_a_count_outside_the_list(k2):
     for count in (-1, 6):
         got = check_plan(k2, [0], [1], [[0]], [1, 2, 3, 4, 5], count, 16, 4)
