@@ -572,8 +572,8 @@ k2_status k2_paged_append(const k2_paged_kv* kv, const void* d_k, const void* d_
     set_error("K and V rows must be K2_BF16, K2_F16 or K2_F32 (got dtype %d)", dtype);
     return K2_ERR_UNSUPPORTED;
   }
-  if (tokens < 0) {
-    set_error("tokens must be >= 0 (got %d)", tokens);
+  if (tokens < 0 || tokens > 1 << 30) {
+    set_error("tokens must be in [0, 2^30] (got %d)", tokens);
     return K2_ERR_ARG;
   }
   if (tokens == 0) return K2_OK;
@@ -583,8 +583,7 @@ k2_status k2_paged_append(const k2_paged_kv* kv, const void* d_k, const void* d_
   }
   const int64_t row = static_cast<int64_t>(kv->n_kv_heads) * kv->head_dim;
   const int bytes = dtype == K2_F32 ? 4 : 2;
-  if ((tokens > 1 && (k_stride < row || v_stride < row)) || k_stride * bytes % 16 || v_stride * bytes % 16 ||
-      !aligned16(d_k) || !aligned16(d_v)) {
+  if ((tokens > 1 && (k_stride < row || v_stride < row || k_stride * bytes % 16 || v_stride * bytes % 16)) || !aligned16(d_k) || !aligned16(d_v)) {
     set_error("K and V rows must be 16-byte aligned and at least n_kv_heads * head_dim elements apart");
     return K2_ERR_ARG;
   }

@@ -635,8 +635,8 @@ k2_status k2_paged_attention(const k2_paged_kv* kv, const void* d_q, int32_t dty
     set_error("n_heads must be 1 to %d times n_kv_heads (got %d over %d)", kMaxRep, n_heads, kv->n_kv_heads);
     return K2_ERR_SHAPE;
   }
-  if (requests < 0 || requests > K2_PAGED_MAX_REQUESTS || tokens < 0 || max_q < 0 || table_stride < 1) {
-    set_error("requests in [0, %d], tokens and max_q >= 0, table_stride >= 1 (got %d, %d, %d, %d)",
+  if (requests < 0 || requests > K2_PAGED_MAX_REQUESTS || tokens < 0 || tokens > 1 << 30 || max_q < 0 || table_stride < 1) {
+    set_error("requests in [0, %d], tokens in [0, 2^30], max_q >= 0, table_stride >= 1 (got %d, %d, %d, %d)",
               K2_PAGED_MAX_REQUESTS, requests, tokens, max_q, table_stride);
     return K2_ERR_SHAPE;
   }
@@ -650,7 +650,7 @@ k2_status k2_paged_attention(const k2_paged_kv* kv, const void* d_q, int32_t dty
     return K2_ERR_ARG;
   }
   const int64_t row = static_cast<int64_t>(n_heads) * kv->head_dim;
-  if ((tokens > 1 && (q_stride < row || out_stride < row)) || q_stride % 8 || out_stride % 8 || !aligned16(d_q) ||
+  if ((tokens > 1 && (q_stride < row || out_stride < row || q_stride % 8 || out_stride % 8)) || !aligned16(d_q) ||
       !aligned16(d_out)) {
     set_error("query and output rows must be 16-byte aligned and at least n_heads * head_dim elements apart");
     return K2_ERR_ARG;
@@ -659,6 +659,10 @@ k2_status k2_paged_attention(const k2_paged_kv* kv, const void* d_q, int32_t dty
     set_error("workspace must be 256-byte aligned and hold k2_paged_workspace_bytes() = %zu bytes (got %zu)",
               k2_paged_workspace_bytes(), ws_bytes);
     return K2_ERR_WORKSPACE;
+  }
+  if (d_q == d_out) {  // a request's queries are read by several CTAs, some after another has stored its rows
+    set_error("the output may not lie over the queries");
+    return K2_ERR_ARG;
   }
   int dev = 0;
   const int sms = sm_count(&dev);

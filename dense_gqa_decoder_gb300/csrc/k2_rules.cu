@@ -6,9 +6,9 @@
 // token history into shared memory, a cell per id: the answer's occurrences, and a top bit for ids of the prompt; so the
 // counts are exact whatever the order of the atomics, and a cell of zero means that no penalty touches the id.  Then the
 // slice streams through registers.  Every slice reads its row's whole history, so slices are as large as still gives
-// every SM three of them.  64 rows of 250624 with up to 8192 tokens and 300 biases each take 32 us, 4.1 TB/s (44 with
+// every SM three of them.  64 rows of 250624 with up to 8192 tokens and 300 biases each take 33 us, 4.0 TB/s (44 with
 // slices of 8192 held in registers, 52 with those staged in shared memory by bulk copies; a prefetch of the slice to L2
-// changes nothing); 256 rows 111 us, 4.7 TB/s; one row, where every step of the way there is a latency, 4.1 us.
+// changes nothing); 256 rows 116 us, 4.5 TB/s; one row, where every step of the way there is a latency, 4.1 us.
 //
 // Biases are few.  The thread that finds the first entry of an id in the slice works that id out by itself, all its
 // entries in list order, so that an id listed twice gives the same sum every time; it stores the result after the slice.
@@ -97,11 +97,10 @@ __device__ __forceinline__ void count_ids(unsigned* words, const int* ids, const
   for (i += threadIdx.x; i < w.len; i += kThreads) count(__ldg(ids + i), i);
 }
 
-// The penalties of an id whose cell is c (not zero).  The quotient by the repetition penalty is a product with its
-// reciprocal, one rounding more: it decides nothing but a few logits' last bits.
+// The penalties of an id whose cell is c (not zero).
 template <typename Cell>
-__device__ __forceinline__ float penalised(const Row& w, float inv, bool repeats, unsigned c, float v) {
-  if (repeats) v *= v > 0.f ? inv : w.rep;
+__device__ __forceinline__ float penalised(const Row& w, bool repeats, unsigned c, float v) {
+  if (repeats) v = v > 0.f ? __fdiv_rn(v, w.rep) : v * w.rep;
   const unsigned times = c & Cells<Cell>::kCount;
   if (times) v = __fsub_rn(__fsub_rn(v, __fmul_rn(w.freq, static_cast<float>(times))), w.pres);
   return v;
@@ -164,7 +163,6 @@ __global__ void __launch_bounds__(kThreads, kCtas)
   const bool counted = u.repetition != nullptr || u.presence != nullptr || u.frequency != nullptr;
   const bool repeats = u.repetition != nullptr;
   const Row w = row_of(u, r, counted);
-  const float inv = 1.f / w.rep;
   auto allowed = [&](int at) { return w.mask == nullptr || ((__ldg(w.mask + ((v0 + at) >> 5)) >> ((v0 + at) & 31)) & 1u); };
 
   if (counted) {
@@ -183,7 +181,7 @@ __global__ void __launch_bounds__(kThreads, kCtas)
       mine = allowed(my_at);
       my_value = x[my_at];
       const unsigned c = counted ? C::get(words, my_at) : 0u;
-      if (c) my_value = penalised<Cell>(w, inv, repeats, c, my_value);
+      if (c) my_value = penalised<Cell>(w, repeats, c, my_value);
       mine = add_biases(b_id, b_val, tid, listed, my_value) && mine;
     }
     __syncthreads();  // in place, x before the slice's stores
@@ -215,10 +213,10 @@ __global__ void __launch_bounds__(kThreads, kCtas)
             c0 = c.x, c1 = c.y, c2 = c.z, c3 = c.w;
           }
           if (c0 | c1 | c2 | c3) {
-            if (c0) f[j].x = penalised<Cell>(w, inv, repeats, c0, f[j].x);
-            if (c1) f[j].y = penalised<Cell>(w, inv, repeats, c1, f[j].y);
-            if (c2) f[j].z = penalised<Cell>(w, inv, repeats, c2, f[j].z);
-            if (c3) f[j].w = penalised<Cell>(w, inv, repeats, c3, f[j].w);
+            if (c0) f[j].x = penalised<Cell>(w, repeats, c0, f[j].x);
+            if (c1) f[j].y = penalised<Cell>(w, repeats, c1, f[j].y);
+            if (c2) f[j].z = penalised<Cell>(w, repeats, c2, f[j].z);
+            if (c3) f[j].w = penalised<Cell>(w, repeats, c3, f[j].w);
           }
         }
         if (!(bits[j] & 1u)) f[j].x = -INFINITY;
@@ -242,7 +240,7 @@ __global__ void __launch_bounds__(kThreads, kCtas)
         const int at = base + j * kThreads;
         if (at >= n) break;
         const unsigned c = counted ? C::get(words, at) : 0u;
-        if (c) f[j] = penalised<Cell>(w, inv, repeats, c, f[j]);
+        if (c) f[j] = penalised<Cell>(w, repeats, c, f[j]);
         y[at] = allowed(at) ? f[j] : -INFINITY;
       }
     }
@@ -320,8 +318,8 @@ extern "C" k2_status k2_adjust_logits(const k2_logit_rules* u, const float* d_lo
     set_error("penalties need the rows' token ids");
     return K2_ERR_ARG;
   }
-  if (u->ids && (!u->ids_len || u->ids_stride < 0)) {
-    set_error("ids need ids_len and ids_stride >= 0");
+  if (u->ids && (!u->ids_len || u->ids_stride < 0 || u->ids_stride > 1 << 30)) {
+    set_error("ids need ids_len and ids_stride 0 .. 2^30");
     return K2_ERR_ARG;
   }
   if (u->bias_offset && (!u->bias_ids || !u->bias || u->n_bias < 0 || u->n_bias > 1 << 30)) {

@@ -583,8 +583,8 @@ size_t k2_paged_workspace_bytes(void);
  * are the last of its d_kv_len[r] positions, so query i of n sees keys
  * 0 .. kv_len - n + i (already appended).  Query heads n_heads / n_kv_heads
  * (1 .. 16) share a KV head.  d_out is written like d_q (out_stride); rows of no
- * request are left as they were, a query that sees no key gets zeros.  max_q:
- * the most queries of one request.  Scores scale * q.k and the softmax are held
+ * request are left as they were, a query that sees no key gets zeros.  d_out may
+ * not lie over d_q.  max_q: the most queries of one request.  Scores scale * q.k and the softmax are held
  * in fp32; codes and queries enter the products exactly, probabilities as
  * fp16. */
 k2_status k2_paged_attention(const k2_paged_kv* kv, const void* d_q, int32_t dtype, int64_t q_stride,
@@ -627,13 +627,14 @@ k2_status k2_paged_step(k2_ctx* ctx, const k2_paged_kv* layers, const int32_t* d
  *      0 (whatever the value was); no mask if mask_row[r] is outside [0, n_masks).
  * Ids outside [0, vocab) are ignored.  NULL arrays switch a rule off (prompt_len
  * NULL: everything is the answer; mask_row NULL: row r uses mask r).  A row whose
- * mask leaves nothing is all -inf: k2_sample_logits then raises its guard. */
+ * mask leaves nothing is all -inf: k2_sample_logits then raises its guard.
+ * Up to 65535 rows and a vocabulary of up to 2^30. */
 typedef struct {
   const float* repetition; /* [rows] > 0; nullable */
   const float* presence;   /* [rows]; nullable */
   const float* frequency;  /* [rows]; nullable */
   const int32_t* ids;      /* [rows][ids_stride]; nullable with the three above */
-  int64_t ids_stride;
+  int64_t ids_stride;      /* up to 2^30 */
   const int32_t* ids_len;    /* [rows] */
   const int32_t* prompt_len; /* [rows]; nullable */
   const int32_t* bias_offset; /* [rows + 1]; nullable: no biases */

@@ -347,6 +347,73 @@ def test_attention_strided_rows(k2):
     assert (wide[:, 8] == 7.0).all()
 
 
+def test_one_row_of_any_stride(k2):
+    """The distance between tokens is of no account where there is one."""
+    c, table, cu, kv_len, q = attention_case(k2, [(40, 1)], 16, 8, 2, 128, "i8", "bf16", 19)
+    one = q[:1].as_strided((1, 8, 128), (3, 128, 1))
+    out = torch.full_like(one, 7.0).as_strided((1, 8, 128), (5, 128, 1))
+    check_attention(k2, c, table, cu, kv_len, one, "i8", "bf16", out=out)
+    k = torch.randn(1, 2, 128, device="cuda")
+    again = new_pool(k2, c.n_blocks, 16, 2, 128, "i8", 20)
+    other = new_pool(k2, c.n_blocks, 16, 2, 128, "i8", 20)
+    k2.paged_append(again, k.as_strided((1, 2, 128), (7, 128, 1)), k, dev([16]))
+    k2.paged_append(other, k, k, dev([16]))
+    assert np.array_equal(raw(again.k), raw(other.k)) and torch.equal(again.k_scale, other.k_scale)
+
+
+def test_a_replayed_mixed_step(k2):
+    """Plan, append and attention captured once, for more tokens than a plan's CTA maps, and replayed as requests grow,
+    end and begin again, against the same calls made eagerly on buffers of their own."""
+    requests, block, heads, kv_heads, dim, most, columns = 5, 32, 8, 2, 64, 1100, 70
+    blocks = 200
+    i32 = dict(dtype=torch.int32, device="cuda")
+
+    def buffers():
+        z = lambda *n: torch.zeros(*n, **i32)  # noqa: E731
+        return dict(cached=z(requests), fresh=z(requests), table=torch.full((requests, columns), -1, **i32),
+                    free=torch.arange(blocks, **i32), count=torch.full((1,), blocks, **i32), cu=z(requests + 1),
+                    slots=z(most), positions=z(most), status=z(4), cache=k2.PagedCache(blocks, block, kv_heads, dim, "f8"),
+                    ws=k2.paged_workspace(), q=torch.zeros(most, heads, dim, dtype=torch.float16, device="cuda"),
+                    kv=torch.zeros(most, 2 * kv_heads, dim, dtype=torch.float16, device="cuda"),
+                    out=torch.zeros(most, heads, dim, dtype=torch.float16, device="cuda"))
+
+    def step(b):
+        k2.paged_plan(b["cached"], b["fresh"], b["table"], b["free"], b["count"], block, kv_len=b["cached"], cu_new=b["cu"],
+                      slots=b["slots"], positions=b["positions"], status=b["status"])
+        k2.paged_append(b["cache"], b["kv"][:, :kv_heads], b["kv"][:, kv_heads:], b["slots"])
+        k2.paged_attention(b["cache"], b["q"], b["out"], b["cu"], b["cached"], b["table"], 900, b["ws"])
+
+    mine, eager = buffers(), buffers()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        step(mine)  # (nothing to do: every length is 0)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            step(mine)
+    side.synchronize()
+    gen = torch.Generator("cuda").manual_seed(4)
+    for fresh in ([900, 3, 0, 70, 100], [1, 1, 1, 1, 1], [1, 40, 800, -1, 0], [-1, 1, 1, 33, 900], [0, 0, 0, 0, 0], [2, 5, 1, 1, -1]):
+        q = torch.randn(most, heads, dim, device="cuda", generator=gen).half()
+        kv = torch.randn(most, 2 * kv_heads, dim, device="cuda", generator=gen).half()
+        for b in (mine, eager):
+            b["fresh"].copy_(dev(fresh))
+            b["q"].copy_(q)
+            b["kv"].copy_(kv)
+            b["out"].fill_(7.0)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            graph.replay()
+        side.synchronize()
+        step(eager)
+        torch.cuda.synchronize()
+        assert int(mine["status"][3]) == 0
+        for n in ("cached", "table", "count", "cu", "slots", "positions", "status", "out"):
+            assert torch.equal(mine[n], eager[n]), (n, fresh)
+        assert np.array_equal(raw(mine["cache"].k), raw(eager["cache"].k))
+        tokens = sum(max(f, 0) for f in fresh)
+        assert (mine["out"][tokens:] == 7.0).all() and not int(mine["cache"].flags)
+
+
 def test_attention_is_the_same_every_time(k2):
     """Splits of a long context are joined in one order, whoever finishes last; the workspace is left clean."""
     pairs = [(6000, 1), (300, 2), (2048, 200)]
@@ -543,6 +610,19 @@ def test_rules_on_strided_rows_that_are_not_16_byte_aligned(k2):
     assert (out[:, :3] == 9.0).all() and (out[:, 1004:] == 9.0).all()
     k2.adjust_logits(wide[:, 7:1008], **on_device(case))
     assert torch.equal(wide[:, 7:1008], out[:, 3:1004]) and (wide[:, :7] == 3.0).all() and (wide[:, 1008:] == 3.0).all()
+
+
+def test_rules_divide_by_any_positive_repetition(k2):
+    """Quotients and products round once, for penalties whose reciprocal is not a normal number too."""
+    rep = np.array([1e-39, 3e38, 3.0, 1.1], np.float32)
+    x = np.array([[1e-3, -1e-3, 7.0, -7.0, 0.0, 30.0, -0.0, 11.0]] * 4, np.float32)
+    ids = np.tile(np.arange(7), (4, 1))
+    d = dev(x, torch.float32)
+    k2.adjust_logits(d, repetition=dev(rep, torch.float32), ids=dev(ids), ids_len=dev([7] * 4))
+    with np.errstate(over="ignore"):
+        want = np.where(x > 0, x / rep[:, None], x * rep[:, None])
+    want[:, 7] = x[:, 7]
+    assert np.array_equal(host(d), want)
 
 
 def test_rules_edge_values(k2):

@@ -106,6 +106,22 @@ def test_rules_refusals(k2):
     assert call(rows=0, x=None, y=None) == k2.K2_OK
 
 
+def test_further_refusals(k2):
+    """Counts that 32-bit indices could not pass, and an output over the queries."""
+    ref = C.addressof(pool(k2))
+    assert k2.LIB.k2_paged_append(ref, A, A, k2.K2_BF16, 256, 256, A, 2 ** 30 + 1, None) == k2.K2_ERR_ARG
+
+    def attend(tokens, out):
+        return k2.LIB.k2_paged_attention(ref, A, k2.K2_F16, 1024, A, A, A, 4, 1, tokens, 8, 1, 0.1, out, 1024, A, 1 << 30, None)
+    assert attend(2 ** 30 + 1, 2 * A) == k2.K2_ERR_SHAPE
+    assert attend(2, A) == k2.K2_ERR_ARG
+    assert "queries" in k2.LIB.k2_last_error(None).decode()
+    for kw, vocab in ((dict(ids=A, ids_len=A, ids_stride=2 ** 30 + 1), 40), (dict(), 2 ** 30 + 1),
+                      (dict(bias_offset=A, bias_ids=A, bias=A, n_bias=2 ** 30 + 1), 40)):
+        u = k2.LogitRules(**kw)
+        assert k2.LIB.k2_adjust_logits(C.byref(u), A, vocab, A + 4096, vocab, 2, vocab, None) == k2.K2_ERR_ARG, kw
+
+
 # ---- the oracle ------------------------------------------------------------------------------
 
 def test_plan_oracle_hands_out_and_takes_back_every_block_once():
