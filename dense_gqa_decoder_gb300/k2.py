@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+import struct
 
 import torch
 
@@ -121,7 +122,7 @@ def _load():
         "k2_paged_attention": (C.c_int, [vp, vp, i32, i64, vp, vp, vp, i32, i32, i32, i32, i32, C.c_float, vp, i64, vp,
                                          C.c_size_t, vp]),
         "k2_paged_step": (C.c_int, [vp, vp, vp, vp, vp, i32, vp, vp, vp, i32, i32, i32, vp, vp, vp, C.c_size_t, vp]),
-        "k2_adjust_logits": (C.c_int, [C.POINTER(LogitRules), vp, i64, vp, i64, i32, i32, vp]),
+        "k2_adjust_logits": (C.c_int, [vp, vp, i64, vp, i64, i32, i32, vp]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -429,20 +430,24 @@ def _need(what, t, dtype, shape, device):
                          f"{t.dtype} {tuple(t.shape)} on {t.device}")
 
 
+# (a tensor on a CUDA device says that CUDA has been set up, which torch.cuda.current_device() checks every time)
+_current_device, _current_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+
+
 # The checks below run before every call of a serving loop, so they are written out with the cheapest tensor
 # accessors (16 us of checks and marshalling per plan became 8); what fails one goes to _need, which says why.
 def _device(t):
     """The call's device index: that of `t`, which has to be the current one (the
     C calls launch there)."""
     d = t.get_device()
-    if d < 0 or d != torch.cuda.current_device():
+    if d < 0 or d != _current_device():
         raise ValueError(f"the tensors must be on the current CUDA device, got {t.device}")
     return d
 
 
 def _raw_stream(stream, dev):
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(dev)
+        return _current_stream(dev)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -501,11 +506,12 @@ def paged_plan(cached, fresh, table, free, free_count, block_tokens, *, kv_len, 
         if t.dtype is not i32 or t.get_device() != dev or not t.is_contiguous():
             break
     else:
-        if (cached.dim() == 1 and fresh.numel() == r and table.dim() == 2 and table.size(0) == r and
+        columns = table.shape
+        if (cached.dim() == 1 and fresh.numel() == r and len(columns) == 2 and columns[0] == r and
                 free_count.numel() == 1 and free_count_out.numel() == 1 and kv_len.numel() == r and
                 cu_new.numel() == r + 1 and positions.numel() == n and status.numel() == 4):
             st = LIB.k2_paged_plan(cached.data_ptr(), fresh.data_ptr(), r, block_tokens, table.data_ptr(),
-                                   table.size(1), free.data_ptr(), free.numel(), free_count.data_ptr(),
+                                   columns[1], free.data_ptr(), free.numel(), free_count.data_ptr(),
                                    free_count_out.data_ptr(), kv_len.data_ptr(), cu_new.data_ptr(), slots.data_ptr(),
                                    positions.data_ptr(), n, status.data_ptr(), _raw_stream(stream, dev))
             if st:
@@ -521,11 +527,12 @@ def paged_plan(cached, fresh, table, free, free_count, block_tokens, *, kv_len, 
 
 
 def _rows(what, t, dtype, heads, head_dim, device):
-    """[tokens, heads, head_dim] rows whose tokens may be apart (a slice of packed rows): their distance"""
-    if t.dtype is dtype and t.get_device() == device and t.dim() == 3 and t.size(1) == heads and t.size(2) == head_dim:
+    """[tokens, heads, head_dim] rows whose tokens may be apart (a slice of packed rows): their number and distance"""
+    if t.dtype is dtype and t.get_device() == device and t.dim() == 3:
+        n, h, d = t.shape
         token, head, one = t.stride()
-        if one == 1 and (heads == 1 or head == head_dim):
-            return token
+        if h == heads and d == head_dim and one == 1 and (heads == 1 or head == head_dim):
+            return n, token
     raise ValueError(f"{what} must be [tokens, {heads}, {head_dim}] {dtype} rows on cuda:{device}, each row contiguous, "
                      f"got {t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
 
@@ -539,11 +546,10 @@ def paged_append(cache, k, v, slots, stream=None):
     dtype = _ROW_DTYPES.get(k.dtype)
     if dtype is None:
         raise ValueError(f"k and v must be float32, bfloat16 or float16, got {k.dtype}")
-    ks = _rows("k", k, k.dtype, cache.n_kv_heads, cache.head_dim, dev)
-    vs = _rows("v", v, k.dtype, cache.n_kv_heads, cache.head_dim, dev)
-    n = k.size(0)
-    if v.size(0) != n:
-        raise ValueError(f"k has {n} rows, v {v.size(0)}")
+    n, ks = _rows("k", k, k.dtype, cache.n_kv_heads, cache.head_dim, dev)
+    m, vs = _rows("v", v, k.dtype, cache.n_kv_heads, cache.head_dim, dev)
+    if m != n:
+        raise ValueError(f"k has {n} rows, v {m}")
     if slots.dtype is not torch.int32 or slots.get_device() != dev or slots.numel() != n or not slots.is_contiguous():
         _need("slots", slots, torch.int32, (n,), dev)
     st = LIB.k2_paged_append(cache._ref, k.data_ptr(), v.data_ptr(), dtype, ks, vs, slots.data_ptr(), n,
@@ -568,21 +574,21 @@ def paged_attention(cache, q, out, cu_q, kv_len, table, max_q, workspace, scale=
     dtype = q.dtype
     if dtype is not torch.bfloat16 and dtype is not torch.float16:
         raise ValueError(f"q must be bfloat16 or float16, got {dtype}")
-    heads, d = (q.size(1) if q.dim() == 3 else 0), cache.head_dim
-    qs = _rows("q", q, dtype, heads, d, dev)
-    os_ = _rows("out", out, dtype, heads, d, dev)
-    n = q.size(0)
-    if out.size(0) != n:
-        raise ValueError(f"q has {n} rows, out {out.size(0)}")
+    heads, d = (q.shape[1] if q.dim() == 3 else 0), cache.head_dim
+    n, qs = _rows("q", q, dtype, heads, d, dev)
+    m, os_ = _rows("out", out, dtype, heads, d, dev)
+    if m != n:
+        raise ValueError(f"q has {n} rows, out {m}")
     r, i32 = kv_len.numel(), torch.int32
     for t in (cu_q, kv_len, table):
         if t.dtype is not i32 or t.get_device() != dev or not t.is_contiguous():
             break
     else:
-        if (cu_q.numel() == r + 1 and table.dim() == 2 and table.size(0) == r and workspace.dtype is torch.uint8 and
+        columns = table.shape
+        if (cu_q.numel() == r + 1 and len(columns) == 2 and columns[0] == r and workspace.dtype is torch.uint8 and
                 workspace.get_device() == dev and workspace.is_contiguous()):
             st = LIB.k2_paged_attention(cache._ref, q.data_ptr(), _ROW_DTYPES[dtype], qs, cu_q.data_ptr(),
-                                        kv_len.data_ptr(), table.data_ptr(), table.size(1), r, n, heads, max_q,
+                                        kv_len.data_ptr(), table.data_ptr(), columns[1], r, n, heads, max_q,
                                         d ** -0.5 if scale is None else scale, out.data_ptr(), os_,
                                         workspace.data_ptr(), workspace.numel(), _raw_stream(stream, dev))
             if st:
@@ -593,6 +599,9 @@ def paged_attention(cache, q, out, cu_q, kv_len, table, max_q, workspace, scale=
     _need("table", table, i32, (r, None), dev)
     _need("workspace", workspace, torch.uint8, (None,), dev)
     raise ValueError("attention: tensors of another shape than the call's")
+
+
+_RULES = struct.Struct("@PPPPqPPPPPiPqiP").pack  # a LogitRules, in a fifth of its constructor's time
 
 
 def adjust_logits(logits, out=None, *, repetition=None, presence=None, frequency=None, ids=None, ids_len=None,
@@ -606,50 +615,72 @@ def adjust_logits(logits, out=None, *, repetition=None, presence=None, frequency
         out = logits
     f32, i32 = torch.float32, torch.int32
     rows, vocab = logits.shape if logits.dim() == 2 else (0, 0)
-    for what, t in (("logits", logits), ("out", out)):
-        if t.dtype is not f32 or t.get_device() != dev or t.dim() != 2 or t.size(0) != rows or t.size(1) != vocab or \
-                t.stride(1) != 1:
-            raise ValueError(f"{what} must be [rows, vocab] float32 rows on cuda:{dev}, got {t.dtype} {tuple(t.shape)} "
-                             f"on {t.device}")
+    ld, one = logits.stride() if logits.dim() == 2 else (0, 0)
+    ld_out, one_out = (ld, one) if out is logits else out.stride() if out.dim() == 2 else (0, 0)
+    if logits.dtype is not f32 or one != 1 or out is not logits and (
+            out.dtype is not f32 or out.get_device() != dev or one_out != 1 or out.shape != logits.shape):
+        raise ValueError(f"logits and out must be [rows, vocab] float32 rows on cuda:{dev}, got {logits.dtype} "
+                         f"{tuple(logits.shape)} and {out.dtype} {tuple(out.shape)} on {out.device}")
 
-    def row(what, t, dtype, n=rows):  # the address of a value per row
-        if t is None:
-            return None
-        if t.dtype is not dtype or t.get_device() != dev or t.numel() != n or not t.is_contiguous():
-            _need(what, t, dtype, (n,), dev)
-        return t.data_ptr()
-    rep, pres, freq = row("repetition", repetition, f32), row("presence", presence, f32), row("frequency", frequency, f32)
+    def fault(t, dtype, n):  # of a value per row
+        return t.dtype is not dtype or t.get_device() != dev or t.numel() != n or not t.is_contiguous()
+    rep = pres = freq = 0
+    if repetition is not None:
+        if fault(repetition, f32, rows):
+            _need("repetition", repetition, f32, (rows,), dev)
+        rep = repetition.data_ptr()
+    if presence is not None:
+        if fault(presence, f32, rows):
+            _need("presence", presence, f32, (rows,), dev)
+        pres = presence.data_ptr()
+    if frequency is not None:
+        if fault(frequency, f32, rows):
+            _need("frequency", frequency, f32, (rows,), dev)
+        freq = frequency.data_ptr()
     id_ptr = id_stride = id_len = id_prompt = 0
     if ids is not None:
-        if ids.dtype is not i32 or ids.get_device() != dev or ids.dim() != 2 or ids.size(0) != rows or \
+        shape = ids.shape
+        if ids.dtype is not i32 or ids.get_device() != dev or len(shape) != 2 or shape[0] != rows or \
                 not ids.is_contiguous():
             _need("ids", ids, i32, (rows, None), dev)
         if ids_len is None:
             raise ValueError("ids need ids_len")
-        id_len, id_prompt = row("ids_len", ids_len, i32), row("prompt_len", prompt_len, i32)
-        if ids.numel():
-            id_ptr, id_stride = ids.data_ptr(), ids.size(1)
-        else:  # no row holds a token: nothing to penalise
-            rep = pres = freq = id_len = id_prompt = None
+        if fault(ids_len, i32, rows):
+            _need("ids_len", ids_len, i32, (rows,), dev)
+        if prompt_len is not None:
+            if fault(prompt_len, i32, rows):
+                _need("prompt_len", prompt_len, i32, (rows,), dev)
+            id_prompt = prompt_len.data_ptr()
+        id_ptr, id_stride, id_len = ids.data_ptr(), shape[1], ids_len.data_ptr()
+        if not rows * id_stride:  # no row holds a token: nothing to penalise
+            rep = pres = freq = id_ptr = id_stride = id_len = id_prompt = 0
     b_off = b_ids = b_val = n_bias = 0
     if bias is not None:
         offset, bias_ids, values = bias
-        b_off, n_bias = row("bias offsets", offset, i32, rows + 1), bias_ids.numel()
-        b_ids, b_val = row("bias ids", bias_ids, i32, n_bias), row("bias values", values, f32, n_bias)
-        if not n_bias:
-            b_off = 0
+        n_bias = bias_ids.numel()
+        if fault(offset, i32, rows + 1):
+            _need("bias offsets", offset, i32, (rows + 1,), dev)
+        if fault(bias_ids, i32, n_bias):
+            _need("bias ids", bias_ids, i32, (n_bias,), dev)
+        if fault(values, f32, n_bias):
+            _need("bias values", values, f32, (n_bias,), dev)
+        if n_bias:
+            b_off, b_ids, b_val = offset.data_ptr(), bias_ids.data_ptr(), values.data_ptr()
     m_ptr = m_stride = n_masks = m_row = 0
     if mask is not None:
-        _need("mask", mask, i32, (None, None), dev)
+        if mask.dtype is not i32 or mask.get_device() != dev or mask.dim() != 2 or not mask.is_contiguous():
+            _need("mask", mask, i32, (None, None), dev)
         m_ptr, (n_masks, m_stride) = mask.data_ptr(), mask.shape
         if m_stride < (vocab + 31) // 32 or (mask_row is None and n_masks < rows):
             raise ValueError(f"mask must have {(vocab + 31) // 32} words for each of its rows (and a row for each of the "
                              f"logits without mask_row), got {tuple(mask.shape)}")
-        m_row = row("mask_row", mask_row, i32)
-    u = LogitRules(rep or None, pres or None, freq or None, id_ptr or None, id_stride, id_len or None, id_prompt or None,
-                   b_off or None, b_ids or None, b_val or None, n_bias, m_ptr or None, m_stride, n_masks, m_row or None)
-    st = LIB.k2_adjust_logits(C.byref(u), logits.data_ptr(), logits.stride(0), out.data_ptr(), out.stride(0), rows, vocab,
-                              _raw_stream(stream, dev))
+        if mask_row is not None:
+            if fault(mask_row, i32, rows):
+                _need("mask_row", mask_row, i32, (rows,), dev)
+            m_row = mask_row.data_ptr()
+    u = _RULES(rep, pres, freq, id_ptr, id_stride, id_len, id_prompt, b_off, b_ids, b_val, n_bias, m_ptr, m_stride, n_masks,
+               m_row)
+    st = LIB.k2_adjust_logits(u, logits.data_ptr(), ld, out.data_ptr(), ld_out, rows, vocab, _raw_stream(stream, dev))
     if st:
         _call(st)
 

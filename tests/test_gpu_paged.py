@@ -361,6 +361,26 @@ def test_one_row_of_any_stride(k2):
     assert np.array_equal(raw(again.k), raw(other.k)) and torch.equal(again.k_scale, other.k_scale)
 
 
+def test_two_streams_at_once(k2):
+    """Calls that overlap, each with a workspace of its own, give what they give alone."""
+    runs = []
+    for seed, pairs in ((23, [(9000, 1), (40, 1), (2500, 150)]), (24, [(7000, 2), (1, 70), (3000, 1)])):
+        c, table, cu, kv_len, q = attention_case(k2, pairs, 16, 8, 2, 128, "i8", "f16", seed)
+        ws = k2.paged_workspace()
+        args = (c, q, torch.zeros_like(q), dev(cu), dev(kv_len), dev(table), 150, ws)
+        k2.paged_attention(*args)
+        runs.append((args, args[2].clone(), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for args, _, stream in runs:
+            args[2].zero_()
+            stream.wait_stream(torch.cuda.current_stream())
+            k2.paged_attention(*args, stream=stream)
+        for args, want, stream in runs:
+            torch.cuda.current_stream().wait_stream(stream)
+            assert torch.equal(args[2], want)
+
+
 def test_a_replayed_mixed_step(k2):
     """Plan, append and attention captured once, for more tokens than a plan's CTA maps, and replayed as requests grow,
     end and begin again, against the same calls made eagerly on buffers of their own."""

@@ -122,6 +122,14 @@ def test_further_refusals(k2):
         assert k2.LIB.k2_adjust_logits(C.byref(u), A, vocab, A + 4096, vocab, 2, vocab, None) == k2.K2_ERR_ARG, kw
 
 
+def test_packed_rules_are_the_structure(k2):
+    """adjust_logits hands the call a packed k2_logit_rules: field by field what ctypes lays out."""
+    values = [(7 * i + 3) << (20 if dict(k2.LogitRules._fields_)[n] is not C.c_int32 else 0)
+              for i, (n, _) in enumerate(k2.LogitRules._fields_)]
+    u = k2.LogitRules.from_buffer_copy(k2._RULES(*values).ljust(C.sizeof(k2.LogitRules), b"\0"))
+    assert [getattr(u, n) for n, _ in k2.LogitRules._fields_] == values
+
+
 # ---- the oracle ------------------------------------------------------------------------------
 
 def test_plan_oracle_hands_out_and_takes_back_every_block_once():
