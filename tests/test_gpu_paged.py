@@ -361,6 +361,22 @@ def test_one_row_of_any_stride(k2):
     assert np.array_equal(raw(again.k), raw(other.k)) and torch.equal(again.k_scale, other.k_scale)
 
 
+@pytest.mark.parametrize("pairs,block,heads,kv_heads,dim,cache,kind", [
+    ([(40, 1), (0, 1), (300, 2)], 16, 128, 128, 64, "i8", "bf16"), ([(40, 30), (17, 1)], 32, 128, 128, 64, "f8", "f16"),
+    ([(33, 1), (5, 3)], 16, 256, 16, 128, "i8", "f16"), ([(20, 1)] * 2047 + [(100, 1)], 16, 4, 1, 64, "f8", "bf16"),
+    ([(3, 1), (0, 0)] * 1023 + [(70, 40)], 128, 4, 2, 64, "i8", "f16"), ([(0, 2)] * 700, 16, 16, 1, 128, "f8", "f16")])
+def test_attention_of_many_heads_and_requests(k2, pairs, block, heads, kv_heads, dim, cache, kind):
+    c, table, cu, kv_len, q = attention_case(k2, pairs, block, heads, kv_heads, dim, cache, kind, 29)
+    check_attention(k2, c, table, cu, kv_len, q, cache, kind)
+    assert int(c.flags) == 0
+
+
+def test_append_of_many_heads(k2):
+    c = new_pool(k2, 6, 32, 128, 64, "f8", 30)
+    x = torch.randn(50, 128, 64, device="cuda", dtype=torch.bfloat16)
+    check_append(k2, c, "f8", x, x.flip(0), slots_of([(2, 5, 20), (0, 0, 30)], 32))
+
+
 def test_two_streams_at_once(k2):
     """Calls that overlap, each with a workspace of its own, give what they give alone."""
     runs = []
