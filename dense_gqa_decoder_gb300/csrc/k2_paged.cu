@@ -227,7 +227,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
 // they are few (every token of a decode step begins one).
 //
 // Bound by the rows' bytes (4 in and 2 out per element pair) for prompts, of which 8192 fp16 rows of 8 heads of 128 to
-// E4M3 move 3.4 TB/s in 15.0 us (20 with the division in line: its instructions, sixteen times over, no longer fit the
+// E4M3 move 3.4 TB/s in 14.7 us (20 with the division in line: its instructions, sixteen times over, no longer fit the
 // instruction cache; 16 with four CTAs per SM, 17 with 8 rows per warp), and by latency for decode steps (64 rows: 3.0 us).  The
 // quotient x / s decides a code only through its rounding, so it is taken as x * (1 / s), at most 2^-22 |x / s| off, and
 // divided, in a second pass, only where that could change the code.
@@ -368,15 +368,23 @@ __global__ void __launch_bounds__(kAppendThreads, sizeof(T) == 4 ? 2 : 3) append
   const int tl = t0 + lane;
   const bool inside = lane < a.window && tl < a.tokens;
   const int mine = inside ? __ldg(a.slots + tl) : -1, prior = inside && tl > 0 ? __ldg(a.slots + tl - 1) : -1;
+  const int ta = t0 + a.window + lane;  // 32 tokens behind the window, whose slots are on their way with the window's
+  const int ahead = ta < a.tokens ? __ldg(a.slots + ta) : -1;
+  const int last = __shfl_sync(0xffffffffu, mine, a.window - 1), up = __shfl_up_sync(0xffffffffu, ahead, 1);
   if (mine >= limit && unit == 0) raise_flag(p.flags, K2_PAGED_BAD_SLOT);
-  unsigned starts = __ballot_sync(0xffffffffu, mine >= 0 && mine < limit && !((mine & bmask) != 0 && prior == mine - 1));
+  // bit i: token t0 + i continues the run of the token before
+  const bool goes_on = (mine & bmask) != 0 && prior == mine - 1;
+  const unsigned long long on = __ballot_sync(0xffffffffu, inside && mine >= 0 && goes_on) |
+                                static_cast<unsigned long long>(__ballot_sync(0xffffffffu, ahead > 0 && (ahead & bmask) != 0 && (lane ? up : last) == ahead - 1))
+                                    << a.window;
+  unsigned starts = __ballot_sync(0xffffffffu, mine >= 0 && mine < limit && !goes_on);
   const long long stride = is_v ? a.v_stride : a.k_stride;
   while (starts) {
     const int first = __ffs(starts) - 1;
     starts &= starts - 1;
     const int t = t0 + first, slot = __shfl_sync(0xffffffffu, mine, first), o = slot & bmask;
-    int n = 1;
-    for (bool more = true; more;) {
+    int n = __ffsll(static_cast<long long>(~(on >> first >> 1)));  // a run of n tokens: n - 1 that go on
+    for (bool more = first + n == a.window + 32; more;) {
       const int i = n + lane;
       const bool same = o + i < B && t + i < a.tokens && __ldg(a.slots + t + i) == slot + i;
       const unsigned m = __ballot_sync(0xffffffffu, same);
