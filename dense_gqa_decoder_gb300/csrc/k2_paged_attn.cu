@@ -48,8 +48,10 @@ __device__ __forceinline__ uint2 lds64(uint32_t a) {
 //
 // Query rows are scaled by a power of two to fp16's upper range (exact for bf16
 // and fp16 inputs); probabilities p enter P.V as fp16(p * (vs / vref) * 2^14), vs
-// the block's V scale and vref the largest so far, so that no block's scale costs
-// precision while the ratio stays above 2^-28.
+// the block's V scale and vref the power of two below the largest so far (2^-126 at
+// least), so that no block's scale costs precision while the ratio stays above 2^-28.
+// vref, 1 / vref and 2^14 are exact normal factors, applied one after another: 2^14 / vref
+// itself may not be finite.
 //
 // 16 requests of 8192 tokens, 32 heads of 128 over 8: 50 us, 5.4 TB/s (79 % of a copy's rate) from int8 codes; 48 requests
 // of 1 .. 32768 in E4M3: 60 us, 5.7 TB/s.  What is left is each CTA's start (lengths, table, first tiles) and the join.
@@ -355,10 +357,11 @@ __global__ void __launch_bounds__(kDecThreads, Dec<D, NT>::kCtas)
       // V: the reference scale, and what each half's probabilities are multiplied with
       const float av = fmaxf(fabsf(v_s[0]), fabsf(v_s[1]));
       float shrink = 1.f;
-      if (av > vref) {
-        shrink = vref * __frcp_rn(av);
-        vref = av;
-        vinv = __frcp_rn(av) * 16384.f;
+      if (av >= 2.f * vref && av > 0.f) {
+        const float now = __uint_as_float(max(__float_as_uint(av) & 0x7f800000u, 0x00800000u));
+        vinv = __frcp_rn(now);
+        shrink = vref * vinv;
+        vref = now;
       }
       const int key = (first + kDecWarps * i) * kDecKeys;
       // some row does not see all of the tile, or a half is missing
@@ -413,7 +416,7 @@ __global__ void __launch_bounds__(kDecThreads, Dec<D, NT>::kCtas)
         l1[j] += (s[1] + s[3]) + (s[5] + s[7]);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const float pv = v_s[h] * vinv;
+          const float pv = v_s[h] * vinv * 16384.f;
           pf[j][2 * h] = movmatrix(pack_half2(s[4 * h] * pv, s[4 * h + 1] * pv));
           pf[j][2 * h + 1] = movmatrix(pack_half2(s[4 * h + 2] * pv, s[4 * h + 3] * pv));
         }

@@ -1,0 +1,71 @@
+"""The paged operators at the ends of what they accept: block scales of any size.  Against
+the plain oracle (oracle/k2_paged.py), with the bounds of test_gpu_paged.py and the terms stated here."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import k2_paged as P
+from test_gpu_paged import attention_case, bound, dev, host, raw
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def k2():
+    from dense_gqa_decoder_gb300 import k2 as mod
+    return mod
+
+
+def attend(k2, c, table, cu, kv_len, q, max_q=None, workspace=None, scale=None):
+    out = torch.full_like(q, 7.0)
+    k2.paged_attention(c, q, out, dev(cu), dev(kv_len), dev(table), int(np.diff(cu).max()) if max_q is None else max_q,
+                       k2.paged_workspace() if workspace is None else workspace, scale=scale)
+    return out
+
+
+def oracle(c, table, cu, kv_len, q, cache, scale=None):
+    return P.attention(host(q.float()), cu, kv_len, table, raw(c.k), host(c.k_scale), raw(c.v), host(c.v_scale), cache,
+                       c.head_dim ** -0.5 if scale is None else scale)
+
+
+def check(k2, c, table, cu, kv_len, q, cache, kind, **kw):
+    """Every row within its bound, those of no request untouched.  bf16 outputs below 2^-126 have a step of 2^-133, of
+    which half is lost, and fp32 numbers below it one of 2^-149: the products with the scale and 1 / sum and the joins
+    lose less than 2^-140 by that."""
+    got = host(attend(k2, c, table, cu, kv_len, q, **kw).float()).astype(np.float64)
+    want, mass, score = oracle(c, table, cu, kv_len, q, cache)
+    rows = ~np.isnan(want[:, 0, 0])
+    assert (got[~rows] == 7.0).all()
+    vmax = float(np.nanmax(host(c.v_scale).astype(np.float64))) * (127 if cache == "i8" else 448)
+    room = bound(want, mass, score, int(max(kv_len)), c.head_dim, kind, vmax) + 2.0 ** -134 + 2.0 ** -140
+    assert np.isfinite(got[rows]).all()
+    worst = (np.abs(got - want) / room)[rows].max()
+    assert worst <= 1.0, float(worst)
+
+
+FEW = [[(90, 1), (40, 1), (700, 1)], [(70, 3), (33, 2)]]
+TINY = [1e-45, 1e-40, 1e-36, 4e-35, 1e-30]
+
+
+def check_v_scales(k2, pairs, cache, kind, size):
+    """All V scales about `size`, then blocks of that size before, behind and between blocks of scale about 1."""
+    c, table, cu, kv_len, q = attention_case(k2, pairs, 16, 8, 2, 128, cache, kind, 41)
+    usual = torch.where(torch.isnan(c.v_scale), 1.0, c.v_scale * 100.0)
+    small = (usual.double() * size).clamp(min=1.5e-45).float()
+    blocks = -(-int(kv_len[0]) // 16)
+    first = torch.tensor(table[:, 0].copy(), device="cuda").long()
+    last = torch.tensor([table[r, -(-int(n) // 16) - 1] for r, n in enumerate(kv_len)], device="cuda").long()
+    odd = torch.tensor(np.unique(table[:, 1:blocks:2][table[:, 1:blocks:2] >= 0]), device="cuda").long()
+    c.v_scale.copy_(small)
+    check(k2, c, table, cu, kv_len, q, cache, kind)
+    for where in (first, last, odd):
+        c.v_scale.copy_(usual)
+        c.v_scale[where] = small[where]
+        check(k2, c, table, cu, kv_len, q, cache, kind)
+
+
+@pytest.mark.parametrize("size", TINY)
+@pytest.mark.parametrize("cache,kind", [("i8", "bf16"), ("f8", "f16"), ("i8", "f16"), ("f8", "bf16")])
+@pytest.mark.parametrize("pairs", FEW)
+def test_few_rows_under_v_scales_of_any_size(k2, pairs, cache, kind, size):
+    check_v_scales(k2, pairs, cache, kind, size)
