@@ -485,8 +485,9 @@ __global__ void __launch_bounds__(kChThreads, 1)
         const bool valid = static_cast<unsigned>(id) < static_cast<unsigned>(p.n_blocks);
         if (!valid && id != -2 && lane < 8) raise_flag(p.flags, K2_PAGED_BAD_BLOCK);
         if (scales) {
-          // a scale of (as good as) zero counts as 2^-60
-          const float up = __log2f(vref > 0.f ? fmaxf(__fdividef(v_s, vref), 8.6736174e-19f) : 8.6736174e-19f) + kUp;
+          // a scale of (as good as) zero counts as 2^-60; divided exactly, for vref may lie below (or near the end of) the
+          // range of normal numbers
+          const float up = __log2f(vref > 0.f ? fmaxf(__fdiv_rn(v_s, vref), 8.6736174e-19f) : 8.6736174e-19f) + kUp;
           sc_k[n % kScaleTiles][quarter] = k_s;
           sc_up[n % kScaleTiles][quarter] = k_s < 0.f ? 0.f : up;
           sc_down[n % kScaleTiles][quarter] = k_s < 0.f ? 0.f : exp2_approx(-up);
@@ -665,7 +666,8 @@ __global__ void __launch_bounds__(kChThreads, 1)
     if (soft) {
       const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
       const float nan = __uint_as_float(0x7fffffffu);
-      const float unit = dead ? nan : vref * (1.f / 2048.f);  // 2^-kUp
+      // outputs are multiplied with 2^-kUp (over the row's sum), then with vref: 2^-kUp vref may not be a normal number
+      const float unit = dead ? nan : 1.f / 2048.f;
       const float inv = whole ? (l > 0.f ? unit / l : dead ? nan : 0.f) : unit;
       T* out = static_cast<T*>(a.out) + (q.q0 + tok) * a.out_stride + static_cast<size_t>(head) * D;
       const int lrow = qi * kChRows + row;
@@ -673,19 +675,20 @@ __global__ void __launch_bounds__(kChThreads, 1)
       for (int c = 0; c < D; c += 32) {
         uint32_t ov[32];
         tmem_ld32(tmem + lanes + qi * D + c, ov);
+#pragma unroll
+        for (int e = 0; e < 32; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * inv * vref);
         if (whole) {
           if (row_ok) {
 #pragma unroll
             for (int e = 0; e < 32; e += 4)
-              store4(out + c + e, __uint_as_float(ov[e]) * inv, __uint_as_float(ov[e + 1]) * inv, __uint_as_float(ov[e + 2]) * inv,
-                     __uint_as_float(ov[e + 3]) * inv);
+              store4(out + c + e, __uint_as_float(ov[e]), __uint_as_float(ov[e + 1]), __uint_as_float(ov[e + 2]),
+                     __uint_as_float(ov[e + 3]));
           }
         } else {
 #pragma unroll
           for (int e = 0; e < 32; e += 4)
             *reinterpret_cast<float4*>(part + (static_cast<size_t>((c + e) / 4) * (2 * kChRows) + lrow) * 4) =
-                make_float4(__uint_as_float(ov[e]) * inv, __uint_as_float(ov[e + 1]) * inv, __uint_as_float(ov[e + 2]) * inv,
-                            __uint_as_float(ov[e + 3]) * inv);
+                make_float4(__uint_as_float(ov[e]), __uint_as_float(ov[e + 1]), __uint_as_float(ov[e + 2]), __uint_as_float(ov[e + 3]));
         }
       }
       if (!whole) *reinterpret_cast<float2*>(part + 2 * kChRows * D + 2 * lrow) = make_float2(dead ? 0.f : m_ref, dead ? 1.f : l);

@@ -44,6 +44,7 @@ def check(k2, c, table, cu, kv_len, q, cache, kind, **kw):
 
 
 FEW = [[(90, 1), (40, 1), (700, 1)], [(70, 3), (33, 2)]]
+CHUNK = [[(100, 60), (300, 1)], [(0, 70), (500, 40)]]
 TINY = [1e-45, 1e-40, 1e-36, 4e-35, 1e-30]
 
 
@@ -68,4 +69,11 @@ def check_v_scales(k2, pairs, cache, kind, size):
 @pytest.mark.parametrize("cache,kind", [("i8", "bf16"), ("f8", "f16"), ("i8", "f16"), ("f8", "bf16")])
 @pytest.mark.parametrize("pairs", FEW)
 def test_few_rows_under_v_scales_of_any_size(k2, pairs, cache, kind, size):
+    check_v_scales(k2, pairs, cache, kind, size)
+
+
+@pytest.mark.parametrize("size", TINY)
+@pytest.mark.parametrize("cache,kind", [("i8", "bf16"), ("f8", "f16"), ("i8", "f16"), ("f8", "bf16")])
+@pytest.mark.parametrize("pairs", CHUNK)
+def test_chunks_under_v_scales_of_any_size(k2, pairs, cache, kind, size):
     check_v_scales(k2, pairs, cache, kind, size)
