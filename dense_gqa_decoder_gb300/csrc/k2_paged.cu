@@ -48,7 +48,10 @@ struct PlanArgs {
   int* status;
 };
 
-__device__ __forceinline__ int sat_add(int a, int b) { return min(a + b, kPlanCap); }
+// (two saturated sums make 2^31: added as unsigned numbers)
+__device__ __forceinline__ int sat_add(int a, int b) {
+  return static_cast<int>(min(static_cast<unsigned>(a) + static_cast<unsigned>(b), static_cast<unsigned>(kPlanCap)));
+}
 
 // what a launch does: map the tokens and blocks, write the lengths, or both
 enum { kPlanMap = 1, kPlanFinish = 2 };

@@ -1,11 +1,11 @@
-"""The paged operators at the ends of what they accept: block scales of any size.  Against
-the plain oracle (oracle/k2_paged.py), with the bounds of test_gpu_paged.py and the terms stated here."""
+"""The paged operators at the ends of what they accept: block scales of any size, token sums beyond 32
+bits.  Against the plain oracle (oracle/k2_paged.py), with the bounds of test_gpu_paged.py and the terms stated here."""
 import numpy as np
 import pytest
 import torch
 
 from oracle import k2_paged as P
-from test_gpu_paged import attention_case, bound, dev, host, raw
+from test_gpu_paged import attention_case, bound, check_plan, dev, host, plan_state, raw
 
 pytestmark = pytest.mark.gpu
 
@@ -77,3 +77,14 @@ def test_few_rows_under_v_scales_of_any_size(k2, pairs, cache, kind, size):
 @pytest.mark.parametrize("pairs", CHUNK)
 def test_chunks_under_v_scales_of_any_size(k2, pairs, cache, kind, size):
     check_v_scales(k2, pairs, cache, kind, size)
+
+
+@pytest.mark.parametrize("requests,fresh", [(2, 2 ** 30), (33, 2 ** 26), (4, 2 ** 29)])
+@pytest.mark.parametrize("max_tokens", [64, 3000])
+@pytest.mark.parametrize("enough", [False, True])
+def test_a_plan_whose_tokens_pass_31_bits_is_refused(k2, requests, fresh, max_tokens, enough):
+    """New tokens that sum to 2^31 or more although each request's fit its table, and all of them the pool."""
+    stride = fresh // 128
+    table, free, count = plan_state([0] * requests, stride, requests * stride if enough else 40, 128, 45)
+    got = check_plan(k2, [0] * requests, [fresh] * requests, table, free, count, 128, max_tokens)
+    assert got["status"][3] == P.TOKENS_FULL | (0 if enough else P.NO_BLOCKS)
