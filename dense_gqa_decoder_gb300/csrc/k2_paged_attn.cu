@@ -255,9 +255,6 @@ __global__ void __launch_bounds__(kDecThreads, Dec<D, NT>::kCtas)
     // query rows as the narrow operand: n-tile j holds rows 8j + gq, this lane their dims QW t ..
     uint32_t qf[NT][KS][2];
     float f0[NT], f1[NT];  // what turns an accumulator of rows 8j + 2t, + 1 into base-2 scores (times the K scale)
-    // int8 codes of K enter as 1152 + c (the widening without its subtraction): the accumulators of the rows start at
-    // -1152 times the row's sum.  That is about nine times a full-scale score, in fp32: far below the rounding of p.
-    float z0[NT], z1[NT];
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
       const int row = 8 * j + gq;
@@ -289,16 +286,6 @@ __global__ void __launch_bounds__(kDecThreads, Dec<D, NT>::kCtas)
       const float back = a.scale * kLog2e * ia * ib;
       f0[j] = __shfl_sync(0xffffffffu, back, 8 * t);
       f1[j] = __shfl_sync(0xffffffffu, back, 8 * t + 4);
-      z0[j] = z1[j] = 0.f;
-      if constexpr (W::kOffset != 0.f) {
-        float sum = 0.f;
-#pragma unroll
-        for (int e = 0; e < QW; ++e) sum += v[e] * sa * sb;  // (exact products)
-        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-        z0[j] = -W::kOffset * __shfl_sync(0xffffffffu, sum, 8 * t);
-        z1[j] = -W::kOffset * __shfl_sync(0xffffffffu, sum, 8 * t + 4);
-      }
     }
 
     float o[NT][MT][4], m0[NT], m1[NT], l0[NT], l1[NT], vref = 0.f, vinv = 0.f;
@@ -336,7 +323,7 @@ __global__ void __launch_bounds__(kDecThreads, Dec<D, NT>::kCtas)
 #pragma unroll
       for (int j = 0; j < NT; ++j)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) sc[j][e] = e & 1 ? z1[j] : z0[j];
+        for (int e = 0; e < 8; ++e) sc[j][e] = 0.f;
 #pragma unroll
       for (int c = 0; c < QW / 16; ++c) {
 #pragma unroll
@@ -347,8 +334,8 @@ __global__ void __launch_bounds__(kDecThreads, Dec<D, NT>::kCtas)
 #pragma unroll
           for (int w = 0; w < 4; ++w) {
             const uint32_t xa = W::prep(wa[w]), xb = W::prep(wb[w]);
-            const uint32_t af[4] = {W::template raw<false>(xa), W::template raw<false>(xb), W::template raw<true>(xa),
-                                    W::template raw<true>(xb)};
+            const uint32_t af[4] = {W::template pair<false>(xa), W::template pair<false>(xb), W::template pair<true>(xa),
+                                    W::template pair<true>(xb)};
 #pragma unroll
             for (int j = 0; j < NT; ++j) mma16816(sc[j] + 4 * h, af, qf[j][4 * c + w][0], qf[j][4 * c + w][1]);
           }

@@ -1,5 +1,6 @@
-"""The paged operators at the ends of what they accept: block scales of any size, token sums beyond 32
-bits.  Against the plain oracle (oracle/k2_paged.py), with the bounds of test_gpu_paged.py and the terms stated here."""
+"""The paged operators at the ends of what they accept: block scales of any size, one-signed queries under small
+int8 codes, token sums beyond 32 bits.  Against the plain oracle (oracle/k2_paged.py), with the bounds of
+test_gpu_paged.py and the terms stated here."""
 import numpy as np
 import pytest
 import torch
@@ -88,3 +89,25 @@ def test_a_plan_whose_tokens_pass_31_bits_is_refused(k2, requests, fresh, max_to
     table, free, count = plan_state([0] * requests, stride, requests * stride if enough else 40, 128, 45)
     got = check_plan(k2, [0] * requests, [fresh] * requests, table, free, count, 128, max_tokens)
     assert got["status"][3] == P.TOKENS_FULL | (0 if enough else P.NO_BLOCKS)
+
+
+def one_signed_case(k2, pairs, dim, kind, outlier):
+    """int8 K codes of -1, 0 and 1 under queries of one sign (or with one large dim): a query row's sum of magnitudes
+    times a full-scale code is some hundred times any of its scores."""
+    c, table, cu, kv_len, q = attention_case(k2, pairs, 16, 8, 2, dim, "i8", kind, 43)
+    rng = np.random.default_rng(44)
+    c.k.copy_(torch.from_numpy(rng.integers(-1, 2, tuple(c.k.shape)).astype(np.int8)))
+    q.copy_((q.float().abs() * 200.0).to(q.dtype))
+    if outlier:
+        q.mul_(1 / 64)
+        q[:, :, 5] = 4000.0
+    return c, table, cu, kv_len, q
+
+
+@pytest.mark.parametrize("outlier", [False, True])
+@pytest.mark.parametrize("dim,kind", [(128, "f16"), (64, "bf16"), (64, "f16"), (128, "bf16")])
+@pytest.mark.parametrize("pairs", FEW)
+def test_few_rows_of_one_signed_queries(k2, pairs, dim, kind, outlier):
+    """The scores' error follows what their own products add up to, not the largest code's: the bound's score term is
+    the sum of |q_d k_jd| over the visible keys' codes, and every code enters exactly."""
+    check(k2, *one_signed_case(k2, pairs, dim, kind, outlier), "i8", kind)
