@@ -14,9 +14,6 @@
 // The two query tiles alternate: while one's softmax runs, the other's MMAs do,
 // and S of the next key tile is issued as soon as the scores are in registers.
 //
-// int8 codes of K enter as 1152 + c (the widening without its subtraction): 1152 times the sum of the query row is
-// taken off the scores, whose fp32 accumulator it makes about nine times a full-scale score's, far below the rounding of p.
-//
 // Scales: the queries carry a power of two that brings a row into fp16's upper
 // range (exact); a block's K scale multiplies its 16 scores' common factor, and its V
 // scale enters the exponent, p' = 2^(s - m + log2(vs / vref) + 11), so neither costs
@@ -275,9 +272,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
   __shared__ __align__(8) uint64_t kv_full[ST], kv_empty[ST], code_full[kCodeTiles], code_empty[kCodeTiles], s_full[2], s_free[2], p_ready[2], o_done[2], drained[2];
   // of a tile's 16-key quarters: the K scale (-1: no keys), log2(vs / vref) + kUp and 2^- of that
   __shared__ __align__(16) float sc_k[kScaleTiles][4], sc_up[kScaleTiles][4], sc_down[kScaleTiles][4];
-  // each query row's power of two (+ 113), and what its scores' accumulators are too large by (W::kOffset times the row's sum)
-  __shared__ uint8_t s_up[2 * kChRows];
-  __shared__ float s_off[W::kOffset != 0.f ? 2 * kChRows : 1];
+  __shared__ uint8_t s_up[2 * kChRows];  // each query row's power of two (+ 113)
   __shared__ uint32_t tmem_slot;
   __shared__ int stop, s_req;
   __shared__ unsigned s_vref;
@@ -377,14 +372,6 @@ __global__ void __launch_bounds__(kChThreads, 1)
         uint32_t h[4];
 #pragma unroll
         for (int d = 0; d < 4; ++d) h[d] = pack_half2(f[2 * d] * sa * sb, f[2 * d + 1] * sa * sb);
-        if constexpr (W::kOffset != 0.f) {
-          float sum = 0.f;
-#pragma unroll
-          for (int d = 0; d < 8; ++d) sum += f[d] * sa * sb;  // (exact products)
-#pragma unroll
-          for (int o = 1; o < LR; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-          if (c == 0) s_off[e] = W::kOffset * sum;
-        }
         *reinterpret_cast<uint4*>(smem + j * S::QB + (c >> 3) * S::QA + sw128(ro, 8 * (c & 7))) = make_uint4(h[0], h[1], h[2], h[3]);
         if (c == 0) s_up[e] = static_cast<uint8_t>(up + 113);  // -113 .. 141
       }
@@ -445,8 +432,8 @@ __global__ void __launch_bounds__(kChThreads, 1)
 #pragma unroll
         for (int c = 0; c < N; ++c) {
           const uint32_t k0 = W::prep(kc[c].x), k1 = W::prep(kc[c].y), v0 = W::prep(vc[c].x), v1 = W::prep(vc[c].y);
-          *reinterpret_cast<uint4*>(kst + put[c]) = make_uint4(W::template raw<false>(k0), W::template raw<true>(k0),
-                                                               W::template raw<false>(k1), W::template raw<true>(k1));
+          *reinterpret_cast<uint4*>(kst + put[c]) = make_uint4(W::template pair<false>(k0), W::template pair<true>(k0),
+                                                               W::template pair<false>(k1), W::template pair<true>(k1));
           *reinterpret_cast<uint4*>(kst + S::KB + put[c]) = make_uint4(W::template pair<false>(v0), W::template pair<true>(v0),
                                                                        W::template pair<false>(v1), W::template pair<true>(v1));
         }
@@ -564,7 +551,6 @@ __global__ void __launch_bounds__(kChThreads, 1)
       const int up = s_up[qi * kChRows + row] - 113, ua = up / 2;
       // from accumulators to base-2 scores
       const float f_row = fabsf(a.scale) * kLog2e * __uint_as_float((127 - ua) << 23) * __uint_as_float((127 - up + ua) << 23);
-      const float q_off = W::kOffset != 0.f ? s_off[qi * kChRows + row] : 0.f;
       bool ok = true;
       for (int i = 0; i < tiles; ++i) {
         const int n = n_kv + i, m = n_q[qi] + i, st = n % ST;
@@ -590,7 +576,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
         const bool masked = __any_sync(0xffffffffu, last < kChKeys - 1) || gap;
         if (masked) {
 #pragma unroll
-          for (int e = 0; e < kChKeys; ++e) s[e] = e <= last && kk[e >> 4] >= 0.f ? (s[e] - q_off) * c1[e >> 4] : -INFINITY;
+          for (int e = 0; e < kChKeys; ++e) s[e] = e <= last && kk[e >> 4] >= 0.f ? s[e] * c1[e >> 4] : -INFINITY;
 #pragma unroll
           for (int h = 0; h < 4; ++h) c1[h] = 1.f;
         }
@@ -600,7 +586,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
           float v = max3(s[16 * h], s[16 * h + 1], s[16 * h + 2]);
 #pragma unroll
           for (int e = 3; e < 15; e += 2) v = max3(v, s[16 * h + e], s[16 * h + e + 1]);
-          mt = fmaxf(mt, (fmaxf(v, s[16 * h + 15]) - (masked ? 0.f : q_off)) * c1[h]);  // factors are >= 0
+          mt = fmaxf(mt, fmaxf(v, s[16 * h + 15]) * c1[h]);  // factors are >= 0
         }
         const bool move = mt > -INFINITY && (m_ref == -INFINITY || mt > m_ref + kLazy);
         const float alpha = move ? (m_ref == -INFINITY ? 0.f : exp2_approx(m_ref - mt)) : 1.f;
@@ -612,7 +598,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
         uint32_t pk[kChKeys / 2];
 #pragma unroll
         for (int h = 0; h < 4; ++h) {
-          const float c2 = uu[h] - zm - (masked ? 0.f : q_off * c1[h]);
+          const float c2 = uu[h] - zm;
           const f32x2 c11 = pk2(c1[h], c1[h]), c22 = pk2(c2, c2);
           f32x2 sums = pk2(0.f, 0.f);
 #pragma unroll

@@ -111,3 +111,10 @@ def test_few_rows_of_one_signed_queries(k2, pairs, dim, kind, outlier):
     """The scores' error follows what their own products add up to, not the largest code's: the bound's score term is
     the sum of |q_d k_jd| over the visible keys' codes, and every code enters exactly."""
     check(k2, *one_signed_case(k2, pairs, dim, kind, outlier), "i8", kind)
+
+
+@pytest.mark.parametrize("outlier", [False, True])
+@pytest.mark.parametrize("dim,kind", [(128, "f16"), (64, "bf16"), (64, "f16"), (128, "bf16")])
+@pytest.mark.parametrize("pairs", CHUNK)
+def test_chunks_of_one_signed_queries(k2, pairs, dim, kind, outlier):
+    check(k2, *one_signed_case(k2, pairs, dim, kind, outlier), "i8", kind)
