@@ -42,6 +42,10 @@ inline k2_status check_paged_kv(const k2_paged_kv* kv) {
     set_error("n_kv_heads must be in [1, 128] and n_blocks >= 1 (got %d, %d)", kv->n_kv_heads, kv->n_blocks);
     return K2_ERR_SHAPE;
   }
+  if (kv->wait_limit_us < 0) {
+    set_error("wait_limit_us must be >= 0 (got %d)", kv->wait_limit_us);
+    return K2_ERR_ARG;
+  }
   // slots are 32-bit numbers, and so are the kernels' places in units of 16 rows of all heads
   if (static_cast<int64_t>(kv->n_blocks) * kv->block_tokens > INT32_MAX ||
       static_cast<int64_t>(kv->n_blocks) * kv->block_tokens / 16 * kv->n_kv_heads >= UINT32_MAX) {
@@ -111,6 +115,7 @@ struct PagedAttnArgs {
   float scale;
   void* out;
   long long out_stride;
+  uint64_t wait_ns;  // the longest wait for another role of a CTA
 };
 
 template <typename T>

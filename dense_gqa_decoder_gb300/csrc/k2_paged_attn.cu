@@ -667,7 +667,8 @@ k2_status k2_paged_attention(const k2_paged_kv* kv, const void* d_q, int32_t dty
   const AttnWorkspace w = {reinterpret_cast<unsigned*>(ws), reinterpret_cast<float*>(ws + kCounterBytes)};
   const PagedPool p(*kv);
   const PagedAttnArgs a = {d_q, q_stride, d_cu_q, d_kv_len, d_table, table_stride, requests,
-                           tokens, n_heads, std::min(max_q, tokens), scale, d_out, out_stride};
+                           tokens, n_heads, std::min(max_q, tokens), scale, d_out, out_stride,
+                           kv->wait_limit_us ? 1000ull * kv->wait_limit_us : kWaitLimitNs};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int d = kv->head_dim;
   const int rep = n_heads / kv->n_kv_heads, small = small_rows_of(a, rep);

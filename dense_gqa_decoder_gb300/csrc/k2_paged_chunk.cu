@@ -125,15 +125,20 @@ __device__ __forceinline__ void tmem_ld64(uint32_t taddr, uint32_t* v) {
       : "memory");
 }
 
+// What a wait that runs out ends: its limit, and the CTA's word that says that one did
+struct Patience {
+  volatile int* stop;
+  uint64_t limit_ns;
+};
 // A wait for completion `n` (0, 1, ...) of a barrier; false once it, or another wait of the CTA, gave up
-__device__ __forceinline__ bool await(uint64_t* bar, int n, volatile int* stop) {
+__device__ __forceinline__ bool await(uint64_t* bar, int n, const Patience& w) {
   const uint32_t parity = static_cast<uint32_t>(n) & 1u;
   if (mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = globaltimer();
   while (!mbar_try_wait(bar, parity)) {
-    if (*stop) return false;
-    if (globaltimer() - t0 > kWaitLimitNs) {
-      *stop = 1;
+    if (*w.stop) return false;
+    if (globaltimer() - t0 > w.limit_ns) {
+      *w.stop = 1;
       return false;
     }
   }
@@ -256,9 +261,9 @@ struct ChunkScan {
 };
 
 // two waits whose first tries overlap (a try takes over a hundred cycles)
-__device__ __forceinline__ bool await2(uint64_t* a, int na, uint64_t* b, int nb, volatile int* stop) {
+__device__ __forceinline__ bool await2(uint64_t* a, int na, uint64_t* b, int nb, const Patience& w) {
   const bool x = mbar_try_wait(a, static_cast<uint32_t>(na) & 1u), y = mbar_try_wait(b, static_cast<uint32_t>(nb) & 1u);
-  return (x || await(a, na, stop)) && (y || await(b, nb, stop));
+  return (x || await(a, na, w)) && (y || await(b, nb, w));
 }
 
 template <typename T, typename C, int D>
@@ -278,6 +283,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
   __shared__ unsigned s_vref;
   __shared__ long long s_sum[kChThreads / 32], s_base;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const Patience patience = {&stop, a.wait_ns};
   const ChunkWork work(p, a, small_rows);
   const int rep = work.rep, QT = work.qt;
   const unsigned rep_inv = (65536u + rep - 1) / rep;  // x / rep = x * rep_inv >> 16 for x < 128 (rep <= 16)
@@ -394,6 +400,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
     }
     const float vref = __uint_as_float(s_vref);
     float m_ref = -INFINITY, l = 0.f;
+    int fetched = 0;  // key tiles of the item whose codes this warp has requested
 
     if (dead) {
     } else if (warp >= kSoftWarps && warp < kSoftWarps + kConvWarps) {
@@ -408,7 +415,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
 #pragma unroll 1
       for (int i = 0; i < tiles; ++i) {
         const int n = n_kv + i, st = n % ST, slot = n % kCodeTiles;
-        if (!__all_sync(0xffffffffu, await(&code_full[slot], n / kCodeTiles, &stop))) break;
+        if (!__all_sync(0xffffffffu, await(&code_full[slot], n / kCodeTiles, patience))) break;
         const uint8_t* cst = smem + S::OFF_CODES + slot * S::CODES + 8 * ct;
         uint2 kc[N], vc[N];
 #pragma unroll
@@ -427,7 +434,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&code_empty[slot]);
-        if (n >= ST && !__all_sync(0xffffffffu, await(&kv_empty[st], n / ST - 1, &stop))) break;
+        if (n >= ST && !__all_sync(0xffffffffu, await(&kv_empty[st], n / ST - 1, patience))) break;
         uint8_t* kst = smem + S::OFF_ST + st * 2 * S::KB;
 #pragma unroll
         for (int c = 0; c < N; ++c) {
@@ -462,13 +469,12 @@ __global__ void __launch_bounds__(kChThreads, 1)
       int id = id_of(0), id_next = id_of(1);
       float k_s, v_s, k_next, v_next;
       scales_of(id, k_s, v_s);
-      int i = 0;
 #pragma unroll 1
-      for (; i < tiles; ++i) {
+      for (int i = 0; i < tiles; ++i) {
         const int n = n_kv + i, slot = n % kCodeTiles;
         const int id_after = id_of(i + 2);
         scales_of(id_next, k_next, v_next);
-        if (n >= kCodeTiles && !__all_sync(0xffffffffu, await(&code_empty[slot], n / kCodeTiles - 1, &stop))) break;
+        if (n >= kCodeTiles && !__all_sync(0xffffffffu, await(&code_empty[slot], n / kCodeTiles - 1, patience))) break;
         const bool valid = static_cast<unsigned>(id) < static_cast<unsigned>(p.n_blocks);
         if (!valid && id != -2 && lane < 8) raise_flag(p.flags, K2_PAGED_BAD_BLOCK);
         if (scales) {
@@ -493,9 +499,8 @@ __global__ void __launch_bounds__(kChThreads, 1)
         id_next = id_after;
         k_s = k_next;
         v_s = v_next;
+        fetched = i + 1;
       }
-      if (i < tiles)  // given up: copies in flight land before the memory goes away
-        for (int n = n_kv + max(0, i - kCodeTiles); n < n_kv + i; ++n) (void)mbar_wait(&code_full[n % kCodeTiles], (n / kCodeTiles) & 1);
     } else if (warp >= kMmaWarp) {
       // ---- the MMAs of query tile j ----------------------------------------------------------------
       const int j = warp - kMmaWarp;
@@ -514,18 +519,18 @@ __global__ void __launch_bounds__(kChThreads, 1)
         bool ok = true;
         int st = n_kv % ST;
         if (j < nqt) {
-          if ((ok = await(&kv_full[st], n_kv / ST, &stop))) {
+          if ((ok = await(&kv_full[st], n_kv / ST, patience))) {
             tc_after();
             issue_s(st);
           }
           for (int i = 0; i < tiles && ok; ++i) {
             const int n = n_kv + i, m = n_q[j] + i, next = st + 1 == ST ? 0 : st + 1;
             if (i + 1 < tiles) {  // the scores of tile i are in registers: S of the next tile
-              if (!(ok = await2(&kv_full[next], (n + 1) / ST, &s_free[j], m, &stop))) break;
+              if (!(ok = await2(&kv_full[next], (n + 1) / ST, &s_free[j], m, patience))) break;
               tc_after();
               issue_s(next);
             }
-            if (!(ok = await(&p_ready[j], m, &stop))) break;
+            if (!(ok = await(&p_ready[j], m, patience))) break;
             tc_after();
             const uint64_t vs = vd + static_cast<uint64_t>(st * (2 * S::KB >> 4));
 #pragma unroll
@@ -537,11 +542,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
           }
         } else {  // no such query tile: the stages are only given back
           for (int i = 0; i < tiles && ok; ++i, st = st + 1 == ST ? 0 : st + 1)
-            if ((ok = await(&kv_full[st], (n_kv + i) / ST, &stop))) mbar_arrive(&kv_empty[st]);
-        }
-        if (!ok) {  // whatever is in flight ends before the memory goes away
-          mma_commit(&drained[j]);
-          (void)mbar_wait(&drained[j], 0);
+            if ((ok = await(&kv_full[st], (n_kv + i) / ST, patience))) mbar_arrive(&kv_empty[st]);
         }
       }
     } else if (soft) {
@@ -554,7 +555,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
       bool ok = true;
       for (int i = 0; i < tiles; ++i) {
         const int n = n_kv + i, m = n_q[qi] + i, st = n % ST;
-        ok = await2(&kv_full[st], n / ST, &s_full[qi], m, &stop);  // the tile's scales; its scores
+        ok = await2(&kv_full[st], n / ST, &s_full[qi], m, patience);  // the tile's scales; its scores
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
         const int sl = n % kScaleTiles;
         const float4 kq = *reinterpret_cast<const float4*>(sc_k[sl]), uq = *reinterpret_cast<const float4*>(sc_up[sl]),
@@ -615,7 +616,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
           l = fmaf(sum, dd[h], l);
         }
         if (i > 0) {  // the previous P.V has read P and written O
-          ok = __all_sync(0xffffffffu, await(&o_done[qi], m - 1, &stop));
+          ok = __all_sync(0xffffffffu, await(&o_done[qi], m - 1, patience));
           if (!ok) break;
           tc_after();
           if (__any_sync(0xffffffffu, move)) {
@@ -634,13 +635,23 @@ __global__ void __launch_bounds__(kChThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_ready[qi]);
       }
-      if (ok) (void)await(&o_done[qi], n_q[qi] + tiles - 1, &stop);
+      if (ok) (void)await(&o_done[qi], n_q[qi] + tiles - 1, patience);
     }
     __syncthreads();
     tc_after();
     if (stop && !dead) {
+      // given up, whoever did: the copies and MMAs that are still on their way end before their memory is left
       dead = true;
       if (tid == 0) raise_flag(p.flags, K2_PAGED_TIMEOUT);
+      if (warp == kFetchWarp) {
+        for (int n = n_kv + max(0, fetched - kCodeTiles); n < n_kv + fetched; ++n)
+          (void)mbar_wait(&code_full[n % kCodeTiles], (n / kCodeTiles) & 1);
+      } else if (warp >= kMmaWarp && elect()) {
+        mma_commit(&drained[warp - kMmaWarp]);
+        (void)mbar_wait(&drained[warp - kMmaWarp], 0);
+      }
+      __syncthreads();
+      tc_after();
     }
     n_kv += tiles;
     n_q[0] += tiles;

@@ -70,7 +70,7 @@ def sampling(temperature=0.0, top_k=0, top_p=1.0, min_p=0.0, repetition_penalty=
 class PagedKv(C.Structure):
     _fields_ = [("k", C.c_void_p), ("v", C.c_void_p), ("k_scale", C.c_void_p), ("v_scale", C.c_void_p),
                 ("n_blocks", C.c_int32), ("block_tokens", C.c_int32), ("n_kv_heads", C.c_int32),
-                ("head_dim", C.c_int32), ("dtype", C.c_int32), ("flags", C.c_void_p)]
+                ("head_dim", C.c_int32), ("dtype", C.c_int32), ("wait_limit_us", C.c_int32), ("flags", C.c_void_p)]
 
 
 class LogitRules(C.Structure):

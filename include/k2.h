@@ -506,6 +506,7 @@ typedef struct {
   int32_t n_kv_heads;
   int32_t head_dim;     /* 64 or 128 */
   int32_t dtype;        /* K2_I8: codes -127 .. 127; K2_F8: E4M3 codes */
+  int32_t wait_limit_us; /* how long a wait inside k2_paged_attention may take; 0: one second */
   uint32_t* flags;      /* device word that faults are OR-ed into (the caller clears it); nullable */
 } k2_paged_kv;
 

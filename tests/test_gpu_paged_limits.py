@@ -1,6 +1,6 @@
 """The paged operators at the ends of what they accept: block scales of any size, one-signed queries under small
-int8 codes, token sums beyond 32 bits.  Against the plain oracle (oracle/k2_paged.py), with the bounds of
-test_gpu_paged.py and the terms stated here."""
+int8 codes, token sums beyond 32 bits, attention whose waits run out.  Against the plain oracle (oracle/k2_paged.py),
+with the bounds of test_gpu_paged.py and the terms stated here."""
 import numpy as np
 import pytest
 import torch
@@ -118,3 +118,28 @@ def test_few_rows_of_one_signed_queries(k2, pairs, dim, kind, outlier):
 @pytest.mark.parametrize("pairs", CHUNK)
 def test_chunks_of_one_signed_queries(k2, pairs, dim, kind, outlier):
     check(k2, *one_signed_case(k2, pairs, dim, kind, outlier), "i8", kind)
+
+
+@pytest.mark.parametrize("pairs,block,dim,cache", [([(6000, 200), (500, 1), (0, 300)], 16, 128, "i8"),
+                                                   ([(9000, 40), (40, 500)], 64, 64, "f8")])
+def test_attention_whose_waits_run_out(k2, pairs, block, dim, cache):
+    """A wait limit of a microsecond, shorter than a key tile takes from memory to the scores: the call ends, says so, and
+    gives each head of a row whole or as NaN.  The next call on the same workspace, with time, is right."""
+    c, table, cu, kv_len, q = attention_case(k2, pairs, block, 8, 2, dim, cache, "f16", 46)
+    ws = k2.paged_workspace()
+    want, mass, score = oracle(c, table, cu, kv_len, q, cache)
+    rows = ~np.isnan(want[:, 0, 0])
+    vmax = float(np.nanmax(host(c.v_scale))) * (127 if cache == "i8" else 448)
+    room = bound(want, mass, score, int(max(kv_len)), dim, "f16", vmax)
+    c.desc.wait_limit_us = 1
+    got = host(attend(k2, c, table, cu, kv_len, q, workspace=ws).float()).astype(np.float64)
+    assert int(c.flags) == k2.K2_PAGED_TIMEOUT
+    lost = np.isnan(got).all(-1)
+    assert lost[rows].any() and not np.isnan(got[~lost]).any() and (got[~rows] == 7.0).all()
+    assert (np.abs(got - want)[rows][~lost[rows]] <= room[rows][~lost[rows]]).all()
+    for r, (_, n) in enumerate(pairs):  # single tokens wait for nobody
+        assert n > 1 or not lost[cu[r]:cu[r + 1]].any()
+    c.desc.wait_limit_us = 0
+    c.flags.zero_()
+    check(k2, c, table, cu, kv_len, q, cache, "f16", workspace=ws)
+    assert int(c.flags) == 0
