@@ -143,3 +143,35 @@ def test_attention_whose_waits_run_out(k2, pairs, block, dim, cache):
     c.flags.zero_()
     check(k2, c, table, cu, kv_len, q, cache, "f16", workspace=ws)
     assert int(c.flags) == 0
+
+
+CONTRADICTIONS = [  # new and cached tokens as given, then the call's lengths and the requests that contradict themselves
+    ([(30, 2), (30, 1)], [0, 2, 3], [1, 20], 2, {0}), ([(30, 2), (30, 1)], [0, 2, 3], [20, -4], 2, {1}),
+    ([(30, 2), (30, 1)], [0, 2, 3], [2 ** 31 - 1, 20], 2, {0}), ([(30, 2), (30, 1)], [0, 2, 900], [20, 900], 900, {1}),
+    ([(30, 2), (30, 1)], [0, 3, 2], [20, 20], 3, {1}), ([(30, 2), (30, 1)], [0, 2, 3], [20, 20], 1, {0}),
+    ([(30, 2), (30, 1)], [-1, 1, 3], [20, 20], 2, {0}),
+    ([(100, 60), (30, 1), (50, 40)], [0, 60, 61, 101], [160, 31, 39], 60, {2}),
+    ([(100, 60), (30, 1), (50, 40)], [0, 60, 61, 101], [59, 31, 90], 60, {0}),
+    ([(100, 60), (30, 1), (50, 40)], [0, 60, 61, 101], [160, 0, 90], 60, {1}),
+    ([(100, 60), (30, 1), (50, 40)], [0, 60, 61, 101], [160, 31, 90], 40, {0}),
+    ([(100, 60), (30, 1), (50, 40)], [0, 60, 61, 101], [160, 31, 2000], 60, {2})]
+
+
+@pytest.mark.parametrize("pairs,cu,kv_len,max_q,faulty", CONTRADICTIONS)
+def test_contradictory_lengths_cost_their_request_alone(k2, pairs, cu, kv_len, max_q, faulty):
+    """Zeros in the faulty requests' rows as far as they lie inside the query rows, the others' results as ever, and rows
+    of no request untouched."""
+    c, table, _, _, q = attention_case(k2, pairs, 16, 4, 1, 64, "i8", "f16", 47)
+    got = host(attend(k2, c, table, cu, kv_len, q, max_q=max_q).float()).astype(np.float64)
+    assert int(c.flags) == k2.K2_PAGED_BAD_LENGTH
+    free = np.ones(q.shape[0], bool)
+    for r in range(len(pairs)):
+        lo, hi = max(cu[r], 0), min(cu[r + 1], q.shape[0])
+        free[lo:hi] = False
+        if r in faulty:
+            assert not got[lo:hi].any(), r
+            continue
+        want, mass, score = oracle(c, table[r:r + 1], cu[r:r + 2], kv_len[r:r + 1], q, "i8")
+        room = bound(want, mass, score, kv_len[r], 64, "f16", float(np.nanmax(host(c.v_scale))) * 127)
+        assert (np.abs(got - want)[lo:hi] <= room[lo:hi]).all(), r
+    assert (got[free] == 7.0).all()
