@@ -18,6 +18,7 @@
 
 #include "../../include/k2.h"
 #include "k2_kernels.h"
+#include "k2_serve.h"
 
 using namespace k2;
 

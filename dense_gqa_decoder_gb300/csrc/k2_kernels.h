@@ -516,19 +516,4 @@ cudaError_t launch_argmax_rows(const float* logits, int rows, int V, int* next, 
                                int part_stride, unsigned* guard, cudaStream_t s, bool pdl = false);
 cudaError_t misc_init_attrs();
 
-// ---- a step over a block-paged cache (k2_prefill.cu)
-// split-half RoPE of packed QKV rows at positions[t]: q [n][nq * D] as fp16 (a value beyond its range raises
-// GUARD_RANGE), k | v [n][2 nkv * D] fp32; a position outside [0, cap) raises GUARD_POS and counts as 0
-cudaError_t launch_rope_rows(const float* qkv, __half* q, float* kv, const float2* rope, const int* positions, int n,
-                             int nq, int nkv, int D, int cap, unsigned* guard, cudaStream_t s);
-// fp16 values as bf16 hi + lo (exact)
-cudaError_t launch_half_hilo(const __half* x, __nv_bfloat16* oh, __nv_bfloat16* ol, size_t n, cudaStream_t s);
-// row r of out = row cu[r + 1] - 1 of X (n rows), zeros for a request without rows
-cudaError_t launch_last_rows(const float* X, const int* cu, int requests, int n, float* out, int H, cudaStream_t s);
-// next[r] = arg[r] for the requests with rows
-cudaError_t launch_active_next(const int* arg, const int* cu, int requests, int* next, cudaStream_t s);
-
-// The message of k2_last_error(NULL): why this thread's last call without a context was refused.
-void set_error(const char* fmt, ...);
-
 }  // namespace k2

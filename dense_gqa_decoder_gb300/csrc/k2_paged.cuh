@@ -10,7 +10,7 @@
 
 #include "../../include/k2.h"
 #include "k2_common.cuh"
-#include "k2_kernels.h"
+#include "k2_serve.h"
 
 namespace k2 {
 

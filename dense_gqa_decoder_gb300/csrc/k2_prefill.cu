@@ -16,6 +16,7 @@
 #include <utility>
 
 #include "k2_kernels.h"
+#include "k2_serve.h"
 #include "k2_common.cuh"
 
 namespace k2 {

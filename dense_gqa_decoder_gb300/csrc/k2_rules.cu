@@ -18,7 +18,7 @@
 #include <algorithm>
 #include <atomic>
 
-#include "k2_kernels.h"
+#include "k2_serve.h"
 #include "k2_common.cuh"
 #include "../../include/k2.h"
 
