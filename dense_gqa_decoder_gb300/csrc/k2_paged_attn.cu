@@ -653,7 +653,7 @@ k2_status k2_paged_attention(const k2_paged_kv* kv, const void* d_q, int32_t dty
               k2_paged_workspace_bytes(), ws_bytes);
     return K2_ERR_WORKSPACE;
   }
-  if (d_q == d_out) {  // a request's queries are read by several CTAs, some after another has stored its rows
+  if (rows_meet(d_q, 2 * q_stride, d_out, 2 * out_stride, 2 * row, tokens)) {  // a request's queries are read by several CTAs, some after another has stored its rows
     set_error("the output may not lie over the queries");
     return K2_ERR_ARG;
   }

@@ -314,6 +314,10 @@ extern "C" k2_status k2_adjust_logits(const k2_logit_rules* u, const float* d_lo
     set_error("in place, both leading dimensions must be the same");
     return K2_ERR_ARG;
   }
+  if (d_logits != d_out && rows_meet(d_logits, 4 * ld, d_out, 4 * ld_out, 4ll * vocab, rows)) {
+    set_error("the output may be the logits, but not lie over a part of them");
+    return K2_ERR_ARG;
+  }
   if ((u->repetition || u->presence || u->frequency) && !u->ids) {
     set_error("penalties need the rows' token ids");
     return K2_ERR_ARG;

@@ -6,6 +6,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stddef.h>
+#include <stdint.h>
 
 namespace k2 {
 
@@ -20,6 +21,16 @@ cudaError_t launch_half_hilo(const __half* x, __nv_bfloat16* oh, __nv_bfloat16* 
 cudaError_t launch_last_rows(const float* X, const int* cu, int requests, int n, float* out, int H, cudaStream_t s);
 // next[r] = arg[r] for the requests with rows
 cudaError_t launch_active_next(const int* arg, const int* cu, int requests, int* next, cudaStream_t s);
+
+// Whether two sets of n rows of `row` bytes, each `stride` >= row bytes apart, share a byte (slices of the same wider
+// rows need not).  Sets of different strides are compared by their first rows alone.
+inline bool rows_meet(const void* a, int64_t a_stride, const void* b, int64_t b_stride, int64_t row, int64_t n) {
+  const int64_t d = static_cast<int64_t>(reinterpret_cast<uintptr_t>(b) - reinterpret_cast<uintptr_t>(a));
+  if (n < 2 || a_stride != b_stride || a_stride < 1) return d > -row && d < row;
+  int64_t k = d / a_stride, m = d % a_stride;  // b's row 0 lies m bytes behind the start of a's row k
+  if (m < 0) m += a_stride, --k;
+  return (m < row && k > -n && k < n) || (a_stride - m < row && k + 1 > -n && k + 1 < n);
+}
 
 // The message of k2_last_error(NULL): why this thread's last call without a context was refused.
 void set_error(const char* fmt, ...);

@@ -175,3 +175,20 @@ def test_contradictory_lengths_cost_their_request_alone(k2, pairs, cu, kv_len, m
         room = bound(want, mass, score, kv_len[r], 64, "f16", float(np.nanmax(host(c.v_scale))) * 127)
         assert (np.abs(got - want)[lo:hi] <= room[lo:hi]).all(), r
     assert (got[free] == 7.0).all()
+
+
+def test_outputs_in_other_columns_of_the_inputs_rows(k2):
+    """Queries and output, logits and adjusted logits as slices of the same wider rows: nothing of the inputs is written."""
+    c, table, cu, kv_len, q = attention_case(k2, [(50, 1), (0, 70), (300, 3)], 16, 8, 2, 128, "i8", "bf16", 48)
+    both = torch.full((q.shape[0], 16, 128), 7.0, dtype=q.dtype, device="cuda")
+    both[:, :8] = q
+    k2.paged_attention(c, both[:, :8], both[:, 8:], dev(cu), dev(kv_len), dev(table), 70, k2.paged_workspace())
+    assert torch.equal(both[:, :8], q) and torch.equal(both[:, 8:], attend(k2, c, table, cu, kv_len, q))
+    x = torch.randn(5, 333, device="cuda")
+    wide = torch.zeros(5, 700, device="cuda")
+    wide[:, :333] = x
+    bias = (dev([0, 1, 2, 3, 4, 5]), dev([1, 2, 3, 4, 5]), torch.full((5,), 2.0, device="cuda"))
+    k2.adjust_logits(wide[:, :333], wide[:, 333:666], bias=bias)
+    want = x.clone()
+    want[torch.arange(5), torch.arange(1, 6)] += 2.0
+    assert torch.equal(wide[:, :333], x) and torch.equal(wide[:, 333:666], want) and not wide[:, 666:].any()
