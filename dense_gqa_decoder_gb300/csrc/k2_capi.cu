@@ -852,6 +852,7 @@ struct PagedBlock {
   int table_stride, requests, max_new;
   void* ws;
   size_t ws_bytes;
+  k2_status refused;  // what the append or the attention of a layer answered (its reason: k2_last_error(NULL))
 };
 
 // One block of n <= pchunk prompt tokens of sequence seq at positions
@@ -861,7 +862,7 @@ struct PagedBlock {
 // replayed at any position), else pos0
 // paged (nullable): a paged step's rows instead (seq, pos0 and d_pos0 are not used)
 cudaError_t prefill_block(k2_ctx* c, int seq, const int32_t* d_tokens, int n, int pos0, cudaStream_t st,
-                          const int* d_pos0 = nullptr, const PagedBlock* paged = nullptr) {
+                          const int* d_pos0 = nullptr, PagedBlock* paged = nullptr) {
   const Sizes& s = c->s;
   float* X = reinterpret_cast<float*>(c->ws + c->lay.px);
   auto* xh = reinterpret_cast<__nv_bfloat16*>(c->ws + c->lay.pxh);
@@ -1010,7 +1011,10 @@ cudaError_t prefill_block(k2_ctx* c, int seq, const int32_t* d_tokens, int n, in
         ps = k2_paged_attention(paged->layers + l, q16, K2_F16, qs, paged->cu, paged->kv_len, paged->table,
                                 paged->table_stride, paged->requests, n, s.nq, paged->max_new, scale, o16, qs, paged->ws,
                                 paged->ws_bytes, st);
-      if (ps != K2_OK && !e) e = cudaErrorInvalidValue;
+      if (ps != K2_OK && !e) {
+        paged->refused = ps;
+        e = cudaErrorUnknown;
+      }
       if (!e && !f16) e = launch_half_hilo(o16, xh, xl, static_cast<size_t>(n) * qs, st);
     } else if (!e) {
       e = launch_rope_append(qkv, Q, c->rope, kvdt, c->kc(l), c->vc(l), c->ks(l), c->vs(l), n, s.nq, s.nkv, s.d,
@@ -2181,9 +2185,10 @@ k2_status k2_paged_step(k2_ctx* c, const k2_paged_kv* layers, const int32_t* d_t
     return c->fail(K2_ERR_WORKSPACE, "workspace must be 256-byte aligned and hold k2_paged_workspace_bytes() = %zu bytes (got %zu)",
                    k2_paged_workspace_bytes(), ws_bytes);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const PagedBlock pb = {layers, d_positions, d_slots, d_cu_new, d_kv_len, d_table, table_stride, requests, max_new,
-                         d_workspace, ws_bytes};
+  PagedBlock pb = {layers, d_positions, d_slots, d_cu_new, d_kv_len, d_table, table_stride, requests, max_new,
+                   d_workspace, ws_bytes, K2_OK};
   cudaError_t e = prefill_block(c, 0, d_tokens, tokens, 0, st, nullptr, &pb);
+  if (pb.refused != K2_OK) return c->fail(pb.refused, "paged step: %s", g_init_error.c_str());
   // the greedy head on each request's last new token
   float* X = reinterpret_cast<float*>(c->ws + c->lay.px);
   auto* xh = reinterpret_cast<__nv_bfloat16*>(c->ws + c->lay.pxh);
