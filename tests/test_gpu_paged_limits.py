@@ -192,3 +192,23 @@ def test_outputs_in_other_columns_of_the_inputs_rows(k2):
     want = x.clone()
     want[torch.arange(5), torch.arange(1, 6)] += 2.0
     assert torch.equal(wide[:, :333], x) and torch.equal(wide[:, 333:666], want) and not wide[:, 666:].any()
+
+
+@pytest.mark.parametrize("kw", [dict(), dict(top_k=5), dict(top_p=0.9), dict(min_p=0.1), dict(top_k=5, top_p=0.5)])
+def test_a_row_whose_mask_leaves_nothing_raises_the_samplers_guard(k2, kw):
+    from dense_gqa_decoder_gb300 import model_io
+    import k2_inputs as ki
+    ctx, _ = model_io.build_context(ki.TINY, max_context=32, max_batch=3, kv_dtype="f32")
+    ctx.set_sampling(k2.sampling(temperature=0.7, seed=5, **kw))
+    logits = torch.randn(3, ki.TINY.vocab, device="cuda", generator=torch.Generator("cuda").manual_seed(6))
+    mask = torch.full((2, (ki.TINY.vocab + 31) // 32), -1, dtype=torch.int32, device="cuda")
+    mask[1] = 0
+    nxt = torch.full((3,), -1, dtype=torch.int32, device="cuda")
+    k2.adjust_logits(logits, mask=mask, mask_row=dev([0, 0, 0]))
+    ctx.sample_logits(logits, 3, dev([1, 2, 3]), nxt)
+    assert ctx.sync_status() == k2.K2_OK and all(0 <= t < ki.TINY.vocab for t in nxt.tolist())
+    alone = nxt.clone()
+    k2.adjust_logits(logits, mask=mask, mask_row=dev([0, 1, 0]))
+    ctx.sample_logits(logits, 3, dev([1, 2, 3]), nxt)
+    assert torch.isneginf(logits[1]).all() and ctx.sync_status() == k2.K2_ERR_DEVICE_GUARD
+    assert nxt[0] == alone[0] and nxt[2] == alone[2] and int(nxt[1]) == 0
