@@ -238,7 +238,14 @@ inline cudaError_t allow_smem(const void* kernel, int bytes, int dev, std::atomi
   return e;
 }
 
-// prompt chunks (k2_paged_chunk.cu): the requests with more than small_rows query rows
+// Prompt chunks (k2_paged_chunk.cu): the requests with more than small_rows query rows.
+//
+// The kernels of a call let their successor start before they have waited themselves (elsewhere a kernel does so only after
+// its own wait, so that whatever starts finds all but its predecessor completed).  The same holds here at the call's end:
+// the kernel for few rows is launched in plain stream order, the one for chunks and the one that joins its parts are its
+// dependents and wait for their predecessor before every exit, and the last lets nobody start early.  Between the kernel for
+// few rows and the one for chunks there is nothing to wait for: they share no output and no part of the workspace.  A plan's
+// two launches follow the same pattern.
 size_t paged_chunk_part_bytes();  // of one CTA's two parts
 cudaError_t launch_paged_chunk(const PagedPool& p, const PagedAttnArgs& a, int head_dim, int kv_dtype, int q_dtype,
                                int small_rows, float* parts, int sms, int dev, cudaStream_t s);

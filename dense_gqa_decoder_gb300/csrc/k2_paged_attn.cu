@@ -50,10 +50,12 @@ __device__ __forceinline__ uint2 lds64(uint32_t a) {
 // and fp16 inputs); probabilities p enter P.V as fp16(p * (vs / vref) * 2^14), vs
 // the block's V scale and vref the power of two below the largest so far (2^-126 at
 // least), so that no block's scale costs precision while the ratio stays above 2^-28.
+// One fp16 number each, for one MMA each: its 2^-11 is the rounding of an fp16 output and an eighth of a bf16 one's (fp16
+// outputs end up 1.1 to 1.4 times as far from the exact ones as with fp32 probabilities, bf16 outputs as far).
 // vref, 1 / vref and 2^14 are exact normal factors, applied one after another: 2^14 / vref
 // itself may not be finite.
 //
-// 16 requests of 8192 tokens, 32 heads of 128 over 8: 50 us, 5.4 TB/s (79 % of a copy's rate) from int8 codes; 48 requests
+// 16 requests of 8192 tokens, 32 heads of 128 over 8: 51 us, 5.3 TB/s (78 % of a copy's rate) from int8 codes; 48 requests
 // of 1 .. 32768 in E4M3: 60 us, 5.7 TB/s.  What is left is each CTA's start (lengths, table, first tiles) and the join.
 constexpr int kDecWarps = 4, kDecThreads = 32 * kDecWarps;
 constexpr int kDecKeys = 32;   // of a tile: two halves of 16, which may lie in two blocks
@@ -99,7 +101,7 @@ __global__ void __launch_bounds__(kDecThreads, Dec<D, NT>::kCtas)
   __shared__ int s_req, s_last;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gq = lane >> 2, t = lane & 3;
   const int rep = a.n_heads / p.n_kv;
-  pdl_trigger();  // the kernel for prompt chunks may start beside this one
+  pdl_trigger();  // a CTA of the kernel for prompt chunks may start on every SM that these CTAs have left
 
   // the tiles of every request, and this CTA's share of them
   auto tiles_of = [&](const Req& x) -> int {

@@ -20,14 +20,14 @@
 // an operation per score.  vref is the largest V scale of the CTA's keys; the row's
 // sum takes each block's p' times 2^-(log2(vs / vref) + 11).  m moves only when a
 // tile's maximum exceeds it by kLazy (then O is rescaled in tensor memory), so
-// p' <= 2^15; p' is rounded to fp16, in full precision down to 2^-14.
+// p' <= 2^15; p' is rounded to fp16, in full precision down to 2^-14 (one number, for the same reason as for few rows).
 //
 // As for single tokens, every CTA takes an equal share of the step's keys (an item =
 // request, KV head, block of query tokens; counted in keys, each with kChStart more
 // for its start and end); a kernel of its own joins the parts of an item.
 //
-// 2048 tokens of 32 heads of 128 on 8192 cached ones take 312 us, 980 TFLOP/s: the exponentials and conversions of the
-// softmax warps and the widening share the issue slots, and the tensor pipe is busy for 43 %.
+// 2048 tokens of 32 heads of 128 on 8192 cached ones take 310 us, 1000 TFLOP/s: the exponentials and conversions of the
+// softmax warps and the widening share the issue slots, and the tensor pipe is busy for 45 % of the SMs' active cycles.
 #include <math.h>
 
 #include <algorithm>
@@ -47,7 +47,7 @@ constexpr int kCodeTiles = 4;  // key tiles of codes on their way
 // tiles whose scales are kept: one is read by a softmax warp up to kCodeTiles + kChStages - 1 tiles after it was fetched
 constexpr int kScaleTiles = 8;
 static_assert(kScaleTiles >= kCodeTiles + kChStages, "scales outlive their tile");
-// An item's start and end count as 768 keys (2048 new tokens on 1 cached one: 94 us, 130 with 256; 8 requests of 512 on 512:
+// An item's start and end count as 768 keys (2048 new tokens on 1 cached one: 92 us, 130 with 256; 8 requests of 512 on 512:
 // 142 and 147; 1536 is slower again), and a CTA's share is 512 keys at least (12 requests, three with chunks of 509, heads of
 // 64: 35 us, 48 with 1024).
 constexpr int kChStart = 768, kChShare = 512;
@@ -313,7 +313,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
   const long long total = scan.total;
   const int ctas = ChunkWork::ctas(total, gridDim.x);
   if (blockIdx.x >= ctas) {
-    pdl_wait();  // this kernel started beside the one for few rows: it ends after it
+    pdl_wait();  // this kernel may have started before the one for few rows has ended: it ends after it
     return;
   }
   const Share share(total, ctas);
@@ -763,7 +763,8 @@ cudaError_t launch(const PagedPool& p, const PagedAttnArgs& a, int small_rows, f
   static std::atomic<uint64_t> ready{0};
   cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), Ch<D>::DYN, dev, ready);
   if (e != cudaSuccess) return e;
-  // beside the kernel for few rows (it lets this one start at once): they share no output, nor workspace
+  // after the kernel for few rows, SM by SM: the shared memory of its three CTAs leaves no room for one of these, so one
+  // starts where those have ended (at once where they had no work)
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(std::min(sms, kAttnMaxCtas));
   cfg.blockDim = dim3(kChThreads);

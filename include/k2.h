@@ -489,9 +489,10 @@ k2_status k2_quantize_q4(const void* d_src, int32_t rows, int32_t cols, int8_t* 
  *   k2_paged_append     the step's K/V rows into the pool    (per layer)
  *   k2_paged_attention  the step's queries over it           (per layer)
  *   k2_adjust_logits    per-request rules, then k2_sample_logits
- * (k2_paged_step runs the model's layers so).  But for that call no context is needed; the calls allocate nothing and enqueue their work on
- * `stream`.  They may be captured into a CUDA graph: every length is read on the
- * device.  Why a call was refused: k2_last_error(NULL).
+ * (k2_paged_step runs the model's layers so).  But for that call no context is
+ * needed; the calls allocate nothing and enqueue their work on `stream`.  They may
+ * be captured into a CUDA graph: every length is read on the device.  Why a call
+ * was refused: k2_last_error(NULL).
  *
  * Faults that only the device can see (a slot or block outside the pool,
  * lengths that contradict each other) are skipped, never read or written, and
@@ -500,7 +501,7 @@ typedef struct {
   void* k;         /* codes [n_blocks][n_kv_heads][block_tokens][head_dim], 16-byte aligned */
   void* v;
   float* k_scale;  /* [n_blocks][n_kv_heads], finite and >= 0 */
-  float* v_scale;
+  float* v_scale;  /* the same, and so small that the sum of a request's values is finite */
   int32_t n_blocks;
   int32_t block_tokens; /* 16, 32, 64 or 128 */
   int32_t n_kv_heads;
@@ -516,7 +517,8 @@ enum {
                               were left out */
   K2_PAGED_BAD_LENGTH = 4, /* cu_q not ascending or beyond the query rows, more queries than max_q or
                               than keys, or a length beyond the table or 2^30: the request's rows are zeros
-                              where they lie inside the query rows */
+                              where they lie inside the query rows (a row that several requests name is
+                              undefined) */
   K2_PAGED_TIMEOUT = 8     /* a bounded wait inside the attention ran out: the rows concerned are NaN */
 };
 #define K2_PAGED_MAX_REQUESTS 2048
@@ -585,9 +587,12 @@ size_t k2_paged_workspace_bytes(void);
  * 0 .. kv_len - n + i (already appended).  Query heads n_heads / n_kv_heads
  * (1 .. 16) share a KV head.  d_out is written like d_q (out_stride); rows of no
  * request are left as they were, a query that sees no key gets zeros.  d_out may
- * not lie over d_q.  max_q: the most queries of one request.  Scores scale * q.k and the softmax are held
- * in fp32; codes and queries enter the products exactly, probabilities as
- * fp16. */
+ * not lie over d_q (both may be slices of the same wider rows).  max_q: the most
+ * queries of one request.  Scores scale * q.k and the softmax are held in fp32;
+ * codes and queries enter the products exactly, probabilities as fp16 numbers in
+ * proportion to their block's V scale: in full precision (2^-11) while probability
+ * times scale stays above 2^-25 of the largest V scale among the request's keys
+ * (those behind the query's own position too), below that to 2^-36 of it. */
 k2_status k2_paged_attention(const k2_paged_kv* kv, const void* d_q, int32_t dtype, int64_t q_stride,
                              const int32_t* d_cu_q, const int32_t* d_kv_len, const int32_t* d_table,
                              int32_t table_stride, int32_t requests, int32_t tokens, int32_t n_heads, int32_t max_q,
@@ -605,7 +610,10 @@ k2_status k2_paged_attention(const k2_paged_kv* kv, const void* d_q, int32_t dty
  * (nullable) [requests][vocab] fp32: the logits after each request's last new
  * token (zeros for one without), for k2_adjust_logits and k2_sample_logits.
  * max_new: the most new tokens of one request.  The context's own sequences and
- * cache are not touched; its scratch and the hidden views are.
+ * cache are not touched; its scratch and the hidden views are.  Queries, attention
+ * probabilities and the attention's output are single fp16 numbers whatever
+ * K2_OPT_PREFILL_SPLIT says (it applies to the GEMMs' activations); a query beyond
+ * fp16's range raises the device guard.
  * K2_ERR_UNSUPPORTED unless the model runs its prefill on the tensor cores with
  * bf16 weights; K2_ERR_SHAPE for more than max_batch requests, more tokens than a
  * prefill block (min(2048, max_context rounded up to 128)), or pools of another
@@ -617,7 +625,8 @@ k2_status k2_paged_step(k2_ctx* ctx, const k2_paged_kv* layers, const int32_t* d
 
 /* Rules on logits that differ per row (k2_set_sampling's repetition penalty is
  * one number for all rows and edits nothing it is given).  For row r of
- * d_logits (fp32, ld elements apart) in this order, into d_out (may be d_logits):
+ * d_logits (fp32, ld elements apart) in this order, into d_out (d_logits itself, or
+ * memory of its own: another column range of the same wider rows too):
  *   1. an id among the row's tokens, ids[r * ids_stride .. + ids_len[r]):
  *      l -> l / repetition[r] if l > 0, l * repetition[r] otherwise;
  *   2. an id that occurs c > 0 times among the tokens from prompt_len[r] on
