@@ -105,7 +105,7 @@ __global__ void __launch_bounds__(kDecThreads, Dec<D, NT>::kCtas)
 
   // the tiles of every request, and this CTA's share of them
   auto tiles_of = [&](const Req& x) -> int {
-    return x.ok && x.nq > 0 && x.nq * rep <= small_rows ? (x.len + kDecKeys - 1) / kDecKeys : 0;
+    return x.ok && x.nq > 0 && static_cast<long long>(x.nq) * rep <= small_rows ? (x.len + kDecKeys - 1) / kDecKeys : 0;
   };
   auto units_of = [&](int tiles) -> long long { return tiles ? static_cast<long long>(tiles + kDecStart) * p.n_kv : 0; };
   const int per = (a.requests + kDecThreads - 1) / kDecThreads;
