@@ -212,3 +212,25 @@ def test_a_row_whose_mask_leaves_nothing_raises_the_samplers_guard(k2, kw):
     ctx.sample_logits(logits, 3, dev([1, 2, 3]), nxt)
     assert torch.isneginf(logits[1]).all() and ctx.sync_status() == k2.K2_ERR_DEVICE_GUARD
     assert nxt[0] == alone[0] and nxt[2] == alone[2] and int(nxt[1]) == 0
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("cache", ["i8", "f8"])
+@pytest.mark.parametrize("pairs", FEW + CHUNK)
+def test_a_query_that_is_no_number_costs_its_own_row(k2, pairs, cache, value):
+    """The head of a token whose query holds a NaN or an infinity gives NaN (zeros if that makes all its scores -inf);
+    every other one gives the same bits as without."""
+    c, table, cu, kv_len, q = attention_case(k2, pairs, 16, 8, 2, 128, cache, "bf16", 49)
+    clean = attend(k2, c, table, cu, kv_len, q)
+    bad = [(0, 1, 0), (int(cu[-1]) - 1, 6, len(pairs) - 1)]
+    for t, h, _ in bad:
+        q[t, h, 17] = value
+    got = attend(k2, c, table, cu, kv_len, q)
+    for t, h, r in bad:
+        seen = int(kv_len[r]) - (int(cu[r + 1]) - t) + 1
+        codes = np.concatenate([raw(c.k)[b, h // 4] for b in table[r, :-(-seen // 16)]])[:seen, 17]
+        with np.errstate(invalid="ignore"):
+            none = (value * P.values(codes, cache) == -np.inf).all()
+        assert not got[t, h].any() if none else torch.isnan(got[t, h]).all()
+        got[t, h] = clean[t, h]
+    assert torch.equal(got, clean)
