@@ -536,8 +536,8 @@ __global__ void __launch_bounds__(kChThreads, 1)
 #pragma unroll
             for (int e = 0; e < kChKeys / 16; ++e)
               mma_ts(to, tp + 8 * e, vs + (e * 16 * 128 >> 4), S::IDESC_O, i == 0 && e == 0 ? 0u : 1u);
-            mma_commit(&o_done[j]);
             mma_commit(&kv_empty[st]);
+            mma_commit(&o_done[j]);  // last: what waits for it has waited for the stage's release too
             st = next;
           }
         } else {  // no such query tile: the stages are only given back
