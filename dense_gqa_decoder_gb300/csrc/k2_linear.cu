@@ -1,0 +1,443 @@
+// Matrix product with an epilogue: out = act(w_scale x_scale (x . w^T) + bias) + residual, on the 5th-generation tensor
+// cores.
+//
+//   z[t][n] = sum_k x[t][k] w[n][k]      (E4M3, bf16 or fp16 operands, exact products, fp32 sums in tensor memory)
+//   out[t][n] = act(z * w_scale[n] * x_scale[t] + bias[n]) + residual[t][n]
+//
+// The weights' 128-row tiles are the first operand (M), 16 to 128 tokens the second (N): few tokens then cost few columns and
+// not 128 rows.  Both arrive as K-major rows of 128 bytes by TMA (zeros behind the last row and behind the last value of a
+// row) through a ring of stages; one thread requests, one issues the MMAs.  Where there are fewer tiles than the SMs can
+// hold, a cluster of up to eight CTAs splits K; their sums are joined through distributed shared memory in the order of K, so
+// that the result does not depend on which CTA came first.
+#include <cuda.h>
+#include <math.h>
+
+#include <algorithm>
+#include <atomic>
+
+#include "k2_common.cuh"
+#include "k2_linear.h"
+#include "k2_paged.cuh"
+#include "k2_tc.cuh"
+
+namespace k2 {
+
+namespace {
+
+constexpr int kRows = 128;      // weight rows of a tile (TMEM lanes)
+constexpr int kStepBytes = 128; // bytes of K per stage: one swizzle row
+constexpr int kMaxSplit = 8;    // CTAs of a cluster (the portable limit)
+
+template <int BN>
+struct Tile {
+  static constexpr int kA = kRows * kStepBytes, kB = BN * kStepBytes, kStage = kA + kB;
+  static constexpr int kStages = BN <= 32 ? 5 : BN == 64 ? 4 : 3;
+  static constexpr int kRing = kStages * kStage;
+  static constexpr int kPart = BN * kRows * 4;  // a CTA's sums, over the ring
+  static constexpr int kSmem = (kRing > kPart ? kRing : kPart) + 1024;
+  static constexpr int kCols = BN < 32 ? 32 : BN;
+  static constexpr uint32_t kDesc = (1u << 4) | (static_cast<uint32_t>(BN >> 3) << 17) | (8u << 24);  // fp32 sums, M = 128
+};
+
+__device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void load_2d(void* dst, const CUtensorMap* m, int c0, int c1, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+          smem_u32(dst)),
+      "l"(m), "r"(c0), "r"(c1), "r"(smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ void load_4d(void* dst, const CUtensorMap* m, int c0, int c1, int c2, int c3, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+      "[%6];" ::"r"(smem_u32(dst)),
+      "l"(m), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, unsigned long long limit_ns) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = globaltimer();
+  while (!mbar_try_wait(bar, parity))
+    if (globaltimer() - t0 > limit_ns) return false;
+  return true;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ float4 peer_load(uint32_t addr, int rank) {
+  uint32_t at;
+  float4 v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(addr), "r"(rank));
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(at)
+               : "memory");
+  return v;
+}
+
+// the activations, in fp32
+__device__ __forceinline__ float activate(float z, int act) {
+  if (act == K2_ACT_RELU) return z < 0.f ? 0.f : z;
+  if (act == K2_ACT_SILU) return z / (1.0f + expf(-z));
+  if (act == K2_ACT_GELU) return 0.5f * z * erfcf(z * -0.70710678f);
+  if (act == K2_ACT_GELU_TANH) return z / (1.0f + expf(-1.5957691216f * (z + 0.044715f * z * z * z)));
+  return z;
+}
+
+__device__ __forceinline__ float load_out(const void* p, long long i, int dtype) {
+  if (dtype == K2_F32) return static_cast<const float*>(p)[i];
+  if (dtype == K2_BF16) return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
+  return __half2float(static_cast<const __half*>(p)[i]);
+}
+__device__ __forceinline__ void store_out(void* p, long long i, int dtype, float v) {
+  if (dtype == K2_F32) static_cast<float*>(p)[i] = v;
+  else if (dtype == K2_BF16) static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
+  else static_cast<__half*>(p)[i] = __float2half_rn(v);
+}
+
+// Four neighbouring sums z of token t, rows n .. n + 3 of the matrix
+__device__ __forceinline__ void finish(const LinearArgs& a, int t, int n, float4 z4) {
+  const float xs = a.x_scale != nullptr ? __ldg(a.x_scale + t) : 1.f;
+  float z[4] = {z4.x, z4.y, z4.z, z4.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if (n + j >= a.rows) break;
+    if (a.w_scale != nullptr) z[j] = z[j] * __ldg(a.w_scale + n + j) * xs;
+    if (a.bias != nullptr) z[j] += __ldg(a.bias + n + j);
+  }
+  if (a.act == K2_ACT_SWIGLU) {
+#pragma unroll
+    for (int j = 0; j < 4; j += 2) {
+      if (n + j >= a.rows) break;
+      float y = z[j] / (1.0f + expf(-z[j])) * z[j + 1];
+      const int o = (n + j) >> 1;
+      if (a.residual != nullptr) y += load_out(a.residual, t * a.residual_stride + o, a.out_dtype);
+      store_out(a.out, t * a.out_stride + o, a.out_dtype, y);
+    }
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if (n + j >= a.rows) break;
+    float y = activate(z[j], a.act);
+    if (a.residual != nullptr) y += load_out(a.residual, t * a.residual_stride + n + j, a.out_dtype);
+    store_out(a.out, t * a.out_stride + n + j, a.out_dtype, y);
+  }
+}
+
+// where a stage's weights lie: rows apart, or packed pairs of rows in chunks of 512 bytes
+struct WeightPlace {
+  int packed;
+  int step;  // elements of K per stage
+};
+__device__ __forceinline__ void load_weights(void* dst, const CUtensorMap* m, const WeightPlace& p, int k, int row, uint64_t* bar) {
+  const int e = k * p.step;
+  if (p.packed) load_4d(dst, m, e & 511, 0, e >> 9, row >> 1, bar);
+  else load_4d(dst, m, e, row, 0, 0, bar);
+}
+
+template <int BN, bool F8>
+__global__ void __launch_bounds__(128) linear_kernel(const __grid_constant__ CUtensorMap map_w,
+                                                     const __grid_constant__ CUtensorMap map_x, const LinearArgs a,
+                                                     const WeightPlace place, int steps, int split) {
+  using C = Tile<BN>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  __shared__ __align__(8) uint64_t full[C::kStages], empty[C::kStages], done;
+  __shared__ uint32_t tmem_slot;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tile = blockIdx.x / split, rank = blockIdx.x - tile * split;
+  const int n0 = tile * kRows, t0 = blockIdx.y * BN;
+  const int k0 = static_cast<int>(static_cast<long long>(steps) * rank / split);
+  const int nk = static_cast<int>(static_cast<long long>(steps) * (rank + 1) / split) - k0;
+  if (tid == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(&done, 1);
+    fence_mbar_init();
+  }
+  if (warp == 0) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_slot)), "r"(C::kCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_before();
+  __syncthreads();
+  tc_after();
+  const uint32_t tmem = tmem_slot;
+  bool ok = true;
+  if (tid == 0) {
+    int i = 0;
+    for (; i < nk; ++i) {
+      const int s = i % C::kStages;
+      if (i >= C::kStages && !wait_for(&empty[s], static_cast<uint32_t>(i / C::kStages - 1) & 1u, a.limit_ns)) {
+        ok = false;
+        break;
+      }
+      uint8_t* st = smem + s * C::kStage;
+      mbar_arrive_expect_tx(&full[s], C::kStage);
+      load_weights(st, &map_w, place, k0 + i, n0, &full[s]);
+      load_2d(st + C::kA, &map_x, (k0 + i) * place.step, t0, &full[s]);
+    }
+    // no copy may be on its way when the ring becomes the place of the sums
+    for (int j = max(0, i - C::kStages); j < i; ++j) mbar_wait(&full[j % C::kStages], static_cast<uint32_t>(j / C::kStages) & 1u);
+  } else if (tid == 32) {
+    const uint32_t idesc = C::kDesc | (a.dtype == K2_BF16 ? (1u << 7) | (1u << 10) : 0u);
+    for (int i = 0; i < nk; ++i) {
+      const int s = i % C::kStages;
+      if (!wait_for(&full[s], static_cast<uint32_t>(i / C::kStages) & 1u, a.limit_ns)) {
+        ok = false;
+        break;
+      }
+      tc_after();
+      const uint8_t* st = smem + s * C::kStage;
+#pragma unroll
+      for (int j = 0; j < kStepBytes / 32; ++j) {
+        const uint64_t ad = smem_desc(st + j * 32), bd = smem_desc(st + C::kA + j * 32);
+        if (F8) mma_f8(tmem, ad, bd, idesc, (i | j) != 0);
+        else mma(tmem, ad, bd, idesc, (i | j) != 0);
+      }
+      mma_commit(&empty[s]);
+    }
+    mma_commit(&done);
+  }
+  __syncthreads();  // both roles have ended: what is waited for now are the MMAs that were issued
+  ok = mbar_wait(&done, 0) && ok;
+  ok = __syncthreads_and(ok);
+  tc_after();
+  if (!ok && tid == 0 && a.flags != nullptr) atomicOr(a.flags, a.bit);
+  // the sums as [token][row]: a warp's 32 rows of a token lie side by side
+  float* part = reinterpret_cast<float*>(smem);
+  constexpr int W = BN < 32 ? BN : 32;
+#pragma unroll 1
+  for (int c = 0; c < BN; c += W) {
+    uint32_t v[W];
+    if constexpr (W == 32) tmem_ld32(tmem + (static_cast<uint32_t>(warp * 32) << 16) + c, v);
+    else tmem_ld16(tmem + (static_cast<uint32_t>(warp * 32) << 16) + c, v);
+#pragma unroll
+    for (int j = 0; j < W; ++j) part[(c + j) * kRows + tid] = ok ? __uint_as_float(v[j]) : __uint_as_float(0x7FC00000u);
+  }
+  tc_before();
+  __syncthreads();
+  if (warp == 0) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::kCols) : "memory");
+  if (split > 1) cluster_sync();
+  // units of four rows of a token, shared among the cluster's CTAs
+  const int units = min(BN, a.tokens - t0) * (kRows / 4);
+  const int u1 = units * (rank + 1) / split;
+  for (int u = units * rank / split + tid; u < u1; u += 128) {
+    float4 z;
+    if (split == 1) {
+      z = reinterpret_cast<const float4*>(part)[u];
+    } else {
+      const uint32_t at = smem_u32(part) + static_cast<uint32_t>(u) * 16u;
+      float4 p[kMaxSplit];
+#pragma unroll
+      for (int r = 0; r < kMaxSplit; ++r)
+        if (r < split) p[r] = peer_load(at, r);
+      z = p[0];
+#pragma unroll
+      for (int r = 1; r < kMaxSplit; ++r)
+        if (r < split) z.x += p[r].x, z.y += p[r].y, z.z += p[r].z, z.w += p[r].w;
+    }
+    finish(a, t0 + (u >> 5), n0 + 4 * (u & 31), z);
+  }
+  __syncwarp();
+  if (split > 1) cluster_sync();  // peers may still read this CTA's sums
+}
+
+typedef CUresult (*EncodeTiled)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                                const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiled encode_fn() {
+  static std::atomic<EncodeTiled> fn{nullptr};
+  EncodeTiled f = fn.load(std::memory_order_acquire);
+  if (!f) {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn.store(f = reinterpret_cast<EncodeTiled>(p), std::memory_order_release);
+  }
+  return f;
+}
+bool encode(CUtensorMap* m, int dtype, int rank, const void* base, const cuuint64_t* dims, const cuuint64_t* strides,
+            const cuuint32_t* box) {
+  const EncodeTiled f = encode_fn();
+  const cuuint32_t one[4] = {1, 1, 1, 1};
+  return f && f(m, dtype == K2_F8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank,
+                const_cast<void*>(base), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+// K-major rows of the tokens (a bf16 map copies fp16 as well: it moves bytes)
+bool encode_tokens(CUtensorMap* m, int dtype, const void* x, long long stride, int cols, int tokens, int box_tokens) {
+  const int b = dtype == K2_F8 ? 1 : 2;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(tokens)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(stride) * b};
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(kStepBytes / b), static_cast<cuuint32_t>(box_tokens)};
+  return encode(m, dtype, 2, x, dims, strides, box);
+}
+bool encode_weights(CUtensorMap* m, int dtype, const LinearWeights& w, int rows, int cols) {
+  const int b = dtype == K2_F8 ? 1 : 2;
+  if (w.packed) {
+    const cuuint64_t chunks = (static_cast<cuuint64_t>(cols) + 511) / 512;
+    const cuuint64_t dims[4] = {512, 2, chunks, static_cast<cuuint64_t>(rows + 1) / 2};
+    const cuuint64_t strides[3] = {512, 1024, 1024 * chunks};
+    const cuuint32_t box[4] = {kStepBytes, 2, 1, kRows / 2};
+    return encode(m, dtype, 4, w.base, dims, strides, box);
+  }
+  const cuuint64_t step = static_cast<cuuint64_t>(w.stride) * b;
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows), 1, 1};
+  const cuuint64_t strides[3] = {step, step, step};
+  const cuuint32_t box[4] = {static_cast<cuuint32_t>(kStepBytes / b), kRows, 1, 1};
+  return encode(m, dtype, 4, w.base, dims, strides, box);
+}
+
+template <int BN, bool F8>
+cudaError_t launch_tile(const CUtensorMap& mw, const CUtensorMap& mx, const LinearArgs& a, const WeightPlace& place, int steps,
+                        int split, int dev, cudaStream_t s) {
+  using C = Tile<BN>;
+  auto kernel = linear_kernel<BN, F8>;
+  static std::atomic<uint64_t> ready{0};
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), C::kSmem, dev, ready);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((a.rows + kRows - 1) / kRows * split, (a.tokens + BN - 1) / BN);
+  cfg.blockDim = dim3(128);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim = {static_cast<unsigned>(split), 1, 1};
+  cfg.attrs = attr;
+  cfg.numAttrs = split > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, mw, mx, a, place, steps, split);
+}
+template <int BN>
+cudaError_t launch_tile(bool f8, const CUtensorMap& mw, const CUtensorMap& mx, const LinearArgs& a, const WeightPlace& place,
+                        int steps, int split, int dev, cudaStream_t s) {
+  return f8 ? launch_tile<BN, true>(mw, mx, a, place, steps, split, dev, s)
+            : launch_tile<BN, false>(mw, mx, a, place, steps, split, dev, s);
+}
+
+}  // namespace
+
+k2_status launch_linear(const LinearWeights& w, const void* x, long long x_stride, const LinearArgs& a, cudaStream_t s) {
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess && (dev < 0 || dev >= 64)) e = cudaErrorInvalidDevice;
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e == cudaSuccess) {
+    const bool f8 = a.dtype == K2_F8;
+    const WeightPlace place = {w.packed ? 1 : 0, f8 ? kStepBytes : kStepBytes / 2};
+    const int bn = a.tokens <= 16 ? 16 : a.tokens <= 32 ? 32 : a.tokens <= 64 ? 64 : 128;
+    const int steps = (a.cols + place.step - 1) / place.step;
+    const long long tiles = static_cast<long long>((a.rows + kRows - 1) / kRows) * ((a.tokens + bn - 1) / bn);
+    const int split = static_cast<int>(std::max<long long>(1, std::min<long long>({2ll * sms / tiles, kMaxSplit, steps})));
+    CUtensorMap mw, mx;
+    if (!encode_weights(&mw, a.dtype, w, a.rows, a.cols) || !encode_tokens(&mx, a.dtype, x, x_stride, a.cols, a.tokens, bn)) {
+      set_error("no tensor map for %d x %d weights and %d tokens", a.rows, a.cols, a.tokens);
+      return K2_ERR_CUDA;
+    }
+    e = bn == 16   ? launch_tile<16>(f8, mw, mx, a, place, steps, split, dev, s)
+        : bn == 32 ? launch_tile<32>(f8, mw, mx, a, place, steps, split, dev, s)
+        : bn == 64 ? launch_tile<64>(f8, mw, mx, a, place, steps, split, dev, s)
+                   : launch_tile<128>(f8, mw, mx, a, place, steps, split, dev, s);
+  }
+  if (e == cudaSuccess) return K2_OK;
+  set_error("linear launch: %s", cudaGetErrorString(e));
+  return K2_ERR_CUDA;
+}
+
+}  // namespace k2
+
+using namespace k2;
+
+extern "C" {
+
+k2_status k2_linear(const k2_linear_args* p, void* stream) {
+  if (!p) {
+    set_error("the arguments must be non-null");
+    return K2_ERR_ARG;
+  }
+  const bool f8 = p->dtype == K2_F8;
+  if (!f8 && p->dtype != K2_BF16 && p->dtype != K2_F16) {
+    set_error("weights and tokens must be K2_F8, K2_BF16 or K2_F16 (got dtype %d)", p->dtype);
+    return K2_ERR_UNSUPPORTED;
+  }
+  if (p->out_dtype != K2_F32 && p->out_dtype != K2_BF16 && p->out_dtype != K2_F16) {
+    set_error("the output must be K2_F32, K2_BF16 or K2_F16 (got dtype %d)", p->out_dtype);
+    return K2_ERR_UNSUPPORTED;
+  }
+  if (p->activation < K2_ACT_NONE || p->activation > K2_ACT_SWIGLU) {
+    set_error("activation must be one of K2_ACT_* (got %d)", p->activation);
+    return K2_ERR_ARG;
+  }
+  if (p->tokens < 0 || p->tokens > 1 << 22 || p->out_features < 1 || p->out_features > 1 << 24 || p->in_features < 1 ||
+      p->in_features > 1 << 24) {
+    set_error("tokens in [0, 2^22], features in [1, 2^24] (got %d, %d and %d)", p->tokens, p->out_features, p->in_features);
+    return K2_ERR_SHAPE;
+  }
+  const bool pairs = p->activation == K2_ACT_SWIGLU;
+  if (pairs && p->out_features % 2) {
+    set_error("K2_ACT_SWIGLU needs an even number of out_features (got %d)", p->out_features);
+    return K2_ERR_SHAPE;
+  }
+  if (p->wait_limit_us < 0 || p->wait_limit_us > 1000000) {
+    set_error("wait_limit_us must be in [0, 1000000] (got %d)", p->wait_limit_us);
+    return K2_ERR_ARG;
+  }
+  if (p->tokens == 0) return K2_OK;
+  if (!p->w || !p->x || !p->out || f8 != (p->w_scale != nullptr) || f8 != (p->x_scale != nullptr)) {
+    set_error("w, x and out must be non-null, and w_scale and x_scale for K2_F8 alone");
+    return K2_ERR_ARG;
+  }
+  const int b = f8 ? 1 : 2, ob = p->out_dtype == K2_F32 ? 4 : 2;
+  const int64_t width = pairs ? p->out_features / 2 : p->out_features, most = 1ll << 36;
+  const int64_t ws = p->out_features > 1 ? p->w_stride : (p->in_features + 15) / 16 * 16;
+  const int64_t xs = p->tokens > 1 ? p->x_stride : (p->in_features + 15) / 16 * 16;
+  const int64_t os = p->tokens > 1 ? p->out_stride : width, rs = p->tokens > 1 ? p->residual_stride : width;
+  if (ws < p->in_features || xs < p->in_features || os < width || (p->residual && rs < width) || ws > most || xs > most ||
+      os > most || (p->residual && rs > most)) {
+    set_error("rows must be at least as far apart as they are long, and at most 2^36 elements (got w %lld, x %lld, out %lld)",
+              static_cast<long long>(ws), static_cast<long long>(xs), static_cast<long long>(os));
+    return K2_ERR_ARG;
+  }
+  if (!aligned16(p->w) || !aligned16(p->x) || ws * b % 16 || xs * b % 16) {
+    set_error("rows of w and x must be 16-byte aligned");
+    return K2_ERR_ARG;
+  }
+  for (const void* q : {static_cast<const void*>(p->w_scale), static_cast<const void*>(p->x_scale), static_cast<const void*>(p->bias),
+                        static_cast<const void*>(p->flags)})
+    if (reinterpret_cast<uintptr_t>(q) % 4) {
+      set_error("scales, bias and flags must be 4-byte aligned");
+      return K2_ERR_ARG;
+    }
+  if (reinterpret_cast<uintptr_t>(p->out) % ob || reinterpret_cast<uintptr_t>(p->residual) % ob) {
+    set_error("out and residual must be aligned to their type");
+    return K2_ERR_ARG;
+  }
+  const RowSet out = {p->out, ob * os, ob * width, p->tokens}, res = {p->residual, ob * rs, ob * width, p->tokens},
+               w = {p->w, b * ws, static_cast<int64_t>(b) * p->in_features, p->out_features},
+               x = {p->x, b * xs, static_cast<int64_t>(b) * p->in_features, p->tokens},
+               wsc = {p->w_scale, 4, 4, p->out_features}, xsc = {p->x_scale, 4, 4, p->tokens}, bias = {p->bias, 4, 4, p->out_features};
+  const bool same = p->residual == p->out && os == rs;
+  if (sets_meet(out, w) || sets_meet(out, x) || sets_meet(out, wsc) || sets_meet(out, xsc) || sets_meet(out, bias) ||
+      (!same && sets_meet(out, res))) {
+    set_error("the output may not lie over an input (but over the residual itself, with its stride)");
+    return K2_ERR_ARG;
+  }
+  const LinearArgs a = {p->w_scale, p->x_scale, p->bias, p->residual, rs, p->out, os, p->tokens, p->out_features, p->in_features,
+                        p->dtype, p->out_dtype, p->activation, p->flags, K2_LINEAR_TIMEOUT,
+                        p->wait_limit_us ? 1000ull * p->wait_limit_us : kWaitLimitNs};
+  return launch_linear({p->w, ws, false}, p->x, xs, a, static_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"

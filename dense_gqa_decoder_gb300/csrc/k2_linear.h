@@ -1,0 +1,55 @@
+// Rows as E4M3 codes, and the matrix product that reads them: what the entry points and the model's layers share.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "../../include/k2.h"
+
+namespace k2 {
+
+// A product as the kernels see it (k2_linear_args, checked).
+struct LinearArgs {
+  const float* w_scale;  // null: none
+  const float* x_scale;
+  const float* bias;
+  const void* residual;
+  long long residual_stride;
+  void* out;
+  long long out_stride;
+  int tokens, rows, cols;  // rows: of the weight matrix
+  int dtype, out_dtype, act;
+  unsigned* flags;         // nullable; raised with `bit` when a wait runs out
+  unsigned bit;
+  unsigned long long limit_ns;
+};
+
+// The weights [rows][cols] of a product: rows `stride` elements apart, or (packed) pairs of rows in 512-byte chunks, as
+// the decode step streams them.
+struct LinearWeights {
+  const void* base;
+  long long stride;
+  bool packed;
+};
+
+// `n` rows of `row` bytes, `stride` bytes apart
+struct RowSet {
+  const void* p;
+  int64_t stride, row, n;
+};
+// Whether two sets share a byte.  Sets of the same stride may be slices of the same wider rows; others are compared by the
+// memory from their first byte to their last.
+inline bool sets_meet(const RowSet& a, const RowSet& b) {
+  if (!a.p || !b.p || a.n < 1 || b.n < 1) return false;
+  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.p), b0 = reinterpret_cast<uintptr_t>(b.p);
+  const uintptr_t a1 = a0 + (a.n - 1) * a.stride + a.row, b1 = b0 + (b.n - 1) * b.stride + b.row;
+  if (a1 <= b0 || b1 <= a0) return false;
+  if (a.n < 2 || b.n < 2 || a.stride != b.stride) return true;
+  const int64_t d = b0 >= a0 ? static_cast<int64_t>((b0 - a0) % a.stride)  // from a row of a to the next start of a row of b
+                             : (a.stride - static_cast<int64_t>((a0 - b0) % a.stride)) % a.stride;
+  return d < a.row || a.stride - d < b.row;
+}
+
+k2_status launch_linear(const LinearWeights& w, const void* x, long long x_stride, const LinearArgs& a, cudaStream_t s);
+
+}  // namespace k2

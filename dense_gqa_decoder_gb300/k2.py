@@ -26,6 +26,10 @@ KERNEL_CLASSES = ("embed", "qkv", "attn", "o_proj", "gate_up", "down", "lm_head"
 K2_PAGED_BAD_SLOT, K2_PAGED_BAD_BLOCK, K2_PAGED_BAD_LENGTH, K2_PAGED_TIMEOUT = 1, 2, 4, 8
 K2_PLAN_BAD_LENGTH, K2_PLAN_TABLE_FULL, K2_PLAN_NO_BLOCKS, K2_PLAN_TOKENS_FULL = 1, 2, 4, 8
 K2_PAGED_MAX_REQUESTS = 2048
+K2_ACT_NONE, K2_ACT_RELU, K2_ACT_SILU, K2_ACT_GELU, K2_ACT_GELU_TANH, K2_ACT_SWIGLU = range(6)
+ACTIVATIONS = {None: K2_ACT_NONE, "none": K2_ACT_NONE, "relu": K2_ACT_RELU, "silu": K2_ACT_SILU, "gelu": K2_ACT_GELU,
+               "gelu_tanh": K2_ACT_GELU_TANH, "swiglu": K2_ACT_SWIGLU}
+K2_LINEAR_TIMEOUT = 1
 DTYPES = {"f32": K2_F32, "bf16": K2_BF16, "f16": K2_F16, "i8": K2_I8, "f8": K2_F8, "q4": K2_Q4}
 
 
@@ -80,6 +84,14 @@ class LogitRules(C.Structure):
                 ("mask", C.c_void_p), ("mask_stride", C.c_int64), ("n_masks", C.c_int32), ("mask_row", C.c_void_p)]
 
 
+class LinearArgs(C.Structure):
+    _fields_ = [("w", C.c_void_p), ("w_stride", C.c_int64), ("w_scale", C.c_void_p), ("x", C.c_void_p),
+                ("x_stride", C.c_int64), ("x_scale", C.c_void_p), ("bias", C.c_void_p), ("residual", C.c_void_p),
+                ("residual_stride", C.c_int64), ("out", C.c_void_p), ("out_stride", C.c_int64), ("tokens", C.c_int32),
+                ("out_features", C.c_int32), ("in_features", C.c_int32), ("dtype", C.c_int32), ("out_dtype", C.c_int32),
+                ("activation", C.c_int32), ("wait_limit_us", C.c_int32), ("flags", C.c_void_p)]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"libk2.so is not built ({LIB_PATH}); run dense_gqa_decoder_gb300.build")
@@ -123,6 +135,10 @@ def _load():
                                          C.c_size_t, vp]),
         "k2_paged_step": (C.c_int, [vp, vp, vp, vp, vp, i32, vp, vp, vp, i32, i32, i32, vp, vp, vp, C.c_size_t, vp]),
         "k2_adjust_logits": (C.c_int, [vp, vp, i64, vp, i64, i32, i32, vp]),
+        "k2_quantize_rows": (C.c_int, [vp, i32, i64, i32, i32, vp, i64, vp, vp]),
+        "k2_norm_quantize": (C.c_int, [vp, i32, i64, vp, i64, vp, i64, i32, vp, i32, i32, i32, i32, C.c_float, vp, i64, vp,
+                                       vp]),
+        "k2_linear": (C.c_int, [vp, vp]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -138,7 +154,8 @@ EXPORTED = ("k2_workspace_bytes", "k2_init_weights", "k2_free", "k2_last_error",
             "k2_kv_state_bytes", "k2_kv_save", "k2_kv_peek", "k2_kv_load", "k2_set_sampling", "k2_sample_logits",
             "k2_philox", "k2_spec_draft", "k2_decode_speculative", "k2_quantize_fp8",
             "k2_quantize_q4", "k2_spec_logits_view", "k2_paged_plan", "k2_paged_append",
-            "k2_paged_workspace_bytes", "k2_paged_attention", "k2_paged_step", "k2_adjust_logits")
+            "k2_paged_workspace_bytes", "k2_paged_attention", "k2_paged_step", "k2_adjust_logits",
+            "k2_quantize_rows", "k2_norm_quantize", "k2_linear")
 
 
 def _ptr(t):
@@ -681,6 +698,119 @@ def adjust_logits(logits, out=None, *, repetition=None, presence=None, frequency
     u = _RULES(rep, pres, freq, id_ptr, id_stride, id_len, id_prompt, b_off, b_ids, b_val, n_bias, m_ptr, m_stride, n_masks,
                m_row)
     st = LIB.k2_adjust_logits(u, logits.data_ptr(), ld, out.data_ptr(), ld_out, rows, vocab, _raw_stream(stream, dev))
+    if st:
+        _call(st)
+
+
+# ---- activations in 8 bits, and a matrix product -------------------------------------------------
+
+_CODE_DTYPES = (torch.float8_e4m3fn, torch.uint8)
+_MATRIX_DTYPES = {torch.float8_e4m3fn: K2_F8, torch.uint8: K2_F8, torch.bfloat16: K2_BF16, torch.float16: K2_F16}
+
+
+def _matrix(what, t, dtypes, dev, shape=None):
+    """A [rows, columns] tensor whose rows are contiguous and may be apart: their distance"""
+    if t.dtype in dtypes and t.get_device() == dev and t.dim() == 2 and (shape is None or t.shape == shape):
+        row, one = t.stride()
+        if one == 1 or t.shape[1] == 1:
+            return row
+    raise ValueError(f"{what} must be {'[rows, columns]' if shape is None else list(shape)} rows of "
+                     f"{' or '.join(str(d) for d in dtypes)} on cuda:{dev}, each row contiguous, got {t.dtype} "
+                     f"{tuple(t.shape)} with strides {t.stride()} on {t.device}")
+
+
+def quantize_rows(x, codes, scales, stream=None):
+    """k2_quantize_rows: rows x [tokens, columns] (fp32, bf16 or fp16) to E4M3 codes
+    of the same shape (float8_e4m3fn or uint8) and scales [tokens] fp32."""
+    dev = _device(x)
+    xs = _matrix("x", x, _ROW_DTYPES, dev)
+    cs = _matrix("codes", codes, _CODE_DTYPES, dev, x.shape)
+    n, cols = x.shape
+    if scales.dtype is not torch.float32 or scales.get_device() != dev or scales.shape != (n,) or not scales.is_contiguous():
+        _need("scales", scales, torch.float32, (n,), dev)
+    st = LIB.k2_quantize_rows(x.data_ptr(), _ROW_DTYPES[x.dtype], xs, n, cols, codes.data_ptr(), cs, scales.data_ptr(),
+                              _raw_stream(stream, dev))
+    if st:
+        _call(st)
+
+
+def norm_quantize(x, gain, codes, scales, *, residual=None, residual_out=None, groups=1, eps=1e-6, stream=None):
+    """k2_norm_quantize: x [tokens, hidden] (+ residual, same shape, the sum into
+    `residual_out`, default residual itself), normalised in `groups` and times gain
+    [hidden], to E4M3 codes (float8_e4m3fn or uint8) and scales [tokens] fp32.  x,
+    residual and gain are fp32, bf16 or fp16."""
+    dev = _device(x)
+    xs = _matrix("x", x, _ROW_DTYPES, dev)
+    cs = _matrix("codes", codes, _CODE_DTYPES, dev, x.shape)
+    n, hidden = x.shape
+    if scales.dtype is not torch.float32 or scales.get_device() != dev or scales.shape != (n,) or not scales.is_contiguous():
+        _need("scales", scales, torch.float32, (n,), dev)
+    if gain.dtype not in _ROW_DTYPES or gain.get_device() != dev or gain.shape != (hidden,) or not gain.is_contiguous():
+        raise ValueError(f"gain must be a contiguous float32, bfloat16 or float16 tensor of {hidden} values on cuda:{dev}, "
+                         f"got {gain.dtype} {tuple(gain.shape)} on {gain.device}")
+    res = rs = out = os_ = rdt = 0
+    if residual is not None:
+        rs = os_ = _matrix("residual", residual, _ROW_DTYPES, dev, x.shape)
+        res = out = residual.data_ptr()
+        rdt = _ROW_DTYPES[residual.dtype]
+        if residual_out is not None:
+            os_ = _matrix("residual_out", residual_out, (residual.dtype,), dev, x.shape)
+            out = residual_out.data_ptr()
+    elif residual_out is not None:
+        raise ValueError("residual_out needs residual")
+    st = LIB.k2_norm_quantize(x.data_ptr(), _ROW_DTYPES[x.dtype], xs, res, rs, out, os_, rdt, gain.data_ptr(),
+                              _ROW_DTYPES[gain.dtype], n, hidden, groups, eps, codes.data_ptr(), cs, scales.data_ptr(),
+                              _raw_stream(stream, dev))
+    if st:
+        _call(st)
+
+
+_LINEAR = struct.Struct("@PqPPqPPPqPqiiiiiiiP").pack  # a LinearArgs
+
+
+def linear(w, x, out, *, w_scale=None, x_scale=None, bias=None, activation=None, residual=None, flags=None,
+           wait_limit_us=0, stream=None):
+    """k2_linear: out [tokens, out_features] (fp32, bf16 or fp16; half as many columns
+    for "swiglu") = act(w_scale * x_scale * (x . w^T) + bias) + residual, of w
+    [out_features, in_features] and x [tokens, in_features] in E4M3 codes (with
+    w_scale [out_features] and x_scale [tokens]), bf16 or fp16.  activation: None,
+    "relu", "silu", "gelu", "gelu_tanh" or "swiglu"; residual: like out, or out itself;
+    flags: an int32 word that K2_LINEAR_TIMEOUT is OR-ed into."""
+    dev = _device(w)
+    ws = _matrix("w", w, _MATRIX_DTYPES, dev)
+    kind = _MATRIX_DTYPES[w.dtype]
+    n, k = w.shape
+    xs = _matrix("x", x, (w.dtype,) if kind != K2_F8 else _CODE_DTYPES, dev)
+    t, kx = x.shape
+    act = ACTIVATIONS.get(activation, -1)
+    if kx != k or act < 0:
+        raise ValueError(f"x has {kx} columns, w {k}" if kx != k else f"no activation {activation!r}")
+    width = n // 2 if act == K2_ACT_SWIGLU else n
+    os_ = _matrix("out", out, _ROW_DTYPES, dev, (t, width))
+    f32 = torch.float32
+    sw = sx = b = r = rs = f = 0
+    if kind == K2_F8:
+        if w_scale is None or x_scale is None:
+            raise ValueError("E4M3 codes need w_scale and x_scale")
+        if w_scale.dtype is not f32 or w_scale.get_device() != dev or w_scale.shape != (n,) or not w_scale.is_contiguous():
+            _need("w_scale", w_scale, f32, (n,), dev)
+        if x_scale.dtype is not f32 or x_scale.get_device() != dev or x_scale.shape != (t,) or not x_scale.is_contiguous():
+            _need("x_scale", x_scale, f32, (t,), dev)
+        sw, sx = w_scale.data_ptr(), x_scale.data_ptr()
+    elif w_scale is not None or x_scale is not None:
+        raise ValueError("scales go with E4M3 codes")
+    if bias is not None:
+        if bias.dtype is not f32 or bias.get_device() != dev or bias.shape != (n,) or not bias.is_contiguous():
+            _need("bias", bias, f32, (n,), dev)
+        b = bias.data_ptr()
+    if residual is not None:
+        rs = os_ if residual is out else _matrix("residual", residual, (out.dtype,), dev, out.shape)
+        r = residual.data_ptr()
+    if flags is not None:
+        _need("flags", flags, torch.int32, (1,), dev)
+        f = flags.data_ptr()
+    st = LIB.k2_linear(_LINEAR(w.data_ptr(), ws, sw, x.data_ptr(), xs, sx, b, r, rs, out.data_ptr(), os_, t, n, k, kind,
+                               _ROW_DTYPES[out.dtype], act, wait_limit_us, f), _raw_stream(stream, dev))
     if st:
         _call(st)
 

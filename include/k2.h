@@ -659,6 +659,81 @@ typedef struct {
 k2_status k2_adjust_logits(const k2_logit_rules* rules, const float* d_logits, int64_t ld, float* d_out,
                            int64_t ld_out, int32_t rows, int32_t vocab, void* stream);
 
+/* ---- activations in 8 bits, and a matrix product ------------------------------------
+ *
+ * The rows between a layer's matrices as E4M3 codes with one fp32 scale per row (what
+ * k2_quantize_fp8 gives for weights), and the product that reads them.  A layer's half is
+ *   k2_norm_quantize   residual stream + last output -> stream, normalised codes
+ *   k2_linear          codes x weights (bias, activation) -> rows
+ *   k2_quantize_rows   rows -> codes
+ *   k2_linear          codes x weights (+ residual) -> residual stream
+ * (option K2_OPT_ACT8 runs the model's layers so).  No context is needed; the calls
+ * allocate nothing, need no workspace, enqueue their work on `stream` and may be captured
+ * into a CUDA graph.  Rows may lie apart: a stride is the distance of two rows in elements,
+ * at least the row's length (not read where there is one row).  Why a call was refused:
+ * k2_last_error(NULL).
+ *
+ * k2_quantize_rows: row t of d_x ([tokens][cols], dtype K2_F32, K2_BF16 or K2_F16) becomes
+ * d_scales[t] = max|x| / 448 and d_codes[t * codes_stride + c] = E4M3(x / scale), in fp32,
+ * rounded to nearest with ties to even and saturating.  A row whose scale is 0 gets codes
+ * 0; one that holds a NaN or an infinity gets the scale NaN and the code NaN (0x7F)
+ * throughout, so that it stays visible in what is computed from it, and costs no other row.
+ * cols: 1 .. 49152.  d_codes and d_scales may not lie over the input or each other. */
+k2_status k2_quantize_rows(const void* d_x, int32_t dtype, int64_t x_stride, int32_t tokens, int32_t cols,
+                           uint8_t* d_codes, int64_t codes_stride, float* d_scales, void* stream);
+
+/* The same of a normalised sum (the two norms of a decoder layer): per row
+ *   h = x + residual (fp32); residual_out = h, rounded to nearest
+ *   y = h / sqrt(mean over its group of h^2 + eps) * gain
+ *   codes and scale of y as above.
+ * `groups` divides hidden into equal contiguous parts (GroupedRMSNorm); the gain is over all
+ * of hidden.  The norm is of h before it is rounded to residual_dtype.  Sums are held in
+ * fp32, and do not overflow for any finite row.  d_residual NULL (with d_residual_out NULL):
+ * h = x.  d_residual_out may be d_residual itself with the same stride, no other buffers may
+ * meet.  x, residual and gain are each K2_F32, K2_BF16 or K2_F16.  eps: at least 2^-126.
+ * hidden: 1 .. 49152. */
+k2_status k2_norm_quantize(const void* d_x, int32_t x_dtype, int64_t x_stride, const void* d_residual,
+                           int64_t residual_stride, void* d_residual_out, int64_t residual_out_stride,
+                           int32_t residual_dtype, const void* d_gain, int32_t gain_dtype, int32_t tokens,
+                           int32_t hidden, int32_t groups, float eps, uint8_t* d_codes, int64_t codes_stride,
+                           float* d_scales, void* stream);
+
+/* out = act(w_scale * x_scale * (x . w^T) + bias) + residual, on the tensor cores:
+ *   w [out_features][in_features], x [tokens][in_features], both of `dtype`: K2_F8 (E4M3
+ *     codes; w_scale [out_features] and x_scale [tokens] are then needed), K2_BF16 or K2_F16
+ *     (scales NULL).  Rows 16-byte aligned, in_features any number >= 1.
+ *   bias [out_features] fp32, nullable
+ *   activation: one of K2_ACT_*.  K2_ACT_SWIGLU pairs the matrix's rows: row 2j is the gate
+ *     of output j, row 2j + 1 its factor (silu(z[2j]) * z[2j + 1]); out_features is even and
+ *     out has half as many columns.
+ *   residual (nullable): rows like out, in out_dtype; may be out itself with the same stride
+ *   out [tokens][out_features or half]: K2_F32, K2_BF16 or K2_F16
+ * Products are exact and summed in fp32, and so is all that follows; the result is rounded
+ * once.  The order of the sums depends on the sizes alone, so that a call repeats bit for
+ * bit.  Except for that one residual, out may not lie over an input.  A NaN costs the outputs
+ * that it enters.  Every wait inside is bounded (wait_limit_us up to 1000000; 0: one second); a tile
+ * whose wait ran out is NaN throughout and K2_LINEAR_TIMEOUT is OR-ed into *flags. */
+enum { K2_ACT_NONE = 0, K2_ACT_RELU, K2_ACT_SILU, K2_ACT_GELU, K2_ACT_GELU_TANH, K2_ACT_SWIGLU };
+enum { K2_LINEAR_TIMEOUT = 1 };
+typedef struct {
+  const void* w;
+  int64_t w_stride;
+  const float* w_scale;
+  const void* x;
+  int64_t x_stride;
+  const float* x_scale;
+  const float* bias;
+  const void* residual;
+  int64_t residual_stride;
+  void* out;
+  int64_t out_stride;
+  int32_t tokens, out_features, in_features;
+  int32_t dtype, out_dtype, activation;
+  int32_t wait_limit_us;
+  uint32_t* flags; /* device word (the caller clears it); nullable */
+} k2_linear_args;
+k2_status k2_linear(const k2_linear_args* args, void* stream);
+
 /* ---- without a workspace ---------------------------------------------------- */
 
 /* The pages have no counterpart to this call: it exists for callers that
