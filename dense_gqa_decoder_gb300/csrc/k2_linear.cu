@@ -90,6 +90,15 @@ __device__ __forceinline__ float activate(float z, int act) {
   return z;
 }
 
+template <typename T>
+__device__ __forceinline__ T from_f32(float v);
+template <>
+__device__ __forceinline__ float from_f32<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+template <>
+__device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
+
 __device__ __forceinline__ float load_out(const void* p, long long i, int dtype) {
   if (dtype == K2_F32) return static_cast<const float*>(p)[i];
   if (dtype == K2_BF16) return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
@@ -253,6 +262,252 @@ __global__ void __launch_bounds__(128) linear_kernel(const __grid_constant__ CUt
   if (split > 1) cluster_sync();  // peers may still read this CTA's sums
 }
 
+// ---- many tokens: pairs of CTAs -------------------------------------------------------------------------------------------
+//
+// A pair of CTAs (the two SMs of a TPC) works on tiles of 256 weight rows x up to 256 tokens with one MMA over both SMs
+// (cta_group::2): each CTA holds its own 128 rows and half of the tokens, so that an SM takes in 32 KB for 128 x 256 x 128
+// products of E4M3 codes (a CTA by itself would take in 48 KB).  Persistent, roles as warps:
+//   warp 0      requests the stages of its CTA (completion is counted by the first CTA's barriers)
+//   warp 1      of the first CTA issues the MMAs, into one of two accumulators of 256 tensor-memory columns
+//   warps 2-9   read the other accumulator and finish its tile; a warp's lanes are 32 neighbouring outputs of a token
+constexpr int kPairTokens = 256, kPairStages = 6, kPairStage = 2 * kRows * kStepBytes, kPairThreads = 320;
+constexpr int kPairSmem = kPairStages * kPairStage + 1024;
+constexpr int kPairFinishers = 8;  // warps
+
+__device__ __forceinline__ uint32_t cta_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+// the address of a barrier in the pair's first CTA
+__device__ __forceinline__ uint32_t first_cta(const uint64_t* bar) {
+  uint32_t at;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(at) : "r"(smem_u32(bar)));
+  return at;
+}
+__device__ __forceinline__ void arrive_at(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void pair_load_2d(void* dst, const CUtensorMap* m, int c0, int c1, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
+      "[%4];" ::"r"(smem_u32(dst)),
+      "l"(m), "r"(c0), "r"(c1), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void pair_load_4d(void* dst, const CUtensorMap* m, int c0, int c1, int c2, int c3, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, "
+      "%5}], [%6];" ::"r"(smem_u32(dst)),
+      "l"(m), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
+      : "memory");
+}
+template <bool F8>
+__device__ __forceinline__ void pair_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  if (F8)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// arrives at the same barrier of both CTAs once all MMAs issued so far are done
+__device__ __forceinline__ void pair_commit(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(smem_u32(bar)),
+      "h"(static_cast<uint16_t>(3))
+      : "memory");
+}
+
+struct PairShape {
+  int tokens;      // of a tile: 32 .. 256, a multiple of 32
+  int steps;       // of K
+  int row_tiles, token_tiles;
+};
+
+// COLS columns of the accumulator (tokens t ..), this lane's row n
+template <typename OT, bool SWIGLU, int COLS>
+__device__ __forceinline__ void finish_columns(const LinearArgs& a, const uint32_t* v, int t, int n, float ws, float bias, bool ok) {
+  const bool odd = n & 1;
+  OT* out = static_cast<OT*>(a.out);
+  const OT* res = static_cast<const OT*>(a.residual);
+  if (SWIGLU) {
+    // a gate and its factor lie in neighbouring lanes: of two columns the even lane finishes the first, the odd lane the second
+#pragma unroll
+    for (int j = 0; j < COLS; j += 2) {
+      if (t + j >= a.tokens) break;
+      const int last = a.tokens - 1;
+      const float x0 = a.x_scale != nullptr ? __ldg(a.x_scale + t + j) : 1.f, x1 = a.x_scale != nullptr ? __ldg(a.x_scale + min(t + j + 1, last)) : 1.f;
+      const float z0 = __uint_as_float(v[j]) * ws * x0 + bias, z1 = __uint_as_float(v[j + 1]) * ws * x1 + bias;
+      const float other = __shfl_xor_sync(0xffffffffu, odd ? z0 : z1, 1);
+      const float g = odd ? other : z0, u = odd ? z1 : other;
+      const int tt = t + j + (odd ? 1 : 0);
+      float y = __fdividef(g, 1.0f + __expf(-g)) * u;
+      if (n < a.rows && tt < a.tokens) {
+        if (res != nullptr) y += to_f32(res[tt * a.residual_stride + (n >> 1)]);
+        out[tt * a.out_stride + (n >> 1)] = from_f32<OT>(ok ? y : __uint_as_float(0x7FC00000u));
+      }
+    }
+    return;
+  }
+  if (n >= a.rows) return;
+#pragma unroll
+  for (int j = 0; j < COLS; ++j) {
+    if (t + j >= a.tokens) break;
+    const float xs = a.x_scale != nullptr ? __ldg(a.x_scale + t + j) : 1.f;
+    float y = activate(__uint_as_float(v[j]) * ws * xs + bias, a.act);
+    if (res != nullptr) y += to_f32(res[(t + j) * a.residual_stride + n]);
+    out[(t + j) * a.out_stride + n] = from_f32<OT>(ok ? y : __uint_as_float(0x7FC00000u));
+  }
+}
+// a warp's part of a tile: 32 rows (this lane's is n), columns c0 .. c1
+template <typename OT, bool SWIGLU>
+__device__ __forceinline__ void finish_part(const LinearArgs& a, uint32_t acc, int c0, int c1, int t0, int n, bool ok) {
+  const float ws = a.w_scale != nullptr && n < a.rows ? __ldg(a.w_scale + n) : 1.f;
+  const float bias = a.bias != nullptr && n < a.rows ? __ldg(a.bias + n) : 0.f;
+#pragma unroll 1
+  for (int c = c0; c < c1 && t0 + c < a.tokens; c += 16) {
+    uint32_t v[16];
+    tmem_ld16(acc + c, v);
+    finish_columns<OT, SWIGLU, 16>(a, v, t0 + c, n, ws, bias, ok);
+  }
+}
+
+template <bool F8>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
+    linear_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x, const LinearArgs a,
+                       const WeightPlace place, const PairShape sh) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  __shared__ __align__(8) uint64_t full[kPairStages], empty[kPairStages], accf[2], acce[2], drain;
+  __shared__ uint32_t tmem_slot;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rank = static_cast<int>(cta_rank());
+  const int tiles = sh.row_tiles * sh.token_tiles, pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  const int mine = pair < tiles ? (tiles - 1 - pair) / pairs + 1 : 0;
+  if (tid == 0) {
+    for (int s = 0; s < kPairStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&accf[b], 1);
+      mbar_init(&acce[b], 2 * kPairFinishers);
+    }
+    mbar_init(&drain, 1);
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&tmem_slot)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  tc_before();
+  __syncthreads();
+  cluster_sync();  // both CTAs' barriers are ready
+  tc_after();
+  const uint32_t tmem = tmem_slot;
+  if (tid == 0) {
+    const int half = sh.tokens / 2;
+    const uint32_t bytes = 2u * (kRows * kStepBytes + half * kStepBytes);
+    int s = 0, filled = 0;
+    uint32_t ph = 0;  // how often the ring wrapped
+    bool ok = true;
+    for (int i = 0; i < mine && ok; ++i) {
+      const int tile = pair + i * pairs, rt = tile / sh.token_tiles;
+      const int n0 = rt * 2 * kRows + rank * kRows, t0 = (tile - rt * sh.token_tiles) * sh.tokens + rank * half;
+      for (int k = 0; k < sh.steps; ++k) {
+        if (ph > 0 && !wait_for(&empty[s], (ph - 1) & 1u, a.limit_ns)) {
+          ok = false;
+          break;
+        }
+        if (rank == 0) mbar_arrive_expect_tx(&full[s], bytes);
+        uint8_t* st = smem + s * kPairStage;
+        const uint32_t bar = first_cta(&full[s]);
+        const int e = k * place.step;
+        if (place.packed) pair_load_4d(st, &map_w, e & 511, 0, e >> 9, n0 >> 1, bar);
+        else pair_load_4d(st, &map_w, e, n0, 0, 0, bar);
+        pair_load_2d(st + kRows * kStepBytes, &map_x, e, t0, bar);
+        filled = min(filled + 1, kPairStages);
+        if (++s == kPairStages) s = 0, ++ph;
+      }
+    }
+    // Every stage that was filled has been multiplied: its copies have landed, and its release has come, before this CTA ends.
+    // (After a wait that ran out these run out too, a second during which what is on its way lands.)
+    for (int j = 0; j < filled; ++j) {
+      s = s == 0 ? (--ph, kPairStages - 1) : s - 1;
+      if (!mbar_wait(&empty[s], ph & 1u)) break;
+    }
+    if (!ok && a.flags != nullptr) atomicOr(a.flags, a.bit);
+  } else if (tid == 32 && rank == 0) {
+    const uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(sh.tokens >> 3) << 17) | (16u << 24) |
+                           (a.dtype == K2_BF16 ? (1u << 7) | (1u << 10) : 0u);
+    int s = 0;
+    uint32_t ph = 0;
+    bool ok = true;
+    for (int i = 0; i < mine && ok; ++i) {
+      const int b = i & 1;
+      if (i >= 2 && !wait_for(&acce[b], static_cast<uint32_t>((i >> 1) - 1) & 1u, a.limit_ns)) {
+        ok = false;
+        break;
+      }
+      tc_after();
+      const uint32_t acc = tmem + b * kPairTokens;
+      for (int k = 0; k < sh.steps; ++k) {
+        if (!wait_for(&full[s], ph & 1u, a.limit_ns)) {
+          ok = false;
+          break;
+        }
+        tc_after();
+        const uint8_t* st = smem + s * kPairStage;
+#pragma unroll
+        for (int j = 0; j < kStepBytes / 32; ++j)
+          pair_mma<F8>(acc, smem_desc(st + j * 32), smem_desc(st + kRows * kStepBytes + j * 32), idesc, (k | j) != 0);
+        pair_commit(&empty[s]);
+        if (++s == kPairStages) s = 0, ++ph;
+      }
+      if (ok) pair_commit(&accf[b]);
+    }
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(&drain)) : "memory");
+    if ((!mbar_wait(&drain, 0) || !ok) && a.flags != nullptr) atomicOr(a.flags, a.bit);
+  } else if (warp >= 2) {
+    const int group = warp & 3, part = (warp - 2) >> 2;
+    const int c0 = part * (sh.tokens / 2), c1 = c0 + sh.tokens / 2;
+    bool ok = true;
+    for (int i = 0; i < mine; ++i) {
+      const int b = i & 1, tile = pair + i * pairs, rt = tile / sh.token_tiles;
+      // once a wait has run out the rest of this CTA's tiles is NaN
+      if (ok) ok = __all_sync(0xffffffffu, wait_for(&accf[b], static_cast<uint32_t>(i >> 1) & 1u, a.limit_ns));
+      tc_after();
+      const uint32_t acc = tmem + b * kPairTokens + (static_cast<uint32_t>(group * 32) << 16);
+      const int n = rt * 2 * kRows + rank * kRows + group * 32 + lane, t0 = (tile - rt * sh.token_tiles) * sh.tokens;
+      if (a.act == K2_ACT_SWIGLU) {
+        if (a.out_dtype == K2_F32) finish_part<float, true>(a, acc, c0, c1, t0, n, ok);
+        else if (a.out_dtype == K2_BF16) finish_part<__nv_bfloat16, true>(a, acc, c0, c1, t0, n, ok);
+        else finish_part<__half, true>(a, acc, c0, c1, t0, n, ok);
+      } else {
+        if (a.out_dtype == K2_F32) finish_part<float, false>(a, acc, c0, c1, t0, n, ok);
+        else if (a.out_dtype == K2_BF16) finish_part<__nv_bfloat16, false>(a, acc, c0, c1, t0, n, ok);
+        else finish_part<__half, false>(a, acc, c0, c1, t0, n, ok);
+      }
+      tc_before();
+      __syncwarp();
+      if (lane == 0) arrive_at(first_cta(&acce[b]));
+    }
+    if (!ok && lane == 0 && a.flags != nullptr) atomicOr(a.flags, a.bit);
+  }
+  tc_before();
+  __syncthreads();
+  cluster_sync();  // both CTAs' roles have ended
+  tc_after();
+  if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+}
+
 typedef CUresult (*EncodeTiled)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
                                 const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
@@ -327,6 +582,18 @@ cudaError_t launch_tile(bool f8, const CUtensorMap& mw, const CUtensorMap& mx, c
             : launch_tile<BN, false>(mw, mx, a, place, steps, split, dev, s);
 }
 
+template <bool F8>
+cudaError_t launch_pair(const CUtensorMap& mw, const CUtensorMap& mx, const LinearArgs& a, const WeightPlace& place,
+                        const PairShape& sh, int sms, int dev, cudaStream_t s) {
+  auto kernel = linear_pair_kernel<F8>;
+  static std::atomic<uint64_t> ready{0};
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), kPairSmem, dev, ready);
+  if (e != cudaSuccess) return e;
+  const int pairs = std::min(sms / 2, sh.row_tiles * sh.token_tiles);
+  kernel<<<2 * pairs, kPairThreads, kPairSmem, s>>>(mw, mx, a, place, sh);
+  return cudaGetLastError();
+}
+
 }  // namespace
 
 k2_status launch_linear(const LinearWeights& w, const void* x, long long x_stride, const LinearArgs& a, cudaStream_t s) {
@@ -337,8 +604,28 @@ k2_status launch_linear(const LinearWeights& w, const void* x, long long x_strid
   if (e == cudaSuccess) {
     const bool f8 = a.dtype == K2_F8;
     const WeightPlace place = {w.packed ? 1 : 0, f8 ? kStepBytes : kStepBytes / 2};
-    const int bn = a.tokens <= 16 ? 16 : a.tokens <= 32 ? 32 : a.tokens <= 64 ? 64 : 128;
     const int steps = (a.cols + place.step - 1) / place.step;
+    if (a.tokens > 256) {
+      // tiles as wide as leave the fewest columns to the pair with the most tiles
+      PairShape sh = {0, steps, (a.rows + 2 * kRows - 1) / (2 * kRows), 0};
+      long long best = 0;
+      for (int n = kPairTokens; n >= 128; n -= 32) {
+        const int tt = (a.tokens + n - 1) / n;
+        const long long cost = (static_cast<long long>(sh.row_tiles) * tt + sms / 2 - 1) / (sms / 2) * n;
+        if (sh.tokens == 0 || cost < best) sh.tokens = n, sh.token_tiles = tt, best = cost;
+      }
+      CUtensorMap mw, mx;
+      if (!encode_weights(&mw, a.dtype, w, a.rows, a.cols) ||
+          !encode_tokens(&mx, a.dtype, x, x_stride, a.cols, a.tokens, sh.tokens / 2)) {
+        set_error("no tensor map for %d x %d weights and %d tokens", a.rows, a.cols, a.tokens);
+        return K2_ERR_CUDA;
+      }
+      e = f8 ? launch_pair<true>(mw, mx, a, place, sh, sms, dev, s) : launch_pair<false>(mw, mx, a, place, sh, sms, dev, s);
+      if (e == cudaSuccess) return K2_OK;
+      set_error("linear launch: %s", cudaGetErrorString(e));
+      return K2_ERR_CUDA;
+    }
+    const int bn = a.tokens <= 16 ? 16 : a.tokens <= 32 ? 32 : a.tokens <= 64 ? 64 : 128;
     const long long tiles = static_cast<long long>((a.rows + kRows - 1) / kRows) * ((a.tokens + bn - 1) / bn);
     const int split = static_cast<int>(std::max<long long>(1, std::min<long long>({2ll * sms / tiles, kMaxSplit, steps})));
     CUtensorMap mw, mx;
