@@ -269,10 +269,11 @@ __global__ void __launch_bounds__(128) linear_kernel(const __grid_constant__ CUt
 // products of E4M3 codes (a CTA by itself would take in 48 KB).  Persistent, roles as warps:
 //   warp 0      requests the stages of its CTA (completion is counted by the first CTA's barriers)
 //   warp 1      of the first CTA issues the MMAs, into one of two accumulators of 256 tensor-memory columns
-//   warps 2-9   read the other accumulator and finish its tile; a warp's lanes are 32 neighbouring outputs of a token
-constexpr int kPairTokens = 256, kPairStages = 6, kPairStage = 2 * kRows * kStepBytes, kPairThreads = 320;
-constexpr int kPairSmem = kPairStages * kPairStage + 1024;
-constexpr int kPairFinishers = 8;  // warps
+//   warps 2-17  read the other accumulator and finish its tile; a warp's lanes are 32 neighbouring outputs of a token
+constexpr int kPairTokens = 256, kPairStages = 8, kPairSteps = 2, kPairRing = 192 * 1024;
+constexpr int kPairSmem = kPairRing + 1024;
+constexpr int kPairFinishers = 16, kPairThreads = 32 * (2 + kPairFinishers);
+constexpr int kColumns = 16;  // columns that a finishing warp has in registers
 
 __device__ __forceinline__ uint32_t cta_rank() {
   uint32_t r;
@@ -286,7 +287,7 @@ __device__ __forceinline__ uint32_t first_cta(const uint64_t* bar) {
   return at;
 }
 __device__ __forceinline__ void arrive_at(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ void pair_load_2d(void* dst, const CUtensorMap* m, int c0, int c1, uint32_t bar) {
   asm volatile(
@@ -326,73 +327,102 @@ __device__ __forceinline__ void pair_commit(uint64_t* bar) {
 }
 
 struct PairShape {
-  int tokens;      // of a tile: 32 .. 256, a multiple of 32
+  int tokens;      // of a tile: 64 .. 256, a multiple of 64
   int steps;       // of K
+  int stages;      // of the ring
   int row_tiles, token_tiles;
 };
 
-// COLS columns of the accumulator (tokens t ..), this lane's row n
-template <typename OT, bool SWIGLU, int COLS>
-__device__ __forceinline__ void finish_columns(const LinearArgs& a, const uint32_t* v, int t, int n, float ws, float bias, bool ok) {
-  const bool odd = n & 1;
-  OT* out = static_cast<OT*>(a.out);
-  const OT* res = static_cast<const OT*>(a.residual);
-  if (SWIGLU) {
+enum { kPlain, kPairsOfRows, kOther };  // what follows the sums: nothing, SwiGLU, another activation
+
+// Some columns of the accumulator (tokens t ..) of this lane's row n: z = v * (ws * xs) + bias, then the activation, the
+// residual and the stores.  Nothing waits for the column before: the scales are in shared memory, the residual is loaded ahead.
+template <typename OT, int ACT, bool FULL>
+__device__ __forceinline__ void finish_columns(const LinearArgs& a, const uint32_t (&v)[kColumns], const float* xs, int t, int n,
+                                               float ws, float bias) {
+  const bool odd = n & 1, row = n < a.rows;
+  const int most = a.tokens - t;  // columns of tokens (not FULL: fewer than there are columns)
+  if (ACT == kPairsOfRows) {
     // a gate and its factor lie in neighbouring lanes: of two columns the even lane finishes the first, the odd lane the second
+    const int mine = odd ? 1 : 0;
+    const long long first = t + mine;
+    float res[kColumns / 2];
+    if (a.residual != nullptr) {
+      const OT* from = static_cast<const OT*>(a.residual) + first * a.residual_stride + (n >> 1);
 #pragma unroll
-    for (int j = 0; j < COLS; j += 2) {
-      if (t + j >= a.tokens) break;
-      const int last = a.tokens - 1;
-      const float x0 = a.x_scale != nullptr ? __ldg(a.x_scale + t + j) : 1.f, x1 = a.x_scale != nullptr ? __ldg(a.x_scale + min(t + j + 1, last)) : 1.f;
-      const float z0 = __uint_as_float(v[j]) * ws * x0 + bias, z1 = __uint_as_float(v[j + 1]) * ws * x1 + bias;
+      for (int j = 0; j < kColumns; j += 2, from += 2 * a.residual_stride)
+        res[j / 2] = row && (FULL || j + mine < most) ? to_f32(*from) : 0.f;
+    }
+    OT* out = static_cast<OT*>(a.out) + first * a.out_stride + (n >> 1);
+#pragma unroll
+    for (int j = 0; j < kColumns; j += 2, out += 2 * a.out_stride) {
+      const float2 x = *reinterpret_cast<const float2*>(xs + j);
+      const float z0 = fmaf(__uint_as_float(v[j]), ws * x.x, bias), z1 = fmaf(__uint_as_float(v[j + 1]), ws * x.y, bias);
       const float other = __shfl_xor_sync(0xffffffffu, odd ? z0 : z1, 1);
       const float g = odd ? other : z0, u = odd ? z1 : other;
-      const int tt = t + j + (odd ? 1 : 0);
       float y = __fdividef(g, 1.0f + __expf(-g)) * u;
-      if (n < a.rows && tt < a.tokens) {
-        if (res != nullptr) y += to_f32(res[tt * a.residual_stride + (n >> 1)]);
-        out[tt * a.out_stride + (n >> 1)] = from_f32<OT>(ok ? y : __uint_as_float(0x7FC00000u));
-      }
+      if (a.residual != nullptr) y += res[j / 2];
+      if (row && (FULL || j + mine < most)) *out = from_f32<OT>(y);
     }
     return;
   }
-  if (n >= a.rows) return;
+  float res[kColumns];
+  if (a.residual != nullptr) {
+    const OT* from = static_cast<const OT*>(a.residual) + static_cast<long long>(t) * a.residual_stride + n;
 #pragma unroll
-  for (int j = 0; j < COLS; ++j) {
-    if (t + j >= a.tokens) break;
-    const float xs = a.x_scale != nullptr ? __ldg(a.x_scale + t + j) : 1.f;
-    float y = activate(__uint_as_float(v[j]) * ws * xs + bias, a.act);
-    if (res != nullptr) y += to_f32(res[(t + j) * a.residual_stride + n]);
-    out[(t + j) * a.out_stride + n] = from_f32<OT>(ok ? y : __uint_as_float(0x7FC00000u));
+    for (int j = 0; j < kColumns; ++j, from += a.residual_stride) res[j] = row && (FULL || j < most) ? to_f32(*from) : 0.f;
+  }
+  OT* out = static_cast<OT*>(a.out) + static_cast<long long>(t) * a.out_stride + n;
+#pragma unroll
+  for (int j = 0; j < kColumns; j += 4) {
+    const float4 x = *reinterpret_cast<const float4*>(xs + j);
+    const float x4[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i, out += a.out_stride) {
+      float y = fmaf(__uint_as_float(v[j + i]), ws * x4[i], bias);
+      if (ACT == kOther) y = activate(y, a.act);
+      if (a.residual != nullptr) y += res[j + i];
+      if (row && (FULL || j + i < most)) *out = from_f32<OT>(y);
+    }
   }
 }
-// a warp's part of a tile: 32 rows (this lane's is n), columns c0 .. c1
-template <typename OT, bool SWIGLU>
-__device__ __forceinline__ void finish_part(const LinearArgs& a, uint32_t acc, int c0, int c1, int t0, int n, bool ok) {
-  const float ws = a.w_scale != nullptr && n < a.rows ? __ldg(a.w_scale + n) : 1.f;
+// A warp's part of a tile: 32 rows (this lane's is n), `columns` of the accumulator from t on, whose scales are at xs.  `free`
+// is the barrier that gives the accumulator back, as soon as the last columns are in registers.
+template <typename OT, int ACT>
+__device__ __forceinline__ void finish_part(const LinearArgs& a, uint32_t acc, const float* xs, int columns, int t, int n, bool ok,
+                                            uint32_t free) {
+  const float ws = !ok ? __uint_as_float(0x7FC00000u) : a.w_scale != nullptr && n < a.rows ? __ldg(a.w_scale + n) : 1.f;
   const float bias = a.bias != nullptr && n < a.rows ? __ldg(a.bias + n) : 0.f;
 #pragma unroll 1
-  for (int c = c0; c < c1 && t0 + c < a.tokens; c += 16) {
-    uint32_t v[16];
+  for (int c = 0; c < columns; c += kColumns) {
+    uint32_t v[kColumns];
     tmem_ld16(acc + c, v);
-    finish_columns<OT, SWIGLU, 16>(a, v, t0 + c, n, ws, bias, ok);
+    if (c + kColumns >= columns) {
+      tc_before();
+      __syncwarp();
+      if ((threadIdx.x & 31) == 0) arrive_at(free);
+    }
+    if (t + c + kColumns <= a.tokens) finish_columns<OT, ACT, true>(a, v, xs + c, t + c, n, ws, bias);
+    else if (t + c < a.tokens) finish_columns<OT, ACT, false>(a, v, xs + c, t + c, n, ws, bias);
   }
 }
-
-template <bool F8>
+template <bool F8, typename OT, int ACT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     linear_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x, const LinearArgs a,
                        const WeightPlace place, const PairShape sh) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   __shared__ __align__(8) uint64_t full[kPairStages], empty[kPairStages], accf[2], acce[2], drain;
+  __shared__ __align__(16) float x_scales[kPairFinishers][kPairTokens / 4];
   __shared__ uint32_t tmem_slot;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank = static_cast<int>(cta_rank());
+  const int step_bytes = (kRows + sh.tokens / 2) * kStepBytes, stage = kPairSteps * step_bytes;  // multiples of 1024
+  const int fills = (sh.steps + kPairSteps - 1) / kPairSteps;  // of a tile
   const int tiles = sh.row_tiles * sh.token_tiles, pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   const int mine = pair < tiles ? (tiles - 1 - pair) / pairs + 1 : 0;
   if (tid == 0) {
-    for (int s = 0; s < kPairStages; ++s) {
+    for (int s = 0; s < sh.stages; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
@@ -414,39 +444,41 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   const uint32_t tmem = tmem_slot;
   if (tid == 0) {
     const int half = sh.tokens / 2;
-    const uint32_t bytes = 2u * (kRows * kStepBytes + half * kStepBytes);
     int s = 0, filled = 0;
     uint32_t ph = 0;  // how often the ring wrapped
     bool ok = true;
     for (int i = 0; i < mine && ok; ++i) {
       const int tile = pair + i * pairs, rt = tile / sh.token_tiles;
       const int n0 = rt * 2 * kRows + rank * kRows, t0 = (tile - rt * sh.token_tiles) * sh.tokens + rank * half;
-      for (int k = 0; k < sh.steps; ++k) {
+      for (int f = 0, e = 0; f < fills; ++f) {
         if (ph > 0 && !wait_for(&empty[s], (ph - 1) & 1u, a.limit_ns)) {
           ok = false;
           break;
         }
-        if (rank == 0) mbar_arrive_expect_tx(&full[s], bytes);
-        uint8_t* st = smem + s * kPairStage;
+        const int count = min(kPairSteps, sh.steps - f * kPairSteps);
+        if (rank == 0) mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(2 * count * step_bytes));  // of both CTAs
+        uint8_t* st = smem + s * stage;
         const uint32_t bar = first_cta(&full[s]);
-        const int e = k * place.step;
-        if (place.packed) pair_load_4d(st, &map_w, e & 511, 0, e >> 9, n0 >> 1, bar);
-        else pair_load_4d(st, &map_w, e, n0, 0, 0, bar);
-        pair_load_2d(st + kRows * kStepBytes, &map_x, e, t0, bar);
-        filled = min(filled + 1, kPairStages);
-        if (++s == kPairStages) s = 0, ++ph;
+        for (int q = 0; q < count; ++q, e += place.step, st += step_bytes) {
+          if (place.packed) pair_load_4d(st, &map_w, e & 511, 0, e >> 9, n0 >> 1, bar);
+          else pair_load_4d(st, &map_w, e, n0, 0, 0, bar);
+          pair_load_2d(st + kRows * kStepBytes, &map_x, e, t0, bar);
+        }
+        filled = min(filled + 1, sh.stages);
+        if (++s == sh.stages) s = 0, ++ph;
       }
     }
     // Every stage that was filled has been multiplied: its copies have landed, and its release has come, before this CTA ends.
     // (After a wait that ran out these run out too, a second during which what is on its way lands.)
     for (int j = 0; j < filled; ++j) {
-      s = s == 0 ? (--ph, kPairStages - 1) : s - 1;
+      s = s == 0 ? (--ph, sh.stages - 1) : s - 1;
       if (!mbar_wait(&empty[s], ph & 1u)) break;
     }
     if (!ok && a.flags != nullptr) atomicOr(a.flags, a.bit);
   } else if (tid == 32 && rank == 0) {
     const uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(sh.tokens >> 3) << 17) | (16u << 24) |
                            (a.dtype == K2_BF16 ? (1u << 7) | (1u << 10) : 0u);
+    const uint64_t ring = smem_desc(smem);
     int s = 0;
     uint32_t ph = 0;
     bool ok = true;
@@ -458,46 +490,44 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       }
       tc_after();
       const uint32_t acc = tmem + b * kPairTokens;
-      for (int k = 0; k < sh.steps; ++k) {
+      for (int f = 0; f < fills; ++f) {
         if (!wait_for(&full[s], ph & 1u, a.limit_ns)) {
           ok = false;
           break;
         }
         tc_after();
-        const uint8_t* st = smem + s * kPairStage;
+        const uint64_t ad = ring + static_cast<uint32_t>(s * (stage >> 4));
+        const int count = min(kPairSteps, sh.steps - f * kPairSteps);
 #pragma unroll
-        for (int j = 0; j < kStepBytes / 32; ++j)
-          pair_mma<F8>(acc, smem_desc(st + j * 32), smem_desc(st + kRows * kStepBytes + j * 32), idesc, (k | j) != 0);
+        for (int q = 0; q < kPairSteps; ++q) {
+          if (q >= count) break;
+          const uint64_t at = ad + (q ? step_bytes >> 4 : 0);
+#pragma unroll
+          for (int j = 0; j < kStepBytes / 32; ++j)  // descriptors count 16 bytes
+            pair_mma<F8>(acc, at + 2 * j, at + (kRows * kStepBytes >> 4) + 2 * j, idesc, (f | q | j) != 0);
+        }
         pair_commit(&empty[s]);
-        if (++s == kPairStages) s = 0, ++ph;
+        if (++s == sh.stages) s = 0, ++ph;
       }
       if (ok) pair_commit(&accf[b]);
     }
     asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(&drain)) : "memory");
     if ((!mbar_wait(&drain, 0) || !ok) && a.flags != nullptr) atomicOr(a.flags, a.bit);
   } else if (warp >= 2) {
-    const int group = warp & 3, part = (warp - 2) >> 2;
-    const int c0 = part * (sh.tokens / 2), c1 = c0 + sh.tokens / 2;
+    const int group = warp & 3, columns = sh.tokens / 4, c0 = ((warp - 2) >> 2) * columns;
+    float* xs = x_scales[warp - 2];
     bool ok = true;
     for (int i = 0; i < mine; ++i) {
       const int b = i & 1, tile = pair + i * pairs, rt = tile / sh.token_tiles;
+      const int n = rt * 2 * kRows + rank * kRows + group * 32 + lane, t = (tile - rt * sh.token_tiles) * sh.tokens + c0;
+      __syncwarp();  // the last tile's scales have been read
+      for (int c = lane; c < columns; c += 32) xs[c] = a.x_scale != nullptr && t + c < a.tokens ? __ldg(a.x_scale + t + c) : 1.f;
+      __syncwarp();
       // once a wait has run out the rest of this CTA's tiles is NaN
       if (ok) ok = __all_sync(0xffffffffu, wait_for(&accf[b], static_cast<uint32_t>(i >> 1) & 1u, a.limit_ns));
       tc_after();
-      const uint32_t acc = tmem + b * kPairTokens + (static_cast<uint32_t>(group * 32) << 16);
-      const int n = rt * 2 * kRows + rank * kRows + group * 32 + lane, t0 = (tile - rt * sh.token_tiles) * sh.tokens;
-      if (a.act == K2_ACT_SWIGLU) {
-        if (a.out_dtype == K2_F32) finish_part<float, true>(a, acc, c0, c1, t0, n, ok);
-        else if (a.out_dtype == K2_BF16) finish_part<__nv_bfloat16, true>(a, acc, c0, c1, t0, n, ok);
-        else finish_part<__half, true>(a, acc, c0, c1, t0, n, ok);
-      } else {
-        if (a.out_dtype == K2_F32) finish_part<float, false>(a, acc, c0, c1, t0, n, ok);
-        else if (a.out_dtype == K2_BF16) finish_part<__nv_bfloat16, false>(a, acc, c0, c1, t0, n, ok);
-        else finish_part<__half, false>(a, acc, c0, c1, t0, n, ok);
-      }
-      tc_before();
-      __syncwarp();
-      if (lane == 0) arrive_at(first_cta(&acce[b]));
+      const uint32_t acc = tmem + b * kPairTokens + c0 + (static_cast<uint32_t>(group * 32) << 16), free = first_cta(&acce[b]);
+      finish_part<OT, ACT>(a, acc, xs, columns, t, n, ok, free);
     }
     if (!ok && lane == 0 && a.flags != nullptr) atomicOr(a.flags, a.bit);
   }
@@ -582,16 +612,30 @@ cudaError_t launch_tile(bool f8, const CUtensorMap& mw, const CUtensorMap& mx, c
             : launch_tile<BN, false>(mw, mx, a, place, steps, split, dev, s);
 }
 
-template <bool F8>
+template <bool F8, typename OT, int ACT>
 cudaError_t launch_pair(const CUtensorMap& mw, const CUtensorMap& mx, const LinearArgs& a, const WeightPlace& place,
                         const PairShape& sh, int sms, int dev, cudaStream_t s) {
-  auto kernel = linear_pair_kernel<F8>;
+  auto kernel = linear_pair_kernel<F8, OT, ACT>;
   static std::atomic<uint64_t> ready{0};
   const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), kPairSmem, dev, ready);
   if (e != cudaSuccess) return e;
   const int pairs = std::min(sms / 2, sh.row_tiles * sh.token_tiles);
   kernel<<<2 * pairs, kPairThreads, kPairSmem, s>>>(mw, mx, a, place, sh);
   return cudaGetLastError();
+}
+template <bool F8, typename OT>
+cudaError_t launch_pair(const CUtensorMap& mw, const CUtensorMap& mx, const LinearArgs& a, const WeightPlace& place,
+                        const PairShape& sh, int sms, int dev, cudaStream_t s) {
+  return a.act == K2_ACT_SWIGLU ? launch_pair<F8, OT, kPairsOfRows>(mw, mx, a, place, sh, sms, dev, s)
+         : a.act == K2_ACT_NONE ? launch_pair<F8, OT, kPlain>(mw, mx, a, place, sh, sms, dev, s)
+                                : launch_pair<F8, OT, kOther>(mw, mx, a, place, sh, sms, dev, s);
+}
+template <bool F8>
+cudaError_t launch_pair(const CUtensorMap& mw, const CUtensorMap& mx, const LinearArgs& a, const WeightPlace& place,
+                        const PairShape& sh, int sms, int dev, cudaStream_t s) {
+  return a.out_dtype == K2_F32    ? launch_pair<F8, float>(mw, mx, a, place, sh, sms, dev, s)
+         : a.out_dtype == K2_BF16 ? launch_pair<F8, __nv_bfloat16>(mw, mx, a, place, sh, sms, dev, s)
+                                  : launch_pair<F8, __half>(mw, mx, a, place, sh, sms, dev, s);
 }
 
 }  // namespace
@@ -605,15 +649,16 @@ k2_status launch_linear(const LinearWeights& w, const void* x, long long x_strid
     const bool f8 = a.dtype == K2_F8;
     const WeightPlace place = {w.packed ? 1 : 0, f8 ? kStepBytes : kStepBytes / 2};
     const int steps = (a.cols + place.step - 1) / place.step;
-    if (a.tokens > 256) {
+    if (a.tokens > 128) {
       // tiles as wide as leave the fewest columns to the pair with the most tiles
-      PairShape sh = {0, steps, (a.rows + 2 * kRows - 1) / (2 * kRows), 0};
+      PairShape sh = {0, steps, 0, (a.rows + 2 * kRows - 1) / (2 * kRows), 0};
       long long best = 0;
-      for (int n = kPairTokens; n >= 128; n -= 32) {
+      for (int n = kPairTokens; n >= 128; n -= 64) {
         const int tt = (a.tokens + n - 1) / n;
-        const long long cost = (static_cast<long long>(sh.row_tiles) * tt + sms / 2 - 1) / (sms / 2) * n;
+        const long long cost = (static_cast<long long>(sh.row_tiles) * tt + sms / 2 - 1) / (sms / 2) * (n + 224);
         if (sh.tokens == 0 || cost < best) sh.tokens = n, sh.token_tiles = tt, best = cost;
       }
+      sh.stages = std::min(kPairStages, kPairRing / (kPairSteps * (kRows + sh.tokens / 2) * kStepBytes));
       CUtensorMap mw, mx;
       if (!encode_weights(&mw, a.dtype, w, a.rows, a.cols) ||
           !encode_tokens(&mx, a.dtype, x, x_stride, a.cols, a.tokens, sh.tokens / 2)) {
