@@ -4,11 +4,10 @@
 //   z[t][n] = sum_k x[t][k] w[n][k]      (E4M3, bf16 or fp16 operands, exact products, fp32 sums in tensor memory)
 //   out[t][n] = act(z * w_scale[n] * x_scale[t] + bias[n]) + residual[t][n]
 //
-// The weights' 128-row tiles are the first operand (M), 16 to 128 tokens the second (N): few tokens then cost few columns and
-// not 128 rows.  Both arrive as K-major rows of 128 bytes by TMA (zeros behind the last row and behind the last value of a
-// row) through a ring of stages; one thread requests, one issues the MMAs.  Where there are fewer tiles than the SMs can
-// hold, a cluster of up to eight CTAs splits K; their sums are joined through distributed shared memory in the order of K, so
-// that the result does not depend on which CTA came first.
+// The weights' 128-row tiles are the first operand (M), the tokens the second (N): few tokens then cost few columns and not 128
+// rows.  Both arrive as K-major rows of 128 bytes by TMA (zeros behind the last row and behind the last value of a row) through
+// a ring of stages; one thread requests, one issues the MMAs.  Two kernels: for few tokens the weights' bytes bound the call
+// (linear_few_kernel), for many the tensor cores (linear_pair_kernel).
 #include <cuda.h>
 #include <math.h>
 
@@ -31,10 +30,10 @@ constexpr int kMaxSplit = 8;    // CTAs of a cluster (the portable limit)
 template <int BN>
 struct Tile {
   static constexpr int kA = kRows * kStepBytes, kB = BN * kStepBytes, kStage = kA + kB;
-  static constexpr int kStages = BN <= 32 ? 5 : BN == 64 ? 4 : 3;
+  static constexpr int kStages = BN == 16 ? 5 : BN == 32 ? 4 : 3;
   static constexpr int kRing = kStages * kStage;
-  static constexpr int kPart = BN * kRows * 4;  // a CTA's sums, over the ring
-  static constexpr int kSmem = (kRing > kPart ? kRing : kPart) + 1024;
+  static constexpr int kPart = (BN + kMaxSplit - 1) * kRows * 4;  // the sums that a CTA joins
+  static constexpr int kSmem = kRing + kPart + 1024;              // two CTAs fit an SM
   static constexpr int kCols = BN < 32 ? 32 : BN;
   static constexpr uint32_t kDesc = (1u << 4) | (static_cast<uint32_t>(BN >> 3) << 17) | (8u << 24);  // fp32 sums, M = 128
 };
@@ -60,26 +59,37 @@ __device__ __forceinline__ void load_4d(void* dst, const CUtensorMap* m, int c0,
       "l"(m), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_u32(bar))
       : "memory");
 }
+// Waits for a phase; false once limit_ns have passed (a single try may sleep for longer, so that counts as run out too).
 __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, unsigned long long limit_ns) {
-  if (mbar_try_wait(bar, parity)) return true;
+  uint32_t ready;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ready)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  if (ready) return true;
   const uint64_t t0 = globaltimer();
   while (!mbar_try_wait(bar, parity))
     if (globaltimer() - t0 > limit_ns) return false;
-  return true;
+  return globaltimer() - t0 <= limit_ns;
 }
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-__device__ __forceinline__ float4 peer_load(uint32_t addr, int rank) {
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+// the address in CTA `rank` of the cluster
+__device__ __forceinline__ uint32_t peer_address(uint32_t addr, int rank) {
   uint32_t at;
-  float4 v;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(addr), "r"(rank));
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(at)
-               : "memory");
-  return v;
+  return at;
 }
+__device__ __forceinline__ void peer_store(uint32_t at, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at), "f"(v) : "memory");
+}
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* m) { asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory"); }
 
 // the activations, in fp32
 __device__ __forceinline__ float activate(float z, int act) {
@@ -99,44 +109,36 @@ __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { retu
 template <>
 __device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
 
-__device__ __forceinline__ float load_out(const void* p, long long i, int dtype) {
-  if (dtype == K2_F32) return static_cast<const float*>(p)[i];
-  if (dtype == K2_BF16) return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
-  return __half2float(static_cast<const __half*>(p)[i]);
-}
-__device__ __forceinline__ void store_out(void* p, long long i, int dtype, float v) {
-  if (dtype == K2_F32) static_cast<float*>(p)[i] = v;
-  else if (dtype == K2_BF16) static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
-  else static_cast<__half*>(p)[i] = __float2half_rn(v);
-}
-
-// Four neighbouring sums z of token t, rows n .. n + 3 of the matrix
-__device__ __forceinline__ void finish(const LinearArgs& a, int t, int n, float4 z4) {
-  const float xs = a.x_scale != nullptr ? __ldg(a.x_scale + t) : 1.f;
+// What follows the sums of one token, of four neighbouring rows n .. n + 3 of the matrix.
+template <typename OT>
+__device__ __forceinline__ void finish_four(const LinearArgs& a, long long t, int n, float4 z4, float xs, const float (&ws)[4],
+                                            const float (&bias)[4]) {
   float z[4] = {z4.x, z4.y, z4.z, z4.w};
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    if (n + j >= a.rows) break;
-    if (a.w_scale != nullptr) z[j] = z[j] * __ldg(a.w_scale + n + j) * xs;
-    if (a.bias != nullptr) z[j] += __ldg(a.bias + n + j);
-  }
+  for (int j = 0; j < 4; ++j) z[j] = fmaf(z[j], ws[j] * xs, bias[j]);
   if (a.act == K2_ACT_SWIGLU) {
+    OT* out = static_cast<OT*>(a.out) + t * a.out_stride + (n >> 1);
+    const OT* res = static_cast<const OT*>(a.residual) + t * a.residual_stride + (n >> 1);
 #pragma unroll
-    for (int j = 0; j < 4; j += 2) {
-      if (n + j >= a.rows) break;
-      float y = z[j] / (1.0f + expf(-z[j])) * z[j + 1];
-      const int o = (n + j) >> 1;
-      if (a.residual != nullptr) y += load_out(a.residual, t * a.residual_stride + o, a.out_dtype);
-      store_out(a.out, t * a.out_stride + o, a.out_dtype, y);
+    for (int j = 0; j < 2; ++j) {
+      if (n + 2 * j >= a.rows) return;
+      float y = __fdividef(z[2 * j], 1.0f + __expf(-z[2 * j])) * z[2 * j + 1];
+      if (a.residual != nullptr) y += to_f32(res[j]);
+      out[j] = from_f32<OT>(y);
     }
     return;
   }
+  OT* out = static_cast<OT*>(a.out) + t * a.out_stride + n;
+  const OT* res = static_cast<const OT*>(a.residual) + t * a.residual_stride + n;
+  float r[4] = {0.f, 0.f, 0.f, 0.f};
+  if (a.residual != nullptr) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) r[j] = n + j < a.rows ? to_f32(res[j]) : 0.f;
+  }
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    if (n + j >= a.rows) break;
-    float y = activate(z[j], a.act);
-    if (a.residual != nullptr) y += load_out(a.residual, t * a.residual_stride + n + j, a.out_dtype);
-    store_out(a.out, t * a.out_stride + n + j, a.out_dtype, y);
+    const float y = activate(z[j], a.act);
+    if (n + j < a.rows) out[j] = from_f32<OT>(a.residual != nullptr ? y + r[j] : y);
   }
 }
 
@@ -151,10 +153,15 @@ __device__ __forceinline__ void load_weights(void* dst, const CUtensorMap* m, co
   else load_4d(dst, m, e, row, 0, 0, bar);
 }
 
-template <int BN, bool F8>
-__global__ void __launch_bounds__(128) linear_kernel(const __grid_constant__ CUtensorMap map_w,
-                                                     const __grid_constant__ CUtensorMap map_x, const LinearArgs a,
-                                                     const WeightPlace place, int steps, int split) {
+// ---- few tokens -----------------------------------------------------------------------------------------------------------
+//
+// A CTA per tile of 128 rows x BN tokens.  Where there are fewer tiles than SMs can hold, a cluster of up to eight CTAs splits K:
+// token j's sums go to CTA j % split, each CTA writing its share into that CTA's shared memory, and are added there in the
+// order of K, so that the result does not depend on which CTA came first.
+template <int BN, bool F8, typename OT>
+__global__ void __launch_bounds__(128) linear_few_kernel(const __grid_constant__ CUtensorMap map_w,
+                                                         const __grid_constant__ CUtensorMap map_x, const LinearArgs a,
+                                                         const WeightPlace place, int steps, int split) {
   using C = Tile<BN>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -165,7 +172,10 @@ __global__ void __launch_bounds__(128) linear_kernel(const __grid_constant__ CUt
   const int n0 = tile * kRows, t0 = blockIdx.y * BN;
   const int k0 = static_cast<int>(static_cast<long long>(steps) * rank / split);
   const int nk = static_cast<int>(static_cast<long long>(steps) * (rank + 1) / split) - k0;
+  if (split > 1) cluster_arrive();  // this CTA runs: its shared memory may be written to
   if (tid == 0) {
+    prefetch_map(&map_w);
+    prefetch_map(&map_x);
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
@@ -173,7 +183,7 @@ __global__ void __launch_bounds__(128) linear_kernel(const __grid_constant__ CUt
     mbar_init(&done, 1);
     fence_mbar_init();
   }
-  if (warp == 0) {
+  if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_slot)), "r"(C::kCols)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -182,6 +192,8 @@ __global__ void __launch_bounds__(128) linear_kernel(const __grid_constant__ CUt
   __syncthreads();
   tc_after();
   const uint32_t tmem = tmem_slot;
+  pdl_wait();  // what the call reads and writes may be the previous kernel's
+  pdl_trigger();
   bool ok = true;
   if (tid == 0) {
     int i = 0;
@@ -196,10 +208,11 @@ __global__ void __launch_bounds__(128) linear_kernel(const __grid_constant__ CUt
       load_weights(st, &map_w, place, k0 + i, n0, &full[s]);
       load_2d(st + C::kA, &map_x, (k0 + i) * place.step, t0, &full[s]);
     }
-    // no copy may be on its way when the ring becomes the place of the sums
+    // no copy may be on its way when this CTA ends
     for (int j = max(0, i - C::kStages); j < i; ++j) mbar_wait(&full[j % C::kStages], static_cast<uint32_t>(j / C::kStages) & 1u);
   } else if (tid == 32) {
     const uint32_t idesc = C::kDesc | (a.dtype == K2_BF16 ? (1u << 7) | (1u << 10) : 0u);
+    const uint64_t ring = smem_desc(smem);
     for (int i = 0; i < nk; ++i) {
       const int s = i % C::kStages;
       if (!wait_for(&full[s], static_cast<uint32_t>(i / C::kStages) & 1u, a.limit_ns)) {
@@ -207,59 +220,76 @@ __global__ void __launch_bounds__(128) linear_kernel(const __grid_constant__ CUt
         break;
       }
       tc_after();
-      const uint8_t* st = smem + s * C::kStage;
+      const uint64_t at = ring + static_cast<uint32_t>(s * (C::kStage >> 4));
 #pragma unroll
-      for (int j = 0; j < kStepBytes / 32; ++j) {
-        const uint64_t ad = smem_desc(st + j * 32), bd = smem_desc(st + C::kA + j * 32);
-        if (F8) mma_f8(tmem, ad, bd, idesc, (i | j) != 0);
-        else mma(tmem, ad, bd, idesc, (i | j) != 0);
+      for (int j = 0; j < kStepBytes / 32; ++j) {  // descriptors count 16 bytes
+        if (F8) mma_f8(tmem, at + 2 * j, at + (C::kA >> 4) + 2 * j, idesc, (i | j) != 0);
+        else mma(tmem, at + 2 * j, at + (C::kA >> 4) + 2 * j, idesc, (i | j) != 0);
       }
       mma_commit(&empty[s]);
     }
     mma_commit(&done);
+  }
+  // meanwhile: scales and biases of the four rows that this thread finishes
+  const int n = n0 + 4 * lane, tokens = min(BN, a.tokens - t0);
+  float ws[4], bias[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    ws[j] = a.w_scale != nullptr && n + j < a.rows ? __ldg(a.w_scale + n + j) : 1.f;
+    bias[j] = a.bias != nullptr && n + j < a.rows ? __ldg(a.bias + n + j) : 0.f;
+  }
+  if (split > 1) {
+    __syncwarp();
+    cluster_wait();  // the others run
   }
   __syncthreads();  // both roles have ended: what is waited for now are the MMAs that were issued
   ok = mbar_wait(&done, 0) && ok;
   ok = __syncthreads_and(ok);
   tc_after();
   if (!ok && tid == 0 && a.flags != nullptr) atomicOr(a.flags, a.bit);
-  // the sums as [token][row]: a warp's 32 rows of a token lie side by side
-  float* part = reinterpret_cast<float*>(smem);
-  constexpr int W = BN < 32 ? BN : 32;
+  // this thread's row of the sums, token by token, to the CTA that joins them: [rank][token / split][row]
+  float* part = reinterpret_cast<float*>(smem + C::kRing);
+  const int slots = (BN + split - 1) / split;
+  {
+    const uint32_t mine = smem_u32(part) + static_cast<uint32_t>(rank * slots * kRows + tid) * 4u;
+    int owner = 0;
+    uint32_t at = mine;
 #pragma unroll 1
-  for (int c = 0; c < BN; c += W) {
-    uint32_t v[W];
-    if constexpr (W == 32) tmem_ld32(tmem + (static_cast<uint32_t>(warp * 32) << 16) + c, v);
-    else tmem_ld16(tmem + (static_cast<uint32_t>(warp * 32) << 16) + c, v);
+    for (int c = 0; c < BN && c < tokens; c += 16) {
+      uint32_t v[16];
+      tmem_ld16(tmem + (static_cast<uint32_t>(warp * 32) << 16) + c, v);
 #pragma unroll
-    for (int j = 0; j < W; ++j) part[(c + j) * kRows + tid] = ok ? __uint_as_float(v[j]) : __uint_as_float(0x7FC00000u);
+      for (int j = 0; j < 16; ++j) {
+        if (c + j < tokens) peer_store(peer_address(at, owner), ok ? __uint_as_float(v[j]) : __uint_as_float(0x7FC00000u));
+        if (++owner == split) owner = 0, at += kRows * 4;
+      }
+    }
   }
   tc_before();
-  __syncthreads();
-  if (warp == 0) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::kCols) : "memory");
-  if (split > 1) cluster_sync();
-  // units of four rows of a token, shared among the cluster's CTAs
-  const int units = min(BN, a.tokens - t0) * (kRows / 4);
-  const int u1 = units * (rank + 1) / split;
-  for (int u = units * rank / split + tid; u < u1; u += 128) {
-    float4 z;
-    if (split == 1) {
-      z = reinterpret_cast<const float4*>(part)[u];
-    } else {
-      const uint32_t at = smem_u32(part) + static_cast<uint32_t>(u) * 16u;
-      float4 p[kMaxSplit];
-#pragma unroll
-      for (int r = 0; r < kMaxSplit; ++r)
-        if (r < split) p[r] = peer_load(at, r);
-      z = p[0];
-#pragma unroll
-      for (int r = 1; r < kMaxSplit; ++r)
-        if (r < split) z.x += p[r].x, z.y += p[r].y, z.z += p[r].z, z.w += p[r].w;
-    }
-    finish(a, t0 + (u >> 5), n0 + 4 * (u & 31), z);
+  if (split > 1) {
+    __syncwarp();
+    cluster_arrive();
+    cluster_wait();
+  } else {
+    __syncthreads();
   }
-  __syncwarp();
-  if (split > 1) cluster_sync();  // peers may still read this CTA's sums
+  for (int slot = warp; rank + slot * split < tokens; slot += 4) {
+    const long long t = t0 + rank + slot * split;
+    const float xs = a.x_scale != nullptr ? __ldg(a.x_scale + t) : 1.f;
+    const float4* from = reinterpret_cast<const float4*>(part + slot * kRows) + lane;
+    float4 z = from[0];
+#pragma unroll
+    for (int r = 1; r < kMaxSplit; ++r) {
+      if (r < split) {
+        const float4 p = from[r * slots * (kRows / 4)];
+        z.x += p.x, z.y += p.y, z.z += p.z, z.w += p.w;
+      }
+    }
+    finish_four<OT>(a, t, n, z, xs, ws, bias);
+  }
+  tc_after();
+  __syncthreads();  // every warp has read the accumulator
+  if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::kCols) : "memory");
 }
 
 // ---- many tokens: pairs of CTAs -------------------------------------------------------------------------------------------
@@ -422,6 +452,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   const int tiles = sh.row_tiles * sh.token_tiles, pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   const int mine = pair < tiles ? (tiles - 1 - pair) / pairs + 1 : 0;
   if (tid == 0) {
+    prefetch_map(&map_w);
+    prefetch_map(&map_x);
     for (int s = 0; s < sh.stages; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
@@ -442,6 +474,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   cluster_sync();  // both CTAs' barriers are ready
   tc_after();
   const uint32_t tmem = tmem_slot;
+  pdl_wait();  // what the call reads and writes may be the previous kernel's
+  pdl_trigger();
   if (tid == 0) {
     const int half = sh.tokens / 2;
     int s = 0, filled = 0;
@@ -585,11 +619,19 @@ bool encode_weights(CUtensorMap* m, int dtype, const LinearWeights& w, int rows,
   return encode(m, dtype, 4, w.base, dims, strides, box);
 }
 
-template <int BN, bool F8>
-cudaError_t launch_tile(const CUtensorMap& mw, const CUtensorMap& mx, const LinearArgs& a, const WeightPlace& place, int steps,
-                        int split, int dev, cudaStream_t s) {
+// launched as a dependent of the kernel before it: the start overlaps that kernel's end, then waits for all of it
+cudaLaunchAttribute early_start() {
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  return attr;
+}
+
+template <int BN, bool F8, typename OT>
+cudaError_t launch_few(const CUtensorMap& mw, const CUtensorMap& mx, const LinearArgs& a, const WeightPlace& place, int steps,
+                       int split, int dev, cudaStream_t s) {
   using C = Tile<BN>;
-  auto kernel = linear_kernel<BN, F8>;
+  auto kernel = linear_few_kernel<BN, F8, OT>;
   static std::atomic<uint64_t> ready{0};
   const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), C::kSmem, dev, ready);
   if (e != cudaSuccess) return e;
@@ -598,18 +640,26 @@ cudaError_t launch_tile(const CUtensorMap& mw, const CUtensorMap& mx, const Line
   cfg.blockDim = dim3(128);
   cfg.dynamicSmemBytes = C::kSmem;
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim = {static_cast<unsigned>(split), 1, 1};
+  cudaLaunchAttribute attr[2] = {early_start(), {}};
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = split;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = split > 1 ? 1 : 0;
+  cfg.numAttrs = split > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, mw, mx, a, place, steps, split);
 }
+template <int BN, bool F8>
+cudaError_t launch_few(const CUtensorMap& mw, const CUtensorMap& mx, const LinearArgs& a, const WeightPlace& place, int steps,
+                       int split, int dev, cudaStream_t s) {
+  return a.out_dtype == K2_F32    ? launch_few<BN, F8, float>(mw, mx, a, place, steps, split, dev, s)
+         : a.out_dtype == K2_BF16 ? launch_few<BN, F8, __nv_bfloat16>(mw, mx, a, place, steps, split, dev, s)
+                                  : launch_few<BN, F8, __half>(mw, mx, a, place, steps, split, dev, s);
+}
 template <int BN>
-cudaError_t launch_tile(bool f8, const CUtensorMap& mw, const CUtensorMap& mx, const LinearArgs& a, const WeightPlace& place,
-                        int steps, int split, int dev, cudaStream_t s) {
-  return f8 ? launch_tile<BN, true>(mw, mx, a, place, steps, split, dev, s)
-            : launch_tile<BN, false>(mw, mx, a, place, steps, split, dev, s);
+cudaError_t launch_few(bool f8, const CUtensorMap& mw, const CUtensorMap& mx, const LinearArgs& a, const WeightPlace& place,
+                       int steps, int split, int dev, cudaStream_t s) {
+  return f8 ? launch_few<BN, true>(mw, mx, a, place, steps, split, dev, s)
+            : launch_few<BN, false>(mw, mx, a, place, steps, split, dev, s);
 }
 
 template <bool F8, typename OT, int ACT>
@@ -620,8 +670,15 @@ cudaError_t launch_pair(const CUtensorMap& mw, const CUtensorMap& mx, const Line
   const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), kPairSmem, dev, ready);
   if (e != cudaSuccess) return e;
   const int pairs = std::min(sms / 2, sh.row_tiles * sh.token_tiles);
-  kernel<<<2 * pairs, kPairThreads, kPairSmem, s>>>(mw, mx, a, place, sh);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * pairs);
+  cfg.blockDim = dim3(kPairThreads);
+  cfg.dynamicSmemBytes = kPairSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1] = {early_start()};
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, mw, mx, a, place, sh);
 }
 template <bool F8, typename OT>
 cudaError_t launch_pair(const CUtensorMap& mw, const CUtensorMap& mx, const LinearArgs& a, const WeightPlace& place,
@@ -670,7 +727,7 @@ k2_status launch_linear(const LinearWeights& w, const void* x, long long x_strid
       set_error("linear launch: %s", cudaGetErrorString(e));
       return K2_ERR_CUDA;
     }
-    const int bn = a.tokens <= 16 ? 16 : a.tokens <= 32 ? 32 : a.tokens <= 64 ? 64 : 128;
+    const int bn = a.tokens <= 16 ? 16 : a.tokens <= 32 ? 32 : 64;
     const long long tiles = static_cast<long long>((a.rows + kRows - 1) / kRows) * ((a.tokens + bn - 1) / bn);
     const int split = static_cast<int>(std::max<long long>(1, std::min<long long>({2ll * sms / tiles, kMaxSplit, steps})));
     CUtensorMap mw, mx;
@@ -678,10 +735,9 @@ k2_status launch_linear(const LinearWeights& w, const void* x, long long x_strid
       set_error("no tensor map for %d x %d weights and %d tokens", a.rows, a.cols, a.tokens);
       return K2_ERR_CUDA;
     }
-    e = bn == 16   ? launch_tile<16>(f8, mw, mx, a, place, steps, split, dev, s)
-        : bn == 32 ? launch_tile<32>(f8, mw, mx, a, place, steps, split, dev, s)
-        : bn == 64 ? launch_tile<64>(f8, mw, mx, a, place, steps, split, dev, s)
-                   : launch_tile<128>(f8, mw, mx, a, place, steps, split, dev, s);
+    e = bn == 16   ? launch_few<16>(f8, mw, mx, a, place, steps, split, dev, s)
+        : bn == 32 ? launch_few<32>(f8, mw, mx, a, place, steps, split, dev, s)
+                   : launch_few<64>(f8, mw, mx, a, place, steps, split, dev, s);
   }
   if (e == cudaSuccess) return K2_OK;
   set_error("linear launch: %s", cudaGetErrorString(e));

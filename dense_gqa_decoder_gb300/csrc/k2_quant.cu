@@ -39,6 +39,8 @@ struct RowArgs {
   float* scales;
 };
 
+int row_type_bytes(int dtype) { return dtype == K2_F32 ? 4 : dtype == K2_BF16 || dtype == K2_F16 ? 2 : 0; }
+
 struct None {};
 
 template <typename T>
@@ -86,7 +88,200 @@ __device__ __forceinline__ unsigned block_max(unsigned v, unsigned* part) {
 // A finite row whose squares overflow is summed in units of 2^80, where 49152 of the largest squares stay below 2^112.
 constexpr float kUnit = 0x1p-80f;
 
-// Any row: one CTA, the values as fp32 in shared memory, element by element.
+// ---- rows of whole 8-value vectors at aligned places ------------------------------------------------------------------
+//
+// A CTA per row, V vectors of 8 values per thread in registers.  The norm's groups hold whole vectors and are at most kGroups,
+// so that a thread adds its squares into one of as many sums.
+constexpr int kGroups = 4;
+
+template <typename T>
+struct Eight;  // 8 values at a 16-byte aligned place
+template <>
+struct Eight<float> {
+  __device__ __forceinline__ static void load(const float* p, float* f) {
+    const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+    f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+  }
+  __device__ __forceinline__ static void store(float* p, const float* f) {
+    *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
+    *reinterpret_cast<float4*>(p + 4) = make_float4(f[4], f[5], f[6], f[7]);
+  }
+};
+template <>
+struct Eight<__nv_bfloat16> {
+  __device__ __forceinline__ static void load(const __nv_bfloat16* p, float* f) {
+    Unpack<__nv_bfloat16>::run(*reinterpret_cast<const uint4*>(p), f);
+  }
+  __device__ __forceinline__ static void store(__nv_bfloat16* p, const float* f) {
+    uint4 v;
+    __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&v);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+    *reinterpret_cast<uint4*>(p) = v;
+  }
+};
+template <>
+struct Eight<__half> {
+  __device__ __forceinline__ static void load(const __half* p, float* f) {
+    Unpack<__half>::run(*reinterpret_cast<const uint4*>(p), f);
+  }
+  __device__ __forceinline__ static void store(__half* p, const float* f) {
+    uint4 v;
+    __half2* h = reinterpret_cast<__half2*>(&v);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h[i] = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
+    *reinterpret_cast<uint4*>(p) = v;
+  }
+};
+__device__ __forceinline__ void load_gain8(const void* g, int dtype, int i, float* f) {
+  if (dtype == K2_F32) Eight<float>::load(static_cast<const float*>(g) + i, f);
+  else if (dtype == K2_BF16) Eight<__nv_bfloat16>::load(static_cast<const __nv_bfloat16*>(g) + i, f);
+  else Eight<__half>::load(static_cast<const __half*>(g) + i, f);
+}
+
+__device__ __forceinline__ uint2 codes_of(const float* y, float s) {
+  uint32_t w[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(__fdiv_rn(y[4 * i], s), __fdiv_rn(y[4 * i + 1], s)), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(__fdiv_rn(y[4 * i + 2], s), __fdiv_rn(y[4 * i + 3], s)), __NV_SATFINITE, __NV_E4M3);
+    w[i] = lo | hi << 16;
+  }
+  return make_uint2(w[0], w[1]);
+}
+
+template <typename XT, typename RT, bool NORM, int V>
+__global__ void __launch_bounds__(1024) vector_rows_kernel(const RowArgs a) {
+  __shared__ float sums[kGroups][32];
+  __shared__ unsigned tops[32];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, warps = blockDim.x >> 5;
+  const int n8 = a.cols >> 3, size8 = NORM ? n8 / a.groups : n8;  // vectors of a row, of a group
+  pdl_wait();  // the rows may be the previous kernel's
+  pdl_trigger();
+  const long long t = blockIdx.x;
+  const XT* x = static_cast<const XT*>(a.x) + a.x_stride * t;
+  float h[V][8];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int v = tid + i * blockDim.x;
+    if (v < n8) Eight<XT>::load(x + 8 * v, h[i]);
+    else
+#pragma unroll
+      for (int j = 0; j < 8; ++j) h[i][j] = 0.f;
+  }
+  if constexpr (!std::is_same<RT, None>::value) {
+    const RT* res = static_cast<const RT*>(a.res) + a.res_stride * t;
+    RT* res_out = static_cast<RT*>(a.res_out) + a.res_out_stride * t;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int v = tid + i * blockDim.x;
+      if (v < n8) {
+        float r[8];
+        Eight<RT>::load(res + 8 * v, r);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) h[i][j] += r[j];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int v = tid + i * blockDim.x;
+      if (v < n8) Eight<RT>::store(res_out + 8 * v, h[i]);
+    }
+  }
+  unsigned top = 0;
+  if constexpr (NORM) {
+    float gain[V][8];  // loaded ahead of the sums
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int v = tid + i * blockDim.x;
+      if (v < n8) load_gain8(a.gain, a.gain_dtype, 8 * v, gain[i]);
+    }
+    int group[V];
+    float factor[kGroups], unit[kGroups];
+#pragma unroll
+    for (int i = 0; i < V; ++i) group[i] = (tid + i * static_cast<int>(blockDim.x)) / size8;
+    const float count = static_cast<float>(8 * size8);
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) unit[g] = 1.f;
+    // the second pass is taken where the squares of a finite row overflow (or one is not finite), in units of kUnit
+    for (bool again = false;; again = true) {
+      float ss[kGroups] = {};
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g) {
+          float sq = 0.f;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) sq = fmaf(h[i][j] * unit[g], h[i][j] * unit[g], sq);
+          if (group[i] == g) ss[g] += sq;
+          if (g + 1 == a.groups) break;
+        }
+      }
+      if (again) __syncthreads();
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g) {
+        const float w = warp_sum(ss[g]);
+        if (lane == 0) sums[g][warp] = w;
+        if (g + 1 == a.groups) break;
+      }
+      __syncthreads();
+      bool over = false;
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g) {
+        const float sum = warp_sum(lane < warps ? sums[g][lane] : 0.f);
+        const float mean = sum / count + a.eps * unit[g] * unit[g];
+        factor[g] = 1.0f / sqrtf(mean);
+        if (!again && !(mean <= 3.4028235e38f)) unit[g] = kUnit, over = true;
+        if (g + 1 == a.groups) break;
+      }
+      if (!over) break;
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      float u = unit[0], f = factor[0];
+#pragma unroll
+      for (int g = 1; g < kGroups; ++g)
+        if (group[i] == g) u = unit[g], f = factor[g];
+      if (tid + i * static_cast<int>(blockDim.x) < n8) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          h[i][j] = h[i][j] * u * f * gain[i][j];
+          top = max(top, magnitude(h[i][j]));
+        }
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) top = max(top, magnitude(h[i][j]));
+  }
+  top = __reduce_max_sync(0xffffffffu, top);
+  if (lane == 0) tops[warp] = top;
+  __syncthreads();
+  top = __reduce_max_sync(0xffffffffu, lane < warps ? tops[lane] : 0u);
+  const bool fine = top < 0x7F800000u;
+  const float s = fine ? __uint_as_float(top) / kTop : __uint_as_float(0x7FC00000u);
+  uint8_t* codes = a.codes + a.codes_stride * t;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int v = tid + i * blockDim.x;
+    if (v < n8)
+      *reinterpret_cast<uint2*>(codes + 8 * v) = !fine   ? make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu)
+                                                 : s > 0.f ? codes_of(h[i], s)
+                                                           : make_uint2(0u, 0u);
+  }
+  if (tid == 0) a.scales[t] = s;
+}
+
+bool at8(const void* p, long long stride, int bytes) {  // 8 values of `bytes` (at most 16 bytes at once) can be taken together
+  const int step = std::min(16, 8 * bytes);
+  return reinterpret_cast<uintptr_t>(p) % step == 0 && stride * bytes % step == 0;
+}
+
+// ---- any row ----------------------------------------------------------------------------------------------------------
+//
+// One CTA, the values as fp32 in shared memory, element by element.
 template <typename XT, typename RT, bool NORM>
 __global__ void __launch_bounds__(256) rows_kernel(RowArgs a) {
   extern __shared__ float row[];
@@ -96,6 +291,8 @@ __global__ void __launch_bounds__(256) rows_kernel(RowArgs a) {
   const XT* x = static_cast<const XT*>(a.x) + a.x_stride * t;
   uint8_t* codes = a.codes + a.codes_stride * t;
   unsigned top = 0;
+  pdl_wait();
+  pdl_trigger();
   for (int i = tid; i < n; i += 256) {
     float h = to_f32(x[i]);
     if constexpr (!std::is_same<RT, None>::value) {
@@ -135,17 +332,43 @@ __global__ void __launch_bounds__(256) rows_kernel(RowArgs a) {
   if (tid == 0) a.scales[t] = s;
 }
 
+template <typename K>
+cudaError_t launch_early(K kernel, const RowArgs& a, int tokens, int threads, size_t smem, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(tokens);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // the start overlaps the end of the kernel before it
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
 template <typename XT, typename RT, bool NORM>
 cudaError_t launch_rows(const RowArgs& a, int tokens, cudaStream_t s) {
-  auto kernel = rows_kernel<XT, RT, NORM>;
-  static std::atomic<uint64_t> ready{0};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  constexpr int rb = std::is_same<RT, None>::value ? 4 : sizeof(RT);
+  const int n8 = a.cols / 8;
+  const bool whole = a.cols % 8 == 0 && n8 <= 4096 && at8(a.x, a.x_stride, sizeof(XT)) && at8(a.codes, a.codes_stride, 1) &&
+                     at8(a.res, a.res_stride, rb) && at8(a.res_out, a.res_out_stride, rb);
+  if (whole && (!NORM || (a.groups <= kGroups && n8 % a.groups == 0 && at8(a.gain, 0, row_type_bytes(a.gain_dtype))))) {
+    // few rows: as many threads as there are vectors; many: a few vectors each, so that more rows are on their way at once
+    const int v = n8 <= 96 ? 1 : n8 <= 640 ? 2 : 4;
+    const int threads = ((n8 + v - 1) / v + 31) / 32 * 32;
+    if (v == 1) return launch_early(vector_rows_kernel<XT, RT, NORM, 1>, a, tokens, threads, 0, s);
+    if (v == 2) return launch_early(vector_rows_kernel<XT, RT, NORM, 2>, a, tokens, threads, 0, s);
+    return launch_early(vector_rows_kernel<XT, RT, NORM, 4>, a, tokens, threads, 0, s);
+  }
+  static std::atomic<uint64_t> ready{0};
+  auto kernel = rows_kernel<XT, RT, NORM>;
   e = allow_smem(reinterpret_cast<const void*>(kernel), kMaxCols * static_cast<int>(sizeof(float)), dev, ready);
   if (e != cudaSuccess) return e;
-  kernel<<<tokens, 256, a.cols * sizeof(float), s>>>(a);
-  return cudaGetLastError();
+  return launch_early(kernel, a, tokens, 256, a.cols * sizeof(float), s);
 }
 
 template <typename XT>
@@ -156,7 +379,6 @@ cudaError_t launch_norm(const RowArgs& a, int res_dtype, int tokens, cudaStream_
   return launch_rows<XT, __half, true>(a, tokens, s);
 }
 
-int row_type_bytes(int dtype) { return dtype == K2_F32 ? 4 : dtype == K2_BF16 || dtype == K2_F16 ? 2 : 0; }
 bool off_type(const void* p, int bytes) { return reinterpret_cast<uintptr_t>(p) % bytes != 0; }
 
 // What both calls refuse of their input rows, codes and scales
