@@ -60,6 +60,11 @@ __device__ __forceinline__ float load_gain(const void* g, int dtype, int i) {
 
 // |v| as a number that grows with it and is largest for a NaN
 __device__ __forceinline__ unsigned magnitude(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
+// the larger of m and |v|; a NaN wins
+__device__ __forceinline__ float max_magnitude(float m, float v) {
+  asm("max.NaN.f32 %0, %0, %1;" : "+f"(m) : "f"(fabsf(v)));
+  return m;
+}
 
 __device__ __forceinline__ uint32_t code_of(float y, float s) {
   return __nv_cvt_float_to_fp8(__fdiv_rn(y, s), __NV_SATFINITE, __NV_E4M3);
@@ -139,139 +144,219 @@ __device__ __forceinline__ void load_gain8(const void* g, int dtype, int i, floa
   else Eight<__half>::load(static_cast<const __half*>(g) + i, f);
 }
 
-__device__ __forceinline__ uint2 codes_of(const float* y, float s) {
-  uint32_t w[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(__fdiv_rn(y[4 * i], s), __fdiv_rn(y[4 * i + 1], s)), __NV_SATFINITE, __NV_E4M3);
-    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(__fdiv_rn(y[4 * i + 2], s), __fdiv_rn(y[4 * i + 3], s)), __NV_SATFINITE, __NV_E4M3);
-    w[i] = lo | hi << 16;
+__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
+  return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3) |
+         static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3)) << 16;
+}
+__device__ __noinline__ uint2 codes_by_division(const float4 a, const float4 b, float s) {
+  return make_uint2(codes4(__fdiv_rn(a.x, s), __fdiv_rn(a.y, s), __fdiv_rn(a.z, s), __fdiv_rn(a.w, s)),
+                    codes4(__fdiv_rn(b.x, s), __fdiv_rn(b.y, s), __fdiv_rn(b.z, s), __fdiv_rn(b.w, s)));
+}
+// A row's scale and what its values are multiplied with in place of the division: the quotient's code lies between the codes of
+// the two products (each is off by less than 2^-22 to its side, the quotient by 2^-24), and where those are the same, as for
+// all but one value in 10^5, it is that.  A power of two has an exact reciprocal.  (With a division per value 8192 x 10240
+// took 59.5 us.)
+struct RowScale {
+  float s, low, high;
+  bool fine, exact;  // all values finite; the products bound the quotient
+  __device__ __forceinline__ explicit RowScale(unsigned top) {
+    fine = top < 0x7F800000u;
+    s = fine ? __uint_as_float(top) / kTop : __uint_as_float(0x7FC00000u);
+    const float r = __frcp_rn(s);
+    const bool power = (__float_as_uint(s) & 0x007FFFFFu) == 0;
+    low = power ? r : r * (1.0f - 0x1p-22f);
+    high = power ? r : r * (1.0f + 0x1p-22f);
+    exact = s >= 0x1p-120f && s <= 0x1p120f;
   }
-  return make_uint2(w[0], w[1]);
+  __device__ __forceinline__ uint2 codes(const float* y) const {
+    if (!fine) return make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
+    if (exact) {
+      const uint2 l = make_uint2(codes4(y[0] * low, y[1] * low, y[2] * low, y[3] * low),
+                                 codes4(y[4] * low, y[5] * low, y[6] * low, y[7] * low));
+      const uint2 h = make_uint2(codes4(y[0] * high, y[1] * high, y[2] * high, y[3] * high),
+                                 codes4(y[4] * high, y[5] * high, y[6] * high, y[7] * high));
+      if (l.x == h.x && l.y == h.y) return l;
+    }
+    if (s == 0.f) return make_uint2(0u, 0u);
+    return codes_by_division(make_float4(y[0], y[1], y[2], y[3]), make_float4(y[4], y[5], y[6], y[7]), s);
+  }
+};
+
+// 8 values as they are held until their row's maximum is known: fp32, or the 16-bit values themselves
+template <typename T>
+struct Held {
+  uint4 bits = {0, 0, 0, 0};
+  __device__ __forceinline__ void load(const T* p) { bits = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void values(float* f) const { Unpack<T>::run(bits, f); }
+};
+template <>
+struct Held<float> {
+  float f8[8] = {};
+  __device__ __forceinline__ void load(const float* p) { Eight<float>::load(p, f8); }
+  __device__ __forceinline__ void values(float* f) const {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] = f8[j];
+  }
+};
+
+constexpr int kVectorThreads = 512;
+
+// the largest of the CTA's values, as a magnitude, in every thread
+__device__ __forceinline__ unsigned top_of(float top, unsigned* tops) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+  const unsigned m = __reduce_max_sync(0xffffffffu, magnitude(top));
+  if (warps == 1) return m;
+  if (lane == 0) tops[warp] = m;
+  __syncthreads();
+  return __reduce_max_sync(0xffffffffu, lane < warps ? tops[lane] : 0u);
 }
 
-template <typename XT, typename RT, bool NORM, int V>
-__global__ void __launch_bounds__(1024) vector_rows_kernel(const RowArgs a) {
+template <typename T, int V>
+__global__ void __launch_bounds__(kVectorThreads) vector_quantize_kernel(const RowArgs a) {
+  __shared__ unsigned tops[32];
+  const int tid = threadIdx.x, n8 = a.cols >> 3;
+  const long long t = blockIdx.x;
+  const T* x = static_cast<const T*>(a.x) + a.x_stride * t;
+  uint8_t* codes = a.codes + a.codes_stride * t;
+  pdl_wait();  // the rows may be the previous kernel's
+  pdl_trigger();
+  Held<T> h[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+    if (tid + i * static_cast<int>(blockDim.x) < n8) h[i].load(x + 8 * (tid + i * blockDim.x));
+  float top = 0.f;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    float f[8];
+    h[i].values(f);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) top = max_magnitude(top, f[j]);
+  }
+  const RowScale scale(top_of(top, tops));
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int v = tid + i * blockDim.x;
+    if (v < n8) {
+      float f[8];
+      h[i].values(f);
+      *reinterpret_cast<uint2*>(codes + 8 * v) = scale.codes(f);
+    }
+  }
+  if (tid == 0) a.scales[t] = scale.s;
+}
+
+template <typename XT, typename RT, int V>
+__global__ void __launch_bounds__(kVectorThreads) vector_norm_kernel(const RowArgs a) {
   __shared__ float sums[kGroups][32];
   __shared__ unsigned tops[32];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, warps = blockDim.x >> 5;
-  const int n8 = a.cols >> 3, size8 = NORM ? n8 / a.groups : n8;  // vectors of a row, of a group
+  const int n8 = a.cols >> 3, size8 = n8 / a.groups;  // vectors of a row, of a group
+  const long long t = blockIdx.x;
+  int group[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) group[i] = (tid + i * static_cast<int>(blockDim.x)) / size8;  // >= groups: none
   pdl_wait();  // the rows may be the previous kernel's
   pdl_trigger();
-  const long long t = blockIdx.x;
   const XT* x = static_cast<const XT*>(a.x) + a.x_stride * t;
-  float h[V][8];
+  float h[V][8] = {};
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const int v = tid + i * blockDim.x;
     if (v < n8) Eight<XT>::load(x + 8 * v, h[i]);
-    else
-#pragma unroll
-      for (int j = 0; j < 8; ++j) h[i][j] = 0.f;
   }
   if constexpr (!std::is_same<RT, None>::value) {
     const RT* res = static_cast<const RT*>(a.res) + a.res_stride * t;
     RT* res_out = static_cast<RT*>(a.res_out) + a.res_out_stride * t;
+    Held<RT> r[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int v = tid + i * blockDim.x;
-      if (v < n8) {
-        float r[8];
-        Eight<RT>::load(res + 8 * v, r);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) h[i][j] += r[j];
-      }
+      if (v < n8) r[i].load(res + 8 * v);
     }
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int v = tid + i * blockDim.x;
+      float f[8];
+      r[i].values(f);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) h[i][j] += f[j];
       if (v < n8) Eight<RT>::store(res_out + 8 * v, h[i]);
     }
   }
-  unsigned top = 0;
-  if constexpr (NORM) {
-    float gain[V][8];  // loaded ahead of the sums
+  // every thread's sums of each group, joined; `unit`: what the values are multiplied with first
+  const float count = static_cast<float>(8 * size8);
+  float mean[kGroups];
+  auto means = [&](float unit) {
+    float ss[kGroups] = {};
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int v = tid + i * blockDim.x;
-      if (v < n8) load_gain8(a.gain, a.gain_dtype, 8 * v, gain[i]);
-    }
-    int group[V];
-    float factor[kGroups], unit[kGroups];
+      float sq = 0.f;
 #pragma unroll
-    for (int i = 0; i < V; ++i) group[i] = (tid + i * static_cast<int>(blockDim.x)) / size8;
-    const float count = static_cast<float>(8 * size8);
-#pragma unroll
-    for (int g = 0; g < kGroups; ++g) unit[g] = 1.f;
-    // the second pass is taken where the squares of a finite row overflow (or one is not finite), in units of kUnit
-    for (bool again = false;; again = true) {
-      float ss[kGroups] = {};
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-#pragma unroll
-        for (int g = 0; g < kGroups; ++g) {
-          float sq = 0.f;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) sq = fmaf(h[i][j] * unit[g], h[i][j] * unit[g], sq);
-          if (group[i] == g) ss[g] += sq;
-          if (g + 1 == a.groups) break;
-        }
+      for (int j = 0; j < 8; ++j) {
+        const float e = h[i][j] * unit;
+        sq = fmaf(e, e, sq);
       }
-      if (again) __syncthreads();
 #pragma unroll
-      for (int g = 0; g < kGroups; ++g) {
-        const float w = warp_sum(ss[g]);
-        if (lane == 0) sums[g][warp] = w;
-        if (g + 1 == a.groups) break;
-      }
-      __syncthreads();
-      bool over = false;
-#pragma unroll
-      for (int g = 0; g < kGroups; ++g) {
-        const float sum = warp_sum(lane < warps ? sums[g][lane] : 0.f);
-        const float mean = sum / count + a.eps * unit[g] * unit[g];
-        factor[g] = 1.0f / sqrtf(mean);
-        if (!again && !(mean <= 3.4028235e38f)) unit[g] = kUnit, over = true;
-        if (g + 1 == a.groups) break;
-      }
-      if (!over) break;
+      for (int g = 0; g < kGroups; ++g) ss[g] += group[i] == g ? sq : 0.f;
     }
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      float u = unit[0], f = factor[0];
-#pragma unroll
-      for (int g = 1; g < kGroups; ++g)
-        if (group[i] == g) u = unit[g], f = factor[g];
-      if (tid + i * static_cast<int>(blockDim.x) < n8) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          h[i][j] = h[i][j] * u * f * gain[i][j];
-          top = max(top, magnitude(h[i][j]));
-        }
-      }
+    for (int g = 0; g < kGroups; ++g) {
+      if (g >= a.groups) break;
+      const float w = warp_sum(ss[g]);
+      if (lane == 0) sums[g][warp] = w;
     }
-  } else {
+    __syncthreads();
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) {
+      if (g >= a.groups) break;
+      mean[g] = warp_sum(lane < warps ? sums[g][lane] : 0.f) / count + a.eps * unit * unit;
+    }
+  };
+  means(1.f);
+  bool over = false;  // the squares of a finite row overflow (or a value is not finite): those groups in other units
+#pragma unroll
+  for (int g = 0; g < kGroups; ++g) over |= g < a.groups && !(mean[g] <= 3.4028235e38f);
+  if (over) {
+    float first[kGroups];
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) first[g] = mean[g];
+    __syncthreads();  // the sums have been read
+    means(kUnit);
 #pragma unroll
     for (int i = 0; i < V; ++i)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) top = max(top, magnitude(h[i][j]));
+      for (int g = 0; g < kGroups; ++g)
+        if (g < a.groups && group[i] == g && !(first[g] <= 3.4028235e38f))
+#pragma unroll
+          for (int j = 0; j < 8; ++j) h[i][j] *= kUnit;
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g)
+      if (g < a.groups && first[g] <= 3.4028235e38f) mean[g] = first[g];
   }
-  top = __reduce_max_sync(0xffffffffu, top);
-  if (lane == 0) tops[warp] = top;
-  __syncthreads();
-  top = __reduce_max_sync(0xffffffffu, lane < warps ? tops[lane] : 0u);
-  const bool fine = top < 0x7F800000u;
-  const float s = fine ? __uint_as_float(top) / kTop : __uint_as_float(0x7FC00000u);
+  float top = 0.f, factor[kGroups];
+#pragma unroll
+  for (int g = 0; g < kGroups; ++g) factor[g] = g < a.groups ? 1.0f / sqrtf(mean[g]) : 0.f;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    float f = factor[0], gain[8] = {};
+#pragma unroll
+    for (int g = 1; g < kGroups; ++g) f = group[i] == g ? factor[g] : f;
+    const int v = tid + i * blockDim.x;
+    if (v < n8) load_gain8(a.gain, a.gain_dtype, 8 * v, gain);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      h[i][j] = v < n8 ? h[i][j] * f * gain[j] : 0.f;
+      top = max_magnitude(top, h[i][j]);
+    }
+  }
+  const RowScale scale(top_of(top, tops));
   uint8_t* codes = a.codes + a.codes_stride * t;
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const int v = tid + i * blockDim.x;
-    if (v < n8)
-      *reinterpret_cast<uint2*>(codes + 8 * v) = !fine   ? make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu)
-                                                 : s > 0.f ? codes_of(h[i], s)
-                                                           : make_uint2(0u, 0u);
+    if (v < n8) *reinterpret_cast<uint2*>(codes + 8 * v) = scale.codes(h[i]);
   }
-  if (tid == 0) a.scales[t] = s;
+  if (tid == 0) a.scales[t] = scale.s;
 }
 
 bool at8(const void* p, long long stride, int bytes) {  // 8 values of `bytes` (at most 16 bytes at once) can be taken together
@@ -354,15 +439,20 @@ cudaError_t launch_rows(const RowArgs& a, int tokens, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   constexpr int rb = std::is_same<RT, None>::value ? 4 : sizeof(RT);
   const int n8 = a.cols / 8;
-  const bool whole = a.cols % 8 == 0 && n8 <= 4096 && at8(a.x, a.x_stride, sizeof(XT)) && at8(a.codes, a.codes_stride, 1) &&
+  const bool whole = a.cols % 8 == 0 && n8 <= (NORM ? 4 : 8) * kVectorThreads && at8(a.x, a.x_stride, sizeof(XT)) && at8(a.codes, a.codes_stride, 1) &&
                      at8(a.res, a.res_stride, rb) && at8(a.res_out, a.res_out_stride, rb);
   if (whole && (!NORM || (a.groups <= kGroups && n8 % a.groups == 0 && at8(a.gain, 0, row_type_bytes(a.gain_dtype))))) {
-    // few rows: as many threads as there are vectors; many: a few vectors each, so that more rows are on their way at once
-    const int v = n8 <= 96 ? 1 : n8 <= 640 ? 2 : 4;
+    const int v = n8 <= 96 ? 1 : n8 <= 640 ? 2 : n8 <= 4 * kVectorThreads ? 4 : 8;
     const int threads = ((n8 + v - 1) / v + 31) / 32 * 32;
-    if (v == 1) return launch_early(vector_rows_kernel<XT, RT, NORM, 1>, a, tokens, threads, 0, s);
-    if (v == 2) return launch_early(vector_rows_kernel<XT, RT, NORM, 2>, a, tokens, threads, 0, s);
-    return launch_early(vector_rows_kernel<XT, RT, NORM, 4>, a, tokens, threads, 0, s);
+    auto go = [&](auto vectors) {
+      constexpr int V = decltype(vectors)::value;
+      if constexpr (NORM) return launch_early(vector_norm_kernel<XT, RT, V>, a, tokens, threads, 0, s);
+      else return launch_early(vector_quantize_kernel<XT, V>, a, tokens, threads, 0, s);
+    };
+    if (v == 1) return go(std::integral_constant<int, 1>());
+    if (v == 2) return go(std::integral_constant<int, 2>());
+    if (v == 4) return go(std::integral_constant<int, 4>());
+    if constexpr (!NORM) return go(std::integral_constant<int, 8>());
   }
   static std::atomic<uint64_t> ready{0};
   auto kernel = rows_kernel<XT, RT, NORM>;
