@@ -18,6 +18,7 @@
 
 #include "../../include/k2.h"
 #include "k2_kernels.h"
+#include "k2_linear.h"
 #include "k2_serve.h"
 
 using namespace k2;
@@ -55,6 +56,9 @@ struct Layout {
   size_t wqkv_layer, wo_layer, wgu_layer, wdown_layer;
   // fp8 weights with a tensor-core prefill: the codes as bf16 in the bf16 packed layout
   size_t tqkv, to, tgu, tdown;
+  // and for E4M3 activations: the gate/up codes in pairs of rows, per layer and first layer; the lm_head's codes as
+  // bf16; the scales of a block's rows
+  size_t e8gu, e8gu_layer, e8lm, e8s;
   size_t tqkv_layer, to_layer, tgu_layer, tdown_layer;
   size_t kc, vc, ks, vs;  // first layer; per-layer stride kv_layer / sc_layer
   size_t kv_layer, sc_layer;
@@ -156,6 +160,7 @@ Layout layout_of(const k2_config& c) {
     l.varg = take(sizeof(int) * (kSpecMax + 1));
     l.vpv = take(nv * kArgmaxPartsMax * 4);
     l.vpi = take(nv * kArgmaxPartsMax * 4);
+    l.e8s = take(c.weight_dtype == K2_F8 ? P * sizeof(float) : 0);
   }
   const size_t scratch_end = o;
   // fp8 / int4: pair or tile units by GEMV kind (tiled_kind); else wb-byte
@@ -183,6 +188,9 @@ Layout layout_of(const k2_config& c) {
     l.to = take(l.to_layer * s.L);
     l.tgu = take(l.tgu_layer * s.L);
     l.tdown = take(l.tdown_layer * s.L);
+    l.e8gu_layer = align_up(f8_packed_bytes(2 * s.I, s.H, false), kAlign);
+    l.e8gu = take(l.e8gu_layer * s.L);
+    l.e8lm = take(packed_bytes(s.V, s.H, 2));
   }
   if (c.weight_dtype == K2_BF16 && l.pchunk > 0) {  // two layers' weights as fp16, rebuilt per layer
     for (int b = 0; b < 2; ++b) {
@@ -297,6 +305,8 @@ struct k2_ctx {
   // down; activations: normed input, attention output, SwiGLU output, hi/lo)
   bool tc_ok = false;    // tensor-core prefill
   bool tc_full = false;  // and the paths that also need a bf16 lm_head (batched decode, speculation)
+  bool e8_ok = false;    // fp8 weights: the layers on E4M3 activations, a paged step's lm_head
+  bool act8 = false;     // option K2_OPT_ACT8
   bool use_tc = true;        // prefill
   bool use_tc_decode = true; // batched decode (batch >= 2)
   std::vector<std::array<uint8_t, kTcMapBytes>> tmw;  // 4 per layer
@@ -354,6 +364,10 @@ struct k2_ctx {
     const size_t base[4] = {lay.tqkv, lay.to, lay.tgu, lay.tdown};
     const size_t stride[4] = {lay.tqkv_layer, lay.to_layer, lay.tgu_layer, lay.tdown_layer};
     return ws + base[m] + stride[m] * l;
+  }
+  // fp8: the codes of matrix m as a product over E4M3 activations reads them (packed pairs of rows)
+  LinearWeights e8w(int l, int m) const {
+    return {m == 0 ? wqkv(l) : m == 1 ? wop(l) : m == 2 ? ws + lay.e8gu + lay.e8gu_layer * l : wdown(l), 0, true};
   }
   const float* tcs(int l, int m) const {
     if (!f8()) return nullptr;
@@ -841,6 +855,9 @@ cudaError_t plan_tc_prefill(k2_ctx* c) {
   if (16 * 2 * static_cast<size_t>(s.I) > static_cast<size_t>(P) * s.qkv_n) return cudaSuccess;
   if (!ok) return cudaSuccess;
   c->tc_ok = true;
+  // fp8: pairs of rows but for gate/up and the lm_head, whose codes are copied (k2_init_weights)
+  c->e8_ok = c->f8() && !tiled_kind(0) && !tiled_kind(1) && !tiled_kind(3) &&
+             tc_encode_weight(c->tm_lm.data(), c->ws + c->lay.e8lm, s.V, s.H);
   c->tc_full = !quantized(c->cfg.weight_dtype) && tc_encode_weight(c->tm_lm.data(), c->wlm(), s.V, s.H);
   return cudaSuccess;
 }
@@ -882,7 +899,9 @@ cudaError_t prefill_block(k2_ctx* c, int seq, const int32_t* d_tokens, int n, in
   // weight matrix with the stream-K kernel over 16-token tiles, one CTA per
   // SM: the 128-token tiles would leave most SMs idle (int4 weights keep the
   // 128-token tiles, the only ones with a low-half weight operand)
-  const bool small = n <= 16 && !q4;
+  // fp8 weights with option K2_OPT_ACT8: every row that enters a matrix as E4M3 codes with a scale, whatever the block's size
+  const bool a8 = c->act8;
+  const bool small = n <= 16 && !q4 && !a8;
   // fp16 operands (option K2_OPT_PREFILL_SPLIT = 3: bf16 weights, fp16 caches on
   // the tcgen05 attention, blocks over 16 tokens): each matrix of the layer is
   // converted to fp16 (exact in fp16's normal range) before its GEMM, and the
@@ -968,14 +987,49 @@ cudaError_t prefill_block(k2_ctx* c, int seq, const int32_t* d_tokens, int n, in
   // without the split (blocks over 16 tokens only) the low-half maps are null:
   // the GEMMs read the high halves alone
   // int4: the low-half weight MMA needs the activations' halves
-  const bool split = !f16 && (small || mode != 0 || q4);
-  const bool attn_split = small || mode == 1;  // 2, 3: the attention's Q and P single
+  const bool split = !f16 && !a8 && (small || mode != 0 || q4);
+  const bool attn_split = !a8 && (small || mode == 1);  // 2, 3: the attention's Q and P single
   const void* m_xh = small ? c->tb_xh.data() : wide ? c->tw_xh.data() : c->tm_xh.data();
   const void* m_xl = small ? c->tb_xl.data() : split ? c->tm_xl.data() : nullptr;
   const void* m_oh = small ? c->tb_oh.data() : wide ? c->tw_oh.data() : c->tm_oh.data();
   const void* m_ol = small ? c->tb_ol.data() : split ? c->tm_ol.data() : nullptr;
   const void* m_ah = small ? c->tb_ah.data() : wide ? c->tw_ah.data() : c->tm_ah.data();
   const void* m_al = small ? c->tb_al.data() : split ? c->tm_al.data() : nullptr;
+  // E4M3: codes of the normed rows and of the attention's output in the places of their bf16 halves, those of the SwiGLU rows
+  // (bf16 in ah) behind them
+  uint8_t *xc = reinterpret_cast<uint8_t*>(xh), *oc = reinterpret_cast<uint8_t*>(xl), *ac = reinterpret_cast<uint8_t*>(al);
+  float* xs = reinterpret_cast<float*>(c->ws + c->lay.e8s);
+  const auto wide16 = [](int k) { return static_cast<int64_t>(k + 15) / 16 * 16; };
+  k2_status st8 = K2_OK;
+  const auto done8 = [&](k2_status got) {
+    if (got != K2_OK) st8 = got;
+    return got == K2_OK ? cudaSuccess : cudaErrorUnknown;
+  };
+  auto norm8 = [&](const void* gain) {
+    return done8(k2_norm_quantize(X, K2_F32, s.H, nullptr, 0, nullptr, 0, K2_F32, gain, K2_BF16, n, s.H, s.G, c->cfg.eps, xc,
+                                  wide16(s.H), xs, st));
+  };
+  auto quantize8 = [&](const void* rows, int dtype, int k, uint8_t* codes) {
+    return done8(k2_quantize_rows(rows, dtype, k, n, k, codes, wide16(k), xs, st));
+  };
+  auto linear8 = [&](int l, int m, const uint8_t* codes, int N, int K, int act, void* out, int out_dtype, const void* resid) {
+    LinearArgs g = {};
+    g.w_scale = c->tcs(l, m);
+    g.x_scale = xs;
+    g.residual = resid;
+    g.out = out;
+    g.residual_stride = g.out_stride = act == K2_ACT_SWIGLU ? N / 2 : N;
+    g.tokens = n;
+    g.rows = N;
+    g.cols = K;
+    g.dtype = K2_F8;
+    g.out_dtype = out_dtype;
+    g.act = act;
+    g.flags = c->guard;
+    g.bit = GUARD_TIMEOUT;
+    g.limit_ns = 1000000000ull;
+    return done8(launch_linear(c->e8w(l, m), codes, wide16(K), g, st));
+  };
   cudaError_t e = launch_embed_rows(d_tokens, n, c->embed, s.gb, X, s.H, s.V, c->guard,
                                     paged ? nullptr : c->hist + static_cast<size_t>(seq) * c->lay.cap, 0, nullptr, pos0,
                                     d_pos0, st);
@@ -989,10 +1043,12 @@ cudaError_t prefill_block(k2_ctx* c, int seq, const int32_t* d_tokens, int n, in
   for (int l = 0; l < s.L && !e; ++l) {
     if (f16 && !e) e = cudaStreamWaitEvent(st, c->ev_conv[l & 1], 0);
     if (!e)
-      e = launch_norm_rows(X, n, c->attn_norm[l], s.gb, xh, xl, s.H, s.G, c->cfg.eps, st, false, nullptr, 0, nullptr,
-                           f16, c->guard);
+      e = a8 ? norm8(c->attn_norm[l])
+             : launch_norm_rows(X, n, c->attn_norm[l], s.gb, xh, xl, s.H, s.G, c->cfg.eps, st, false, nullptr, 0, nullptr,
+                                f16, c->guard);
     if (!e) e = dequant(l, 0);
-    if (!e)
+    if (!e && a8) e = linear8(l, 0, xc, s.qkv_n, s.H, K2_ACT_NONE, qkv, K2_F32, nullptr);
+    else if (!e)
       e = small ? gemm_sk(wmap(l, 0), c->tcs(l, 0), m_xh, m_xl, s.qkv_n, s.H, TC_STORE, qkv, s.qkv_n)
                 : gemm(wmap(l, 0), c->tcs(l, 0), m_xh, m_xl, s.qkv_n, s.H, TC_STORE, qkv, nullptr, nullptr, s.qkv_n);
     if (!e && paged) {
@@ -1015,7 +1071,8 @@ cudaError_t prefill_block(k2_ctx* c, int seq, const int32_t* d_tokens, int n, in
         paged->refused = ps;
         e = cudaErrorUnknown;
       }
-      if (!e && !f16) e = launch_half_hilo(o16, xh, xl, static_cast<size_t>(n) * qs, st);
+      if (!e && a8) e = quantize8(o16, K2_F16, static_cast<int>(qs), oc);
+      else if (!e && !f16) e = launch_half_hilo(o16, xh, xl, static_cast<size_t>(n) * qs, st);
     } else if (!e) {
       e = launch_rope_append(qkv, Q, c->rope, kvdt, c->kc(l), c->vc(l), c->ks(l), c->vs(l), n, s.nq, s.nkv, s.d,
                              pos0, d_pos0, head_row0, c->lay.cap, st, c->pdl);
@@ -1047,7 +1104,7 @@ cudaError_t prefill_block(k2_ctx* c, int seq, const int32_t* d_tokens, int n, in
       pa.oh = xh;
       pa.ol = split ? xl : nullptr;
       pa.split = attn_split ? 1 : 0;
-      pa.f16out = f16 ? 1 : 0;
+      pa.f16out = f16 || a8 ? 1 : 0;
       pa.n = n;
       pa.nq = s.nq;
       pa.nkv = s.nkv;
@@ -1058,9 +1115,19 @@ cudaError_t prefill_block(k2_ctx* c, int seq, const int32_t* d_tokens, int n, in
       pa.scale = scale;
       pa.guard = c->guard;
       e = launch_prefill_attn_tc(c->pf_maps, pa, s.d, s.rep, st);
+      if (!e && a8) e = quantize8(xh, K2_F16, s.nq * s.d, oc);
     } else if (!e) {
       e = launch_prefill_attn(Q, kvdt, c->kc(l), c->vc(l), c->ks(l), c->vs(l), xh, xl, n, s.nq, s.nkv, s.d, pos0,
                               head_row0, c->lay.cap, scale, st);
+      if (!e && a8) e = quantize8(xh, K2_BF16, s.nq * s.d, oc);  // of the high halves
+    }
+    if (a8) {
+      if (!e) e = linear8(l, 1, oc, s.H, s.nq * s.d, K2_ACT_NONE, X, K2_F32, X);
+      if (!e) e = norm8(c->mlp_norm[l]);
+      if (!e) e = linear8(l, 2, xc, 2 * s.I, s.H, K2_ACT_SWIGLU, ah, K2_BF16, nullptr);
+      if (!e) e = quantize8(ah, K2_BF16, s.I, ac);
+      if (!e) e = linear8(l, 3, ac, s.H, s.I, K2_ACT_NONE, X, K2_F32, X);
+      continue;
     }
     // o_proj and down have few row tiles: stream-K over one CTA per SM
     if (!e) e = dequant(l, 1);
@@ -1086,6 +1153,7 @@ cudaError_t prefill_block(k2_ctx* c, int seq, const int32_t* d_tokens, int n, in
       if (!e) e = convert_layer(l + 2);
     }
   }
+  if (paged && st8 != K2_OK) paged->refused = st8;
   if (f16) {  // st waits for everything issued on the second stream (a failed call included)
     cudaError_t j = cudaEventRecord(c->ev_join, c->side);
     if (!j) j = cudaStreamWaitEvent(st, c->ev_join, 0);
@@ -1543,7 +1611,11 @@ k2_status k2_init_weights(const k2_config* cfg, const k2_weights* w, void* d_wor
       e = launch_f8_expand(c->tcw(l, 2), static_cast<const uint8_t*>(c->wgu(l)), 2 * z.I, z.H, tiled_kind(2), s);
     if (e == cudaSuccess)
       e = launch_f8_expand(c->tcw(l, 3), static_cast<const uint8_t*>(c->wdown(l)), z.H, z.I, tiled_kind(3), s);
+    if (e == cudaSuccess)
+      e = launch_f8_pairs(ws + c->lay.e8gu + c->lay.e8gu_layer * l, static_cast<const uint8_t*>(c->wgu(l)), 2 * z.I, z.H, s);
   }
+  if (e == cudaSuccess && cfg->weight_dtype == K2_F8 && c->lay.pchunk > 0)
+    e = launch_f8_expand(ws + c->lay.e8lm, static_cast<const uint8_t*>(c->wlm()), z.V, z.H, tiled_kind(4), s);
   if (e != cudaSuccess) {
     g_init_error = std::string("repack: ") + cudaGetErrorString(e);
     delete c;
@@ -1812,6 +1884,12 @@ k2_status k2_set_option(k2_ctx* c, int32_t option, int64_t value) {
       break;
     case K2_OPT_PREFILL_ATTN: c->use_pf_tc = value != 0; break;
     case K2_OPT_PREFILL_GEMM: c->pf_whole = value != 0; break;
+    case K2_OPT_ACT8:
+      if (value < 0 || value > 1) return c->fail(K2_ERR_ARG, "act8 %lld must be 0 or 1", (long long)value);
+      if (value && !c->e8_ok)
+        return c->fail(K2_ERR_UNSUPPORTED, "E4M3 activations need fp8 weights on the tensor-core prefill");
+      c->act8 = value != 0;
+      break;
     case K2_OPT_PREFILL_SPLIT:
       if (value < 0 || value > 3) return c->fail(K2_ERR_ARG, "prefill split %lld outside [0, 3]", (long long)value);
       c->pf_split = static_cast<int>(value);
@@ -2165,8 +2243,8 @@ k2_status k2_paged_step(k2_ctx* c, const k2_paged_kv* layers, const int32_t* d_t
                         int32_t* d_next, float* d_logits, void* d_workspace, size_t ws_bytes, void* stream) {
   if (!c) return K2_ERR_ARG;
   const Sizes& s = c->s;
-  if (!c->tc_full || s.d * s.nq > s.I || s.rep < 4)
-    return c->fail(K2_ERR_UNSUPPORTED, "a paged step needs bf16 weights on the tensor-core path (head_dim 64 or 128, 4 query heads per KV head)");
+  if (!(c->tc_full || (c->act8 && c->tc_ok)) || s.d * s.nq > s.I || s.rep < 4)
+    return c->fail(K2_ERR_UNSUPPORTED, "a paged step needs bf16 weights, or fp8 weights with K2_OPT_ACT8, on the tensor-core path (head_dim 64 or 128, 4 query heads per KV head)");
   if (!layers || !d_tokens || !d_positions || !d_slots || !d_cu_new || !d_kv_len || !d_table || !d_next)
     return c->fail(K2_ERR_ARG, "layers, d_tokens, d_positions, d_slots, d_cu_new, d_kv_len, d_table and d_next must be non-null");
   if (tokens < 1 || tokens > c->lay.pchunk)
@@ -2195,7 +2273,7 @@ k2_status k2_paged_step(k2_ctx* c, const k2_paged_kv* layers, const int32_t* d_t
   auto* xl = reinterpret_cast<__nv_bfloat16*>(c->ws + c->lay.pxl);
   float* logits = d_logits ? d_logits : reinterpret_cast<float*>(c->ws + c->lay.plog);
   if (!e) e = launch_last_rows(X, d_cu_new, requests, tokens, c->resid, s.H, st);
-  if (!e) e = launch_norm_rows(c->resid, requests, c->final_norm, s.wb, xh, xl, s.H, s.G, c->cfg.eps, st);
+  if (!e) e = launch_norm_rows(c->resid, requests, c->final_norm, s.gb, xh, xl, s.H, s.G, c->cfg.eps, st);
   if (!e) {
     const bool small = requests <= 16;
     TcGemmArgs g = {};
@@ -2210,6 +2288,7 @@ k2_status k2_paged_step(k2_ctx* c, const k2_paged_kv* layers, const int32_t* d_t
     g.out = logits;
     g.guard = c->guard;
     g.whole = 1;
+    g.row_scale = c->f8() ? reinterpret_cast<const float*>(c->ws + c->lay.slm) : nullptr;
     e = launch_tc_gemm_sk(c->tm_lm.data(), nullptr, small ? c->tb_xh.data() : c->tm_xh.data(),
                           small ? c->tb_xl.data() : c->tm_xl.data(), g, c->sms, st);
   }

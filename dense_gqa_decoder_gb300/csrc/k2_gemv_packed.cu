@@ -29,6 +29,7 @@
 #include <math.h>
 
 #include "k2_kernels.h"
+#include "k2_linear.h"
 #include "k2_common.cuh"
 
 namespace k2 {
@@ -650,6 +651,21 @@ cudaError_t launch_f8_expand(void* dst, const uint8_t* src, int N, int K, bool t
   if (rows <= 0 || CT16 <= 0) return cudaSuccess;
   f8_expand_kernel<<<dim3(rows, CT16), 256, 0, s>>>(static_cast<__nv_bfloat16*>(dst), src, CT8, CT16,
                                                     tiles ? (K + 63) / 64 : 0);
+  return cudaGetLastError();
+}
+
+// fp8 codes in tile units as pairs of rows in 512-byte chunks (the layout that a tensor map reads), zeros past the last row's
+// and the last column's; one CTA per (packed row, chunk)
+__global__ void __launch_bounds__(512) f8_pairs_kernel(uint8_t* __restrict__ dst, const uint8_t* __restrict__ src, int N, int K,
+                                                       int CT8) {
+  const int R = blockIdx.x, c = blockIdx.y, k = c * 512 + threadIdx.x;
+  dst[(static_cast<size_t>(R >> 1) * CT8 + c) * 1024 + (R & 1) * 512 + threadIdx.x] =
+      R < N && k < K ? src[f8_tile_offset(R, k, (K + 63) / 64)] : static_cast<uint8_t>(0);
+}
+cudaError_t launch_f8_pairs(uint8_t* dst, const uint8_t* src, int N, int K, cudaStream_t s) {
+  const int CT8 = (K + 511) / 512, rows = 2 * ((N + 1) / 2);
+  if (rows <= 0 || CT8 <= 0) return cudaSuccess;
+  f8_pairs_kernel<<<dim3(rows, CT8), 512, 0, s>>>(dst, src, N, K, CT8);
   return cudaGetLastError();
 }
 

@@ -27,17 +27,6 @@ constexpr int kRows = 128;      // weight rows of a tile (TMEM lanes)
 constexpr int kStepBytes = 128; // bytes of K per stage: one swizzle row
 constexpr int kMaxSplit = 8;    // CTAs of a cluster (the portable limit)
 
-template <int BN>
-struct Tile {
-  static constexpr int kA = kRows * kStepBytes, kB = BN * kStepBytes, kStage = kA + kB;
-  static constexpr int kStages = BN == 16 ? 5 : BN == 32 ? 4 : 3;
-  static constexpr int kRing = kStages * kStage;
-  static constexpr int kPart = (BN + kMaxSplit - 1) * kRows * 4;  // the sums that a CTA joins
-  static constexpr int kSmem = kRing + kPart + 1024;              // two CTAs fit an SM
-  static constexpr int kCols = BN < 32 ? 32 : BN;
-  static constexpr uint32_t kDesc = (1u << 4) | (static_cast<uint32_t>(BN >> 3) << 17) | (8u << 24);  // fp32 sums, M = 128
-};
-
 __device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
       "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
@@ -109,14 +98,69 @@ __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { retu
 template <>
 __device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
 
+enum { kPlain, kPairsOfRows, kOther };  // what follows the sums: nothing, SwiGLU, another activation
+
+constexpr int kColumns = 16;  // columns of the accumulator that a warp has in registers
+
+// Some columns of the accumulator (tokens t ..) of this lane's row n: z = v * (ws * xs) + bias, then the activation, the
+// residual and the stores.  Nothing waits for the column before: the scales are in shared memory, the residual is loaded ahead.
+template <typename OT, int ACT, bool FULL>
+__device__ __forceinline__ void finish_columns(const LinearArgs& a, const uint32_t (&v)[kColumns], const float* xs, int t, int n,
+                                               float ws, float bias) {
+  const bool odd = n & 1, row = n < a.rows;
+  const int most = a.tokens - t;  // columns of tokens (not FULL: fewer than there are columns)
+  if (ACT == kPairsOfRows) {
+    // a gate and its factor lie in neighbouring lanes: of two columns the even lane finishes the first, the odd lane the second
+    const int mine = odd ? 1 : 0;
+    const long long first = t + mine;
+    float res[kColumns / 2];
+    if (a.residual != nullptr) {
+      const OT* from = static_cast<const OT*>(a.residual) + first * a.residual_stride + (n >> 1);
+#pragma unroll
+      for (int j = 0; j < kColumns; j += 2, from += 2 * a.residual_stride)
+        res[j / 2] = row && (FULL || j + mine < most) ? to_f32(*from) : 0.f;
+    }
+    OT* out = static_cast<OT*>(a.out) + first * a.out_stride + (n >> 1);
+#pragma unroll
+    for (int j = 0; j < kColumns; j += 2, out += 2 * a.out_stride) {
+      const float2 x = *reinterpret_cast<const float2*>(xs + j);
+      const float z0 = fmaf(__uint_as_float(v[j]), ws * x.x, bias), z1 = fmaf(__uint_as_float(v[j + 1]), ws * x.y, bias);
+      const float other = __shfl_xor_sync(0xffffffffu, odd ? z0 : z1, 1);
+      const float g = odd ? other : z0, u = odd ? z1 : other;
+      float y = __fdividef(g, 1.0f + __expf(-g)) * u;
+      if (a.residual != nullptr) y += res[j / 2];
+      if (row && (FULL || j + mine < most)) *out = from_f32<OT>(y);
+    }
+    return;
+  }
+  float res[kColumns];
+  if (a.residual != nullptr) {
+    const OT* from = static_cast<const OT*>(a.residual) + static_cast<long long>(t) * a.residual_stride + n;
+#pragma unroll
+    for (int j = 0; j < kColumns; ++j, from += a.residual_stride) res[j] = row && (FULL || j < most) ? to_f32(*from) : 0.f;
+  }
+  OT* out = static_cast<OT*>(a.out) + static_cast<long long>(t) * a.out_stride + n;
+#pragma unroll
+  for (int j = 0; j < kColumns; j += 4) {
+    const float4 x = *reinterpret_cast<const float4*>(xs + j);
+    const float x4[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i, out += a.out_stride) {
+      float y = fmaf(__uint_as_float(v[j + i]), ws * x4[i], bias);
+      if (ACT == kOther) y = activate(y, a.act);
+      if (a.residual != nullptr) y += res[j + i];
+      if (row && (FULL || j + i < most)) *out = from_f32<OT>(y);
+    }
+  }
+}
 // What follows the sums of one token, of four neighbouring rows n .. n + 3 of the matrix.
-template <typename OT>
+template <typename OT, int ACT>
 __device__ __forceinline__ void finish_four(const LinearArgs& a, long long t, int n, float4 z4, float xs, const float (&ws)[4],
                                             const float (&bias)[4]) {
   float z[4] = {z4.x, z4.y, z4.z, z4.w};
 #pragma unroll
   for (int j = 0; j < 4; ++j) z[j] = fmaf(z[j], ws[j] * xs, bias[j]);
-  if (a.act == K2_ACT_SWIGLU) {
+  if (ACT == kPairsOfRows) {
     OT* out = static_cast<OT*>(a.out) + t * a.out_stride + (n >> 1);
     const OT* res = static_cast<const OT*>(a.residual) + t * a.residual_stride + (n >> 1);
 #pragma unroll
@@ -137,7 +181,7 @@ __device__ __forceinline__ void finish_four(const LinearArgs& a, long long t, in
   }
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const float y = activate(z[j], a.act);
+    const float y = ACT == kOther ? activate(z[j], a.act) : z[j];
     if (n + j < a.rows) out[j] = from_f32<OT>(a.residual != nullptr ? y + r[j] : y);
   }
 }
@@ -155,28 +199,42 @@ __device__ __forceinline__ void load_weights(void* dst, const CUtensorMap* m, co
 
 // ---- few tokens -----------------------------------------------------------------------------------------------------------
 //
-// A CTA per tile of 128 rows x BN tokens.  Where there are fewer tiles than SMs can hold, a cluster of up to eight CTAs splits K:
-// token j's sums go to CTA j % split, each CTA writing its share into that CTA's shared memory, and are added there in the
-// order of K, so that the result does not depend on which CTA came first.
-template <int BN, bool F8, typename OT>
+// A CTA per tile of 128 rows x 16, 32 or 64 tokens.  Where there are fewer tiles than SMs, a cluster of up to eight CTAs splits
+// K: token j's sums go to CTA j % split, each CTA writing its share into that CTA's shared memory, and are added there in the
+// order of K, so that the result does not depend on which CTA came first.  One CTA per SM is enough (q|k|v of one token: 8.6 us
+// with twice as many, whose clusters no longer fit at once, 5.7 with these).
+constexpr int kFewTokens = 64, kFewStages = 5, kFewRing = 92 * 1024;  // two CTAs fit an SM
+
+struct FewShape {
+  int tokens;  // of a tile: 16, 32 or 64
+  int steps;   // of K
+  int stages;  // of the ring
+  int split;   // CTAs that share a tile's K
+};
+__host__ __device__ constexpr int few_stage(int tokens) { return (kRows + tokens) * kStepBytes; }
+// the sums that a CTA joins
+__host__ __device__ constexpr int few_part(int tokens, int split) { return split > 1 ? (tokens + split - 1) * kRows * 4 : 0; }
+
+template <bool F8, typename OT, int ACT>
 __global__ void __launch_bounds__(128) linear_few_kernel(const __grid_constant__ CUtensorMap map_w,
                                                          const __grid_constant__ CUtensorMap map_x, const LinearArgs a,
-                                                         const WeightPlace place, int steps, int split) {
-  using C = Tile<BN>;
+                                                         const WeightPlace place, const FewShape sh) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  __shared__ __align__(8) uint64_t full[C::kStages], empty[C::kStages], done;
+  __shared__ __align__(8) uint64_t full[kFewStages], empty[kFewStages], done;
+  __shared__ __align__(16) float xs[kFewTokens];
   __shared__ uint32_t tmem_slot;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, split = sh.split;
   const int tile = blockIdx.x / split, rank = blockIdx.x - tile * split;
-  const int n0 = tile * kRows, t0 = blockIdx.y * BN;
-  const int k0 = static_cast<int>(static_cast<long long>(steps) * rank / split);
-  const int nk = static_cast<int>(static_cast<long long>(steps) * (rank + 1) / split) - k0;
+  const int n0 = tile * kRows, t0 = blockIdx.y * sh.tokens, tokens = min(sh.tokens, a.tokens - t0);
+  const int k0 = static_cast<int>(static_cast<long long>(sh.steps) * rank / split);
+  const int nk = static_cast<int>(static_cast<long long>(sh.steps) * (rank + 1) / split) - k0;
+  const int stage = few_stage(sh.tokens);
   if (split > 1) cluster_arrive();  // this CTA runs: its shared memory may be written to
   if (tid == 0) {
     prefetch_map(&map_w);
     prefetch_map(&map_x);
-    for (int s = 0; s < C::kStages; ++s) {
+    for (int s = 0; s < sh.stages; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
@@ -184,7 +242,7 @@ __global__ void __launch_bounds__(128) linear_few_kernel(const __grid_constant__
     fence_mbar_init();
   }
   if (warp == 1) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_slot)), "r"(C::kCols)
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_slot)), "n"(kFewTokens)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
@@ -196,48 +254,57 @@ __global__ void __launch_bounds__(128) linear_few_kernel(const __grid_constant__
   pdl_trigger();
   bool ok = true;
   if (tid == 0) {
-    int i = 0;
+    int i = 0, s = 0;
+    uint32_t ph = 0;  // how often the ring wrapped
     for (; i < nk; ++i) {
-      const int s = i % C::kStages;
-      if (i >= C::kStages && !wait_for(&empty[s], static_cast<uint32_t>(i / C::kStages - 1) & 1u, a.limit_ns)) {
+      if (ph > 0 && !wait_for(&empty[s], (ph - 1) & 1u, a.limit_ns)) {
         ok = false;
         break;
       }
-      uint8_t* st = smem + s * C::kStage;
-      mbar_arrive_expect_tx(&full[s], C::kStage);
+      uint8_t* st = smem + s * stage;
+      mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(stage));
       load_weights(st, &map_w, place, k0 + i, n0, &full[s]);
-      load_2d(st + C::kA, &map_x, (k0 + i) * place.step, t0, &full[s]);
+      load_2d(st + kRows * kStepBytes, &map_x, (k0 + i) * place.step, t0, &full[s]);
+      if (++s == sh.stages) s = 0, ++ph;
     }
     // no copy may be on its way when this CTA ends
-    for (int j = max(0, i - C::kStages); j < i; ++j) mbar_wait(&full[j % C::kStages], static_cast<uint32_t>(j / C::kStages) & 1u);
+    for (int j = min(i, sh.stages); j > 0; --j) {
+      s = s == 0 ? (--ph, sh.stages - 1) : s - 1;
+      mbar_wait(&full[s], ph & 1u);
+    }
   } else if (tid == 32) {
-    const uint32_t idesc = C::kDesc | (a.dtype == K2_BF16 ? (1u << 7) | (1u << 10) : 0u);
+    const uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(sh.tokens >> 3) << 17) | (8u << 24) |  // fp32 sums, M = 128
+                           (a.dtype == K2_BF16 ? (1u << 7) | (1u << 10) : 0u);
     const uint64_t ring = smem_desc(smem);
+    int s = 0;
+    uint32_t ph = 0;
     for (int i = 0; i < nk; ++i) {
-      const int s = i % C::kStages;
-      if (!wait_for(&full[s], static_cast<uint32_t>(i / C::kStages) & 1u, a.limit_ns)) {
+      if (!wait_for(&full[s], ph & 1u, a.limit_ns)) {
         ok = false;
         break;
       }
       tc_after();
-      const uint64_t at = ring + static_cast<uint32_t>(s * (C::kStage >> 4));
+      const uint64_t at = ring + static_cast<uint32_t>(s * (stage >> 4));
 #pragma unroll
       for (int j = 0; j < kStepBytes / 32; ++j) {  // descriptors count 16 bytes
-        if (F8) mma_f8(tmem, at + 2 * j, at + (C::kA >> 4) + 2 * j, idesc, (i | j) != 0);
-        else mma(tmem, at + 2 * j, at + (C::kA >> 4) + 2 * j, idesc, (i | j) != 0);
+        if (F8) mma_f8(tmem, at + 2 * j, at + (kRows * kStepBytes >> 4) + 2 * j, idesc, (i | j) != 0);
+        else mma(tmem, at + 2 * j, at + (kRows * kStepBytes >> 4) + 2 * j, idesc, (i | j) != 0);
       }
       mma_commit(&empty[s]);
+      if (++s == sh.stages) s = 0, ++ph;
     }
     mma_commit(&done);
   }
-  // meanwhile: scales and biases of the four rows that this thread finishes
-  const int n = n0 + 4 * lane, tokens = min(BN, a.tokens - t0);
+  // meanwhile: the scales and biases of what this thread finishes, its own row or (split) four neighbouring ones
+  const int n = n0 + (split > 1 ? 4 * lane : tid);
   float ws[4], bias[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    ws[j] = a.w_scale != nullptr && n + j < a.rows ? __ldg(a.w_scale + n + j) : 1.f;
-    bias[j] = a.bias != nullptr && n + j < a.rows ? __ldg(a.bias + n + j) : 0.f;
+    const bool there = n + j < a.rows && (j == 0 || split > 1);
+    ws[j] = a.w_scale != nullptr && there ? __ldg(a.w_scale + n + j) : 1.f;
+    bias[j] = a.bias != nullptr && there ? __ldg(a.bias + n + j) : 0.f;
   }
+  if (tid >= 64) xs[tid - 64] = a.x_scale != nullptr && tid - 64 < tokens ? __ldg(a.x_scale + t0 + tid - 64) : 1.f;
   if (split > 1) {
     __syncwarp();
     cluster_wait();  // the others run
@@ -247,49 +314,52 @@ __global__ void __launch_bounds__(128) linear_few_kernel(const __grid_constant__
   ok = __syncthreads_and(ok);
   tc_after();
   if (!ok && tid == 0 && a.flags != nullptr) atomicOr(a.flags, a.bit);
-  // this thread's row of the sums, token by token, to the CTA that joins them: [rank][token / split][row]
-  float* part = reinterpret_cast<float*>(smem + C::kRing);
-  const int slots = (BN + split - 1) / split;
-  {
-    const uint32_t mine = smem_u32(part) + static_cast<uint32_t>(rank * slots * kRows + tid) * 4u;
-    int owner = 0;
-    uint32_t at = mine;
+  const uint32_t acc = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+  if (split == 1) {
+    if (!ok) ws[0] = __uint_as_float(0x7FC00000u);
 #pragma unroll 1
-    for (int c = 0; c < BN && c < tokens; c += 16) {
-      uint32_t v[16];
-      tmem_ld16(tmem + (static_cast<uint32_t>(warp * 32) << 16) + c, v);
+    for (int c = 0; c < tokens; c += kColumns) {
+      uint32_t v[kColumns];
+      tmem_ld16(acc + c, v);
+      if (c + kColumns <= tokens) finish_columns<OT, ACT, true>(a, v, xs + c, t0 + c, n, ws[0], bias[0]);
+      else finish_columns<OT, ACT, false>(a, v, xs + c, t0 + c, n, ws[0], bias[0]);
+    }
+  } else {
+    // this thread's row of the sums, token by token, to the CTA that joins them: [rank][token / split][row]
+    float* part = reinterpret_cast<float*>(smem + sh.stages * stage);
+    const int slots = (sh.tokens + split - 1) / split;
+    int owner = 0;
+    uint32_t at = smem_u32(part) + static_cast<uint32_t>(rank * slots * kRows + tid) * 4u;
+#pragma unroll 1
+    for (int c = 0; c < tokens; c += kColumns) {
+      uint32_t v[kColumns];
+      tmem_ld16(acc + c, v);
 #pragma unroll
-      for (int j = 0; j < 16; ++j) {
+      for (int j = 0; j < kColumns; ++j) {
         if (c + j < tokens) peer_store(peer_address(at, owner), ok ? __uint_as_float(v[j]) : __uint_as_float(0x7FC00000u));
         if (++owner == split) owner = 0, at += kRows * 4;
       }
     }
-  }
-  tc_before();
-  if (split > 1) {
     __syncwarp();
     cluster_arrive();
     cluster_wait();
-  } else {
-    __syncthreads();
-  }
-  for (int slot = warp; rank + slot * split < tokens; slot += 4) {
-    const long long t = t0 + rank + slot * split;
-    const float xs = a.x_scale != nullptr ? __ldg(a.x_scale + t) : 1.f;
-    const float4* from = reinterpret_cast<const float4*>(part + slot * kRows) + lane;
-    float4 z = from[0];
+    for (int slot = warp; rank + slot * split < tokens; slot += 4) {
+      const int j = rank + slot * split;
+      const float4* from = reinterpret_cast<const float4*>(part + slot * kRows) + lane;
+      float4 z = from[0];
 #pragma unroll
-    for (int r = 1; r < kMaxSplit; ++r) {
-      if (r < split) {
-        const float4 p = from[r * slots * (kRows / 4)];
-        z.x += p.x, z.y += p.y, z.z += p.z, z.w += p.w;
+      for (int r = 1; r < kMaxSplit; ++r) {
+        if (r < split) {
+          const float4 p = from[r * slots * (kRows / 4)];
+          z.x += p.x, z.y += p.y, z.z += p.z, z.w += p.w;
+        }
       }
+      finish_four<OT, ACT>(a, t0 + j, n, z, xs[j], ws, bias);
     }
-    finish_four<OT>(a, t, n, z, xs, ws, bias);
   }
-  tc_after();
+  tc_before();
   __syncthreads();  // every warp has read the accumulator
-  if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::kCols) : "memory");
+  if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(kFewTokens) : "memory");
 }
 
 // ---- many tokens: pairs of CTAs -------------------------------------------------------------------------------------------
@@ -303,7 +373,6 @@ __global__ void __launch_bounds__(128) linear_few_kernel(const __grid_constant__
 constexpr int kPairTokens = 256, kPairStages = 8, kPairSteps = 2, kPairRing = 192 * 1024;
 constexpr int kPairSmem = kPairRing + 1024;
 constexpr int kPairFinishers = 16, kPairThreads = 32 * (2 + kPairFinishers);
-constexpr int kColumns = 16;  // columns that a finishing warp has in registers
 
 __device__ __forceinline__ uint32_t cta_rank() {
   uint32_t r;
@@ -363,59 +432,6 @@ struct PairShape {
   int row_tiles, token_tiles;
 };
 
-enum { kPlain, kPairsOfRows, kOther };  // what follows the sums: nothing, SwiGLU, another activation
-
-// Some columns of the accumulator (tokens t ..) of this lane's row n: z = v * (ws * xs) + bias, then the activation, the
-// residual and the stores.  Nothing waits for the column before: the scales are in shared memory, the residual is loaded ahead.
-template <typename OT, int ACT, bool FULL>
-__device__ __forceinline__ void finish_columns(const LinearArgs& a, const uint32_t (&v)[kColumns], const float* xs, int t, int n,
-                                               float ws, float bias) {
-  const bool odd = n & 1, row = n < a.rows;
-  const int most = a.tokens - t;  // columns of tokens (not FULL: fewer than there are columns)
-  if (ACT == kPairsOfRows) {
-    // a gate and its factor lie in neighbouring lanes: of two columns the even lane finishes the first, the odd lane the second
-    const int mine = odd ? 1 : 0;
-    const long long first = t + mine;
-    float res[kColumns / 2];
-    if (a.residual != nullptr) {
-      const OT* from = static_cast<const OT*>(a.residual) + first * a.residual_stride + (n >> 1);
-#pragma unroll
-      for (int j = 0; j < kColumns; j += 2, from += 2 * a.residual_stride)
-        res[j / 2] = row && (FULL || j + mine < most) ? to_f32(*from) : 0.f;
-    }
-    OT* out = static_cast<OT*>(a.out) + first * a.out_stride + (n >> 1);
-#pragma unroll
-    for (int j = 0; j < kColumns; j += 2, out += 2 * a.out_stride) {
-      const float2 x = *reinterpret_cast<const float2*>(xs + j);
-      const float z0 = fmaf(__uint_as_float(v[j]), ws * x.x, bias), z1 = fmaf(__uint_as_float(v[j + 1]), ws * x.y, bias);
-      const float other = __shfl_xor_sync(0xffffffffu, odd ? z0 : z1, 1);
-      const float g = odd ? other : z0, u = odd ? z1 : other;
-      float y = __fdividef(g, 1.0f + __expf(-g)) * u;
-      if (a.residual != nullptr) y += res[j / 2];
-      if (row && (FULL || j + mine < most)) *out = from_f32<OT>(y);
-    }
-    return;
-  }
-  float res[kColumns];
-  if (a.residual != nullptr) {
-    const OT* from = static_cast<const OT*>(a.residual) + static_cast<long long>(t) * a.residual_stride + n;
-#pragma unroll
-    for (int j = 0; j < kColumns; ++j, from += a.residual_stride) res[j] = row && (FULL || j < most) ? to_f32(*from) : 0.f;
-  }
-  OT* out = static_cast<OT*>(a.out) + static_cast<long long>(t) * a.out_stride + n;
-#pragma unroll
-  for (int j = 0; j < kColumns; j += 4) {
-    const float4 x = *reinterpret_cast<const float4*>(xs + j);
-    const float x4[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i, out += a.out_stride) {
-      float y = fmaf(__uint_as_float(v[j + i]), ws * x4[i], bias);
-      if (ACT == kOther) y = activate(y, a.act);
-      if (a.residual != nullptr) y += res[j + i];
-      if (row && (FULL || j + i < most)) *out = from_f32<OT>(y);
-    }
-  }
-}
 // A warp's part of a tile: 32 rows (this lane's is n), `columns` of the accumulator from t on, whose scales are at xs.  `free`
 // is the barrier that gives the accumulator back, as soon as the last columns are in registers.
 template <typename OT, int ACT>
@@ -627,44 +643,29 @@ cudaLaunchAttribute early_start() {
   return attr;
 }
 
-template <int BN, bool F8, typename OT>
-cudaError_t launch_few(const CUtensorMap& mw, const CUtensorMap& mx, const LinearArgs& a, const WeightPlace& place, int steps,
-                       int split, int dev, cudaStream_t s) {
-  using C = Tile<BN>;
-  auto kernel = linear_few_kernel<BN, F8, OT>;
+template <bool F8, typename OT, int ACT>
+cudaError_t launch(const CUtensorMap& mw, const CUtensorMap& mx, const LinearArgs& a, const WeightPlace& place,
+                   const FewShape& sh, int, int dev, cudaStream_t s) {
+  auto kernel = linear_few_kernel<F8, OT, ACT>;
   static std::atomic<uint64_t> ready{0};
-  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), C::kSmem, dev, ready);
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), kFewRing + few_part(kFewTokens, kMaxSplit) + 1024, dev, ready);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((a.rows + kRows - 1) / kRows * split, (a.tokens + BN - 1) / BN);
+  cfg.gridDim = dim3((a.rows + kRows - 1) / kRows * sh.split, (a.tokens + sh.tokens - 1) / sh.tokens);
   cfg.blockDim = dim3(128);
-  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.dynamicSmemBytes = sh.stages * few_stage(sh.tokens) + few_part(sh.tokens, sh.split) + 1024;
   cfg.stream = s;
   cudaLaunchAttribute attr[2] = {early_start(), {}};
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = split;
+  attr[1].val.clusterDim.x = sh.split;
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = split > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kernel, mw, mx, a, place, steps, split);
+  cfg.numAttrs = sh.split > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, mw, mx, a, place, sh);
 }
-template <int BN, bool F8>
-cudaError_t launch_few(const CUtensorMap& mw, const CUtensorMap& mx, const LinearArgs& a, const WeightPlace& place, int steps,
-                       int split, int dev, cudaStream_t s) {
-  return a.out_dtype == K2_F32    ? launch_few<BN, F8, float>(mw, mx, a, place, steps, split, dev, s)
-         : a.out_dtype == K2_BF16 ? launch_few<BN, F8, __nv_bfloat16>(mw, mx, a, place, steps, split, dev, s)
-                                  : launch_few<BN, F8, __half>(mw, mx, a, place, steps, split, dev, s);
-}
-template <int BN>
-cudaError_t launch_few(bool f8, const CUtensorMap& mw, const CUtensorMap& mx, const LinearArgs& a, const WeightPlace& place,
-                       int steps, int split, int dev, cudaStream_t s) {
-  return f8 ? launch_few<BN, true>(mw, mx, a, place, steps, split, dev, s)
-            : launch_few<BN, false>(mw, mx, a, place, steps, split, dev, s);
-}
-
 template <bool F8, typename OT, int ACT>
-cudaError_t launch_pair(const CUtensorMap& mw, const CUtensorMap& mx, const LinearArgs& a, const WeightPlace& place,
-                        const PairShape& sh, int sms, int dev, cudaStream_t s) {
+cudaError_t launch(const CUtensorMap& mw, const CUtensorMap& mx, const LinearArgs& a, const WeightPlace& place,
+                   const PairShape& sh, int sms, int dev, cudaStream_t s) {
   auto kernel = linear_pair_kernel<F8, OT, ACT>;
   static std::atomic<uint64_t> ready{0};
   const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), kPairSmem, dev, ready);
@@ -680,19 +681,34 @@ cudaError_t launch_pair(const CUtensorMap& mw, const CUtensorMap& mx, const Line
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, mw, mx, a, place, sh);
 }
-template <bool F8, typename OT>
-cudaError_t launch_pair(const CUtensorMap& mw, const CUtensorMap& mx, const LinearArgs& a, const WeightPlace& place,
-                        const PairShape& sh, int sms, int dev, cudaStream_t s) {
-  return a.act == K2_ACT_SWIGLU ? launch_pair<F8, OT, kPairsOfRows>(mw, mx, a, place, sh, sms, dev, s)
-         : a.act == K2_ACT_NONE ? launch_pair<F8, OT, kPlain>(mw, mx, a, place, sh, sms, dev, s)
-                                : launch_pair<F8, OT, kOther>(mw, mx, a, place, sh, sms, dev, s);
+template <bool F8, typename OT, typename Shape>
+cudaError_t launch(const CUtensorMap& mw, const CUtensorMap& mx, const LinearArgs& a, const WeightPlace& place, const Shape& sh,
+                   int sms, int dev, cudaStream_t s) {
+  return a.act == K2_ACT_SWIGLU ? launch<F8, OT, kPairsOfRows>(mw, mx, a, place, sh, sms, dev, s)
+         : a.act == K2_ACT_NONE ? launch<F8, OT, kPlain>(mw, mx, a, place, sh, sms, dev, s)
+                                : launch<F8, OT, kOther>(mw, mx, a, place, sh, sms, dev, s);
 }
-template <bool F8>
-cudaError_t launch_pair(const CUtensorMap& mw, const CUtensorMap& mx, const LinearArgs& a, const WeightPlace& place,
-                        const PairShape& sh, int sms, int dev, cudaStream_t s) {
-  return a.out_dtype == K2_F32    ? launch_pair<F8, float>(mw, mx, a, place, sh, sms, dev, s)
-         : a.out_dtype == K2_BF16 ? launch_pair<F8, __nv_bfloat16>(mw, mx, a, place, sh, sms, dev, s)
-                                  : launch_pair<F8, __half>(mw, mx, a, place, sh, sms, dev, s);
+template <bool F8, typename Shape>
+cudaError_t launch(const CUtensorMap& mw, const CUtensorMap& mx, const LinearArgs& a, const WeightPlace& place, const Shape& sh,
+                   int sms, int dev, cudaStream_t s) {
+  return a.out_dtype == K2_F32    ? launch<F8, float>(mw, mx, a, place, sh, sms, dev, s)
+         : a.out_dtype == K2_BF16 ? launch<F8, __nv_bfloat16>(mw, mx, a, place, sh, sms, dev, s)
+                                  : launch<F8, __half>(mw, mx, a, place, sh, sms, dev, s);
+}
+// tensor maps for tiles of box_tokens, and the kernel of the shape
+template <typename Shape>
+k2_status launch(const LinearWeights& w, const void* x, long long x_stride, const LinearArgs& a, const WeightPlace& place,
+                 const Shape& sh, int box_tokens, int sms, int dev, cudaStream_t s) {
+  CUtensorMap mw, mx;
+  if (!encode_weights(&mw, a.dtype, w, a.rows, a.cols) || !encode_tokens(&mx, a.dtype, x, x_stride, a.cols, a.tokens, box_tokens)) {
+    set_error("no tensor map for %d x %d weights and %d tokens", a.rows, a.cols, a.tokens);
+    return K2_ERR_CUDA;
+  }
+  const cudaError_t e = a.dtype == K2_F8 ? launch<true>(mw, mx, a, place, sh, sms, dev, s)
+                                         : launch<false>(mw, mx, a, place, sh, sms, dev, s);
+  if (e == cudaSuccess) return K2_OK;
+  set_error("linear launch: %s", cudaGetErrorString(e));
+  return K2_ERR_CUDA;
 }
 
 }  // namespace
@@ -702,46 +718,40 @@ k2_status launch_linear(const LinearWeights& w, const void* x, long long x_strid
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess && (dev < 0 || dev >= 64)) e = cudaErrorInvalidDevice;
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e == cudaSuccess) {
-    const bool f8 = a.dtype == K2_F8;
-    const WeightPlace place = {w.packed ? 1 : 0, f8 ? kStepBytes : kStepBytes / 2};
-    const int steps = (a.cols + place.step - 1) / place.step;
-    if (a.tokens > 128) {
-      // tiles as wide as leave the fewest columns to the pair with the most tiles
-      PairShape sh = {0, steps, 0, (a.rows + 2 * kRows - 1) / (2 * kRows), 0};
-      long long best = 0;
-      for (int n = kPairTokens; n >= 128; n -= 64) {
-        const int tt = (a.tokens + n - 1) / n;
-        const long long cost = (static_cast<long long>(sh.row_tiles) * tt + sms / 2 - 1) / (sms / 2) * (n + 224);
-        if (sh.tokens == 0 || cost < best) sh.tokens = n, sh.token_tiles = tt, best = cost;
-      }
-      sh.stages = std::min(kPairStages, kPairRing / (kPairSteps * (kRows + sh.tokens / 2) * kStepBytes));
-      CUtensorMap mw, mx;
-      if (!encode_weights(&mw, a.dtype, w, a.rows, a.cols) ||
-          !encode_tokens(&mx, a.dtype, x, x_stride, a.cols, a.tokens, sh.tokens / 2)) {
-        set_error("no tensor map for %d x %d weights and %d tokens", a.rows, a.cols, a.tokens);
-        return K2_ERR_CUDA;
-      }
-      e = f8 ? launch_pair<true>(mw, mx, a, place, sh, sms, dev, s) : launch_pair<false>(mw, mx, a, place, sh, sms, dev, s);
-      if (e == cudaSuccess) return K2_OK;
-      set_error("linear launch: %s", cudaGetErrorString(e));
-      return K2_ERR_CUDA;
-    }
-    const int bn = a.tokens <= 16 ? 16 : a.tokens <= 32 ? 32 : 64;
-    const long long tiles = static_cast<long long>((a.rows + kRows - 1) / kRows) * ((a.tokens + bn - 1) / bn);
-    const int split = static_cast<int>(std::max<long long>(1, std::min<long long>({2ll * sms / tiles, kMaxSplit, steps})));
-    CUtensorMap mw, mx;
-    if (!encode_weights(&mw, a.dtype, w, a.rows, a.cols) || !encode_tokens(&mx, a.dtype, x, x_stride, a.cols, a.tokens, bn)) {
-      set_error("no tensor map for %d x %d weights and %d tokens", a.rows, a.cols, a.tokens);
-      return K2_ERR_CUDA;
-    }
-    e = bn == 16   ? launch_few<16>(f8, mw, mx, a, place, steps, split, dev, s)
-        : bn == 32 ? launch_few<32>(f8, mw, mx, a, place, steps, split, dev, s)
-                   : launch_few<64>(f8, mw, mx, a, place, steps, split, dev, s);
+  if (e != cudaSuccess) {
+    set_error("linear: %s", cudaGetErrorString(e));
+    return K2_ERR_CUDA;
   }
-  if (e == cudaSuccess) return K2_OK;
-  set_error("linear launch: %s", cudaGetErrorString(e));
-  return K2_ERR_CUDA;
+  const WeightPlace place = {w.packed ? 1 : 0, a.dtype == K2_F8 ? kStepBytes : kStepBytes / 2};
+  const int steps = (a.cols + place.step - 1) / place.step;
+  // Few tokens per tile and K split over CTAs, or wide tiles on pairs of SMs: the cheaper by what was measured, in units of
+  // 0.67 ns.  Few: a K step takes 0.30 us on an SM with one CTA and 0.37 for the two of an SM with two, and 1.2 us more to
+  // join (down of 128 tokens 14.4 us against the pairs' 20.5, q|k|v of 256 tokens 10.5 against 9.1).  Up to 64 tokens it is
+  // always that one (gate and up of 64 tokens 14.4 against 16.5).
+  FewShape few = {a.tokens <= 16 ? 16 : a.tokens <= 32 ? 32 : 64, steps, 0, 1};
+  const long long few_tiles = static_cast<long long>((a.rows + kRows - 1) / kRows) * ((a.tokens + few.tokens - 1) / few.tokens);
+  long long few_cost = 0;
+  for (int per_sm = 1; per_sm <= (a.tokens > 64 ? 2 : 1); ++per_sm) {
+    const int split = static_cast<int>(std::max<long long>(1, std::min<long long>({per_sm * sms / few_tiles, kMaxSplit, steps})));
+    const long long mine = (steps + split - 1) / split, load = (few_tiles * split + sms - 1) / sms;
+    const long long cost = std::max(448 * mine, 276 * mine * load) + 1800;
+    if (few_cost == 0 || cost < few_cost) few.split = split, few_cost = cost;
+  }
+  if (a.tokens > 64) {
+    // tiles as wide as cost the pair with the most tiles least: a K step of n columns takes as long as n + 224 in the matrix
+    // unit (0.24 us for 128, 0.26 for 192, 0.32 for 256)
+    PairShape sh = {0, steps, 0, (a.rows + 2 * kRows - 1) / (2 * kRows), 0};
+    long long best = 0;
+    for (int n = kPairTokens; n >= 64; n -= 64) {
+      const int tt = (a.tokens + n - 1) / n;
+      const long long cost = (static_cast<long long>(sh.row_tiles) * tt + sms / 2 - 1) / (sms / 2) * (n + 224) * steps;
+      if (sh.tokens == 0 || cost < best) sh.tokens = n, sh.token_tiles = tt, best = cost;
+    }
+    sh.stages = std::min(kPairStages, kPairRing / (kPairSteps * (kRows + sh.tokens / 2) * kStepBytes));
+    if (best <= few_cost) return launch(w, x, x_stride, a, place, sh, sh.tokens / 2, sms, dev, s);
+  }
+  few.stages = std::min({kFewStages, kFewRing / few_stage(few.tokens), (steps + few.split - 1) / few.split});
+  return launch(w, x, x_stride, a, place, few, few.tokens, sms, dev, s);
 }
 
 }  // namespace k2

@@ -50,6 +50,9 @@ inline bool sets_meet(const RowSet& a, const RowSet& b) {
   return d < a.row || a.stride - d < b.row;
 }
 
+// fp8 codes [N][K] in the decode step's tile units as packed pairs (k2_gemv_packed.cu)
+cudaError_t launch_f8_pairs(uint8_t* dst, const uint8_t* src, int N, int K, cudaStream_t s);
+
 k2_status launch_linear(const LinearWeights& w, const void* x, long long x_stride, const LinearArgs& a, cudaStream_t s);
 
 }  // namespace k2

@@ -431,10 +431,18 @@ typedef enum {
                              the prefill's logits), and a 4096-token prompt takes 46.5 ms against 73.3 ms
                              with 1 and 66.3 ms with 2 (1 and 2 measured before the prefill kernels ran
                              under PDL). */
-  K2_OPT_PREFILL_GEMM = 13 /* tensor-core prefill of blocks over 16 tokens, QKV and gate/up GEMMs: 1 (default)
+  K2_OPT_PREFILL_GEMM = 13, /* tensor-core prefill of blocks over 16 tokens, QKV and gate/up GEMMs: 1 (default)
                              one persistent CTA per SM over whole 128 x 128 tiles, two TMEM accumulators so
                              that a tile's epilogue (store, SwiGLU) overlaps the next tile's K steps; 0 one
                              CTA per tile (the epilogue after its own K steps) */
+  K2_OPT_ACT8 = 14 /* fp8 weights: 1 runs the layers of prefill blocks and of k2_paged_step on E4M3 activations
+                             (each row that enters a matrix as codes with one scale: k2_norm_quantize,
+                             k2_quantize_rows and k2_linear over the codes of the weights), and is what
+                             k2_paged_step needs with fp8 weights; 0 (default) feeds the exact weights as bf16
+                             and the activations in halves.  The last token of a prompt and the decode steps
+                             keep fp32 activations, and so does the lm_head.  K2_ERR_UNSUPPORTED for other
+                             weights or where the tensor-core prefill does not run.  Rounding an activation to
+                             E4M3 is off by up to 2^-4 of its value: about 2.6 % of a row (relative L2). */
 } k2_option;
 k2_status k2_set_option(k2_ctx* ctx, int32_t option, int64_t value);
 
@@ -615,7 +623,7 @@ k2_status k2_paged_attention(const k2_paged_kv* kv, const void* d_q, int32_t dty
  * K2_OPT_PREFILL_SPLIT says (it applies to the GEMMs' activations); a query beyond
  * fp16's range raises the device guard.
  * K2_ERR_UNSUPPORTED unless the model runs its prefill on the tensor cores with
- * bf16 weights; K2_ERR_SHAPE for more than max_batch requests, more tokens than a
+ * bf16 weights, or with fp8 weights and K2_OPT_ACT8; K2_ERR_SHAPE for more than max_batch requests, more tokens than a
  * prefill block (min(2048, max_context rounded up to 128)), or pools of another
  * shape.  A position at or beyond max_context's rows raises the device guard. */
 k2_status k2_paged_step(k2_ctx* ctx, const k2_paged_kv* layers, const int32_t* d_tokens, const int32_t* d_positions,

@@ -90,3 +90,35 @@ def linear(w, x, w_scale=None, x_scale=None, bias=None, activation=None, residua
         y = y + np.asarray(residual, np.float64)
         off = off + U * np.abs(y)
     return y, off
+
+
+class _RoundedMatrix:
+    """A weight matrix that rounds the rows multiplied with it to E4M3 codes first (`before`: and to a 16-bit type before that)."""
+
+    __array_ufunc__ = None  # x @ self asks self
+
+    def __init__(self, w, before):
+        self.w, self.before = w, before
+
+    @property
+    def T(self):
+        return self
+
+    def __rmatmul__(self, x):
+        x = np.asarray(x, dtype=F32)
+        if self.before == "f16":
+            x = x.astype(np.float16).astype(F32)
+        elif self.before == "bf16":
+            u = x.view(np.uint32)
+            x = ((u + 0x7FFF + ((u >> 16) & 1)) & 0xFFFF0000).astype(np.uint32).view(F32)
+        codes, scale = encode_rows(x)
+        return (E4M3_VALUES[codes] * scale.astype(np.float64)[:, None]) @ self.w.T
+
+
+def act8(model, attention="f16"):
+    """The oracle model with the projections of its layers over E4M3 activations: the library keeps the attention's output as
+    `attention` ("f16" or "bf16") and the SwiGLU's as bf16 until they are rounded to codes."""
+    plain = model._w
+    before = {"wq": None, "wk": None, "wv": None, "w_gate": None, "w_up": None, "wo": attention, "w_down": "bf16"}
+    model._w = lambda name, layer=-1: _RoundedMatrix(plain(name, layer), before[name]) if name in before else plain(name, layer)
+    return model
