@@ -60,10 +60,26 @@ __device__ __forceinline__ float load_gain(const void* g, int dtype, int i) {
 
 // |v| as a number that grows with it and is largest for a NaN
 __device__ __forceinline__ unsigned magnitude(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
-// the larger of m and |v|; a NaN wins
-__device__ __forceinline__ float max_magnitude(float m, float v) {
-  asm("max.NaN.f32 %0, %0, %1;" : "+f"(m) : "f"(fabsf(v)));
+// the largest of |m|, |a| and |b|; a NaN wins
+__device__ __forceinline__ float max_magnitude(float m, float a, float b) {
+  asm("max.NaN.abs.f32 %0, %0, %1, %2;" : "+f"(m) : "f"(a), "f"(b));
   return m;
+}
+// pairs of fp32 numbers, each product and sum rounded as by itself
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ float2 two(f32x2 v) {
+  float2 f;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+  return f;
 }
 
 __device__ __forceinline__ uint32_t code_of(float y, float s) {
@@ -99,49 +115,75 @@ constexpr float kUnit = 0x1p-80f;
 // so that a thread adds its squares into one of as many sums.
 constexpr int kGroups = 4;
 
+// 8 values as they are held until their row's maximum is known: fp32, or the 16-bit values themselves
 template <typename T>
-struct Eight;  // 8 values at a 16-byte aligned place
-template <>
-struct Eight<float> {
-  __device__ __forceinline__ static void load(const float* p, float* f) {
-    const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-    f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
-  }
-  __device__ __forceinline__ static void store(float* p, const float* f) {
-    *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
-    *reinterpret_cast<float4*>(p + 4) = make_float4(f[4], f[5], f[6], f[7]);
-  }
-};
-template <>
-struct Eight<__nv_bfloat16> {
-  __device__ __forceinline__ static void load(const __nv_bfloat16* p, float* f) {
-    Unpack<__nv_bfloat16>::run(*reinterpret_cast<const uint4*>(p), f);
-  }
-  __device__ __forceinline__ static void store(__nv_bfloat16* p, const float* f) {
-    uint4 v;
-    __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&v);
+struct Held {
+  uint4 bits = {0, 0, 0, 0};
+  __device__ __forceinline__ void load(const T* p) { bits = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void values(f32x2 (&f)[4]) const {
+    float v[8];
+    Unpack<T>::run(bits, v);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-    *reinterpret_cast<uint4*>(p) = v;
+    for (int i = 0; i < 4; ++i) f[i] = pk2(v[2 * i], v[2 * i + 1]);
+  }
+  // the largest magnitude so far: as pairs of 15-bit numbers, among which a NaN's is larger than all others
+  using Top = uint32_t;
+  __device__ __forceinline__ void raise(Top& top) const {
+    const uint32_t w[4] = {bits.x, bits.y, bits.z, bits.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) top = __vmaxu2(top, w[i] & 0x7FFF7FFFu);
+  }
+  __device__ __forceinline__ static float top(Top t) {
+    const uint32_t m = max(t >> 16, t & 0xFFFFu);
+    if (std::is_same<T, __nv_bfloat16>::value) return __uint_as_float(m << 16);
+    return __half2float(__ushort_as_half(static_cast<unsigned short>(m)));
   }
 };
 template <>
-struct Eight<__half> {
-  __device__ __forceinline__ static void load(const __half* p, float* f) {
-    Unpack<__half>::run(*reinterpret_cast<const uint4*>(p), f);
+struct Held<float> {
+  ulonglong2 bits[2] = {{0, 0}, {0, 0}};
+  __device__ __forceinline__ void load(const float* p) {
+    bits[0] = reinterpret_cast<const ulonglong2*>(p)[0];
+    bits[1] = reinterpret_cast<const ulonglong2*>(p)[1];
   }
-  __device__ __forceinline__ static void store(__half* p, const float* f) {
-    uint4 v;
-    __half2* h = reinterpret_cast<__half2*>(&v);
+  __device__ __forceinline__ void values(f32x2 (&f)[4]) const { f[0] = bits[0].x, f[1] = bits[0].y, f[2] = bits[1].x, f[3] = bits[1].y; }
+  using Top = float;
+  __device__ __forceinline__ void raise(Top& top) const {
+    f32x2 f[4];
+    values(f);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) h[i] = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
-    *reinterpret_cast<uint4*>(p) = v;
+    for (int i = 0; i < 4; ++i) top = max_magnitude(top, two(f[i]).x, two(f[i]).y);
   }
+  __device__ __forceinline__ static float top(Top t) { return t; }
 };
-__device__ __forceinline__ void load_gain8(const void* g, int dtype, int i, float* f) {
-  if (dtype == K2_F32) Eight<float>::load(static_cast<const float*>(g) + i, f);
-  else if (dtype == K2_BF16) Eight<__nv_bfloat16>::load(static_cast<const __nv_bfloat16*>(g) + i, f);
-  else Eight<__half>::load(static_cast<const __half*>(g) + i, f);
+__device__ __forceinline__ void store8(float* p, const f32x2 (&f)[4]) {
+  reinterpret_cast<ulonglong2*>(p)[0] = make_ulonglong2(f[0], f[1]);
+  reinterpret_cast<ulonglong2*>(p)[1] = make_ulonglong2(f[2], f[3]);
+}
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const f32x2 (&f)[4]) {
+  uint4 v;
+  __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&v);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(two(f[i]).x, two(f[i]).y);
+  *reinterpret_cast<uint4*>(p) = v;
+}
+__device__ __forceinline__ void store8(__half* p, const f32x2 (&f)[4]) {
+  uint4 v;
+  __half2* h = reinterpret_cast<__half2*>(&v);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) h[i] = __floats2half2_rn(two(f[i]).x, two(f[i]).y);
+  *reinterpret_cast<uint4*>(p) = v;
+}
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, f32x2 (&f)[4]) {
+  Held<T> h;
+  h.load(p);
+  h.values(f);
+}
+__device__ __forceinline__ void load_gain8(const void* g, int dtype, int i, f32x2 (&f)[4]) {
+  if (dtype == K2_F32) load8(static_cast<const float*>(g) + i, f);
+  else if (dtype == K2_BF16) load8(static_cast<const __nv_bfloat16*>(g) + i, f);
+  else load8(static_cast<const __half*>(g) + i, f);
 }
 
 __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
@@ -157,206 +199,211 @@ __device__ __noinline__ uint2 codes_by_division(const float4 a, const float4 b, 
 // all but one value in 10^5, it is that.  A power of two has an exact reciprocal.  (With a division per value 8192 x 10240
 // took 59.5 us.)
 struct RowScale {
-  float s, low, high;
+  float s;
+  f32x2 low, high;
   bool fine, exact;  // all values finite; the products bound the quotient
   __device__ __forceinline__ explicit RowScale(unsigned top) {
     fine = top < 0x7F800000u;
     s = fine ? __uint_as_float(top) / kTop : __uint_as_float(0x7FC00000u);
     const float r = __frcp_rn(s);
     const bool power = (__float_as_uint(s) & 0x007FFFFFu) == 0;
-    low = power ? r : r * (1.0f - 0x1p-22f);
-    high = power ? r : r * (1.0f + 0x1p-22f);
-    exact = s >= 0x1p-120f && s <= 0x1p120f;
+    const float l = power ? r : r * (1.0f - 0x1p-22f), h = power ? r : r * (1.0f + 0x1p-22f);
+    low = pk2(l, l);
+    high = pk2(h, h);
+    exact = s >= 0x1p-120f && s <= 0x1p120f;  // (not where it is NaN)
   }
-  __device__ __forceinline__ uint2 codes(const float* y) const {
-    if (!fine) return make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
+  __device__ __forceinline__ static uint32_t four(f32x2 a, f32x2 b, f32x2 r) {
+    const float2 x = two(mul2(a, r)), y = two(mul2(b, r));
+    return codes4(x.x, x.y, y.x, y.y);
+  }
+  __device__ __forceinline__ uint2 codes(const f32x2 (&y)[4]) const {
     if (exact) {
-      const uint2 l = make_uint2(codes4(y[0] * low, y[1] * low, y[2] * low, y[3] * low),
-                                 codes4(y[4] * low, y[5] * low, y[6] * low, y[7] * low));
-      const uint2 h = make_uint2(codes4(y[0] * high, y[1] * high, y[2] * high, y[3] * high),
-                                 codes4(y[4] * high, y[5] * high, y[6] * high, y[7] * high));
+      const uint2 l = make_uint2(four(y[0], y[1], low), four(y[2], y[3], low)), h = make_uint2(four(y[0], y[1], high), four(y[2], y[3], high));
       if (l.x == h.x && l.y == h.y) return l;
     }
+    if (!fine) return make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
     if (s == 0.f) return make_uint2(0u, 0u);
-    return codes_by_division(make_float4(y[0], y[1], y[2], y[3]), make_float4(y[4], y[5], y[6], y[7]), s);
+    const float2 a = two(y[0]), b = two(y[1]), c = two(y[2]), d = two(y[3]);
+    return codes_by_division(make_float4(a.x, a.y, b.x, b.y), make_float4(c.x, c.y, d.x, d.y), s);
   }
 };
 
-// 8 values as they are held until their row's maximum is known: fp32, or the 16-bit values themselves
-template <typename T>
-struct Held {
-  uint4 bits = {0, 0, 0, 0};
-  __device__ __forceinline__ void load(const T* p) { bits = *reinterpret_cast<const uint4*>(p); }
-  __device__ __forceinline__ void values(float* f) const { Unpack<T>::run(bits, f); }
-};
-template <>
-struct Held<float> {
-  float f8[8] = {};
-  __device__ __forceinline__ void load(const float* p) { Eight<float>::load(p, f8); }
-  __device__ __forceinline__ void values(float* f) const {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) f[j] = f8[j];
-  }
+constexpr int kRowThreads = 320, kVectorThreads = 512, kWideThreads = 1024;
+
+// what the warps of a CTA tell each other
+struct RowShared {
+  float sums[32][kGroups];
+  unsigned tops[32];
 };
 
-constexpr int kVectorThreads = 512;
+// One row, spread over the CTA: thread i holds vectors i, i + threads, ...
+template <typename XT, typename RT, bool NORM, int V>
+struct Row {
+  static constexpr bool kAdds = !std::is_same<RT, None>::value;
+  using Added = typename std::conditional<kAdds, RT, float>::type;
+  Held<XT> x[V];
+  Held<Added> r[kAdds ? V : 1];
 
-// the largest of the CTA's values, as a magnitude, in every thread
-__device__ __forceinline__ unsigned top_of(float top, unsigned* tops) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-  const unsigned m = __reduce_max_sync(0xffffffffu, magnitude(top));
-  if (warps == 1) return m;
-  if (lane == 0) tops[warp] = m;
-  __syncthreads();
-  return __reduce_max_sync(0xffffffffu, lane < warps ? tops[lane] : 0u);
-}
-
-template <typename T, int V>
-__global__ void __launch_bounds__(kVectorThreads) vector_quantize_kernel(const RowArgs a) {
-  __shared__ unsigned tops[32];
-  const int tid = threadIdx.x, n8 = a.cols >> 3;
-  const long long t = blockIdx.x;
-  const T* x = static_cast<const T*>(a.x) + a.x_stride * t;
-  uint8_t* codes = a.codes + a.codes_stride * t;
-  pdl_wait();  // the rows may be the previous kernel's
-  pdl_trigger();
-  Held<T> h[V];
-#pragma unroll
-  for (int i = 0; i < V; ++i)
-    if (tid + i * static_cast<int>(blockDim.x) < n8) h[i].load(x + 8 * (tid + i * blockDim.x));
-  float top = 0.f;
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    float f[8];
-    h[i].values(f);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) top = max_magnitude(top, f[j]);
-  }
-  const RowScale scale(top_of(top, tops));
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int v = tid + i * blockDim.x;
-    if (v < n8) {
-      float f[8];
-      h[i].values(f);
-      *reinterpret_cast<uint2*>(codes + 8 * v) = scale.codes(f);
-    }
-  }
-  if (tid == 0) a.scales[t] = scale.s;
-}
-
-template <typename XT, typename RT, int V>
-__global__ void __launch_bounds__(kVectorThreads) vector_norm_kernel(const RowArgs a) {
-  __shared__ float sums[kGroups][32];
-  __shared__ unsigned tops[32];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, warps = blockDim.x >> 5;
-  const int n8 = a.cols >> 3, size8 = n8 / a.groups;  // vectors of a row, of a group
-  const long long t = blockIdx.x;
-  int group[V];
-#pragma unroll
-  for (int i = 0; i < V; ++i) group[i] = (tid + i * static_cast<int>(blockDim.x)) / size8;  // >= groups: none
-  pdl_wait();  // the rows may be the previous kernel's
-  pdl_trigger();
-  const XT* x = static_cast<const XT*>(a.x) + a.x_stride * t;
-  float h[V][8] = {};
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int v = tid + i * blockDim.x;
-    if (v < n8) Eight<XT>::load(x + 8 * v, h[i]);
-  }
-  if constexpr (!std::is_same<RT, None>::value) {
-    const RT* res = static_cast<const RT*>(a.res) + a.res_stride * t;
-    RT* res_out = static_cast<RT*>(a.res_out) + a.res_out_stride * t;
-    Held<RT> r[V];
+  __device__ __forceinline__ void load(const XT* from, const Added* added, int n8) {
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int v = tid + i * blockDim.x;
-      if (v < n8) r[i].load(res + 8 * v);
+      const int v = threadIdx.x + i * blockDim.x;
+      if (v < n8) x[i].load(from + 8 * v);
     }
+    if constexpr (kAdds) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int v = tid + i * blockDim.x;
-      float f[8];
-      r[i].values(f);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) h[i][j] += f[j];
-      if (v < n8) Eight<RT>::store(res_out + 8 * v, h[i]);
+      for (int i = 0; i < V; ++i) {
+        const int v = threadIdx.x + i * blockDim.x;
+        if (v < n8) r[i].load(added + 8 * v);
+      }
     }
   }
-  // every thread's sums of each group, joined; `unit`: what the values are multiplied with first
-  const float count = static_cast<float>(8 * size8);
-  float mean[kGroups];
-  auto means = [&](float unit) {
-    float ss[kGroups] = {};
+
+  // the largest of the CTA's values, as a magnitude, in every thread
+  __device__ __forceinline__ static unsigned top_of(float top, unsigned* tops) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+    const unsigned m = __reduce_max_sync(0xffffffffu, magnitude(top));
+    if (lane == 0) tops[warp] = m;
+    __syncthreads();
+    return __reduce_max_sync(0xffffffffu, lane < warps ? tops[lane] : 0u);
+  }
+  __device__ __forceinline__ static void store_codes(const RowArgs& a, long long t, int v, uint2 w) {
+    *reinterpret_cast<uint2*>(a.codes + a.codes_stride * t + 8 * v) = w;
+  }
+
+  // what is stored of row t
+  __device__ __forceinline__ void finish(const RowArgs& a, long long t, RowShared& sh) {
+    const int n8 = a.cols >> 3;
+    if constexpr (NORM) {
+      normalise(a, t, n8, sh);
+    } else {
+      typename Held<XT>::Top top = 0;
+#pragma unroll
+      for (int i = 0; i < V; ++i) x[i].raise(top);
+      const RowScale scale(top_of(Held<XT>::top(top), sh.tops));
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int v = threadIdx.x + i * blockDim.x;
+        f32x2 f[4];
+        x[i].values(f);
+        if (v < n8) store_codes(a, t, v, scale.codes(f));
+      }
+      if (threadIdx.x == 0) a.scales[t] = scale.s;
+    }
+  }
+
+  __device__ __forceinline__ void normalise(const RowArgs& a, long long t, int n8, RowShared& sh) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5, size8 = n8 / a.groups;
+    int group[V];
+    f32x2 h[V][4];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      float sq = 0.f;
+      const int v = threadIdx.x + i * blockDim.x;
+      group[i] = v < size8 ? 0 : v < 2 * size8 ? 1 : v < 3 * size8 ? 2 : 3;  // (what lies behind the row is 0)
+      x[i].values(h[i]);
+      if constexpr (kAdds) {
+        f32x2 f[4];
+        r[i].values(f);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float e = h[i][j] * unit;
-        sq = fmaf(e, e, sq);
+        for (int j = 0; j < 4; ++j) h[i][j] = add2(h[i][j], f[j]);
+        if (v < n8) store8(static_cast<RT*>(a.res_out) + a.res_out_stride * t + 8 * v, h[i]);
+      }
+    }
+    // the sum of each group's squares over the CTA, lanes g, g + 4, ... of every warp taking the last steps of group g; `unit`:
+    // what the values are multiplied with first
+    const float count = static_cast<float>(8 * size8);
+    auto mean_of_lane = [&](float unit) {
+      float ss[kGroups] = {};
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        f32x2 sq2 = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const f32x2 e = unit == 1.f ? h[i][j] : mul2(h[i][j], pk2(unit, unit));
+          sq2 = fma2(e, e, sq2);
+        }
+        const float sq = sum2(sq2);
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g) ss[g] += group[i] == g ? sq : 0.f;
       }
 #pragma unroll
-      for (int g = 0; g < kGroups; ++g) ss[g] += group[i] == g ? sq : 0.f;
+      for (int g = 0; g < kGroups; ++g) {
+        if (g >= a.groups) break;
+        const float w = warp_sum(ss[g]);
+        if (lane == 0) sh.sums[warp][g] = w;
+      }
+      __syncthreads();
+      float sum = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWideThreads / 32; w += 8) {
+        if (w >= warps) break;
+        if (w + (lane >> 2) < warps) sum += sh.sums[w + (lane >> 2)][lane & 3];
+      }
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      return sum / count + a.eps * unit * unit;
+    };
+    float mean = mean_of_lane(1.f);
+    // a finite row's squares overflow (or a value is not finite): those groups in other units
+    const bool over = (lane & 3) < a.groups && !(mean <= 3.4028235e38f);
+    const unsigned overs = __ballot_sync(0xffffffffu, over);
+    if (overs != 0) {
+      __syncthreads();  // the sums have been read
+      const float again = mean_of_lane(kUnit);
+      if (over) mean = again;
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if ((overs >> group[i] & 1u) != 0)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) h[i][j] = mul2(h[i][j], pk2(kUnit, kUnit));
     }
+    const float mine = __frsqrt_rn(mean);
+    float top = 0.f, factor[kGroups];
 #pragma unroll
     for (int g = 0; g < kGroups; ++g) {
-      if (g >= a.groups) break;
-      const float w = warp_sum(ss[g]);
-      if (lane == 0) sums[g][warp] = w;
+      factor[g] = 0.f;
+      if (g < a.groups) factor[g] = __shfl_sync(0xffffffffu, mine, g);
     }
-    __syncthreads();
 #pragma unroll
-    for (int g = 0; g < kGroups; ++g) {
-      if (g >= a.groups) break;
-      mean[g] = warp_sum(lane < warps ? sums[g][lane] : 0.f) / count + a.eps * unit * unit;
+    for (int i = 0; i < V; ++i) {
+      float f = factor[0];
+#pragma unroll
+      for (int g = 1; g < kGroups; ++g) f = group[i] == g ? factor[g] : f;
+      const int v = threadIdx.x + i * blockDim.x;
+      if (v < n8) {
+        f32x2 gain[4];
+        load_gain8(a.gain, a.gain_dtype, 8 * v, gain);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          h[i][j] = mul2(mul2(h[i][j], pk2(f, f)), gain[j]);
+          top = max_magnitude(top, two(h[i][j]).x, two(h[i][j]).y);
+        }
+      }
     }
-  };
-  means(1.f);
-  bool over = false;  // the squares of a finite row overflow (or a value is not finite): those groups in other units
+    const RowScale scale(top_of(top, sh.tops));
 #pragma unroll
-  for (int g = 0; g < kGroups; ++g) over |= g < a.groups && !(mean[g] <= 3.4028235e38f);
-  if (over) {
-    float first[kGroups];
-#pragma unroll
-    for (int g = 0; g < kGroups; ++g) first[g] = mean[g];
-    __syncthreads();  // the sums have been read
-    means(kUnit);
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-#pragma unroll
-      for (int g = 0; g < kGroups; ++g)
-        if (g < a.groups && group[i] == g && !(first[g] <= 3.4028235e38f))
-#pragma unroll
-          for (int j = 0; j < 8; ++j) h[i][j] *= kUnit;
-#pragma unroll
-    for (int g = 0; g < kGroups; ++g)
-      if (g < a.groups && first[g] <= 3.4028235e38f) mean[g] = first[g];
-  }
-  float top = 0.f, factor[kGroups];
-#pragma unroll
-  for (int g = 0; g < kGroups; ++g) factor[g] = g < a.groups ? 1.0f / sqrtf(mean[g]) : 0.f;
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    float f = factor[0], gain[8] = {};
-#pragma unroll
-    for (int g = 1; g < kGroups; ++g) f = group[i] == g ? factor[g] : f;
-    const int v = tid + i * blockDim.x;
-    if (v < n8) load_gain8(a.gain, a.gain_dtype, 8 * v, gain);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      h[i][j] = v < n8 ? h[i][j] * f * gain[j] : 0.f;
-      top = max_magnitude(top, h[i][j]);
+    for (int i = 0; i < V; ++i) {
+      const int v = threadIdx.x + i * blockDim.x;
+      if (v < n8) store_codes(a, t, v, scale.codes(h[i]));
     }
+    if (threadIdx.x == 0) a.scales[t] = scale.s;
   }
-  const RowScale scale(top_of(top, tops));
-  uint8_t* codes = a.codes + a.codes_stride * t;
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int v = tid + i * blockDim.x;
-    if (v < n8) *reinterpret_cast<uint2*>(codes + 8 * v) = scale.codes(h[i]);
-  }
-  if (tid == 0) a.scales[t] = scale.s;
+};
+
+// A CTA per row.  Many rows, the usual case: up to 320 threads (512 with 4 and more vectors each), so few registers that 1280
+// threads fit an SM and their rows are on their way while others are worked on.  WIDE: up to 1024 threads.
+// (Rows copied ahead into shared memory by CTAs that stay: 8192 x 10240 values 58 us, 49 as it is.)
+template <typename XT, typename RT, bool NORM, int V, bool WIDE>
+__global__ void __launch_bounds__(WIDE ? kWideThreads : V <= 2 ? kRowThreads : kVectorThreads, !WIDE && V <= 2 ? 1280 / kRowThreads : 1)
+    vector_rows_kernel(const RowArgs a) {
+  using R = Row<XT, RT, NORM, V>;
+  __shared__ RowShared sh;
+  const long long t = blockIdx.x;
+  pdl_wait();  // the rows may be the previous kernel's
+  pdl_trigger();
+  R row;
+  row.load(static_cast<const XT*>(a.x) + a.x_stride * t, static_cast<const typename R::Added*>(a.res) + a.res_stride * t, a.cols >> 3);
+  row.finish(a, t, sh);
 }
 
 bool at8(const void* p, long long stride, int bytes) {  // 8 values of `bytes` (at most 16 bytes at once) can be taken together
@@ -417,10 +464,10 @@ __global__ void __launch_bounds__(256) rows_kernel(RowArgs a) {
   if (tid == 0) a.scales[t] = s;
 }
 
-template <typename K>
-cudaError_t launch_early(K kernel, const RowArgs& a, int tokens, int threads, size_t smem, cudaStream_t s) {
+template <typename K, typename... Args>
+cudaError_t launch_early(K kernel, int ctas, int threads, size_t smem, cudaStream_t s, const Args&... args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(tokens);
+  cfg.gridDim = dim3(ctas);
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
@@ -429,7 +476,7 @@ cudaError_t launch_early(K kernel, const RowArgs& a, int tokens, int threads, si
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, a);
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 template <typename XT, typename RT, bool NORM>
@@ -442,23 +489,33 @@ cudaError_t launch_rows(const RowArgs& a, int tokens, cudaStream_t s) {
   const bool whole = a.cols % 8 == 0 && n8 <= (NORM ? 4 : 8) * kVectorThreads && at8(a.x, a.x_stride, sizeof(XT)) && at8(a.codes, a.codes_stride, 1) &&
                      at8(a.res, a.res_stride, rb) && at8(a.res_out, a.res_out_stride, rb);
   if (whole && (!NORM || (a.groups <= kGroups && n8 % a.groups == 0 && at8(a.gain, 0, row_type_bytes(a.gain_dtype))))) {
-    const int v = n8 <= 96 ? 1 : n8 <= 640 ? 2 : n8 <= 4 * kVectorThreads ? 4 : 8;
-    const int threads = ((n8 + v - 1) / v + 31) / 32 * 32;
-    auto go = [&](auto vectors) {
-      constexpr int V = decltype(vectors)::value;
-      if constexpr (NORM) return launch_early(vector_norm_kernel<XT, RT, V>, a, tokens, threads, 0, s);
-      else return launch_early(vector_quantize_kernel<XT, V>, a, tokens, threads, 0, s);
+    // Few rows, fewer than SMs: many threads, few vectors each (16 x 10240 values: 2.6 us with 640 threads, 3.4 with 320);
+    // many: fewer threads, so that more rows are on their way at once (8192 x 10240: 66 and 56 us).
+    constexpr std::integral_constant<int, 1> one;
+    constexpr std::integral_constant<int, 2> both;
+    constexpr std::integral_constant<int, 4> four;
+    constexpr std::integral_constant<int, 8> eight;
+    auto threads = [&](int v) { return ((n8 + v - 1) / v + 31) / 32 * 32; };
+    int sms = 0;
+    e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    constexpr std::integral_constant<bool, true> wide;
+    constexpr std::integral_constant<bool, false> narrow;
+    auto go = [&](auto v, auto w) {
+      return launch_early(vector_rows_kernel<XT, RT, NORM, decltype(v)::value, decltype(w)::value>, tokens, threads(v), 0, s, a);
     };
-    if (v == 1) return go(std::integral_constant<int, 1>());
-    if (v == 2) return go(std::integral_constant<int, 2>());
-    if (v == 4) return go(std::integral_constant<int, 4>());
-    if constexpr (!NORM) return go(std::integral_constant<int, 8>());
+    if (tokens <= sms && n8 <= 640) return go(one, wide);
+    if (tokens <= sms && n8 <= 2 * kWideThreads) return go(both, wide);
+    if (n8 <= 96) return go(one, narrow);
+    if (n8 <= 2 * kRowThreads) return go(both, narrow);
+    if (n8 <= 4 * kVectorThreads) return go(four, narrow);
+    if constexpr (!NORM) return go(eight, narrow);
   }
   static std::atomic<uint64_t> ready{0};
   auto kernel = rows_kernel<XT, RT, NORM>;
   e = allow_smem(reinterpret_cast<const void*>(kernel), kMaxCols * static_cast<int>(sizeof(float)), dev, ready);
   if (e != cudaSuccess) return e;
-  return launch_early(kernel, a, tokens, 256, a.cols * sizeof(float), s);
+  return launch_early(kernel, tokens, 256, a.cols * sizeof(float), s, a);
 }
 
 template <typename XT>
