@@ -174,57 +174,47 @@ __device__ __forceinline__ void store8(__half* p, const f32x2 (&f)[4]) {
   for (int i = 0; i < 4; ++i) h[i] = __floats2half2_rn(two(f[i]).x, two(f[i]).y);
   *reinterpret_cast<uint4*>(p) = v;
 }
-template <typename T>
-__device__ __forceinline__ void load8(const T* p, f32x2 (&f)[4]) {
-  Held<T> h;
-  h.load(p);
-  h.values(f);
-}
-__device__ __forceinline__ void load_gain8(const void* g, int dtype, int i, f32x2 (&f)[4]) {
-  if (dtype == K2_F32) load8(static_cast<const float*>(g) + i, f);
-  else if (dtype == K2_BF16) load8(static_cast<const __nv_bfloat16*>(g) + i, f);
-  else load8(static_cast<const __half*>(g) + i, f);
-}
-
 __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
   return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3) |
          static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3)) << 16;
 }
-__device__ __noinline__ uint2 codes_by_division(const float4 a, const float4 b, float s) {
-  return make_uint2(codes4(__fdiv_rn(a.x, s), __fdiv_rn(a.y, s), __fdiv_rn(a.z, s), __fdiv_rn(a.w, s)),
-                    codes4(__fdiv_rn(b.x, s), __fdiv_rn(b.y, s), __fdiv_rn(b.z, s), __fdiv_rn(b.w, s)));
-}
-// A row's scale and what its values are multiplied with in place of the division: the quotient's code lies between the codes of
-// the two products (each is off by less than 2^-22 to its side, the quotient by 2^-24), and where those are the same, as for
-// all but one value in 10^5, it is that.  A power of two has an exact reciprocal.  (With a division per value 8192 x 10240
-// took 59.5 us.)
+// A row's scale, and the codes of its values.  The quotients y / s are correctly rounded without a division each: with r the
+// rounded reciprocal of s, a quotient q that is close is improved by q + (y - q s) r, whose remainder is exact; from within one
+// step of the quotient this gives the rounded quotient itself (P. Markstein, Computation of elementary functions on the IBM RISC
+// System/6000 processor, IBM J. Res. Dev. 34, 1990), and one improvement of y r leads there.  s is far enough from the ends of
+// fp32 (`plain`) that no remainder of a quotient above 2^-11 is lost; what lies below gets the code 0 anyhow.  (With a division
+// per value 8192 x 10240 took 59.5 us.  Two products that bound the quotient, and a division where they give two codes: 49 us,
+// because quotients of bf16 rows lie half way between two codes so often that every third row needed divisions.)
 struct RowScale {
   float s;
-  f32x2 low, high;
-  bool fine, exact;  // all values finite; the products bound the quotient
+  f32x2 r2, minus_s2;
+  bool fine, plain;  // all values finite; the codes can be had so
   __device__ __forceinline__ explicit RowScale(unsigned top) {
     fine = top < 0x7F800000u;
     s = fine ? __uint_as_float(top) / kTop : __uint_as_float(0x7FC00000u);
     const float r = __frcp_rn(s);
-    const bool power = (__float_as_uint(s) & 0x007FFFFFu) == 0;
-    const float l = power ? r : r * (1.0f - 0x1p-22f), h = power ? r : r * (1.0f + 0x1p-22f);
-    low = pk2(l, l);
-    high = pk2(h, h);
-    exact = s >= 0x1p-120f && s <= 0x1p120f;  // (not where it is NaN)
+    r2 = pk2(r, r);
+    minus_s2 = pk2(-s, -s);
+    plain = s >= 0x1p-80f && s <= 0x1p110f;  // (not where it is NaN)
   }
-  __device__ __forceinline__ static uint32_t four(f32x2 a, f32x2 b, f32x2 r) {
-    const float2 x = two(mul2(a, r)), y = two(mul2(b, r));
-    return codes4(x.x, x.y, y.x, y.y);
+  __device__ __forceinline__ f32x2 quotients(f32x2 y) const {
+    f32x2 q = mul2(y, r2);
+    q = fma2(fma2(q, minus_s2, y), r2, q);
+    return fma2(fma2(q, minus_s2, y), r2, q);
   }
   __device__ __forceinline__ uint2 codes(const f32x2 (&y)[4]) const {
-    if (exact) {
-      const uint2 l = make_uint2(four(y[0], y[1], low), four(y[2], y[3], low)), h = make_uint2(four(y[0], y[1], high), four(y[2], y[3], high));
-      if (l.x == h.x && l.y == h.y) return l;
-    }
+    const float2 a = two(quotients(y[0])), b = two(quotients(y[1])), c = two(quotients(y[2])), d = two(quotients(y[3]));
+    return make_uint2(codes4(a.x, a.y, b.x, b.y), codes4(c.x, c.y, d.x, d.y));
+  }
+  __device__ __noinline__ static uint2 divided(const float4 a, const float4 b, float s, bool fine) {
     if (!fine) return make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
     if (s == 0.f) return make_uint2(0u, 0u);
+    return make_uint2(codes4(__fdiv_rn(a.x, s), __fdiv_rn(a.y, s), __fdiv_rn(a.z, s), __fdiv_rn(a.w, s)),
+                      codes4(__fdiv_rn(b.x, s), __fdiv_rn(b.y, s), __fdiv_rn(b.z, s), __fdiv_rn(b.w, s)));
+  }
+  __device__ __forceinline__ uint2 divided(const f32x2 (&y)[4]) const {
     const float2 a = two(y[0]), b = two(y[1]), c = two(y[2]), d = two(y[3]);
-    return codes_by_division(make_float4(a.x, a.y, b.x, b.y), make_float4(c.x, c.y, d.x, d.y), s);
+    return divided(make_float4(a.x, a.y, b.x, b.y), make_float4(c.x, c.y, d.x, d.y), s, fine);
   }
 };
 
@@ -267,8 +257,20 @@ struct Row {
     __syncthreads();
     return __reduce_max_sync(0xffffffffu, lane < warps ? tops[lane] : 0u);
   }
-  __device__ __forceinline__ static void store_codes(const RowArgs& a, long long t, int v, uint2 w) {
-    *reinterpret_cast<uint2*>(a.codes + a.codes_stride * t + 8 * v) = w;
+  // the codes of row t, whose vector i is value(i, .), and its scale; again(.) stores them by divisions
+  template <typename F, typename G>
+  __device__ __forceinline__ static void store_codes(const RowArgs& a, long long t, int n8, const RowScale& scale, F value, G again) {
+    uint2* codes = reinterpret_cast<uint2*>(a.codes + a.codes_stride * t);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int v = threadIdx.x + i * blockDim.x;
+      f32x2 f[4];
+      value(i, f);
+      const uint2 w = scale.codes(f);
+      if (v < n8) codes[v] = w;
+    }
+    if (!scale.plain) again(codes);
+    if (threadIdx.x == 0) a.scales[t] = scale.s;
   }
 
   // what is stored of row t
@@ -281,14 +283,18 @@ struct Row {
 #pragma unroll
       for (int i = 0; i < V; ++i) x[i].raise(top);
       const RowScale scale(top_of(Held<XT>::top(top), sh.tops));
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const int v = threadIdx.x + i * blockDim.x;
-        f32x2 f[4];
-        x[i].values(f);
-        if (v < n8) store_codes(a, t, v, scale.codes(f));
-      }
-      if (threadIdx.x == 0) a.scales[t] = scale.s;
+      store_codes(a, t, n8, scale, [&](int i, f32x2 (&f)[4]) { x[i].values(f); },
+                  [&](uint2* codes) {  // read again: the values need not stay in registers
+                    const XT* from = static_cast<const XT*>(a.x) + a.x_stride * t;
+#pragma unroll 1
+                    for (int v = threadIdx.x; v < n8; v += blockDim.x) {
+                      Held<XT> h;
+                      f32x2 f[4];
+                      h.load(from + 8 * v);
+                      h.values(f);
+                      codes[v] = scale.divided(f);
+                    }
+                  });
     }
   }
 
@@ -364,37 +370,55 @@ struct Row {
       factor[g] = 0.f;
       if (g < a.groups) factor[g] = __shfl_sync(0xffffffffu, mine, g);
     }
+    if (a.gain_dtype == K2_F32) apply<float>(a, n8, group, factor, h, top);
+    else if (a.gain_dtype == K2_BF16) apply<__nv_bfloat16>(a, n8, group, factor, h, top);
+    else apply<__half>(a, n8, group, factor, h, top);
+    const RowScale scale(top_of(top, sh.tops));
+    store_codes(a, t, n8, scale, [&](int i, f32x2 (&f)[4]) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) f[j] = h[i][j];
+    }, [&](uint2* codes) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int v = threadIdx.x + i * blockDim.x;
+        if (v < n8) codes[v] = scale.divided(h[i]);
+      }
+    });
+  }
+
+  // the factors of the groups and the gain
+  template <typename GT>
+  __device__ __forceinline__ static void apply(const RowArgs& a, int n8, const int (&group)[V], const float (&factor)[kGroups],
+                                               f32x2 (&h)[V][4], float& top) {
+    Held<GT> gain[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int v = threadIdx.x + i * blockDim.x;
+      if (v < n8) gain[i].load(static_cast<const GT*>(a.gain) + 8 * v);
+    }
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       float f = factor[0];
 #pragma unroll
       for (int g = 1; g < kGroups; ++g) f = group[i] == g ? factor[g] : f;
-      const int v = threadIdx.x + i * blockDim.x;
-      if (v < n8) {
-        f32x2 gain[4];
-        load_gain8(a.gain, a.gain_dtype, 8 * v, gain);
+      f32x2 g8[4];
+      gain[i].values(g8);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          h[i][j] = mul2(mul2(h[i][j], pk2(f, f)), gain[j]);
-          top = max_magnitude(top, two(h[i][j]).x, two(h[i][j]).y);
-        }
+      for (int j = 0; j < 4; ++j) {
+        h[i][j] = mul2(mul2(h[i][j], pk2(f, f)), g8[j]);
+        top = max_magnitude(top, two(h[i][j]).x, two(h[i][j]).y);
       }
     }
-    const RowScale scale(top_of(top, sh.tops));
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int v = threadIdx.x + i * blockDim.x;
-      if (v < n8) store_codes(a, t, v, scale.codes(h[i]));
-    }
-    if (threadIdx.x == 0) a.scales[t] = scale.s;
   }
 };
 
 // A CTA per row.  Many rows, the usual case: up to 320 threads (512 with 4 and more vectors each), so few registers that 1280
-// threads fit an SM and their rows are on their way while others are worked on.  WIDE: up to 1024 threads.
+// threads (1536) fit an SM and their rows are on their way while others are worked on (8192 x 10240 values with 78 registers
+// 69 us, with 40 registers 49).  WIDE: up to 1024 threads.
 // (Rows copied ahead into shared memory by CTAs that stay: 8192 x 10240 values 58 us, 49 as it is.)
 template <typename XT, typename RT, bool NORM, int V, bool WIDE>
-__global__ void __launch_bounds__(WIDE ? kWideThreads : V <= 2 ? kRowThreads : kVectorThreads, !WIDE && V <= 2 ? 1280 / kRowThreads : 1)
+__global__ void __launch_bounds__(WIDE ? kWideThreads : V <= 2 ? kRowThreads : kVectorThreads,
+                                  WIDE ? 1 : V <= 2 ? 1280 / kRowThreads : V == 4 && !NORM && sizeof(XT) == 2 ? 1536 / kVectorThreads : 1)
     vector_rows_kernel(const RowArgs a) {
   using R = Row<XT, RT, NORM, V>;
   __shared__ RowShared sh;

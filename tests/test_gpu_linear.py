@@ -98,6 +98,30 @@ def test_rows_at_the_ends_of_their_type(k2, n, kind):
     check_codes(k2, x.to(T[kind]).cuda())
 
 
+def test_quotients_next_to_the_border_of_two_codes(k2):
+    """Rows of values s * B and their neighbours in float32, B half way between two codes: the code is that of the rounded
+    quotient, which falls on B, above or below it."""
+    gen = np.random.default_rng(23)
+    values = np.sort(E4M3_VALUES[:0x7F])
+    middles = ((values[1:] + values[:-1]) / 2).astype(np.float32)
+    for lo, hi in ((1.0, 2.0), (1e-20, 1e-18), (1e15, 1e16), (2.0 ** -71, 2.0 ** -70)):
+        tops = gen.uniform(lo, hi, 300).astype(np.float32)
+        scale = (tops / np.float32(448)).astype(np.float32)
+        y = (scale[:, None] * middles).astype(np.float32)
+        rows = [y, np.nextafter(y, np.float32(np.inf)), np.nextafter(y, np.float32(0)), np.nextafter(np.nextafter(y, np.float32(0)), np.float32(0))]
+        x = np.concatenate([np.repeat(tops[:, None], 4, 1)] + rows + [-r for r in rows], 1)
+        x = np.minimum(np.abs(x), tops[:, None]) * np.sign(x)
+        assert x.shape[1] % 8 == 4  # odd rows too
+        check_codes(k2, torch.from_numpy(x).cuda())
+        check_codes(k2, torch.from_numpy(np.concatenate([x, x[:, :4]], 1)).cuda())
+    # bf16 rows, whose quotients lie on such borders by themselves: every mantissa of the largest value
+    x = torch.randn(256, 2560, generator=torch.Generator().manual_seed(5)) * 0.2
+    x = x.clamp(-0.99, 0.99)
+    x[:, 7] = 1 + torch.arange(256) / 256
+    check_codes(k2, x.bfloat16().cuda())
+    check_codes(k2, x.half().cuda())
+
+
 def norm(k2, x, gain, residual=None, groups=1, eps=1e-6, inplace=False, pad=0, **kw):
     t, n = x.shape
     codes = torch.full((t, n + pad), 0x55, dtype=torch.uint8, device="cuda")
