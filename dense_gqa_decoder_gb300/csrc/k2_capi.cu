@@ -1005,12 +1005,29 @@ cudaError_t prefill_block(k2_ctx* c, int seq, const int32_t* d_tokens, int n, in
     if (got != K2_OK) st8 = got;
     return got == K2_OK ? cudaSuccess : cudaErrorUnknown;
   };
+  auto rows8 = [&](const void* rows, int dtype, int k, uint8_t* codes) {
+    k2_row_args r = {};
+    r.x = rows;
+    r.x_dtype = dtype;
+    r.tokens = n;
+    r.cols = k;
+    r.x_stride = k;
+    r.codes = codes;
+    r.codes_stride = wide16(k);
+    r.scales = xs;
+    return r;
+  };
   auto norm8 = [&](const void* gain) {
-    return done8(k2_norm_quantize(X, K2_F32, s.H, nullptr, 0, nullptr, 0, K2_F32, gain, K2_BF16, n, s.H, s.G, c->cfg.eps, xc,
-                                  wide16(s.H), xs, st));
+    k2_row_args r = rows8(X, K2_F32, s.H, xc);
+    r.gain = gain;
+    r.gain_dtype = K2_BF16;
+    r.groups = s.G;
+    r.eps = c->cfg.eps;
+    return done8(k2_norm_quantize(&r, st));
   };
   auto quantize8 = [&](const void* rows, int dtype, int k, uint8_t* codes) {
-    return done8(k2_quantize_rows(rows, dtype, k, n, k, codes, wide16(k), xs, st));
+    const k2_row_args r = rows8(rows, dtype, k, codes);
+    return done8(k2_quantize_rows(&r, st));
   };
   auto linear8 = [&](int l, int m, const uint8_t* codes, int N, int K, int act, void* out, int out_dtype, const void* resid) {
     LinearArgs g = {};

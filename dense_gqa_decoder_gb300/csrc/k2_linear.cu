@@ -725,18 +725,21 @@ k2_status launch_linear(const LinearWeights& w, const void* x, long long x_strid
   const WeightPlace place = {w.packed ? 1 : 0, a.dtype == K2_F8 ? kStepBytes : kStepBytes / 2};
   const int steps = (a.cols + place.step - 1) / place.step;
   // Few tokens per tile and K split over CTAs, or wide tiles on pairs of SMs: the cheaper by what was measured, in units of
-  // 0.67 ns.  Few: a K step takes 0.30 us on an SM with one CTA and 0.37 for the two of an SM with two, and 1.2 us more to
-  // join (down of 128 tokens 14.4 us against the pairs' 20.5, q|k|v of 256 tokens 10.5 against 9.1).  Up to 64 tokens it is
-  // always that one (gate and up of 64 tokens 14.4 against 16.5).
+  // 0.67 ns.  Few: a K step takes 0.30 us on an SM with one CTA and 0.37 for the two of an SM with two; joining shares of K
+  // takes some 1.3 us, and 2 us more where there are more CTAs than SMs.  Pairs: see below, and 2 us more to start than the
+  // few without a split.  (Down of 128 tokens: few 14.4 us, pairs 20.5; gate and up of 128 15.2 and 17.6; q|k|v of 128 9.0 and
+  // 8.3, of 256 10.5 and 9.1.)  Activations take the few's four finishing warps longer (333 x 640 by 1664 with a GELU 12.0 us,
+  // pairs 7.9).  Up to 64 tokens it is always the few (gate and up of 64 tokens 14.4 us against 16.5).
   FewShape few = {a.tokens <= 16 ? 16 : a.tokens <= 32 ? 32 : 64, steps, 0, 1};
   const long long few_tiles = static_cast<long long>((a.rows + kRows - 1) / kRows) * ((a.tokens + few.tokens - 1) / few.tokens);
   long long few_cost = 0;
   for (int per_sm = 1; per_sm <= (a.tokens > 64 ? 2 : 1); ++per_sm) {
     const int split = static_cast<int>(std::max<long long>(1, std::min<long long>({per_sm * sms / few_tiles, kMaxSplit, steps})));
     const long long mine = (steps + split - 1) / split, load = (few_tiles * split + sms - 1) / sms;
-    const long long cost = std::max(448 * mine, 276 * mine * load) + 1800;
+    const long long cost = std::max(448 * mine, 276 * mine * load) + (split == 1 ? 1000 : load == 1 ? 3000 : 6000);
     if (few_cost == 0 || cost < few_cost) few.split = split, few_cost = cost;
   }
+  if (a.act != K2_ACT_NONE && a.act != K2_ACT_SWIGLU) few_cost += 94ll * few.tokens;
   if (a.tokens > 64) {
     // tiles as wide as cost the pair with the most tiles least: a K step of n columns takes as long as n + 224 in the matrix
     // unit (0.24 us for 128, 0.26 for 192, 0.32 for 256)
@@ -748,7 +751,7 @@ k2_status launch_linear(const LinearWeights& w, const void* x, long long x_strid
       if (sh.tokens == 0 || cost < best) sh.tokens = n, sh.token_tiles = tt, best = cost;
     }
     sh.stages = std::min(kPairStages, kPairRing / (kPairSteps * (kRows + sh.tokens / 2) * kStepBytes));
-    if (best <= few_cost) return launch(w, x, x_stride, a, place, sh, sh.tokens / 2, sms, dev, s);
+    if (best + 4000 <= few_cost || a.tokens > 65535 * few.tokens) return launch(w, x, x_stride, a, place, sh, sh.tokens / 2, sms, dev, s);
   }
   few.stages = std::min({kFewStages, kFewRing / few_stage(few.tokens), (steps + few.split - 1) / few.split});
   return launch(w, x, x_stride, a, place, few, few.tokens, sms, dev, s);

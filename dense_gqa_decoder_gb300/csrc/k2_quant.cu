@@ -507,6 +507,7 @@ template <typename XT, typename RT, bool NORM>
 cudaError_t launch_rows(const RowArgs& a, int tokens, cudaStream_t s) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess && (dev < 0 || dev >= 64)) e = cudaErrorInvalidDevice;
   if (e != cudaSuccess) return e;
   constexpr int rb = std::is_same<RT, None>::value ? 4 : sizeof(RT);
   const int n8 = a.cols / 8;
@@ -553,39 +554,49 @@ cudaError_t launch_norm(const RowArgs& a, int res_dtype, int tokens, cudaStream_
 bool off_type(const void* p, int bytes) { return reinterpret_cast<uintptr_t>(p) % bytes != 0; }
 
 // What both calls refuse of their input rows, codes and scales
-k2_status check_rows(const char* what, const void* d_x, int dtype, int64_t x_stride, int tokens, int cols,
-                     const uint8_t* d_codes, int64_t codes_stride, const float* d_scales) {
-  const int b = row_type_bytes(dtype);
+k2_status check_rows(const k2_row_args* p) {
+  if (!p) {
+    set_error("the arguments must be non-null");
+    return K2_ERR_ARG;
+  }
+  const int b = row_type_bytes(p->x_dtype);
   if (!b) {
-    set_error("%s must be K2_F32, K2_BF16 or K2_F16 (got dtype %d)", what, dtype);
+    set_error("rows must be K2_F32, K2_BF16 or K2_F16 (got dtype %d)", p->x_dtype);
     return K2_ERR_UNSUPPORTED;
   }
-  if (tokens < 0 || tokens > 1 << 30 || cols < 1 || cols > kMaxCols) {
-    set_error("tokens in [0, 2^30] and rows of 1 .. %d values (got %d, %d)", kMaxCols, tokens, cols);
+  if (p->tokens < 0 || p->tokens > 1 << 30 || p->cols < 1 || p->cols > kMaxCols) {
+    set_error("tokens in [0, 2^30] and rows of 1 .. %d values (got %d, %d)", kMaxCols, p->tokens, p->cols);
     return K2_ERR_SHAPE;
   }
-  if (tokens == 0) return K2_OK;
-  if (!d_x || !d_codes || !d_scales) {
-    set_error("the input rows, d_codes and d_scales must be non-null");
+  if (p->tokens == 0) return K2_OK;
+  if (!p->x || !p->codes || !p->scales) {
+    set_error("x, codes and scales must be non-null");
     return K2_ERR_ARG;
   }
-  if (off_type(d_x, b) || off_type(d_scales, 4)) {
-    set_error("%s and d_scales must be aligned to their types", what);
+  if (off_type(p->x, b) || off_type(p->scales, 4)) {
+    set_error("x and scales must be aligned to their types");
     return K2_ERR_ARG;
   }
-  const int64_t most = INT64_MAX / 8 / (tokens + 1);  // so that no offset overflows
-  if (tokens > 1 && (x_stride < cols || codes_stride < cols || x_stride > most || codes_stride > most)) {
-    set_error("rows must be at least as far apart as they are long (%d; got %lld, codes %lld)", cols,
-              static_cast<long long>(x_stride), static_cast<long long>(codes_stride));
+  const int64_t most = INT64_MAX / 8 / (p->tokens + 1);  // so that no offset overflows
+  if (p->tokens > 1 && (p->x_stride < p->cols || p->codes_stride < p->cols || p->x_stride > most || p->codes_stride > most)) {
+    set_error("rows must be at least as far apart as they are long (%d; got %lld, codes %lld)", p->cols,
+              static_cast<long long>(p->x_stride), static_cast<long long>(p->codes_stride));
     return K2_ERR_ARG;
   }
-  const RowSet x = {d_x, b * x_stride, static_cast<int64_t>(b) * cols, tokens}, codes = {d_codes, codes_stride, cols, tokens},
-               scales = {d_scales, 4, 4, tokens};
+  const RowSet x = {p->x, b * p->x_stride, static_cast<int64_t>(b) * p->cols, p->tokens},
+               codes = {p->codes, p->codes_stride, p->cols, p->tokens}, scales = {p->scales, 4, 4, p->tokens};
   if (sets_meet(x, codes) || sets_meet(x, scales) || sets_meet(codes, scales)) {
     set_error("the codes and scales may not lie over the input or each other");
     return K2_ERR_ARG;
   }
   return K2_OK;
+}
+
+// (the distance of the one row of a single token is not read)
+RowArgs row_args(const k2_row_args& p) {
+  const long long many = p.tokens > 1;
+  return {p.x, many * p.x_stride, p.residual, many * p.residual_stride, p.residual_out, many * p.residual_out_stride, p.gain,
+          p.gain_dtype, p.cols, p.groups, p.eps, p.codes, many * p.codes_stride, p.scales};
 }
 
 }  // namespace
@@ -596,82 +607,71 @@ using namespace k2;
 
 extern "C" {
 
-k2_status k2_quantize_rows(const void* d_x, int32_t dtype, int64_t x_stride, int32_t tokens, int32_t cols,
-                           uint8_t* d_codes, int64_t codes_stride, float* d_scales, void* stream) {
-  const k2_status st = check_rows("d_x", d_x, dtype, x_stride, tokens, cols, d_codes, codes_stride, d_scales);
-  if (st != K2_OK || tokens == 0) return st;
-  RowArgs a = {};
-  a.x = d_x;
-  a.x_stride = tokens > 1 ? x_stride : 0;
-  a.cols = cols;
-  a.groups = 1;
-  a.codes = d_codes;
-  a.codes_stride = tokens > 1 ? codes_stride : 0;
-  a.scales = d_scales;
+k2_status k2_quantize_rows(const k2_row_args* p, void* stream) {
+  const k2_status st = check_rows(p);
+  if (st != K2_OK) return st;
+  if (p->residual || p->residual_out || p->gain) {
+    set_error("residual, residual_out and gain belong to k2_norm_quantize");
+    return K2_ERR_ARG;
+  }
+  if (p->tokens == 0) return K2_OK;
+  const RowArgs a = row_args(*p);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = dtype == K2_F32    ? launch_rows<float, None, false>(a, tokens, s)
-                        : dtype == K2_BF16 ? launch_rows<__nv_bfloat16, None, false>(a, tokens, s)
-                                           : launch_rows<__half, None, false>(a, tokens, s);
+  const cudaError_t e = p->x_dtype == K2_F32    ? launch_rows<float, None, false>(a, p->tokens, s)
+                        : p->x_dtype == K2_BF16 ? launch_rows<__nv_bfloat16, None, false>(a, p->tokens, s)
+                                                : launch_rows<__half, None, false>(a, p->tokens, s);
   if (e == cudaSuccess) return K2_OK;
   set_error("quantize launch: %s", cudaGetErrorString(e));
   return K2_ERR_CUDA;
 }
 
-k2_status k2_norm_quantize(const void* d_x, int32_t x_dtype, int64_t x_stride, const void* d_residual,
-                           int64_t residual_stride, void* d_residual_out, int64_t residual_out_stride,
-                           int32_t residual_dtype, const void* d_gain, int32_t gain_dtype, int32_t tokens,
-                           int32_t hidden, int32_t groups, float eps, uint8_t* d_codes, int64_t codes_stride,
-                           float* d_scales, void* stream) {
-  const k2_status st = check_rows("d_x", d_x, x_dtype, x_stride, tokens, hidden, d_codes, codes_stride, d_scales);
+k2_status k2_norm_quantize(const k2_row_args* p, void* stream) {
+  const k2_status st = check_rows(p);
   if (st != K2_OK) return st;
-  const int gb = row_type_bytes(gain_dtype), rb = d_residual || d_residual_out ? row_type_bytes(residual_dtype) : 4;
+  const bool adds = p->residual || p->residual_out;
+  const int gb = row_type_bytes(p->gain_dtype), rb = adds ? row_type_bytes(p->residual_dtype) : 4;
   if (!gb || !rb) {
-    set_error("gain and residual must be K2_F32, K2_BF16 or K2_F16 (got dtypes %d, %d)", gain_dtype, residual_dtype);
+    set_error("gain and residual must be K2_F32, K2_BF16 or K2_F16 (got dtypes %d, %d)", p->gain_dtype, p->residual_dtype);
     return K2_ERR_UNSUPPORTED;
   }
-  if (groups < 1 || hidden % groups) {
-    set_error("hidden %d must be a multiple of groups (got %d)", hidden, groups);
+  if (p->groups < 1 || p->cols % p->groups) {
+    set_error("cols %d must be a multiple of groups (got %d)", p->cols, p->groups);
     return K2_ERR_SHAPE;
   }
-  if (!(eps >= 0x1p-126f) || isinf(eps)) {
-    set_error("eps must be finite and at least 2^-126 (got %g)", eps);
+  if (!(p->eps >= 0x1p-126f) || isinf(p->eps)) {
+    set_error("eps must be finite and at least 2^-126 (got %g)", p->eps);
     return K2_ERR_ARG;
   }
-  if (tokens == 0) return K2_OK;
-  if (!d_gain || !d_residual != !d_residual_out) {
-    set_error("d_gain must be non-null, d_residual and d_residual_out both given or both NULL");
+  if (p->tokens == 0) return K2_OK;
+  if (!p->gain || !p->residual != !p->residual_out) {
+    set_error("gain must be non-null, residual and residual_out both given or both NULL");
     return K2_ERR_ARG;
   }
-  if (off_type(d_gain, gb) || off_type(d_residual, rb) || off_type(d_residual_out, rb)) {
+  if (off_type(p->gain, gb) || off_type(p->residual, rb) || off_type(p->residual_out, rb)) {
     set_error("gain and residual must be aligned to their types");
     return K2_ERR_ARG;
   }
-  const int64_t most = INT64_MAX / 8 / (tokens + 1);
-  if (d_residual && tokens > 1 &&
-      (residual_stride < hidden || residual_out_stride < hidden || residual_stride > most || residual_out_stride > most)) {
-    set_error("residual rows must be at least hidden = %d elements apart (got %lld, %lld)", hidden,
-              static_cast<long long>(residual_stride), static_cast<long long>(residual_out_stride));
+  const int64_t most = INT64_MAX / 8 / (p->tokens + 1), rs = p->residual_stride, os = p->residual_out_stride;
+  if (adds && p->tokens > 1 && (rs < p->cols || os < p->cols || rs > most || os > most)) {
+    set_error("residual rows must be at least cols = %d elements apart (got %lld, %lld)", p->cols, static_cast<long long>(rs),
+              static_cast<long long>(os));
     return K2_ERR_ARG;
   }
-  const int64_t xb = row_type_bytes(x_dtype);
-  const RowSet x = {d_x, xb * x_stride, xb * hidden, tokens}, codes = {d_codes, codes_stride, hidden, tokens},
-               scales = {d_scales, 4, 4, tokens}, gain = {d_gain, 0, static_cast<int64_t>(gb) * hidden, 1},
-               res = {d_residual, rb * residual_stride, static_cast<int64_t>(rb) * hidden, tokens},
-               out = {d_residual_out, rb * residual_out_stride, static_cast<int64_t>(rb) * hidden, tokens};
-  const bool same = d_residual == d_residual_out && (tokens == 1 || residual_stride == residual_out_stride);
+  const int64_t xb = row_type_bytes(p->x_dtype), n = p->cols, t = p->tokens;
+  const RowSet x = {p->x, xb * p->x_stride, xb * n, t}, codes = {p->codes, p->codes_stride, n, t}, scales = {p->scales, 4, 4, t},
+               gain = {p->gain, 0, gb * n, 1}, res = {p->residual, rb * rs, rb * n, t}, out = {p->residual_out, rb * os, rb * n, t};
+  const bool same = p->residual == p->residual_out && (t == 1 || rs == os);
   if ((!same && sets_meet(res, out)) || sets_meet(out, x) || sets_meet(out, codes) || sets_meet(out, scales) ||
       sets_meet(out, gain) || sets_meet(codes, res) || sets_meet(codes, gain) || sets_meet(scales, res) ||
       sets_meet(scales, gain)) {
-    set_error("outputs may not lie over inputs or each other (d_residual_out may be d_residual, with its stride)");
+    set_error("outputs may not lie over inputs or each other (residual_out may be residual, with its stride)");
     return K2_ERR_ARG;
   }
-  RowArgs a = {d_x, tokens > 1 ? x_stride : 0, d_residual, tokens > 1 ? residual_stride : 0, d_residual_out,
-               tokens > 1 ? residual_out_stride : 0, d_gain, gain_dtype, hidden, groups, eps, d_codes,
-               tokens > 1 ? codes_stride : 0, d_scales};
+  const RowArgs a = row_args(*p);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = x_dtype == K2_F32    ? launch_norm<float>(a, residual_dtype, tokens, s)
-                        : x_dtype == K2_BF16 ? launch_norm<__nv_bfloat16>(a, residual_dtype, tokens, s)
-                                             : launch_norm<__half>(a, residual_dtype, tokens, s);
+  const cudaError_t e = p->x_dtype == K2_F32    ? launch_norm<float>(a, p->residual_dtype, p->tokens, s)
+                        : p->x_dtype == K2_BF16 ? launch_norm<__nv_bfloat16>(a, p->residual_dtype, p->tokens, s)
+                                                : launch_norm<__half>(a, p->residual_dtype, p->tokens, s);
   if (e == cudaSuccess) return K2_OK;
   set_error("norm launch: %s", cudaGetErrorString(e));
   return K2_ERR_CUDA;

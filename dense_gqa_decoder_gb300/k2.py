@@ -84,6 +84,14 @@ class LogitRules(C.Structure):
                 ("mask", C.c_void_p), ("mask_stride", C.c_int64), ("n_masks", C.c_int32), ("mask_row", C.c_void_p)]
 
 
+class RowArgs(C.Structure):
+    _fields_ = [("x", C.c_void_p), ("x_stride", C.c_int64), ("residual", C.c_void_p), ("residual_stride", C.c_int64),
+                ("residual_out", C.c_void_p), ("residual_out_stride", C.c_int64), ("gain", C.c_void_p),
+                ("codes", C.c_void_p), ("codes_stride", C.c_int64), ("scales", C.c_void_p), ("tokens", C.c_int32),
+                ("cols", C.c_int32), ("groups", C.c_int32), ("x_dtype", C.c_int32), ("residual_dtype", C.c_int32),
+                ("gain_dtype", C.c_int32), ("eps", C.c_float)]
+
+
 class LinearArgs(C.Structure):
     _fields_ = [("w", C.c_void_p), ("w_stride", C.c_int64), ("w_scale", C.c_void_p), ("x", C.c_void_p),
                 ("x_stride", C.c_int64), ("x_scale", C.c_void_p), ("bias", C.c_void_p), ("residual", C.c_void_p),
@@ -135,9 +143,8 @@ def _load():
                                          C.c_size_t, vp]),
         "k2_paged_step": (C.c_int, [vp, vp, vp, vp, vp, i32, vp, vp, vp, i32, i32, i32, vp, vp, vp, C.c_size_t, vp]),
         "k2_adjust_logits": (C.c_int, [vp, vp, i64, vp, i64, i32, i32, vp]),
-        "k2_quantize_rows": (C.c_int, [vp, i32, i64, i32, i32, vp, i64, vp, vp]),
-        "k2_norm_quantize": (C.c_int, [vp, i32, i64, vp, i64, vp, i64, i32, vp, i32, i32, i32, i32, C.c_float, vp, i64, vp,
-                                       vp]),
+        "k2_quantize_rows": (C.c_int, [vp, vp]),
+        "k2_norm_quantize": (C.c_int, [vp, vp]),
         "k2_linear": (C.c_int, [vp, vp]),
     }
     for name, (res, args) in sig.items():
@@ -710,13 +717,16 @@ _MATRIX_DTYPES = {torch.float8_e4m3fn: K2_F8, torch.uint8: K2_F8, torch.bfloat16
 
 def _matrix(what, t, dtypes, dev, shape=None):
     """A [rows, columns] tensor whose rows are contiguous and may be apart: their distance"""
-    if t.dtype in dtypes and t.get_device() == dev and t.dim() == 2 and (shape is None or t.shape == shape):
-        row, one = t.stride()
-        if one == 1 or t.shape[1] == 1:
-            return row
+    stride = t.stride()
+    if len(stride) == 2 and t.dtype in dtypes and t.get_device() == dev and (shape is None or t.shape == shape) and (
+            stride[1] == 1 or t.shape[1] == 1):
+        return stride[0]
     raise ValueError(f"{what} must be {'[rows, columns]' if shape is None else list(shape)} rows of "
                      f"{' or '.join(str(d) for d in dtypes)} on cuda:{dev}, each row contiguous, got {t.dtype} "
-                     f"{tuple(t.shape)} with strides {t.stride()} on {t.device}")
+                     f"{tuple(t.shape)} with strides {stride} on {t.device}")
+
+
+_ROWS = struct.Struct("@PqPqPqPPqPiiiiiif4x").pack  # a RowArgs
 
 
 def quantize_rows(x, codes, scales, stream=None):
@@ -724,12 +734,14 @@ def quantize_rows(x, codes, scales, stream=None):
     of the same shape (float8_e4m3fn or uint8) and scales [tokens] fp32."""
     dev = _device(x)
     xs = _matrix("x", x, _ROW_DTYPES, dev)
-    cs = _matrix("codes", codes, _CODE_DTYPES, dev, x.shape)
-    n, cols = x.shape
-    if scales.dtype is not torch.float32 or scales.get_device() != dev or scales.shape != (n,) or not scales.is_contiguous():
+    cs = _matrix("codes", codes, _CODE_DTYPES, dev)
+    n, cols = shape = x.shape
+    if codes.shape != shape:
+        _matrix("codes", codes, _CODE_DTYPES, dev, shape)
+    if scales.dtype is not torch.float32 or scales.get_device() != dev or scales.numel() != n or not scales.is_contiguous():
         _need("scales", scales, torch.float32, (n,), dev)
-    st = LIB.k2_quantize_rows(x.data_ptr(), _ROW_DTYPES[x.dtype], xs, n, cols, codes.data_ptr(), cs, scales.data_ptr(),
-                              _raw_stream(stream, dev))
+    st = LIB.k2_quantize_rows(_ROWS(x.data_ptr(), xs, 0, 0, 0, 0, 0, codes.data_ptr(), cs, scales.data_ptr(), n, cols, 1,
+                                    _ROW_DTYPES[x.dtype], 0, 0, 1.0), _raw_stream(stream, dev))
     if st:
         _call(st)
 
@@ -741,25 +753,30 @@ def norm_quantize(x, gain, codes, scales, *, residual=None, residual_out=None, g
     residual and gain are fp32, bf16 or fp16."""
     dev = _device(x)
     xs = _matrix("x", x, _ROW_DTYPES, dev)
-    cs = _matrix("codes", codes, _CODE_DTYPES, dev, x.shape)
-    n, hidden = x.shape
-    if scales.dtype is not torch.float32 or scales.get_device() != dev or scales.shape != (n,) or not scales.is_contiguous():
+    cs = _matrix("codes", codes, _CODE_DTYPES, dev)
+    n, hidden = shape = x.shape
+    if codes.shape != shape:
+        _matrix("codes", codes, _CODE_DTYPES, dev, shape)
+    if scales.dtype is not torch.float32 or scales.get_device() != dev or scales.numel() != n or not scales.is_contiguous():
         _need("scales", scales, torch.float32, (n,), dev)
-    if gain.dtype not in _ROW_DTYPES or gain.get_device() != dev or gain.shape != (hidden,) or not gain.is_contiguous():
+    gdt = _ROW_DTYPES.get(gain.dtype)
+    if gdt is None or gain.get_device() != dev or gain.numel() != hidden or not gain.is_contiguous():
         raise ValueError(f"gain must be a contiguous float32, bfloat16 or float16 tensor of {hidden} values on cuda:{dev}, "
                          f"got {gain.dtype} {tuple(gain.shape)} on {gain.device}")
     res = rs = out = os_ = rdt = 0
     if residual is not None:
-        rs = os_ = _matrix("residual", residual, _ROW_DTYPES, dev, x.shape)
+        rs = os_ = _matrix("residual", residual, _ROW_DTYPES, dev)
         res = out = residual.data_ptr()
         rdt = _ROW_DTYPES[residual.dtype]
         if residual_out is not None:
-            os_ = _matrix("residual_out", residual_out, (residual.dtype,), dev, x.shape)
+            os_ = _matrix("residual_out", residual_out, (residual.dtype,), dev)
             out = residual_out.data_ptr()
+        if residual.shape != shape or residual_out is not None and residual_out.shape != shape:
+            raise ValueError(f"residual and residual_out must be {tuple(shape)} like x")
     elif residual_out is not None:
         raise ValueError("residual_out needs residual")
-    st = LIB.k2_norm_quantize(x.data_ptr(), _ROW_DTYPES[x.dtype], xs, res, rs, out, os_, rdt, gain.data_ptr(),
-                              _ROW_DTYPES[gain.dtype], n, hidden, groups, eps, codes.data_ptr(), cs, scales.data_ptr(),
+    st = LIB.k2_norm_quantize(_ROWS(x.data_ptr(), xs, res, rs, out, os_, gain.data_ptr(), codes.data_ptr(), cs,
+                                    scales.data_ptr(), n, hidden, groups, _ROW_DTYPES[x.dtype], rdt, gdt, eps),
                               _raw_stream(stream, dev))
     if st:
         _call(st)
@@ -792,15 +809,15 @@ def linear(w, x, out, *, w_scale=None, x_scale=None, bias=None, activation=None,
     if kind == K2_F8:
         if w_scale is None or x_scale is None:
             raise ValueError("E4M3 codes need w_scale and x_scale")
-        if w_scale.dtype is not f32 or w_scale.get_device() != dev or w_scale.shape != (n,) or not w_scale.is_contiguous():
+        if w_scale.dtype is not f32 or w_scale.get_device() != dev or w_scale.numel() != n or not w_scale.is_contiguous():
             _need("w_scale", w_scale, f32, (n,), dev)
-        if x_scale.dtype is not f32 or x_scale.get_device() != dev or x_scale.shape != (t,) or not x_scale.is_contiguous():
+        if x_scale.dtype is not f32 or x_scale.get_device() != dev or x_scale.numel() != t or not x_scale.is_contiguous():
             _need("x_scale", x_scale, f32, (t,), dev)
         sw, sx = w_scale.data_ptr(), x_scale.data_ptr()
     elif w_scale is not None or x_scale is not None:
         raise ValueError("scales go with E4M3 codes")
     if bias is not None:
-        if bias.dtype is not f32 or bias.get_device() != dev or bias.shape != (n,) or not bias.is_contiguous():
+        if bias.dtype is not f32 or bias.get_device() != dev or bias.numel() != n or not bias.is_contiguous():
             _need("bias", bias, f32, (n,), dev)
         b = bias.data_ptr()
     if residual is not None:

@@ -681,30 +681,41 @@ k2_status k2_adjust_logits(const k2_logit_rules* rules, const float* d_logits, i
  * at least the row's length (not read where there is one row).  Why a call was refused:
  * k2_last_error(NULL).
  *
- * k2_quantize_rows: row t of d_x ([tokens][cols], dtype K2_F32, K2_BF16 or K2_F16) becomes
- * d_scales[t] = max|x| / 448 and d_codes[t * codes_stride + c] = E4M3(x / scale), in fp32,
+ * k2_quantize_rows: row t of x ([tokens][cols], x_dtype K2_F32, K2_BF16 or K2_F16) becomes
+ * scales[t] = max|x| / 448 and codes[t * codes_stride + c] = E4M3(x / scale), in fp32,
  * rounded to nearest with ties to even and saturating.  A row whose scale is 0 gets codes
  * 0; one that holds a NaN or an infinity gets the scale NaN and the code NaN (0x7F)
  * throughout, so that it stays visible in what is computed from it, and costs no other row.
- * cols: 1 .. 49152.  d_codes and d_scales may not lie over the input or each other. */
-k2_status k2_quantize_rows(const void* d_x, int32_t dtype, int64_t x_stride, int32_t tokens, int32_t cols,
-                           uint8_t* d_codes, int64_t codes_stride, float* d_scales, void* stream);
-
-/* The same of a normalised sum (the two norms of a decoder layer): per row
+ * residual, residual_out and gain are NULL; groups, eps and their dtypes are not read.
+ *
+ * k2_norm_quantize: the same of a normalised sum (the two norms of a decoder layer).  Per row
  *   h = x + residual (fp32); residual_out = h, rounded to nearest
  *   y = h / sqrt(mean over its group of h^2 + eps) * gain
  *   codes and scale of y as above.
- * `groups` divides hidden into equal contiguous parts (GroupedRMSNorm); the gain is over all
- * of hidden.  The norm is of h before it is rounded to residual_dtype.  Sums are held in
- * fp32, and do not overflow for any finite row.  d_residual NULL (with d_residual_out NULL):
- * h = x.  d_residual_out may be d_residual itself with the same stride, no other buffers may
- * meet.  x, residual and gain are each K2_F32, K2_BF16 or K2_F16.  eps: at least 2^-126.
- * hidden: 1 .. 49152. */
-k2_status k2_norm_quantize(const void* d_x, int32_t x_dtype, int64_t x_stride, const void* d_residual,
-                           int64_t residual_stride, void* d_residual_out, int64_t residual_out_stride,
-                           int32_t residual_dtype, const void* d_gain, int32_t gain_dtype, int32_t tokens,
-                           int32_t hidden, int32_t groups, float eps, uint8_t* d_codes, int64_t codes_stride,
-                           float* d_scales, void* stream);
+ * `groups` divides cols into equal contiguous parts (GroupedRMSNorm); the gain is over all
+ * of cols.  The norm is of h before it is rounded to residual_dtype.  Sums are held in
+ * fp32, and do not overflow for any finite row.  residual NULL (with residual_out NULL):
+ * h = x.  x, residual and gain are each K2_F32, K2_BF16 or K2_F16.  eps: at least 2^-126.
+ *
+ * cols: 1 .. 49152.  No output may lie over an input or another output, but residual_out may
+ * be residual itself with the same stride. */
+typedef struct {
+  const void* x;
+  int64_t x_stride;
+  const void* residual; /* nullable */
+  int64_t residual_stride;
+  void* residual_out;
+  int64_t residual_out_stride;
+  const void* gain;
+  uint8_t* codes;
+  int64_t codes_stride;
+  float* scales;
+  int32_t tokens, cols, groups;
+  int32_t x_dtype, residual_dtype, gain_dtype;
+  float eps;
+} k2_row_args;
+k2_status k2_quantize_rows(const k2_row_args* args, void* stream);
+k2_status k2_norm_quantize(const k2_row_args* args, void* stream);
 
 /* out = act(w_scale * x_scale * (x . w^T) + bias) + residual, on the tensor cores:
  *   w [out_features][in_features], x [tokens][in_features], both of `dtype`: K2_F8 (E4M3

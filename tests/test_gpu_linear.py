@@ -313,6 +313,45 @@ def test_a_nan_costs_what_it_enters(k2, t):
     assert (call(k2, w, x, "f32", 260, **kw)[at] == 0).all()
 
 
+@pytest.mark.parametrize("t,n", [(1 << 22, 1), (1 << 22, 130), (65535 * 64 + 1, 3), (70000, 700), (1, 300000), (65, 300000), (40, 1)])
+def test_the_most_tokens_and_features(k2, t, n):
+    gen = torch.Generator().manual_seed(t + n)
+    w, x = small_numbers(gen, n, 24, "bf16", 8), small_numbers(gen, 1000, 24, "bf16", 8).repeat(-(-t // 1000), 1)[:t]
+    out = torch.zeros(t, n, dtype=torch.float16, device="cuda")
+    k2.linear(w, x, out)
+    want = (x[:1000].float() @ w.float().T).half()  # whole numbers up to 384
+    for lo in range(0, t, 1000 * 64):
+        got = out[lo:lo + 64000]
+        assert torch.equal(got, want.repeat(64, 1)[:got.shape[0]])
+
+
+def test_rows_further_apart_than_32_bits_count(k2):
+    """300 rows 8 Mi elements apart: offsets beyond 2^31."""
+    far, t, n, k = 1 << 23, 300, 136, 160
+    gen = torch.Generator().manual_seed(15)
+    for kind, tokens in (("bf16", t), ("f8", t), ("bf16", 60)):
+        w, x = small_numbers(gen, n, k, kind, 16), small_numbers(gen, tokens, k, kind, 16)
+        xf = torch.empty(tokens * far, dtype=torch.uint8, device="cuda").view(x.dtype).as_strided((tokens, k), (far // x.element_size(), 1))
+        xf.copy_(x) if kind != "f8" else xf.view(torch.uint8).copy_(x.view(torch.uint8))
+        of = torch.empty(tokens * far, dtype=torch.float16, device="cuda").as_strided((tokens, n), (far, 1))
+        kw = dict(w_scale=torch.ones(n).cuda(), x_scale=torch.ones(tokens).cuda()) if kind == "f8" else {}
+        k2.linear(w, xf, of, **kw)
+        assert torch.equal(of.float(), x.float() @ w.float().T)
+        of.fill_(1)
+        k2.linear(w, xf, of, residual=of, **kw)
+        assert torch.equal(of.float(), x.float() @ w.float().T + 1)
+    x = rows(gen, t, 640, "bf16")
+    xf = torch.empty(t * far, dtype=torch.bfloat16, device="cuda").as_strided((t, 640), (far, 1))
+    xf.copy_(x)
+    codes = torch.empty(t * far, dtype=torch.uint8, device="cuda").as_strided((t, 640), (far, 1))
+    scales = torch.empty(t, device="cuda")
+    k2.quantize_rows(xf, codes, scales)
+    want, scale = L.encode_rows(host(x))
+    assert (raw(codes) == want).all() and np.array_equal(host(scales), scale)
+    k2.norm_quantize(x, torch.ones(640).cuda(), codes, scales, residual=xf)
+    check_norm(k2, x, torch.ones(640).cuda(), x, got=(codes, scales, xf))
+
+
 @pytest.mark.parametrize("t,n,k", [(1, 2560, 10240), (7, 300, 4096), (64, 2560, 2560), (130, 1664, 640), (700, 2560, 640)])
 def test_calls_repeat_bit_for_bit(k2, t, n, k):
     x, w, kw = operands(torch.Generator().manual_seed(13), t, n, k, "f8")
@@ -438,3 +477,68 @@ def test_two_streams_at_once(k2):
     torch.cuda.synchronize()
     for m, w in zip(ms, want):
         assert torch.equal(m.mid, w)
+
+
+@pytest.mark.parametrize("captured", [False, True])
+@pytest.mark.parametrize("t", [5, 300])
+def test_inputs_from_other_streams_copies_and_kernels(k2, t, captured):
+    """The kernels start before the one ahead of them on the stream has ended; what they read may come from it, from a copy, a
+    fill, or another stream that was joined, each of them slow."""
+    gen = torch.Generator().manual_seed(60 + t)
+    m = Half(k2, t)
+    big = torch.randn(4096, 4096, device="cuda")
+    sources = [(rows(gen, t, 640, "f32"), rows(gen, t, 640, "f32")) for _ in range(2)]
+    pinned = [(x.cpu().pin_memory(), r.cpu().pin_memory()) for x, r in sources]
+    side = torch.cuda.Stream()
+
+    def slow():
+        for _ in range(6):
+            torch.mm(big, big)
+
+    def passes(i, how):
+        here = torch.cuda.current_stream()
+        if how == "side":
+            side.wait_stream(here)
+            with torch.cuda.stream(side):
+                slow()
+                m.x.copy_(sources[i][0])
+                m.stream.copy_(sources[i][1])
+            here.wait_stream(side)
+        elif how == "kernel":
+            slow()
+            m.x.copy_(sources[i][0])
+            torch.add(sources[i][1], 0, out=m.stream)
+        elif how == "copy":
+            slow()
+            m.x.copy_(pinned[i][0], non_blocking=True)
+            m.stream.copy_(pinned[i][1], non_blocking=True)
+        else:  # a fill right ahead
+            m.x.copy_(sources[i][0])
+            m.stream.copy_(sources[i][1])
+            slow()
+            m.stream.zero_()
+        return m.run(here)
+
+    want = {}
+    for how in ("side", "kernel", "copy", "fill"):
+        for i in range(2):
+            m.x.copy_(sources[i][0])
+            m.stream.copy_(sources[i][1]) if how != "fill" else m.stream.zero_()
+            torch.cuda.synchronize()
+            want[how, i] = m.run().clone()
+    work = torch.cuda.Stream()
+    work.wait_stream(torch.cuda.current_stream())
+    for how in ("side", "kernel", "copy", "fill"):
+        for i in (0, 1, 0):
+            if captured:
+                graph = torch.cuda.CUDAGraph()
+                with torch.cuda.graph(graph, stream=work):
+                    passes(i, how)
+                m.x.fill_(7)
+                m.stream.fill_(7)
+                graph.replay()
+            else:
+                with torch.cuda.stream(work):
+                    passes(i, how)
+            torch.cuda.synchronize()
+            assert torch.equal(m.mid, want[how, i]), how

@@ -1,5 +1,7 @@
 """Host-side checks of activations in 8 bits and of the matrix product: what the C calls refuse before they touch a GPU, and
 pins of their oracle (oracle/k2_linear.py).  No GPU is needed."""
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -21,17 +23,23 @@ X, C8, SC, R, RO, G, W, O = (0x1000000 * i for i in range(1, 9))
 
 
 def quantize(k2, **kw):
-    d = dict(x=X, dtype=k2.K2_BF16, xs=64, t=4, n=64, c=C8, cs=64, s=SC)
+    d = dict(x=X, x_dtype=k2.K2_BF16, x_stride=64, tokens=4, cols=64, codes=C8, codes_stride=64, scales=SC)
     d.update(kw)
-    return k2.LIB.k2_quantize_rows(d["x"], d["dtype"], d["xs"], d["t"], d["n"], d["c"], d["cs"], d["s"], None)
+    a = k2.RowArgs(**d)
+    return k2.LIB.k2_quantize_rows(ctypes.addressof(a), None)
 
 
 @pytest.mark.parametrize("kw,why", [
-    (dict(x=None), "ARG"), (dict(c=None), "ARG"), (dict(s=None), "ARG"), (dict(dtype=3), "UNSUPPORTED"), (dict(dtype=9), "UNSUPPORTED"),
-    (dict(t=-1), "SHAPE"), (dict(n=0), "SHAPE"), (dict(n=49153, xs=49153, cs=49153), "SHAPE"), (dict(t=2 ** 30 + 1), "SHAPE"),
-    (dict(xs=63), "ARG"), (dict(cs=63), "ARG"), (dict(xs=-64), "ARG"), (dict(xs=2 ** 62), "ARG"), (dict(x=X + 1), "ARG"),
-    (dict(s=SC + 2), "ARG"), (dict(c=X), "ARG"), (dict(c=X + 200), "ARG"), (dict(s=X + 64), "ARG"), (dict(s=C8 + 128), "ARG"),
-    (dict(t=0), None), (dict(t=0, x=None, c=None, s=None), None)])
+    (dict(x=None), "ARG"), (dict(codes=None), "ARG"), (dict(scales=None), "ARG"), (dict(x_dtype=3), "UNSUPPORTED"),
+    (dict(x_dtype=9), "UNSUPPORTED"),
+    (dict(tokens=-1), "SHAPE"), (dict(cols=0), "SHAPE"), (dict(cols=49153, x_stride=49153, codes_stride=49153), "SHAPE"),
+    (dict(tokens=2 ** 30 + 1), "SHAPE"),
+    (dict(x_stride=63), "ARG"), (dict(codes_stride=63), "ARG"), (dict(x_stride=-64), "ARG"), (dict(x_stride=2 ** 62), "ARG"),
+    (dict(x=X + 1), "ARG"),
+    (dict(scales=SC + 2), "ARG"), (dict(codes=X), "ARG"), (dict(codes=X + 200), "ARG"), (dict(scales=X + 64), "ARG"),
+    (dict(scales=C8 + 128), "ARG"),
+    (dict(residual=R), "ARG"), (dict(gain=G), "ARG"), (dict(tokens=0), None),
+    (dict(tokens=0, x=None, codes=None, scales=None), None)])
 def test_rows_that_are_refused(k2, kw, why):
     assert quantize(k2, **kw) == (k2.K2_OK if why is None else getattr(k2, "K2_ERR_" + why))
     if why:
@@ -39,19 +47,25 @@ def test_rows_that_are_refused(k2, kw, why):
 
 
 def norm(k2, **kw):
-    d = dict(x=X, dtype=k2.K2_F32, xs=64, r=R, rs=64, ro=RO, ros=64, rdt=k2.K2_BF16, g=G, gdt=k2.K2_BF16, t=4, n=64, groups=2, eps=1e-6,
-             c=C8, cs=64, s=SC)
+    d = dict(x=X, x_dtype=k2.K2_F32, x_stride=64, residual=R, residual_stride=64, residual_out=RO, residual_out_stride=64,
+             residual_dtype=k2.K2_BF16, gain=G, gain_dtype=k2.K2_BF16, tokens=4, cols=64, groups=2, eps=1e-6, codes=C8, codes_stride=64,
+             scales=SC)
     d.update(kw)
-    return k2.LIB.k2_norm_quantize(d["x"], d["dtype"], d["xs"], d["r"], d["rs"], d["ro"], d["ros"], d["rdt"], d["g"], d["gdt"], d["t"],
-                                   d["n"], d["groups"], d["eps"], d["c"], d["cs"], d["s"], None)
+    a = k2.RowArgs(**d)
+    return k2.LIB.k2_norm_quantize(ctypes.addressof(a), None)
 
 
 @pytest.mark.parametrize("kw,why", [
-    (dict(x=None), "ARG"), (dict(g=None), "ARG"), (dict(r=None), "ARG"), (dict(ro=None), "ARG"), (dict(rdt=4), "UNSUPPORTED"),
-    (dict(gdt=3), "UNSUPPORTED"), (dict(groups=0), "SHAPE"), (dict(groups=3), "SHAPE"), (dict(eps=0.0), "ARG"), (dict(eps=-1e-6), "ARG"),
-    (dict(eps=float("nan")), "ARG"), (dict(eps=float("inf")), "ARG"), (dict(rs=63), "ARG"), (dict(ros=63), "ARG"), (dict(r=R + 1), "ARG"),
-    (dict(g=G + 1), "ARG"), (dict(ro=R + 128), "ARG"), (dict(ro=R, ros=128), "ARG"), (dict(ro=X), "ARG"), (dict(c=R), "ARG"),
-    (dict(c=G), "ARG"), (dict(ro=G), "ARG"), (dict(s=RO + 4), "ARG"), (dict(s=R), "ARG"), (dict(ro=C8 + 64), "ARG"), (dict(t=0), None)])
+    (dict(x=None), "ARG"), (dict(gain=None), "ARG"), (dict(residual=None), "ARG"), (dict(residual_out=None), "ARG"),
+    (dict(residual_dtype=4), "UNSUPPORTED"),
+    (dict(gain_dtype=3), "UNSUPPORTED"), (dict(groups=0), "SHAPE"), (dict(groups=3), "SHAPE"), (dict(eps=0.0), "ARG"),
+    (dict(eps=-1e-6), "ARG"),
+    (dict(eps=float("nan")), "ARG"), (dict(eps=float("inf")), "ARG"), (dict(residual_stride=63), "ARG"),
+    (dict(residual_out_stride=63), "ARG"), (dict(residual=R + 1), "ARG"),
+    (dict(gain=G + 1), "ARG"), (dict(residual_out=R + 128), "ARG"), (dict(residual_out=R, residual_out_stride=128), "ARG"),
+    (dict(residual_out=X), "ARG"), (dict(codes=R), "ARG"),
+    (dict(codes=G), "ARG"), (dict(residual_out=G), "ARG"), (dict(scales=RO + 4), "ARG"), (dict(scales=R), "ARG"),
+    (dict(residual_out=C8 + 64), "ARG"), (dict(tokens=0), None)])
 def test_norms_that_are_refused(k2, kw, why):
     assert norm(k2, **kw) == (k2.K2_OK if why is None else getattr(k2, "K2_ERR_" + why))
 
@@ -60,7 +74,6 @@ def linear(k2, **kw):
     d = dict(w=W, w_stride=64, w_scale=G, x=X, x_stride=64, x_scale=SC, out=O, out_stride=32, tokens=4, out_features=32, in_features=64,
              dtype=k2.K2_F8, out_dtype=k2.K2_F32, activation=0)
     d.update(kw)
-    import ctypes
     a = k2.LinearArgs(**d)
     return k2.LIB.k2_linear(ctypes.addressof(a), None)
 
@@ -82,6 +95,8 @@ def test_products_that_are_refused(k2, kw, why):
 
 
 def test_null_arguments_are_refused(k2):
+    assert k2.LIB.k2_quantize_rows(None, None) == k2.K2_ERR_ARG
+    assert k2.LIB.k2_norm_quantize(None, None) == k2.K2_ERR_ARG
     assert k2.LIB.k2_linear(None, None) == k2.K2_ERR_ARG
 
 
