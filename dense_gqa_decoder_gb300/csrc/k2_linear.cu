@@ -153,36 +153,30 @@ __device__ __forceinline__ void finish_columns(const LinearArgs& a, const uint32
     }
   }
 }
-// What follows the sums of one token, of four neighbouring rows n .. n + 3 of the matrix.
+// The residual of what four neighbouring rows n .. n + 3 of the matrix give token t.
+template <typename OT, int ACT>
+__device__ __forceinline__ void residual_four(const LinearArgs& a, long long t, int n, float (&r)[4]) {
+  constexpr int kPer = ACT == kPairsOfRows ? 2 : 1, kOut = 4 / kPer;  // rows of an output, outputs
+  const OT* from = static_cast<const OT*>(a.residual) + t * a.residual_stride + n / kPer;
+#pragma unroll
+  for (int j = 0; j < kOut; ++j) r[j] = a.residual != nullptr && n + kPer * j < a.rows ? to_f32(from[j]) : 0.f;
+}
+// What follows the sums of these.
 template <typename OT, int ACT>
 __device__ __forceinline__ void finish_four(const LinearArgs& a, long long t, int n, float4 z4, float xs, const float (&ws)[4],
-                                            const float (&bias)[4]) {
+                                            const float (&bias)[4], const float (&r)[4]) {
+  constexpr int kPer = ACT == kPairsOfRows ? 2 : 1, kOut = 4 / kPer;
   float z[4] = {z4.x, z4.y, z4.z, z4.w};
 #pragma unroll
   for (int j = 0; j < 4; ++j) z[j] = fmaf(z[j], ws[j] * xs, bias[j]);
-  if (ACT == kPairsOfRows) {
-    OT* out = static_cast<OT*>(a.out) + t * a.out_stride + (n >> 1);
-    const OT* res = static_cast<const OT*>(a.residual) + t * a.residual_stride + (n >> 1);
+  OT* out = static_cast<OT*>(a.out) + t * a.out_stride + n / kPer;
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      if (n + 2 * j >= a.rows) return;
-      float y = __fdividef(z[2 * j], 1.0f + __expf(-z[2 * j])) * z[2 * j + 1];
-      if (a.residual != nullptr) y += to_f32(res[j]);
-      out[j] = from_f32<OT>(y);
-    }
-    return;
-  }
-  OT* out = static_cast<OT*>(a.out) + t * a.out_stride + n;
-  const OT* res = static_cast<const OT*>(a.residual) + t * a.residual_stride + n;
-  float r[4] = {0.f, 0.f, 0.f, 0.f};
-  if (a.residual != nullptr) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) r[j] = n + j < a.rows ? to_f32(res[j]) : 0.f;
-  }
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const float y = ACT == kOther ? activate(z[j], a.act) : z[j];
-    if (n + j < a.rows) out[j] = from_f32<OT>(a.residual != nullptr ? y + r[j] : y);
+  for (int j = 0; j < kOut; ++j) {
+    float y = ACT == kPairsOfRows ? __fdividef(z[2 * j % 4], 1.0f + __expf(-z[2 * j % 4])) * z[(2 * j + 1) % 4]
+              : ACT == kOther     ? activate(z[j], a.act)
+                                  : z[j];
+    if (a.residual != nullptr) y += r[j];
+    if (n + kPer * j < a.rows) out[j] = from_f32<OT>(y);
   }
 }
 
@@ -304,6 +298,15 @@ __global__ void __launch_bounds__(128) linear_few_kernel(const __grid_constant__
     ws[j] = a.w_scale != nullptr && there ? __ldg(a.w_scale + n + j) : 1.f;
     bias[j] = a.bias != nullptr && there ? __ldg(a.bias + n + j) : 0.f;
   }
+  constexpr int kEarly = 4;  // residuals of a warp's first tokens, loaded ahead of the sums
+  float early[kEarly][4];
+  if (split > 1) {
+#pragma unroll
+    for (int q = 0; q < kEarly; ++q) {
+      const int j = rank + (warp + 4 * q) * split;
+      if (j < tokens) residual_four<OT, ACT>(a, t0 + j, n, early[q]);
+    }
+  }
   if (tid >= 64) xs[tid - 64] = a.x_scale != nullptr && tid - 64 < tokens ? __ldg(a.x_scale + t0 + tid - 64) : 1.f;
   if (split > 1) {
     __syncwarp();
@@ -343,18 +346,27 @@ __global__ void __launch_bounds__(128) linear_few_kernel(const __grid_constant__
     __syncwarp();
     cluster_arrive();
     cluster_wait();
-    for (int slot = warp; rank + slot * split < tokens; slot += 4) {
-      const int j = rank + slot * split;
+    auto join = [&](int slot, const float (&r)[4]) {
       const float4* from = reinterpret_cast<const float4*>(part + slot * kRows) + lane;
       float4 z = from[0];
 #pragma unroll
-      for (int r = 1; r < kMaxSplit; ++r) {
-        if (r < split) {
-          const float4 p = from[r * slots * (kRows / 4)];
+      for (int i = 1; i < kMaxSplit; ++i) {
+        if (i < split) {
+          const float4 p = from[i * slots * (kRows / 4)];
           z.x += p.x, z.y += p.y, z.z += p.z, z.w += p.w;
         }
       }
-      finish_four<OT, ACT>(a, t0 + j, n, z, xs[j], ws, bias);
+      const int j = rank + slot * split;
+      finish_four<OT, ACT>(a, t0 + j, n, z, xs[j], ws, bias, r);
+    };
+#pragma unroll
+    for (int q = 0; q < kEarly; ++q)
+      if (rank + (warp + 4 * q) * split < tokens) join(warp + 4 * q, early[q]);
+#pragma unroll 1
+    for (int slot = warp + 4 * kEarly; rank + slot * split < tokens; slot += 4) {
+      float r[4];
+      residual_four<OT, ACT>(a, t0 + rank + slot * split, n, r);
+      join(slot, r);
     }
   }
   tc_before();
