@@ -89,6 +89,13 @@ __device__ __forceinline__ float activate(float z, int act) {
   return z;
 }
 
+// silu(g) u: exponential and reciprocal to two or three steps of fp32
+__device__ __forceinline__ float swiglu(float g, float u) {
+  float r;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(1.0f + __expf(-g)));
+  return g * r * u;
+}
+
 template <typename T>
 __device__ __forceinline__ T from_f32(float v);
 template <>
@@ -102,7 +109,8 @@ enum { kPlain, kPairsOfRows, kOther };  // what follows the sums: nothing, SwiGL
 
 constexpr int kColumns = 16;  // columns of the accumulator that a warp has in registers
 
-// Some columns of the accumulator (tokens t ..) of this lane's row n: z = v * (ws * xs) + bias, then the activation, the
+// Some columns of the accumulator (tokens t ..) of this lane's row n: z = (v * ws) * xs + bias (a product of the two scales
+// might leave the normal numbers where the result does not), then the activation, the
 // residual and the stores.  Nothing waits for the column before: the scales are in shared memory, the residual is loaded ahead.
 template <typename OT, int ACT, bool FULL>
 __device__ __forceinline__ void finish_columns(const LinearArgs& a, const uint32_t (&v)[kColumns], const float* xs, int t, int n,
@@ -124,10 +132,10 @@ __device__ __forceinline__ void finish_columns(const LinearArgs& a, const uint32
 #pragma unroll
     for (int j = 0; j < kColumns; j += 2, out += 2 * a.out_stride) {
       const float2 x = *reinterpret_cast<const float2*>(xs + j);
-      const float z0 = fmaf(__uint_as_float(v[j]), ws * x.x, bias), z1 = fmaf(__uint_as_float(v[j + 1]), ws * x.y, bias);
+      const float z0 = fmaf(__uint_as_float(v[j]) * ws, x.x, bias), z1 = fmaf(__uint_as_float(v[j + 1]) * ws, x.y, bias);
       const float other = __shfl_xor_sync(0xffffffffu, odd ? z0 : z1, 1);
       const float g = odd ? other : z0, u = odd ? z1 : other;
-      float y = __fdividef(g, 1.0f + __expf(-g)) * u;
+      float y = swiglu(g, u);
       if (a.residual != nullptr) y += res[j / 2];
       if (row && (FULL || j + mine < most)) *out = from_f32<OT>(y);
     }
@@ -146,7 +154,7 @@ __device__ __forceinline__ void finish_columns(const LinearArgs& a, const uint32
     const float x4[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i, out += a.out_stride) {
-      float y = fmaf(__uint_as_float(v[j + i]), ws * x4[i], bias);
+      float y = fmaf(__uint_as_float(v[j + i]) * ws, x4[i], bias);
       if (ACT == kOther) y = activate(y, a.act);
       if (a.residual != nullptr) y += res[j + i];
       if (row && (FULL || j + i < most)) *out = from_f32<OT>(y);
@@ -168,11 +176,11 @@ __device__ __forceinline__ void finish_four(const LinearArgs& a, long long t, in
   constexpr int kPer = ACT == kPairsOfRows ? 2 : 1, kOut = 4 / kPer;
   float z[4] = {z4.x, z4.y, z4.z, z4.w};
 #pragma unroll
-  for (int j = 0; j < 4; ++j) z[j] = fmaf(z[j], ws[j] * xs, bias[j]);
+  for (int j = 0; j < 4; ++j) z[j] = fmaf(z[j] * ws[j], xs, bias[j]);
   OT* out = static_cast<OT*>(a.out) + t * a.out_stride + n / kPer;
 #pragma unroll
   for (int j = 0; j < kOut; ++j) {
-    float y = ACT == kPairsOfRows ? __fdividef(z[2 * j % 4], 1.0f + __expf(-z[2 * j % 4])) * z[(2 * j + 1) % 4]
+    float y = ACT == kPairsOfRows ? swiglu(z[2 * j % 4], z[(2 * j + 1) % 4])
               : ACT == kOther     ? activate(z[j], a.act)
                                   : z[j];
     if (a.residual != nullptr) y += r[j];

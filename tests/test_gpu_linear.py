@@ -292,6 +292,42 @@ def test_strided_operands(k2, kind):
 
 
 @pytest.mark.parametrize("t", [1, 20, 130, 300])
+@pytest.mark.parametrize("ws,xs", [(1e-22, 1e-20), (1e-30, 1e3), (1e25, 1e-20), (1e-38, 1e-3), (1e15, 1e15), (3e-44, 1e30)])
+def test_scales_whose_product_leaves_the_normal_numbers(k2, t, ws, xs):
+    """What matters is the result, here between 1e-37 and 1e38."""
+    gen = torch.Generator().manual_seed(16)
+    n, k = 140, 96
+    w, x = small_numbers(gen, n, k, "f8", 16), small_numbers(gen, t, k, "f8", 16)
+    sw, sx = torch.full((n,), ws).cuda(), torch.full((t,), xs).cuda()
+    z = (x.double() @ w.double().T)
+    want = z * sw.double()[0] * sx.double()[0]
+    assert want.abs().max() < 3e38
+    got = call(k2, w, x, "f32", n, w_scale=sw, x_scale=sx).double()
+    # two roundings of numbers that are normal, or of the smallest step
+    assert ((got - want).abs() <= want.abs() * 2.0 ** -22 + 2.0 ** -149 * max(1.0, xs)).all()
+
+
+def test_gates_far_below_zero(k2):
+    """silu vanishes slowly against a large factor: gates down to where e^-g overflows."""
+    k = 16
+    gates = torch.arange(-128, 0, dtype=torch.float32)
+    w = torch.zeros(256, k)
+    w[0::2, 0] = gates
+    w[1::2, 1] = 2.0 ** 100
+    x = torch.zeros(3, k)
+    x[:, 0] = x[:, 1] = 1
+    out = torch.zeros(3, 128, device="cuda")
+    k2.linear(w.bfloat16().cuda(), x.bfloat16().cuda(), out, activation="swiglu")
+    g = gates.double()
+    want = g / (1 + torch.exp(-g)) * 2.0 ** 100
+    # e^-g to 2^-23 |g| / ln 2 and two steps; from 88.7 on it is infinite in fp32
+    room = want.abs() * (2.0 ** -23 * (g.abs() * 1.5 + 6))
+    got = out.double().cpu()
+    near = g > -88
+    assert ((got - want).abs() <= room)[:, near].all() and (got[:, g < -89].abs() <= want[g < -89].abs().max()).all()
+
+
+@pytest.mark.parametrize("t", [1, 20, 130, 300])
 def test_a_nan_costs_what_it_enters(k2, t):
     gen = torch.Generator().manual_seed(12)
     x, w, kw = operands(gen, t, 260, 200, "f8")
