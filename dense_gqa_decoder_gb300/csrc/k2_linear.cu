@@ -64,6 +64,23 @@ __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, unsigne
     if (globaltimer() - t0 > limit_ns) return false;
   return globaltimer() - t0 <= limit_ns;
 }
+// The requesting and the issuing warp run their loops as whole warps, and one lane does what has to be done once: so the compiler
+// keeps what those instructions take in uniform registers, where they want it.  (With the whole loop in one thread four MMAs took
+// 231 clocks to issue, 107 to look at a barrier that had completed and 85 to commit, and a K step of few tokens 0.30 us.)
+__device__ __forceinline__ int warp_index() { return __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x) >> 5, 0); }
+__device__ __forceinline__ bool elected() {
+  uint32_t yes;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(yes));
+  return yes != 0;
+}
+// the same answer in all lanes
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, unsigned long long limit_ns) {
+  return __all_sync(0xffffffffu, wait_for(bar, parity, limit_ns));
+}
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
@@ -226,7 +243,7 @@ __global__ void __launch_bounds__(128) linear_few_kernel(const __grid_constant__
   __shared__ __align__(8) uint64_t full[kFewStages], empty[kFewStages], done;
   __shared__ __align__(16) float xs[kFewTokens];
   __shared__ uint32_t tmem_slot;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, split = sh.split;
+  const int tid = threadIdx.x, warp = warp_index(), lane = tid & 31, split = sh.split;
   const int tile = blockIdx.x / split, rank = blockIdx.x - tile * split;
   const int n0 = tile * kRows, t0 = blockIdx.y * sh.tokens, tokens = min(sh.tokens, a.tokens - t0);
   const int k0 = static_cast<int>(static_cast<long long>(sh.steps) * rank / split);
@@ -255,18 +272,21 @@ __global__ void __launch_bounds__(128) linear_few_kernel(const __grid_constant__
   pdl_wait();  // what the call reads and writes may be the previous kernel's
   pdl_trigger();
   bool ok = true;
-  if (tid == 0) {
+  if (warp == 0) {
     int i = 0, s = 0;
     uint32_t ph = 0;  // how often the ring wrapped
     for (; i < nk; ++i) {
-      if (ph > 0 && !wait_for(&empty[s], (ph - 1) & 1u, a.limit_ns)) {
+      if (ph > 0 && !warp_wait(&empty[s], (ph - 1) & 1u, a.limit_ns)) {
         ok = false;
         break;
       }
-      uint8_t* st = smem + s * stage;
-      mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(stage));
-      load_weights(st, &map_w, place, k0 + i, n0, &full[s]);
-      load_2d(st + kRows * kStepBytes, &map_x, (k0 + i) * place.step, t0, &full[s]);
+      if (elected()) {
+        uint8_t* st = smem + s * stage;
+        mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(stage));
+        load_weights(st, &map_w, place, k0 + i, n0, &full[s]);
+        load_2d(st + kRows * kStepBytes, &map_x, (k0 + i) * place.step, t0, &full[s]);
+      }
+      __syncwarp();
       if (++s == sh.stages) s = 0, ++ph;
     }
     // no copy may be on its way when this CTA ends
@@ -274,28 +294,33 @@ __global__ void __launch_bounds__(128) linear_few_kernel(const __grid_constant__
       s = s == 0 ? (--ph, sh.stages - 1) : s - 1;
       mbar_wait(&full[s], ph & 1u);
     }
-  } else if (tid == 32) {
+    __syncwarp();
+  } else if (warp == 1) {
     const uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(sh.tokens >> 3) << 17) | (8u << 24) |  // fp32 sums, M = 128
                            (a.dtype == K2_BF16 ? (1u << 7) | (1u << 10) : 0u);
     const uint64_t ring = smem_desc(smem);
     int s = 0;
     uint32_t ph = 0;
     for (int i = 0; i < nk; ++i) {
-      if (!wait_for(&full[s], ph & 1u, a.limit_ns)) {
+      if (!warp_wait(&full[s], ph & 1u, a.limit_ns)) {
         ok = false;
         break;
       }
       tc_after();
       const uint64_t at = ring + static_cast<uint32_t>(s * (stage >> 4));
+      if (elected()) {
 #pragma unroll
-      for (int j = 0; j < kStepBytes / 32; ++j) {  // descriptors count 16 bytes
-        if (F8) mma_f8(tmem, at + 2 * j, at + (kRows * kStepBytes >> 4) + 2 * j, idesc, (i | j) != 0);
-        else mma(tmem, at + 2 * j, at + (kRows * kStepBytes >> 4) + 2 * j, idesc, (i | j) != 0);
+        for (int j = 0; j < kStepBytes / 32; ++j) {  // descriptors count 16 bytes
+          if (F8) mma_f8(tmem, at + 2 * j, at + (kRows * kStepBytes >> 4) + 2 * j, idesc, (i | j) != 0);
+          else mma(tmem, at + 2 * j, at + (kRows * kStepBytes >> 4) + 2 * j, idesc, (i | j) != 0);
+        }
+        mma_commit(&empty[s]);
       }
-      mma_commit(&empty[s]);
+      __syncwarp();
       if (++s == sh.stages) s = 0, ++ph;
     }
-    mma_commit(&done);
+    if (elected()) mma_commit(&done);
+    __syncwarp();
   }
   // meanwhile: the scales and biases of what this thread finishes, its own row or (split) four neighbouring ones
   const int n = n0 + (split > 1 ? 4 * lane : tid);
@@ -481,7 +506,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   __shared__ __align__(8) uint64_t full[kPairStages], empty[kPairStages], accf[2], acce[2], drain;
   __shared__ __align__(16) float x_scales[kPairFinishers][kPairTokens / 4];
   __shared__ uint32_t tmem_slot;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = warp_index(), lane = tid & 31;
   const int rank = static_cast<int>(cta_rank());
   const int step_bytes = (kRows + sh.tokens / 2) * kStepBytes, stage = kPairSteps * step_bytes;  // multiples of 1024
   const int fills = (sh.steps + kPairSteps - 1) / kPairSteps;  // of a tile
@@ -512,7 +537,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   const uint32_t tmem = tmem_slot;
   pdl_wait();  // what the call reads and writes may be the previous kernel's
   pdl_trigger();
-  if (tid == 0) {
+  if (warp == 0) {
     const int half = sh.tokens / 2;
     int s = 0, filled = 0;
     uint32_t ph = 0;  // how often the ring wrapped
@@ -521,19 +546,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       const int tile = pair + i * pairs, rt = tile / sh.token_tiles;
       const int n0 = rt * 2 * kRows + rank * kRows, t0 = (tile - rt * sh.token_tiles) * sh.tokens + rank * half;
       for (int f = 0, e = 0; f < fills; ++f) {
-        if (ph > 0 && !wait_for(&empty[s], (ph - 1) & 1u, a.limit_ns)) {
+        if (ph > 0 && !warp_wait(&empty[s], (ph - 1) & 1u, a.limit_ns)) {
           ok = false;
           break;
         }
         const int count = min(kPairSteps, sh.steps - f * kPairSteps);
-        if (rank == 0) mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(2 * count * step_bytes));  // of both CTAs
-        uint8_t* st = smem + s * stage;
-        const uint32_t bar = first_cta(&full[s]);
-        for (int q = 0; q < count; ++q, e += place.step, st += step_bytes) {
-          if (place.packed) pair_load_4d(st, &map_w, e & 511, 0, e >> 9, n0 >> 1, bar);
-          else pair_load_4d(st, &map_w, e, n0, 0, 0, bar);
-          pair_load_2d(st + kRows * kStepBytes, &map_x, e, t0, bar);
+        if (elected()) {
+          if (rank == 0) mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(2 * count * step_bytes));  // of both CTAs
+          uint8_t* st = smem + s * stage;
+          const uint32_t bar = first_cta(&full[s]);
+#pragma unroll
+          for (int q = 0; q < kPairSteps; ++q) {
+            if (q >= count) break;
+            const int at = e + q * place.step;
+            if (place.packed) pair_load_4d(st + q * step_bytes, &map_w, at & 511, 0, at >> 9, n0 >> 1, bar);
+            else pair_load_4d(st + q * step_bytes, &map_w, at, n0, 0, 0, bar);
+            pair_load_2d(st + q * step_bytes + kRows * kStepBytes, &map_x, at, t0, bar);
+          }
         }
+        __syncwarp();
+        e += kPairSteps * place.step;
         filled = min(filled + 1, sh.stages);
         if (++s == sh.stages) s = 0, ++ph;
       }
@@ -544,8 +576,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       s = s == 0 ? (--ph, sh.stages - 1) : s - 1;
       if (!mbar_wait(&empty[s], ph & 1u)) break;
     }
-    if (!ok && a.flags != nullptr) atomicOr(a.flags, a.bit);
-  } else if (tid == 32 && rank == 0) {
+    if (!ok && lane == 0 && a.flags != nullptr) atomicOr(a.flags, a.bit);
+    __syncwarp();
+  } else if (warp == 1 && rank == 0) {
     const uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(sh.tokens >> 3) << 17) | (16u << 24) |
                            (a.dtype == K2_BF16 ? (1u << 7) | (1u << 10) : 0u);
     const uint64_t ring = smem_desc(smem);
@@ -554,35 +587,41 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     bool ok = true;
     for (int i = 0; i < mine && ok; ++i) {
       const int b = i & 1;
-      if (i >= 2 && !wait_for(&acce[b], static_cast<uint32_t>((i >> 1) - 1) & 1u, a.limit_ns)) {
+      if (i >= 2 && !warp_wait(&acce[b], static_cast<uint32_t>((i >> 1) - 1) & 1u, a.limit_ns)) {
         ok = false;
         break;
       }
       tc_after();
       const uint32_t acc = tmem + b * kPairTokens;
       for (int f = 0; f < fills; ++f) {
-        if (!wait_for(&full[s], ph & 1u, a.limit_ns)) {
+        if (!warp_wait(&full[s], ph & 1u, a.limit_ns)) {
           ok = false;
           break;
         }
         tc_after();
         const uint64_t ad = ring + static_cast<uint32_t>(s * (stage >> 4));
         const int count = min(kPairSteps, sh.steps - f * kPairSteps);
+        if (elected()) {
 #pragma unroll
-        for (int q = 0; q < kPairSteps; ++q) {
-          if (q >= count) break;
-          const uint64_t at = ad + (q ? step_bytes >> 4 : 0);
+          for (int q = 0; q < kPairSteps; ++q) {
+            if (q >= count) break;
+            const uint64_t at = ad + (q ? step_bytes >> 4 : 0);
 #pragma unroll
-          for (int j = 0; j < kStepBytes / 32; ++j)  // descriptors count 16 bytes
-            pair_mma<F8>(acc, at + 2 * j, at + (kRows * kStepBytes >> 4) + 2 * j, idesc, (f | q | j) != 0);
+            for (int j = 0; j < kStepBytes / 32; ++j)  // descriptors count 16 bytes
+              pair_mma<F8>(acc, at + 2 * j, at + (kRows * kStepBytes >> 4) + 2 * j, idesc, (f | q | j) != 0);
+          }
+          pair_commit(&empty[s]);
+          if (f == fills - 1) pair_commit(&accf[b]);
         }
-        pair_commit(&empty[s]);
+        __syncwarp();
         if (++s == sh.stages) s = 0, ++ph;
       }
-      if (ok) pair_commit(&accf[b]);
     }
+    if (elected())
     asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(&drain)) : "memory");
-    if ((!mbar_wait(&drain, 0) || !ok) && a.flags != nullptr) atomicOr(a.flags, a.bit);
+    __syncwarp();
+    if ((!mbar_wait(&drain, 0) || !ok) && lane == 0 && a.flags != nullptr) atomicOr(a.flags, a.bit);
+    __syncwarp();
   } else if (warp >= 2) {
     const int group = warp & 3, columns = sh.tokens / 4, c0 = ((warp - 2) >> 2) * columns;
     float* xs = x_scales[warp - 2];
