@@ -272,7 +272,7 @@ __global__ void __launch_bounds__(128) linear_few_kernel(const __grid_constant__
   pdl_wait();  // what the call reads and writes may be the previous kernel's
   pdl_trigger();
   bool ok = true;
-  if (warp == 0) {
+  if (warp == 0 || warp == 2) {  // the weights, the tokens: a request takes some 125 clocks to issue
     int i = 0, s = 0;
     uint32_t ph = 0;  // how often the ring wrapped
     for (; i < nk; ++i) {
@@ -282,9 +282,12 @@ __global__ void __launch_bounds__(128) linear_few_kernel(const __grid_constant__
       }
       if (elected()) {
         uint8_t* st = smem + s * stage;
-        mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(stage));
-        load_weights(st, &map_w, place, k0 + i, n0, &full[s]);
-        load_2d(st + kRows * kStepBytes, &map_x, (k0 + i) * place.step, t0, &full[s]);
+        if (warp == 0) {
+          mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(stage));
+          load_weights(st, &map_w, place, k0 + i, n0, &full[s]);
+        } else {
+          load_2d(st + kRows * kStepBytes, &map_x, (k0 + i) * place.step, t0, &full[s]);
+        }
       }
       __syncwarp();
       if (++s == sh.stages) s = 0, ++ph;
@@ -412,12 +415,12 @@ __global__ void __launch_bounds__(128) linear_few_kernel(const __grid_constant__
 // A pair of CTAs (the two SMs of a TPC) works on tiles of 256 weight rows x up to 256 tokens with one MMA over both SMs
 // (cta_group::2): each CTA holds its own 128 rows and half of the tokens, so that an SM takes in 32 KB for 128 x 256 x 128
 // products of E4M3 codes (a CTA by itself would take in 48 KB).  Persistent, roles as warps:
-//   warp 0      requests the stages of its CTA (completion is counted by the first CTA's barriers)
+//   warps 0, 2  request the weights and the tokens of their CTA's stages (completion is counted by the first CTA's barriers)
 //   warp 1      of the first CTA issues the MMAs, into one of two accumulators of 256 tensor-memory columns
-//   warps 2-17  read the other accumulator and finish its tile; a warp's lanes are 32 neighbouring outputs of a token
-constexpr int kPairTokens = 256, kPairStages = 8, kPairSteps = 2, kPairRing = 192 * 1024;
+//   warps 3-18  read the other accumulator and finish its tile; a warp's lanes are 32 neighbouring outputs of a token
+constexpr int kPairTokens = 256, kPairStages = 8, kPairRing = 192 * 1024;
 constexpr int kPairSmem = kPairRing + 1024;
-constexpr int kPairFinishers = 16, kPairThreads = 32 * (2 + kPairFinishers);
+constexpr int kPairOthers = 3, kPairFinishers = 16, kPairThreads = 32 * (kPairOthers + kPairFinishers);
 
 __device__ __forceinline__ uint32_t cta_rank() {
   uint32_t r;
@@ -473,6 +476,7 @@ __device__ __forceinline__ void pair_commit(uint64_t* bar) {
 struct PairShape {
   int tokens;      // of a tile: 64 .. 256, a multiple of 64
   int steps;       // of K
+  int group;       // steps of a stage: 1 or 2
   int stages;      // of the ring
   int row_tiles, token_tiles;
 };
@@ -508,8 +512,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   __shared__ uint32_t tmem_slot;
   const int tid = threadIdx.x, warp = warp_index(), lane = tid & 31;
   const int rank = static_cast<int>(cta_rank());
-  const int step_bytes = (kRows + sh.tokens / 2) * kStepBytes, stage = kPairSteps * step_bytes;  // multiples of 1024
-  const int fills = (sh.steps + kPairSteps - 1) / kPairSteps;  // of a tile
+  const int step_bytes = (kRows + sh.tokens / 2) * kStepBytes, stage = sh.group * step_bytes;  // multiples of 1024
+  const int fills = (sh.steps + sh.group - 1) / sh.group;  // of a tile
   const int tiles = sh.row_tiles * sh.token_tiles, pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   const int mine = pair < tiles ? (tiles - 1 - pair) / pairs + 1 : 0;
   if (tid == 0) {
@@ -537,7 +541,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   const uint32_t tmem = tmem_slot;
   pdl_wait();  // what the call reads and writes may be the previous kernel's
   pdl_trigger();
-  if (warp == 0) {
+  if (warp == 0 || warp == 2) {
     const int half = sh.tokens / 2;
     int s = 0, filled = 0;
     uint32_t ph = 0;  // how often the ring wrapped
@@ -550,22 +554,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           ok = false;
           break;
         }
-        const int count = min(kPairSteps, sh.steps - f * kPairSteps);
+        const int count = min(sh.group, sh.steps - f * sh.group);
         if (elected()) {
-          if (rank == 0) mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(2 * count * step_bytes));  // of both CTAs
+          if (warp == 0 && rank == 0) mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(2 * count * step_bytes));  // of both CTAs
           uint8_t* st = smem + s * stage;
           const uint32_t bar = first_cta(&full[s]);
 #pragma unroll
-          for (int q = 0; q < kPairSteps; ++q) {
+          for (int q = 0; q < 2; ++q) {
             if (q >= count) break;
             const int at = e + q * place.step;
-            if (place.packed) pair_load_4d(st + q * step_bytes, &map_w, at & 511, 0, at >> 9, n0 >> 1, bar);
+            if (warp == 2) pair_load_2d(st + q * step_bytes + kRows * kStepBytes, &map_x, at, t0, bar);
+            else if (place.packed) pair_load_4d(st + q * step_bytes, &map_w, at & 511, 0, at >> 9, n0 >> 1, bar);
             else pair_load_4d(st + q * step_bytes, &map_w, at, n0, 0, 0, bar);
-            pair_load_2d(st + q * step_bytes + kRows * kStepBytes, &map_x, at, t0, bar);
           }
         }
         __syncwarp();
-        e += kPairSteps * place.step;
+        e += sh.group * place.step;
         filled = min(filled + 1, sh.stages);
         if (++s == sh.stages) s = 0, ++ph;
       }
@@ -600,10 +604,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         }
         tc_after();
         const uint64_t ad = ring + static_cast<uint32_t>(s * (stage >> 4));
-        const int count = min(kPairSteps, sh.steps - f * kPairSteps);
+        const int count = min(sh.group, sh.steps - f * sh.group);
         if (elected()) {
 #pragma unroll
-          for (int q = 0; q < kPairSteps; ++q) {
+          for (int q = 0; q < 2; ++q) {
             if (q >= count) break;
             const uint64_t at = ad + (q ? step_bytes >> 4 : 0);
 #pragma unroll
@@ -622,9 +626,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     __syncwarp();
     if ((!mbar_wait(&drain, 0) || !ok) && lane == 0 && a.flags != nullptr) atomicOr(a.flags, a.bit);
     __syncwarp();
-  } else if (warp >= 2) {
-    const int group = warp & 3, columns = sh.tokens / 4, c0 = ((warp - 2) >> 2) * columns;
-    float* xs = x_scales[warp - 2];
+  } else if (warp >= kPairOthers) {
+    const int group = warp & 3, columns = sh.tokens / 4, c0 = ((warp - kPairOthers) >> 2) * columns;
+    float* xs = x_scales[warp - kPairOthers];
     bool ok = true;
     for (int i = 0; i < mine; ++i) {
       const int b = i & 1, tile = pair + i * pairs, rt = tile / sh.token_tiles;
@@ -783,34 +787,40 @@ k2_status launch_linear(const LinearWeights& w, const void* x, long long x_strid
   }
   const WeightPlace place = {w.packed ? 1 : 0, a.dtype == K2_F8 ? kStepBytes : kStepBytes / 2};
   const int steps = (a.cols + place.step - 1) / place.step;
-  // Few tokens per tile and K split over CTAs, or wide tiles on pairs of SMs: the cheaper by what was measured, in units of
-  // 0.67 ns.  Few: a K step takes 0.30 us on an SM with one CTA and 0.37 for the two of an SM with two; joining shares of K
-  // takes some 1.3 us, and 2 us more where there are more CTAs than SMs.  Pairs: see below, and 2 us more to start than the
-  // few without a split.  (Down of 128 tokens: few 14.4 us, pairs 20.5; gate and up of 128 15.2 and 17.6; q|k|v of 128 9.0 and
-  // 8.3, of 256 10.5 and 9.1.)  Activations take the few's four finishing warps longer (333 x 640 by 1664 with a GELU 12.0 us,
-  // pairs 7.9).  Up to 64 tokens it is always the few (gate and up of 64 tokens 14.4 us against 16.5).
+  // Few tokens per tile and K split over CTAs, or wide tiles on pairs of SMs: the cheaper by what was measured, in nanoseconds.
+  // Few: a K step takes 270 on an SM by itself and 165 more for each further CTA there; 2600 for the rest, 2200 more to join
+  // shares of K, and 2000 where those are more CTAs than SMs.  Pairs: a step takes 157, 180, 260 or 310 for 64 to 256 tokens a tile;
+  // 3000 for the rest and 8 per column of the last tile.  Neither is done before the weights have been read (6800 bytes a ns, 5400
+  // as the few read them).  Measured as this says within a sixth (us, few and pairs): down of 128 tokens 14.3 and 16.6, of 256
+  // 15.7 and 18.1, of 512 28.6 and 19.9; gate and up of 128 15.0 and 16.3, of 256 24.2 and 18.8; q|k|v of 128 9.8 and 7.0.
+  // Activations take the few's four finishing warps longer.  Up to 64 tokens it is always the few (gate and up of 64 tokens 14.4
+  // us against 16.5).
   FewShape few = {a.tokens <= 16 ? 16 : a.tokens <= 32 ? 32 : 64, steps, 0, 1};
   const long long few_tiles = static_cast<long long>((a.rows + kRows - 1) / kRows) * ((a.tokens + few.tokens - 1) / few.tokens);
+  const long long bytes = static_cast<long long>(a.rows) * a.cols * (a.dtype == K2_F8 ? 1 : 2);
   long long few_cost = 0;
   for (int per_sm = 1; per_sm <= (a.tokens > 64 ? 2 : 1); ++per_sm) {
-    const int split = static_cast<int>(std::max<long long>(1, std::min<long long>({per_sm * sms / few_tiles, kMaxSplit, steps})));
-    const long long mine = (steps + split - 1) / split, load = (few_tiles * split + sms - 1) / sms;
-    const long long cost = std::max(448 * mine, 276 * mine * load) + (split == 1 ? 1000 : load == 1 ? 3000 : 6000);
+    int split = static_cast<int>(std::max<long long>(1, std::min<long long>({per_sm * sms / few_tiles, kMaxSplit, steps})));
+    if (split == 7) split = 6;  // SMs come in twos: 20 tiles of 10240 by 64 tokens 9.3 us with clusters of six, 9.7 of seven
+    const long long mine = (steps + split - 1) / split, ctas = few_tiles * split, load = (ctas + sms - 1) / sms;
+    const long long cost = 2600 + std::max(mine * std::max(270ll, 165 * load), bytes / 5400) +
+                           (split == 1 ? 0 : ctas <= sms ? 2200 : 4200);
     if (few_cost == 0 || cost < few_cost) few.split = split, few_cost = cost;
   }
-  if (a.act != K2_ACT_NONE && a.act != K2_ACT_SWIGLU) few_cost += 94ll * few.tokens;
+  if (a.act != K2_ACT_NONE && a.act != K2_ACT_SWIGLU) few_cost += 60ll * few.tokens;
   if (a.tokens > 64) {
-    // tiles as wide as cost the pair with the most tiles least: a K step of n columns takes as long as n + 224 in the matrix
-    // unit (0.24 us for 128, 0.26 for 192, 0.32 for 256)
-    PairShape sh = {0, steps, 0, (a.rows + 2 * kRows - 1) / (2 * kRows), 0};
+    PairShape sh = {0, steps, 1, 0, (a.rows + 2 * kRows - 1) / (2 * kRows), 0};
     long long best = 0;
     for (int n = kPairTokens; n >= 64; n -= 64) {
       const int tt = (a.tokens + n - 1) / n;
-      const long long cost = (static_cast<long long>(sh.row_tiles) * tt + sms / 2 - 1) / (sms / 2) * (n + 224) * steps;
+      const long long wave = static_cast<long long>(steps) * (n == 256 ? 310 : n == 192 ? 260 : n == 128 ? 180 : 157);
+      const long long waves = (static_cast<long long>(sh.row_tiles) * tt + sms / 2 - 1) / (sms / 2);
+      const long long cost = waves * wave + 3000 + 8 * n + std::max(0ll, bytes / 6800 - wave);
       if (sh.tokens == 0 || cost < best) sh.tokens = n, sh.token_tiles = tt, best = cost;
     }
-    sh.stages = std::min(kPairStages, kPairRing / (kPairSteps * (kRows + sh.tokens / 2) * kStepBytes));
-    if (best + 4000 <= few_cost || a.tokens > 65535 * few.tokens) return launch(w, x, x_stride, a, place, sh, sh.tokens / 2, sms, dev, s);
+    sh.group = sh.tokens <= 128 ? 2 : 1;  // (the issuing warp takes some 300 clocks a stage beside its MMAs)
+    sh.stages = std::min(kPairStages, kPairRing / (sh.group * (kRows + sh.tokens / 2) * kStepBytes));
+    if (best <= few_cost || a.tokens > 65535 * few.tokens) return launch(w, x, x_stride, a, place, sh, sh.tokens / 2, sms, dev, s);
   }
   few.stages = std::min({kFewStages, kFewRing / few_stage(few.tokens), (steps + few.split - 1) / few.split});
   return launch(w, x, x_stride, a, place, few, few.tokens, sms, dev, s);
