@@ -182,29 +182,31 @@ __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
 // rounded reciprocal of s, a quotient q that is close is improved by q + (y - q s) r, whose remainder is exact; from within one
 // step of the quotient this gives the rounded quotient itself (P. Markstein, Computation of elementary functions on the IBM RISC
 // System/6000 processor, IBM J. Res. Dev. 34, 1990), and one improvement of y r leads there.  s is far enough from the ends of
-// fp32 (`plain`) that no remainder of a quotient above 2^-11 is lost; what lies below gets the code 0 anyhow.  (With a division
+// fp32 (`plain`) that no remainder of a quotient above 2^-11 is lost; what lies below gets the code 0 anyhow.  All with the
+// quotients' signs turned, which keeps the sign of a zero, and turned back in the codes.  (With a division
 // per value 8192 x 10240 took 59.5 us.  Two products that bound the quotient, and a division where they give two codes: 49 us,
 // because quotients of bf16 rows lie half way between two codes so often that every third row needed divisions.)
 struct RowScale {
   float s;
-  f32x2 r2, minus_s2;
+  f32x2 s2, minus_r2;
   bool fine, plain;  // all values finite; the codes can be had so
   __device__ __forceinline__ explicit RowScale(unsigned top) {
     fine = top < 0x7F800000u;
     s = fine ? __uint_as_float(top) / kTop : __uint_as_float(0x7FC00000u);
     const float r = __frcp_rn(s);
-    r2 = pk2(r, r);
-    minus_s2 = pk2(-s, -s);
+    s2 = pk2(s, s);
+    minus_r2 = pk2(-r, -r);
     plain = s >= 0x1p-80f && s <= 0x1p110f;  // (not where it is NaN)
   }
-  __device__ __forceinline__ f32x2 quotients(f32x2 y) const {
-    f32x2 q = mul2(y, r2);
-    q = fma2(fma2(q, minus_s2, y), r2, q);
-    return fma2(fma2(q, minus_s2, y), r2, q);
+  __device__ __forceinline__ f32x2 minus_quotients(f32x2 y) const {
+    f32x2 q = mul2(y, minus_r2);
+    q = fma2(fma2(q, s2, y), minus_r2, q);
+    return fma2(fma2(q, s2, y), minus_r2, q);
   }
   __device__ __forceinline__ uint2 codes(const f32x2 (&y)[4]) const {
-    const float2 a = two(quotients(y[0])), b = two(quotients(y[1])), c = two(quotients(y[2])), d = two(quotients(y[3]));
-    return make_uint2(codes4(a.x, a.y, b.x, b.y), codes4(c.x, c.y, d.x, d.y));
+    const float2 a = two(minus_quotients(y[0])), b = two(minus_quotients(y[1])), c = two(minus_quotients(y[2])),
+                 d = two(minus_quotients(y[3]));
+    return make_uint2(codes4(a.x, a.y, b.x, b.y) ^ 0x80808080u, codes4(c.x, c.y, d.x, d.y) ^ 0x80808080u);
   }
   __device__ __noinline__ static uint2 divided(const float4 a, const float4 b, float s, bool fine) {
     if (!fine) return make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
@@ -472,7 +474,7 @@ __global__ void __launch_bounds__(256) rows_kernel(RowArgs a) {
         for (int i = tid; i < size; i += 256) ss += (part_of[i] * unit) * (part_of[i] * unit);
         mean = block_sum(ss, part) / static_cast<float>(size) + a.eps * unit * unit;
       }
-      const float r = 1.0f / sqrtf(mean);
+      const float r = __frsqrt_rn(mean);
       for (int i = tid; i < size; i += 256) {
         const float y = part_of[i] * unit * r * load_gain(a.gain, a.gain_dtype, g * size + i);
         part_of[i] = y;

@@ -98,6 +98,16 @@ def test_rows_at_the_ends_of_their_type(k2, n, kind):
     check_codes(k2, x.to(T[kind]).cuda())
 
 
+@pytest.mark.parametrize("kind", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("n", [64, 61])
+def test_zeros_keep_their_sign(k2, n, kind):
+    """Zeros of both signs, and values of both signs that round to zero, beside others."""
+    x = torch.randn(9, n, generator=torch.Generator().manual_seed(n))
+    x[:, 0::4], x[:, 1::4], x[:, 2::8], x[:, 3::8] = 0.0, -0.0, 1e-5, -1e-5
+    x[:, 5] = torch.tensor([1.0, -1.0, 448.0, -3.3, 0.7, 100.0, 5e4, 1e-3, -1.75])
+    check_codes(k2, x.to(T[kind]).cuda())
+
+
 def test_quotients_next_to_the_border_of_two_codes(k2):
     """Rows of values s * B and their neighbours in float32, B half way between two codes: the code is that of the rounded
     quotient, which falls on B, above or below it."""
