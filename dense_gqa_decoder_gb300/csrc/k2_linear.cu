@@ -271,6 +271,26 @@ __global__ void __launch_bounds__(128) linear_few_kernel(const __grid_constant__
   const uint32_t tmem = tmem_slot;
   pdl_wait();  // what the call reads and writes may be the previous kernel's
   pdl_trigger();
+  // on their way meanwhile: scales and biases of what this thread finishes, its own row or (split) four neighbouring ones
+  const int n = n0 + (split > 1 ? 4 * lane : tid);
+  float ws[4], bias[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const bool there = n + j < a.rows && (j == 0 || split > 1);
+    ws[j] = a.w_scale != nullptr && there ? __ldg(a.w_scale + n + j) : 1.f;
+    bias[j] = a.bias != nullptr && there ? __ldg(a.bias + n + j) : 0.f;
+  }
+  constexpr int kEarly = 4;  // residuals of a warp's first tokens, loaded ahead of the sums
+  float early[kEarly][4];
+  if (split > 1) {
+#pragma unroll
+    for (int q = 0; q < kEarly; ++q) {
+      const int j = rank + (warp + 4 * q) * split;
+      if (j < tokens) residual_four<OT, ACT>(a, t0 + j, n, early[q]);
+    }
+  }
+  if (warp == 3)
+    for (int j = lane; j < kFewTokens; j += 32) xs[j] = a.x_scale != nullptr && j < tokens ? __ldg(a.x_scale + t0 + j) : 1.f;
   bool ok = true;
   if (warp == 0 || warp == 2) {  // the weights, the tokens: a request takes some 125 clocks to issue
     int i = 0, s = 0;
@@ -325,25 +345,6 @@ __global__ void __launch_bounds__(128) linear_few_kernel(const __grid_constant__
     if (elected()) mma_commit(&done);
     __syncwarp();
   }
-  // meanwhile: the scales and biases of what this thread finishes, its own row or (split) four neighbouring ones
-  const int n = n0 + (split > 1 ? 4 * lane : tid);
-  float ws[4], bias[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const bool there = n + j < a.rows && (j == 0 || split > 1);
-    ws[j] = a.w_scale != nullptr && there ? __ldg(a.w_scale + n + j) : 1.f;
-    bias[j] = a.bias != nullptr && there ? __ldg(a.bias + n + j) : 0.f;
-  }
-  constexpr int kEarly = 4;  // residuals of a warp's first tokens, loaded ahead of the sums
-  float early[kEarly][4];
-  if (split > 1) {
-#pragma unroll
-    for (int q = 0; q < kEarly; ++q) {
-      const int j = rank + (warp + 4 * q) * split;
-      if (j < tokens) residual_four<OT, ACT>(a, t0 + j, n, early[q]);
-    }
-  }
-  if (tid >= 64) xs[tid - 64] = a.x_scale != nullptr && tid - 64 < tokens ? __ldg(a.x_scale + t0 + tid - 64) : 1.f;
   if (split > 1) {
     __syncwarp();
     cluster_wait();  // the others run
@@ -484,10 +485,8 @@ struct PairShape {
 // A warp's part of a tile: 32 rows (this lane's is n), `columns` of the accumulator from t on, whose scales are at xs.  `free`
 // is the barrier that gives the accumulator back, as soon as the last columns are in registers.
 template <typename OT, int ACT>
-__device__ __forceinline__ void finish_part(const LinearArgs& a, uint32_t acc, const float* xs, int columns, int t, int n, bool ok,
-                                            uint32_t free) {
-  const float ws = !ok ? __uint_as_float(0x7FC00000u) : a.w_scale != nullptr && n < a.rows ? __ldg(a.w_scale + n) : 1.f;
-  const float bias = a.bias != nullptr && n < a.rows ? __ldg(a.bias + n) : 0.f;
+__device__ __forceinline__ void finish_part(const LinearArgs& a, uint32_t acc, const float* xs, int columns, int t, int n, float ws,
+                                            float bias, uint32_t free) {
 #pragma unroll 1
   for (int c = 0; c < columns; c += kColumns) {
     uint32_t v[kColumns];
@@ -636,11 +635,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       __syncwarp();  // the last tile's scales have been read
       for (int c = lane; c < columns; c += 32) xs[c] = a.x_scale != nullptr && t + c < a.tokens ? __ldg(a.x_scale + t + c) : 1.f;
       __syncwarp();
+      const float ws = a.w_scale != nullptr && n < a.rows ? __ldg(a.w_scale + n) : 1.f;
+      const float bias = a.bias != nullptr && n < a.rows ? __ldg(a.bias + n) : 0.f;
       // once a wait has run out the rest of this CTA's tiles is NaN
       if (ok) ok = __all_sync(0xffffffffu, wait_for(&accf[b], static_cast<uint32_t>(i >> 1) & 1u, a.limit_ns));
       tc_after();
       const uint32_t acc = tmem + b * kPairTokens + c0 + (static_cast<uint32_t>(group * 32) << 16), free = first_cta(&acce[b]);
-      finish_part<OT, ACT>(a, acc, xs, columns, t, n, ok, free);
+      finish_part<OT, ACT>(a, acc, xs, columns, t, n, ok ? ws : __uint_as_float(0x7FC00000u), bias, free);
     }
     if (!ok && lane == 0 && a.flags != nullptr) atomicOr(a.flags, a.bit);
   }
