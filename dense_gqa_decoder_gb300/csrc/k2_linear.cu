@@ -6,7 +6,7 @@
 //
 // The weights' 128-row tiles are the first operand (M), the tokens the second (N): few tokens then cost few columns and not 128
 // rows.  Both arrive as K-major rows of 128 bytes by TMA (zeros behind the last row and behind the last value of a row) through
-// a ring of stages; one thread requests, one issues the MMAs.  Two kernels: for few tokens the weights' bytes bound the call
+// a ring of stages; two warps request, one issues the MMAs.  Two kernels: for few tokens the weights' bytes bound the call
 // (linear_few_kernel), for many the tensor cores (linear_pair_kernel).
 #include <cuda.h>
 #include <math.h>
@@ -312,10 +312,11 @@ __global__ void __launch_bounds__(128) linear_few_kernel(const __grid_constant__
       __syncwarp();
       if (++s == sh.stages) s = 0, ++ph;
     }
-    // no copy may be on its way when this CTA ends
+    // no copy may be on its way when this CTA ends (after a wait that ran out this one runs out too, a second during which what
+    // is on its way lands)
     for (int j = min(i, sh.stages); j > 0; --j) {
       s = s == 0 ? (--ph, sh.stages - 1) : s - 1;
-      mbar_wait(&full[s], ph & 1u);
+      if (!mbar_wait(&full[s], ph & 1u)) break;
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -364,6 +365,9 @@ __global__ void __launch_bounds__(128) linear_few_kernel(const __grid_constant__
       if (c + kColumns <= tokens) finish_columns<OT, ACT, true>(a, v, xs + c, t0 + c, n, ws[0], bias[0]);
       else finish_columns<OT, ACT, false>(a, v, xs + c, t0 + c, n, ws[0], bias[0]);
     }
+    tc_before();
+    __syncthreads();  // every warp has read the accumulator
+    if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(kFewTokens) : "memory");
   } else {
     // this thread's row of the sums, token by token, to the CTA that joins them: [rank][token / split][row]
     float* part = reinterpret_cast<float*>(smem + sh.stages * stage);
@@ -380,7 +384,11 @@ __global__ void __launch_bounds__(128) linear_few_kernel(const __grid_constant__
         if (++owner == split) owner = 0, at += kRows * 4;
       }
     }
-    __syncwarp();
+    // Tensor memory is given back before the others are waited for: no CTA holds any while one of its cluster may still be
+    // waiting for its own behind another kernel's, so that kernels on several streams cannot wait for one another in a ring.
+    tc_before();
+    __syncthreads();
+    if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(kFewTokens) : "memory");
     cluster_arrive();
     cluster_wait();
     auto join = [&](int slot, const float (&r)[4]) {
@@ -406,9 +414,6 @@ __global__ void __launch_bounds__(128) linear_few_kernel(const __grid_constant__
       join(slot, r);
     }
   }
-  tc_before();
-  __syncthreads();  // every warp has read the accumulator
-  if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(kFewTokens) : "memory");
 }
 
 // ---- many tokens: pairs of CTAs -------------------------------------------------------------------------------------------
@@ -419,6 +424,8 @@ __global__ void __launch_bounds__(128) linear_few_kernel(const __grid_constant__
 //   warps 0, 2  request the weights and the tokens of their CTA's stages (completion is counted by the first CTA's barriers)
 //   warp 1      of the first CTA issues the MMAs, into one of two accumulators of 256 tensor-memory columns
 //   warps 3-18  read the other accumulator and finish its tile; a warp's lanes are 32 neighbouring outputs of a token
+// (Both SMs' tensor memory is taken at once and whole; what else may hold some there gives it back by itself, and a second
+// pair has no room in shared memory.)
 constexpr int kPairTokens = 256, kPairStages = 8, kPairRing = 192 * 1024;
 constexpr int kPairSmem = kPairRing + 1024;
 constexpr int kPairOthers = 3, kPairFinishers = 16, kPairThreads = 32 * (kPairOthers + kPairFinishers);
@@ -621,7 +628,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       }
     }
     if (elected())
-    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(&drain)) : "memory");
+      asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(&drain)) : "memory");
     __syncwarp();
     if ((!mbar_wait(&drain, 0) || !ok) && lane == 0 && a.flags != nullptr) atomicOr(a.flags, a.bit);
     __syncwarp();
