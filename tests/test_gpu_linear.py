@@ -525,6 +525,36 @@ def test_two_streams_at_once(k2):
         assert torch.equal(m.mid, w)
 
 
+def test_kernels_of_several_streams_share_the_sms(k2):
+    """Clusters of few tokens whose K is short (little shared memory), long ones, and pairs of CTAs, on four streams at once:
+    all of them hold tensor memory, and each ends with the result that it has alone."""
+    cases = []
+    for i, (t, n, k) in enumerate([(9, 2560, 200), (300, 2560, 1000), (16, 6000, 384), (40, 2560, 2560), (1, 5000, 256), (513, 640, 640)]):
+        gen = torch.Generator().manual_seed(900 + i)
+        wq, wqs = L.encode_rows(torch.randn(n, k, generator=gen).numpy())
+        xq, xqs = L.encode_rows(torch.randn(t, k, generator=gen).numpy())
+        pad = (k + 15) // 16 * 16
+        codes = [torch.zeros(len(q), pad, dtype=torch.uint8, device="cuda") for q in (wq, xq)]
+        for c, q in zip(codes, (wq, xq)):
+            c[:, :k] = torch.from_numpy(q).cuda()
+        w, x = (c[:, :k] for c in codes)
+        scales = dict(w_scale=torch.from_numpy(wqs).cuda(), x_scale=torch.from_numpy(xqs).cuda())
+        alone, flags = torch.empty(t, n, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+        k2.linear(w, x, alone, flags=flags, **scales)
+        cases.append((w, x, alone, scales, flags))
+    torch.cuda.synchronize()
+    streams, outs = [torch.cuda.Stream() for _ in range(4)], []
+    for turn in range(40):
+        for i, s in enumerate(streams):
+            w, x, alone, scales, flags = case = cases[(turn * (i + 1) + i) % len(cases)]
+            with torch.cuda.stream(s):
+                out = torch.full_like(alone, -7.0)
+                k2.linear(w, x, out, flags=flags, **scales)
+            outs.append((out, case))
+    torch.cuda.synchronize()
+    assert all(torch.equal(out, alone) and not flags.item() for out, (_, _, alone, _, flags) in outs)
+
+
 @pytest.mark.parametrize("captured", [False, True])
 @pytest.mark.parametrize("t", [5, 300])
 def test_inputs_from_other_streams_copies_and_kernels(k2, t, captured):
