@@ -426,7 +426,7 @@ __global__ void __launch_bounds__(128) linear_few_kernel(const __grid_constant__
 //   warps 3-18  read the other accumulator and finish its tile; a warp's lanes are 32 neighbouring outputs of a token
 // (Both SMs' tensor memory is taken at once and whole; what else may hold some there gives it back by itself, and a second
 // pair has no room in shared memory.)
-constexpr int kPairTokens = 256, kPairStages = 8, kPairRing = 192 * 1024;
+constexpr int kPairTokens = 256, kPairStages = 8, kPairRing = 208 * 1024;  // four stages of two steps of 160 tokens
 constexpr int kPairSmem = kPairRing + 1024;
 constexpr int kPairOthers = 3, kPairFinishers = 16, kPairThreads = 32 * (kPairOthers + kPairFinishers);
 
@@ -482,7 +482,7 @@ __device__ __forceinline__ void pair_commit(uint64_t* bar) {
 }
 
 struct PairShape {
-  int tokens;      // of a tile: 64 .. 256, a multiple of 64
+  int tokens;      // of a tile: 64 .. 256, a multiple of 32
   int steps;       // of K
   int group;       // steps of a stage: 1 or 2
   int stages;      // of the ring
@@ -633,7 +633,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     if ((!mbar_wait(&drain, 0) || !ok) && lane == 0 && a.flags != nullptr) atomicOr(a.flags, a.bit);
     __syncwarp();
   } else if (warp >= kPairOthers) {
-    const int group = warp & 3, columns = sh.tokens / 4, c0 = ((warp - kPairOthers) >> 2) * columns;
+    // 32 of the rows, and a quarter of the columns, in whole passes
+    const int group = warp & 3, quarter = (warp - kPairOthers) >> 2, passes = sh.tokens / kColumns;
+    const int c0 = (quarter * passes >> 2) * kColumns, columns = ((quarter + 1) * passes >> 2) * kColumns - c0;
     float* xs = x_scales[warp - kPairOthers];
     bool ok = true;
     for (int i = 0; i < mine; ++i) {
@@ -797,8 +799,9 @@ k2_status launch_linear(const LinearWeights& w, const void* x, long long x_strid
   const int steps = (a.cols + place.step - 1) / place.step;
   // Few tokens per tile and K split over CTAs, or wide tiles on pairs of SMs: the cheaper by what was measured, in nanoseconds.
   // Few: a K step takes 270 on an SM by itself and 165 more for each further CTA there; 2600 for the rest, 2200 more to join
-  // shares of K, and 2000 where those are more CTAs than SMs.  Pairs: a step takes 157, 180, 260 or 310 for 64 to 256 tokens a tile;
-  // 3000 for the rest and 8 per column of the last tile.  Neither is done before the weights have been read (6800 bytes a ns, 5400
+  // shares of K, and 2000 where those are more CTAs than SMs.  Pairs: a step takes kStepNs for 64, 96 .. 256 tokens a tile;
+  // 3000 for the rest and 8 per column of the last tile.  (Down of 2048 tokens: two waves of 130 tiles of 160, 38 us; of 110 of
+  // 192 tokens 43; of 80 of 256, 51.)  Neither is done before the weights have been read (6800 bytes a ns, 5400
   // as the few read them).  Measured as this says within a sixth (us, few and pairs): down of 128 tokens 14.3 and 16.6, of 256
   // 15.7 and 18.1, of 512 28.6 and 19.9; gate and up of 128 15.0 and 16.3, of 256 24.2 and 18.8; q|k|v of 128 9.8 and 7.0.
   // Activations take the few's four finishing warps longer.  Up to 64 tokens it is always the few (gate and up of 64 tokens 14.4
@@ -817,16 +820,19 @@ k2_status launch_linear(const LinearWeights& w, const void* x, long long x_strid
   }
   if (a.act != K2_ACT_NONE && a.act != K2_ACT_SWIGLU) few_cost += 60ll * few.tokens;
   if (a.tokens > 64) {
+    constexpr int kStepNs[] = {140, 170, 175, 220, 250, 270, 305};
     PairShape sh = {0, steps, 1, 0, (a.rows + 2 * kRows - 1) / (2 * kRows), 0};
     long long best = 0;
-    for (int n = kPairTokens; n >= 64; n -= 64) {
+    for (int n = kPairTokens; n >= 64; n -= 32) {
       const int tt = (a.tokens + n - 1) / n;
-      const long long wave = static_cast<long long>(steps) * (n == 256 ? 310 : n == 192 ? 260 : n == 128 ? 180 : 157);
+      const long long wave = static_cast<long long>(steps) * kStepNs[n / 32 - 2];
       const long long waves = (static_cast<long long>(sh.row_tiles) * tt + sms / 2 - 1) / (sms / 2);
       const long long cost = waves * wave + 3000 + 8 * n + std::max(0ll, bytes / 6800 - wave);
       if (sh.tokens == 0 || cost < best) sh.tokens = n, sh.token_tiles = tt, best = cost;
     }
-    sh.group = sh.tokens <= 128 ? 2 : 1;  // (the issuing warp takes some 300 clocks a stage beside its MMAs)
+    // a stage of one step costs 230 ns whatever the tile, so that narrow tiles' have two (down of 2048 tokens by tiles of 160: 38
+    // and 43 us); of wider tiles only three such stages would fit (tiles of 160 with three: 46)
+    sh.group = sh.tokens <= 160 ? 2 : 1;
     sh.stages = std::min(kPairStages, kPairRing / (sh.group * (kRows + sh.tokens / 2) * kStepBytes));
     if (best <= few_cost || a.tokens > 65535 * few.tokens) return launch(w, x, x_stride, a, place, sh, sh.tokens / 2, sms, dev, s);
   }
