@@ -220,8 +220,9 @@ __device__ __forceinline__ void load_weights(void* dst, const CUtensorMap* m, co
 //
 // A CTA per tile of 128 rows x 16, 32 or 64 tokens.  Where there are fewer tiles than SMs, a cluster of up to eight CTAs splits
 // K: token j's sums go to CTA j % split, each CTA writing its share into that CTA's shared memory, and are added there in the
-// order of K, so that the result does not depend on which CTA came first.  One CTA per SM is enough (q|k|v of one token: 8.6 us
-// with twice as many, whose clusters no longer fit at once, 5.7 with these).
+// order of K, so that the result does not depend on which CTA came first.  One CTA per SM is enough (q|k|v of one token took 8.6
+// us with twice as many, whose clusters no longer fit at once, and 5.7 with these; 4.9 now).  The weights stream at 6.7 TB/s
+// behind some 3.6 us of start, first loads and end (gate and up of 16 tokens, 52 MB: 11.2 us).
 constexpr int kFewTokens = 64, kFewStages = 5, kFewRing = 92 * 1024;  // two CTAs fit an SM
 
 struct FewShape {
@@ -420,7 +421,8 @@ __global__ void __launch_bounds__(128) linear_few_kernel(const __grid_constant__
 //
 // A pair of CTAs (the two SMs of a TPC) works on tiles of 256 weight rows x up to 256 tokens with one MMA over both SMs
 // (cta_group::2): each CTA holds its own 128 rows and half of the tokens, so that an SM takes in 32 KB for 128 x 256 x 128
-// products of E4M3 codes (a CTA by itself would take in 48 KB).  Persistent, roles as warps:
+// products of E4M3 codes (a CTA by itself would take in 48 KB).  Gate and up of 2048 tokens take 66 us (3250 TFLOP/s), 240 by
+// single CTAs; 4096 x 10240 by 2560 in bf16 130 us (1650).  Persistent, roles as warps:
 //   warps 0, 2  request the weights and the tokens of their CTA's stages (completion is counted by the first CTA's barriers)
 //   warp 1      of the first CTA issues the MMAs, into one of two accumulators of 256 tensor-memory columns
 //   warps 3-18  read the other accumulator and finish its tile; a warp's lanes are 32 neighbouring outputs of a token
@@ -803,7 +805,7 @@ k2_status launch_linear(const LinearWeights& w, const void* x, long long x_strid
   // 3000 for the rest and 8 per column of the last tile.  (Down of 2048 tokens: two waves of 130 tiles of 160, 38 us; of 110 of
   // 192 tokens 43; of 80 of 256, 51.)  Neither is done before the weights have been read (6800 bytes a ns, 5400
   // as the few read them).  Measured as this says within a sixth (us, few and pairs): down of 128 tokens 14.3 and 16.6, of 256
-  // 15.7 and 18.1, of 512 28.6 and 19.9; gate and up of 128 15.0 and 16.3, of 256 24.2 and 18.8; q|k|v of 128 9.8 and 7.0.
+  // 15.6 and 15.7, of 512 28.6 and 18.6; gate and up of 128 15.0 and 16.3, of 256 24.2 and 18.4; q|k|v of 128 9.8 and 7.0.
   // Activations take the few's four finishing warps longer.  Up to 64 tokens it is always the few (gate and up of 64 tokens 14.4
   // us against 16.5).
   FewShape few = {a.tokens <= 16 ? 16 : a.tokens <= 32 ? 32 : 64, steps, 0, 1};
