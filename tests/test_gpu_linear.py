@@ -237,6 +237,22 @@ def test_whole_numbers_are_exact(k2, t, n, k, kind):
     assert torch.equal(got, x.float() @ w.float().T)
 
 
+@pytest.mark.parametrize("kind,t,n,k", [
+    ("f8", 70, 700, 300), ("f8", 70, 9730, 1000), ("f8", 333, 9730, 640), ("f8", 431, 6146, 1000), ("f8", 505, 5000, 1500),
+    ("f8", 220, 12002, 1500), ("f8", 250, 12002, 2565), ("bf16", 70, 9730, 640), ("f16", 333, 9730, 300), ("bf16", 150, 9730, 1000),
+    ("f16", 505, 5000, 640), ("bf16", 220, 12002, 640), ("f16", 250, 12002, 1000)])
+def test_every_width_of_tile(k2, kind, t, n, k):
+    """Sizes for which tiles of 64, 96, 128, 160, 192, 224 and 256 tokens are chosen, the last of them not full; out = x . w^T + bias +
+    residual in whole numbers, at most 16 * 2565 + 2000 of them: exact."""
+    gen = torch.Generator().manual_seed(t + n + k)
+    step = 16 if kind == "f8" else 8
+    w, x = small_numbers(gen, n, k, kind, step), small_numbers(gen, t, k, kind, step)
+    kw = dict(w_scale=torch.ones(n).cuda(), x_scale=torch.ones(t).cuda()) if kind == "f8" else {}
+    bias, res = (torch.randint(-1000, 1001, shape, generator=gen).float().cuda() for shape in ((n,), (t, n)))
+    got = call(k2, w, x, "f32", n, pad=3, bias=bias, residual=res, **kw)
+    assert torch.equal(got, x.float() @ w.float().T + bias + res)
+
+
 def check_product(k2, w, x, kind, pad=0, inplace=False, **kw):
     res = kw.get("residual")
     act = kw.get("activation")
