@@ -800,8 +800,9 @@ k2_status launch_linear(const LinearWeights& w, const void* x, long long x_strid
   const WeightPlace place = {w.packed ? 1 : 0, a.dtype == K2_F8 ? kStepBytes : kStepBytes / 2};
   const int steps = (a.cols + place.step - 1) / place.step;
   // Few tokens per tile and K split over CTAs, or wide tiles on pairs of SMs: the cheaper by what was measured, in nanoseconds.
-  // Few: a K step takes 270 on an SM by itself and 165 more for each further CTA there; 2600 for the rest, 2200 more to join
-  // shares of K, and 2000 where those are more CTAs than SMs.  Pairs: a step takes kStepNs for 64, 96 .. 256 tokens a tile;
+  // Few: a K step takes 270 on an SM by itself and 165 more for each further CTA there; 2600 for the rest, again for every three
+  // CTAs that an SM gets (300 tokens of 640 by 20480 in bf16: 17.4 us, pairs 12.9; 2000 by 1664 in E4M3, three each: 6.3 and 7.0),
+  // 2200 more to join shares of K, and 2000 where those are more CTAs than SMs.  Pairs: a step takes kStepNs for 64, 96 .. 256 tokens a tile;
   // 3000 for the rest and 8 per column of the last tile.  (Down of 2048 tokens: two waves of 130 tiles of 160, 38 us; of 110 of
   // 192 tokens 43; of 80 of 256, 51.)  Neither is done before the weights have been read (6800 bytes a ns, 5400
   // as the few read them).  Measured as this says within a sixth (us, few and pairs): down of 128 tokens 14.3 and 16.6, of 256
@@ -816,7 +817,7 @@ k2_status launch_linear(const LinearWeights& w, const void* x, long long x_strid
     int split = static_cast<int>(std::max<long long>(1, std::min<long long>({per_sm * sms / few_tiles, kMaxSplit, steps})));
     if (split == 7) split = 6;  // SMs come in twos: 20 tiles of 10240 by 64 tokens 9.3 us with clusters of six, 9.7 of seven
     const long long mine = (steps + split - 1) / split, ctas = few_tiles * split, load = (ctas + sms - 1) / sms;
-    const long long cost = 2600 + std::max(mine * std::max(270ll, 165 * load), bytes / 5400) +
+    const long long cost = 2600 * ((load + 2) / 3) + std::max(mine * std::max(270ll, 165 * load), bytes / 5400) +
                            (split == 1 ? 0 : ctas <= sms ? 2200 : 4200);
     if (few_cost == 0 || cost < few_cost) few.split = split, few_cost = cost;
   }
