@@ -9,6 +9,7 @@
 // a ring of stages; two warps request, one issues the MMAs.  Two kernels: for few tokens the weights' bytes bound the call
 // (linear_few_kernel), for many the tensor cores (linear_pair_kernel).
 #include <cuda.h>
+#include <limits.h>
 #include <math.h>
 
 #include <algorithm>
@@ -491,19 +492,43 @@ struct PairShape {
   int row_tiles, token_tiles;
 };
 
+// Which of the pair's tiles come is for the issuing warp alone to say, so that all of a tile is right or all of it is NaN: `ends`
+// is the first that does not.  It is told to both CTAs.
+__device__ __forceinline__ void tell_both(int* ends, int tile) {
+#pragma unroll
+  for (int r = 0; r < 2; ++r)
+    asm volatile("st.relaxed.cluster.shared::cluster.u32 [%0], %1;" ::"r"(peer_address(smem_u32(ends), r)), "r"(tile) : "memory");
+}
+__device__ __forceinline__ int told(const int* ends) {
+  int tile;
+  asm volatile("ld.relaxed.cluster.shared::cta.u32 %0, [%1];" : "=r"(tile) : "r"(smem_u32(ends)) : "memory");
+  return tile;
+}
+// Waits for the sums of a tile; false where the issuing warp has said that they do not come.  (That warp's own waits all end, the
+// longest time being limit_ns; it is never reached.)
+__device__ __forceinline__ bool sums_come(uint64_t* bar, uint32_t parity, const int* ends, int tile, unsigned long long limit_ns) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = globaltimer();
+  while (!mbar_try_wait(bar, parity))
+    if (told(ends) <= tile || globaltimer() - t0 > limit_ns) return false;
+  return true;
+}
 // A warp's part of a tile: 32 rows (this lane's is n), `columns` of the accumulator from t on, whose scales are at xs.  `free`
-// is the barrier that gives the accumulator back, as soon as the last columns are in registers.
+// is the barrier that gives the accumulator back, as soon as the last columns are in registers.  Of a tile that does not come
+// (`ok` false, ws NaN) neither is touched: its accumulator may be that of an earlier one, which other warps still read.
 template <typename OT, int ACT>
 __device__ __forceinline__ void finish_part(const LinearArgs& a, uint32_t acc, const float* xs, int columns, int t, int n, float ws,
-                                            float bias, uint32_t free) {
+                                            float bias, uint32_t free, bool ok) {
 #pragma unroll 1
   for (int c = 0; c < columns; c += kColumns) {
-    uint32_t v[kColumns];
-    tmem_ld16(acc + c, v);
-    if (c + kColumns >= columns) {
-      tc_before();
-      __syncwarp();
-      if ((threadIdx.x & 31) == 0) arrive_at(free);
+    uint32_t v[kColumns] = {};
+    if (ok) {
+      tmem_ld16(acc + c, v);
+      if (c + kColumns >= columns) {
+        tc_before();
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) arrive_at(free);
+      }
     }
     if (t + c + kColumns <= a.tokens) finish_columns<OT, ACT, true>(a, v, xs + c, t + c, n, ws, bias);
     else if (t + c < a.tokens) finish_columns<OT, ACT, false>(a, v, xs + c, t + c, n, ws, bias);
@@ -518,6 +543,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   __shared__ __align__(8) uint64_t full[kPairStages], empty[kPairStages], accf[2], acce[2], drain;
   __shared__ __align__(16) float x_scales[kPairFinishers][kPairTokens / 4];
   __shared__ uint32_t tmem_slot;
+  __shared__ int ends;  // the first of the pair's tiles whose sums do not come
   const int tid = threadIdx.x, warp = warp_index(), lane = tid & 31;
   const int rank = static_cast<int>(cta_rank());
   const int step_bytes = (kRows + sh.tokens / 2) * kStepBytes, stage = sh.group * step_bytes;  // multiples of 1024
@@ -537,6 +563,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     }
     mbar_init(&drain, 1);
     fence_mbar_init();
+    ends = INT_MAX;
   }
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&tmem_slot)) : "memory");
@@ -599,13 +626,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     bool ok = true;
     for (int i = 0; i < mine && ok; ++i) {
       const int b = i & 1;
-      if (i >= 2 && !warp_wait(&acce[b], static_cast<uint32_t>((i >> 1) - 1) & 1u, a.limit_ns)) {
-        ok = false;
-        break;
-      }
+      if (i >= 2) ok = warp_wait(&acce[b], static_cast<uint32_t>((i >> 1) - 1) & 1u, a.limit_ns);
       tc_after();
       const uint32_t acc = tmem + b * kPairTokens;
-      for (int f = 0; f < fills; ++f) {
+      for (int f = 0; f < fills && ok; ++f) {
         if (!warp_wait(&full[s], ph & 1u, a.limit_ns)) {
           ok = false;
           break;
@@ -628,17 +652,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         __syncwarp();
         if (++s == sh.stages) s = 0, ++ph;
       }
+      if (!ok && lane == 0) tell_both(&ends, i);
     }
     if (elected())
       asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(&drain)) : "memory");
     __syncwarp();
-    if ((!mbar_wait(&drain, 0) || !ok) && lane == 0 && a.flags != nullptr) atomicOr(a.flags, a.bit);
+    const bool drained = __all_sync(0xffffffffu, mbar_wait(&drain, 0));
+    if (!drained && lane == 0) tell_both(&ends, 0);  // of the tiles whose MMAs were issued, those that have not come
+    if ((!drained || !ok) && lane == 0 && a.flags != nullptr) atomicOr(a.flags, a.bit);
     __syncwarp();
   } else if (warp >= kPairOthers) {
     // 32 of the rows, and a quarter of the columns, in whole passes
     const int group = warp & 3, quarter = (warp - kPairOthers) >> 2, passes = sh.tokens / kColumns;
     const int c0 = (quarter * passes >> 2) * kColumns, columns = ((quarter + 1) * passes >> 2) * kColumns - c0;
     float* xs = x_scales[warp - kPairOthers];
+    const unsigned long long longest = (fills + 2) * a.limit_ns + 2 * kWaitLimitNs;
     bool ok = true;
     for (int i = 0; i < mine; ++i) {
       const int b = i & 1, tile = pair + i * pairs, rt = tile / sh.token_tiles;
@@ -648,11 +676,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       __syncwarp();
       const float ws = a.w_scale != nullptr && n < a.rows ? __ldg(a.w_scale + n) : 1.f;
       const float bias = a.bias != nullptr && n < a.rows ? __ldg(a.bias + n) : 0.f;
-      // once a wait has run out the rest of this CTA's tiles is NaN
-      if (ok) ok = __all_sync(0xffffffffu, wait_for(&accf[b], static_cast<uint32_t>(i >> 1) & 1u, a.limit_ns));
+      // from the first tile that does not come on, the rest of the pair's is NaN
+      if (ok) ok = __all_sync(0xffffffffu, sums_come(&accf[b], static_cast<uint32_t>(i >> 1) & 1u, &ends, i, longest));
       tc_after();
       const uint32_t acc = tmem + b * kPairTokens + c0 + (static_cast<uint32_t>(group * 32) << 16), free = first_cta(&acce[b]);
-      finish_part<OT, ACT>(a, acc, xs, columns, t, n, ok ? ws : __uint_as_float(0x7FC00000u), bias, free);
+      finish_part<OT, ACT>(a, acc, xs, columns, t, n, ok ? ws : __uint_as_float(0x7FC00000u), bias, free, ok);
     }
     if (!ok && lane == 0 && a.flags != nullptr) atomicOr(a.flags, a.bit);
   }

@@ -730,8 +730,10 @@ k2_status k2_norm_quantize(const k2_row_args* args, void* stream);
  * Products are exact and summed in fp32, and so is all that follows; the result is rounded
  * once.  The order of the sums depends on the sizes alone, so that a call repeats bit for
  * bit.  Except for that one residual, out may not lie over an input.  A NaN costs the outputs
- * that it enters.  Every wait inside is bounded (wait_limit_us up to 1000000; 0: one second); a tile
- * whose wait ran out is NaN throughout and K2_LINEAR_TIMEOUT is OR-ed into *flags. */
+ * that it enters.  Every wait inside is bounded (wait_limit_us up to 1000000; 0: one second): a tile
+ * whose wait ran out, and the later ones of the CTAs that worked on it, are NaN throughout, and
+ * K2_LINEAR_TIMEOUT is OR-ed into *flags (which may be where no tile was lost after all).  What such a
+ * call has on its way is then waited for, whatever wait_limit_us says, for a second or two at most. */
 enum { K2_ACT_NONE = 0, K2_ACT_RELU, K2_ACT_SILU, K2_ACT_GELU, K2_ACT_GELU_TANH, K2_ACT_SWIGLU };
 enum { K2_LINEAR_TIMEOUT = 1 };
 typedef struct {
