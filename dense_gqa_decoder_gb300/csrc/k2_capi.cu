@@ -901,7 +901,7 @@ cudaError_t prefill_block(k2_ctx* c, int seq, const int32_t* d_tokens, int n, in
   // 128-token tiles, the only ones with a low-half weight operand)
   // fp8 weights with option K2_OPT_ACT8: every row that enters a matrix as E4M3 codes with a scale, whatever the block's size
   const bool a8 = c->act8;
-  const bool small = n <= 16 && !q4 && !a8;
+  const bool few = n <= 16 && !q4, small = few && !a8;
   // fp16 operands (option K2_OPT_PREFILL_SPLIT = 3: bf16 weights, fp16 caches on
   // the tcgen05 attention, blocks over 16 tokens): each matrix of the layer is
   // converted to fp16 (exact in fp16's normal range) before its GEMM, and the
@@ -988,7 +988,7 @@ cudaError_t prefill_block(k2_ctx* c, int seq, const int32_t* d_tokens, int n, in
   // the GEMMs read the high halves alone
   // int4: the low-half weight MMA needs the activations' halves
   const bool split = !f16 && !a8 && (small || mode != 0 || q4);
-  const bool attn_split = !a8 && (small || mode == 1);  // 2, 3: the attention's Q and P single
+  const bool attn_split = few || mode == 1;  // 2, 3: the attention's Q and P single
   const void* m_xh = small ? c->tb_xh.data() : wide ? c->tw_xh.data() : c->tm_xh.data();
   const void* m_xl = small ? c->tb_xl.data() : split ? c->tm_xl.data() : nullptr;
   const void* m_oh = small ? c->tb_oh.data() : wide ? c->tw_oh.data() : c->tm_oh.data();

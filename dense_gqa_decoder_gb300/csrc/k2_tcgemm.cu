@@ -973,7 +973,7 @@ cudaError_t prefill_attn_tc_init_attrs() {
 cudaError_t launch_prefill_attn_tc(const KvMaps& maps, const PrefillAttnArgs& a, int head_dim, int rep,
                                    cudaStream_t s) {
   if (a.n <= 0) return cudaSuccess;
-  if (!prefill_attn_tc_supported(head_dim, rep) || (a.split && a.ol == nullptr)) return cudaErrorInvalidValue;
+  if (!prefill_attn_tc_supported(head_dim, rep) || (a.split && a.ol == nullptr && !a.f16out)) return cudaErrorInvalidValue;
   const dim3 grid((a.n + kPaRows / rep - 1) / (kPaRows / rep), a.nkv);
   if (head_dim == 128 && a.split)
     prefill_attn_tc_kernel<128, 4, true><<<grid, PaSmem<128, true>::THREADS, PaSmem<128, true>::DYN, s>>>(maps, a);

@@ -442,7 +442,11 @@ typedef enum {
                              and the activations in halves.  The last token of a prompt and the decode steps
                              keep fp32 activations, and so does the lm_head.  K2_ERR_UNSUPPORTED for other
                              weights or where the tensor-core prefill does not run.  Rounding an activation to
-                             E4M3 is off by up to 2^-4 of its value: about 2.6 % of a row (relative L2). */
+                             E4M3 is off by up to 2^-4 of its value: about 2.6 % of a row (relative L2).
+                             On their way to codes the attention's rows are rounded to 16 bits (fp16 with fp16
+                             caches and in k2_paged_step, bf16 otherwise) and the SwiGLU's to bf16.  The
+                             attention's queries and probabilities are halves or single as K2_OPT_PREFILL_SPLIT
+                             says (the activations of the GEMMs, of which it speaks too, are codes) */
 } k2_option;
 k2_status k2_set_option(k2_ctx* ctx, int32_t option, int64_t value);
 

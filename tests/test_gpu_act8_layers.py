@@ -1,0 +1,101 @@
+"""fp8 weights with E4M3 activations (option K2_OPT_ACT8), layer by layer: the cache rows that a prompt's block leaves in the second
+and third layer against the oracle whose projections round their rows to codes.
+
+Both round the same numbers at the same places, so where no value falls to the neighbouring code a row agrees to the rounding of
+the cache.  A value that differs by e (relative) before it is rounded to E4M3 falls to another code in at most 2^4 e of all
+cases; with e of 1e-6 (fp32 sums, attention in halves) and some 3600 rounded values behind a row, one row in twenty holds such a value, and
+with e of 2^-12 or 2^-9 (queries and probabilities in single fp16, the attention's output in bf16) every row does.  So the median
+row tells the two apart without a tolerance for codes.  A row of the first layer that holds such a value differs by 2^-4 /
+sqrt(512) or more, and so, through the attention, e is no longer 1e-6 in the rows behind it: those are not looked at.
+"""
+import numpy as np
+import pytest
+import torch
+
+import k2_inputs as ki
+from oracle import k2_fp8 as Q8
+from oracle import k2_linear as L
+from oracle import k2_oracle as O
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def k2():
+    from dense_gqa_decoder_gb300 import k2 as mod
+    return mod
+
+
+def sharp(s, kv, n, heat):
+    """A context of s with E4M3 activations whose first layer's queries are `heat` times as long, and the oracle's weights."""
+    from dense_gqa_decoder_gb300 import k2, model_io
+    dev, host = model_io.device_weights(s, gain_scale=0.1, keep_host=True)
+    dev["wq"][0] *= heat  # a power of two: exact
+    host[("wq", 0)] = host[("wq", 0)] * np.float32(heat)
+    ctx = k2.Context(k2.make_config(s, max_context=n + 16, kv_dtype=kv, weights="f8"), dev)
+    ctx.set_option(k2.K2_OPT_ACT8, 1)
+    return ctx, Q8.fp8_weights(lambda name, l: host[(name, l)])
+
+
+def cached(k2, ctx, s, kv, ids, layer):
+    """K and V rows [tokens, heads, dim] of a layer for all of the prompt but its last token (that one is the decode step's)."""
+    ctx.kv_reset()
+    nxt = torch.zeros(1, dtype=torch.int32, device="cuda")
+    ctx.prefill(0, torch.tensor(ids, dtype=torch.int32, device="cuda"), nxt)
+    assert ctx.sync_status() == k2.K2_OK
+    n, cap = len(ids) - 1, ctx.info().kv_capacity
+    rows = []
+    k, v, ks, vs, _ = ctx.kv_view(layer, 0)
+    for p, sc in ((k, ks), (v, vs)):
+        r = k2.device_view(p, s.n_kv_heads * cap * s.head_dim, torch.float16 if kv == "f16" else torch.int8)
+        r = r.view(s.n_kv_heads, cap, s.head_dim)[:, :n].float()
+        if kv == "i8":
+            r = r * k2.device_view(sc, s.n_kv_heads * cap, torch.float16).view(s.n_kv_heads, cap, 1)[:, :n].float()
+        rows.append(r.permute(1, 0, 2).cpu().numpy().astype(np.float64))
+    return rows
+
+
+def oracle_rows(s, get, kv, attention, ids, layer):
+    m = L.act8(O.OracleModel(s, get, kv), attention)
+    cache = m.new_cache(len(ids))
+    m.run(ids[:-1], cache, None)
+    return [c[layer][:len(ids) - 1] for c in (cache.k, cache.v)]
+
+
+def difference(a, b):
+    """The relative L2 difference of every row, the larger of K's and V's."""
+    return np.max([np.linalg.norm((x - y).reshape(len(x), -1), axis=1) / np.linalg.norm(y.reshape(len(y), -1), axis=1) for x, y in zip(a, b)], 0)
+
+
+def rows_that_agree(k2, ctx, s, kv, get, attention, ids):
+    """How many rows of the first layer there are before one that differs."""
+    apart = difference(cached(k2, ctx, s, kv, ids, 0), oracle_rows(s, get, kv, attention, ids, 0)) > SAME
+    return int(np.argmax(apart)) if apart.any() else len(apart)
+
+
+# falling to the neighbouring fp16 number, in every element: 2^-10 of it
+SAME = 2.0 ** -10
+
+
+@pytest.mark.parametrize("heat", [1, 32])
+@pytest.mark.parametrize("n", [251, 16, 90])
+def test_the_attention_keeps_its_halves(k2, heat, n):
+    """K2_OPT_PREFILL_SPLIT says whether the attention takes queries and probabilities in halves, and blocks of up to 16 tokens
+    always do; E4M3 activations change nothing in that."""
+    s = ki.MEDIUM.replace(n_layers=2)
+    ctx, get = sharp(s, "f16", n, heat)
+    ids = ki.prompt_ids(s.vocab, n, seed=51)
+    want = oracle_rows(s, get, "f16", "f16", ids, 1)
+    rows = rows_that_agree(k2, ctx, s, "f16", get, "f16", ids)
+    assert rows >= min(n - 1, 20)
+    far = {}
+    for split in (3, 1, 2, 0):
+        ctx.set_option(k2.K2_OPT_PREFILL_SPLIT, split)
+        far[split] = float(np.median(difference(cached(k2, ctx, s, "f16", ids, 1), want)[:rows]))
+    assert far[1] <= SAME and far[3] == far[1], far
+    if n <= 17:
+        assert far[2] == far[1] and far[0] == far[1], far
+    else:
+        assert far[0] == far[2], far
+    if n == 251:
+        assert far[2] > 2 * SAME, far  # in single fp16 it shows
