@@ -289,8 +289,9 @@ template <int D, int REP, typename KVT>
 __global__ void __launch_bounds__(kPaThreads) prefill_attn_kernel(const float* __restrict__ Q, const KVT* __restrict__ kc,
                                                                   const KVT* __restrict__ vc, const __half* __restrict__ ks,
                                                                   const __half* __restrict__ vs, __nv_bfloat16* __restrict__ oh,
-                                                                  __nv_bfloat16* __restrict__ ol, int n, int nq, int pos0,
-                                                                  size_t head_row0, int cap, float scale) {
+                                                                  __nv_bfloat16* __restrict__ ol, float* __restrict__ of,
+                                                                  int n, int nq, int pos0, size_t head_row0, int cap,
+                                                                  float scale) {
   constexpr int QR = kPaQT * REP;   // query rows of the CTA (64 for REP 4)
   constexpr int DP = D + 1;         // padded row (bank spread)
   constexpr int RPT = QR / 16;      // rows per thread (threads as 16 x 16)
@@ -407,6 +408,10 @@ __global__ void __launch_bounds__(kPaThreads) prefill_attn_kernel(const float* _
     const size_t base = static_cast<size_t>(t0 + tq) * nq * D + (g * REP + h) * D + tx * DPT;
 #pragma unroll
     for (int e = 0; e < DPT; ++e) {
+      if (of != nullptr) {
+        of[base + e] = o[i][e] * inv;
+        continue;
+      }
       __nv_bfloat16 hi, lo;
       split_bf16(o[i][e] * inv, hi, lo);
       oh[base + e] = hi;
@@ -436,8 +441,8 @@ __device__ __forceinline__ int swz(int r, int c) {
 template <int D, int REP, typename KVT>
 __global__ void __launch_bounds__(kMaThreads) prefill_attn_mma_kernel(
     const float* __restrict__ Q, const KVT* __restrict__ kc, const KVT* __restrict__ vc, const __half* __restrict__ ks,
-    const __half* __restrict__ vs, __nv_bfloat16* __restrict__ oh, __nv_bfloat16* __restrict__ ol, int n, int nq,
-    int pos0, size_t head_row0, int cap, float scale) {
+    const __half* __restrict__ vs, __nv_bfloat16* __restrict__ oh, __nv_bfloat16* __restrict__ ol, float* __restrict__ of,
+    int n, int nq, int pos0, size_t head_row0, int cap, float scale) {
   constexpr bool I8 = std::is_same<KVT, int8_t>::value;
   constexpr int QT = kMaRows / REP;  // tokens per CTA
   constexpr int KS = D / 16;         // k-steps of Q.K
@@ -602,7 +607,7 @@ __global__ void __launch_bounds__(kMaThreads) prefill_attn_mma_kernel(
       }
     }
   }
-  // normalise and write rows r0, r1 (dims 8j + 2t, +1) as bf16 hi/lo
+  // normalise and write rows r0, r1 (dims 8j + 2t, +1) as bf16 hi/lo, or (of) as they are
   const float inv0 = l0 > 0.f ? 1.0f / l0 : 0.f, inv1 = l1 > 0.f ? 1.0f / l1 : 0.f;
 #pragma unroll
   for (int row = 0; row < 2; ++row) {
@@ -614,6 +619,10 @@ __global__ void __launch_bounds__(kMaThreads) prefill_attn_mma_kernel(
     for (int j = 0; j < NT; ++j) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
+        if (of != nullptr) {
+          of[base + 8 * j + 2 * t + e] = o[j][2 * row + e] * inv;
+          continue;
+        }
         __nv_bfloat16 hi, lo;
         split_bf16(o[j][2 * row + e] * inv, hi, lo);
         oh[base + 8 * j + 2 * t + e] = hi;
@@ -838,8 +847,8 @@ cudaError_t launch_rope_append(const float* qkv, float* Q, const float2* rope, i
 }
 
 cudaError_t launch_prefill_attn(const float* Q, int kv_dtype, const void* kc, const void* vc, const void* ks,
-                                const void* vs, __nv_bfloat16* oh, __nv_bfloat16* ol, int n, int nq, int nkv, int D,
-                                int pos0, size_t head_row0, int cap, float scale, cudaStream_t s) {
+                                const void* vs, __nv_bfloat16* oh, __nv_bfloat16* ol, float* of, int n, int nq, int nkv,
+                                int D, int pos0, size_t head_row0, int cap, float scale, cudaStream_t s) {
   const int rep = nq / nkv;
   dim3 grid((n + kPaQT - 1) / kPaQT, nkv);
 #define K2_PA_LAUNCH(DD, R)                                                                                       \
@@ -847,17 +856,17 @@ cudaError_t launch_prefill_attn(const float* Q, int kv_dtype, const void* kc, co
     const size_t sm = attn_smem<DD, R>();                                                                         \
     const dim3 mgrid((n + kMaRows / R - 1) / (kMaRows / R), nkv);                                              \
     if (kv_dtype == 0)                                                                                            \
-      prefill_attn_kernel<DD, R, float><<<grid, kPaThreads, sm, s>>>(                                             \
-          Q, static_cast<const float*>(kc), static_cast<const float*>(vc), nullptr, nullptr, oh, ol, n, nq, pos0, \
-          head_row0, cap, scale);                                                                                 \
+      prefill_attn_kernel<DD, R, float><<<grid, kPaThreads, sm, s>>>(                                                  \
+          Q, static_cast<const float*>(kc), static_cast<const float*>(vc), nullptr, nullptr, oh, ol, of, n, nq,  \
+          pos0, head_row0, cap, scale);                                                                          \
     else if (kv_dtype == 2)                                                                                       \
       prefill_attn_mma_kernel<DD, R, __half><<<mgrid, kMaThreads, 0, s>>>(                                        \
-          Q, static_cast<const __half*>(kc), static_cast<const __half*>(vc), nullptr, nullptr, oh, ol, n, nq,     \
+          Q, static_cast<const __half*>(kc), static_cast<const __half*>(vc), nullptr, nullptr, oh, ol, of, n, nq, \
           pos0, head_row0, cap, scale);                                                                           \
     else                                                                                                          \
       prefill_attn_mma_kernel<DD, R, int8_t><<<mgrid, kMaThreads, 0, s>>>(                                        \
           Q, static_cast<const int8_t*>(kc), static_cast<const int8_t*>(vc), static_cast<const __half*>(ks),      \
-          static_cast<const __half*>(vs), oh, ol, n, nq, pos0, head_row0, cap, scale);                            \
+          static_cast<const __half*>(vs), oh, ol, of, n, nq, pos0, head_row0, cap, scale);                        \
     return cudaGetLastError();                                                                                    \
   }
   K2_PREFILL_ATTN_SHAPES(K2_PA_LAUNCH)

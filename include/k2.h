@@ -443,8 +443,8 @@ typedef enum {
                              keep fp32 activations, and so does the lm_head.  K2_ERR_UNSUPPORTED for other
                              weights or where the tensor-core prefill does not run.  Rounding an activation to
                              E4M3 is off by up to 2^-4 of its value: about 2.6 % of a row (relative L2).
-                             On their way to codes the attention's rows are rounded to 16 bits (fp16 with fp16
-                             caches and in k2_paged_step, bf16 otherwise) and the SwiGLU's to bf16.  The
+                             On their way to codes the attention's rows are rounded to fp16 where the tcgen05
+                             attention or k2_paged_step made them, and the SwiGLU's rows to bf16.  The
                              attention's queries and probabilities are halves or single as K2_OPT_PREFILL_SPLIT
                              says (the activations of the GEMMs, of which it speaks too, are codes) */
 } k2_option;

@@ -117,7 +117,7 @@ class _RoundedMatrix:
 
 def act8(model, attention="f16"):
     """The oracle model with the projections of its layers over E4M3 activations: the library keeps the attention's output as
-    `attention` ("f16" or "bf16") and the SwiGLU's as bf16 until they are rounded to codes."""
+    `attention` ("f16", or None: in fp32) and the SwiGLU's as bf16 until they are rounded to codes."""
     plain = model._w
     before = {"wq": None, "wk": None, "wv": None, "w_gate": None, "w_up": None, "wo": attention, "w_down": "bf16"}
     model._w = lambda name, layer=-1: _RoundedMatrix(plain(name, layer), before[name]) if name in before else plain(name, layer)

@@ -99,3 +99,17 @@ def test_the_attention_keeps_its_halves(k2, heat, n):
         assert far[0] == far[2], far
     if n == 251:
         assert far[2] > 2 * SAME, far  # in single fp16 it shows
+
+
+@pytest.mark.parametrize("kv,tcgen05,n", [("i8", 1, 251), ("i8", 1, 16), ("i8", 1, 60), ("f16", 0, 251), ("f16", 0, 16)])
+def test_the_attentions_rows_become_codes_as_they_are(k2, kv, tcgen05, n):
+    """Where the attention is that of int8 caches (or of K2_OPT_PREFILL_ATTN 0) its fp32 rows are rounded once, to E4M3."""
+    s = ki.MEDIUM.replace(n_layers=2)
+    ctx, get = sharp(s, kv, n, 1)
+    ctx.set_option(k2.K2_OPT_PREFILL_ATTN, tcgen05)
+    ids = ki.prompt_ids(s.vocab, n, seed=51)
+    rows = rows_that_agree(k2, ctx, s, kv, get, None, ids)
+    assert rows >= min(n - 1, 20)
+    got = cached(k2, ctx, s, kv, ids, 1)
+    far = {a: float(np.median(difference(got, oracle_rows(s, get, kv, a, ids, 1))[:rows])) for a in (None, "bf16")}
+    assert far[None] <= SAME and far["bf16"] > 2 * SAME, far
