@@ -285,7 +285,7 @@ __global__ void active_next_kernel(const int* __restrict__ arg, const int* __res
 // softmax per row, output written as bf16 hi/lo for the o_proj GEMM.
 constexpr int kPaQT = 16, kPaKT = 64, kPaThreads = 256;
 
-template <int D, int REP, typename KVT>
+template <int D, int REP, typename KVT, bool WHOLE>
 __global__ void __launch_bounds__(kPaThreads) prefill_attn_kernel(const float* __restrict__ Q, const KVT* __restrict__ kc,
                                                                   const KVT* __restrict__ vc, const __half* __restrict__ ks,
                                                                   const __half* __restrict__ vs, __nv_bfloat16* __restrict__ oh,
@@ -408,14 +408,14 @@ __global__ void __launch_bounds__(kPaThreads) prefill_attn_kernel(const float* _
     const size_t base = static_cast<size_t>(t0 + tq) * nq * D + (g * REP + h) * D + tx * DPT;
 #pragma unroll
     for (int e = 0; e < DPT; ++e) {
-      if (of != nullptr) {
+      if constexpr (WHOLE) {
         of[base + e] = o[i][e] * inv;
-        continue;
+      } else {
+        __nv_bfloat16 hi, lo;
+        split_bf16(o[i][e] * inv, hi, lo);
+        oh[base + e] = hi;
+        ol[base + e] = lo;
       }
-      __nv_bfloat16 hi, lo;
-      split_bf16(o[i][e] * inv, hi, lo);
-      oh[base + e] = hi;
-      ol[base + e] = lo;
     }
   }
 }
@@ -438,7 +438,7 @@ __device__ __forceinline__ int swz(int r, int c) {
   return r * (D * 2) + ((c ^ (r & 7)) << 4);
 }
 
-template <int D, int REP, typename KVT>
+template <int D, int REP, typename KVT, bool WHOLE>
 __global__ void __launch_bounds__(kMaThreads) prefill_attn_mma_kernel(
     const float* __restrict__ Q, const KVT* __restrict__ kc, const KVT* __restrict__ vc, const __half* __restrict__ ks,
     const __half* __restrict__ vs, __nv_bfloat16* __restrict__ oh, __nv_bfloat16* __restrict__ ol, float* __restrict__ of,
@@ -607,7 +607,7 @@ __global__ void __launch_bounds__(kMaThreads) prefill_attn_mma_kernel(
       }
     }
   }
-  // normalise and write rows r0, r1 (dims 8j + 2t, +1) as bf16 hi/lo, or (of) as they are
+  // normalise and write rows r0, r1 (dims 8j + 2t, +1) as bf16 hi/lo, or (WHOLE) as they are
   const float inv0 = l0 > 0.f ? 1.0f / l0 : 0.f, inv1 = l1 > 0.f ? 1.0f / l1 : 0.f;
 #pragma unroll
   for (int row = 0; row < 2; ++row) {
@@ -619,14 +619,14 @@ __global__ void __launch_bounds__(kMaThreads) prefill_attn_mma_kernel(
     for (int j = 0; j < NT; ++j) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        if (of != nullptr) {
+        if constexpr (WHOLE) {
           of[base + 8 * j + 2 * t + e] = o[j][2 * row + e] * inv;
-          continue;
+        } else {
+          __nv_bfloat16 hi, lo;
+          split_bf16(o[j][2 * row + e] * inv, hi, lo);
+          oh[base + 8 * j + 2 * t + e] = hi;
+          ol[base + 8 * j + 2 * t + e] = lo;
         }
-        __nv_bfloat16 hi, lo;
-        split_bf16(o[j][2 * row + e] * inv, hi, lo);
-        oh[base + 8 * j + 2 * t + e] = hi;
-        ol[base + 8 * j + 2 * t + e] = lo;
       }
     }
   }
@@ -753,11 +753,9 @@ bool prefill_attn_supported(int head_dim, int rep) {
 cudaError_t prefill_init_attrs() {
   cudaError_t e = cudaSuccess;
 #define K2_PA_ATTR(D, R)                                                                                     \
-  if (!e) e = cudaFuncSetAttribute(prefill_attn_kernel<D, R, float>, cudaFuncAttributeMaxDynamicSharedMemorySize, \
-                                   static_cast<int>(attn_smem<D, R>()));                                    \
-  if (!e) e = cudaFuncSetAttribute(prefill_attn_kernel<D, R, __half>,                                        \
-                                   cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(attn_smem<D, R>())); \
-  if (!e) e = cudaFuncSetAttribute(prefill_attn_kernel<D, R, int8_t>,                                        \
+  if (!e) e = cudaFuncSetAttribute(prefill_attn_kernel<D, R, float, false>,                                   \
+                                   cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(attn_smem<D, R>()));\
+  if (!e) e = cudaFuncSetAttribute(prefill_attn_kernel<D, R, float, true>,                                    \
                                    cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(attn_smem<D, R>()));
   K2_PREFILL_ATTN_SHAPES(K2_PA_ATTR)
 #undef K2_PA_ATTR
@@ -846,29 +844,38 @@ cudaError_t launch_rope_append(const float* qkv, float* Q, const float2* rope, i
   }
 }
 
+namespace {
+template <int D, int REP, bool WHOLE>
+cudaError_t launch_prefill_attn_of(const float* Q, int kv_dtype, const void* kc, const void* vc, const void* ks,
+                                   const void* vs, __nv_bfloat16* oh, __nv_bfloat16* ol, float* of, int n, int nq, int nkv,
+                                   int pos0, size_t head_row0, int cap, float scale, cudaStream_t s) {
+  const dim3 grid((n + kPaQT - 1) / kPaQT, nkv), mgrid((n + kMaRows / REP - 1) / (kMaRows / REP), nkv);
+  if (kv_dtype == 0)
+    prefill_attn_kernel<D, REP, float, WHOLE><<<grid, kPaThreads, attn_smem<D, REP>(), s>>>(
+        Q, static_cast<const float*>(kc), static_cast<const float*>(vc), nullptr, nullptr, oh, ol, of, n, nq, pos0,
+        head_row0, cap, scale);
+  else if (kv_dtype == 2)
+    prefill_attn_mma_kernel<D, REP, __half, WHOLE><<<mgrid, kMaThreads, 0, s>>>(
+        Q, static_cast<const __half*>(kc), static_cast<const __half*>(vc), nullptr, nullptr, oh, ol, of, n, nq, pos0,
+        head_row0, cap, scale);
+  else
+    prefill_attn_mma_kernel<D, REP, int8_t, WHOLE><<<mgrid, kMaThreads, 0, s>>>(
+        Q, static_cast<const int8_t*>(kc), static_cast<const int8_t*>(vc), static_cast<const __half*>(ks),
+        static_cast<const __half*>(vs), oh, ol, of, n, nq, pos0, head_row0, cap, scale);
+  return cudaGetLastError();
+}
+}  // namespace
+
 cudaError_t launch_prefill_attn(const float* Q, int kv_dtype, const void* kc, const void* vc, const void* ks,
                                 const void* vs, __nv_bfloat16* oh, __nv_bfloat16* ol, float* of, int n, int nq, int nkv,
                                 int D, int pos0, size_t head_row0, int cap, float scale, cudaStream_t s) {
   const int rep = nq / nkv;
-  dim3 grid((n + kPaQT - 1) / kPaQT, nkv);
 #define K2_PA_LAUNCH(DD, R)                                                                                       \
-  if (D == DD && rep == R) {                                                                                      \
-    const size_t sm = attn_smem<DD, R>();                                                                         \
-    const dim3 mgrid((n + kMaRows / R - 1) / (kMaRows / R), nkv);                                              \
-    if (kv_dtype == 0)                                                                                            \
-      prefill_attn_kernel<DD, R, float><<<grid, kPaThreads, sm, s>>>(                                                  \
-          Q, static_cast<const float*>(kc), static_cast<const float*>(vc), nullptr, nullptr, oh, ol, of, n, nq,  \
-          pos0, head_row0, cap, scale);                                                                          \
-    else if (kv_dtype == 2)                                                                                       \
-      prefill_attn_mma_kernel<DD, R, __half><<<mgrid, kMaThreads, 0, s>>>(                                        \
-          Q, static_cast<const __half*>(kc), static_cast<const __half*>(vc), nullptr, nullptr, oh, ol, of, n, nq, \
-          pos0, head_row0, cap, scale);                                                                           \
-    else                                                                                                          \
-      prefill_attn_mma_kernel<DD, R, int8_t><<<mgrid, kMaThreads, 0, s>>>(                                        \
-          Q, static_cast<const int8_t*>(kc), static_cast<const int8_t*>(vc), static_cast<const __half*>(ks),      \
-          static_cast<const __half*>(vs), oh, ol, of, n, nq, pos0, head_row0, cap, scale);                        \
-    return cudaGetLastError();                                                                                    \
-  }
+  if (D == DD && rep == R)                                                                                        \
+    return of ? launch_prefill_attn_of<DD, R, true>(Q, kv_dtype, kc, vc, ks, vs, oh, ol, of, n, nq, nkv, pos0,    \
+                                                    head_row0, cap, scale, s)                                     \
+              : launch_prefill_attn_of<DD, R, false>(Q, kv_dtype, kc, vc, ks, vs, oh, ol, of, n, nq, nkv, pos0,   \
+                                                     head_row0, cap, scale, s);
   K2_PREFILL_ATTN_SHAPES(K2_PA_LAUNCH)
 #undef K2_PA_LAUNCH
   return cudaErrorInvalidValue;
