@@ -56,9 +56,6 @@ struct Layout {
   size_t wqkv_layer, wo_layer, wgu_layer, wdown_layer;
   // fp8 weights with a tensor-core prefill: the codes as bf16 in the bf16 packed layout
   size_t tqkv, to, tgu, tdown;
-  // and for E4M3 activations: the gate/up codes in pairs of rows, per layer and first layer; the lm_head's codes as
-  // bf16; the scales of a block's rows
-  size_t e8gu, e8gu_layer, e8lm, e8s;
   size_t tqkv_layer, to_layer, tgu_layer, tdown_layer;
   size_t kc, vc, ks, vs;  // first layer; per-layer stride kv_layer / sc_layer
   size_t kv_layer, sc_layer;
@@ -160,7 +157,6 @@ Layout layout_of(const k2_config& c) {
     l.varg = take(sizeof(int) * (kSpecMax + 1));
     l.vpv = take(nv * kArgmaxPartsMax * 4);
     l.vpi = take(nv * kArgmaxPartsMax * 4);
-    l.e8s = take(c.weight_dtype == K2_F8 ? P * sizeof(float) : 0);
   }
   const size_t scratch_end = o;
   // fp8 / int4: pair or tile units by GEMV kind (tiled_kind); else wb-byte
@@ -188,9 +184,6 @@ Layout layout_of(const k2_config& c) {
     l.to = take(l.to_layer * s.L);
     l.tgu = take(l.tgu_layer * s.L);
     l.tdown = take(l.tdown_layer * s.L);
-    l.e8gu_layer = align_up(f8_packed_bytes(2 * s.I, s.H, false), kAlign);
-    l.e8gu = take(l.e8gu_layer * s.L);
-    l.e8lm = take(packed_bytes(s.V, s.H, 2));
   }
   if (c.weight_dtype == K2_BF16 && l.pchunk > 0) {  // two layers' weights as fp16, rebuilt per layer
     for (int b = 0; b < 2; ++b) {
@@ -217,6 +210,20 @@ Layout layout_of(const k2_config& c) {
   l.vs = take(l.sc_layer * s.L);
   l.kv_bytes = o - kv_start;
   l.total = o;
+  return l;
+}
+
+// What E4M3 activations need beside the workspace (k2_act8_init): the gate/up codes in pairs of rows, first layer and per
+// layer; the lm_head's codes as bf16; the scales of a block's rows.
+struct Act8Layout {
+  size_t gu, gu_layer, lm, scales, total;
+};
+Act8Layout act8_layout_of(const Sizes& s, int pchunk) {
+  Act8Layout l = {};
+  l.gu_layer = align_up(f8_packed_bytes(2 * s.I, s.H, false), kAlign);
+  l.lm = l.gu_layer * s.L;
+  l.scales = align_up(l.lm + packed_bytes(s.V, s.H, 2), kAlign);
+  l.total = align_up(l.scales + sizeof(float) * pchunk, kAlign);
   return l;
 }
 
@@ -305,8 +312,10 @@ struct k2_ctx {
   // down; activations: normed input, attention output, SwiGLU output, hi/lo)
   bool tc_ok = false;    // tensor-core prefill
   bool tc_full = false;  // and the paths that also need a bf16 lm_head (batched decode, speculation)
-  bool e8_ok = false;    // fp8 weights: the layers on E4M3 activations, a paged step's lm_head
-  bool act8 = false;     // option K2_OPT_ACT8
+  bool e8_ok = false;    // fp8 weights: the layers can run on E4M3 activations
+  Act8Layout e8lay = {};
+  uint8_t* e8 = nullptr; // the caller's buffer of k2_act8_init
+  bool act8 = false;     // option K2_OPT_ACT8 (needs e8)
   bool use_tc = true;        // prefill
   bool use_tc_decode = true; // batched decode (batch >= 2)
   std::vector<std::array<uint8_t, kTcMapBytes>> tmw;  // 4 per layer
@@ -367,7 +376,7 @@ struct k2_ctx {
   }
   // fp8: the codes of matrix m as a product over E4M3 activations reads them (packed pairs of rows)
   LinearWeights e8w(int l, int m) const {
-    return {m == 0 ? wqkv(l) : m == 1 ? wop(l) : m == 2 ? ws + lay.e8gu + lay.e8gu_layer * l : wdown(l), 0, true};
+    return {m == 0 ? wqkv(l) : m == 1 ? wop(l) : m == 2 ? e8 + e8lay.gu + e8lay.gu_layer * l : wdown(l), 0, true};
   }
   const float* tcs(int l, int m) const {
     if (!f8()) return nullptr;
@@ -855,9 +864,9 @@ cudaError_t plan_tc_prefill(k2_ctx* c) {
   if (16 * 2 * static_cast<size_t>(s.I) > static_cast<size_t>(P) * s.qkv_n) return cudaSuccess;
   if (!ok) return cudaSuccess;
   c->tc_ok = true;
-  // fp8: pairs of rows but for gate/up and the lm_head, whose codes are copied (k2_init_weights)
-  c->e8_ok = c->f8() && !tiled_kind(0) && !tiled_kind(1) && !tiled_kind(3) &&
-             tc_encode_weight(c->tm_lm.data(), c->ws + c->lay.e8lm, s.V, s.H);
+  // fp8: pairs of rows but for gate/up and the lm_head, whose codes are copied (k2_act8_init)
+  c->e8_ok = c->f8() && !tiled_kind(0) && !tiled_kind(1) && !tiled_kind(3);
+  if (c->e8_ok) c->e8lay = act8_layout_of(s, P);
   c->tc_full = !quantized(c->cfg.weight_dtype) && tc_encode_weight(c->tm_lm.data(), c->wlm(), s.V, s.H);
   return cudaSuccess;
 }
@@ -998,7 +1007,7 @@ cudaError_t prefill_block(k2_ctx* c, int seq, const int32_t* d_tokens, int n, in
   // E4M3: codes of the normed rows and of the attention's output in the places of their bf16 halves, those of the SwiGLU rows
   // (bf16 in ah) behind them
   uint8_t *xc = reinterpret_cast<uint8_t*>(xh), *oc = reinterpret_cast<uint8_t*>(xl), *ac = reinterpret_cast<uint8_t*>(al);
-  float* xs = reinterpret_cast<float*>(c->ws + c->lay.e8s);
+  float* xs = a8 ? reinterpret_cast<float*>(c->e8 + c->e8lay.scales) : nullptr;
   const auto wide16 = [](int k) { return static_cast<int64_t>(k + 15) / 16 * 16; };
   k2_status st8 = K2_OK;
   const auto done8 = [&](k2_status got) {
@@ -1629,11 +1638,7 @@ k2_status k2_init_weights(const k2_config* cfg, const k2_weights* w, void* d_wor
       e = launch_f8_expand(c->tcw(l, 2), static_cast<const uint8_t*>(c->wgu(l)), 2 * z.I, z.H, tiled_kind(2), s);
     if (e == cudaSuccess)
       e = launch_f8_expand(c->tcw(l, 3), static_cast<const uint8_t*>(c->wdown(l)), z.H, z.I, tiled_kind(3), s);
-    if (e == cudaSuccess)
-      e = launch_f8_pairs(ws + c->lay.e8gu + c->lay.e8gu_layer * l, static_cast<const uint8_t*>(c->wgu(l)), 2 * z.I, z.H, s);
   }
-  if (e == cudaSuccess && cfg->weight_dtype == K2_F8 && c->lay.pchunk > 0)
-    e = launch_f8_expand(ws + c->lay.e8lm, static_cast<const uint8_t*>(c->wlm()), z.V, z.H, tiled_kind(4), s);
   if (e != cudaSuccess) {
     g_init_error = std::string("repack: ") + cudaGetErrorString(e);
     delete c;
@@ -1906,6 +1911,8 @@ k2_status k2_set_option(k2_ctx* c, int32_t option, int64_t value) {
       if (value < 0 || value > 1) return c->fail(K2_ERR_ARG, "act8 %lld must be 0 or 1", (long long)value);
       if (value && !c->e8_ok)
         return c->fail(K2_ERR_UNSUPPORTED, "E4M3 activations need fp8 weights on the tensor-core prefill");
+      if (value && !c->e8)
+        return c->fail(K2_ERR_WORKSPACE, "E4M3 activations need k2_act8_init first (a buffer of %zu bytes)", c->e8lay.total);
       c->act8 = value != 0;
       break;
     case K2_OPT_PREFILL_SPLIT:
@@ -1927,6 +1934,29 @@ k2_status k2_set_option(k2_ctx* c, int32_t option, int64_t value) {
   for (auto& kv : c->spec_graphs) cudaGraphExecDestroy(kv.second);
   c->graphs.clear();
   c->spec_graphs.clear();
+  return K2_OK;
+}
+
+size_t k2_act8_bytes(const k2_ctx* c) { return c && c->e8_ok ? c->e8lay.total : 0; }
+
+k2_status k2_act8_init(k2_ctx* c, void* d_buffer, size_t bytes, void* stream) {
+  if (!c) return K2_ERR_ARG;
+  if (!c->e8_ok) return c->fail(K2_ERR_UNSUPPORTED, "E4M3 activations need fp8 weights on the tensor-core prefill");
+  if (!d_buffer || reinterpret_cast<uintptr_t>(d_buffer) % kAlign || bytes < c->e8lay.total)
+    return c->fail(K2_ERR_WORKSPACE, "the buffer must be 256-byte aligned and hold k2_act8_bytes() = %zu bytes (got %zu)",
+                   c->e8lay.total, bytes);
+  const Sizes& s = c->s;
+  uint8_t* e8 = static_cast<uint8_t*>(d_buffer);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  std::array<uint8_t, kTcMapBytes> map{};
+  if (!tc_encode_weight(map.data(), e8 + c->e8lay.lm, s.V, s.H)) return c->fail(K2_ERR_CUDA, "no tensor map for the lm_head");
+  cudaError_t e = cudaSuccess;
+  for (int l = 0; l < s.L && !e; ++l)
+    e = launch_f8_pairs(e8 + c->e8lay.gu + c->e8lay.gu_layer * l, static_cast<const uint8_t*>(c->wgu(l)), 2 * s.I, s.H, st);
+  if (!e) e = launch_f8_expand(e8 + c->e8lay.lm, static_cast<const uint8_t*>(c->wlm()), s.V, s.H, tiled_kind(4), st);
+  if (e) return c->cuda_fail(e, "act8 init");
+  c->e8 = e8;
+  c->tm_lm = map;
   return K2_OK;
 }
 

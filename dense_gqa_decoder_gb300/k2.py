@@ -145,6 +145,8 @@ def _load():
         "k2_adjust_logits": (C.c_int, [vp, vp, i64, vp, i64, i32, i32, vp]),
         "k2_quantize_rows": (C.c_int, [vp, vp]),
         "k2_norm_quantize": (C.c_int, [vp, vp]),
+        "k2_act8_bytes": (C.c_size_t, [vp]),
+        "k2_act8_init": (C.c_int, [vp, vp, C.c_size_t, vp]),
         "k2_linear": (C.c_int, [vp, vp]),
     }
     for name, (res, args) in sig.items():
@@ -162,7 +164,7 @@ EXPORTED = ("k2_workspace_bytes", "k2_init_weights", "k2_free", "k2_last_error",
             "k2_philox", "k2_spec_draft", "k2_decode_speculative", "k2_quantize_fp8",
             "k2_quantize_q4", "k2_spec_logits_view", "k2_paged_plan", "k2_paged_append",
             "k2_paged_workspace_bytes", "k2_paged_attention", "k2_paged_step", "k2_adjust_logits",
-            "k2_quantize_rows", "k2_norm_quantize", "k2_linear")
+            "k2_quantize_rows", "k2_norm_quantize", "k2_linear", "k2_act8_bytes", "k2_act8_init")
 
 
 def _ptr(t):
@@ -205,6 +207,7 @@ class Context:
         if nbytes == 0:
             raise K2Error(K2_ERR_ARG, "invalid config: " + (LIB.k2_last_error(None) or b"").decode())
         self.workspace = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+        self.act8_buffer = None  # what K2_OPT_ACT8 needs beside it
         L = cfg.n_layers
         arrs = {}
         for n in ("attn_norm", "wq", "wk", "wv", "wo", "mlp_norm", "w_gate", "w_up", "w_down"):
@@ -283,7 +286,18 @@ class Context:
         self._check(LIB.k2_clear_status(self.ctx, _stream(stream)))
 
     def set_option(self, opt, value):
+        """K2_OPT_ACT8 = 1 calls act8_init first where that was not done."""
+        if opt == K2_OPT_ACT8 and value == 1 and self.act8_buffer is None and LIB.k2_act8_bytes(self.ctx):
+            self.act8_init()
+            torch.cuda.current_stream().synchronize()  # the option holds for any stream
         self._check(LIB.k2_set_option(self.ctx, opt, value))
+
+    def act8_init(self, stream=None):
+        """k2_act8_init, over memory that the context keeps."""
+        n = LIB.k2_act8_bytes(self.ctx)
+        buffer = torch.empty(n, dtype=torch.uint8, device="cuda") if n else None
+        self._check(LIB.k2_act8_init(self.ctx, _ptr(buffer), n, _stream(stream)))
+        self.act8_buffer = buffer
 
     def set_sampling(self, params=None):
         """k2_set_sampling: a Sampling (see sampling()) or None for greedy."""

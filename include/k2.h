@@ -439,8 +439,8 @@ typedef enum {
                              (each row that enters a matrix as codes with one scale: k2_norm_quantize,
                              k2_quantize_rows and k2_linear over the codes of the weights), and is what
                              k2_paged_step needs with fp8 weights; 0 (default) feeds the exact weights as bf16
-                             and the activations in halves.  The last token of a prompt and the decode steps
-                             keep fp32 activations, and so does the lm_head.  K2_ERR_UNSUPPORTED for other
+                             and the activations in halves.  Needs k2_act8_init first (else
+                             K2_ERR_WORKSPACE).  The last token of a prompt and the decode steps keep fp32 activations, and so does the lm_head.  K2_ERR_UNSUPPORTED for other
                              weights or where the tensor-core prefill does not run.  Rounding an activation to
                              E4M3 is off by up to 2^-4 of its value: about 2.6 % of a row (relative L2).
                              On their way to codes the attention's rows are rounded to fp16 where the tcgen05
@@ -449,6 +449,16 @@ typedef enum {
                              says (the activations of the GEMMs, of which it speaks too, are codes) */
 } k2_option;
 k2_status k2_set_option(k2_ctx* ctx, int32_t option, int64_t value);
+
+/* What option K2_OPT_ACT8 needs beside the workspace: copies of the gate/up codes and of
+ * the lm_head's (as bf16) in the forms that its products read.  k2_act8_bytes: how much
+ * device memory that is (3.2 GB for the 3.7B model; 0 where the option is not supported).
+ * k2_act8_init fills d_buffer (256-byte aligned, the caller's, kept until k2_free or the
+ * next k2_act8_init; a captured step keeps reading the one it was captured with) from the
+ * packed weights, enqueued on `stream`, and allows the option.  Contexts that never set the
+ * option need neither. */
+size_t k2_act8_bytes(const k2_ctx* ctx);
+k2_status k2_act8_init(k2_ctx* ctx, void* d_buffer, size_t bytes, void* stream);
 
 /* Kernel classes timed by k2_profile_decode. */
 enum {
