@@ -227,6 +227,9 @@ Act8Layout act8_layout_of(const Sizes& s, int pchunk) {
   return l;
 }
 
+const char kNoAct8[] = "E4M3 activations need fp8 weights on the tensor-core prefill, rows of at most %d values and eps of at "
+                       "least 2^-126";
+
 std::string check_config(const k2_config* c) {
   if (!c) return "config is NULL";
   if (c->hidden <= 0 || c->n_layers <= 0 || c->n_heads <= 0 || c->n_kv_heads <= 0 || c->head_dim <= 0 ||
@@ -865,7 +868,8 @@ cudaError_t plan_tc_prefill(k2_ctx* c) {
   if (!ok) return cudaSuccess;
   c->tc_ok = true;
   // fp8: pairs of rows but for gate/up and the lm_head, whose codes are copied (k2_act8_init)
-  c->e8_ok = c->f8() && !tiled_kind(0) && !tiled_kind(1) && !tiled_kind(3);
+  c->e8_ok = c->f8() && !tiled_kind(0) && !tiled_kind(1) && !tiled_kind(3) && c->cfg.eps >= kMinEps && std::isfinite(c->cfg.eps) &&
+             std::max({s.H, s.nq * s.d, s.I}) <= kMaxRowCols;
   if (c->e8_ok) c->e8lay = act8_layout_of(s, P);
   c->tc_full = !quantized(c->cfg.weight_dtype) && tc_encode_weight(c->tm_lm.data(), c->wlm(), s.V, s.H);
   return cudaSuccess;
@@ -1910,7 +1914,7 @@ k2_status k2_set_option(k2_ctx* c, int32_t option, int64_t value) {
     case K2_OPT_ACT8:
       if (value < 0 || value > 1) return c->fail(K2_ERR_ARG, "act8 %lld must be 0 or 1", (long long)value);
       if (value && !c->e8_ok)
-        return c->fail(K2_ERR_UNSUPPORTED, "E4M3 activations need fp8 weights on the tensor-core prefill");
+        return c->fail(K2_ERR_UNSUPPORTED, kNoAct8, kMaxRowCols);
       if (value && !c->e8)
         return c->fail(K2_ERR_WORKSPACE, "E4M3 activations need k2_act8_init first (a buffer of %zu bytes)", c->e8lay.total);
       c->act8 = value != 0;
@@ -1941,7 +1945,7 @@ size_t k2_act8_bytes(const k2_ctx* c) { return c && c->e8_ok ? c->e8lay.total : 
 
 k2_status k2_act8_init(k2_ctx* c, void* d_buffer, size_t bytes, void* stream) {
   if (!c) return K2_ERR_ARG;
-  if (!c->e8_ok) return c->fail(K2_ERR_UNSUPPORTED, "E4M3 activations need fp8 weights on the tensor-core prefill");
+  if (!c->e8_ok) return c->fail(K2_ERR_UNSUPPORTED, kNoAct8, kMaxRowCols);
   if (!d_buffer || reinterpret_cast<uintptr_t>(d_buffer) % kAlign || bytes < c->e8lay.total)
     return c->fail(K2_ERR_WORKSPACE, "the buffer must be 256-byte aligned and hold k2_act8_bytes() = %zu bytes (got %zu)",
                    c->e8lay.total, bytes);

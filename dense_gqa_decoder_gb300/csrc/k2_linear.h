@@ -8,6 +8,11 @@
 
 namespace k2 {
 
+// What k2_quantize_rows and k2_norm_quantize take: rows of up to kMaxRowCols values (as fp32 in shared memory: 192 KB), and
+// for the norm an eps that is a normal number.
+constexpr int kMaxRowCols = 49152;
+constexpr float kMinEps = 0x1p-126f;
+
 // A product as the kernels see it (k2_linear_args, checked).
 struct LinearArgs {
   const float* w_scale;  // null: none

@@ -19,7 +19,6 @@ namespace k2 {
 
 namespace {
 
-constexpr int kMaxCols = 49152;   // a row in shared memory as fp32: 192 KB
 constexpr float kTop = 448.0f;    // the largest finite E4M3 value
 constexpr uint8_t kCodeNaN = 0x7F;
 
@@ -540,7 +539,7 @@ cudaError_t launch_rows(const RowArgs& a, int tokens, cudaStream_t s) {
   }
   static std::atomic<uint64_t> ready{0};
   auto kernel = rows_kernel<XT, RT, NORM>;
-  e = allow_smem(reinterpret_cast<const void*>(kernel), kMaxCols * static_cast<int>(sizeof(float)), dev, ready);
+  e = allow_smem(reinterpret_cast<const void*>(kernel), kMaxRowCols * static_cast<int>(sizeof(float)), dev, ready);
   if (e != cudaSuccess) return e;
   return launch_early(kernel, tokens, 256, a.cols * sizeof(float), s, a);
 }
@@ -566,8 +565,8 @@ k2_status check_rows(const k2_row_args* p) {
     set_error("rows must be K2_F32, K2_BF16 or K2_F16 (got dtype %d)", p->x_dtype);
     return K2_ERR_UNSUPPORTED;
   }
-  if (p->tokens < 0 || p->tokens > 1 << 30 || p->cols < 1 || p->cols > kMaxCols) {
-    set_error("tokens in [0, 2^30] and rows of 1 .. %d values (got %d, %d)", kMaxCols, p->tokens, p->cols);
+  if (p->tokens < 0 || p->tokens > 1 << 30 || p->cols < 1 || p->cols > kMaxRowCols) {
+    set_error("tokens in [0, 2^30] and rows of 1 .. %d values (got %d, %d)", kMaxRowCols, p->tokens, p->cols);
     return K2_ERR_SHAPE;
   }
   if (p->tokens == 0) return K2_OK;
@@ -640,7 +639,7 @@ k2_status k2_norm_quantize(const k2_row_args* p, void* stream) {
     set_error("cols %d must be a multiple of groups (got %d)", p->cols, p->groups);
     return K2_ERR_SHAPE;
   }
-  if (!(p->eps >= 0x1p-126f) || isinf(p->eps)) {
+  if (!(p->eps >= kMinEps) || isinf(p->eps)) {
     set_error("eps must be finite and at least 2^-126 (got %g)", p->eps);
     return K2_ERR_ARG;
   }

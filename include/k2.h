@@ -441,7 +441,8 @@ typedef enum {
                              k2_paged_step needs with fp8 weights; 0 (default) feeds the exact weights as bf16
                              and the activations in halves.  Needs k2_act8_init first (else
                              K2_ERR_WORKSPACE).  The last token of a prompt and the decode steps keep fp32 activations, and so does the lm_head.  K2_ERR_UNSUPPORTED for other
-                             weights or where the tensor-core prefill does not run.  Rounding an activation to
+                             weights, where the tensor-core prefill does not run, and for rows or an eps
+                             that k2_norm_quantize does not take.  Rounding an activation to
                              E4M3 is off by up to 2^-4 of its value: about 2.6 % of a row (relative L2).
                              On their way to codes the attention's rows are rounded to fp16 where the tcgen05
                              attention or k2_paged_step made them, and the SwiGLU's rows to bf16.  The

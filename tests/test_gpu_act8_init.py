@@ -67,3 +67,15 @@ def test_where_there_is_no_such_option(k2, weights, kv, shape):
     with pytest.raises(k2.K2Error) as e:
         ctx.act8_init()
     assert e.value.status == k2.K2_ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("eps", [0.0, 1e-39, float("inf")])
+def test_a_norm_that_the_rows_calls_refuse(k2, eps):
+    """k2_norm_quantize takes no eps below 2^-126, and so the option is refused, ahead of any prompt."""
+    ctx = context(shape=ki.MEDIUM.replace(eps=eps))
+    with pytest.raises(k2.K2Error) as e:
+        ctx.set_option(k2.K2_OPT_ACT8, 1)
+    assert e.value.status == k2.K2_ERR_UNSUPPORTED and "eps" in str(e.value)
+    assert k2.LIB.k2_act8_bytes(ctx.ctx) == 0
+    if eps < 1:
+        assert torch.isfinite(logits(k2, ctx)).all()
