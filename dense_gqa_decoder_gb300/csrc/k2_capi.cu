@@ -319,6 +319,7 @@ struct k2_ctx {
   Act8Layout e8lay = {};
   uint8_t* e8 = nullptr; // the caller's buffer of k2_act8_init
   bool act8 = false;     // option K2_OPT_ACT8 (needs e8)
+  k2_status refused8 = K2_OK;  // what a conversion or product of the last block answered (its reason: k2_last_error(NULL))
   bool use_tc = true;        // prefill
   bool use_tc_decode = true; // batched decode (batch >= 2)
   std::vector<std::array<uint8_t, kTcMapBytes>> tmw;  // 4 per layer
@@ -1013,9 +1014,9 @@ cudaError_t prefill_block(k2_ctx* c, int seq, const int32_t* d_tokens, int n, in
   uint8_t *xc = reinterpret_cast<uint8_t*>(xh), *oc = reinterpret_cast<uint8_t*>(xl), *ac = reinterpret_cast<uint8_t*>(al);
   float* xs = a8 ? reinterpret_cast<float*>(c->e8 + c->e8lay.scales) : nullptr;
   const auto wide16 = [](int k) { return static_cast<int64_t>(k + 15) / 16 * 16; };
-  k2_status st8 = K2_OK;
+  c->refused8 = K2_OK;
   const auto done8 = [&](k2_status got) {
-    if (got != K2_OK) st8 = got;
+    if (got != K2_OK) c->refused8 = got;
     return got == K2_OK ? cudaSuccess : cudaErrorUnknown;
   };
   auto rows8 = [&](const void* rows, int dtype, int k, uint8_t* codes) {
@@ -1184,7 +1185,7 @@ cudaError_t prefill_block(k2_ctx* c, int seq, const int32_t* d_tokens, int n, in
       if (!e) e = convert_layer(l + 2);
     }
   }
-  if (paged && st8 != K2_OK) paged->refused = st8;
+  if (paged && c->refused8 != K2_OK) paged->refused = c->refused8;
   if (f16) {  // st waits for everything issued on the second stream (a failed call included)
     cudaError_t j = cudaEventRecord(c->ev_join, c->side);
     if (!j) j = cudaStreamWaitEvent(st, c->ev_join, 0);
@@ -1706,6 +1707,7 @@ k2_status k2_prefill(k2_ctx* c, int32_t seq, const int32_t* d_tokens, int32_t n,
   Launcher ln{c, static_cast<cudaStream_t>(stream), c->pdl};
   if (c->tc_ok && c->use_tc && n >= kTcPrefillMin) {
     const cudaError_t e = prefill_tc(c, seq, d_tokens, n, d_next_token, lg, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess && c->refused8 != K2_OK) return c->fail(c->refused8, "tensor-core prefill: %s", g_init_error.c_str());
     if (e != cudaSuccess) return c->cuda_fail(e, "tensor-core prefill");
   } else {
     for (int i = 0; i < n; ++i) {
