@@ -113,3 +113,63 @@ def test_the_attentions_rows_become_codes_as_they_are(k2, kv, tcgen05, n):
     got = cached(k2, ctx, s, kv, ids, 1)
     far = {a: float(np.median(difference(got, oracle_rows(s, get, kv, a, ids, 1))[:rows])) for a in (None, "bf16")}
     assert far[None] <= SAME and far["bf16"] > 2 * SAME, far
+
+
+def layer_by_hand(k2, s, dev, tokens, cache, slots, cu, kv_len, table, workspace):
+    """A layer of first tokens out of the public calls: what each of them reads is what the one before it left."""
+    empty = lambda *n: torch.empty(*n, device="cuda")  # noqa: E731
+    t, h, qs, ks = len(tokens), s.hidden, s.n_heads * s.head_dim, s.n_kv_heads * s.head_dim
+
+    def codes_for(n):
+        return torch.zeros(t, -(-n // 16) * 16, dtype=torch.uint8, device="cuda")[:, :n].view(torch.float8_e4m3fn), empty(t)
+
+    def product(w, x, out, **kw):
+        codes, scale = k2.quantize_fp8(w.contiguous())
+        rows = torch.zeros(len(codes), -(-codes.shape[1] // 16) * 16, dtype=torch.uint8, device="cuda")[:, :codes.shape[1]]
+        rows.copy_(codes)
+        k2.linear(rows, x[0], out, w_scale=scale, x_scale=x[1], **kw)
+        return out
+
+    x0 = dev["embed"][tokens].float()
+    xn = codes_for(h)
+    k2.norm_quantize(x0, dev["attn_norm"][0], *xn, groups=s.norm_groups, eps=s.eps)
+    qkv = product(torch.cat([dev[n][0] for n in ("wq", "wk", "wv")]), xn, empty(t, qs + 2 * ks))
+    q, k, v = (p.reshape(t, -1, s.head_dim).contiguous() for p in qkv.split([qs, ks, ks], 1))  # at position 0: not rotated
+    k2.paged_append(cache, k, v, slots)
+    o = torch.zeros(t, s.n_heads, s.head_dim, dtype=torch.float16, device="cuda")
+    k2.paged_attention(cache, q.half(), o, cu, kv_len, table, 1, workspace)
+    on = codes_for(qs)
+    k2.quantize_rows(o.view(t, qs), *on)
+    x1 = product(dev["wo"][0], on, x0, residual=x0)
+    k2.norm_quantize(x1, dev["mlp_norm"][0], *xn, groups=s.norm_groups, eps=s.eps)
+    gate_up = torch.stack([dev["w_gate"][0], dev["w_up"][0]], 1).reshape(2 * s.intermediate, h)
+    act = product(gate_up, xn, torch.empty(t, s.intermediate, dtype=torch.bfloat16, device="cuda"), activation="swiglu")
+    an = codes_for(s.intermediate)
+    k2.quantize_rows(act, *an)
+    return product(dev["w_down"][0], an, x1, residual=x1)
+
+
+@pytest.mark.parametrize("shape,cache", [("medium", "i8"), ("medium", "f8"), ("layer", "i8"), ("odd", "i8")])
+@pytest.mark.parametrize("requests", [1, 5, 48])
+def test_a_paged_steps_layer_is_its_calls(k2, shape, cache, requests):
+    """First tokens of some requests through a model of one layer: the residual that k2_paged_step leaves is that of the public
+    calls on the same weights, bit for bit (one key alone has the weight 1, whatever the query)."""
+    from dense_gqa_decoder_gb300 import model_io
+    s = {"medium": ki.MEDIUM.replace(n_layers=1), "layer": ki.K2_LAYER,
+         "odd": ki.MEDIUM.replace(hidden=200, n_layers=1, n_heads=4, n_kv_heads=1, intermediate=328, vocab=301)}[shape]
+    dev, _ = model_io.device_weights(s, gain_scale=0.1)
+    ctx = k2.Context(k2.make_config(s, max_context=64, max_batch=requests, kv_dtype="f16", weights="f8"), dev)
+    ctx.set_option(k2.K2_OPT_ACT8, 1)
+    i32 = lambda v: torch.as_tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    tokens = i32(ki.prompt_ids(s.vocab, requests, seed=requests))
+    at = torch.arange(requests, device="cuda")
+    cu, kv_len, table, slots = i32(torch.arange(requests + 1)), i32(at * 0 + 1), i32(at).view(-1, 1), i32(16 * at)
+    pools = [k2.PagedCache(requests, 16, s.n_kv_heads, s.head_dim, cache) for _ in range(2)]
+    ws = k2.paged_workspace()
+    nxt = torch.zeros(requests, dtype=torch.int32, device="cuda")
+    ctx.paged_step(pools[:1], tokens, i32(at * 0), slots, cu, kv_len, table, 1, nxt, ws)
+    assert ctx.sync_status() == k2.K2_OK
+    want = layer_by_hand(k2, s, dev, tokens.long(), pools[1], slots, cu, kv_len, table, ws)
+    got = torch.cat([k2.device_view(ctx.hidden_view(r), s.hidden, torch.float32)[None] for r in range(requests)])
+    assert torch.equal(pools[0].v.view(torch.uint8), pools[1].v.view(torch.uint8)) and torch.equal(pools[0].v_scale, pools[1].v_scale)
+    assert torch.isfinite(want).all() and torch.equal(got, want)
