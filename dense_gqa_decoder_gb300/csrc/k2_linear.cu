@@ -227,7 +227,7 @@ __device__ __forceinline__ void load_weights(void* dst, const CUtensorMap* m, co
 // A CTA per tile of 128 rows x 16, 32 or 64 tokens.  Where there are fewer tiles than SMs, a cluster of up to eight CTAs splits
 // K: token j's sums go to CTA j % split, each CTA writing its share into that CTA's shared memory, and are added there in the
 // order of K, so that the result does not depend on which CTA came first.  One CTA per SM is enough (q|k|v of one token took 8.6
-// us with twice as many, whose clusters no longer fit at once, and 5.7 with these; 4.9 now).  The weights stream at 6.7 TB/s
+// us with twice as many, whose clusters no longer fit at once, and 5.7 with these; 4.8 now).  The weights stream at 6.7 TB/s
 // behind some 3.6 us of start, first loads and end (gate and up of 16 tokens, 52 MB: 11.2 us).
 constexpr int kFewTokens = 64, kFewStages = 5, kFewRing = 92 * 1024;  // two CTAs fit an SM
 
@@ -427,8 +427,9 @@ __global__ void __launch_bounds__(128) linear_few_kernel(const __grid_constant__
 //
 // A pair of CTAs (the two SMs of a TPC) works on tiles of 256 weight rows x up to 256 tokens with one MMA over both SMs
 // (cta_group::2): each CTA holds its own 128 rows and half of the tokens, so that an SM takes in 32 KB for 128 x 256 x 128
-// products of E4M3 codes (a CTA by itself would take in 48 KB).  Gate and up of 2048 tokens take 66 us (3250 TFLOP/s), 240 by
-// single CTAs; 4096 x 10240 by 2560 in bf16 130 us (1650).  Persistent, roles as warps:
+// products of E4M3 codes (a CTA by itself would take in 48 KB).  Gate and up of 2048 tokens take 66 us (3250 TFLOP/s) in bursts and
+// 76 (2810) back to back under the power cap, 240 by single CTAs; 4096 x 10240 by 2560 in bf16 131 us (1640) and 151 (1420).
+// Persistent, roles as warps:
 //   warps 0, 2  request the weights and the tokens of their CTA's stages (completion is counted by the first CTA's barriers)
 //   warp 1      of the first CTA issues the MMAs, into one of two accumulators of 256 tensor-memory columns
 //   warps 3-18  read the other accumulator and finish its tile; a warp's lanes are 32 neighbouring outputs of a token
@@ -833,12 +834,14 @@ k2_status launch_linear(const LinearWeights& w, const void* x, long long x_strid
   const WeightPlace place = {w.packed ? 1 : 0, a.dtype == K2_F8 ? kStepBytes : kStepBytes / 2};
   const int steps = (a.cols + place.step - 1) / place.step;
   // Few tokens per tile and K split over CTAs, or wide tiles on pairs of SMs: the cheaper by what was measured, in nanoseconds.
-  // Few: a K step takes 270 on an SM by itself and 165 more for each further CTA there; 2600 for the rest, again for every three
+  // Few: a K step takes 270, or 165 for each CTA of the SM where that is more; 2600 for the rest, again for every three
   // CTAs that an SM gets (300 tokens of 640 by 20480 in bf16: 17.4 us, pairs 12.9; 2000 by 1664 in E4M3, three each: 6.3 and 7.0),
   // 2200 more to join shares of K, and 2000 where those are more CTAs than SMs.  Pairs: a step takes kStepNs for 64, 96 .. 256 tokens a tile;
   // 3000 for the rest and 8 per column of the last tile.  (Down of 2048 tokens: two waves of 130 tiles of 160, 38 us; of 110 of
   // 192 tokens 43; of 80 of 256, 51.)  Neither is done before the weights have been read (6800 bytes a ns, 5400
-  // as the few read them).  Measured as this says within a sixth (us, few and pairs): down of 128 tokens 14.3 and 16.6, of 256
+  // as the few read them).  The costs serve to choose by: of more than 64 tokens they are up to a third below what the kernels
+  // take, outputs and residuals not being counted, in both kernels alike (12.5 for the few and 14.7 measured, gate and up of 128
+  // tokens; 23 for pairs and 28, q|k|v of 2048).  The choice was compared at (us, few and pairs): down of 128 tokens 14.3 and 16.6, of 256
   // 15.6 and 15.7, of 512 28.6 and 18.6; gate and up of 128 15.0 and 16.3, of 256 24.2 and 18.4; q|k|v of 128 9.8 and 7.0.
   // Activations take the few's four finishing warps longer.  Up to 64 tokens it is always the few (gate and up of 64 tokens 14.4
   // us against 16.5).
@@ -848,7 +851,9 @@ k2_status launch_linear(const LinearWeights& w, const void* x, long long x_strid
   long long few_cost = 0;
   for (int per_sm = 1; per_sm <= (a.tokens > 64 ? 2 : 1); ++per_sm) {
     int split = static_cast<int>(std::max<long long>(1, std::min<long long>({per_sm * sms / few_tiles, kMaxSplit, steps})));
-    if (split == 7) split = 6;  // SMs come in twos: 20 tiles of 10240 by 64 tokens 9.3 us with clusters of six, 9.7 of seven
+    // SMs come in twos.  With clusters of six and of seven, 20 and 21 tiles (the numbers that seven would be taken for), us: 64 tokens
+    // by 10240 9.1 .. 9.3 and 9.7 .. 9.9, by 4096 5.4 and 6.5, one by 4096 4.2 and 4.6 .. 4.8; by 640 (five steps) the same.
+    if (split == 7) split = 6;
     const long long mine = (steps + split - 1) / split, ctas = few_tiles * split, load = (ctas + sms - 1) / sms;
     const long long cost = 2600 * ((load + 2) / 3) + std::max(mine * std::max(270ll, 165 * load), bytes / 5400) +
                            (split == 1 ? 0 : ctas <= sms ? 2200 : 4200);

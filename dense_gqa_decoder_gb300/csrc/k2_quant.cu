@@ -414,9 +414,10 @@ struct Row {
 };
 
 // A CTA per row.  Many rows, the usual case: up to 320 threads (512 with 4 and more vectors each), so few registers that 1280
-// threads (1536) fit an SM and their rows are on their way while others are worked on (8192 x 10240 values with 78 registers
-// 69 us, with 40 registers 49).  WIDE: up to 1024 threads.
-// (Rows copied ahead into shared memory by CTAs that stay: 8192 x 10240 values 58 us, 49 as it is.)
+// threads (1536) fit an SM and their rows are on their way while others are worked on (without these limits 8192 x 10240 bf16
+// values 57.8 us, 40.4 with them; norm of 8192 x 2560 in bf16 30.0 and 27.1, in fp32, where two vectors a thread spill eight bytes
+// for it, 41.7 and 42.4).  WIDE: up to 1024 threads.
+// (Rows copied ahead into shared memory by CTAs that stay were slower: 8192 x 10240 values 58 us, when this form took 49.)
 template <typename XT, typename RT, bool NORM, int V, bool WIDE>
 __global__ void __launch_bounds__(WIDE ? kWideThreads : V <= 2 ? kRowThreads : kVectorThreads,
                                   WIDE ? 1 : V <= 2 ? 1280 / kRowThreads : V == 4 && !NORM && sizeof(XT) == 2 ? 1536 / kVectorThreads : 1)
@@ -515,8 +516,9 @@ cudaError_t launch_rows(const RowArgs& a, int tokens, cudaStream_t s) {
   const bool whole = a.cols % 8 == 0 && n8 <= (NORM ? 4 : 8) * kVectorThreads && at8(a.x, a.x_stride, sizeof(XT)) && at8(a.codes, a.codes_stride, 1) &&
                      at8(a.res, a.res_stride, rb) && at8(a.res_out, a.res_out_stride, rb);
   if (whole && (!NORM || (a.groups <= kGroups && n8 % a.groups == 0 && at8(a.gain, 0, row_type_bytes(a.gain_dtype))))) {
-    // Few rows, fewer than SMs: many threads, few vectors each (16 x 10240 values: 2.6 us with 640 threads, 3.4 with 320);
-    // many: fewer threads, so that more rows are on their way at once (8192 x 10240: 66 and 56 us).
+    // Few rows, fewer than SMs: many threads, few vectors each (norm of 64 x 2560 2.6 us with 320 threads, 2.8 with 160; of 16 x 10240
+    // 4.5 with 640 and 4.2 with 320; conversions the same either way); many: fewer threads, so that more rows are on their way at
+    // once (8192 x 10240 values 40.4 us, wide 57.1; norm of 8192 x 2560 in bf16 27.1 and 36.2, in fp32 42.4 and 45.0).
     constexpr std::integral_constant<int, 1> one;
     constexpr std::integral_constant<int, 2> both;
     constexpr std::integral_constant<int, 4> four;
