@@ -288,8 +288,9 @@ class Context:
     def set_option(self, opt, value):
         """K2_OPT_ACT8 = 1 calls act8_init first where that was not done."""
         if opt == K2_OPT_ACT8 and value == 1 and self.act8_buffer is None and LIB.k2_act8_bytes(self.ctx):
+            torch.cuda.synchronize()  # the weights may be on their way on another stream
             self.act8_init()
-            torch.cuda.current_stream().synchronize()  # the option holds for any stream
+            torch.cuda.synchronize()  # and the option holds for any stream
         self._check(LIB.k2_set_option(self.ctx, opt, value))
 
     def act8_init(self, stream=None):

@@ -456,8 +456,9 @@ k2_status k2_set_option(k2_ctx* ctx, int32_t option, int64_t value);
  * device memory that is (3.2 GB for the 3.7B model; 0 where the option is not supported).
  * k2_act8_init fills d_buffer (256-byte aligned, the caller's, kept until k2_free or the
  * next k2_act8_init; a captured step keeps reading the one it was captured with) from the
- * packed weights, enqueued on `stream`, and allows the option.  Contexts that never set the
- * option need neither. */
+ * packed weights, enqueued on `stream` (behind k2_init_weights, ahead of the calls that use
+ * it: where those are on other streams the caller orders them), and allows the option.
+ * Contexts that never set the option need neither. */
 size_t k2_act8_bytes(const k2_ctx* ctx);
 k2_status k2_act8_init(k2_ctx* ctx, void* d_buffer, size_t bytes, void* stream);
 

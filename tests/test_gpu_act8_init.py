@@ -79,3 +79,22 @@ def test_a_norm_that_the_rows_calls_refuse(k2, eps):
     assert k2.LIB.k2_act8_bytes(ctx.ctx) == 0
     if eps < 1:
         assert torch.isfinite(logits(k2, ctx)).all()
+
+
+def test_weights_that_are_still_on_their_way_on_another_stream(k2):
+    """The option set right behind a context whose weights are packed on another stream, which is busy."""
+    from dense_gqa_decoder_gb300 import model_io
+    dev, _ = model_io.device_weights(ki.MEDIUM, gain_scale=0.1)
+    cfg = k2.make_config(ki.MEDIUM, max_context=128, kv_dtype="f16", weights="f8")
+    rows = []
+    for side in (None, torch.cuda.Stream()):
+        big = torch.randn(8192, 8192, device="cuda")
+        torch.cuda.synchronize()
+        if side is not None:
+            with torch.cuda.stream(side):
+                for _ in range(20):
+                    torch.mm(big, big)
+        ctx = k2.Context(cfg, dev, stream=side)
+        ctx.set_option(k2.K2_OPT_ACT8, 1)
+        rows.append(logits(k2, ctx))
+    assert torch.equal(*rows)
