@@ -1147,11 +1147,13 @@ cudaError_t prefill_block(k2_ctx* c, int seq, const int32_t* d_tokens, int n, in
       pa.guard = c->guard;
       e = launch_prefill_attn_tc(c->pf_maps, pa, s.d, s.rep, st);
       if (!e && a8) e = quantize8(xh, K2_F16, s.nq * s.d, oc);
+    } else if (!e && a8) {  // the rows in fp32, where q | k | v were
+      e = launch_prefill_attn_f32(Q, kvdt, c->kc(l), c->vc(l), c->ks(l), c->vs(l), qkv, n, s.nq, s.nkv, s.d, pos0, head_row0,
+                                  c->lay.cap, scale, st);
+      if (!e) e = quantize8(qkv, K2_F32, s.nq * s.d, oc);
     } else if (!e) {
-      // E4M3: the rows in fp32, where q | k | v were
-      e = launch_prefill_attn(Q, kvdt, c->kc(l), c->vc(l), c->ks(l), c->vs(l), xh, xl, a8 ? qkv : nullptr, n, s.nq, s.nkv, s.d,
-                              pos0, head_row0, c->lay.cap, scale, st);
-      if (!e && a8) e = quantize8(qkv, K2_F32, s.nq * s.d, oc);
+      e = launch_prefill_attn(Q, kvdt, c->kc(l), c->vc(l), c->ks(l), c->vs(l), xh, xl, n, s.nq, s.nkv, s.d, pos0,
+                              head_row0, c->lay.cap, scale, st);
     }
     if (a8) {
       if (!e) e = linear8(l, 1, oc, s.H, s.nq * s.d, K2_ACT_NONE, X, K2_F32, X);

@@ -58,6 +58,11 @@ inline bool sets_meet(const RowSet& a, const RowSet& b) {
 // fp8 codes [N][K] in the decode step's tile units as packed pairs (k2_gemv_packed.cu)
 cudaError_t launch_f8_pairs(uint8_t* dst, const uint8_t* src, int N, int K, cudaStream_t s);
 
+// launch_prefill_attn with fp32 rows in place of bf16 halves (k2_prefill.cu)
+cudaError_t launch_prefill_attn_f32(const float* Q, int kv_dtype, const void* kc, const void* vc, const void* ks, const void* vs,
+                                    float* out, int n, int nq, int nkv, int D, int pos0, size_t head_row0, int cap, float scale,
+                                    cudaStream_t s);
+
 k2_status launch_linear(const LinearWeights& w, const void* x, long long x_stride, const LinearArgs& a, cudaStream_t s);
 
 }  // namespace k2

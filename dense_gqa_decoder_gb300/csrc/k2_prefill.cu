@@ -16,6 +16,7 @@
 #include <utility>
 
 #include "k2_kernels.h"
+#include "k2_linear.h"
 #include "k2_serve.h"
 #include "k2_common.cuh"
 
@@ -867,15 +868,26 @@ cudaError_t launch_prefill_attn_of(const float* Q, int kv_dtype, const void* kc,
 }  // namespace
 
 cudaError_t launch_prefill_attn(const float* Q, int kv_dtype, const void* kc, const void* vc, const void* ks,
-                                const void* vs, __nv_bfloat16* oh, __nv_bfloat16* ol, float* of, int n, int nq, int nkv,
-                                int D, int pos0, size_t head_row0, int cap, float scale, cudaStream_t s) {
+                                const void* vs, __nv_bfloat16* oh, __nv_bfloat16* ol, int n, int nq, int nkv, int D,
+                                int pos0, size_t head_row0, int cap, float scale, cudaStream_t s) {
   const int rep = nq / nkv;
 #define K2_PA_LAUNCH(DD, R)                                                                                       \
   if (D == DD && rep == R)                                                                                        \
-    return of ? launch_prefill_attn_of<DD, R, true>(Q, kv_dtype, kc, vc, ks, vs, oh, ol, of, n, nq, nkv, pos0,    \
-                                                    head_row0, cap, scale, s)                                     \
-              : launch_prefill_attn_of<DD, R, false>(Q, kv_dtype, kc, vc, ks, vs, oh, ol, of, n, nq, nkv, pos0,   \
-                                                     head_row0, cap, scale, s);
+    return launch_prefill_attn_of<DD, R, false>(Q, kv_dtype, kc, vc, ks, vs, oh, ol, nullptr, n, nq, nkv, pos0,   \
+                                                head_row0, cap, scale, s);
+  K2_PREFILL_ATTN_SHAPES(K2_PA_LAUNCH)
+#undef K2_PA_LAUNCH
+  return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_prefill_attn_f32(const float* Q, int kv_dtype, const void* kc, const void* vc, const void* ks,
+                                    const void* vs, float* out, int n, int nq, int nkv, int D, int pos0, size_t head_row0,
+                                    int cap, float scale, cudaStream_t s) {
+  const int rep = nq / nkv;
+#define K2_PA_LAUNCH(DD, R)                                                                                       \
+  if (D == DD && rep == R)                                                                                        \
+    return launch_prefill_attn_of<DD, R, true>(Q, kv_dtype, kc, vc, ks, vs, nullptr, nullptr, out, n, nq, nkv,    \
+                                               pos0, head_row0, cap, scale, s);
   K2_PREFILL_ATTN_SHAPES(K2_PA_LAUNCH)
 #undef K2_PA_LAUNCH
   return cudaErrorInvalidValue;
